@@ -11,6 +11,8 @@ from ._binding import (FAError, attention, backward, combine, default_scale, fa_
                        forward_sequence_sharded, fa_combine, fa_fwd_slab, fa_fwd, fa_fwd_kernel, fa_fwd_blocksparse, fa_fwd_fp8, fa_fwd_host, fa_fwd_mma,
                        forward_blocksparse, forward_fp8, forward_host, host_staging,
                        fa_fwd_splitkv, fa_fwd_splitkv_noalloc, fa_fwd_splitkv_workspace_bytes,
-                       fa_get_device_status,
+                       KV4Cache, kv4_cache, kv4_append, kv4_read, forward_kv4, kv4_evict, key_weights,
+                       KV4CacheStruct, fa_kv4_append, fa_kv4_read, fa_fwd_kv4, fa_fwd_kv4_workspace_bytes,
+                       fa_kv4_evict, fa_key_weights, fa_get_device_status,
                        fa_status_string, fa_version, forward, forward_splitkv, lib)
 from .workloads import HEADLINE, WORKLOADS, Workload, make_inputs, workload_inputs  # noqa: F401

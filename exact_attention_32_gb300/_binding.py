@@ -7,10 +7,12 @@ no fallback: if libfa.so is missing or fails to load, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
 import threading
+from typing import NamedTuple
 
 import numpy as np
 import torch
@@ -22,10 +24,19 @@ _lock = threading.Lock()
 
 FA_OK = 0
 STATUS_NAMES = {0: "FA_OK", 1: "FA_ERR_INVALID_ARG", 2: "FA_ERR_UNSUPPORTED", 3: "FA_ERR_NO_DEVICE",
-                4: "FA_ERR_ARCH", 5: "FA_ERR_LAUNCH", 6: "FA_ERR_TIMEOUT", 7: "FA_ERR_WORKSPACE_LIMIT"}
+                4: "FA_ERR_ARCH", 5: "FA_ERR_LAUNCH", 6: "FA_ERR_TIMEOUT", 7: "FA_ERR_WORKSPACE_LIMIT",
+                8: "FA_ERR_BAD_PAGE"}
 EXPORTED = ("fa_fwd", "fa_fwd_kernel", "fa_bh_partition", "fa_kv_shard", "fa_fwd_kv_shard", "fa_fwd_slab", "fa_fwd_host", "fa_fwd_mma", "fa_fwd_splitkv", "fa_fwd_splitkv_workspace_bytes", "fa_combine",
             "fa_fwd_splitkv_noalloc", "fa_fwd_fp8", "fa_fwd_blocksparse", "fa_bwd", "fa_bwd_workspace_bytes", "fa_get_device_status",
-            "fa_status_string", "fa_version")
+            "fa_status_string", "fa_version", "fa_kv4_append", "fa_kv4_read", "fa_fwd_kv4", "fa_fwd_kv4_workspace_bytes",
+            "fa_kv4_evict", "fa_key_weights")
+
+
+class KV4CacheStruct(ctypes.Structure):
+    """``fa_kv4_cache`` of include/fa.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("weights", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("Hkv", ctypes.c_int64), ("page_size", ctypes.c_int64), ("d", ctypes.c_int64)]
 
 
 class FAError(RuntimeError):
@@ -82,6 +93,20 @@ def lib():
             L.fa_bwd_workspace_bytes.argtypes = [i64] * 4
             L.fa_combine.restype = ctypes.c_int
             L.fa_combine.argtypes = [vp, vp, i64, vp, vp, i64, i64, i64, i64, vp]
+            cp = ctypes.POINTER(KV4CacheStruct)
+            L.fa_kv4_append.restype = ctypes.c_int
+            L.fa_kv4_append.argtypes = [cp, vp, vp, vp, vp, vp, vp, i64, i64, i64, vp]
+            L.fa_kv4_read.restype = ctypes.c_int
+            L.fa_kv4_read.argtypes = [cp, vp, vp, vp, i64, i64, i64, vp, vp, vp]
+            L.fa_fwd_kv4.restype = ctypes.c_int
+            L.fa_fwd_kv4.argtypes = [vp, cp, vp, vp, vp, vp, i64, i64, i64, i64, ctypes.c_float, ctypes.c_int, vp,
+                                     i64, vp]
+            L.fa_fwd_kv4_workspace_bytes.restype = i64
+            L.fa_fwd_kv4_workspace_bytes.argtypes = [i64] * 6 + [ctypes.c_int]
+            L.fa_kv4_evict.restype = ctypes.c_int
+            L.fa_kv4_evict.argtypes = [cp, vp, vp, i64, cp, vp, i64, i64, i64, i64, vp, vp, vp]
+            L.fa_key_weights.restype = ctypes.c_int
+            L.fa_key_weights.argtypes = [vp, vp, vp, vp, i64, i64, i64, i64, i64, ctypes.c_float, ctypes.c_int, i64, vp]
             L.fa_get_device_status.restype = ctypes.c_int
             L.fa_get_device_status.argtypes = [vp]
             L.fa_status_string.restype = ctypes.c_char_p
@@ -198,6 +223,40 @@ def fa_bwd_workspace_bytes(B, H, N, d) -> int:
 def fa_combine(o_parts, lse_parts, n_parts, o, lse, B, H, N, d, stream) -> int:
     """Raw call of the merge of partial (O, LSE) results."""
     return lib().fa_combine(o_parts, lse_parts, n_parts, o, lse, B, H, N, d, stream)
+
+
+def fa_kv4_append(cache, k_new, v_new, w_new, n_new, lens, page_table, B, S, max_pages, stream) -> int:
+    """Raw call of the append to a 4-bit cache; ``cache`` is a ``KV4CacheStruct``."""
+    return lib().fa_kv4_append(ctypes.byref(cache), k_new, v_new, w_new, n_new, lens, page_table, B, S, max_pages,
+                               stream)
+
+
+def fa_kv4_read(cache, first, lens, page_table, B, max_pages, T, k_out, v_out, stream) -> int:
+    """Raw call of the read of a 4-bit cache's rows as bf16."""
+    return lib().fa_kv4_read(ctypes.byref(cache), first, lens, page_table, B, max_pages, T, k_out, v_out, stream)
+
+
+def fa_fwd_kv4(q, cache, lens, page_table, o, lse, B, H, n_q, max_pages, scale, accumulate, workspace,
+               workspace_bytes, stream) -> int:
+    """Raw call of attention over a 4-bit cache (caller-owned workspace)."""
+    return lib().fa_fwd_kv4(q, ctypes.byref(cache), lens, page_table, o, lse, B, H, n_q, max_pages, scale, accumulate,
+                            workspace, workspace_bytes, stream)
+
+
+def fa_fwd_kv4_workspace_bytes(B, H, Hkv, n_q, d, max_tokens, accumulate) -> int:
+    return lib().fa_fwd_kv4_workspace_bytes(B, H, Hkv, n_q, d, max_tokens, int(accumulate))
+
+
+def fa_kv4_evict(cache, lens, page_table, max_pages, to, to_table, to_max_pages, B, keep, recent, kept, new_lens,
+                 stream) -> int:
+    """Raw call of the eviction from a 4-bit cache by accumulated weight."""
+    return lib().fa_kv4_evict(ctypes.byref(cache), lens, page_table, max_pages, ctypes.byref(to), to_table,
+                              to_max_pages, B, keep, recent, kept, new_lens, stream)
+
+
+def fa_key_weights(q, k, lse, weights, B, H, Hkv, N, d, scale, causal, first_query, stream) -> int:
+    """Raw call of the accumulated attention weight of a prompt's keys."""
+    return lib().fa_key_weights(q, k, lse, weights, B, H, Hkv, N, d, scale, int(causal), first_query, stream)
 
 
 def fa_get_device_status(stream=0) -> int:
@@ -509,3 +568,224 @@ def forward_blocksparse(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, block
     if st != FA_OK:
         raise FAError(st, "fa_fwd_blocksparse")
     return o, lse
+
+
+class KV4Cache(NamedTuple):
+    """The arrays of a 4-bit KV cache (format in include/fa.h): CUDA tensors, contiguous.
+
+    k, v     uint8 [n_pages, Hkv, page_size, d/2], two E2M1 codes a byte
+    k_scale  uint8 [n_pages, Hkv, page_size, d/32];  v_scale  uint8 [n_pages, Hkv, page_size]
+    weights  fp32 [n_pages, Hkv, page_size], each key's accumulated attention weight, or None
+    """
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+    weights: torch.Tensor | None = None
+
+
+def kv4_cache(n_pages: int, n_kv_heads: int, page_size: int, d: int, device="cuda", weights: bool = True) -> KV4Cache:
+    """A zeroed 4-bit cache of ``n_pages`` pages of ``page_size`` tokens."""
+    if d not in (64, 128):
+        raise FAError(2, "kv4_cache")
+    shape = (n_pages, n_kv_heads, page_size)
+
+    def zeros(*s, dtype=torch.uint8):
+        return torch.zeros(s, dtype=dtype, device=device)
+    return KV4Cache(zeros(*shape, d // 2), zeros(*shape, d // 2), zeros(*shape, d // 32), zeros(*shape),
+                    zeros(*shape, dtype=torch.float32) if weights else None)
+
+
+def _kv4_struct(c: KV4Cache) -> KV4CacheStruct:
+    shape = c.k.shape
+    if len(shape) != 4:
+        raise ValueError("cache.k must be [n_pages, Hkv, page_size, d/2]")
+    n, heads, page, half = shape
+    dev = c.k.device
+    w = c.weights
+    if c.v.shape != shape or c.k_scale.shape != (n, heads, page, half // 16) or c.v_scale.shape != (n, heads, page):
+        raise ValueError("cache arrays must be k, v [n_pages, Hkv, page_size, d/2], k_scale [..., d/32], "
+                         "v_scale [n_pages, Hkv, page_size]")
+    for t in (c.k, c.v, c.k_scale, c.v_scale):
+        if t.dtype != torch.uint8 or t.device != dev or not t.is_contiguous():
+            raise ValueError("k, v, k_scale, v_scale of a cache must be contiguous uint8 tensors on one CUDA device")
+    if w is not None and (w.shape != (n, heads, page) or w.dtype != torch.float32 or w.device != dev
+                          or not w.is_contiguous()):
+        raise ValueError("cache.weights must be a contiguous fp32 tensor [n_pages, Hkv, page_size]")
+    if not c.k.is_cuda:
+        raise ValueError("a 4-bit cache lives on a CUDA device")
+    return KV4CacheStruct(c.k.data_ptr(), c.v.data_ptr(), c.k_scale.data_ptr(), c.v_scale.data_ptr(),
+                          None if w is None else w.data_ptr(), n, heads, page, 2 * half)
+
+
+def _kv4_index(name: str, t: torch.Tensor, dims: int, B: int | None, device) -> int:
+    """Pointer of an int32 index tensor ([B] or [B, columns])."""
+    if (t.dtype != torch.int32 or t.dim() != dims or t.device != device or not t.is_contiguous()
+            or (B is not None and t.shape[0] != B)):
+        raise ValueError(f"{name} must be a contiguous int32 tensor {'[B]' if dims == 1 else '[B, pages]'} on the "
+                         "cache's device")
+    return t.data_ptr()
+
+
+def _current(device) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _on(device, stream):
+    """(context that makes ``device`` current, stream handle); no context where it already is."""
+    s = _current(device) if stream is None else stream.cuda_stream
+    here = torch.cuda.current_device() == device.index
+    return (contextlib.nullcontext() if here else torch.cuda.device(device)), s
+
+
+def kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, lens: torch.Tensor, page_table: torch.Tensor,
+               n_new: torch.Tensor | None = None, weights: torch.Tensor | None = None,
+               stream: torch.cuda.Stream | None = None) -> None:
+    """Quantise new tokens into the cache by ``fa_kv4_append``.
+
+    k, v: contiguous bf16 [B, Hkv, S, d].  lens: int32 [B], the lengths AFTER
+    the append; of its S rows sequence b gains the first n_new[b] (all where
+    n_new is None), as its last positions.  page_table: int32 [B, pages].
+    weights: fp32 [B, Hkv, S], what the new tokens' weights start from (0
+    where None)."""
+    c = _kv4_struct(cache)
+    dev = cache.k.device
+    if k.dim() != 4 or k.shape != v.shape or k.shape[1] != c.Hkv or k.shape[3] != c.d:
+        raise ValueError("k and v must be [B, Hkv, S, d] with the cache's Hkv and d")
+    for t in (k, v):
+        if t.dtype != torch.bfloat16 or t.device != dev or not t.is_contiguous():
+            raise ValueError("k and v must be contiguous bf16 tensors on the cache's device")
+    B, _, S, _ = k.shape
+    if weights is not None and (weights.shape != (B, c.Hkv, S) or weights.dtype != torch.float32
+                                or weights.device != dev or not weights.is_contiguous()):
+        raise ValueError("weights must be a contiguous fp32 tensor [B, Hkv, S]")
+    if weights is not None and cache.weights is None:
+        raise ValueError("the cache holds no weights")
+    pl, pt = _kv4_index("lens", lens, 1, B, dev), _kv4_index("page_table", page_table, 2, B, dev)
+    pn = None if n_new is None else _kv4_index("n_new", n_new, 1, B, dev)
+    ctx, s = _on(dev, stream)
+    with ctx:
+        st = fa_kv4_append(c, k.data_ptr(), v.data_ptr(), None if weights is None else weights.data_ptr(), pn, pl, pt,
+                           B, S, page_table.shape[1], s)
+    if st != FA_OK:
+        raise FAError(st, "fa_kv4_append")
+
+
+def kv4_read(cache: KV4Cache, lens: torch.Tensor, page_table: torch.Tensor, count: int,
+             first: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None):
+    """(K, V) bf16 [B, Hkv, count, d]: positions first[b] .. first[b] + count - 1
+    (from 0 where first is None) of each sequence by ``fa_kv4_read``; rows at or
+    past lens[b] are zero."""
+    c = _kv4_struct(cache)
+    dev = cache.k.device
+    B = lens.shape[0] if lens.dim() == 1 else -1
+    pl, pt = _kv4_index("lens", lens, 1, None, dev), _kv4_index("page_table", page_table, 2, B, dev)
+    pf = None if first is None else _kv4_index("first", first, 1, B, dev)
+    if count < 1:
+        raise ValueError("count must be at least 1")
+    k = torch.empty((B, c.Hkv, count, c.d), dtype=torch.bfloat16, device=dev)
+    v = torch.empty_like(k)
+    ctx, s = _on(dev, stream)
+    with ctx:
+        st = fa_kv4_read(c, pf, pl, pt, B, page_table.shape[1], count, k.data_ptr(), v.data_ptr(), s)
+    if st != FA_OK:
+        raise FAError(st, "fa_kv4_read")
+    return k, v
+
+
+def forward_kv4(q: torch.Tensor, cache: KV4Cache, lens: torch.Tensor, page_table: torch.Tensor,
+                scale: float | None = None, accumulate: bool = False, workspace: torch.Tensor | None = None,
+                stream: torch.cuda.Stream | None = None):
+    """(O bf16 [B, H, n_q, d], LSE fp32 [B, H, n_q]) by ``fa_fwd_kv4``: the newest
+    n_q tokens of each sequence (their keys already appended) over its cache.
+
+    q: contiguous bf16 [B, H, n_q, d], H a multiple of the cache's key heads;
+    lens: int32 [B]; page_table: int32 [B, pages].  ``accumulate`` adds each
+    key's attention weight over these rows to cache.weights.  The workspace
+    (uint8 CUDA tensor) is allocated with torch when not given."""
+    c = _kv4_struct(cache)
+    dev = cache.k.device
+    if q.dim() != 4 or q.shape[3] != c.d or q.shape[1] % c.Hkv != 0:
+        raise ValueError("q must be [B, H, n_q, d] with the cache's d and H a multiple of its key heads")
+    if q.dtype != torch.bfloat16 or q.device != dev or not q.is_contiguous():
+        raise ValueError("q must be a contiguous bf16 tensor on the cache's device")
+    if accumulate and cache.weights is None:
+        raise ValueError("the cache holds no weights")
+    B, H, n_q, d = q.shape
+    pl, pt = _kv4_index("lens", lens, 1, B, dev), _kv4_index("page_table", page_table, 2, B, dev)
+    scale = default_scale(d) if scale is None else scale
+    cols = page_table.shape[1]
+    need = fa_fwd_kv4_workspace_bytes(B, H, c.Hkv, n_q, d, cols * c.page_size, accumulate)
+    if need < 0:
+        raise FAError(1 if d in (64, 128) else 2, "fa_fwd_kv4_workspace_bytes")
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    o = torch.empty_like(q)
+    lse = torch.empty((B, H, n_q), dtype=torch.float32, device=dev)
+    ctx, s = _on(dev, stream)
+    with ctx:
+        st = fa_fwd_kv4(q.data_ptr(), c, pl, pt, o.data_ptr(), lse.data_ptr(), B, H, n_q, cols, float(scale),
+                        bool(accumulate), workspace.data_ptr(), workspace.numel() * workspace.element_size(), s)
+    if st != FA_OK:
+        raise FAError(st, "fa_fwd_kv4")
+    return o, lse
+
+
+def kv4_evict(cache: KV4Cache, lens: torch.Tensor, page_table: torch.Tensor, to: KV4Cache, to_table: torch.Tensor,
+              keep: int, recent: int = 0, stream: torch.cuda.Stream | None = None):
+    """(kept int32 [B, Hkv, keep], new_lens int32 [B]) by ``fa_kv4_evict``: the last
+    ``recent`` tokens of every sequence and key head, and of the others those with the
+    largest cache.weights, ``keep`` in all, copied in order to the pages of
+    ``to_table`` (int32 [B, pages]) in ``to`` (another cache of the same layout, or the
+    same one: the pages must then be free).  kept holds their positions, -1
+    past the end."""
+    c, t = _kv4_struct(cache), _kv4_struct(to)
+    dev = cache.k.device
+    if to.k.device != dev or (t.Hkv, t.page_size, t.d) != (c.Hkv, c.page_size, c.d):
+        raise ValueError("both caches must have the same key heads, page size, d and device")
+    if cache.weights is None or to.weights is None:
+        raise ValueError("eviction needs the weights of both caches")
+    B = lens.shape[0] if lens.dim() == 1 else -1
+    pl, pt = _kv4_index("lens", lens, 1, None, dev), _kv4_index("page_table", page_table, 2, B, dev)
+    ptt = _kv4_index("to_table", to_table, 2, B, dev)
+    if keep < 1 or not 0 <= recent <= keep or keep > to_table.shape[1] * c.page_size:
+        raise ValueError("need 1 <= keep <= the tokens of to_table's pages, and 0 <= recent <= keep")
+    kept = torch.empty((B, c.Hkv, keep), dtype=torch.int32, device=dev)
+    new_lens = torch.empty((B,), dtype=torch.int32, device=dev)
+    ctx, s = _on(dev, stream)
+    with ctx:
+        st = fa_kv4_evict(c, pl, pt, page_table.shape[1], t, ptt, to_table.shape[1], B, keep, recent, kept.data_ptr(),
+                          new_lens.data_ptr(), s)
+    if st != FA_OK:
+        raise FAError(st, "fa_kv4_evict")
+    return kept, new_lens
+
+
+def key_weights(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor, scale: float | None = None, causal: bool = False,
+                first_query: int = 0, stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """fp32 [B, Hkv, N]: the attention weight each key of a prompt has gathered over
+    its group's heads and the queries from ``first_query`` on, by
+    ``fa_key_weights``.  q: contiguous bf16 [B, H, N, d]; k: [B, Hkv, N, d], H a
+    multiple of Hkv; lse: fp32 [B, H, N], ``forward``'s."""
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q must be [B, H, N, d] and k [B, Hkv, N, d]")
+    B, H, N, d = q.shape
+    heads = k.shape[1]
+    if k.shape != (B, heads, N, d) or heads < 1 or H % heads != 0:
+        raise ValueError("k must be [B, Hkv, N, d] with H a multiple of Hkv")
+    for t in (q, k):
+        if t.dtype != torch.bfloat16 or not t.is_cuda or t.device != q.device or not t.is_contiguous():
+            raise ValueError("q and k must be contiguous bf16 CUDA tensors on one device")
+    if lse.shape != (B, H, N) or lse.dtype != torch.float32 or lse.device != q.device or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous fp32 tensor [B, H, N]")
+    if not 0 <= first_query < N:
+        raise ValueError("first_query must lie in [0, N)")
+    scale = default_scale(d) if scale is None else scale
+    w = torch.empty((B, heads, N), dtype=torch.float32, device=q.device)
+    ctx, s = _on(q.device, stream)
+    with ctx:
+        st = fa_key_weights(q.data_ptr(), k.data_ptr(), lse.data_ptr(), w.data_ptr(), B, H, heads, N, d, float(scale),
+                            bool(causal), first_query, s)
+    if st != FA_OK:
+        raise FAError(st, "fa_key_weights")
+    return w

@@ -83,6 +83,10 @@ typedef cudaError_t (*Launcher)(const FaProblem &, cudaStream_t);
 
 }  // namespace
 
+int fa_current_device(int *dev, int *sm_count) { return current_device(dev, sm_count); }
+int fa_check_device_pointer(const void *p, int dev, uintptr_t align) { return check_pointer(p, dev, align); }
+bool fa_ranges_overlap(const void *a, uint64_t na, const void *b, uint64_t nb) { return overlaps(a, na, b, nb); }
+
 int fa_check_sizes(int64_t B, int64_t H, int64_t N, int64_t d)
 {
     if (B < 1 || H < 1 || N < 1 || d < 1) return FA_ERR_INVALID_ARG;
@@ -546,7 +550,12 @@ extern "C" int fa_get_device_status(void *stream)
     const int fwd = fa_tc_take_status(static_cast<cudaStream_t>(stream));
     const int dp = fa_dp_take_status(static_cast<cudaStream_t>(stream));
     const int bwd = fa_bwd_take_status(static_cast<cudaStream_t>(stream));
-    return fwd != FA_OK ? fwd : (dp != FA_OK ? dp : bwd);
+    const int weights = fa_key_weights_take_status(static_cast<cudaStream_t>(stream));
+    const int decode = fa_kv4_decode_take_status(static_cast<cudaStream_t>(stream));
+    const int cache = fa_kv4_cache_take_status(static_cast<cudaStream_t>(stream));
+    for (const int st : {fwd, dp, bwd, weights, decode})
+        if (st != FA_OK) return st;
+    return cache;
 }
 
 extern "C" const char *fa_status_string(int status)
@@ -561,6 +570,7 @@ extern "C" const char *fa_status_string(int status)
     case FA_ERR_TIMEOUT: return "FA_ERR_TIMEOUT: a bounded in-kernel wait gave up";
     case FA_ERR_WORKSPACE_LIMIT:
         return "FA_ERR_WORKSPACE_LIMIT: the problem needs more scratch than the static array holds";
+    case FA_ERR_BAD_PAGE: return "FA_ERR_BAD_PAGE: a page index or a length lay outside the cache";
     default: return "unknown fa_status";
     }
 }

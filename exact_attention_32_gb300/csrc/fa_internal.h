@@ -90,6 +90,68 @@ int fa_bwd_take_status(cudaStream_t stream);
 // Warp-level tensor-core (mma.sync) kernel: one CTA per 128-row query tile.
 cudaError_t fa_launch_mma(const FaProblem &p, cudaStream_t stream);
 
+// Checks shared by the entry points (fa_api.cu): the current device and its SM
+// count; a device pointer of that device aligned to `align` bytes; whether two
+// ranges meet; and the softmax arguments.  Each returns an fa_status but the third.
+int fa_current_device(int *dev, int *sm_count);
+int fa_check_device_pointer(const void *p, int dev, uintptr_t align);
+bool fa_ranges_overlap(const void *a, uint64_t na, const void *b, uint64_t nb);
+
+// The 4-bit cache as its kernels see it (the format is in fa_kv4.cuh).
+struct Kv4Cache {
+    uint8_t *k, *v, *k_scale, *v_scale;
+    float *weights;  // or null
+    int n_pages, heads, log2_page, d;
+};
+// fa_kv4_append / fa_kv4_read / fa_kv4_evict on validated arguments (fa_kv4_cache.cu).
+cudaError_t fa_launch_kv4_append(const Kv4Cache &c, const void *k_new, const void *v_new, const float *w_new,
+                                 const int32_t *n_new, const int32_t *lens, const int32_t *table, int64_t B, int64_t S,
+                                 int64_t max_pages, int sm_count, cudaStream_t stream);
+cudaError_t fa_launch_kv4_read(const Kv4Cache &c, const int32_t *first, const int32_t *lens, const int32_t *table,
+                               int64_t B, int64_t max_pages, int64_t T, void *k_out, void *v_out, int sm_count,
+                               cudaStream_t stream);
+struct Kv4EvictProblem {
+    Kv4Cache from, to;
+    const int32_t *lens, *table, *to_table;
+    int32_t *kept, *new_lens;
+    int64_t B, max_pages, to_max_pages, keep, recent;
+    int sm_count;
+};
+cudaError_t fa_launch_kv4_evict(const Kv4EvictProblem &p, cudaStream_t stream);
+int fa_kv4_cache_take_status(cudaStream_t stream);
+
+// Attention over the 4-bit cache (fa_kv4_decode.cu).
+struct Kv4DecodeProblem {
+    Kv4Cache cache;
+    const void *q;
+    const int32_t *lens, *table;
+    void *o;
+    float *lse;
+    int64_t B, H, n_q, max_pages;
+    float scale;
+    int accumulate;
+    int sm_count;
+};
+// Bytes of workspace for sequences of at most max_pages pages.
+int64_t fa_kv4_decode_workspace(int64_t B, int64_t H, int64_t heads, int64_t n_q, int64_t d, int64_t max_tokens,
+                                int accumulate);
+cudaError_t fa_launch_kv4_decode(const Kv4DecodeProblem &p, void *workspace, cudaStream_t stream);
+int fa_kv4_decode_take_status(cudaStream_t stream);
+
+// Accumulated attention weight of a prompt's keys (fa_key_weights.cu).
+struct FaKeyWeightsProblem {
+    const void *q, *k;
+    const float *lse;
+    float *weights;
+    int64_t B, H, Hkv, N, first_query;
+    int d;
+    float scale;
+    int causal;
+    int sm_count;
+};
+cudaError_t fa_launch_key_weights(const FaKeyWeightsProblem &p, cudaStream_t stream);
+int fa_key_weights_take_status(cudaStream_t stream);
+
 // Forward on host buffers (fa_fwd_host): q, k, v, o, lse are host pointers,
 // *_dev the caller's device staging buffers of the same shapes; the (b, h)
 // slices go in n_groups consecutive groups whose copies in, forward and

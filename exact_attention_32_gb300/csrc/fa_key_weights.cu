@@ -1,0 +1,329 @@
+// Accumulated attention weight of a prompt's keys (fa_key_weights):
+//     w_j = sum over the heads of key head j's group and the queries i of
+//           exp(scale q_i . k_j - LSE_i),
+// the column sums of the softmax matrix, recomputed from the forward's LSE as the
+// backward recomputes it, never stored.
+//
+// One CTA takes 256 keys of one (b, key head) as two tiles of 128 and goes over
+// the group's queries 128 at a time (causal: from the diagonal).  Per query block
+// and key tile S^T = K Q^T is one 128 x 128 x d tcgen05 product with the key as the
+// TMEM lane, so a thread owns a key: it takes exp2(S scale log2e - LSE log2e) of 128
+// queries and adds them up in fp32, with nothing to exchange between threads.
+//
+// What bounds it is the tensor pipe (2 d operations per pair; the exponentials
+// take half the time).  A product whose operands both come from shared memory
+// at N = 128 would need all of its 128 bytes a clock, so K lies in tensor memory
+// as the A operand (2 x d/2 columns, for the CTA's life) and only Q streams
+// through shared memory (TMA, 128-byte swizzle, four stages); a Q block is used for
+// both key tiles.  The other columns hold three 128 x 128 accumulators in turn,
+// so the pipe runs on while the two warpgroups (one per key tile) read theirs.
+// Roles (352 threads): warps 0-3 and 4-7 the warpgroups, warp 8 loads Q, warp 9
+// issues the products and owns the tensor memory, warp 10 loads LSE log2 e.
+//
+// Every mbarrier wait is bounded; one that gives up sets FA_ERR_TIMEOUT in this
+// file's status word and the CTA winds down.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "fa_fwd_common.cuh"
+
+using namespace sm100;
+
+namespace {
+
+constexpr int kKeyTile = 128, kKeys = 256, kQBlock = 128;
+constexpr int kKwThreads = 352, kKwLoad = 8, kKwMma = 9, kKwLse = 10;
+constexpr int kStages = 4;  // Q blocks in shared memory
+constexpr int kBufs = 3;    // accumulators in tensor memory
+
+__device__ int g_key_weights_status;
+__device__ __forceinline__ void kw_report(int code) { atomicExch(&g_key_weights_status, code); }
+
+template <int D>
+struct KwCfg {
+    static constexpr int kStageBytes = kQBlock * D * 2;
+    static constexpr int kLse = kStages * kStageBytes;  // per stage: 128 floats
+    static constexpr int kBar = kLse + kStages * kQBlock * 4;
+    static constexpr int kNumBars = 4 * kStages + 4 * kBufs + 2;
+    static constexpr int kSmemBytes = kBar + kNumBars * 8 + 16;
+};
+// barriers: Q_FULL, Q_FREE (both key tiles' products read it), LSE_FULL, LSE_FREE per stage; S_FULL, S_FREE per
+// (buffer, warpgroup).  Product n (query block n / 2, key tile n % 2) goes to buffer n % 3, so a warpgroup takes a
+// buffer every sixth product; with a barrier of its own it sees every phase of it.
+enum { KW_Q_FULL = 0, KW_Q_FREE = kStages, KW_LSE_FULL = 2 * kStages, KW_LSE_FREE = 3 * kStages,
+       KW_S_FULL = 4 * kStages, KW_S_FREE = 4 * kStages + 2 * kBufs, KW_K_READY = 4 * kStages + 4 * kBufs,
+       KW_MMA_DONE = KW_K_READY + 1 };
+static_assert(kBufs == 3, "the phases below count a warpgroup's uses of a buffer as n / 6");
+__device__ __forceinline__ int kw_slot(int n) { return 2 * (n % kBufs) + (n & 1); }
+
+struct KwArgs {
+    const __nv_bfloat16 *k;
+    const float *lse;
+    float *weights;
+    int N, H, heads, n_kblocks, n_qblocks, first;
+    float scale_log2;
+};
+
+template <int D, bool CAUSAL>
+__global__ void __launch_bounds__(kKwThreads, 1)
+fa_key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const KwArgs a)
+{
+    using C = KwCfg<D>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sb = smem_u32(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if ((sb & 1023u) != 0) {  // the swizzled tiles need a 1024-byte-aligned base
+        if (tid == 0) kw_report(FA_ERR_LAUNCH);
+        return;
+    }
+    const uint32_t bar0 = sb + C::kBar;
+    auto BAR = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kBar + C::kNumBars * 8);
+
+    // key-block major: causal CTAs with many query blocks (small kb) start first
+    const int BHkv = static_cast<int>(gridDim.x) / a.n_kblocks;
+    const int kb = blockIdx.x / BHkv, bhk = blockIdx.x % BHkv;
+    const int k0 = kb * kKeys;
+    const int G = a.H / a.heads;
+    const int qh0 = bhk * G;  // (b, query head) slices of the group: b * H + hkv * G = bhk * G
+    const int qb0 = max(CAUSAL ? k0 / kQBlock : 0, a.first / kQBlock);
+    const int per_head = a.n_qblocks - qb0;
+    const int nq = per_head * G;  // query blocks, head by head
+    const bool run = *reinterpret_cast<volatile int *>(&g_key_weights_status) == 0;
+
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(BAR(KW_Q_FULL + s), 1);
+            mbar_init(BAR(KW_Q_FREE + s), 1);
+            mbar_init(BAR(KW_LSE_FULL + s), 1);
+            mbar_init(BAR(KW_LSE_FREE + s), 8);
+        }
+        for (int s = 0; s < 2 * kBufs; ++s) {
+            mbar_init(BAR(KW_S_FULL + s), 1);
+            mbar_init(BAR(KW_S_FREE + s), 4);
+        }
+        mbar_init(BAR(KW_K_READY), 8);
+        mbar_init(BAR(KW_MMA_DONE), 1);
+        fence_mbar_init();
+    }
+    if (warp == kKwMma) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t tS = tmem, tK = tmem + kBufs * 128;  // K tile w at columns tK + w * 64
+
+    if (!run) {
+        // nothing to do
+    } else if (warp == kKwLoad) {
+        if (lane == 0) {
+            prefetch_tmap(&tm_q);
+            bool ok = true;
+            int issued = 0;
+            for (int i = 0; i < nq; ++i) {
+                const int st = i % kStages;
+                if (i >= kStages && !(ok = mbar_wait(BAR(KW_Q_FREE + st), (i / kStages - 1) & 1, kWaitLimitNs))) break;
+                mbar_arrive_expect_tx(BAR(KW_Q_FULL + st), C::kStageBytes);
+                for (int c = 0; c < D / 64; ++c)
+                    tma_load_3d(sb + st * C::kStageBytes + c * 16384, &tm_q, BAR(KW_Q_FULL + st), c * 64,
+                                (qb0 + i % per_head) * kQBlock, qh0 + i / per_head);
+                ++issued;
+            }
+            if (!ok) kw_report(FA_ERR_TIMEOUT);
+            // no copy in flight when the CTA ends
+            for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+                mbar_wait(BAR(KW_Q_FULL + i % kStages), (i / kStages) & 1, ok ? kWaitLimitNs : kCleanupLimitNs);
+        }
+    } else if (warp == kKwLse) {
+        // -LSE log2 e of each query; -inf (weight 0) for rows past N, before first, or without a key
+        bool ok = true;
+        for (int i = 0; i < nq && ok; ++i) {
+            const int st = i % kStages;
+            if (i >= kStages && !(ok = mbar_wait_warp(BAR(KW_LSE_FREE + st), (i / kStages - 1) & 1, kWaitLimitNs))) break;
+            const int q0 = (qb0 + i % per_head) * kQBlock;
+            const float *src = a.lse + static_cast<int64_t>(qh0 + i / per_head) * a.N;
+            float *dst = reinterpret_cast<float *>(smem + C::kLse) + st * kQBlock;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int q = q0 + j * 32 + lane;
+                float x = -INFINITY;
+                if (q < a.N && q >= a.first) {
+                    x = src[q];
+                    x = x == -INFINITY ? x : -x * 1.4426950408889634f;
+                }
+                dst[j * 32 + lane] = x;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(KW_LSE_FULL + st));
+        }
+        if (!ok && lane == 0) kw_report(FA_ERR_TIMEOUT);
+    } else if (warp == kKwMma) {
+        if (lane == 0) {
+            constexpr uint32_t id = idesc_bf16_f32(kKeyTile, kQBlock, false);
+            const uint64_t dq = smem_desc_sw128(sb, 16, 1024);
+            const uint32_t q_lo = static_cast<uint32_t>(dq), q_hi = static_cast<uint32_t>(dq >> 32);
+            bool ok = mbar_wait(BAR(KW_K_READY), 0, kWaitLimitNs);
+            tc_fence_after();
+            int n = 0;  // products so far
+            for (int i = 0; i < nq && ok; ++i) {
+                const int st = i % kStages;
+                if (!(ok = mbar_wait(BAR(KW_Q_FULL + st), (i / kStages) & 1, kWaitLimitNs))) break;
+                const uint32_t b_lo = q_lo + st * (C::kStageBytes >> 4);
+                for (int w = 0; w < 2; ++w, ++n) {
+                    const int buf = n % kBufs;
+                    const int last = n - kBufs;  // the buffer's product before this one
+                    if (last >= 0 && !(ok = mbar_wait(BAR(KW_S_FREE + kw_slot(last)), (last / 6) & 1, kWaitLimitNs))) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        mma_ts_lohi(tS + buf * 128, tK + w * 64 + kk * 8,
+                                    b_lo + (((kk / 4) * 16384 + (kk % 4) * 32) >> 4), q_hi, id, kk > 0 ? 1u : 0u);
+                    mma_commit(BAR(KW_S_FULL + kw_slot(n)));
+                }
+                if (!ok) break;
+                mma_commit(BAR(KW_Q_FREE + st));
+            }
+            if (!ok) kw_report(FA_ERR_TIMEOUT);
+            mma_commit(BAR(KW_MMA_DONE));
+            mbar_wait(BAR(KW_MMA_DONE), 0, ok ? kWaitLimitNs : kCleanupLimitNs);
+        }
+    } else {
+        // ------------------------------------------------ one warpgroup per key tile, one thread per key
+        const int w = warp >> 2;
+        const int key = k0 + w * kKeyTile + (warp & 3) * 32 + lane;
+        const uint32_t loff = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        // K row into tensor memory: bf16 pairs, channel 2c, 2c + 1 in column c
+        {
+            const uint4 *src = reinterpret_cast<const uint4 *>(a.k + (static_cast<int64_t>(bhk) * a.N + key) * D);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+                uint32_t x[32];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    uint4 u = make_uint4(0, 0, 0, 0);
+                    if (key < a.N) u = src[c * 8 + j];
+                    x[4 * j] = u.x;
+                    x[4 * j + 1] = u.y;
+                    x[4 * j + 2] = u.z;
+                    x[4 * j + 3] = u.w;
+                }
+                tmem_st32(tK + w * 64 + loff + c * 32, x);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(KW_K_READY));
+        }
+        const float2 sc = make_float2(a.scale_log2, a.scale_log2);
+        float total = 0.f;
+        bool ok = true;
+        for (int i = 0; i < nq && ok; ++i) {
+            const int st = i % kStages, n = 2 * i + w, buf = n % kBufs;
+            const int q0 = (qb0 + i % per_head) * kQBlock;
+            if (!mbar_wait_warp(BAR(KW_LSE_FULL + st), (i / kStages) & 1, kWaitLimitNs) ||
+                !mbar_wait_warp(BAR(KW_S_FULL + kw_slot(n)), (n / 6) & 1, kWaitLimitNs)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const float *ls = reinterpret_cast<const float *>(smem + C::kLse) + st * kQBlock;
+            // sums of one block in their own registers first: 128 terms, then one addition to the total
+            float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+            const bool diag = CAUSAL && q0 < k0 + w * kKeyTile + kKeyTile - 1;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t x[32];
+                tmem_ld32(tS + buf * 128 + loff + c * 32, x);
+                tmem_wait_ld();
+                if (c == 3) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(BAR(KW_S_FREE + kw_slot(n)));
+                }
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    const float4 l = *reinterpret_cast<const float4 *>(ls + c * 32 + j);
+                    const float2 y0 = fma2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), sc,
+                                           make_float2(l.x, l.y));
+                    const float2 y1 = fma2(make_float2(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3])), sc,
+                                           make_float2(l.z, l.w));
+                    float2 p0 = make_float2(ex2(y0.x), ex2(y0.y)), p1 = make_float2(ex2(y1.x), ex2(y1.y));
+                    if (diag) {
+                        const int q = q0 + c * 32 + j;
+                        if (key > q) p0.x = 0.f;
+                        if (key > q + 1) p0.y = 0.f;
+                        if (key > q + 2) p1.x = 0.f;
+                        if (key > q + 3) p1.y = 0.f;
+                    }
+                    s0 = add2(s0, p0);
+                    s1 = add2(s1, p1);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(KW_LSE_FREE + st));
+            total += (s0.x + s0.y) + (s1.x + s1.y);
+        }
+        if (!ok && lane == 0) kw_report(FA_ERR_TIMEOUT);
+        if (ok && key < a.N) a.weights[static_cast<int64_t>(bhk) * a.N + key] = total;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kKwMma) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D, bool CAUSAL>
+cudaError_t launch_kw(const FaKeyWeightsProblem &p, cudaStream_t s)
+{
+    using C = KwCfg<D>;
+    CUtensorMap mq;
+    if (!make_map(&mq, p.q, p.B * p.H, p.N, D)) return cudaErrorInvalidValue;
+    cudaError_t e = set_max_dynamic_smem<fa_key_weights_kernel<D, CAUSAL>>(C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    KwArgs a;
+    a.k = static_cast<const __nv_bfloat16 *>(p.k);
+    a.lse = p.lse;
+    a.weights = p.weights;
+    a.N = static_cast<int>(p.N);
+    a.H = static_cast<int>(p.H);
+    a.heads = static_cast<int>(p.Hkv);
+    a.n_kblocks = static_cast<int>((p.N + kKeys - 1) / kKeys);
+    a.n_qblocks = static_cast<int>((p.N + kQBlock - 1) / kQBlock);
+    a.first = static_cast<int>(p.first_query);
+    a.scale_log2 = static_cast<float>(static_cast<double>(p.scale) * 1.4426950408889634);
+    const int64_t grid = p.B * p.Hkv * a.n_kblocks;
+    if (grid > 0x7fffffffLL || p.B * p.H > 0x7fffffffLL || (p.H / p.Hkv) * a.n_qblocks > 0x3fffffffLL)
+        return cudaErrorInvalidConfiguration;
+    fa_key_weights_kernel<D, CAUSAL><<<static_cast<unsigned>(grid), kKwThreads, C::kSmemBytes, s>>>(mq, a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t fa_launch_key_weights(const FaKeyWeightsProblem &p, cudaStream_t s)
+{
+    if (p.d == 64) return p.causal ? launch_kw<64, true>(p, s) : launch_kw<64, false>(p, s);
+    return p.causal ? launch_kw<128, true>(p, s) : launch_kw<128, false>(p, s);
+}
+
+int fa_key_weights_take_status(cudaStream_t stream)
+{
+    int h = 0;
+    const int zero = 0;
+    if (cudaMemcpyFromSymbolAsync(&h, g_key_weights_status, sizeof(int), 0, cudaMemcpyDeviceToHost, stream) !=
+            cudaSuccess ||
+        cudaMemcpyToSymbolAsync(g_key_weights_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, stream) !=
+            cudaSuccess ||
+        cudaStreamSynchronize(stream) != cudaSuccess) {
+        cudaGetLastError();
+        return FA_ERR_LAUNCH;
+    }
+    return h;
+}

@@ -45,8 +45,10 @@ enum fa_status {
     FA_ERR_ARCH = 4,        /* the current device is not compute capability 10.3 */
     FA_ERR_LAUNCH = 5,      /* the kernel launch itself failed (CUDA error) */
     FA_ERR_TIMEOUT = 6,     /* a bounded in-kernel wait gave up (see fa_get_device_status) */
-    FA_ERR_WORKSPACE_LIMIT = 7 /* fa_fwd_splitkv_noalloc: the problem needs more scratch
-                                  than FA_SPLITKV_NOALLOC_MAX_BYTES */
+    FA_ERR_WORKSPACE_LIMIT = 7, /* fa_fwd_splitkv_noalloc: the problem needs more scratch
+                                   than FA_SPLITKV_NOALLOC_MAX_BYTES */
+    FA_ERR_BAD_PAGE = 8 /* reported by fa_get_device_status: a kernel met a page index or a
+                           length outside its 4-bit cache and left that part out */
 };
 
 /* Size of the library-owned scratch array behind fa_fwd_splitkv_noalloc. */
@@ -374,10 +376,144 @@ int fa_bwd(const void *q, const void *k, const void *v, const void *o, const flo
 int64_t fa_bwd_workspace_bytes(int64_t B, int64_t H, int64_t N, int64_t d);
 
 /*
+ * The 4-bit KV cache: keys and values of many sequences in pages of a shared
+ * pool, for single-token serving (fa_fwd_kv4), which reads all of it for every
+ * token and is bound by those bytes.  Nothing on the pages describes it; the
+ * entry points are this library's own.
+ *
+ * Format.  A row is one token of one key head.  Its d values are E2M1 codes
+ * (0, .5, 1, 1.5, 2, 3, 4, 6 and a sign bit), two a byte, the even channel in
+ * the low nibble.  K has one scale per 32 channels, V one per row.  A scale is one
+ * byte, the top bits of a half without its sign (value half(byte << 7)):
+ * s = amax / 6 rounded to nearest even on that grid, at most 10240; a code is
+ * x / s rounded to nearest even, at most 6.  Values beyond 61440 saturate; a block
+ * whose amax is below 6 * 2^-18 becomes zeros; a block that holds a NaN or an
+ * infinity gets scale 255 and reads back as NaN.
+ *
+ * Pages hold page_size tokens (a power of two, 16..1024) of every key head:
+ *   k, v    : uint8 [n_pages][Hkv][page_size][d / 2], 16-byte aligned
+ *   k_scale : uint8 [n_pages][Hkv][page_size][d / 32], 16-byte aligned
+ *   v_scale : uint8 [n_pages][Hkv][page_size], 16-byte aligned
+ *   weights : fp32  [n_pages][Hkv][page_size], 16-byte aligned, or NULL: the
+ *             accumulated attention weight of each key
+ *   n_pages : 1 .. 2^31 - 1;  Hkv : key heads;  d : 64 or 128 (else
+ *             FA_ERR_UNSUPPORTED); n_pages * Hkv * page_size * d < 2^44
+ *
+ * Token j of sequence b lives in page page_table[b][j / page_size] at slot
+ * j % page_size, for 0 <= j < lens[b].  page_table is a device int32
+ * [B][max_pages], lens a device int32 [B]; entries of the table past a
+ * sequence's last page are not read.  A page index outside the pool, or a length
+ * outside [0, max_pages * page_size], cannot be refused by the host: the kernels
+ * leave such a page's tokens out, hold the length to the range, and report
+ * FA_ERR_BAD_PAGE through fa_get_device_status (later calls run as usual).
+ * Several sequences may share pages that are only read.  A page that a call writes
+ * (append, evict's destination, weights under accumulate) must appear once.
+ */
+typedef struct fa_kv4_cache {
+    void *k, *v, *k_scale, *v_scale;
+    float *weights;
+    int64_t n_pages, Hkv, page_size, d;
+} fa_kv4_cache;
+
+/*
+ * fa_kv4_append - quantise new tokens into the cache.
+ *
+ *   k_new, v_new : const bf16 [B][Hkv][S][d], 16-byte aligned
+ *   w_new  : const fp32 [B][Hkv][S] initial weights of the new tokens (4-byte
+ *            aligned), or NULL for 0; needs cache->weights
+ *   n_new  : const int32 [B], how many of the S tokens sequence b gains (held to
+ *            [0, S]), or NULL for S
+ *   lens   : lengths AFTER the append: token i goes to position
+ *            lens[b] - n_new[b] + i (tokens whose position is negative are
+ *            dropped and reported as FA_ERR_BAD_PAGE)
+ * Everything else in the pages is left as it was.
+ */
+int fa_kv4_append(const fa_kv4_cache *cache, const void *k_new, const void *v_new, const float *w_new,
+                  const int32_t *n_new, const int32_t *lens, const int32_t *page_table, int64_t B,
+                  int64_t S, int64_t max_pages, void *stream);
+
+/*
+ * fa_kv4_read - rows of the cache as bf16 (exact: a stored value has at most 6
+ * significant bits), for what takes contiguous K and V.
+ *
+ *   first : const int32 [B], first position of sequence b (negative ones and
+ *           those past the length give zero rows), or NULL for 0
+ *   T     : rows per sequence, >= 1
+ *   k_out, v_out : bf16 [B][Hkv][T][d]; rows at or past lens[b] are zero.
+ */
+int fa_kv4_read(const fa_kv4_cache *cache, const int32_t *first, const int32_t *lens,
+                const int32_t *page_table, int64_t B, int64_t max_pages, int64_t T, void *k_out,
+                void *v_out, void *stream);
+
+/*
+ * fa_fwd_kv4 - attention of the newest n_q tokens of each sequence over its
+ * cache (their own keys and values already appended):
+ * query t (0 <= t < n_q) of sequence b admits the keys j <= lens[b] - n_q + t.
+ * Query head h reads key head h / (H / Hkv).  O = softmax(scale q K^T) V and LSE
+ * as fa_fwd; a row that admits no key gets O = 0, LSE = -inf.
+ *
+ *   q   : const bf16 [B][H][n_q][d];  o : bf16 out, same shape;  lse : fp32 out [B][H][n_q]
+ *   H   : query heads, a multiple of Hkv;  n_q : 1..64, H / Hkv * n_q <= 1024
+ *   accumulate : 1 adds each key's weight over this call's rows of its head,
+ *         sum exp(scale q.k_j - LSE), to cache->weights; 0 leaves them alone
+ *   workspace : device scratch, 16-byte aligned, at least
+ *         fa_fwd_kv4_workspace_bytes(...) bytes; contents on entry do not
+ *         matter.  Calls that share one must be ordered on one stream (or by
+ *         events): two that overlap race on it.
+ * Keys are read once per 32 rows of a key head; the split of a sequence's keys
+ * depends on the sizes alone, and so do the results, bit for bit.
+ */
+int fa_fwd_kv4(const void *q, const fa_kv4_cache *cache, const int32_t *lens, const int32_t *page_table,
+               void *o, float *lse, int64_t B, int64_t H, int64_t n_q, int64_t max_pages, float scale,
+               int accumulate, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Workspace bytes fa_fwd_kv4 needs for sequences of at most max_tokens =
+ * max_pages * page_size tokens, or -1 for invalid sizes.  Pure host computation. */
+int64_t fa_fwd_kv4_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t n_q, int64_t d,
+                                   int64_t max_tokens, int accumulate);
+
+/*
+ * fa_kv4_evict - keep `keep` tokens of every (sequence, key head): the last
+ * `recent` ones, and of the others those with the largest weights (ties: the lowest
+ * position; a NaN counts as larger than every number), in their order, as rows
+ * 0, 1, ... of the pages of to_table.  A sequence of at most `keep` tokens is
+ * copied whole.
+ *
+ *   from, to : caches of the same Hkv, page_size, d, with weights; the same pool
+ *         or two.  The pages of to_table must not hold tokens that are read.
+ *   lens, page_table, max_pages : of `from`
+ *   to_table : const int32 [B][to_max_pages], to_max_pages * page_size >= keep
+ *   keep : >= 1;  recent : 0 .. keep
+ *   kept : int32 out [B][Hkv][keep], the positions kept, ascending, -1 past the end
+ *   new_lens : int32 out [B], min(lens[b], keep)
+ */
+int fa_kv4_evict(const fa_kv4_cache *from, const int32_t *lens, const int32_t *page_table,
+                 int64_t max_pages, const fa_kv4_cache *to, const int32_t *to_table,
+                 int64_t to_max_pages, int64_t B, int64_t keep, int64_t recent, int32_t *kept,
+                 int32_t *new_lens, void *stream);
+
+/*
+ * fa_key_weights - the attention weight that each key of a prompt has gathered,
+ * from fa_fwd's LSE (what a cache starts its weights from):
+ *     w_j = sum over the query heads h of key head j's group and the queries
+ *           i >= first_query (causal: i >= j) of exp(scale q_hi . k_j - LSE_hi).
+ *
+ *   q : const bf16 [B][H][N][d];  k : const bf16 [B][Hkv][N][d], H a multiple of
+ *       Hkv, query head h reading key head h / (H / Hkv);  lse : const fp32 [B][H][N]
+ *   weights : fp32 out [B][Hkv][N], overwritten
+ *   first_query : 0 .. N - 1
+ * A query whose LSE is -inf (it admitted no key) adds nothing.  Alignment as
+ * fa_fwd (lse and weights 4 bytes).  Errors as fa_fwd.
+ */
+int fa_key_weights(const void *q, const void *k, const float *lse, float *weights, int64_t B, int64_t H,
+                   int64_t Hkv, int64_t N, int64_t d, float scale, int causal, int64_t first_query,
+                   void *stream);
+
+/*
  * fa_get_device_status - synchronise `stream`, then return and clear the
  * current device's sticky in-kernel status (FA_OK, or FA_ERR_TIMEOUT when a
  * bounded wait inside a kernel gave up and the kernel returned early, leaving
- * its outputs incomplete).  While FA_ERR_TIMEOUT is set, fa_fwd launches do
+ * its outputs incomplete; or FA_ERR_BAD_PAGE, see the 4-bit cache).  While FA_ERR_TIMEOUT is set, fa_fwd launches do
  * no work (their outputs are left unwritten) until this call clears it.
  * Returns FA_ERR_LAUNCH if the synchronisation itself reports a CUDA error.
  */

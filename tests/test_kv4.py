@@ -1,0 +1,689 @@
+"""The 4-bit KV cache: append, read, attention, eviction, and key weights.
+
+Everything that is whole numbers or moved bytes is compared exactly with the
+fp64 reference (oracle/kv4.py).  Computed outputs are compared within bounds
+made of the formats, per output:
+
+S    a score is a sum of d products, exact in the MMA's inputs, added in fp32: each of
+     the at most d + 4 additions is off by at most 2^-23 of the largest partial
+     sum (the tensor cores truncate), which sum |q k| scale bounds.  Its product
+     with scale log2 e and the subtraction of the maximum round by 2^-24 each.
+     eS = (d + 8) 2^-23 sum |q k| scale.
+LSE  its scores' error, and fp32's: eS + 2^-22 (|LSE| + 1).
+w    a probability is off by the factor exp(eS + error of LSE) and the exponential's 2^-22:
+     w (2 eS + 2^-21 (|LSE| + 2)), a sum of n rows in fp32 adds n 2^-24.
+O    the weights' relative error on sum p |v|, P's rounding to a half (half a step: 2^-11; a
+     subnormal half loses at most 2^-25 of p times V's scale times 4, which a code of at most 6 multiplies: 1.5 2^-25 a key), and bf16's
+     rounding of the result (eight significant bits: half a step is 2^-8 of the value).
+"""
+import numpy as np
+import pytest
+import torch
+
+import exact_attention_32_gb300 as fa
+from oracle import kv4 as ref
+
+gpu = pytest.mark.gpu
+
+
+def dev(x):
+    return torch.as_tensor(np.ascontiguousarray(x)).cuda()
+
+
+def bf16(x):
+    return torch.as_tensor(np.asarray(x, dtype=np.float32)).bfloat16()
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+class Pool:
+    """A filled cache with the pages of B sequences shuffled in it, unused pages and slots holding rubbish: any code,
+    and scale 255 (NaN).  `lens` may be shorter than what is stored."""
+
+    def __init__(self, B, Hkv, d, P, stored, seed, spare=2, gain=1.0):
+        rng = np.random.default_rng(seed)
+        self.B, self.Hkv, self.d, self.P = B, Hkv, d, P
+        stored = np.asarray(stored)
+        self.cols = max(1, -(-int(stored.max()) // P)) + 1
+        need = [-(-int(n) // P) for n in stored]
+        order = rng.permutation(sum(need) + spare)
+        self.n_pages = len(order)
+        self.table = np.full((B, self.cols), -7, dtype=np.int32)  # entries past the last page are never read
+        at = 0
+        for b, n in enumerate(need):
+            self.table[b, :n] = order[at:at + n]
+            at += n
+        shape = (self.n_pages, Hkv, P)
+        self.k = rng.integers(0, 256, (*shape, d // 2), dtype=np.uint8)
+        self.v = rng.integers(0, 256, (*shape, d // 2), dtype=np.uint8)
+        self.ks = np.full((*shape, d // 32), 255, dtype=np.uint8)
+        self.vs = np.full(shape, 255, dtype=np.uint8)
+        self.w = rng.random(shape, dtype=np.float32)
+        for b, n in enumerate(stored):
+            if n:
+                j = np.arange(n)
+                pg, sl = self.table[b, j // P], j % P
+                k, ks = ref.quantise(f64(bf16(gain * rng.standard_normal((n, Hkv, d)))), 32)
+                v, vs = ref.quantise(f64(bf16(gain * rng.standard_normal((n, Hkv, d)))), d)
+                self.k[pg, :, sl], self.ks[pg, :, sl] = k, ks
+                self.v[pg, :, sl], self.vs[pg, :, sl] = v, vs[..., 0]
+
+    def cache(self):
+        return fa.KV4Cache(dev(self.k), dev(self.v), dev(self.ks), dev(self.vs), dev(self.w))
+
+    def kv(self, b, n):
+        r = lambda t: ref.rows(t, self.table[b], n, self.P)  # noqa: E731
+        return ref.values(r(self.k), r(self.ks)), ref.values(r(self.v), r(self.vs)[..., None])
+
+
+def ok():
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_status(0) == 0
+
+
+# ------------------------------------------------------------------- the reference (CPU)
+
+def test_reference_rounds_to_the_nearest_value_of_the_grid():
+    rng = np.random.default_rng(0)
+    x = f64(bf16(rng.standard_normal((50, 64)) * np.exp(4 * rng.standard_normal((50, 1)))))
+    code, s = ref.quantise(x, 32)
+    y = ref.values(code, s).reshape(50, 2, 32)
+    step = ref.SCALES[s][..., None]
+    grid = np.concatenate([-ref.E2M1[::-1], ref.E2M1]) * step[..., None]
+    best = np.abs(x.reshape(50, 2, 32)[..., None] - grid).min(-1)
+    assert (np.abs(x.reshape(50, 2, 32) - y) == best).all()
+
+
+def test_reference_attention_is_the_textbook_softmax():
+    rng = np.random.default_rng(1)
+    q, k, v = rng.standard_normal((4, 3, 8)), rng.standard_normal((2, 5, 8)), rng.standard_normal((2, 5, 8))
+    r = ref.attention(q, k, v, 0.3, 5)
+    e = np.exp(0.3 * k[1, :4] @ q[3, 1])
+    assert np.allclose(r["o"][3, 1], e / e.sum() @ v[1, :4], atol=1e-14) and np.isclose(r["lse"][3, 1], np.log(e.sum()))
+    assert np.isclose(r["weights"].sum(), 4 * 3) and r["weights"][0, 4] < r["weights"].sum()
+
+
+def test_reference_eviction_orders_ties_and_nan():
+    w = np.array([1.0, 3.0, 3.0, np.nan, 0.0, 3.0, 9.0, 9.0])
+    assert ref.evict(w, 8, 5, 2).tolist() == [1, 2, 3, 6, 7]
+    assert ref.evict(w, 8, 8, 0).tolist() == list(range(8)) and ref.evict(w, 3, 5, 1).tolist() == [0, 1, 2]
+
+
+# -------------------------------------------------------------------------- refusals (CPU)
+
+def _struct(**kw):
+    f = dict(k=1 << 12, v=1 << 13, k_scale=1 << 14, v_scale=1 << 15, weights=1 << 16, n_pages=8, Hkv=2, page_size=16, d=64)
+    f.update(kw)
+    return fa.KV4CacheStruct(*[f[n] for n, _ in fa.KV4CacheStruct._fields_])
+
+
+BAD_CACHES = [(dict(n_pages=0), 1), (dict(n_pages=1 << 31), 1), (dict(Hkv=0), 1), (dict(Hkv=1 << 21), 1),
+              (dict(page_size=8), 1), (dict(page_size=48), 1), (dict(page_size=2048), 1), (dict(d=0), 1), (dict(d=96), 2),
+              (dict(n_pages=1 << 30, Hkv=1 << 10), 1)]
+
+
+@pytest.mark.parametrize("kw,code", BAD_CACHES)
+def test_bad_caches_are_refused_before_any_device_call(kw, code):
+    c, p = _struct(**kw), 1 << 20
+    assert fa.fa_kv4_append(c, p, p, None, None, p, p, 1, 1, 1, 0) == code
+    assert fa.fa_kv4_read(c, None, p, p, 1, 1, 1, p, p, 0) == code
+    assert fa.fa_fwd_kv4(p, c, p, p, p, p, 1, 2, 1, 1, 0.1, 0, p, 1 << 40, 0) == code
+    assert fa.fa_kv4_evict(c, p, p, 1, c, p, 1, 1, 1, 0, p, p, 0) == code
+    assert fa.fa_kv4_evict(_struct(), p, p, 1, c, p, 1, 1, 1, 0, p, p, 0) == code
+
+
+def test_bad_arguments_are_refused_before_any_device_call():
+    p, c, none = 1 << 20, _struct(), _struct(weights=None)
+    INV = 1
+    for B, S, pages in [(0, 1, 1), (1, 0, 1), (1, 1, 0), (1 << 40, 1, 1), (1, 1 << 31, 1), (1, 1, 1 << 31)]:
+        assert fa.fa_kv4_append(c, p, p, None, None, p, p, B, S, pages, 0) == INV
+        assert fa.fa_kv4_read(c, None, p, p, B, pages, S, p, p, 0) == INV
+    assert fa.fa_kv4_append(none, p, p, p, None, p, p, 1, 1, 1, 0) == INV  # weights for a cache without
+    ws = 1 << 40
+    for kw in [dict(B=0), dict(H=0), dict(H=3), dict(n_q=0), dict(n_q=65), dict(H=2 * 512, n_q=3), dict(pages=0),
+               dict(scale=0.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(acc=2), dict(ws=255)]:
+        a = dict(B=1, H=2, n_q=1, pages=1, scale=0.1, acc=0, ws=ws)
+        a.update(kw)
+        assert fa.fa_fwd_kv4(p, c, p, p, p, p, a["B"], a["H"], a["n_q"], a["pages"], a["scale"], a["acc"], p, a["ws"], 0) == INV
+    assert fa.fa_fwd_kv4(p, none, p, p, p, p, 1, 2, 1, 1, 0.1, 1, p, ws, 0) == INV
+    for other in [_struct(Hkv=3), _struct(page_size=32), _struct(d=128), none]:
+        assert fa.fa_kv4_evict(c, p, p, 1, other, p, 1, 1, 1, 0, p, p, 0) == INV
+    for keep, recent in [(0, 0), (17, 0), (4, 5), (4, -1)]:
+        assert fa.fa_kv4_evict(c, p, p, 1, c, p, 1, 1, keep, recent, p, p, 0) == INV
+    for kw in [dict(H=0), dict(Hkv=0), dict(H=3), dict(N=0), dict(scale=-1.0), dict(causal=2), dict(first=-1), dict(first=8)]:
+        a = dict(B=1, H=2, Hkv=2, N=8, d=64, scale=0.1, causal=0, first=0)
+        a.update(kw)
+        assert fa.fa_key_weights(p, p, p, p, *a.values(), 0) == INV
+    assert fa.fa_key_weights(p, p, p, p, 1, 2, 2, 8, 96, 0.1, 0, 0, 0) == 2
+
+
+def test_workspace_bytes():
+    f = fa.fa_fwd_kv4_workspace_bytes
+    assert f(1, 8, 2, 1, 96, 64, 0) == -1 and f(1, 7, 2, 1, 64, 64, 0) == -1 and f(1, 8, 2, 0, 64, 64, 0) == -1
+    small, long = f(1, 8, 2, 1, 64, 64, 0), f(1, 8, 2, 1, 64, 1 << 17, 0)
+    assert 0 < small < long and f(1, 8, 2, 1, 64, 1 << 17, 1) >= long + 8 * (1 << 17) * 4
+
+
+def test_python_calls_refuse_wrong_tensors():
+    c = fa.kv4_cache(2, 1, 16, 64, device="cpu")
+    i = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        fa.kv4_read(c, i, i[None], 1)  # not on a CUDA device
+    with pytest.raises(ValueError):
+        fa.kv4_read(c._replace(v=c.v[:1]), i, i[None], 1)
+    with pytest.raises(ValueError):
+        fa.kv4_read(c._replace(k=c.k[0]), i, i[None], 1)
+    with pytest.raises(fa.FAError):
+        fa.kv4_cache(2, 1, 16, 96, device="cpu")
+    with pytest.raises(ValueError):
+        fa.key_weights(torch.zeros(1, 3, 8, 64).bfloat16(), torch.zeros(1, 2, 8, 64).bfloat16(), torch.zeros(1, 3, 8))
+
+
+# ------------------------------------------------------------------------------- append, read
+
+SPECIAL = np.array([0.0, -0.0, 1e-30, 2.0 ** -18 * 6, 2.0 ** -17 * 5, 3e-4, 0.1, 1.0, 5.0, 6.0, 448.0, 61440.0, 65000.0, 3e38])
+
+
+def _hard_rows(rng, n, d):
+    """Rows whose blocks have every size, values in the middle of two codes, zeros, and non-finite ones."""
+    x = rng.standard_normal((n, d)) * np.exp(5 * rng.standard_normal((n, 1)))
+    x[0] = 0
+    mid = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0])
+    for i in range(1, min(n, 12)):  # middles times a scale of four significant bits: exact in bf16
+        s = (8 + rng.integers(0, 8)) / 8 * 2.0 ** rng.integers(-14, 9)
+        x[i] = np.tile(mid, d // 8) * s * np.where(rng.random(d) < 0.5, -1, 1)
+    for i in range(12, min(n, 12 + len(SPECIAL))):
+        x[i] = SPECIAL[i - 12] * np.where(rng.random(d) < 0.5, -1, rng.random(d))
+    if n > 30:
+        x[27, 3], x[28, d - 1], x[29, 5] = np.nan, np.inf, -np.inf
+    return x
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,Hkv,S,P", [(1, 1, 1, 16), (3, 2, 37, 16), (2, 5, 130, 64), (1, 3, 300, 1024)])
+def test_append_writes_the_reference_codes_and_nothing_else(B, Hkv, S, P, d):
+    rng = np.random.default_rng(B * 1000 + S + d)
+    k = bf16(np.stack([_hard_rows(rng, Hkv * S, d) for _ in range(B)]).reshape(B, Hkv, S, d))
+    v = bf16(np.stack([_hard_rows(rng, Hkv * S, d) for _ in range(B)]).reshape(B, Hkv, S, d))
+    n_new = rng.integers(0, S + 1, B)
+    n_new[0] = S
+    lens = n_new + rng.integers(0, 50, B)
+    pool = Pool(B, Hkv, d, P, lens, seed=S)
+    w = rng.random((B, Hkv, S), dtype=np.float32)
+    for given in (True, False):
+        c = pool.cache()
+        fa.kv4_append(c, k.cuda(), v.cuda(), dev(lens.astype(np.int32)), dev(pool.table), n_new=dev(n_new.astype(np.int32)),
+                      weights=dev(w) if given else None)
+        ok()
+        want = [pool.k.copy(), pool.v.copy(), pool.ks.copy(), pool.vs.copy(), pool.w.copy()]
+        for b in range(B):
+            n = n_new[b]
+            j = np.arange(lens[b] - n, lens[b])
+            pg, sl = pool.table[b, j // P], j % P
+            kc, ks = ref.quantise(f64(k[b, :, :n]), 32)
+            vc, vs = ref.quantise(f64(v[b, :, :n]), d)
+            for t, x in zip(want, (kc, vc, ks, vs[..., 0], w[b, :, :n] if given else 0 * w[b, :, :n])):
+                t[pg, :, sl] = np.moveaxis(x, 0, 1)
+        for got, t in zip(c, want):
+            assert torch.equal(got.cpu(), torch.as_tensor(t))
+
+
+@gpu
+def test_append_without_counts_or_weights():
+    B, Hkv, S, d, P = 2, 2, 3, 64, 16
+    pool = Pool(B, Hkv, d, P, [3, 20], seed=5)
+    x = bf16(np.random.default_rng(6).standard_normal((B, Hkv, S, d)))
+    c = pool.cache()._replace(weights=None)
+    fa.kv4_append(c, x.cuda(), x.cuda(), dev(np.array([3, 20], np.int32)), dev(pool.table))
+    ok()
+    kc, _ = ref.quantise(f64(x), 32)
+    got = c.k.cpu().numpy()
+    for b, at in ((0, 0), (1, 17)):
+        for i in range(S):
+            j = at + i
+            assert (got[pool.table[b, j // P], :, j % P] == kc[b, :, i]).all()
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("P", [16, 128])
+def test_read_gives_the_stored_values_and_zeros_behind_them(P, d):
+    lens = np.array([0, 1, 16, 77, 200], np.int32)
+    pool = Pool(5, 3, d, P, lens, seed=d + P)
+    first = np.array([0, 0, 5, -3, 190], np.int32)
+    k, v = fa.kv4_read(pool.cache(), dev(lens), dev(pool.table), 33, first=dev(first))
+    ok()
+    for b in range(5):
+        kk, vv = pool.kv(b, lens[b])
+        for i in range(33):
+            j = first[b] + i
+            for got, x in ((k, kk), (v, vv)):
+                assert (f64(got[b, :, i]) == (x[:, j] if 0 <= j < lens[b] else 0)).all()
+    k0, _ = fa.kv4_read(pool.cache(), dev(lens), dev(pool.table), 300)
+    assert torch.equal(k0[4, :, 190:200], k[4, :, :10]) and (k0[4, :, 200:] == 0).all()
+
+
+# ----------------------------------------------------------------------------------- attention
+
+def check_attention(pool, q, lens, scale, o, lse, w_before=None, w_after=None, gone=()):
+    B, H, n_q, d = q.shape
+    o, lse, qd = f64(o), f64(lse), f64(q)
+    want_w = None if w_before is None else w_before.astype(np.float64)
+    tol_w = None if w_before is None else np.zeros_like(want_w)
+    for b in range(B):
+        n = int(lens[b])
+        k, v = pool.kv(b, n)
+        r = ref.attention(qd[b], k, v, scale, n)
+        eS = (d + 8) * 2.0 ** -23 * r["reach"]
+        none = r["lse"] == -np.inf
+        assert (lse[b][none] == -np.inf).all() and (o[b][none] == 0).all()
+        live = ~none
+        top = np.where(live, np.abs(r["lse"]), 0)
+        assert (np.abs(lse[b][live] - r["lse"][live]) <= (eS + 2.0 ** -22 * (top + 1))[live]).all()
+        rel = 2 * eS + 2.0 ** -21 * (top + 2)
+        tol = (rel + 2.0 ** -11)[..., None] * r["spread"] + 2.0 ** -24 * n + 2.0 ** -8 * np.abs(r["o"])
+        err = np.abs(o[b] - r["o"])
+        assert (err <= tol).all(), (b, (err / np.maximum(tol, 1e-300)).max())
+        if want_w is not None and n:
+            j = np.arange(n)
+            pg, sl = pool.table[b, j // pool.P], j % pool.P
+            want_w[pg, :, sl] += r["weights"].T
+            G = H // pool.Hkv
+            worst = rel.reshape(pool.Hkv, G * n_q).max(-1)
+            tol_w[pg, :, sl] = (r["weights"] * worst[:, None]).T + 2.0 ** -24 * (G * n_q + 2) * want_w[pg, :, sl]
+    if want_w is not None:
+        assert (np.abs(w_after - want_w) <= tol_w).all()
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hkv,G,n_q", [(1, 1, 1), (2, 4, 1), (1, 8, 1), (3, 7, 1), (2, 1, 5), (1, 3, 4), (2, 16, 1),
+                                       (1, 8, 3), (1, 16, 8), (2, 2, 64)])
+def test_attention_over_short_and_odd_lengths(Hkv, G, n_q, d):
+    # 0 and 1 token; fewer tokens than queries (rows that admit nothing); tile and page borders and beside them
+    lens = np.array([0, 1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 129, 255, 256, 257, 300], np.int32)
+    pool = Pool(len(lens), Hkv, d, 16, lens, seed=Hkv * 100 + G * 10 + n_q)
+    q = bf16(np.random.default_rng(G).standard_normal((len(lens), Hkv * G, n_q, d))).cuda()
+    scale = fa.default_scale(d)
+    c = pool.cache()
+    o, lse = fa.forward_kv4(q, c, dev(lens), dev(pool.table), accumulate=True)
+    o2, lse2 = fa.forward_kv4(q, c, dev(lens), dev(pool.table))
+    ok()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    check_attention(pool, q, lens, scale, o, lse, pool.w, f64(c.weights))
+
+
+@gpu
+@pytest.mark.parametrize("d,P,Hkv,G,n_q", [(128, 64, 2, 4, 1), (64, 32, 1, 8, 2), (128, 1024, 1, 1, 1), (128, 16, 1, 12, 2)])
+def test_attention_over_long_ragged_lengths(d, P, Hkv, G, n_q):
+    # several chunks, some sequences far shorter than the table's columns
+    lens = np.array([9000, 4097, 1, 700], np.int32)
+    pool = Pool(4, Hkv, d, P, lens, seed=d + P)
+    q = bf16(3 * np.random.default_rng(G).standard_normal((4, Hkv * G, n_q, d))).cuda()
+    c = pool.cache()
+    o, lse = fa.forward_kv4(q, c, dev(lens), dev(pool.table), scale=0.11, accumulate=True)
+    ok()
+    check_attention(pool, q, lens, float(np.float32(0.11)), o, lse, pool.w, f64(c.weights))
+
+
+@gpu
+@pytest.mark.parametrize("gain", [1e-4, 1e3])
+@pytest.mark.parametrize("q_gain", [1e-20, 1e-3, 40.0])
+def test_attention_over_small_and_large_values(gain, q_gain):
+    lens = np.array([100, 513], np.int32)
+    pool = Pool(2, 1, 128, 32, lens, seed=3, gain=gain)
+    q = bf16(q_gain / gain * np.random.default_rng(2).standard_normal((2, 4, 1, 128))).cuda()
+    o, lse = fa.forward_kv4(q, pool.cache(), dev(lens), dev(pool.table))
+    ok()
+    check_attention(pool, q, lens, fa.default_scale(128), o, lse)
+
+
+@gpu
+def test_a_stored_nan_reaches_the_rows_that_admit_it_and_no_other():
+    lens = np.array([40, 40], np.int32)
+    pool = Pool(2, 1, 64, 16, lens, seed=11)
+    pool.vs[pool.table[0, 39 // 16], 0, 39 % 16] = 255  # the last token: only the last query admits it
+    pool.ks[pool.table[1, 38 // 16], 0, 38 % 16, 1] = 255
+    q = bf16(np.random.default_rng(3).standard_normal((2, 2, 3, 64))).cuda()
+    o, lse = (f64(x) for x in fa.forward_kv4(q, pool.cache(), dev(lens), dev(pool.table)))
+    ok()
+    assert np.isfinite(o[0, :, :2]).all() and np.isnan(o[0, :, 2]).all() and np.isfinite(lse[0]).all()
+    assert np.isfinite(o[1, :, 0]).all() and np.isnan(o[1, :, 1:]).all() and np.isnan(lse[1, :, 1:]).all()
+
+
+@gpu
+def test_bad_pages_and_lengths_are_left_out_and_reported():
+    # the kernels check the table and the lengths themselves: nothing outside the pool is read or written
+    lens = np.array([100, 60], np.int32)
+    pool = Pool(2, 2, 64, 16, lens, seed=21)
+    table = pool.table.copy()
+    table[0, 2] = pool.n_pages
+    q = bf16(np.random.default_rng(4).standard_normal((2, 4, 1, 64))).cuda()
+    c = pool.cache()
+    o, lse = fa.forward_kv4(q, c, dev(lens), dev(table), accumulate=True)
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_status(0) == 8 and fa.fa_get_device_status(0) == 0
+    k, v = pool.kv(0, 100)
+    left = np.r_[0:32, 48:100]
+    r = ref.attention(f64(q[0]), k[:, left], v[:, left], fa.default_scale(64), 84)
+    assert np.abs(f64(o[0]) - r["o"]).max() < 2.0 ** -8 * np.abs(r["o"]).max() and np.abs(f64(lse[0]) - r["lse"]).max() < 1e-4
+    check_attention_one = ref.attention(f64(q[1]), *pool.kv(1, 60), fa.default_scale(64), 60)
+    assert np.abs(f64(o[1]) - check_attention_one["o"]).max() < 2.0 ** -8 * np.abs(check_attention_one["o"]).max()
+    # a length past the table's columns, a negative one, a negative position
+    cols = pool.cols
+    o, lse = fa.forward_kv4(q, c, dev(np.array([-5, 60], np.int32)), dev(pool.table))
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_status(0) == 8 and (lse[0] == float("-inf")).all() and (o[0] == 0).all()
+    full = np.abs(table) % pool.n_pages
+    k1, _ = fa.kv4_read(c, dev(np.array([10 ** 6, 60], np.int32)), dev(full.astype(np.int32)), 16 * cols + 5)
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_status(0) == 8 and (k1[0, :, 16 * cols:] == 0).all()
+    before = [t.clone() for t in c]
+    x = bf16(np.ones((2, 2, 4, 64))).cuda()
+    fa.kv4_append(c, x, x, dev(np.array([0, 0], np.int32)), dev(pool.table))
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_status(0) == 8 and all(torch.equal(a, b) for a, b in zip(before, c))
+
+
+@gpu
+def test_workspace_is_all_that_is_used_and_small_ones_are_refused():
+    lens = np.array([1000], np.int32)
+    pool = Pool(1, 1, 64, 16, lens, seed=31)
+    q = bf16(np.random.default_rng(5).standard_normal((1, 4, 2, 64))).cuda()
+    need = fa.fa_fwd_kv4_workspace_bytes(1, 4, 1, 2, 64, pool.cols * 16, True)
+    ws = torch.full((need + 4096,), 171, dtype=torch.uint8, device="cuda")
+    c = pool.cache()
+    o, lse = fa.forward_kv4(q, c, dev(lens), dev(pool.table), accumulate=True, workspace=ws[:need])
+    o2, lse2 = fa.forward_kv4(q, pool.cache(), dev(lens), dev(pool.table), accumulate=True)
+    ok()
+    assert (ws[need:] == 171).all() and torch.equal(o, o2) and torch.equal(lse, lse2)
+    with pytest.raises(fa.FAError):
+        fa.forward_kv4(q, c, dev(lens), dev(pool.table), accumulate=True, workspace=ws[:need - 1])
+
+
+@gpu
+def test_overlapping_and_misplaced_pointers_are_refused():
+    lens, pool = np.array([20], np.int32), Pool(1, 1, 64, 16, [20], seed=41)
+    c, p = pool.cache(), dev(pool.table)
+    s, n = fa._binding._kv4_struct(c), dev(lens)
+    q = torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16, device="cuda")
+    ws, lse = torch.empty(1 << 20, dtype=torch.uint8, device="cuda"), torch.zeros(1, device="cuda")
+    call = lambda o, l, w: fa.fa_fwd_kv4(q.data_ptr(), s, n.data_ptr(), p.data_ptr(), o, l, 1, 1, 1, p.shape[1], 0.1,  # noqa: E731
+                                         0, w, ws.numel(), 0)
+    assert call(c.k.data_ptr(), lse.data_ptr(), ws.data_ptr()) == 1
+    assert call(q.data_ptr(), lse.data_ptr(), ws.data_ptr()) == 1
+    assert call(ws.data_ptr(), lse.data_ptr(), ws.data_ptr()) == 1
+    assert call(lse.data_ptr() + 2, lse.data_ptr(), ws.data_ptr()) == 1
+    host = torch.zeros(64, dtype=torch.bfloat16)
+    assert call(host.data_ptr(), lse.data_ptr(), ws.data_ptr()) == 1
+    assert fa.fa_kv4_append(s, c.k.data_ptr(), q.data_ptr(), None, None, n.data_ptr(), p.data_ptr(), 1, 1, p.shape[1], 0) == 1
+    assert fa.fa_kv4_read(s, None, n.data_ptr(), p.data_ptr(), 1, p.shape[1], 1, c.v.data_ptr(), q.data_ptr(), 0) == 1
+    assert fa.fa_kv4_evict(s, n.data_ptr(), p.data_ptr(), p.shape[1], s, p.data_ptr(), p.shape[1], 1, 4, 0,
+                           c.weights.data_ptr(), lse.data_ptr(), 0) == 1
+    ok()
+
+
+# ------------------------------------------------------------------------------------ eviction
+
+def check_eviction(pool, w, lens, keep, recent, same_pool, seed=0):
+    B, Hkv, P, d = pool.B, pool.Hkv, pool.P, pool.d
+    rng = np.random.default_rng(seed)
+    cols = -(-keep // P)
+    src = pool.cache()._replace(weights=dev(w))
+    if same_pool:  # fresh pages behind the old ones
+        grow = lambda t: torch.cat([t, t[:1].expand(B * cols, *t.shape[1:])]).contiguous()  # noqa: E731
+        src = to = fa.KV4Cache(*(grow(t) for t in src))
+        to_table = (pool.n_pages + rng.permutation(B * cols)).reshape(B, cols).astype(np.int32)
+    else:
+        to = fa.kv4_cache(B * cols + 1, Hkv, P, d)
+        to_table = rng.permutation(B * cols + 1)[:B * cols].reshape(B, cols).astype(np.int32)
+    before = [t.cpu().numpy().copy() for t in to]
+    kept, now = fa.kv4_evict(src, dev(lens), dev(pool.table), to, dev(to_table), keep, recent=recent)
+    ok()
+    assert (now.cpu().numpy() == np.minimum(lens, keep)).all()
+    kept = kept.cpu().numpy()
+    for b in range(B):
+        n, m = int(lens[b]), min(int(lens[b]), keep)
+        for h in range(Hkv):
+            at = ref.evict(ref.rows(w, pool.table[b], n, P)[h] if n else np.zeros(0), n, keep, recent)
+            assert (kept[b, h, :m] == at).all() and (kept[b, h, m:] == -1).all()
+            i = np.arange(m)
+            for t, x in zip(before, (pool.k, pool.v, pool.ks, pool.vs, w)):
+                t[to_table[b, i // P], h, i % P] = x[pool.table[b, at // P], h, at % P]
+    for got, t in zip(to, before):
+        assert np.array_equal(got.cpu().numpy(), t, equal_nan=True)  # the rest of the pages is as it was
+
+
+@gpu
+@pytest.mark.parametrize("same_pool", [False, True])
+@pytest.mark.parametrize("d,P,keep,recent", [(64, 16, 1, 0), (64, 16, 1, 1), (128, 16, 40, 8), (64, 64, 100, 100), (128, 32, 200, 0),
+                                             (128, 16, 3000, 100)])
+def test_eviction_keeps_the_heaviest_and_the_latest(d, P, keep, recent, same_pool):
+    lens = np.array([0, 1, 39, 40, 41, 130, 1024, 2500], np.int32)
+    pool = Pool(len(lens), 2, d, P, lens, seed=keep + recent)
+    rng = np.random.default_rng(keep)
+    w = np.exp(2 * rng.standard_normal(pool.w.shape)).astype(np.float32)
+    w[rng.random(w.shape) < 0.3] = 0  # ties
+    check_eviction(pool, w, lens, keep, recent, same_pool)
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["equal", "signed", "nonfinite", "neighbours"])
+def test_eviction_orders_every_float(kind):
+    lens = np.array([1500, 333], np.int32)
+    pool = Pool(2, 3, 64, 16, lens, seed=7)
+    rng = np.random.default_rng(8)
+    w = rng.standard_normal(pool.w.shape).astype(np.float32)
+    if kind == "equal":
+        w[:] = 1.5
+    elif kind == "signed":
+        w[rng.random(w.shape) < 0.2], w[rng.random(w.shape) < 0.2] = 0.0, -0.0
+    elif kind == "nonfinite":
+        w[rng.random(w.shape) < 0.1], w[rng.random(w.shape) < 0.1], w[rng.random(w.shape) < 0.1] = np.nan, np.inf, -np.inf
+    else:
+        w[:] = np.float32(1) + rng.integers(0, 4, w.shape) * np.float32(2.0 ** -23)
+    check_eviction(pool, w, lens, 200, 17, False)
+
+
+@gpu
+@pytest.mark.parametrize("n", [16384, 60000, 70001])
+def test_eviction_from_long_sequences(n):
+    lens = np.array([n, n // 2], np.int32)
+    pool = Pool(2, 1, 64, 128, lens, seed=9)
+    w = np.exp(np.random.default_rng(10).standard_normal(pool.w.shape)).astype(np.float32)
+    check_eviction(pool, w, lens, n // 3, 512, False)
+
+
+# --------------------------------------------------------------------------------- key weights
+
+def _lse(q, k, scale, causal):
+    B, H, N, d = q.shape
+    s = scale * np.einsum("bhid,bhjd->bhij", q, np.repeat(k, H // k.shape[1], axis=1))
+    if causal:
+        s = np.where(np.tril(np.ones((N, N), dtype=bool)), s, -np.inf)
+    top = s.max(-1)
+    return (top + np.log(np.exp(s - top[..., None]).sum(-1))).astype(np.float32)
+
+
+@gpu
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,H,Hkv,N,first", [(1, 1, 1, 1, 0), (1, 1, 1, 2, 1), (2, 2, 1, 127, 0), (1, 4, 2, 128, 5), (1, 3, 3, 129, 128),
+                                             (2, 8, 1, 255, 0), (1, 2, 2, 256, 200), (1, 7, 1, 257, 0), (1, 2, 1, 511, 300),
+                                             (1, 4, 2, 1000, 0), (1, 1, 1, 2049, 2048)])
+def test_key_weights(B, H, Hkv, N, first, d, causal):
+    rng = np.random.default_rng(N + H)
+    q, k = bf16(rng.standard_normal((B, H, N, d))), bf16(rng.standard_normal((B, Hkv, N, d)))
+    scale = fa.default_scale(d)
+    lse = _lse(f64(q), f64(k), scale, causal)
+    if N > 2:
+        lse[0, 0, N // 2] = -np.inf  # a query that admitted no key adds nothing
+    w = fa.key_weights(q.cuda(), k.cuda(), dev(lse), causal=causal, first_query=first)
+    ok()
+    want, reach = ref.key_weights(f64(q), f64(k), lse.astype(np.float64), scale, causal, first)
+    top = np.abs(np.where(np.isfinite(lse), lse, 0)).max()
+    tol = want * (2 * (d + 8) * 2.0 ** -23 * reach + 2.0 ** -21 * (top + 2)) + 1e-37
+    assert w.shape == want.shape and (np.abs(f64(w) - want) <= tol).all()
+
+
+@gpu
+def test_key_weights_sum_to_the_number_of_queries():
+    # from the forward's own LSE: the columns of a softmax matrix add up to its rows
+    q, k, v = (t.cuda() for t in fa.make_inputs(1, 4, 3000, 128, seed=3))
+    _, lse = fa.forward(q, k, v, causal=True)
+    w = fa.key_weights(q, k, lse, causal=True)
+    half = fa.key_weights(q, k, lse, causal=True, first_query=1500)
+    ok()
+    # the forward's LSE is within 1e-3 of the truth (its own tests' bound)
+    assert (w.double().sum(-1) / 3000 - 1).abs().max() < 1e-3 and (half.double().sum(-1) / 1500 - 1).abs().max() < 1e-3
+
+
+# --------------------------------------------------------- streams, graphs, all of them together
+
+def _serve(fa_forward, steps, B=2, H=4, Hkv=2, d=64, P=16, N=150, keep=96, recent=16):
+    """A prompt, then `steps` tokens with an eviction between: the calls as a program makes them."""
+    g = torch.Generator().manual_seed(1)
+    randn = lambda *s: torch.randn(s, generator=g).bfloat16().cuda()  # noqa: E731
+    q, k, v = randn(B, H, N, d), randn(B, Hkv, N, d), randn(B, Hkv, N, d)
+    G = H // Hkv
+    _, lse = fa.forward(q, k.repeat_interleave(G, 1), v.repeat_interleave(G, 1), causal=True)
+    w = fa.key_weights(q, k, lse, causal=True)
+    cache = fa.kv4_cache(64, Hkv, P, d)
+    order = torch.randperm(64, generator=g).to(torch.int32).cuda()
+    table, table2 = order[:B * 16].view(B, 16).contiguous(), order[B * 16:2 * B * 16].view(B, 16).contiguous()
+    lens = torch.full((B,), N, dtype=torch.int32, device="cuda")
+    fa.kv4_append(cache, k, v, lens, table, weights=w)
+    outs, log = [], [(k, v)]
+    for s in range(steps):
+        if s == steps // 2:
+            kept, lens = fa.kv4_evict(cache, lens, table, cache, table2, keep, recent=recent)
+            table = table2
+            outs.append(kept)
+        qn, kn, vn = randn(B, H, 1, d), randn(B, Hkv, 1, d), randn(B, Hkv, 1, d)
+        lens = lens + 1
+        fa.kv4_append(cache, kn, vn, lens, table)
+        o, lse = fa_forward(qn, cache, lens, table)
+        outs += [o, lse]
+        log.append((qn, kn, vn))
+    return outs, log, cache, lens, table, w
+
+
+@gpu
+def test_prompt_decode_evict_decode():
+    steps = 8
+    outs, log, cache, lens, table, w0 = _serve(lambda *a: fa.forward_kv4(*a, accumulate=True), steps)
+    ok()
+    (k0, v0), B, H, Hkv, d, G = log[0], 2, 4, 2, 64, 2
+    it = iter(outs)
+    for b in range(B):
+        it = iter(outs)
+        K = [ref.values(*ref.quantise(f64(k0[b, h]), 32)) for h in range(Hkv)]
+        V = [ref.values(*ref.quantise(f64(v0[b, h]), d)) for h in range(Hkv)]
+        W = [f64(w0[b, h]) for h in range(Hkv)]
+        for s in range(steps):
+            if s == steps // 2:
+                kept = next(it)[b].cpu().numpy()
+                for h in range(Hkv):
+                    # every key kept is at least as heavy as any left out (up to the weights' own rounding)
+                    old = np.arange(len(W[h]) - 16)
+                    out = np.setdiff1d(old, kept[h])
+                    stay = np.intersect1d(old, kept[h])
+                    assert len(kept[h]) == 96 and W[h][stay].min() >= W[h][out].max() * (1 - 1e-4)
+                    K[h], V[h], W[h] = K[h][kept[h]], V[h][kept[h]], W[h][kept[h]]
+            qn, kn, vn = log[1 + s]
+            o, lse = next(it), next(it)
+            for h in range(Hkv):
+                K[h] = np.concatenate([K[h], ref.values(*ref.quantise(f64(kn[b, h]), 32))])
+                V[h] = np.concatenate([V[h], ref.values(*ref.quantise(f64(vn[b, h]), d))])
+                n = len(K[h])
+                r = ref.attention(f64(qn[b, h * G:(h + 1) * G]), K[h][None], V[h][None], fa.default_scale(d), n)
+                W[h] = np.concatenate([W[h], [0.0]]) + r["weights"][0]
+                assert np.abs(f64(o[b, h * G:(h + 1) * G]) - r["o"]).max() <= 2.0 ** -8 * np.abs(r["o"]).max()
+                assert np.abs(f64(lse[b, h * G:(h + 1) * G]) - r["lse"]).max() <= 1e-4
+        got = np.stack([ref.rows(cache.weights.cpu().numpy(), table[b].cpu().numpy(), int(lens[b]), 16)[h] for h in range(Hkv)])
+        assert np.abs(got - np.stack(W)).max() <= 1e-4 * np.stack(W).max()
+
+
+@gpu
+def test_captured_step_replays_with_new_lengths():
+    lens = np.array([300, 41], np.int32)
+    pool = Pool(2, 2, 128, 16, [320, 320], seed=51)
+    c, table, n = pool.cache(), dev(pool.table), dev(lens)
+    rng = np.random.default_rng(52)
+    q, kn = bf16(rng.standard_normal((2, 8, 1, 128))).cuda(), bf16(rng.standard_normal((2, 2, 1, 128))).cuda()
+    ws = torch.empty(fa.fa_fwd_kv4_workspace_bytes(2, 8, 2, 1, 128, pool.cols * 16, True), dtype=torch.uint8, device="cuda")
+    step = lambda cache, m: (fa.kv4_append(cache, kn, kn, m, table), fa.forward_kv4(q, cache, m, table, accumulate=True, workspace=ws))[1]  # noqa: E731
+    step(pool.cache(), n.clone())
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        n.add_(1)
+        o, lse = step(c, n)
+    plain, m = pool.cache(), dev(lens)
+    for _ in range(3):
+        g.replay()
+        m = m + 1
+        o2, lse2 = step(plain, m)
+        torch.cuda.synchronize()
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+        assert all(torch.equal(a, b) for a, b in zip(c, plain))
+    ok()
+
+
+@gpu
+def test_given_stream_and_repeated_calls_give_the_same_bits():
+    lens = np.array([3000, 77], np.int32)
+    pool = Pool(2, 1, 128, 64, lens, seed=61)
+    q = bf16(np.random.default_rng(62).standard_normal((2, 8, 1, 128))).cuda()
+    c, table, n = pool.cache(), dev(pool.table), dev(lens)
+    o, lse = fa.forward_kv4(q, c, n, table)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        with torch.cuda.stream(s):
+            ws = torch.empty(fa.fa_fwd_kv4_workspace_bytes(2, 8, 1, 1, 128, table.shape[1] * 64, False), dtype=torch.uint8, device="cuda")
+        o2, lse2 = fa.forward_kv4(q, c, n, table, workspace=ws, stream=s)
+        s.synchronize()
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    ok()
+
+
+@gpu
+def test_sequences_may_share_pages_that_are_read():
+    lens = np.array([90, 50], np.int32)
+    pool = Pool(2, 1, 64, 16, lens, seed=71)
+    table = pool.table.copy()
+    table[1, :3] = table[0, :3]  # a common prefix of three pages
+    q = bf16(np.random.default_rng(72).standard_normal((1, 2, 1, 64)))
+    o, lse = fa.forward_kv4(torch.cat([q, q]).cuda(), pool.cache(), dev(np.array([48, 48], np.int32)), dev(table))
+    ok()
+    assert torch.equal(o[0], o[1]) and torch.equal(lse[0], lse[1])
+
+
+@gpu
+def test_rows_past_four_gibibytes():
+    # a pool of 4.6 GB of K codes: byte offsets pass 32 bits
+    d, P, Hkv = 128, 1024, 1
+    n_pages = 70_000
+    c = fa.kv4_cache(n_pages, Hkv, P, d)
+    pages = np.array([[n_pages - 1, 0, n_pages - 2]], np.int32)
+    rng = np.random.default_rng(81)
+    x = bf16(rng.standard_normal((1, 1, 2100, d)))
+    n = np.array([2100], np.int32)
+    fa.kv4_append(c, x.cuda(), x.cuda(), dev(n), dev(pages))
+    k, v = fa.kv4_read(c, dev(n), dev(pages), 2100)
+    q = bf16(rng.standard_normal((1, 4, 1, d))).cuda()
+    o, lse = fa.forward_kv4(q, c, dev(n), dev(pages), accumulate=True)
+    to = np.array([[n_pages - 3]], np.int32)
+    kept, now = fa.kv4_evict(c, dev(n), dev(pages), c, dev(to), 1000, recent=10)
+    k2, _ = fa.kv4_read(c, now, dev(to), 1000)
+    ok()
+    kk = ref.values(*ref.quantise(f64(x[0]), 32))
+    vv = ref.values(*ref.quantise(f64(x[0]), d))
+    assert (f64(k[0]) == kk).all() and (f64(v[0]) == vv).all()
+    r = ref.attention(f64(q[0]), kk, vv, fa.default_scale(d), 2100)
+    assert np.abs(f64(o[0]) - r["o"]).max() <= 2.0 ** -8 * np.abs(r["o"]).max()
+    assert torch.equal(k2[0, 0], k[0, 0][kept[0, 0].long()])
