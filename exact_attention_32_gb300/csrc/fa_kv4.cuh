@@ -21,10 +21,11 @@
 namespace {
 
 // Sticky status of this translation unit's kernels: FA_ERR_BAD_PAGE once a
-// kernel met a page index or a length outside its cache (it left that part out).
+// kernel met a page index or a length outside its cache (it left that part out),
+// FA_ERR_TIMEOUT once a bounded wait gave up (which a bad page does not overwrite).
 __device__ int g_kv4_status;
 
-__device__ __forceinline__ void kv4_report() { atomicExch(&g_kv4_status, FA_ERR_BAD_PAGE); }
+__device__ __forceinline__ void kv4_report() { atomicCAS(&g_kv4_status, 0, FA_ERR_BAD_PAGE); }
 
 int kv4_take_status_here(cudaStream_t stream)
 {

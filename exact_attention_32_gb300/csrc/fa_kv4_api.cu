@@ -66,8 +66,9 @@ void cache_ranges(const fa_kv4_cache *c, Range (&r)[5])
 int check_cache_pointers(const fa_kv4_cache *c, int dev)
 {
     int st;
-    for (const void *p : {static_cast<const void *>(c->k), static_cast<const void *>(c->v),
-                          static_cast<const void *>(c->k_scale), static_cast<const void *>(c->v_scale)})
+    for (const void *p : {static_cast<const void *>(c->k), static_cast<const void *>(c->v)})
+        if ((st = fa_check_device_pointer(p, dev, 32)) != FA_OK) return st;  // what a TMA of 4-bit values asks for
+    for (const void *p : {static_cast<const void *>(c->k_scale), static_cast<const void *>(c->v_scale)})
         if ((st = fa_check_device_pointer(p, dev, 16)) != FA_OK) return st;
     if (c->weights != nullptr) return fa_check_device_pointer(c->weights, dev, 16);
     return FA_OK;

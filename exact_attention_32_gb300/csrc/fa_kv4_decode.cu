@@ -1,37 +1,65 @@
 // Attention of the newest tokens over a 4-bit KV cache (fa_fwd_kv4).
 //
 // For each (sequence, key head) the R = H / Hkv * n_q query rows that share its
-// keys go together, so a key's 4-bit row is read and decoded once for all of them:
+// keys go together (up to 32 at a time), so a key's row is read once for all of them:
 //     S = scale q K^T,  O = softmax(S) V,  LSE = ln sum exp S
-// with one pass over the keys, a running maximum m and sum l per row, and O
-// rescaled when m grows.  The keys are cut into chunks; every CTA takes one chunk
-// of one (sequence, key head) and up to 32 rows, its warps take 32 keys a step, and
-// nothing is exchanged until the end: the warps' (m, l, O) are merged in shared
-// memory, the chunks' in a second kernel (O = sum 2^(m_s - m) O_s / sum 2^(m_s - m) l_s).
+// in one pass over the keys with a running maximum m and sum l per row.
 //
-// What bounds it is the bytes of the cache (133 a key and head at d = 128), so
-// the K and V codes go from global memory straight into registers in the layout
-// of the warp-level MMA (m16n8k16, f16 in, fp32 out), where the decoded halves are
-// its A operand: a tile's 16 keys (K) or 16 channels (V) are its M, eight query
-// rows its N.  Per pair of values that costs one conversion and, for K, one multiply
-// by the scale, for V one byte permute; there is no shared-memory traffic in the
-// loop and no barrier.  Both products are exact in what they multiply: q is bf16
-// scaled by a power of two into a half (its maximum at 2^14, so only values 2^28
-// below the row's maximum lose bits), a K value is exact in a half, a V code is
-// too.  P is rounded once, to a half: p <= 1 times V's scale times 4 (at most
-// 40960), relative error 2^-11, below bf16's 2^-8 of the output; the sum l takes
-// the unrounded p in fp32.
+// What bounds it is the bytes of the cache (133 a key and head at d = 128), at
+// which an SM has 2.8 instruction slots for every cached value: too few to decode them
+// in registers for warp-level products (that form of this kernel spent 2.9, and
+// reached 62 % of the copy bandwidth).  So the codes are never decoded: E2M1 is an
+// operand type of tcgen05.mma (kind::f8f6f4), and the TMA spreads each 8 bytes of codes
+// over the 16-byte slot that the tensor core reads them from (16U4_ALIGN16B).
+//   S^T = K Q^T      A = K as stored (128 rows, K-major), B = Q in E4M3.  One product per 32
+//                    channels, into columns of its own: K's scale differs per 32 channels
+//                    and is applied to the sums, one thread per key.
+//   O^T += V^T P^T   A = V as stored, MN-major; B = P times V's scale, in E4M3.
+// E4M3 has four significant bits, so what is not 4-bit goes in twice, as a high part
+// and 16 times the rest, in columns next to one another (N = 16 for 8 rows; a product's time
+// is A's, so they cost nothing).  For q (bf16, eight bits, scaled by a power of
+// two to a maximum in [128, 256)) that is exact down to 2^-13 of the row's maximum, and
+// to 2^-21 of it below.  P is off by at most 2^-8 of itself, as if rounded to bf16,
+// l is summed in fp32.  The products are exact and added in fp32.
+//
+// Work: a tile is 128 rows of 128 values: 128 keys at d = 128, 256 at d = 64 (keys 2i and
+// 2i + 1 side by side, as they lie in the page).  All tiles of all (sequence, head, row chunk) items in a row
+// are cut into equal shares, one a CTA, so lengths may differ as they like; a CTA
+// takes its share as segments of items.  A segment that is a whole item is finished in
+// place; the others leave (m, l, O) in the workspace, which a second kernel merges
+// (O = sum 2^(m_s - m) O_s / sum 2^(m_s - m) l_s).
+// Roles (192 threads, three CTAs an SM up to 8 rows, two up to 16): warps 0-3 the softmax, one thread a
+// TMEM lane; warp 4 loads, a lane a page (or the part of a page in the tile); warp 5
+// issues the products.  A softmax takes about 2000 cycles a tile, waits between its steps
+// for the most part, so an SM needs three of them at work to keep up with the 720
+// cycles that a tile's bytes take.  K and V have stages of their own, K's free as soon as S is there.
+// Copies of 8 bytes a lane by the load warps (cp.async) in the TMA's place took 3500 cycles
+// to issue a tile, two and a half times what all of the tile may take.
+#include <cuda.h>
+#include <float.h>
 #include <math.h>
 
+#include <mutex>
+
 #include "fa_kv4.cuh"
+#include "sm100_ptx.cuh"
+
+using namespace sm100;
 
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kStep = 32;                  // keys a warp takes at a time
-constexpr int kChunkUnit = kWarps * kStep;  // chunks are a multiple of this
-constexpr int kMaxChunk = 4096;
+constexpr int kDecThreads = 192, kDecWarps = 6;
+constexpr int kLoadWarp = 4, kMmaWarp = 5;
+constexpr int kMinShare = 2;     // tiles: a shorter share costs more in merging than it saves
+constexpr int kSms = 152;
+// A row's reference is set this far (log2) above the largest score when one passes it: with the maximum itself some of a
+// tile's 8 or 16 rows grow in nearly every one of the first dozens of tiles, at 1300 cycles each time.
+constexpr float kHeadroom = 3.f;
 constexpr float kLn2 = 0.69314718055994531f;
+constexpr uint64_t kWaitLimitNs = 1000000000ull;   // 1 s per pipeline wait
+constexpr uint64_t kCleanupLimitNs = 20000000ull;  // 20 ms while winding down
+
+__device__ __forceinline__ void kv4_timeout() { atomicExch(&g_kv4_status, FA_ERR_TIMEOUT); }
 
 struct DecodeArgs {
     Kv4Cache c;
@@ -39,454 +67,679 @@ struct DecodeArgs {
     const int32_t *lens, *table;
     __nv_bfloat16 *o;
     float *lse;
-    float *part_o;    // [rows][n_splits][D], unnormalised
-    float2 *part_ml;  // [rows][n_splits]: running maximum (log2), sum
-    float *scores;    // [B][heads][R][max_tokens] log2 scores, or null
-    float2 *row_ml;   // [rows]: maximum (log2), 1 / sum; with scores
+    float *part_o;     // [CTA][2][RP][D], unnormalised; slot 0: the segment that starts its share, 1: that ends it
+    float2 *part_ml;   // [CTA][2][RP]: running maximum (log2), sum
+    int64_t *prefix;   // [B + 2]: units before sequence b, all units, units a share
+    float *scores;     // [B][heads][R][max_tokens] log2 scores, or null
+    float2 *row_ml;    // [rows]: maximum (log2), 1 / sum; with scores
     int64_t max_pages;
-    int R, n_q, n_rc, n_splits, chunk;
+    int B, R, n_q, n_rc;
     float scale_log2;
 };
 
-__device__ __forceinline__ float ex2f(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1)
-{
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Transpose of an 8 x 8 matrix of halves held a row per quad (two columns a lane).
-__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x)
-{
-    uint32_t y;
-    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
-    return y;
-}
-
-__device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b)
-{
-    const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
-    return *reinterpret_cast<const uint32_t *>(&r);
-}
-
-__device__ __forceinline__ uint32_t pack_h2(float lo, float hi)
-{
-    const __half2 r = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&r);
-}
-
-// Streaming loads: each byte of the cache is read once by one SM.
-template <int WORDS>
-__device__ __forceinline__ void ld_stream(const void *p, uint32_t (&r)[WORDS])
-{
-    if constexpr (WORDS == 4)
-        asm("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n"
-            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-            : "l"(p));
-    else if constexpr (WORDS == 2)
-        asm("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];\n" : "=r"(r[0]), "=r"(r[1]) : "l"(p));
-    else
-        asm("ld.global.nc.L1::no_allocate.u32 %0, [%1];\n" : "=r"(r[0]) : "l"(p));
-}
-
-// 16 keys of K as one lane holds them: of keys g and g + 8 (g = lane / 4) the D/4
-// channels from t * D/4 (t = lane % 4), and the scales of those channels' block.
-template <int D>
-struct KTile {
-    uint32_t x[2][D / 32];
-    uint32_t s[2];
+template <int D, int RT>
+struct DecCfg {
+    static constexpr int RP = 8 * RT;          // rows a CTA takes
+    static constexpr int N = 16 * RT;          // columns: per 8 rows, 8 high parts and 8 rests
+    static constexpr int KPT = 128 / D;        // keys a thread (and a 128-byte row) holds
+    static constexpr int TK = 128 * KPT;       // keys a tile
+    static constexpr int NG = TK / 16;         // runs of 16 tokens, each in one page
+    static constexpr int kHalf = 16384;        // K or V of a tile
+    static constexpr int kPerSm = RT == 1 ? 3 : RT == 2 ? 2 : 1;   // CTAs an SM
+    static constexpr int kStages = RT == 1 ? 2 : RT == 2 ? 3 : 5;  // of K, and of V
+    static constexpr int kPBufs = RT == 2 && D == 64 ? 1 : 2;      // (what fits two CTAs an SM)
+    static constexpr int kV = kStages * kHalf;
+    static constexpr int kQ = 2 * kStages * kHalf;
+    static constexpr int kP = kQ + N * 128;
+    static constexpr int kPBytes = 128 * N * KPT;
+    static constexpr int kScale = kP + kPBufs * kPBytes;         // with V's stage: K scales 512, V scales 256, page flags 64
+    static constexpr int kScaleBytes = 512 + 256 + 64;
+    static constexpr int kFloat = kScale + kStages * kScaleBytes;  // mult, m, alpha [32]; red [4][32]; misc [32]
+    static constexpr int kWalk = kFloat + (3 * 32 + 4 * 32 + 32) * 4;  // the scan's sums, the share's start
+    static constexpr int kBar = kWalk + 128;
+    static constexpr int kNumBars = 4 * kStages + 7;
+    static constexpr int kSmemBytes = kBar + kNumBars * 8 + 16;
+    static constexpr int kSCols = 4 * N, kOCols = N * KPT;
+    static constexpr int kTmemCols = kSCols + kOCols <= 128 ? 128 : kSCols + kOCols <= 256 ? 256 : 512;
 };
-// 16 keys of V: of keys 2t, 2t+1, 2t+8, 2t+9 the D/8 channels from g * D/8; the
-// scales of keys g and g + 8.
-template <int D>
-struct VTile {
-    uint32_t x[4][D / 64];
-    uint32_t s[2];
+enum { D_S_FULL = 0, D_S_FREE, D_P_READY, D_PV_DONE, D_PV_DONE1, D_Q_READY, D_DONE, D_STAGES };  // then K_FULL, K_FREE, V_FULL, V_FREE
+
+__host__ __device__ inline int tile_keys(int d) { return 128 * (128 / d); }
+
+// Units (tiles) of one (sequence, head, row chunk): at least one, so that an empty sequence's rows are written too.
+__device__ __forceinline__ int tiles_of(int len, int tk) { return len <= tk ? 1 : (len + tk - 1) / tk; }
+
+// A CTA's way through its share: segments [t0, t1) of the n_t tiles of item `it` (head * n_rc + chunk) of sequence b.
+struct Walk {
+    int64_t left;  // units of the share still to come
+    int b, it, t0, t1, n_t, len;
 };
+
+template <int TK>
+__device__ __forceinline__ void walk_open(Walk &w, const DecodeArgs &a)
+{
+    w.len = kv4_length(a.lens, w.b, a.max_pages << a.c.log2_page);
+    w.n_t = tiles_of(w.len, TK);
+}
+__device__ __forceinline__ void walk_clip(Walk &w) { w.t1 = static_cast<int>(min(static_cast<int64_t>(w.n_t), w.t0 + w.left)); }
+
+template <int TK>
+__device__ __forceinline__ void walk_next(Walk &w, const DecodeArgs &a)
+{
+    w.left -= w.t1 - w.t0;
+    w.t0 = 0;
+    if (w.left <= 0) return;
+    if (++w.it == a.c.heads * a.n_rc) {
+        w.it = 0;
+        ++w.b;
+        walk_open<TK>(w, a);
+    }
+    walk_clip(w);
+}
+
+// Two fp32 -> two E4M3 bytes (`lo` in the low one), and back, exactly.
+__device__ __forceinline__ uint32_t e4m3x2(float2 v)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;\n" : "=h"(r) : "f"(v.x), "f"(v.y));
+    return r;
+}
+__device__ __forceinline__ float2 e4m3x2_f32(uint32_t b)
+{
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(h) : "h"(static_cast<uint16_t>(b)));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+
+// Barrier of the softmax warps; with an OR over their threads.
+__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, 128;\n" ::: "memory"); }
+__device__ __forceinline__ bool softmax_or(bool x)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbarrier.cta.red.or.pred q, 1, 128, p;\nselp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(x))
+        : "memory");
+    return r != 0;
+}
+
+// Maximum of finite floats over the warp.
+__device__ __forceinline__ float warp_max(float x)
+{
+    int i = __float_as_int(x);
+    i ^= (i >> 31) & 0x7FFFFFFF;
+    i = __reduce_max_sync(0xffffffffu, i);
+    i ^= (i >> 31) & 0x7FFFFFFF;
+    return __int_as_float(i);
+}
+
+__device__ __forceinline__ uint32_t lo32(uint64_t x) { return static_cast<uint32_t>(x); }
+__device__ __forceinline__ uint32_t hi32(uint64_t x) { return static_cast<uint32_t>(x >> 32); }
 
 template <int D, int RT, bool SCORES>
-__global__ void __launch_bounds__(kWarps * 32, RT == 1 ? 4 : RT == 2 ? 3 : 2)
-fa_kv4_decode_kernel(const DecodeArgs a)
+__global__ void __launch_bounds__(kDecThreads, DecCfg<D, RT>::kPerSm)
+fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const DecodeArgs a)
 {
-    constexpr int ROWS = 8 * RT;
-    constexpr int KW = D / 32, VW = D / 64, MT = D / 16;
-    extern __shared__ __align__(16) float sm_o[];  // [kWarps][ROWS][D], for the warps' merge
-    __shared__ float sm_m[kWarps][ROWS], sm_l[kWarps][ROWS];
-    __shared__ int sm_page[kMaxChunk / 16 + 1];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    using C = DecCfg<D, RT>;
+    constexpr int RP = C::RP, N = C::N, KPT = C::KPT, TK = C::TK, ST = C::kStages;
+    constexpr int K_FULL = D_STAGES, K_FREE = K_FULL + ST, V_FULL = K_FREE + ST, V_FREE = V_FULL + ST;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sb = smem_u32(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if ((sb & 1023u) != 0) {  // the swizzled tiles need a 1024-byte-aligned base
+        if (tid == 0) kv4_timeout();
+        return;
+    }
+    const uint32_t bar0 = sb + C::kBar;
+    auto BAR = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kBar + C::kNumBars * 8);
+    float *sm_mult = reinterpret_cast<float *>(smem + C::kFloat), *sm_m = sm_mult + 32, *sm_alpha = sm_m + 32;
+    float *sm_red = sm_alpha + 32, *sm_misc = sm_red + 4 * 32;
+    const int64_t cap = a.max_pages << a.c.log2_page;
 
-    const int split = blockIdx.x % a.n_splits;
-    const int64_t item = blockIdx.x / a.n_splits;
-    const int rc = static_cast<int>(item % a.n_rc);
-    const int64_t bh = item / a.n_rc, b = bh / a.c.heads;
-    const int h = static_cast<int>(bh - b * a.c.heads);
-    const int row0 = rc * ROWS, n_rows = min(ROWS, a.R - row0);
-    const int len = kv4_length(a.lens, b, a.max_pages << a.c.log2_page);
-    const int k_begin = split * a.chunk;
-    if (k_begin >= len && split > 0) return;  // (the merge counts the chunks from the length)
-    const int k_end = min(len, k_begin + a.chunk);
+    if (tid == 0) {
+        for (int s = 0; s < 4 * ST; ++s) mbar_init(BAR(D_STAGES + s), 1);
+        mbar_init(BAR(D_S_FULL), 1);
+        mbar_init(BAR(D_S_FREE), 4);
+        mbar_init(BAR(D_P_READY), 4);
+        mbar_init(BAR(D_PV_DONE), 1);
+        mbar_init(BAR(D_PV_DONE1), 1);
+        mbar_init(BAR(D_Q_READY), 4);
+        mbar_init(BAR(D_DONE), 1);
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
+        tmem_relinquish();
+    }
 
-    // pages of this chunk
-    const int page0 = k_begin >> a.c.log2_page;
-    const int n_pg = k_end > k_begin ? ((k_end - 1) >> a.c.log2_page) - page0 + 1 : 0;
-    for (int i = tid; i < n_pg; i += kWarps * 32)
-        sm_page[i] = kv4_page(a.c, a.table, b, a.max_pages, (page0 + i) << a.c.log2_page);
-
-    // Q as the MMA's B operand: lane (g, t) holds row g's channels from t * D/4, in halves
-    uint32_t qb[RT][MT][2];
-    float mult[RT][2];  // log2 score of rows 2t, 2t + 1 per unit of the product
-    int limit[RT][2];   // keys those rows admit
+    // the share of this CTA: units before each sequence by a scan over the lengths, 192 at a time
+    int64_t *scan = reinterpret_cast<int64_t *>(smem + C::kWalk);
+    Walk &start = *reinterpret_cast<Walk *>(smem + C::kWalk + 64);
+    static_assert(sizeof(Walk) <= 64, "fits behind the scan");
+    const int items = a.c.heads * a.n_rc;
+    auto units_of = [&](int b) -> int64_t {
+        return b < a.B ? static_cast<int64_t>(tiles_of(kv4_length(a.lens, b, cap), TK)) * items : 0;
+    };
+    int64_t total = 0;
     {
-        const __nv_bfloat16 *q0 = a.q + (bh * a.R + row0) * D;
+        int64_t n = 0;
+        for (int b = tid; b < a.B; b += kDecThreads) n += units_of(b);
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            uint32_t x[MT][2];
-            float amax = 0.f;
-            const bool live = rt * 8 + g < n_rows;
-#pragma unroll
-            for (int i = 0; i < MT / 2; ++i) {
-                uint4 u = make_uint4(0, 0, 0, 0);
-                if (live) u = *reinterpret_cast<const uint4 *>(q0 + (rt * 8 + g) * D + t * (D / 4) + i * 8);
-                x[2 * i][0] = u.x;
-                x[2 * i][1] = u.y;
-                x[2 * i + 1][0] = u.z;
-                x[2 * i + 1][1] = u.w;
-            }
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(x[i][j] << 16)),
-                                             fabsf(__uint_as_float(x[i][j] & 0xFFFF0000u))));
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            // exponent of the row's maximum, held where 2^(14 - e) and 2^(e - 14) are normal numbers
-            int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
-            e = amax == 0.f || e > 127 ? 14 : max(e, -100);
-            const float up = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    qb[rt][i][j] = pack_h2(__uint_as_float(x[i][j] << 16) * up,
-                                           __uint_as_float(x[i][j] & 0xFFFF0000u) * up);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int er = __shfl_sync(0xffffffffu, e, (2 * t + j) * 4);
-                mult[rt][j] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(er - 14 + 127) << 23);
-                limit[rt][j] = len - a.n_q + 1 + (row0 + rt * 8 + 2 * t + j) % a.n_q;
-            }
-        }
+        for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+        if (lane == 0) scan[warp] = n;
+        __syncthreads();
+        for (int i = 0; i < kDecWarps; ++i) total += scan[i];
     }
+    int64_t share = (total + gridDim.x - 1) / gridDim.x;
+    if (share < kMinShare) share = kMinShare;
+    const int64_t u0 = blockIdx.x * share;
+    if (tid == 0) start.left = 0;
+    int64_t base = 0;
+    for (int b0 = 0; b0 < a.B && (base <= u0 || blockIdx.x == 0); b0 += kDecThreads) {
+        const int b = b0 + tid;
+        const int64_t mine = units_of(b);
+        int64_t x = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        __syncthreads();
+        if (lane == 31) scan[warp] = x;
+        __syncthreads();
+        int64_t all = 0;
+        for (int i = 0; i < kDecWarps; ++i) {
+            if (i < warp) x += scan[i];
+            all += scan[i];
+        }
+        const int64_t before = base + x - mine;
+        if (blockIdx.x == 0 && b < a.B) a.prefix[b] = before;
+        if (b < a.B && u0 >= before && u0 < before + mine) {
+            Walk w;
+            w.b = b;
+            w.left = min(share, total - u0);
+            walk_open<TK>(w, a);
+            w.it = static_cast<int>((u0 - before) / w.n_t);
+            w.t0 = static_cast<int>((u0 - before) % w.n_t);
+            walk_clip(w);
+            start = w;
+        }
+        base += all;
+    }
+    if (blockIdx.x == 0 && tid == 0) {
+        a.prefix[a.B] = total;
+        a.prefix[a.B + 1] = share;
+    }
+    tc_fence_before();
     __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t tS = tmem, tO = tmem + C::kSCols;
+    // P's buffer of tile n, and the barrier and phase of its product
+    auto pbuf = [&](int n) { return C::kPBufs == 2 ? n & 1 : 0; };
+    auto pv_bar = [&](int n) { return BAR(D_PV_DONE + pbuf(n)); };
+    auto pv_phase = [&](int n) -> uint32_t { return (C::kPBufs == 2 ? n >> 1 : n) & 1; };
+    const bool run = *reinterpret_cast<volatile int *>(&g_kv4_status) != FA_ERR_TIMEOUT;
+    Walk w = start;
+    if (!run) w.left = 0;
 
-    float m[RT][2], l[RT][2], acc[RT][MT][4];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            m[rt][j] = -INFINITY;
-            l[rt][j] = 0.f;
+    if (warp == kLoadWarp) {
+        // -------------------------------------------------------------------- loads
+        if (lane == 0) {
+            prefetch_tmap(&tm_k);
+            prefetch_tmap(&tm_v);
         }
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[rt][i][j] = 0.f;
-    }
-
-    // row of the pool that holds the first of 16 keys from `key`, or -1 (nothing to read)
-    auto row_of = [&](int key) -> int64_t {
-        if (key >= k_end) return -1;
-        const int page = sm_page[(key >> a.c.log2_page) - page0];
-        return page < 0 ? -1 : kv4_row(a.c, page, h, key);
-    };
-    auto load_k = [&](KTile<D> &kt, int64_t row) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            kt.s[j] = 0;
-#pragma unroll
-            for (int i = 0; i < KW; ++i) kt.x[j][i] = 0;
-            if (row >= 0) {
-                const int64_t r = row + g + 8 * j;
-                ld_stream<KW>(a.c.k + r * (D / 2) + t * (D / 8), kt.x[j]);
-                kt.s[j] = __ldg(a.c.k_scale + r * (D / 32) + t * (D / 32) / 4);
-            }
-        }
-    };
-    auto load_v = [&](VTile<D> &vt, int64_t row) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-#pragma unroll
-            for (int i = 0; i < VW; ++i) vt.x[j][i] = 0;
-            if (row >= 0) ld_stream<VW>(a.c.v + (row + 2 * t + (j & 1) + 8 * (j >> 1)) * (D / 2) + g * (D / 16), vt.x[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) vt.s[j] = row >= 0 ? __ldg(a.c.v_scale + row + g + 8 * j) : 0;
-    };
-
-    KTile<D> kt[2];
-    VTile<D> vt[2];
-    int key = k_begin + warp * kStep;
-    int64_t rows[2] = {row_of(key), row_of(key + 16)};
-#pragma unroll
-    for (int u = 0; u < 2; ++u) load_k(kt[u], rows[u]);
-#pragma unroll
-    for (int u = 0; u < 2; ++u) load_v(vt[u], rows[u]);
-
-    for (; key < k_end; key += kChunkUnit) {
-        const int64_t next[2] = {row_of(key + kChunkUnit), row_of(key + kChunkUnit + 16)};
-        float x[RT][2][4];  // scores of keys g, g + 8 of each tile: (g, 2t), (g, 2t+1), (g+8, 2t), (g+8, 2t+1)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const uint32_t s0 = (kt[u].s[0] << 7) * 0x10001u, s1 = (kt[u].s[1] << 7) * 0x10001u;
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) x[rt][u][i] = 0.f;
-#pragma unroll
-            for (int w = 0; w < KW; ++w) {
-                uint32_t r0[4], r1[4];
-                kv4_decode8(kt[u].x[0][w], r0);
-                kv4_decode8(kt[u].x[1][w], r1);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    r0[i] = mul_h2(r0[i], s0);
-                    r1[i] = mul_h2(r1[i], s1);
-                }
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    mma16816(x[rt][u], r0[0], r1[0], r0[1], r1[1], qb[rt][2 * w][0], qb[rt][2 * w][1]);
-                    mma16816(x[rt][u], r0[2], r1[2], r0[3], r1[3], qb[rt][2 * w + 1][0], qb[rt][2 * w + 1][1]);
+        const int bt = min(1 << a.c.log2_page, TK);  // tokens a box: a page, or the tile's part of one
+        const int in_page = (1 << a.c.log2_page) - 1;
+        int n = 0;
+        bool ok = true;
+        for (; w.left > 0 && ok; walk_next<TK>(w, a)) {
+            const int h = w.it / a.n_rc;
+            for (int t = w.t0; t < w.t1; ++t, ++n) {
+                const int st = n % ST, key = t * TK + lane * bt;
+                int page = -1;
+                if (lane * bt < TK && key < w.len) page = kv4_page(a.c, a.table, w.b, a.max_pages, key);
+                const uint32_t boxes = __ballot_sync(0xffffffffu, page >= 0);
+                const uint32_t tokens = __popc(boxes) * bt;
+                if (n >= ST && !(ok = mbar_wait_warp(BAR(K_FREE + st), (n / ST - 1) & 1, kWaitLimitNs))) break;
+                if (lane == 0) mbar_arrive_expect_tx(BAR(K_FULL + st), tokens * (D / 2));
+                __syncwarp();
+                // (rows of a box that is left out keep stale codes, as good as any: their weight is 0)
+                if (page >= 0)
+                    tma_load_4d(sb + st * C::kHalf + lane * bt / KPT * 128, &tm_k, BAR(K_FULL + st), 0,
+                                (key & in_page) / KPT, h, page);
+                if (n >= ST && !(ok = mbar_wait_warp(BAR(V_FREE + st), (n / ST - 1) & 1, kWaitLimitNs))) break;
+                uint8_t *scale = smem + C::kScale + st * C::kScaleBytes;
+                if (lane < C::NG) reinterpret_cast<int *>(scale + 768)[lane] = (boxes >> (lane * 16 / bt)) & 1u;
+                __syncwarp();
+                if (lane == 0) mbar_arrive_expect_tx(BAR(V_FULL + st), tokens * (D / 2 + D / 32 + 1));
+                __syncwarp();
+                if (page >= 0) {
+                    tma_load_4d(sb + C::kV + st * C::kHalf + lane * bt / KPT * 128, &tm_v, BAR(V_FULL + st), 0,
+                                (key & in_page) / KPT, h, page);
+                    const int64_t row = kv4_row(a.c, page, h, key);
+                    bulk_load(smem_u32(scale) + lane * bt * (D / 32), a.c.k_scale + row * (D / 32), bt * (D / 32),
+                              BAR(V_FULL + st));
+                    bulk_load(smem_u32(scale) + 512 + lane * bt, a.c.v_scale + row, bt, BAR(V_FULL + st));
                 }
             }
         }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) load_k(kt[u], next[u]);
-
-        // log2 scores; keys that a row does not admit, or that no page holds, leave it
-        float vs[2][2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) vs[u][j] = kv4_scale(vt[u].s[j]) * 4.f;
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) x[rt][u][i] *= mult[rt][i & 1];
-        const bool edge = key + kStep > len - a.n_q + 1 || key + kStep > k_end || rows[0] < 0 || rows[1] < 0;
-        if (edge) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int kk = key + 16 * u + g + 8 * j;
-                    const bool gone = rows[u] < 0 || kk >= k_end;
-                    if (gone) vs[u][j] = 0.f;  // what lies behind the length may be anything
-#pragma unroll
-                    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            if (gone || kk >= limit[rt][i]) x[rt][u][2 * j + i] = -INFINITY;
-                }
+        if (!ok && lane == 0) kv4_timeout();
+        // no copy in flight when the CTA ends (after a break, K of one tile more than V is)
+        const uint64_t lim = ok ? kWaitLimitNs : kCleanupLimitNs;
+        for (int i = n > ST ? n - ST : 0; i < n; ++i) {
+            mbar_wait(BAR(K_FULL + i % ST), (i / ST) & 1, lim);
+            mbar_wait(BAR(V_FULL + i % ST), (i / ST) & 1, lim);
         }
-        if constexpr (SCORES) {
-            const int64_t cap = a.max_pages << a.c.log2_page;
+        if (!ok) mbar_wait(BAR(K_FULL + n % ST), (n / ST) & 1, lim);
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------------------------- products
+        if (lane == 0) {
+            constexpr uint32_t idS = idesc_e2m1_e4m3_f32(128, N, false, false);
+            constexpr uint32_t idO = idesc_e2m1_e4m3_f32(128, N * KPT, true, true);
+            const uint64_t dA = smem_desc_sw128(sb, 16, 1024);  // K tiles, and V tiles read the other way
+            const uint64_t dQ = smem_desc_sw128(sb + C::kQ, 16, 1024);
+            const uint64_t dP = smem_desc_plain(sb + C::kP, 128, 2048);
+            bool ok = true;
+            int n = 0, seg = 0;
+            auto pv = [&](int m, bool first) -> bool {  // O^T (+)= V^T P^T of tile m
+                if (!mbar_wait(BAR(D_P_READY), m & 1, kWaitLimitNs)) return false;
+                if (!mbar_wait(BAR(V_FULL + m % ST), (m / ST) & 1, kWaitLimitNs)) return false;
+                tc_fence_after();
+                const uint32_t v = lo32(dA) + ((C::kV + m % ST * C::kHalf) >> 4);
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_ss_f8_lohi(tO, v + kk * 256, hi32(dA), lo32(dP) + pbuf(m) * (C::kPBytes >> 4) + kk * 32, hi32(dP), idO,
+                                   first && kk == 0 ? 0u : 1u);
+                mma_commit(BAR(V_FREE + m % ST));
+                mma_commit(pv_bar(m));
+                return true;
+            };
+            for (; w.left > 0 && ok; walk_next<TK>(w, a), ++seg) {
+                if (!(ok = mbar_wait(BAR(D_Q_READY), seg & 1, kWaitLimitNs))) break;
+                for (int t = w.t0; t < w.t1; ++t, ++n) {
+                    const int st = n % ST;
+                    if (!(ok = mbar_wait(BAR(K_FULL + st), (n / ST) & 1, kWaitLimitNs))) break;
+                    if (n > 0 && !(ok = mbar_wait(BAR(D_S_FREE), (n - 1) & 1, kWaitLimitNs))) break;
+                    tc_fence_after();
+                    const uint32_t k = lo32(dA) + st * (C::kHalf >> 4);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int r = rt * 8 + 2 * t + i;
-                    if (r < n_rows) {
-                        float *s = a.scores + (bh * a.R + row0 + r) * cap + key + g;
+                    for (int i = 0; i < 4; ++i)
+                        mma_ss_f8_lohi(tS + i * N, k + i * 2, hi32(dA), lo32(dQ) + (D == 128 ? i : i & 1) * 2, hi32(dQ), idS, 0u);
+                    mma_commit(BAR(K_FREE + st));
+                    mma_commit(BAR(D_S_FULL));
+                    if (t > w.t0 && !(ok = pv(n - 1, t - 1 == w.t0))) break;
+                }
+                if (!ok || !(ok = pv(n - 1, w.t1 - 1 == w.t0))) break;
+            }
+            if (!ok) kv4_timeout();
+            mma_commit(BAR(D_DONE));
+            mbar_wait(BAR(D_DONE), 0, ok ? kWaitLimitNs : kCleanupLimitNs);
+        }
+    } else {
+        // ------------------------------------------------------------------- softmax
+        const uint32_t loff = static_cast<uint32_t>(warp * 32) << 16;
+        int n = 0;
+        bool ok = true;
+        for (; w.left > 0 && ok; walk_next<TK>(w, a)) {
+            const int h = w.it / a.n_rc, rc = w.it - h * a.n_rc;
+            const int64_t bh = static_cast<int64_t>(w.b) * a.c.heads + h;
+            const int row0 = rc * RP, n_rows = min(RP, a.R - row0);
+            // Q: 8 channels a thread, D / 8 threads a row
+            {
+                constexpr int TPR = D / 8;
+                for (int r = tid / TPR; r < RP; r += 128 / TPR) {
+                    uint4 u = make_uint4(0, 0, 0, 0);
+                    const int ch = tid % TPR;
+                    if (r < n_rows) u = *reinterpret_cast<const uint4 *>(a.q + (bh * a.R + row0 + r) * D + ch * 8);
+                    const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+                    float2 f[4];
+                    float amax = 0.f;
 #pragma unroll
-                        for (int u = 0; u < 2; ++u)
+                    for (int i = 0; i < 4; ++i) {
+                        f[i] = make_float2(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xFFFF0000u));
+                        amax = fmaxf(amax, fmaxf(fabsf(f[i].x), fabsf(f[i].y)));
+                    }
 #pragma unroll
-                            for (int j = 0; j < 2; ++j)
-                                if (key + 16 * u + g + 8 * j < k_end) s[16 * u + 8 * j] = x[rt][u][2 * j + i];
+                    for (int o = 1; o < TPR; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                    // exponent of the row's maximum, held where 2^(7 - e) and 2^(e - 7) are normal numbers
+                    int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
+                    e = amax == 0.f ? 7 : min(max(e, -100), 127);
+                    const float up = __uint_as_float(static_cast<uint32_t>(7 - e + 127) << 23);
+                    uint32_t hb[4], lb[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        f[i].x *= up;
+                        f[i].y *= up;
+                        hb[i] = e4m3x2(f[i]);
+                        const float2 g = e4m3x2_f32(hb[i]);
+                        lb[i] = e4m3x2(make_float2((f[i].x - g.x) * 16.f, (f[i].y - g.y) * 16.f));
+                    }
+                    // row r's high part in column (r / 8) * 16 + r % 8, its rest 8 columns on
+#pragma unroll
+                    for (int part = 0; part < 2; ++part) {
+                        const int col = (r >> 3) * 16 + (r & 7) + part * 8;
+                        const uint32_t *y = part ? lb : hb;
+                        *reinterpret_cast<uint2 *>(smem + C::kQ + col * 128 + (((ch >> 1) ^ (col & 7)) << 4) + (ch & 1) * 8) =
+                            make_uint2(y[0] | (y[1] << 16), y[2] | (y[3] << 16));
+                    }
+                    if (ch == 0) {
+                        sm_mult[r] = !(amax < INFINITY) ? NAN : a.scale_log2 * __uint_as_float(static_cast<uint32_t>(e - 7 + 127) << 23);
+                        sm_m[r] = -FLT_MAX;
                     }
                 }
-        }
-        // the running maximum: grown only where some key passes it, which soon is rare
-        bool grows = false;
-        float mx[RT][2];
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                mx[rt][i] = fmaxf(fmaxf(x[rt][0][i], x[rt][0][2 + i]), fmaxf(x[rt][1][i], x[rt][1][2 + i]));
-                grows |= mx[rt][i] > m[rt][i];
+                // V's scale reference: P carries scale / reference * 256; two octaves above every scale so far
+                if (tid == 0) sm_misc[0] = 0x1p-16f;
+                fence_proxy_async_smem();
+                softmax_sync();
+                if (lane == 0) mbar_arrive(BAR(D_Q_READY));
             }
-        if (__any_sync(0xffffffffu, grows)) {
+            float2 l[RP / 2];
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                float al[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float v = mx[rt][i];
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                    v = fmaxf(v, m[rt][i]);
-                    al[i] = m[rt][i] == -INFINITY ? 0.f : ex2f(m[rt][i] - v);  // (nothing yet: l and O are 0)
-                    if (m[rt][i] == v) al[i] = 1.f;
-                    m[rt][i] = v;
-                    l[rt][i] *= al[i];
-                }
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[rt][i][j] *= al[j & 1];
-            }
-        }
-        // P: the sum in fp32, the MMA's operand as halves times V's scale times 4
-        uint32_t pb[RT][2][2];
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            const float m0 = m[rt][0] == -INFINITY ? 0.f : m[rt][0], m1 = m[rt][1] == -INFINITY ? 0.f : m[rt][1];
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float p0 = ex2f(x[rt][u][2 * j] - m0), p1 = ex2f(x[rt][u][2 * j + 1] - m1);
-                    l[rt][0] += p0;
-                    l[rt][1] += p1;
-                    float y0 = p0 * vs[u][j], y1 = p1 * vs[u][j];
-                    if (edge) {  // a value that a row does not admit stays out of it, a NaN too
-                        if (x[rt][u][2 * j] == -INFINITY) y0 = 0.f;
-                        if (x[rt][u][2 * j + 1] == -INFINITY) y1 = 0.f;
-                    }
-                    pb[rt][u][j] = movmatrix_trans(pack_h2(y0, y1));
-                }
-        }
-        // O^T += V^T P^T
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int w = 0; w < VW; ++w) {
-                uint32_t r[4][4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) kv4_decode8(vt[u].x[j][w], r[j]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t a0 = __byte_perm(r[0][i], r[1][i], 0x5410), a1 = __byte_perm(r[0][i], r[1][i], 0x7632);
-                    const uint32_t a2 = __byte_perm(r[2][i], r[3][i], 0x5410), a3 = __byte_perm(r[2][i], r[3][i], 0x7632);
-#pragma unroll
-                    for (int rt = 0; rt < RT; ++rt) mma16816(acc[rt][4 * w + i], a0, a1, a2, a3, pb[rt][u][0], pb[rt][u][1]);
-                }
-            }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            load_v(vt[u], next[u]);
-            rows[u] = next[u];
-        }
-    }
+            for (int i = 0; i < RP / 2; ++i) l[i] = make_float2(0.f, 0.f);
 
-    // the warps' states: l over the lanes, then all through shared memory
+            for (int t = w.t0; t < w.t1; ++t, ++n) {
+                const int st = n % ST;
+                const uint8_t *scale = smem + C::kScale + st * C::kScaleBytes;
+                const int key0 = t * TK;
+                if (!mbar_wait_warp(BAR(V_FULL + st), (n / ST) & 1, kWaitLimitNs) ||
+                    !mbar_wait_warp(BAR(D_S_FULL), n & 1, kWaitLimitNs)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                // log2 scores of this thread's keys
+                float2 x[KPT][RP / 2];
+                float ks[4], vs[KPT];
+                {
+                    const uint32_t b = *reinterpret_cast<const uint32_t *>(scale + tid * 4);
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
+                    for (int i = 0; i < 4; ++i) ks[i] = kv4_scale((b >> (8 * i)) & 255u);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            float v = l[rt][i];
-            v += __shfl_xor_sync(0xffffffffu, v, 4);
-            v += __shfl_xor_sync(0xffffffffu, v, 8);
-            v += __shfl_xor_sync(0xffffffffu, v, 16);
-            if (g == 0) {
-                sm_m[warp][rt * 8 + 2 * t + i] = m[rt][i];
-                sm_l[warp][rt * 8 + 2 * t + i] = v;
+                    for (int k = 0; k < KPT; ++k) vs[k] = kv4_scale(scale[512 + tid * KPT + k]);
+                }
+#pragma unroll
+                for (int rg = 0; rg < RT; ++rg) {
+                    uint32_t s[4][16];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) tmem_ld16(tS + loff + i * N + rg * 16, s[i]);
+                    tmem_wait_ld();
+                    if (rg == RT - 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(BAR(D_S_FREE));
+                    }
+#pragma unroll
+                    for (int k = 0; k < KPT; ++k)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            float2 hi = make_float2(0.f, 0.f), lo = hi;
+#pragma unroll
+                            for (int i = 0; i < 4 / KPT; ++i) {
+                                const int q = k * (4 / KPT) + i;
+                                const float2 f = make_float2(ks[q], ks[q]);
+                                const float2 sh = make_float2(__uint_as_float(s[q][2 * j]), __uint_as_float(s[q][2 * j + 1]));
+                                const float2 sl = make_float2(__uint_as_float(s[q][8 + 2 * j]), __uint_as_float(s[q][9 + 2 * j]));
+                                hi = i == 0 ? mul2(f, sh) : fma2(f, sh, hi);
+                                lo = i == 0 ? mul2(f, sl) : fma2(f, sl, lo);
+                            }
+                            const float2 m = *reinterpret_cast<const float2 *>(sm_mult + rg * 8 + 2 * j);
+                            x[k][rg * 4 + j] = mul2(fma2(lo, make_float2(0.0625f, 0.0625f), hi), m);
+                        }
+                }
+                // keys that a row does not admit, or that no page holds, leave it; what lies there may be anything
+                const bool edge = key0 + TK > w.len - a.n_q + 1 ||
+                                  __any_sync(0xffffffffu, lane < C::NG && reinterpret_cast<const int *>(scale + 768)[lane < C::NG ? lane : 0] == 0);
+                if (edge) {
+#pragma unroll
+                    for (int k = 0; k < KPT; ++k) {
+                        const int j = tid * KPT + k, key = key0 + j;
+                        const bool gone = key >= w.len || reinterpret_cast<const int *>(scale + 768)[j >> 4] == 0;
+                        if (gone) vs[k] = 0.f;
+#pragma unroll
+                        for (int r = 0; r < RP; ++r) {
+                            const int limit = w.len - a.n_q + 1 + (row0 + r) % a.n_q;
+                            if (gone || key >= limit) (r & 1 ? x[k][r / 2].y : x[k][r / 2].x) = -INFINITY;
+                        }
+                    }
+                }
+                if constexpr (SCORES) {
+#pragma unroll
+                    for (int k = 0; k < KPT; ++k) {
+                        const int key = key0 + tid * KPT + k;
+                        if (key < w.len) {
+                            float *s = a.scores + (bh * a.R + row0) * cap + key;
+#pragma unroll
+                            for (int r = 0; r < RP; ++r, s += cap)
+                                if (r < n_rows) *s = r & 1 ? x[k][r / 2].y : x[k][r / 2].x;
+                        }
+                    }
+                }
+                // does a key pass its row's maximum, or a V scale the reference?  Soon that is rare.
+                bool grows = false;
+                const float vref = sm_misc[0];
+#pragma unroll
+                for (int k = 0; k < KPT; ++k) grows |= vs[k] > vref;
+#pragma unroll
+                for (int r = 0; r < RP / 2; ++r) {
+                    const float2 m = *reinterpret_cast<const float2 *>(sm_m + 2 * r);
+#pragma unroll
+                    for (int k = 0; k < KPT; ++k) grows |= x[k][r].x > m.x || x[k][r].y > m.y;
+                }
+                grows = softmax_or(grows);
+                // O is complete so far, where it will be rescaled; P's buffer has been read
+                if (grows && t > w.t0 && !mbar_wait_warp(pv_bar(n - 1), pv_phase(n - 1), kWaitLimitNs)) {
+                    ok = false;
+                    break;
+                }
+                if (n >= C::kPBufs && !mbar_wait_warp(pv_bar(n), pv_phase(n - C::kPBufs), kWaitLimitNs)) {
+                    ok = false;
+                    break;
+                }
+                if (grows) {
+#pragma unroll
+                    for (int r = 0; r < RP; ++r) {
+                        float v = -FLT_MAX;
+#pragma unroll
+                        for (int k = 0; k < KPT; ++k) v = fmaxf(v, r & 1 ? x[k][r / 2].y : x[k][r / 2].x);
+                        v = warp_max(v);
+                        if (lane == 0) sm_red[warp * 32 + r] = v;
+                    }
+                    {
+                        float v = 0.f;
+#pragma unroll
+                        for (int k = 0; k < KPT; ++k) v = fmaxf(v, vs[k]);
+                        v = warp_max(v);
+                        if (lane == 0) sm_misc[4 + warp] = v;
+                    }
+                    softmax_sync();
+                    const float vmax = fmaxf(fmaxf(sm_misc[4], sm_misc[5]), fmaxf(sm_misc[6], sm_misc[7]));
+                    const float vnew = vmax > vref ? __uint_as_float((__float_as_uint(vmax) & 0x7F800000u) + (2u << 23)) : vref;
+                    if (tid < RP) {
+                        const float old = sm_m[tid];
+                        float v = fmaxf(fmaxf(sm_red[tid], sm_red[32 + tid]), fmaxf(sm_red[64 + tid], sm_red[96 + tid]));
+                        v = v > old ? v + kHeadroom : old;
+                        sm_m[tid] = v;
+                        sm_alpha[tid] = ex2(old - v);
+                    }
+                    if (tid == 0) sm_misc[0] = vnew;
+                    softmax_sync();
+#pragma unroll
+                    for (int r = 0; r < RP / 2; ++r) l[r] = mul2(l[r], *reinterpret_cast<const float2 *>(sm_alpha + 2 * r));
+                    if (t > w.t0) {
+                        tc_fence_after();
+                        const float vf = vref / vnew;
+#pragma unroll
+                        for (int c = 0; c < C::kOCols / 16; ++c) {
+                            uint32_t o[16];
+                            tmem_ld16(tO + loff + c * 16, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                o[j] = __float_as_uint(__uint_as_float(o[j]) * (sm_alpha[(c % RT) * 8 + (j & 7)] * vf));
+                            tmem_st16(tO + loff + c * 16, o);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                // P: the sum in fp32; the product's operand times V's scale, as a high part and 16 times the rest
+                const float vc = 256.f / sm_misc[0];
+#pragma unroll
+                for (int k = 0; k < KPT; ++k) {
+                    const float c1 = vs[k] * vc, c16 = c1 * 16.f;
+#pragma unroll
+                    for (int rg = 0; rg < RT; ++rg) {
+                        uint32_t hb[4], lb[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 m = *reinterpret_cast<const float2 *>(sm_m + rg * 8 + 2 * j);
+                            const float2 xx = x[k][rg * 4 + j];
+                            const float2 p = make_float2(ex2(xx.x - m.x), ex2(xx.y - m.y));
+                            l[rg * 4 + j] = add2(l[rg * 4 + j], p);
+                            float2 y = mul2(p, make_float2(c1, c1)), y16 = mul2(p, make_float2(c16, c16));
+                            if (edge) {  // a value that a row does not admit stays out of it, a NaN too
+                                if (xx.x == -INFINITY) y.x = y16.x = 0.f;
+                                if (xx.y == -INFINITY) y.y = y16.y = 0.f;
+                            }
+                            hb[j] = e4m3x2(y);
+                            lb[j] = e4m3x2(fma2(e4m3x2_f32(hb[j]), make_float2(-16.f, -16.f), y16));
+                        }
+                        *reinterpret_cast<uint4 *>(smem + C::kP + pbuf(n) * C::kPBytes + (k * RT + rg) * 2048 + tid * 16) =
+                            make_uint4(hb[0] | (hb[1] << 16), hb[2] | (hb[3] << 16), lb[0] | (lb[1] << 16), lb[2] | (lb[3] << 16));
+                    }
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(BAR(D_P_READY));
             }
+            if (!ok) break;
+
+            // ---------------------------------------------------- end of the segment
+            if (!mbar_wait_warp(pv_bar(n - 1), pv_phase(n - 1), kWaitLimitNs)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-                *reinterpret_cast<float2 *>(sm_o + (warp * ROWS + rt * 8 + 2 * t + i) * D + g * (D / 8) + 2 * mt) =
-                    make_float2(acc[rt][mt][i], acc[rt][mt][2 + i]);
+            for (int r = 0; r < RP; ++r) {
+                float v = r & 1 ? l[r / 2].y : l[r / 2].x;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+                if (lane == 0) sm_red[warp * 32 + r] = v;
+            }
+            // this lane's channel of every row: high part and a sixteenth of the rest, P's factor taken out
+            float y[RP];
+            const float back = sm_misc[0] * 0.00390625f;
+            const int half = D == 64 ? warp >> 1 : 0;  // d = 64: lanes 64-127 hold the odd keys' part of channel lane - 64
+#pragma unroll
+            for (int rg = 0; rg < RT; ++rg) {
+                uint32_t o[16];
+                tmem_ld16(tO + loff + half * N + rg * 16, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    y[rg * 8 + j] = fmaf(__uint_as_float(o[8 + j]), 0.0625f, __uint_as_float(o[j])) * back;
+            }
+            tc_fence_before();
+            float *sx = reinterpret_cast<float *>(smem + C::kP);  // (the products have read P)
+            if (D == 64 && half == 1) {
+#pragma unroll
+                for (int r = 0; r < RP; ++r) sx[r * 64 + tid - 64] = y[r];
+            }
+            softmax_sync();
+            if (D == 128 || half == 0) {
+                const bool whole = w.t0 == 0 && w.t1 == w.n_t;
+                const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (n == w.t1 - w.t0 ? 0 : 1);
+#pragma unroll
+                for (int r = 0; r < RP; ++r) {
+                    if (r >= n_rows) break;
+                    float v = y[r];
+                    if (D == 64) v += sx[r * 64 + tid];
+                    const float ll = (sm_red[r] + sm_red[32 + r]) + (sm_red[64 + r] + sm_red[96 + r]);
+                    const int64_t row = bh * a.R + row0 + r;
+                    if (whole) {
+                        const float inv = ll == 0.f ? 0.f : 1.f / ll;
+                        a.o[row * D + tid] = __float2bfloat16_rn(v * inv);
+                        if (tid == 0) {
+                            a.lse[row] = ll == 0.f ? -INFINITY : (sm_m[r] + log2f(ll)) * kLn2;
+                            if (SCORES) a.row_ml[row] = make_float2(ll == 0.f ? 0.f : sm_m[r], inv);
+                        }
+                    } else {
+                        a.part_o[(slot * RP + r) * D + tid] = v;
+                        if (tid == 0) a.part_ml[slot * RP + r] = make_float2(sm_m[r], ll);
+                    }
+                }
+            }
+            softmax_sync();  // before the next segment's Q and state take the place of these
         }
+        if (!ok && lane == 0) kv4_timeout();
     }
+    tc_fence_before();
     __syncthreads();
-    for (int e = tid; e < n_rows * (D / 4); e += kWarps * 32) {
-        const int r = e / (D / 4), ch = (e % (D / 4)) * 4;
-        float mm = sm_m[0][r];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, sm_m[w][r]);
-        float ll = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float f = sm_m[w][r] == -INFINITY && !isnan(sm_l[w][r]) ? 0.f : ex2f(sm_m[w][r] - mm);
-            const float4 v = *reinterpret_cast<const float4 *>(sm_o + (w * ROWS + r) * D + ch);
-            ll = fmaf(f, sm_l[w][r], ll);
-            o.x = fmaf(f, v.x, o.x);
-            o.y = fmaf(f, v.y, o.y);
-            o.z = fmaf(f, v.z, o.z);
-            o.w = fmaf(f, v.w, o.w);
-        }
-        o.x *= 0.25f;  // P carried a factor of 4
-        o.y *= 0.25f;
-        o.z *= 0.25f;
-        o.w *= 0.25f;
-        const int64_t row = bh * a.R + row0 + r;
-        if (a.n_splits > 1) {
-            *reinterpret_cast<float4 *>(a.part_o + (row * a.n_splits + split) * D + ch) = o;
-            if (ch == 0) a.part_ml[row * a.n_splits + split] = make_float2(mm, ll);
-        } else {
-            const float inv = ll == 0.f ? 0.f : 1.f / ll;
-            uint2 y;
-            const __nv_bfloat162 y0 = __floats2bfloat162_rn(o.x * inv, o.y * inv), y1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-            y.x = *reinterpret_cast<const uint32_t *>(&y0);
-            y.y = *reinterpret_cast<const uint32_t *>(&y1);
-            *reinterpret_cast<uint2 *>(a.o + row * D + ch) = y;
-            if (ch == 0) {
-                a.lse[row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
-                if (SCORES) a.row_ml[row] = make_float2(ll == 0.f ? 0.f : mm, inv);
-            }
-        }
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kTmemCols);
     }
 }
 
-// Merge of a row's chunks: one warp a row, D/32 channels a lane.
+// Merge of a row whose item lies in several shares: one block a row, its warps over the parts.
 template <int D>
-__global__ void __launch_bounds__(128)
-fa_kv4_merge_kernel(const DecodeArgs a, int64_t rows)
+__global__ void __launch_bounds__(256)
+fa_kv4_merge_kernel(const DecodeArgs a, int RP)
 {
-    constexpr int PER = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    if (row >= rows) return;
-    const int64_t b = row / a.R / a.c.heads;
-    const int len = kv4_length(a.lens, b, a.max_pages << a.c.log2_page);
-    const int parts = max(1, (len + a.chunk - 1) / a.chunk);
-    const float2 *ml = a.part_ml + row * a.n_splits;
-    float m = -INFINITY;
-    for (int s = lane; s < parts; s += 32) m = fmaxf(m, ml[s].x);
+    constexpr int PER = D / 32, kWarps = 8;
+    __shared__ float sm_l[kWarps];
+    __shared__ float sm_x[kWarps][D];
+    __shared__ float sm_max[kWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t row = blockIdx.x, bh = row / a.R;
+    const int r = static_cast<int>(row - bh * a.R), b = static_cast<int>(bh / a.c.heads), h = static_cast<int>(bh % a.c.heads);
+    const int n_t = tiles_of(kv4_length(a.lens, b, a.max_pages << a.c.log2_page), 128 * (128 / D));
+    const int64_t share = a.prefix[a.B + 1];
+    const int64_t u0 = a.prefix[b] + static_cast<int64_t>(h * a.n_rc + r / RP) * n_t;
+    const int64_t c0 = u0 / share, c1 = (u0 + n_t - 1) / share;
+    if (c0 == c1) return;  // finished in place
+    const int parts = static_cast<int>(c1 - c0) + 1, rr = r % RP;
+    // an item's first part starts its CTA's share or ends it; the later ones start theirs
+    auto slot = [&](int i) { return (c0 + i) * 2 + (i == 0 && u0 != c0 * share ? 1 : 0); };
+    float m = -FLT_MAX;
+    for (int i = threadIdx.x; i < parts; i += 256) m = fmaxf(m, a.part_ml[slot(i) * RP + rr].x);
+    m = warp_max(m);
+    if (lane == 0) sm_max[warp] = m;
+    __syncthreads();
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int i = 0; i < kWarps; ++i) m = fmaxf(m, sm_max[i]);
     float l = 0.f, x[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) x[i] = 0.f;
-    const float *po = a.part_o + row * a.n_splits * D + lane * PER;
 #pragma unroll 4
-    for (int s = 0; s < parts; ++s) {
-        const float2 v = ml[s];
-        const float f = v.x == -INFINITY && !isnan(v.y) ? 0.f : ex2f(v.x - m);
+    for (int i = warp; i < parts; i += kWarps) {
+        const int64_t s = slot(i) * RP + rr;
+        const float2 v = a.part_ml[s];
+        const float f = ex2(v.x - m);
         l = fmaf(f, v.y, l);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) x[i] = fmaf(f, po[static_cast<int64_t>(s) * D + i], x[i]);
+        for (int j = 0; j < PER; ++j) x[j] = fmaf(f, a.part_o[s * D + j * 32 + lane], x[j]);
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (lane == 0) sm_l[warp] = l;
 #pragma unroll
-    for (int i = 0; i < PER; i += 2)
-        *reinterpret_cast<__nv_bfloat162 *>(a.o + row * D + lane * PER + i) = __floats2bfloat162_rn(x[i] * inv, x[i + 1] * inv);
-    if (lane == 0) {
-        a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-        if (a.scores != nullptr) a.row_ml[row] = make_float2(l == 0.f ? 0.f : m, inv);
+    for (int j = 0; j < PER; ++j) sm_x[warp][j * 32 + lane] = x[j];
+    __syncthreads();
+    if (threadIdx.x >= D) return;
+    float y = 0.f, ll = 0.f;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        y += sm_x[i][threadIdx.x];
+        ll += sm_l[i];
+    }
+    const float inv = ll == 0.f ? 0.f : 1.f / ll;
+    a.o[row * D + threadIdx.x] = __float2bfloat16_rn(y * inv);
+    if (threadIdx.x == 0) {
+        a.lse[row] = ll == 0.f ? -INFINITY : (m + log2f(ll)) * kLn2;
+        if (a.scores != nullptr) a.row_ml[row] = make_float2(ll == 0.f ? 0.f : m, inv);
     }
 }
 
@@ -505,7 +758,7 @@ fa_kv4_weights_kernel(const DecodeArgs a, int blocks)
         const float2 *ml = a.row_ml + bh * a.R;
         float w = 0.f;
 #pragma unroll 4
-        for (int r = 0; r < a.R; ++r) w = fmaf(ex2f(s[r * cap] - ml[r].x), ml[r].y, w);
+        for (int r = 0; r < a.R; ++r) w = fmaf(ex2(s[r * cap] - ml[r].x), ml[r].y, w);
         a.c.weights[kv4_row(a.c, page, h, key)] += w;
     }
 }
@@ -513,52 +766,87 @@ fa_kv4_weights_kernel(const DecodeArgs a, int blocks)
 // ------------------------------------------------------------------ host side
 
 struct Geometry {
-    int rt, n_rc, n_splits, chunk;
-    int64_t part_o, part_ml, scores, row_ml, total;  // byte offsets in the workspace
+    int rt, n_rc, ctas;
+    int64_t part_o, part_ml, prefix, scores, row_ml, total;  // byte offsets in the workspace
 };
 
-// The split of the keys, from the sizes alone (152 SMs, 4 CTAs each, four waves of
-// them where the keys allow: sequences are seldom of equal length).
 Geometry geometry(int64_t B, int64_t H, int64_t heads, int64_t n_q, int64_t d, int64_t max_tokens, int accumulate)
 {
     Geometry g;
     const int64_t R = H / heads * n_q, rows = B * H * n_q;
     g.rt = R <= 8 ? 1 : R <= 16 ? 2 : 4;
     g.n_rc = static_cast<int>((R + 8 * g.rt - 1) / (8 * g.rt));
-    const int64_t items = B * heads * g.n_rc, want = 152 * 4 * 4;
-    int64_t splits = (want + items - 1) / items;
-    int64_t chunk = (max_tokens + splits - 1) / splits;
-    if (chunk < 2 * kChunkUnit) chunk = 2 * kChunkUnit;
-    if (chunk > kMaxChunk) chunk = kMaxChunk;
-    chunk = (chunk + kChunkUnit - 1) / kChunkUnit * kChunkUnit;
-    g.chunk = static_cast<int>(chunk);
-    g.n_splits = static_cast<int>((max_tokens + chunk - 1) / chunk);
+    const int64_t tk = tile_keys(static_cast<int>(d));
+    const int64_t most = B * heads * g.n_rc * ((max_tokens + tk - 1) / tk);  // units
+    const int64_t ctas = kSms * (g.rt == 1 ? 3 : g.rt == 2 ? 2 : 1), need = (most + kMinShare - 1) / kMinShare;
+    g.ctas = static_cast<int>(need < ctas ? need : ctas);
     auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
     int64_t at = 0;
     g.part_o = at;
-    if (g.n_splits > 1) at = up(at + rows * g.n_splits * d * 4);
+    at = up(at + g.ctas * 2 * 8 * g.rt * d * 4);
     g.part_ml = at;
-    if (g.n_splits > 1) at = up(at + rows * g.n_splits * 8);
+    at = up(at + g.ctas * 2 * 8 * g.rt * 8);
+    g.prefix = at;
+    at = up(at + (B + 2) * 8);
     g.scores = at;
     if (accumulate) at = up(at + rows * max_tokens * 4);
     g.row_ml = at;
     if (accumulate) at = up(at + rows * 8);
-    g.total = at < 256 ? 256 : at;
+    g.total = at;
     return g;
 }
 
-template <int D, int RT, bool SCORES>
-cudaError_t launch(const DecodeArgs &a, int64_t ctas, cudaStream_t s)
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn()
 {
-    constexpr int kSmem = kWarps * 8 * RT * D * 4;
-    cudaError_t e = set_max_dynamic_smem<fa_kv4_decode_kernel<D, RT, SCORES>>(kSmem);
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+        else
+            cudaGetLastError();
+    });
+    return fn;
+}
+
+// The pool's codes as [page][head][row][128 values], a row being one token (d = 128) or two (d = 64); a box is
+// one page's rows of one head, at most a tile's.
+bool make_code_map(CUtensorMap *m, const Kv4Cache &c, void *base)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t rows = (cuuint64_t(1) << c.log2_page) * c.d / 128;
+    const cuuint64_t dims[4] = {128, rows, static_cast<cuuint64_t>(c.heads), static_cast<cuuint64_t>(c.n_pages)};
+    const cuuint64_t strides[3] = {64, rows * 64, rows * 64 * c.heads};
+    const cuuint32_t box[4] = {128, static_cast<cuuint32_t>(rows < 128 ? rows : 128), 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 4, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int RT, bool SCORES>
+cudaError_t launch(const DecodeArgs &a, int ctas, cudaStream_t s)
+{
+    using C = DecCfg<D, RT>;
+    CUtensorMap mk, mv;
+    if (!make_code_map(&mk, a.c, a.c.k) || !make_code_map(&mv, a.c, a.c.v)) return cudaErrorInvalidValue;
+    cudaError_t e = set_max_dynamic_smem<fa_kv4_decode_kernel<D, RT, SCORES>>(C::kSmemBytes);
     if (e != cudaSuccess) return e;
-    fa_kv4_decode_kernel<D, RT, SCORES><<<static_cast<unsigned>(ctas), kWarps * 32, kSmem, s>>>(a);
+    fa_kv4_decode_kernel<D, RT, SCORES><<<static_cast<unsigned>(ctas), kDecThreads, C::kSmemBytes, s>>>(mk, mv, a);
     return cudaGetLastError();
 }
 
 template <int D, bool SCORES>
-cudaError_t launch_rt(const DecodeArgs &a, int rt, int64_t ctas, cudaStream_t s)
+cudaError_t launch_rt(const DecodeArgs &a, int rt, int ctas, cudaStream_t s)
 {
     return rt == 1 ? launch<D, 1, SCORES>(a, ctas, s)
                    : rt == 2 ? launch<D, 2, SCORES>(a, ctas, s) : launch<D, 4, SCORES>(a, ctas, s);
@@ -576,8 +864,8 @@ cudaError_t fa_launch_kv4_decode(const Kv4DecodeProblem &p, void *workspace, cud
 {
     const int64_t cap = p.max_pages << p.cache.log2_page, heads = p.cache.heads;
     const Geometry g = geometry(p.B, p.H, heads, p.n_q, p.cache.d, cap, p.accumulate);
-    const int64_t rows = p.B * p.H * p.n_q, ctas = p.B * heads * g.n_rc * g.n_splits;
-    if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    const int64_t rows = p.B * p.H * p.n_q;
+    if (rows > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     char *ws = static_cast<char *>(workspace);
     DecodeArgs a;
     a.c = p.cache;
@@ -588,27 +876,27 @@ cudaError_t fa_launch_kv4_decode(const Kv4DecodeProblem &p, void *workspace, cud
     a.lse = p.lse;
     a.part_o = reinterpret_cast<float *>(ws + g.part_o);
     a.part_ml = reinterpret_cast<float2 *>(ws + g.part_ml);
+    a.prefix = reinterpret_cast<int64_t *>(ws + g.prefix);
     a.scores = p.accumulate ? reinterpret_cast<float *>(ws + g.scores) : nullptr;
     a.row_ml = reinterpret_cast<float2 *>(ws + g.row_ml);
     a.max_pages = p.max_pages;
+    a.B = static_cast<int>(p.B);
     a.R = static_cast<int>(p.H / heads * p.n_q);
     a.n_q = static_cast<int>(p.n_q);
     a.n_rc = g.n_rc;
-    a.n_splits = g.n_splits;
-    a.chunk = g.chunk;
     a.scale_log2 = static_cast<float>(static_cast<double>(p.scale) * 1.4426950408889634);
     cudaError_t e;
     if (p.cache.d == 128)
-        e = p.accumulate ? launch_rt<128, true>(a, g.rt, ctas, stream) : launch_rt<128, false>(a, g.rt, ctas, stream);
+        e = p.accumulate ? launch_rt<128, true>(a, g.rt, g.ctas, stream) : launch_rt<128, false>(a, g.rt, g.ctas, stream);
     else
-        e = p.accumulate ? launch_rt<64, true>(a, g.rt, ctas, stream) : launch_rt<64, false>(a, g.rt, ctas, stream);
+        e = p.accumulate ? launch_rt<64, true>(a, g.rt, g.ctas, stream) : launch_rt<64, false>(a, g.rt, g.ctas, stream);
     if (e != cudaSuccess) return e;
-    if (g.n_splits > 1) {
-        const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
+    // (where every item fits the smallest share and starts one, there is nothing to merge)
+    if (g.ctas > 1) {
         if (p.cache.d == 128)
-            fa_kv4_merge_kernel<128><<<grid, 128, 0, stream>>>(a, rows);
+            fa_kv4_merge_kernel<128><<<static_cast<unsigned>(rows), 256, 0, stream>>>(a, 8 * g.rt);
         else
-            fa_kv4_merge_kernel<64><<<grid, 128, 0, stream>>>(a, rows);
+            fa_kv4_merge_kernel<64><<<static_cast<unsigned>(rows), 256, 0, stream>>>(a, 8 * g.rt);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     if (p.accumulate) {

@@ -391,7 +391,7 @@ int64_t fa_bwd_workspace_bytes(int64_t B, int64_t H, int64_t N, int64_t d);
  * infinity gets scale 255 and reads back as NaN.
  *
  * Pages hold page_size tokens (a power of two, 16..1024) of every key head:
- *   k, v    : uint8 [n_pages][Hkv][page_size][d / 2], 16-byte aligned
+ *   k, v    : uint8 [n_pages][Hkv][page_size][d / 2], 32-byte aligned
  *   k_scale : uint8 [n_pages][Hkv][page_size][d / 32], 16-byte aligned
  *   v_scale : uint8 [n_pages][Hkv][page_size], 16-byte aligned
  *   weights : fp32  [n_pages][Hkv][page_size], 16-byte aligned, or NULL: the

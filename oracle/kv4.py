@@ -53,12 +53,14 @@ def rows(pages, table_row, n, page_size):
 
 def attention(q, k, v, scale, length):
     """One sequence: q [H, n_q, d], k, v [Hkv, length, d] -> O, LSE, per-key weight [Hkv, length], and
-    the sums that rounding bounds are made of: sum |q k| scale (largest over the keys a row admits) and sum p |v|."""
+    what rounding bounds are made of: sum |q k| scale and sum |k| max |q| scale (largest over the keys a row admits),
+    sum p |v|, and the softmax's sum with the largest term 1."""
     H, n_q, d = q.shape
     Hkv = k.shape[0]
     G = H // Hkv
     o, lse = np.zeros((H, n_q, d)), np.full((H, n_q), -np.inf)
     w, reach, spread = np.zeros((Hkv, length)), np.zeros((H, n_q)), np.zeros((H, n_q, d))
+    top_q, total = np.zeros((H, n_q)), np.ones((H, n_q))
     for h in range(H):
         for t in range(n_q):
             m = length - n_q + 1 + t
@@ -72,7 +74,8 @@ def attention(q, k, v, scale, length):
             o[h, t], lse[h, t] = p @ vv, top + np.log(e.sum())
             w[h // G, :m] += p
             reach[h, t], spread[h, t] = scale * (np.abs(kk) @ np.abs(q[h, t])).max(), p @ np.abs(vv)
-    return dict(o=o, lse=lse, weights=w, reach=reach, spread=spread)
+            top_q[h, t], total[h, t] = scale * np.abs(q[h, t]).max() * np.abs(kk).sum(-1).max(), e.sum()
+    return dict(o=o, lse=lse, weights=w, reach=reach, spread=spread, top_q=top_q, total=total)
 
 
 def evict(weights, length, keep, recent):

@@ -4,17 +4,20 @@ Everything that is whole numbers or moved bytes is compared exactly with the
 fp64 reference (oracle/kv4.py).  Computed outputs are compared within bounds
 made of the formats, per output:
 
-S    a score is a sum of d products, exact in the MMA's inputs, added in fp32: each of
-     the at most d + 4 additions is off by at most 2^-23 of the largest partial
-     sum (the tensor cores truncate), which sum |q k| scale bounds.  Its product
-     with scale log2 e and the subtraction of the maximum round by 2^-24 each.
-     eS = (d + 8) 2^-23 sum |q k| scale.
+S    a score is a sum of d products, exact in what the MMA multiplies, added in fp32 (each of
+     the at most d + 4 additions is off by at most 2^-23 of the largest partial sum, which
+     sum |q k| scale bounds).  Its product with scale log2 e and the subtraction of the maximum
+     round by 2^-24 each.  q goes in as two E4M3 parts, scaled to a maximum of at least 2^7, the second
+     16 times larger: their steps are 2^-9 / 16 at the least, so an element is off by at most
+     2^-14 of 2^7, 2^-21 of the row's maximum (and exact from 2^-6 on: eight bits in two times four).
+     eS = (d + 8) 2^-23 sum |q k| scale + 2^-21 max |q| sum |k| scale.
 LSE  its scores' error, and fp32's: eS + 2^-22 (|LSE| + 1).
 w    a probability is off by the factor exp(eS + error of LSE) and the exponential's 2^-22:
      w (2 eS + 2^-21 (|LSE| + 2)), a sum of n rows in fp32 adds n 2^-24.
-O    the weights' relative error on sum p |v|, P's rounding to a half (half a step: 2^-11; a
-     subnormal half loses at most 2^-25 of p times V's scale times 4, which a code of at most 6 multiplies: 1.5 2^-25 a key), and bf16's
-     rounding of the result (eight significant bits: half a step is 2^-8 of the value).
+O    the weights' relative error on sum p |v|; P in two E4M3 parts: the first is off by half a step, at most 2^-4,
+     the second by 2^-4 of that, 2^-8 together; the smallest steps, as above, 2^-14 of a scale of 256 that
+     stands for at most 2^3 times the row's largest term and four times the largest V scale: 2^-17 times 6
+     (a code) times that scale a key, over the sum l; and bf16's rounding of the result (eight significant bits: half a step is 2^-8 of the value).
 """
 import numpy as np
 import pytest
@@ -72,6 +75,9 @@ class Pool:
 
     def cache(self):
         return fa.KV4Cache(dev(self.k), dev(self.v), dev(self.ks), dev(self.vs), dev(self.w))
+
+    def largest_v_scale(self, b, n):
+        return ref.SCALES[ref.rows(self.vs, self.table[b], n, self.P)].max() if n else 0.0
 
     def kv(self, b, n):
         r = lambda t: ref.rows(t, self.table[b], n, self.P)  # noqa: E731
@@ -277,14 +283,15 @@ def check_attention(pool, q, lens, scale, o, lse, w_before=None, w_after=None, g
         n = int(lens[b])
         k, v = pool.kv(b, n)
         r = ref.attention(qd[b], k, v, scale, n)
-        eS = (d + 8) * 2.0 ** -23 * r["reach"]
+        eS = (d + 8) * 2.0 ** -23 * r["reach"] + 2.0 ** -21 * r["top_q"]
         none = r["lse"] == -np.inf
         assert (lse[b][none] == -np.inf).all() and (o[b][none] == 0).all()
         live = ~none
         top = np.where(live, np.abs(r["lse"]), 0)
         assert (np.abs(lse[b][live] - r["lse"][live]) <= (eS + 2.0 ** -22 * (top + 1))[live]).all()
         rel = 2 * eS + 2.0 ** -21 * (top + 2)
-        tol = (rel + 2.0 ** -11)[..., None] * r["spread"] + 2.0 ** -24 * n + 2.0 ** -8 * np.abs(r["o"])
+        tiny = n * 2.0 ** -17 * 6 * pool.largest_v_scale(b, n) / r["total"]
+        tol = (rel + 2.0 ** -8)[..., None] * r["spread"] + tiny[..., None] + 2.0 ** -8 * np.abs(r["o"])
         err = np.abs(o[b] - r["o"])
         assert (err <= tol).all(), (b, (err / np.maximum(tol, 1e-300)).max())
         if want_w is not None and n:
