@@ -16,9 +16,11 @@
 // as the A operand (2 x d/2 columns, for the CTA's life) and only Q streams
 // through shared memory (TMA, 128-byte swizzle, four stages); a Q block is used for
 // both key tiles.  The other columns hold three 128 x 128 accumulators in turn,
-// so the pipe runs on while the two warpgroups (one per key tile) read theirs.
-// Roles (352 threads): warps 0-3 and 4-7 the warpgroups, warp 8 loads Q, warp 9
-// issues the products and owns the tensor memory, warp 10 loads LSE log2 e.
+// so the pipe runs on while the warpgroups read theirs.
+// Roles (608 threads): warps 0-15 four warpgroups, two per key tile, each with half of a
+// block's queries (with one per tile a warpgroup's waits between its steps left the
+// tensor pipe idle: 829 us in place of XXX for 32 heads of 16384 queries, causal); warp 16
+// loads Q, warp 17 issues the products and owns the tensor memory, warp 18 loads LSE log2 e.
 //
 // Every mbarrier wait is bounded; one that gives up sets FA_ERR_TIMEOUT in this
 // file's status word and the CTA winds down.
@@ -27,6 +29,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "fa_fwd_common.cuh"
 
 using namespace sm100;
@@ -34,7 +38,7 @@ using namespace sm100;
 namespace {
 
 constexpr int kKeyTile = 128, kKeys = 256, kQBlock = 128;
-constexpr int kKwThreads = 352, kKwLoad = 8, kKwMma = 9, kKwLse = 10;
+constexpr int kKwThreads = 608, kKwLoad = 16, kKwMma = 17, kKwLse = 18;
 constexpr int kStages = 4;  // Q blocks in shared memory
 constexpr int kBufs = 3;    // accumulators in tensor memory
 
@@ -98,13 +102,13 @@ fa_key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const KwArgs a)
             mbar_init(BAR(KW_Q_FULL + s), 1);
             mbar_init(BAR(KW_Q_FREE + s), 1);
             mbar_init(BAR(KW_LSE_FULL + s), 1);
-            mbar_init(BAR(KW_LSE_FREE + s), 8);
+            mbar_init(BAR(KW_LSE_FREE + s), 16);
         }
         for (int s = 0; s < 2 * kBufs; ++s) {
             mbar_init(BAR(KW_S_FULL + s), 1);
-            mbar_init(BAR(KW_S_FREE + s), 4);
+            mbar_init(BAR(KW_S_FREE + s), 8);
         }
-        mbar_init(BAR(KW_K_READY), 8);
+        mbar_init(BAR(KW_K_READY), 16);
         mbar_init(BAR(KW_MMA_DONE), 1);
         fence_mbar_init();
     }
@@ -124,14 +128,17 @@ fa_key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const KwArgs a)
         if (lane == 0) {
             prefetch_tmap(&tm_q);
             bool ok = true;
-            int issued = 0;
+            int issued = 0, qb = qb0, qh = qh0;
             for (int i = 0; i < nq; ++i) {
                 const int st = i % kStages;
                 if (i >= kStages && !(ok = mbar_wait(BAR(KW_Q_FREE + st), (i / kStages - 1) & 1, kWaitLimitNs))) break;
                 mbar_arrive_expect_tx(BAR(KW_Q_FULL + st), C::kStageBytes);
                 for (int c = 0; c < D / 64; ++c)
-                    tma_load_3d(sb + st * C::kStageBytes + c * 16384, &tm_q, BAR(KW_Q_FULL + st), c * 64,
-                                (qb0 + i % per_head) * kQBlock, qh0 + i / per_head);
+                    tma_load_3d(sb + st * C::kStageBytes + c * 16384, &tm_q, BAR(KW_Q_FULL + st), c * 64, qb * kQBlock, qh);
+                if (++qb == a.n_qblocks) {
+                    qb = qb0;
+                    ++qh;
+                }
                 ++issued;
             }
             if (!ok) kw_report(FA_ERR_TIMEOUT);
@@ -163,56 +170,58 @@ fa_key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const KwArgs a)
         }
         if (!ok && lane == 0) kw_report(FA_ERR_TIMEOUT);
     } else if (warp == kKwMma) {
-        if (lane == 0) {
-            constexpr uint32_t id = idesc_bf16_f32(kKeyTile, kQBlock, false);
-            const uint64_t dq = smem_desc_sw128(sb, 16, 1024);
-            const uint32_t q_lo = static_cast<uint32_t>(dq), q_hi = static_cast<uint32_t>(dq >> 32);
-            bool ok = mbar_wait(BAR(KW_K_READY), 0, kWaitLimitNs);
-            tc_fence_after();
-            int n = 0;  // products so far
-            for (int i = 0; i < nq && ok; ++i) {
-                const int st = i % kStages;
-                if (!(ok = mbar_wait(BAR(KW_Q_FULL + st), (i / kStages) & 1, kWaitLimitNs))) break;
-                const uint32_t b_lo = q_lo + st * (C::kStageBytes >> 4);
-                for (int w = 0; w < 2; ++w, ++n) {
-                    const int buf = n % kBufs;
-                    const int last = n - kBufs;  // the buffer's product before this one
-                    if (last >= 0 && !(ok = mbar_wait(BAR(KW_S_FREE + kw_slot(last)), (last / 6) & 1, kWaitLimitNs))) break;
-                    tc_fence_after();
+        constexpr uint32_t id = idesc_bf16_f32(kKeyTile, kQBlock, false);
+        const uint64_t dq = smem_desc_sw128(sb, 16, 1024);
+        const uint32_t q_lo = static_cast<uint32_t>(dq), q_hi = static_cast<uint32_t>(dq >> 32);
+        bool ok = mbar_wait_warp(BAR(KW_K_READY), 0, kWaitLimitNs);
+        tc_fence_after();
+        int n = 0;  // products so far
+        for (int i = 0; i < nq && ok; ++i) {
+            const int st = i % kStages;
+            if (!(ok = mbar_wait_warp(BAR(KW_Q_FULL + st), (i / kStages) & 1, kWaitLimitNs))) break;
+            const uint32_t b_lo = q_lo + st * (C::kStageBytes >> 4);
+            for (int w = 0; w < 2; ++w, ++n) {
+                const int buf = n % kBufs;
+                const int last = n - kBufs;  // the buffer's product before this one
+                if (last >= 0 && !(ok = mbar_wait_warp(BAR(KW_S_FREE + kw_slot(last)), (last / 6) & 1, kWaitLimitNs))) break;
+                tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk)
                         mma_ts_lohi(tS + buf * 128, tK + w * 64 + kk * 8,
                                     b_lo + (((kk / 4) * 16384 + (kk % 4) * 32) >> 4), q_hi, id, kk > 0 ? 1u : 0u);
                     mma_commit(BAR(KW_S_FULL + kw_slot(n)));
+                    if (w == 1) mma_commit(BAR(KW_Q_FREE + st));
                 }
-                if (!ok) break;
-                mma_commit(BAR(KW_Q_FREE + st));
+                __syncwarp();
             }
-            if (!ok) kw_report(FA_ERR_TIMEOUT);
-            mma_commit(BAR(KW_MMA_DONE));
-            mbar_wait(BAR(KW_MMA_DONE), 0, ok ? kWaitLimitNs : kCleanupLimitNs);
         }
+        if (!ok && lane == 0) kw_report(FA_ERR_TIMEOUT);
+        if (elect_one()) mma_commit(BAR(KW_MMA_DONE));
+        __syncwarp();
+        mbar_wait_warp(BAR(KW_MMA_DONE), 0, ok ? kWaitLimitNs : kCleanupLimitNs);
     } else {
-        // ------------------------------------------------ one warpgroup per key tile, one thread per key
-        const int w = warp >> 2;
+        // --------------------------- two warpgroups per key tile, a thread per key and half of each query block
+        const int w = warp >> 3, half = (warp >> 2) & 1;
         const int key = k0 + w * kKeyTile + (warp & 3) * 32 + lane;
         const uint32_t loff = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        // K row into tensor memory: bf16 pairs, channel 2c, 2c + 1 in column c
+        // this half of the K row into tensor memory: bf16 pairs, channels 2c, 2c + 1 in column c
         {
-            const uint4 *src = reinterpret_cast<const uint4 *>(a.k + (static_cast<int64_t>(bhk) * a.N + key) * D);
+            const uint4 *src = reinterpret_cast<const uint4 *>(a.k + (static_cast<int64_t>(bhk) * a.N + key) * D) +
+                               half * (D / 16);
 #pragma unroll
             for (int c = 0; c < D / 64; ++c) {
-                uint32_t x[32];
+                uint32_t x[16];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < 4; ++j) {
                     uint4 u = make_uint4(0, 0, 0, 0);
-                    if (key < a.N) u = src[c * 8 + j];
+                    if (key < a.N) u = src[c * 4 + j];
                     x[4 * j] = u.x;
                     x[4 * j + 1] = u.y;
                     x[4 * j + 2] = u.z;
                     x[4 * j + 3] = u.w;
                 }
-                tmem_st32(tK + w * 64 + loff + c * 32, x);
+                tmem_st16(tK + w * 64 + loff + half * (D / 4) + c * 16, x);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -222,29 +231,23 @@ fa_key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const KwArgs a)
         const float2 sc = make_float2(a.scale_log2, a.scale_log2);
         float total = 0.f;
         bool ok = true;
+        int qb = qb0;  // query block within the head
         for (int i = 0; i < nq && ok; ++i) {
             const int st = i % kStages, n = 2 * i + w, buf = n % kBufs;
-            const int q0 = (qb0 + i % per_head) * kQBlock;
+            const int q0 = qb * kQBlock;
+            if (++qb == a.n_qblocks) qb = qb0;
             if (!mbar_wait_warp(BAR(KW_LSE_FULL + st), (i / kStages) & 1, kWaitLimitNs) ||
                 !mbar_wait_warp(BAR(KW_S_FULL + kw_slot(n)), (n / 6) & 1, kWaitLimitNs)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            const float *ls = reinterpret_cast<const float *>(smem + C::kLse) + st * kQBlock;
-            // sums of one block in their own registers first: 128 terms, then one addition to the total
+            const float *ls = reinterpret_cast<const float *>(smem + C::kLse) + st * kQBlock + half * 64;
+            const uint32_t src = tS + buf * 128 + loff + half * 64;
+            // 32 queries of this key: their scores in x, their sum added to s0, s1 (the tile's sums in registers of
+            // their own first: 64 terms, then one addition to the total)
             float2 s0 = make_float2(0.f, 0.f), s1 = s0;
-            const bool diag = CAUSAL && q0 < k0 + w * kKeyTile + kKeyTile - 1;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t x[32];
-                tmem_ld32(tS + buf * 128 + loff + c * 32, x);
-                tmem_wait_ld();
-                if (c == 3) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(BAR(KW_S_FREE + kw_slot(n)));
-                }
+            auto take = [&](const uint32_t (&x)[32], int c, auto diag) {
 #pragma unroll
                 for (int j = 0; j < 32; j += 4) {
                     const float4 l = *reinterpret_cast<const float4 *>(ls + c * 32 + j);
@@ -253,8 +256,8 @@ fa_key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const KwArgs a)
                     const float2 y1 = fma2(make_float2(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3])), sc,
                                            make_float2(l.z, l.w));
                     float2 p0 = make_float2(ex2(y0.x), ex2(y0.y)), p1 = make_float2(ex2(y1.x), ex2(y1.y));
-                    if (diag) {
-                        const int q = q0 + c * 32 + j;
+                    if constexpr (decltype(diag)::value) {
+                        const int q = q0 + half * 64 + c * 32 + j;
                         if (key > q) p0.x = 0.f;
                         if (key > q + 1) p0.y = 0.f;
                         if (key > q + 2) p1.x = 0.f;
@@ -263,13 +266,36 @@ fa_key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const KwArgs a)
                     s0 = add2(s0, p0);
                     s1 = add2(s1, p1);
                 }
-            }
+            };
+            // the next 32 scores are on their way from tensor memory while the last are used
+            auto tile = [&](auto diag) {
+                uint32_t x0[32], x1[32];
+                tmem_ld32(src, x0);
+                tmem_wait_ld();
+                tmem_ld32(src + 32, x1);
+                take(x0, 0, diag);
+                tmem_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(BAR(KW_S_FREE + kw_slot(n)));
+                take(x1, 1, diag);
+            };
+            if (CAUSAL && q0 < k0 + w * kKeyTile + kKeyTile - 1)
+                tile(std::true_type{});
+            else
+                tile(std::false_type{});
             __syncwarp();
             if (lane == 0) mbar_arrive(BAR(KW_LSE_FREE + st));
             total += (s0.x + s0.y) + (s1.x + s1.y);
         }
         if (!ok && lane == 0) kw_report(FA_ERR_TIMEOUT);
-        if (ok && key < a.N) a.weights[static_cast<int64_t>(bhk) * a.N + key] = total;
+        // the halves' sums, through the LSE stages (their last readers are behind the barrier)
+        float *sum = reinterpret_cast<float *>(smem + C::kLse);
+        asm volatile("barrier.cta.sync 1, 512;\n" ::: "memory");
+        if (half == 1) sum[w * kKeyTile + (warp & 3) * 32 + lane] = total;
+        asm volatile("barrier.cta.sync 1, 512;\n" ::: "memory");
+        if (ok && half == 0 && key < a.N)
+            a.weights[static_cast<int64_t>(bhk) * a.N + key] = total + sum[w * kKeyTile + (warp & 3) * 32 + lane];
     }
     tc_fence_before();
     __syncthreads();

@@ -336,48 +336,54 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         if (!ok) mbar_wait(BAR(K_FULL + n % ST), (n / ST) & 1, lim);
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------------- products
-        if (lane == 0) {
-            constexpr uint32_t idS = idesc_e2m1_e4m3_f32(128, N, false, false);
-            constexpr uint32_t idO = idesc_e2m1_e4m3_f32(128, N * KPT, true, true);
-            const uint64_t dA = smem_desc_sw128(sb, 16, 1024);  // K tiles, and V tiles read the other way
-            const uint64_t dQ = smem_desc_sw128(sb + C::kQ, 16, 1024);
-            const uint64_t dP = smem_desc_plain(sb + C::kP, 128, 2048);
-            bool ok = true;
-            int n = 0, seg = 0;
-            auto pv = [&](int m, bool first) -> bool {  // O^T (+)= V^T P^T of tile m
-                if (!mbar_wait(BAR(D_P_READY), m & 1, kWaitLimitNs)) return false;
-                if (!mbar_wait(BAR(V_FULL + m % ST), (m / ST) & 1, kWaitLimitNs)) return false;
-                tc_fence_after();
-                const uint32_t v = lo32(dA) + ((C::kV + m % ST * C::kHalf) >> 4);
+        constexpr uint32_t idS = idesc_e2m1_e4m3_f32(128, N, false, false);
+        constexpr uint32_t idO = idesc_e2m1_e4m3_f32(128, N * KPT, true, true);
+        const uint64_t dA = smem_desc_sw128(sb, 16, 1024);  // K tiles, and V tiles read the other way
+        const uint64_t dQ = smem_desc_sw128(sb + C::kQ, 16, 1024);
+        const uint64_t dP = smem_desc_plain(sb + C::kP, 128, 2048);
+        bool ok = true;
+        int n = 0, seg = 0;
+        auto pv = [&](int m, bool first) -> bool {  // O^T (+)= V^T P^T of tile m
+            if (!mbar_wait_warp(BAR(V_FULL + m % ST), (m / ST) & 1, kWaitLimitNs) ||
+                !mbar_wait_warp(BAR(D_P_READY), m & 1, kWaitLimitNs))
+                return false;
+            tc_fence_after();
+            const uint32_t v = lo32(dA) + ((C::kV + m % ST * C::kHalf) >> 4);
+            if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
                     mma_ss_f8_lohi(tO, v + kk * 256, hi32(dA), lo32(dP) + pbuf(m) * (C::kPBytes >> 4) + kk * 32, hi32(dP), idO,
                                    first && kk == 0 ? 0u : 1u);
-                mma_commit(BAR(V_FREE + m % ST));
                 mma_commit(pv_bar(m));
-                return true;
-            };
-            for (; w.left > 0 && ok; walk_next<TK>(w, a), ++seg) {
-                if (!(ok = mbar_wait(BAR(D_Q_READY), seg & 1, kWaitLimitNs))) break;
-                for (int t = w.t0; t < w.t1; ++t, ++n) {
-                    const int st = n % ST;
-                    if (!(ok = mbar_wait(BAR(K_FULL + st), (n / ST) & 1, kWaitLimitNs))) break;
-                    if (n > 0 && !(ok = mbar_wait(BAR(D_S_FREE), (n - 1) & 1, kWaitLimitNs))) break;
-                    tc_fence_after();
-                    const uint32_t k = lo32(dA) + st * (C::kHalf >> 4);
+                mma_commit(BAR(V_FREE + m % ST));
+            }
+            __syncwarp();
+            return true;
+        };
+        for (; w.left > 0 && ok; walk_next<TK>(w, a), ++seg) {
+            if (!(ok = mbar_wait_warp(BAR(D_Q_READY), seg & 1, kWaitLimitNs))) break;
+            for (int t = w.t0; t < w.t1; ++t, ++n) {
+                const int st = n % ST;
+                if (!(ok = mbar_wait_warp(BAR(K_FULL + st), (n / ST) & 1, kWaitLimitNs))) break;
+                if (n > 0 && !(ok = mbar_wait_warp(BAR(D_S_FREE), (n - 1) & 1, kWaitLimitNs))) break;
+                tc_fence_after();
+                const uint32_t k = lo32(dA) + st * (C::kHalf >> 4);
+                if (elect_one()) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         mma_ss_f8_lohi(tS + i * N, k + i * 2, hi32(dA), lo32(dQ) + (D == 128 ? i : i & 1) * 2, hi32(dQ), idS, 0u);
-                    mma_commit(BAR(K_FREE + st));
                     mma_commit(BAR(D_S_FULL));
-                    if (t > w.t0 && !(ok = pv(n - 1, t - 1 == w.t0))) break;
+                    mma_commit(BAR(K_FREE + st));
                 }
-                if (!ok || !(ok = pv(n - 1, w.t1 - 1 == w.t0))) break;
+                __syncwarp();
+                if (t > w.t0 && !(ok = pv(n - 1, t - 1 == w.t0))) break;
             }
-            if (!ok) kv4_timeout();
-            mma_commit(BAR(D_DONE));
-            mbar_wait(BAR(D_DONE), 0, ok ? kWaitLimitNs : kCleanupLimitNs);
+            if (!ok || !(ok = pv(n - 1, w.t1 - 1 == w.t0))) break;
         }
+        if (!ok && lane == 0) kv4_timeout();
+        if (elect_one()) mma_commit(BAR(D_DONE));
+        __syncwarp();
+        mbar_wait_warp(BAR(D_DONE), 0, ok ? kWaitLimitNs : kCleanupLimitNs);
     } else {
         // ------------------------------------------------------------------- softmax
         const uint32_t loff = static_cast<uint32_t>(warp * 32) << 16;

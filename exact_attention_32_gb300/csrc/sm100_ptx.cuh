@@ -98,6 +98,16 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, ui
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit_ns));
 }
 
+// True in one lane of a converged warp, the same each time.  Code around it stays uniform, so that what a
+// tcgen05.mma takes (descriptors, addresses) is computed in uniform registers: issued from an `if (lane == 0)`
+// branch, a product with small N took 46 cycles to issue, from an elected lane 39 (its operand's time).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n.reg .pred q;\nelect.sync _|q, 0xffffffff;\nselp.u32 %0, 1, 0, q;\n}\n" : "=r"(p));
+    return p != 0;
+}
+
 // ---------------------------------------------------------------- TMA copies
 
 // 3-D tiled bulk tensor load global -> shared, completing on `bar` (tx bytes).
