@@ -50,7 +50,9 @@ namespace {
 
 constexpr int kDecThreads = 192, kDecWarps = 6;
 constexpr int kLoadWarp = 4, kMmaWarp = 5;
-constexpr int kMinShare = 2;     // tiles: a shorter share costs more in merging than it saves
+constexpr int kMinShare = 4;   // units: a shorter share costs more in merging than it saves
+constexpr int kItemUnits = 3;  // what starting and ending an item costs, in tiles (4 to 6 us beside 1.4 us a tile)
+constexpr int kWholeTiles = 4;  // tables of so few tiles: items go to CTAs whole, and nothing is merged
 constexpr int kSms = 152;
 // A row's reference is set this far (log2) above the largest score when one passes it: with the maximum itself some of a
 // tile's 8 or 16 rows grow in nearly every one of the first dozens of tiles, at 1300 cycles each time.
@@ -61,6 +63,13 @@ constexpr uint64_t kCleanupLimitNs = 20000000ull;  // 20 ms while winding down
 
 __device__ __forceinline__ void kv4_timeout() { atomicExch(&g_kv4_status, FA_ERR_TIMEOUT); }
 
+// An item in several shares: its rows, its parts (0: this CTA holds no first part) and the first part's slot; the
+// others are slot 0 of the CTAs that follow.
+struct Split {
+    int64_t row;
+    int n_rows, parts, slot, pad;
+};
+
 struct DecodeArgs {
     Kv4Cache c;
     const __nv_bfloat16 *q;
@@ -69,11 +78,11 @@ struct DecodeArgs {
     float *lse;
     float *part_o;     // [CTA][2][RP][D], unnormalised; slot 0: the segment that starts its share, 1: that ends it
     float2 *part_ml;   // [CTA][2][RP]: running maximum (log2), sum
-    int64_t *prefix;   // [B + 2]: units before sequence b, all units, units a share
-    float *scores;     // [B][heads][R][max_tokens] log2 scores, or null
+    struct Split *split;  // [CTA]: the item whose first part is this CTA's, for the merge
+    float *scores;     // [B][heads][max_tokens][Rs] log2 scores, or null
     float2 *row_ml;    // [rows]: maximum (log2), 1 / sum; with scores
     int64_t max_pages;
-    int B, R, n_q, n_rc;
+    int B, R, Rs, n_q, n_rc, whole;
     float scale_log2;
 };
 
@@ -106,13 +115,16 @@ enum { D_S_FULL = 0, D_S_FREE, D_P_READY, D_PV_DONE, D_PV_DONE1, D_Q_READY, D_DO
 
 __host__ __device__ inline int tile_keys(int d) { return 128 * (128 / d); }
 
-// Units (tiles) of one (sequence, head, row chunk): at least one, so that an empty sequence's rows are written too.
+// Tiles of one (sequence, head, row chunk): at least one, so that an empty sequence's rows are written too.
 __device__ __forceinline__ int tiles_of(int len, int tk) { return len <= tk ? 1 : (len + tk - 1) / tk; }
+// Units of it: its tiles behind kItemUnits for its start and end; one where items go whole.
+__device__ __forceinline__ int item_units(const DecodeArgs &a, int n_t) { return a.whole ? 1 : n_t + kItemUnits; }
 
 // A CTA's way through its share: segments [t0, t1) of the n_t tiles of item `it` (head * n_rc + chunk) of sequence b.
+// The segment that a share begins or ends with may lie in an item's first units and hold no tile.
 struct Walk {
     int64_t left;  // units of the share still to come
-    int b, it, t0, t1, n_t, len;
+    int b, it, at, t0, t1, n_t, len;  // at: unit of the item where the segment begins
 };
 
 template <int TK>
@@ -121,20 +133,31 @@ __device__ __forceinline__ void walk_open(Walk &w, const DecodeArgs &a)
     w.len = kv4_length(a.lens, w.b, a.max_pages << a.c.log2_page);
     w.n_t = tiles_of(w.len, TK);
 }
-__device__ __forceinline__ void walk_clip(Walk &w) { w.t1 = static_cast<int>(min(static_cast<int64_t>(w.n_t), w.t0 + w.left)); }
+// The segment from unit w.at on, as far as the share or the item goes.
+__device__ __forceinline__ void walk_clip(Walk &w, const DecodeArgs &a)
+{
+    if (a.whole) {
+        w.t0 = 0;
+        w.t1 = w.n_t;
+        return;
+    }
+    const int end = static_cast<int>(min(static_cast<int64_t>(w.n_t + kItemUnits), w.at + w.left));
+    w.t0 = max(0, w.at - kItemUnits);
+    w.t1 = max(0, end - kItemUnits);
+}
 
 template <int TK>
 __device__ __forceinline__ void walk_next(Walk &w, const DecodeArgs &a)
 {
-    w.left -= w.t1 - w.t0;
-    w.t0 = 0;
+    w.left -= item_units(a, w.n_t) - w.at;
+    w.at = 0;
     if (w.left <= 0) return;
     if (++w.it == a.c.heads * a.n_rc) {
         w.it = 0;
         ++w.b;
         walk_open<TK>(w, a);
     }
-    walk_clip(w);
+    walk_clip(w, a);
 }
 
 // Two fp32 -> two E4M3 bytes (`lo` in the low one), and back, exactly.
@@ -214,13 +237,16 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         tmem_relinquish();
     }
 
+    // the kernel behind this one may be set up meanwhile (it waits for this one's end before it reads)
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+
     // the share of this CTA: units before each sequence by a scan over the lengths, 192 at a time
     int64_t *scan = reinterpret_cast<int64_t *>(smem + C::kWalk);
     Walk &start = *reinterpret_cast<Walk *>(smem + C::kWalk + 64);
     static_assert(sizeof(Walk) <= 64, "fits behind the scan");
     const int items = a.c.heads * a.n_rc;
     auto units_of = [&](int b) -> int64_t {
-        return b < a.B ? static_cast<int64_t>(tiles_of(kv4_length(a.lens, b, cap), TK)) * items : 0;
+        return b < a.B ? static_cast<int64_t>(item_units(a, tiles_of(kv4_length(a.lens, b, cap), TK))) * items : 0;
     };
     int64_t total = 0;
     {
@@ -233,11 +259,11 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         for (int i = 0; i < kDecWarps; ++i) total += scan[i];
     }
     int64_t share = (total + gridDim.x - 1) / gridDim.x;
-    if (share < kMinShare) share = kMinShare;
+    if (!a.whole && share < kMinShare) share = kMinShare;
     const int64_t u0 = blockIdx.x * share;
     if (tid == 0) start.left = 0;
     int64_t base = 0;
-    for (int b0 = 0; b0 < a.B && (base <= u0 || blockIdx.x == 0); b0 += kDecThreads) {
+    for (int b0 = 0; b0 < a.B && base <= u0; b0 += kDecThreads) {
         const int b = b0 + tid;
         const int64_t mine = units_of(b);
         int64_t x = mine;
@@ -255,23 +281,20 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             all += scan[i];
         }
         const int64_t before = base + x - mine;
-        if (blockIdx.x == 0 && b < a.B) a.prefix[b] = before;
         if (b < a.B && u0 >= before && u0 < before + mine) {
             Walk w;
             w.b = b;
             w.left = min(share, total - u0);
             walk_open<TK>(w, a);
-            w.it = static_cast<int>((u0 - before) / w.n_t);
-            w.t0 = static_cast<int>((u0 - before) % w.n_t);
-            walk_clip(w);
+            const int units = item_units(a, w.n_t);
+            w.it = static_cast<int>((u0 - before) / units);
+            w.at = static_cast<int>((u0 - before) % units);
+            walk_clip(w, a);
             start = w;
         }
         base += all;
     }
-    if (blockIdx.x == 0 && tid == 0) {
-        a.prefix[a.B] = total;
-        a.prefix[a.B + 1] = share;
-    }
+    if (tid == 0) a.split[blockIdx.x].parts = 0;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -296,7 +319,7 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         int n = 0;
         bool ok = true;
         for (; w.left > 0 && ok; walk_next<TK>(w, a)) {
-            const int h = w.it / a.n_rc;
+            const int h = w.it / a.n_rc;  // (a segment without a tile falls through every role)
             for (int t = w.t0; t < w.t1; ++t, ++n) {
                 const int st = n % ST, key = t * TK + lane * bt;
                 int page = -1;
@@ -360,8 +383,9 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             __syncwarp();
             return true;
         };
-        for (; w.left > 0 && ok; walk_next<TK>(w, a), ++seg) {
-            if (!(ok = mbar_wait_warp(BAR(D_Q_READY), seg & 1, kWaitLimitNs))) break;
+        for (; w.left > 0 && ok; walk_next<TK>(w, a)) {
+            if (w.t0 == w.t1) continue;
+            if (!(ok = mbar_wait_warp(BAR(D_Q_READY), seg++ & 1, kWaitLimitNs))) break;
             for (int t = w.t0; t < w.t1; ++t, ++n) {
                 const int st = n % ST;
                 if (!(ok = mbar_wait_warp(BAR(K_FULL + st), (n / ST) & 1, kWaitLimitNs))) break;
@@ -390,6 +414,7 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         int n = 0;
         bool ok = true;
         for (; w.left > 0 && ok; walk_next<TK>(w, a)) {
+            if (w.t0 == w.t1) continue;
             const int h = w.it / a.n_rc, rc = w.it - h * a.n_rc;
             const int64_t bh = static_cast<int64_t>(w.b) * a.c.heads + h;
             const int row0 = rc * RP, n_rows = min(RP, a.R - row0);
@@ -516,10 +541,17 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                     for (int k = 0; k < KPT; ++k) {
                         const int key = key0 + tid * KPT + k;
                         if (key < w.len) {
-                            float *s = a.scores + (bh * a.R + row0) * cap + key;
+                            float *s = a.scores + (bh * cap + key) * a.Rs + row0;
+                            if (a.R <= 2) {
+                                s[0] = x[k][0].x;
+                                if (a.R == 2) s[1] = x[k][0].y;
+                            } else {
 #pragma unroll
-                            for (int r = 0; r < RP; ++r, s += cap)
-                                if (r < n_rows) *s = r & 1 ? x[k][r / 2].y : x[k][r / 2].x;
+                                for (int r = 0; r < RP / 4; ++r)
+                                    if (row0 + 4 * r < a.R)
+                                        *reinterpret_cast<float4 *>(s + 4 * r) =
+                                            make_float4(x[k][2 * r].x, x[k][2 * r].y, x[k][2 * r + 1].x, x[k][2 * r + 1].y);
+                            }
                         }
                     }
                 }
@@ -659,6 +691,15 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             if (D == 128 || half == 0) {
                 const bool whole = w.t0 == 0 && w.t1 == w.n_t;
                 const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (n == w.t1 - w.t0 ? 0 : 1);
+                if (tid == 0 && w.t0 == 0 && !whole) {
+                    Split sp;
+                    sp.row = bh * a.R + row0;
+                    sp.n_rows = n_rows;
+                    sp.parts = 1 + static_cast<int>((w.n_t - w.t1 + share - 1) / share);
+                    sp.slot = static_cast<int>(slot);
+                    sp.pad = 0;
+                    a.split[blockIdx.x] = sp;
+                }
 #pragma unroll
                 for (int r = 0; r < RP; ++r) {
                     if (r >= n_rows) break;
@@ -691,61 +732,71 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     }
 }
 
-// Merge of a row whose item lies in several shares: one block a row, its warps over the parts.
+// Merge of the items that lie in several shares: a block per CTA of the kernel before, for the item whose first part that
+// CTA holds; its warps over the item's rows and each row's parts.
+constexpr int kMergeWarps = 16;
+
 template <int D>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kMergeWarps * 32)
 fa_kv4_merge_kernel(const DecodeArgs a, int RP)
 {
-    constexpr int PER = D / 32, kWarps = 8;
-    __shared__ float sm_l[kWarps];
-    __shared__ float sm_x[kWarps][D];
-    __shared__ float sm_max[kWarps];
+    constexpr int PER = D / 32;
+    __shared__ float sm_l[kMergeWarps];
+    __shared__ float sm_x[kMergeWarps][D];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t row = blockIdx.x, bh = row / a.R;
-    const int r = static_cast<int>(row - bh * a.R), b = static_cast<int>(bh / a.c.heads), h = static_cast<int>(bh % a.c.heads);
-    const int n_t = tiles_of(kv4_length(a.lens, b, a.max_pages << a.c.log2_page), 128 * (128 / D));
-    const int64_t share = a.prefix[a.B + 1];
-    const int64_t u0 = a.prefix[b] + static_cast<int64_t>(h * a.n_rc + r / RP) * n_t;
-    const int64_t c0 = u0 / share, c1 = (u0 + n_t - 1) / share;
-    if (c0 == c1) return;  // finished in place
-    const int parts = static_cast<int>(c1 - c0) + 1, rr = r % RP;
-    // an item's first part starts its CTA's share or ends it; the later ones start theirs
-    auto slot = [&](int i) { return (c0 + i) * 2 + (i == 0 && u0 != c0 * share ? 1 : 0); };
-    float m = -FLT_MAX;
-    for (int i = threadIdx.x; i < parts; i += 256) m = fmaxf(m, a.part_ml[slot(i) * RP + rr].x);
-    m = warp_max(m);
-    if (lane == 0) sm_max[warp] = m;
-    __syncthreads();
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    const Split sp = a.split[blockIdx.x];
+    if (sp.parts == 0) return;
+    auto slot = [&](int i) -> int64_t { return i == 0 ? sp.slot : (static_cast<int64_t>(blockIdx.x) + i) * 2; };
+    const int per_row = max(1, kMergeWarps / sp.n_rows);  // warps a row
+    for (int r0 = 0; r0 < sp.n_rows; r0 += kMergeWarps / per_row) {
+        const int rr = r0 + warp / per_row, w = warp % per_row;
+        const bool live = rr < sp.n_rows;
+        float m = -FLT_MAX, l = 0.f, x[PER];
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) m = fmaxf(m, sm_max[i]);
-    float l = 0.f, x[PER];
+        for (int i = 0; i < PER; ++i) x[i] = 0.f;
+        if (live) {
+            for (int i = lane; i < sp.parts; i += 32) m = fmaxf(m, a.part_ml[slot(i) * RP + rr].x);
+            m = warp_max(m);
+#pragma unroll 8
+            for (int i = w; i < sp.parts; i += per_row) {
+                const int64_t s = slot(i) * RP + rr;
+                const float2 v = a.part_ml[s];
+                const float *po = a.part_o + s * D + lane * PER;
+                float y[PER];
+                if constexpr (PER == 4)
+                    *reinterpret_cast<float4 *>(y) = *reinterpret_cast<const float4 *>(po);
+                else
+                    *reinterpret_cast<float2 *>(y) = *reinterpret_cast<const float2 *>(po);
+                const float f = ex2(v.x - m);
+                l = fmaf(f, v.y, l);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) x[i] = 0.f;
-#pragma unroll 4
-    for (int i = warp; i < parts; i += kWarps) {
-        const int64_t s = slot(i) * RP + rr;
-        const float2 v = a.part_ml[s];
-        const float f = ex2(v.x - m);
-        l = fmaf(f, v.y, l);
+                for (int j = 0; j < PER; ++j) x[j] = fmaf(f, y[j], x[j]);
+            }
+        }
+        if (per_row > 1) {
+            if (lane == 0) sm_l[warp] = l;
 #pragma unroll
-        for (int j = 0; j < PER; ++j) x[j] = fmaf(f, a.part_o[s * D + j * 32 + lane], x[j]);
-    }
-    if (lane == 0) sm_l[warp] = l;
+            for (int j = 0; j < PER; ++j) sm_x[warp][lane * PER + j] = x[j];
+            __syncthreads();  // (with several warps a row all rows go in one turn)
+            if (live && w == 0)
+                for (int i = 1; i < per_row; ++i) {
+                    l += sm_l[warp + i];
 #pragma unroll
-    for (int j = 0; j < PER; ++j) sm_x[warp][j * 32 + lane] = x[j];
-    __syncthreads();
-    if (threadIdx.x >= D) return;
-    float y = 0.f, ll = 0.f;
+                    for (int j = 0; j < PER; ++j) x[j] += sm_x[warp + i][lane * PER + j];
+                }
+        }
+        if (!live || w != 0) continue;
+        const int64_t row = sp.row + rr;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-        y += sm_x[i][threadIdx.x];
-        ll += sm_l[i];
-    }
-    const float inv = ll == 0.f ? 0.f : 1.f / ll;
-    a.o[row * D + threadIdx.x] = __float2bfloat16_rn(y * inv);
-    if (threadIdx.x == 0) {
-        a.lse[row] = ll == 0.f ? -INFINITY : (m + log2f(ll)) * kLn2;
-        if (a.scores != nullptr) a.row_ml[row] = make_float2(ll == 0.f ? 0.f : m, inv);
+        for (int j = 0; j < PER; j += 2)
+            *reinterpret_cast<__nv_bfloat162 *>(a.o + row * D + lane * PER + j) = __floats2bfloat162_rn(x[j] * inv, x[j + 1] * inv);
+        if (lane == 0) {
+            a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+            if (a.scores != nullptr) a.row_ml[row] = make_float2(l == 0.f ? 0.f : m, inv);
+        }
     }
 }
 
@@ -757,14 +808,24 @@ fa_kv4_weights_kernel(const DecodeArgs a, int blocks)
     const int h = static_cast<int>(bh - b * a.c.heads);
     const int64_t cap = a.max_pages << a.c.log2_page;
     const int len = kv4_length(a.lens, b, cap);
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    const float2 *ml = a.row_ml + bh * a.R;
     for (int key = blockIdx.x % blocks * 256 + threadIdx.x; key < len; key += blocks * 256) {
         const int page = kv4_page(a.c, a.table, b, a.max_pages, key);
         if (page < 0) continue;
-        const float *s = a.scores + bh * a.R * cap + key;
-        const float2 *ml = a.row_ml + bh * a.R;
+        const float *s = a.scores + (bh * cap + key) * a.Rs;
         float w = 0.f;
-#pragma unroll 4
-        for (int r = 0; r < a.R; ++r) w = fmaf(ex2(s[r * cap] - ml[r].x), ml[r].y, w);
+        if (a.R <= 2) {
+            for (int r = 0; r < a.R; ++r) w = fmaf(ex2(s[r] - ml[r].x), ml[r].y, w);
+        } else {
+            for (int r = 0; r < a.R; r += 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(s + r);
+                w = fmaf(ex2(v.x - ml[r].x), ml[r].y, w);
+                if (r + 1 < a.R) w = fmaf(ex2(v.y - ml[r + 1].x), ml[r + 1].y, w);
+                if (r + 2 < a.R) w = fmaf(ex2(v.z - ml[r + 2].x), ml[r + 2].y, w);
+                if (r + 3 < a.R) w = fmaf(ex2(v.w - ml[r + 3].x), ml[r + 3].y, w);
+            }
+        }
         a.c.weights[kv4_row(a.c, page, h, key)] += w;
     }
 }
@@ -772,8 +833,8 @@ fa_kv4_weights_kernel(const DecodeArgs a, int blocks)
 // ------------------------------------------------------------------ host side
 
 struct Geometry {
-    int rt, n_rc, ctas;
-    int64_t part_o, part_ml, prefix, scores, row_ml, total;  // byte offsets in the workspace
+    int rt, n_rc, ctas, whole, Rs;
+    int64_t part_o, part_ml, split, scores, row_ml, total;  // byte offsets in the workspace
 };
 
 Geometry geometry(int64_t B, int64_t H, int64_t heads, int64_t n_q, int64_t d, int64_t max_tokens, int accumulate)
@@ -783,8 +844,11 @@ Geometry geometry(int64_t B, int64_t H, int64_t heads, int64_t n_q, int64_t d, i
     g.rt = R <= 8 ? 1 : R <= 16 ? 2 : 4;
     g.n_rc = static_cast<int>((R + 8 * g.rt - 1) / (8 * g.rt));
     const int64_t tk = tile_keys(static_cast<int>(d));
-    const int64_t most = B * heads * g.n_rc * ((max_tokens + tk - 1) / tk);  // units
-    const int64_t ctas = kSms * (g.rt == 1 ? 3 : g.rt == 2 ? 2 : 1), need = (most + kMinShare - 1) / kMinShare;
+    const int64_t items = B * heads * g.n_rc, tiles = (max_tokens + tk - 1) / tk;
+    g.whole = tiles <= kWholeTiles;
+    g.Rs = static_cast<int>(R <= 2 ? R : (R + 3) / 4 * 4);
+    const int64_t ctas = kSms * (g.rt == 1 ? 3 : g.rt == 2 ? 2 : 1);
+    const int64_t need = g.whole ? items : (items * (tiles + kItemUnits) + kMinShare - 1) / kMinShare;
     g.ctas = static_cast<int>(need < ctas ? need : ctas);
     auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
     int64_t at = 0;
@@ -792,10 +856,10 @@ Geometry geometry(int64_t B, int64_t H, int64_t heads, int64_t n_q, int64_t d, i
     at = up(at + g.ctas * 2 * 8 * g.rt * d * 4);
     g.part_ml = at;
     at = up(at + g.ctas * 2 * 8 * g.rt * 8);
-    g.prefix = at;
-    at = up(at + (B + 2) * 8);
+    g.split = at;
+    at = up(at + g.ctas * static_cast<int64_t>(sizeof(Split)));
     g.scores = at;
-    if (accumulate) at = up(at + rows * max_tokens * 4);
+    if (accumulate) at = up(at + B * heads * g.Rs * max_tokens * 4);
     g.row_ml = at;
     if (accumulate) at = up(at + rows * 8);
     g.total = at;
@@ -860,6 +924,26 @@ cudaError_t launch_rt(const DecodeArgs &a, int rt, int ctas, cudaStream_t s)
 
 }  // namespace
 
+namespace {
+
+// Launch of a kernel that waits for the one before it itself (griddepcontrol.wait), so that its own launch overlaps that one.
+template <typename K>
+cudaError_t launch_behind(K kern, int64_t grid, int threads, cudaStream_t s, const DecodeArgs &a, int arg)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.stream = s;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, a, arg);
+}
+
+}  // namespace
+
 int64_t fa_kv4_decode_workspace(int64_t B, int64_t H, int64_t heads, int64_t n_q, int64_t d, int64_t max_tokens,
                                 int accumulate)
 {
@@ -882,7 +966,7 @@ cudaError_t fa_launch_kv4_decode(const Kv4DecodeProblem &p, void *workspace, cud
     a.lse = p.lse;
     a.part_o = reinterpret_cast<float *>(ws + g.part_o);
     a.part_ml = reinterpret_cast<float2 *>(ws + g.part_ml);
-    a.prefix = reinterpret_cast<int64_t *>(ws + g.prefix);
+    a.split = reinterpret_cast<Split *>(ws + g.split);
     a.scores = p.accumulate ? reinterpret_cast<float *>(ws + g.scores) : nullptr;
     a.row_ml = reinterpret_cast<float2 *>(ws + g.row_ml);
     a.max_pages = p.max_pages;
@@ -890,6 +974,8 @@ cudaError_t fa_launch_kv4_decode(const Kv4DecodeProblem &p, void *workspace, cud
     a.R = static_cast<int>(p.H / heads * p.n_q);
     a.n_q = static_cast<int>(p.n_q);
     a.n_rc = g.n_rc;
+    a.Rs = g.Rs;
+    a.whole = g.whole;
     a.scale_log2 = static_cast<float>(static_cast<double>(p.scale) * 1.4426950408889634);
     cudaError_t e;
     if (p.cache.d == 128)
@@ -897,20 +983,17 @@ cudaError_t fa_launch_kv4_decode(const Kv4DecodeProblem &p, void *workspace, cud
     else
         e = p.accumulate ? launch_rt<64, true>(a, g.rt, g.ctas, stream) : launch_rt<64, false>(a, g.rt, g.ctas, stream);
     if (e != cudaSuccess) return e;
-    // (where every item fits the smallest share and starts one, there is nothing to merge)
-    if (g.ctas > 1) {
-        if (p.cache.d == 128)
-            fa_kv4_merge_kernel<128><<<static_cast<unsigned>(rows), 256, 0, stream>>>(a, 8 * g.rt);
-        else
-            fa_kv4_merge_kernel<64><<<static_cast<unsigned>(rows), 256, 0, stream>>>(a, 8 * g.rt);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (!g.whole && g.ctas > 1) {
+        e = p.cache.d == 128 ? launch_behind(fa_kv4_merge_kernel<128>, g.ctas, kMergeWarps * 32, stream, a, 8 * g.rt)
+                             : launch_behind(fa_kv4_merge_kernel<64>, g.ctas, kMergeWarps * 32, stream, a, 8 * g.rt);
+        if (e != cudaSuccess) return e;
     }
     if (p.accumulate) {
         int64_t blocks = (cap + 255) / 256;
         if (blocks > 512) blocks = 512;
         if (blocks * p.B * heads > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-        fa_kv4_weights_kernel<<<static_cast<unsigned>(blocks * p.B * heads), 256, 0, stream>>>(a, static_cast<int>(blocks));
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        e = launch_behind(fa_kv4_weights_kernel, blocks * p.B * heads, 256, stream, a, static_cast<int>(blocks));
+        if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
 }
