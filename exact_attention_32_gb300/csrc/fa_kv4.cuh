@@ -58,6 +58,16 @@ __device__ __forceinline__ int kv4_page(const Kv4Cache &c, const int32_t *table,
     return -1;
 }
 
+// The same without the report and without a branch, for loops that keep several rows under way: page 0 where the
+// entry is no page, and whether it is one.
+__device__ __forceinline__ int kv4_page_quiet(const Kv4Cache &c, const int32_t *table, int64_t b, int64_t max_pages,
+                                              int pos, bool *valid)
+{
+    const int page = table[b * max_pages + (pos >> c.log2_page)];
+    *valid = static_cast<unsigned>(page) < static_cast<unsigned>(c.n_pages);
+    return *valid ? page : 0;
+}
+
 // Row of the pool that holds token `pos` of head h in `page`: the index into
 // k, v (rows of d/2 bytes), k_scale (d/32 bytes), v_scale (one byte) and weights.
 __device__ __forceinline__ int64_t kv4_row(const Kv4Cache &c, int page, int h, int pos)
@@ -82,16 +92,16 @@ __device__ __forceinline__ void kv4_decode8(uint32_t x, uint32_t (&r)[4])
         : "r"(x));
 }
 
-// Eight fp32 values as four bytes of codes: to nearest, ties to the even code, at most 6 in magnitude.
-__device__ __forceinline__ uint32_t kv4_encode8(const float (&y)[8])
+// Eight halves as four bytes of codes: to nearest, ties to the even code, at most 6 in magnitude.
+__device__ __forceinline__ uint32_t kv4_encode8(const uint32_t (&y)[4])
 {
     uint32_t r;
     asm("{\n.reg .b8 a, b, c, d;\n"
-        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\ncvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
-        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\ncvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+        "cvt.rn.satfinite.e2m1x2.f16x2 a, %1;\ncvt.rn.satfinite.e2m1x2.f16x2 b, %2;\n"
+        "cvt.rn.satfinite.e2m1x2.f16x2 c, %3;\ncvt.rn.satfinite.e2m1x2.f16x2 d, %4;\n"
         "mov.b32 %0, {a, b, c, d};\n}\n"
         : "=r"(r)
-        : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
+        : "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]));
     return r;
 }
 

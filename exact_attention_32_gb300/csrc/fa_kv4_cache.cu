@@ -7,58 +7,83 @@ namespace {
 
 // --------------------------------------------------------------------- append
 
-// amax / 6 on the scale grid (to nearest even), as a byte; 255 for a block with a NaN or an infinity.
-// amax is a bf16 value, so amax / 6 either is a middle of two grid values exactly or
-// lies at least 2^-9 (relative) from one: the rounded fp32 quotient falls on the
-// same side as the exact one.
-__device__ __forceinline__ uint32_t kv4_scale_byte(float amax)
+// amax / 6 on the scale grid (to nearest even), as a byte, from amax's bf16 bits; 255 for a block with a NaN or an
+// infinity.  amax = X 2^a (X < 256) and a middle of two scales is M 2^b (M < 32), so amax / 6 is a middle exactly or
+// differs from it by at least 1 part in 255 (X 2^k against 3 M).  From 2^-14 on, the product with the rounded 1/6,
+// rounded to a half (2^-11), is the middle where the quotient is one and keeps the side where it is not; the byte is
+// that half's upper bits, to nearest even.  Below, a half's steps are too coarse for the same argument: there the
+// rounded quotient (2^-24) is taken to multiples of 2^-17 (adding 96 rounds to its last place).
+__device__ __forceinline__ uint32_t kv4_scale_byte(uint32_t amax)
 {
-    if (!(amax < INFINITY)) return 255u;
-    const float s = fminf(__fdiv_rn(amax, 6.f), 10240.f);
-    if (s < 6.103515625e-05f)  // below 2^-14: multiples of 2^-17 (adding 96 rounds to its last place)
-        return __float2uint_rn(__fsub_rn(__fadd_rn(s, 96.f), 96.f) * 131072.f);
-    uint32_t b = __float_as_uint(s);
-    b += 0x7FFFFu + ((b >> 20) & 1u);  // four significant bits, to nearest even
-    return (b >> 20) - (112u << 3);
+    if (amax >= 0x7F80u) return 255u;
+    const float x = __uint_as_float(amax << 16);
+    const float s = fminf(x * 0.16666667163372039794921875f, 10240.f);
+    if (s < 6.2e-05f) {  // (a little above 2^-14, where both ways agree)
+        const float q = __fdiv_rn(x, 6.f);
+        if (q < 6.103515625e-05f) return __float2uint_rn(__fsub_rn(__fadd_rn(q, 96.f), 96.f) * 131072.f);
+    }
+    const uint32_t h = __half_as_ushort(__float2half_rn(s));
+    return (h + 63u + ((h >> 7) & 1u)) >> 7;
 }
 
-// Four bytes of codes of eight values under the scale of `byte`.  x is a bf16
-// value and the scale has four significant bits, so x / s meets a middle of two
-// E2M1 values exactly or not within 2^-9 of it: the rounded quotient keeps the side.
+// Four bytes of codes of eight values under the scale of `byte`.  x is a bf16 value X 2^a (X < 256), the scale
+// n 2^b (n < 16), a middle of two E2M1 values M 2^c (M <= 7), so x / s is a middle exactly or differs from it by at
+// least 1 part in 255 (X 2^k against n M <= 105, both whole or X < 256).  The product with 1 / s (rcp.approx, 2^-23) is
+// within 2^-22 of x / s, and rounding it to a half (2^-11) gives the middle where x / s is one and keeps the side
+// where it is not: the codes are those of the exact quotient, for a third of a division's instructions.
 __device__ __forceinline__ uint32_t kv4_codes(const float (&x)[8], uint32_t byte)
 {
-    const float s = kv4_scale(byte);
     if (byte == 0u || byte == 255u) return 0u;
-    float y[8];
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(kv4_scale(byte)));
+    uint32_t y[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[i], s);
+    for (int i = 0; i < 4; ++i) {
+        const __half2 q = __floats2half2_rn(x[2 * i] * r, x[2 * i + 1] * r);
+        y[i] = *reinterpret_cast<const uint32_t *>(&q);
+    }
     return kv4_encode8(y);
 }
 
-// amax that keeps a NaN (fmaxf would drop it).
-__device__ __forceinline__ float max_nan(float a, float b)
+// Larger of two pairs of unsigned 16-bit values.  The bits of |x| order bf16 values, infinities and NaNs (above all).
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b)
 {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 
-__device__ __forceinline__ float unpack8(uint4 u, float (&x)[8])
+// Eight bf16 values as fp32; returns the bits of the largest |x|, in both halves.
+__device__ __forceinline__ uint32_t unpack8(uint4 u, float (&x)[8])
 {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    float m = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         x[2 * i] = __uint_as_float(w[i] << 16);
         x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        m = max_nan(m, max_nan(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
     }
-    return m;
+    const uint32_t m = max_u16x2(max_u16x2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
+                                 max_u16x2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+    return max_u16x2(m, __byte_perm(m, m, 0x1032));
+}
+
+// n / d and n % d of row indices, in 32 bits where all of them fit (a 64-bit division costs as much as the rest of a row).
+__device__ __forceinline__ int64_t row_div(int64_t n, int64_t d, int64_t rows, int64_t *rest)
+{
+    if (rows <= 0x7fffffffLL) {
+        const uint32_t q = static_cast<uint32_t>(n) / static_cast<uint32_t>(d);
+        *rest = static_cast<uint32_t>(n) - q * static_cast<uint32_t>(d);
+        return q;
+    }
+    const int64_t q = n / d;
+    *rest = n - q * d;
+    return q;
 }
 
 // D / 8 threads a row, eight channels each: one 16-byte load of K and of V, the
 // maxima over 4 threads (a K block) and over the row (V) by shuffles, four bytes of
-// codes out.  Memory-bound: 4 d bytes in and d + d/32 + 1 out a row.
+// codes out.  Memory-bound: 4 d bytes in and d + d/32 + 1 out a row; a thread has two rows
+// under way, and asks for their values before it knows their pages.
 template <int D>
 __global__ void __launch_bounds__(256)
 fa_kv4_append_kernel(Kv4Cache c, const uint4 *__restrict__ k_new, const uint4 *__restrict__ v_new,
@@ -66,51 +91,71 @@ fa_kv4_append_kernel(Kv4Cache c, const uint4 *__restrict__ k_new, const uint4 *_
                      const int32_t *__restrict__ lens, const int32_t *__restrict__ table, int64_t rows, int64_t S,
                      int64_t max_pages)
 {
-    constexpr int TPR = D / 8;
+    constexpr int TPR = D / 8, U = 2;
     const int t = threadIdx.x % TPR;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * (256 / TPR);
-    // whole warps stay in the loop together: rows past the end are computed on row 0's data and not stored
-    for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * (256 / TPR); r0 < rows; r0 += stride) {
-        const int64_t r = r0 + threadIdx.x / TPR;
-        const int64_t rr = r < rows ? r : 0;
-        const int64_t bh = rr / S;
-        const int i = static_cast<int>(rr - bh * S);
-        const int64_t b = bh / c.heads;
-        const int h = static_cast<int>(bh - b * c.heads);
-        int n = n_new != nullptr ? n_new[b] : static_cast<int>(S);
-        n = n < 0 ? 0 : (n > S ? static_cast<int>(S) : n);
-        const int len = kv4_length(lens, b, max_pages << c.log2_page);
-        const int pos = len - n + i;
-        const bool mine = r < rows && i < n;
-        int page = -1;
-        if (mine) {
-            if (pos >= 0)
-                page = kv4_page(c, table, b, max_pages, pos);
-            else if (t == 0)
-                kv4_report();
+    constexpr int kStep = 256 / TPR;  // rows of a block at a time
+    bool bad = false;
+    // whole warps stay in the loop together
+    for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * (U * kStep); r0 < rows; r0 += static_cast<int64_t>(gridDim.x) * (U * kStep)) {
+        int64_t row[U], in[U];
+        int pos[U], head[U];
+        int64_t seq[U];
+        bool mine[U];
+        uint4 uk[U], uv[U];
+        float w[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            in[u] = r0 + u * kStep + threadIdx.x / TPR;
+            mine[u] = in[u] < rows;
+            const int64_t rr = mine[u] ? in[u] : 0;
+            int64_t at, h;
+            const int64_t bh = row_div(rr, S, rows, &at);
+            seq[u] = row_div(bh, c.heads, rows, &h);
+            head[u] = static_cast<int>(h);
+            int n = n_new != nullptr ? n_new[seq[u]] : static_cast<int>(S);
+            n = n < 0 ? 0 : (n > S ? static_cast<int>(S) : n);
+            mine[u] = mine[u] && at < n;
+            uk[u] = uv[u] = make_uint4(0, 0, 0, 0);
+            if (mine[u]) {
+                uk[u] = k_new[rr * TPR + t];
+                uv[u] = v_new[rr * TPR + t];
+            }
+            w[u] = mine[u] && t == 0 && w_new != nullptr ? w_new[rr] : 0.f;
+            pos[u] = static_cast<int>(at) - n;
         }
-        float xk[8], xv[8];
-        float mk = 0.f, mv = 0.f;
-        if (page >= 0) {
-            mk = unpack8(k_new[rr * TPR + t], xk);
-            mv = unpack8(v_new[rr * TPR + t], xv);
+        if (!__any_sync(0xffffffffu, mine[0] || mine[1])) continue;  // (past the tokens of a short sequence)
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            // (a thread without a row looks up position 0's page, and drops it)
+            const int len = kv4_length(lens, seq[u], max_pages << c.log2_page);
+            pos[u] += len;
+            bool valid;
+            const int page = kv4_page_quiet(c, table, seq[u], max_pages, max(0, mine[u] ? pos[u] : 0), &valid);
+            valid = valid && pos[u] >= 0;
+            bad |= mine[u] && !valid;
+            row[u] = mine[u] && valid ? kv4_row(c, page, head[u], pos[u]) : -1;
         }
 #pragma unroll
-        for (int o = 1; o < TPR; o <<= 1) {
-            if (o < 4) mk = max_nan(mk, __shfl_xor_sync(0xffffffffu, mk, o));
-            mv = max_nan(mv, __shfl_xor_sync(0xffffffffu, mv, o));
-        }
-        if (page < 0) continue;
-        const int64_t row = kv4_row(c, page, h, pos);
-        const uint32_t bk = kv4_scale_byte(mk), bv = kv4_scale_byte(mv);
-        reinterpret_cast<uint32_t *>(c.k)[row * TPR + t] = kv4_codes(xk, bk);
-        reinterpret_cast<uint32_t *>(c.v)[row * TPR + t] = kv4_codes(xv, bv);
-        if ((t & 3) == 0) c.k_scale[row * (D / 32) + (t >> 2)] = static_cast<uint8_t>(bk);
-        if (t == 0) {
-            c.v_scale[row] = static_cast<uint8_t>(bv);
-            if (c.weights != nullptr) c.weights[row] = w_new != nullptr ? w_new[rr] : 0.f;
+        for (int u = 0; u < U; ++u) {
+            float xk[8], xv[8];
+            uint32_t mk = unpack8(uk[u], xk), mv = unpack8(uv[u], xv);
+#pragma unroll
+            for (int o = 1; o < TPR; o <<= 1) {
+                if (o < 4) mk = max_u16x2(mk, __shfl_xor_sync(0xffffffffu, mk, o));
+                mv = max_u16x2(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+            }
+            if (row[u] < 0) continue;
+            const uint32_t bk = kv4_scale_byte(mk & 0xFFFFu), bv = kv4_scale_byte(mv & 0xFFFFu);
+            reinterpret_cast<uint32_t *>(c.k)[row[u] * TPR + t] = kv4_codes(xk, bk);
+            reinterpret_cast<uint32_t *>(c.v)[row[u] * TPR + t] = kv4_codes(xv, bv);
+            if ((t & 3) == 0) c.k_scale[row[u] * (D / 32) + (t >> 2)] = static_cast<uint8_t>(bk);
+            if (t == 0) {
+                c.v_scale[row[u]] = static_cast<uint8_t>(bv);
+                if (c.weights != nullptr) c.weights[row[u]] = w[u];
+            }
         }
     }
+    if (bad) kv4_report();
 }
 
 // ----------------------------------------------------------------------- read
@@ -140,10 +185,10 @@ fa_kv4_read_kernel(Kv4Cache c, const int32_t *__restrict__ first, const int32_t 
     const int t = threadIdx.x % TPR;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * (256 / TPR);
     for (int64_t r = static_cast<int64_t>(blockIdx.x) * (256 / TPR) + threadIdx.x / TPR; r < rows; r += stride) {
-        const int64_t bh = r / T;
-        const int64_t b = bh / c.heads;
-        const int h = static_cast<int>(bh - b * c.heads);
-        const int64_t pos = (r - bh * T) + (first != nullptr ? first[b] : 0);
+        int64_t at, head;
+        const int64_t bh = row_div(r, T, rows, &at), b = row_div(bh, c.heads, rows, &head);
+        const int h = static_cast<int>(head);
+        const int64_t pos = at + (first != nullptr ? first[b] : 0);
         uint4 k = make_uint4(0, 0, 0, 0), v = k;
         if (pos >= 0 && pos < kv4_length(lens, b, max_pages << c.log2_page)) {
             const int page = kv4_page(c, table, b, max_pages, static_cast<int>(pos));
@@ -171,18 +216,120 @@ __device__ __forceinline__ uint32_t weight_key(float w)
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Which tokens of one (sequence, key head) stay.  The candidates are the tokens
-// before the protected last ones; `need` of them stay.  The need-th largest key is
-// found bit by bit from the top: a bit is set where at least `need` candidates reach
-// the value with it.  Above it all stay, at it the lowest positions.
+// The `need` (1 .. cand - 1) candidates with the largest keys, ties to the lowest position, to out[0 .. need) in order.
+// Thread t has the keys of positions i 1024 + t (those past 1024 KPT are read again each time).  The need-th largest
+// key is found 11 bits at a time from the top: a histogram of the digit over the keys that share the digits so far,
+// and the digit at which its sums from above reach what is still needed.  Above the key all stay, at it the first
+// `ties`.  (Bit by bit, with the keys counted against 32 bounds, 15360 candidates took 30 us; with digits of 8 bits 22 us:
+// the first is nearly the exponent, and a warp's additions meet on few counters.)
+constexpr int kBins = 2048;
+struct SelectShared {
+    uint32_t counts[kBins];  // the histogram, then the places
+    int warp_sum[32];
+    int digit, rest;
+};
+
+template <int KPT, bool MORE, typename KeyAt>
+__device__ __forceinline__ void select_top(KeyAt key_at, int cand, int need, int32_t *out, SelectShared &sh)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint32_t (&counts)[kBins] = sh.counts;
+    uint32_t key[KPT];
+#pragma unroll
+    for (int i = 0; i < KPT; ++i) key[i] = key_at(min(i * kSelThreads + tid, cand - 1));
+    uint32_t at = 0, mask = 0;
+    int ties = need;
+    for (int turn = 0; turn < 3; ++turn) {
+        const int shift = turn == 0 ? 21 : turn == 1 ? 10 : 0;
+        const uint32_t bins = turn == 2 ? 1024u : 2048u;
+        counts[tid] = 0;
+        counts[tid + 1024] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < KPT; ++i)
+            if (i * kSelThreads + tid < cand && (key[i] & mask) == at) atomicAdd(&counts[(key[i] >> shift) & (bins - 1u)], 1u);
+        for (int j = KPT * kSelThreads + tid; MORE && j < cand; j += kSelThreads) {
+            const uint32_t k = key_at(j);
+            if ((k & mask) == at) atomicAdd(&counts[(k >> shift) & (bins - 1u)], 1u);
+        }
+        __syncthreads();
+        // thread t: digits 2047 - 2t and 2046 - 2t, and the sum from the top down to them
+        const int c0 = static_cast<int>(counts[2047 - 2 * tid]), c1 = static_cast<int>(counts[2046 - 2 * tid]);
+        int sum = c0 + c1;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += y;
+        }
+        if (lane == 31) sh.warp_sum[warp] = sum;
+        __syncthreads();
+        sum += __reduce_add_sync(0xffffffffu, lane < warp ? sh.warp_sum[lane] : 0);
+        const int before0 = sum - c0 - c1, before1 = sum - c1;
+        if (sum >= ties && before0 < ties) {
+            const bool first = before1 >= ties;
+            sh.digit = first ? 2047 - 2 * tid : 2046 - 2 * tid;
+            sh.rest = ties - (first ? before0 : before1);
+        }
+        __syncthreads();
+        at |= static_cast<uint32_t>(sh.digit) << shift;
+        mask |= (bins - 1u) << shift;
+        ties = sh.rest;
+    }
+    __syncthreads();
+    // positions in order, in rounds of up to 1024 KPT: how many above and at the bound each warp has in each block of 1024,
+    // their prefix sums (16 bits each), and each thread's place
+    int gt0 = 0, eq0 = 0;
+    const uint32_t below = (1u << lane) - 1u;
+    for (int j0 = 0; j0 < cand; j0 += KPT * kSelThreads) {
+        uint32_t bg[KPT], be[KPT];
+#pragma unroll
+        for (int i = 0; i < KPT; ++i) {
+            const int j = j0 + i * kSelThreads + tid;
+            if (MORE && j0 > 0) key[i] = j < cand ? key_at(j) : 0u;
+            bg[i] = __ballot_sync(0xffffffffu, j < cand && key[i] > at);
+            be[i] = __ballot_sync(0xffffffffu, j < cand && key[i] == at);
+            if (lane == 0) counts[i * 32 + warp] = __popc(bg[i]) | (__popc(be[i]) << 16);
+        }
+        __syncthreads();
+        const uint32_t own = tid < KPT * 32 ? counts[tid] : 0u;
+        uint32_t sum = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += y;
+        }
+        if (lane == 31) sh.warp_sum[warp] = static_cast<int>(sum);
+        __syncthreads();
+        uint32_t before = 0, all = 0;
+        for (int i = 0; i < KPT; ++i) {  // (the first KPT warps hold the counts)
+            const uint32_t n = static_cast<uint32_t>(sh.warp_sum[i]);
+            if (i < warp) before += n;
+            all += n;
+        }
+        if (tid < KPT * 32) counts[tid] = before + sum - own;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < KPT; ++i) {
+            const int j = j0 + i * kSelThreads + tid;
+            const uint32_t n = counts[i * 32 + warp];
+            const int gt = gt0 + static_cast<int>(n & 0xFFFFu) + __popc(bg[i] & below);
+            const int eq = eq0 + static_cast<int>(n >> 16) + __popc(be[i] & below);
+            if (((bg[i] >> lane) & 1u) || (((be[i] >> lane) & 1u) && eq < ties)) out[gt + (eq < ties ? eq : ties)] = j;
+        }
+        gt0 += all & 0xFFFFu;
+        eq0 += all >> 16;
+        __syncthreads();  // before the next round's counts
+    }
+}
+
+// Which tokens of one (sequence, key head) stay: a block each.
 __global__ void __launch_bounds__(kSelThreads)
 fa_kv4_select_kernel(Kv4Cache c, const int32_t *__restrict__ lens, const int32_t *__restrict__ table,
                      int64_t max_pages, int keep, int recent, int32_t *__restrict__ kept,
                      int32_t *__restrict__ new_lens)
 {
-    __shared__ int warp_sum[2][32];
-    __shared__ int warp_gt[32], warp_eq[32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __shared__ SelectShared sh;
+    const int tid = threadIdx.x;
     const int64_t bh = blockIdx.x, b = bh / c.heads;
     const int h = static_cast<int>(bh - b * c.heads);
     const int len = kv4_length(lens, b, max_pages << c.log2_page);
@@ -198,91 +345,90 @@ fa_kv4_select_kernel(Kv4Cache c, const int32_t *__restrict__ lens, const int32_t
     }
     for (int i = tid; i < len - cand; i += kSelThreads) out[need + i] = cand + i;
     if (need == 0) return;
-
-    auto key_at = [&](int j) -> uint32_t {
-        const int page = kv4_page(c, table, b, max_pages, j);
-        return page < 0 ? 0u : weight_key(c.weights[kv4_row(c, page, h, j)]);
+    bool bad = false;
+    auto key_at = [&](int j) -> uint32_t {  // (no branch: a thread's loads go out together)
+        bool valid;
+        const int page = kv4_page_quiet(c, table, b, max_pages, j, &valid);
+        const float w = c.weights[kv4_row(c, page, h, j)];
+        bad |= !valid;
+        return valid ? weight_key(w) : 0u;
     };
-    uint32_t at = 0;
-    for (int bit = 31, turn = 0; bit >= 0; --bit, turn ^= 1) {
-        const uint32_t v = at | (1u << bit);
-        int n = 0;
-        for (int j = tid; j < cand; j += kSelThreads) n += key_at(j) >= v;
-        n = __reduce_add_sync(0xffffffffu, n);
-        if (lane == 0) warp_sum[turn][warp] = n;
-        __syncthreads();
-        if (__reduce_add_sync(0xffffffffu, warp_sum[turn][lane]) >= need) at = v;
-    }
-    // how many lie above it
-    int n = 0;
-    for (int j = tid; j < cand; j += kSelThreads) n += key_at(j) > at;
-    n = __reduce_add_sync(0xffffffffu, n);
-    __syncthreads();
-    if (lane == 0) warp_sum[0][warp] = n;
-    __syncthreads();
-    const int ties = need - __reduce_add_sync(0xffffffffu, warp_sum[0][lane]);
-    // positions in order, a block of 1024 at a time
-    int gt0 = 0, eq0 = 0;
-    for (int j0 = 0; j0 < cand; j0 += kSelThreads) {
-        const int j = j0 + tid;
-        const uint32_t key = j < cand ? key_at(j) : 0u;
-        const bool gt = j < cand && key > at, eq = j < cand && key == at;
-        const uint32_t bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
-        __syncthreads();
-        if (lane == 0) {
-            warp_gt[warp] = __popc(bg);
-            warp_eq[warp] = __popc(be);
-        }
-        __syncthreads();
-        const int wg = warp_gt[lane], we = warp_eq[lane];
-        const uint32_t below = (1u << lane) - 1u;
-        const int gt_before = gt0 + __reduce_add_sync(0xffffffffu, lane < warp ? wg : 0) + __popc(bg & below);
-        const int eq_before = eq0 + __reduce_add_sync(0xffffffffu, lane < warp ? we : 0) + __popc(be & below);
-        if (gt || (eq && eq_before < ties)) out[gt_before + (eq_before < ties ? eq_before : ties)] = j;
-        gt0 += __reduce_add_sync(0xffffffffu, wg);
-        eq0 += __reduce_add_sync(0xffffffffu, we);
-    }
+    if (cand <= 4 * kSelThreads)
+        select_top<4, false>(key_at, cand, need, out, sh);
+    else if (cand <= 16 * kSelThreads)
+        select_top<16, false>(key_at, cand, need, out, sh);
+    else
+        select_top<16, true>(key_at, cand, need, out, sh);
+    if (bad) kv4_report();
 }
 
 // The kept rows to their new pages: D / 16 threads a row (half for K, half for V),
-// 16 bytes each.
+// 16 bytes each.  Memory-bound; a row waits for its position, then the pages, then the row,
+// so a thread has two rows under way.
 template <int D>
 __global__ void __launch_bounds__(256)
 fa_kv4_move_kernel(Kv4Cache from, Kv4Cache to, const int32_t *__restrict__ table, int64_t max_pages,
                    const int32_t *__restrict__ to_table, int64_t to_max_pages, const int32_t *__restrict__ kept,
                    int64_t rows, int keep)
 {
-    constexpr int TPR = D / 16, HALF = TPR / 2;
-    const int t = threadIdx.x % TPR;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * (256 / TPR);
-    for (int64_t r = static_cast<int64_t>(blockIdx.x) * (256 / TPR) + threadIdx.x / TPR; r < rows; r += stride) {
-        const int src = kept[r];
-        if (src < 0) continue;
-        const int64_t bh = r / keep, b = bh / from.heads;
-        const int h = static_cast<int>(bh - b * from.heads), dst = static_cast<int>(r - bh * keep);
-        const int ps = kv4_page(from, table, b, max_pages, src), pd = kv4_page(to, to_table, b, to_max_pages, dst);
-        if (ps < 0 || pd < 0) continue;
-        const int64_t rs = kv4_row(from, ps, h, src), rd = kv4_row(to, pd, h, dst);
-        const int i = t % HALF;
-        const uint4 x = reinterpret_cast<const uint4 *>(t < HALF ? from.k : from.v)[rs * HALF + i];
-        reinterpret_cast<uint4 *>(t < HALF ? to.k : to.v)[rd * HALF + i] = x;
-        if (t == 0) {
-            if (D == 128)
-                reinterpret_cast<uint32_t *>(to.k_scale)[rd] = reinterpret_cast<const uint32_t *>(from.k_scale)[rs];
-            else
-                reinterpret_cast<uint16_t *>(to.k_scale)[rd] = reinterpret_cast<const uint16_t *>(from.k_scale)[rs];
-        } else if (t == 1) {
-            to.v_scale[rd] = from.v_scale[rs];
-        } else if (t == 2) {
-            to.weights[rd] = from.weights[rs];
+    constexpr int TPR = D / 16, HALF = TPR / 2, U = 2;
+    const int t = threadIdx.x % TPR, i = t % HALF;
+    constexpr int kStep = 256 / TPR;  // rows of a block at a time
+    bool bad = false;
+    for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * (U * kStep) + threadIdx.x / TPR; r0 < rows;
+         r0 += static_cast<int64_t>(gridDim.x) * (U * kStep)) {
+        int src[U];
+        int64_t rs[U], rd[U];
+        uint4 x[U];
+        uint32_t y[U];
+        bool go[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) src[u] = r0 + u * kStep < rows ? kept[r0 + u * kStep] : -1;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            int64_t dst, h;
+            const int64_t bh = row_div(min(r0 + u * kStep, rows - 1), keep, rows, &dst), b = row_div(bh, from.heads, rows, &h);
+            bool vs, vd;
+            const int ps = kv4_page_quiet(from, table, b, max_pages, max(src[u], 0), &vs);
+            const int pd = kv4_page_quiet(to, to_table, b, to_max_pages, static_cast<int>(dst), &vd);
+            rs[u] = kv4_row(from, ps, static_cast<int>(h), max(src[u], 0));
+            rd[u] = kv4_row(to, pd, static_cast<int>(h), static_cast<int>(dst));
+            go[u] = src[u] >= 0 && vs && vd;
+            bad |= src[u] >= 0 && !go[u];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            x[u] = reinterpret_cast<const uint4 *>(t < HALF ? from.k : from.v)[rs[u] * HALF + i];
+            // the row's small parts, one a thread: K's scales, V's scale, the weight
+            y[u] = 0;
+            if (t == 0)
+                y[u] = D == 128 ? reinterpret_cast<const uint32_t *>(from.k_scale)[rs[u]]
+                                : reinterpret_cast<const uint16_t *>(from.k_scale)[rs[u]];
+            if (t == 1) y[u] = from.v_scale[rs[u]];
+            if (t == 2) y[u] = reinterpret_cast<const uint32_t *>(from.weights)[rs[u]];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (!go[u]) continue;
+            reinterpret_cast<uint4 *>(t < HALF ? to.k : to.v)[rd[u] * HALF + i] = x[u];
+            if (t == 0) {
+                if (D == 128)
+                    reinterpret_cast<uint32_t *>(to.k_scale)[rd[u]] = y[u];
+                else
+                    reinterpret_cast<uint16_t *>(to.k_scale)[rd[u]] = static_cast<uint16_t>(y[u]);
+            }
+            if (t == 1) to.v_scale[rd[u]] = static_cast<uint8_t>(y[u]);
+            if (t == 2) reinterpret_cast<uint32_t *>(to.weights)[rd[u]] = y[u];
         }
     }
+    if (bad) kv4_report();
 }
 
-// Blocks of 256 threads for `rows` rows of `per` threads, at most 16 blocks an SM in one wave.
-unsigned row_grid(int64_t rows, int per, int sm_count)
+// Blocks of 256 threads for `rows` rows of `per` threads, `turns` rows a thread; at most `waves` x 8 blocks an SM (then
+// a block takes several turns).
+unsigned row_grid(int64_t rows, int per, int turns, int sm_count, int waves = 2)
 {
-    const int64_t want = (rows + 256 / per - 1) / (256 / per), cap = static_cast<int64_t>(sm_count) * 16;
+    const int64_t step = 256 / per * turns, want = (rows + step - 1) / step, cap = static_cast<int64_t>(sm_count) * 8 * waves;
     return static_cast<unsigned>(want < cap ? want : cap);
 }
 
@@ -294,7 +440,7 @@ cudaError_t fa_launch_kv4_append(const Kv4Cache &c, const void *k_new, const voi
 {
     const int64_t rows = B * c.heads * S;
     auto *kern = c.d == 128 ? fa_kv4_append_kernel<128> : fa_kv4_append_kernel<64>;
-    kern<<<row_grid(rows, c.d / 8, sm_count), 256, 0, stream>>>(c, static_cast<const uint4 *>(k_new),
+    kern<<<row_grid(rows, c.d / 8, 2, sm_count, 64), 256, 0, stream>>>(c, static_cast<const uint4 *>(k_new),
                                                                 static_cast<const uint4 *>(v_new), w_new, n_new, lens,
                                                                 table, rows, S, max_pages);
     return cudaGetLastError();
@@ -306,7 +452,7 @@ cudaError_t fa_launch_kv4_read(const Kv4Cache &c, const int32_t *first, const in
 {
     const int64_t rows = B * c.heads * T;
     auto *kern = c.d == 128 ? fa_kv4_read_kernel<128> : fa_kv4_read_kernel<64>;
-    kern<<<row_grid(rows, c.d / 8, sm_count), 256, 0, stream>>>(c, first, lens, table, rows, T, max_pages,
+    kern<<<row_grid(rows, c.d / 8, 1, sm_count), 256, 0, stream>>>(c, first, lens, table, rows, T, max_pages,
                                                                 static_cast<uint4 *>(k_out),
                                                                 static_cast<uint4 *>(v_out));
     return cudaGetLastError();
@@ -321,7 +467,7 @@ cudaError_t fa_launch_kv4_evict(const Kv4EvictProblem &p, cudaStream_t stream)
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     auto *kern = p.from.d == 128 ? fa_kv4_move_kernel<128> : fa_kv4_move_kernel<64>;
-    kern<<<row_grid(rows, p.from.d / 16, p.sm_count), 256, 0, stream>>>(p.from, p.to, p.table, p.max_pages, p.to_table,
+    kern<<<row_grid(rows, p.from.d / 16, 2, p.sm_count, 64), 256, 0, stream>>>(p.from, p.to, p.table, p.max_pages, p.to_table,
                                                                         p.to_max_pages, p.kept, rows,
                                                                         static_cast<int>(p.keep));
     return cudaGetLastError();

@@ -249,9 +249,10 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         return b < a.B ? static_cast<int64_t>(item_units(a, tiles_of(kv4_length(a.lens, b, cap), TK))) * items : 0;
     };
     int64_t total = 0;
+    const int64_t units0 = units_of(tid);  // (most batches have no more sequences than this)
     {
-        int64_t n = 0;
-        for (int b = tid; b < a.B; b += kDecThreads) n += units_of(b);
+        int64_t n = units0;
+        for (int b = tid + kDecThreads; b < a.B; b += kDecThreads) n += units_of(b);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
         if (lane == 0) scan[warp] = n;
@@ -265,7 +266,7 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     int64_t base = 0;
     for (int b0 = 0; b0 < a.B && base <= u0; b0 += kDecThreads) {
         const int b = b0 + tid;
-        const int64_t mine = units_of(b);
+        const int64_t mine = b0 == 0 ? units0 : units_of(b);
         int64_t x = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
