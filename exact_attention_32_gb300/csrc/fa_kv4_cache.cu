@@ -80,10 +80,10 @@ __device__ __forceinline__ int64_t row_div(int64_t n, int64_t d, int64_t rows, i
     return q;
 }
 
-// D / 8 threads a row, eight channels each: one 16-byte load of K and of V, the
-// maxima over 4 threads (a K block) and over the row (V) by shuffles, four bytes of
-// codes out.  Memory-bound: 4 d bytes in and d + d/32 + 1 out a row; a thread has two rows
-// under way, and asks for their values before it knows their pages.
+// D / 16 threads a row, 16 channels of K and of V each: the maxima over 2 threads (a K
+// block) and over the row (V) by shuffles, eight bytes of codes out of each.  4 d bytes in and d + d/32 + 1 out a row;
+// with eight channels a thread the work of finding a row's place, done by all of its threads, bound it (44 us in
+// place of XXX for 8 x 8 heads of up to 4096 tokens).  The values are asked for before the row's page is known.
 template <int D>
 __global__ void __launch_bounds__(256)
 fa_kv4_append_kernel(Kv4Cache c, const uint4 *__restrict__ k_new, const uint4 *__restrict__ v_new,
@@ -91,68 +91,49 @@ fa_kv4_append_kernel(Kv4Cache c, const uint4 *__restrict__ k_new, const uint4 *_
                      const int32_t *__restrict__ lens, const int32_t *__restrict__ table, int64_t rows, int64_t S,
                      int64_t max_pages)
 {
-    constexpr int TPR = D / 8, U = 2;
+    constexpr int TPR = D / 16, kStep = 256 / TPR;  // rows of a block at a time
     const int t = threadIdx.x % TPR;
-    constexpr int kStep = 256 / TPR;  // rows of a block at a time
     bool bad = false;
     // whole warps stay in the loop together
-    for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * (U * kStep); r0 < rows; r0 += static_cast<int64_t>(gridDim.x) * (U * kStep)) {
-        int64_t row[U], in[U];
-        int pos[U], head[U];
-        int64_t seq[U];
-        bool mine[U];
-        uint4 uk[U], uv[U];
-        float w[U];
+    for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kStep; r0 < rows; r0 += static_cast<int64_t>(gridDim.x) * kStep) {
+        const int64_t r = r0 + threadIdx.x / TPR, rr = r < rows ? r : 0;
+        int64_t at, h;
+        const int64_t bh = row_div(rr, S, rows, &at), b = row_div(bh, c.heads, rows, &h);
+        int n = n_new != nullptr ? n_new[b] : static_cast<int>(S);
+        n = n < 0 ? 0 : (n > S ? static_cast<int>(S) : n);
+        const bool mine = r < rows && at < n;
+        if (!__any_sync(0xffffffffu, mine)) continue;  // (past the tokens of a short sequence)
+        uint4 uk[2], uv[2];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            in[u] = r0 + u * kStep + threadIdx.x / TPR;
-            mine[u] = in[u] < rows;
-            const int64_t rr = mine[u] ? in[u] : 0;
-            int64_t at, h;
-            const int64_t bh = row_div(rr, S, rows, &at);
-            seq[u] = row_div(bh, c.heads, rows, &h);
-            head[u] = static_cast<int>(h);
-            int n = n_new != nullptr ? n_new[seq[u]] : static_cast<int>(S);
-            n = n < 0 ? 0 : (n > S ? static_cast<int>(S) : n);
-            mine[u] = mine[u] && at < n;
-            uk[u] = uv[u] = make_uint4(0, 0, 0, 0);
-            if (mine[u]) {
-                uk[u] = k_new[rr * TPR + t];
-                uv[u] = v_new[rr * TPR + t];
+        for (int i = 0; i < 2; ++i) {
+            uk[i] = uv[i] = make_uint4(0, 0, 0, 0);
+            if (mine) {
+                uk[i] = k_new[(rr * TPR + t) * 2 + i];
+                uv[i] = v_new[(rr * TPR + t) * 2 + i];
             }
-            w[u] = mine[u] && t == 0 && w_new != nullptr ? w_new[rr] : 0.f;
-            pos[u] = static_cast<int>(at) - n;
         }
-        if (!__any_sync(0xffffffffu, mine[0] || mine[1])) continue;  // (past the tokens of a short sequence)
+        const float w = mine && t == 0 && w_new != nullptr ? w_new[rr] : 0.f;
+        // (a thread without a row looks up position 0's page, and drops it)
+        const int pos = static_cast<int>(at) - n + kv4_length(lens, b, max_pages << c.log2_page);
+        bool valid;
+        const int page = kv4_page_quiet(c, table, b, max_pages, max(0, mine ? pos : 0), &valid);
+        valid = valid && pos >= 0;
+        bad |= mine && !valid;
+        float xk[2][8], xv[2][8];
+        uint32_t mk = max_u16x2(unpack8(uk[0], xk[0]), unpack8(uk[1], xk[1]));
+        uint32_t mv = max_u16x2(unpack8(uv[0], xv[0]), unpack8(uv[1], xv[1]));
+        mk = max_u16x2(mk, __shfl_xor_sync(0xffffffffu, mk, 1));
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            // (a thread without a row looks up position 0's page, and drops it)
-            const int len = kv4_length(lens, seq[u], max_pages << c.log2_page);
-            pos[u] += len;
-            bool valid;
-            const int page = kv4_page_quiet(c, table, seq[u], max_pages, max(0, mine[u] ? pos[u] : 0), &valid);
-            valid = valid && pos[u] >= 0;
-            bad |= mine[u] && !valid;
-            row[u] = mine[u] && valid ? kv4_row(c, page, head[u], pos[u]) : -1;
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            float xk[8], xv[8];
-            uint32_t mk = unpack8(uk[u], xk), mv = unpack8(uv[u], xv);
-#pragma unroll
-            for (int o = 1; o < TPR; o <<= 1) {
-                if (o < 4) mk = max_u16x2(mk, __shfl_xor_sync(0xffffffffu, mk, o));
-                mv = max_u16x2(mv, __shfl_xor_sync(0xffffffffu, mv, o));
-            }
-            if (row[u] < 0) continue;
-            const uint32_t bk = kv4_scale_byte(mk & 0xFFFFu), bv = kv4_scale_byte(mv & 0xFFFFu);
-            reinterpret_cast<uint32_t *>(c.k)[row[u] * TPR + t] = kv4_codes(xk, bk);
-            reinterpret_cast<uint32_t *>(c.v)[row[u] * TPR + t] = kv4_codes(xv, bv);
-            if ((t & 3) == 0) c.k_scale[row[u] * (D / 32) + (t >> 2)] = static_cast<uint8_t>(bk);
-            if (t == 0) {
-                c.v_scale[row[u]] = static_cast<uint8_t>(bv);
-                if (c.weights != nullptr) c.weights[row[u]] = w[u];
-            }
+        for (int o = 1; o < TPR; o <<= 1) mv = max_u16x2(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+        if (!mine || !valid) continue;
+        const int64_t row = kv4_row(c, page, static_cast<int>(h), pos);
+        const uint32_t bk = kv4_scale_byte(mk & 0xFFFFu), bv = kv4_scale_byte(mv & 0xFFFFu);
+        reinterpret_cast<uint2 *>(c.k)[row * TPR + t] = make_uint2(kv4_codes(xk[0], bk), kv4_codes(xk[1], bk));
+        reinterpret_cast<uint2 *>(c.v)[row * TPR + t] = make_uint2(kv4_codes(xv[0], bv), kv4_codes(xv[1], bv));
+        if ((t & 1) == 0) c.k_scale[row * (D / 32) + (t >> 1)] = static_cast<uint8_t>(bk);
+        if (t == 0) {
+            c.v_scale[row] = static_cast<uint8_t>(bv);
+            if (c.weights != nullptr) c.weights[row] = w;
         }
     }
     if (bad) kv4_report();
@@ -440,7 +421,7 @@ cudaError_t fa_launch_kv4_append(const Kv4Cache &c, const void *k_new, const voi
 {
     const int64_t rows = B * c.heads * S;
     auto *kern = c.d == 128 ? fa_kv4_append_kernel<128> : fa_kv4_append_kernel<64>;
-    kern<<<row_grid(rows, c.d / 8, 2, sm_count, 64), 256, 0, stream>>>(c, static_cast<const uint4 *>(k_new),
+    kern<<<row_grid(rows, c.d / 16, 1, sm_count, 64), 256, 0, stream>>>(c, static_cast<const uint4 *>(k_new),
                                                                 static_cast<const uint4 *>(v_new), w_new, n_new, lens,
                                                                 table, rows, S, max_pages);
     return cudaGetLastError();
