@@ -40,6 +40,7 @@ namespace {
 constexpr int kKeyTile = 128, kKeys = 256, kQBlock = 128;
 constexpr int kKwThreads = 608, kKwLoad = 16, kKwMma = 17, kKwLse = 18;
 constexpr int kStages = 4;  // Q blocks in shared memory
+constexpr int kMaxRanks = 8;
 constexpr int kBufs = 3;    // accumulators in tensor memory
 
 __device__ int g_key_weights_status;
@@ -49,7 +50,8 @@ template <int D>
 struct KwCfg {
     static constexpr int kStageBytes = kQBlock * D * 2;
     static constexpr int kLse = kStages * kStageBytes;  // per stage: 128 floats
-    static constexpr int kBar = kLse + kStages * kQBlock * 4;
+    static constexpr int kSum = kLse + kStages * kQBlock * 4;  // rank 0: [rank][key] sums of its cluster
+    static constexpr int kBar = kSum + kMaxRanks * kKeys * 4;
     static constexpr int kNumBars = 4 * kStages + 4 * kBufs + 2;
     static constexpr int kSmemBytes = kBar + kNumBars * 8 + 16;
 };
@@ -66,9 +68,40 @@ struct KwArgs {
     const __nv_bfloat16 *k;
     const float *lse;
     float *weights;
-    int N, H, heads, n_kblocks, n_qblocks, first;
+    int N, H, heads, n_kblocks, n_qblocks, first, ranks;
     float scale_log2;
 };
+
+// A CTA's query blocks: every ranks-th of its key block's, heads one after the other.
+struct KwWalk {
+    int left, qb, qh;  // blocks still to come; block within the head; (b, head) slice
+    int qb0, n_qblocks, step;
+    __device__ __forceinline__ void next()
+    {
+        --left;
+        qb += step;
+        while (qb >= n_qblocks) {
+            qb -= n_qblocks - qb0;
+            ++qh;
+        }
+    }
+};
+
+// Address of another rank's shared memory in the cluster, a store to it, and the cluster's barrier.
+__device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank)
+{
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float x)
+{
+    asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(addr), "f"(x) : "memory");
+}
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
 
 template <int D, bool CAUSAL>
 __global__ void __launch_bounds__(kKwThreads, 1)
@@ -86,15 +119,25 @@ fa_key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const KwArgs a)
     auto BAR = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kBar + C::kNumBars * 8);
 
-    // key-block major: causal CTAs with many query blocks (small kb) start first
-    const int BHkv = static_cast<int>(gridDim.x) / a.n_kblocks;
-    const int kb = blockIdx.x / BHkv, bhk = blockIdx.x % BHkv;
+    // key-block major: causal CTAs with many query blocks (small kb) start first.  Where there are too few key blocks for
+    // the SMs, the `ranks` CTAs of a cluster share one: rank r takes the query blocks r, r + ranks, ...
+    const int BHkv = static_cast<int>(gridDim.x) / (a.n_kblocks * a.ranks);
+    const int unit = blockIdx.x / a.ranks, rank = blockIdx.x % a.ranks;
+    const int kb = unit / BHkv, bhk = unit % BHkv;
     const int k0 = kb * kKeys;
     const int G = a.H / a.heads;
     const int qh0 = bhk * G;  // (b, query head) slices of the group: b * H + hkv * G = bhk * G
     const int qb0 = max(CAUSAL ? k0 / kQBlock : 0, a.first / kQBlock);
     const int per_head = a.n_qblocks - qb0;
-    const int nq = per_head * G;  // query blocks, head by head
+    const int nq_all = per_head * G;
+    const int nq = nq_all > rank ? (nq_all - rank + a.ranks - 1) / a.ranks : 0;
+    KwWalk walk;
+    walk.left = nq;
+    walk.qb = qb0 + rank % per_head;
+    walk.qh = qh0 + rank / per_head;
+    walk.qb0 = qb0;
+    walk.n_qblocks = a.n_qblocks;
+    walk.step = a.ranks;
     const bool run = *reinterpret_cast<volatile int *>(&g_key_weights_status) == 0;
 
     if (tid == 0) {
@@ -118,6 +161,7 @@ fa_key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const KwArgs a)
     }
     tc_fence_before();
     __syncthreads();
+    if (a.ranks > 1) cluster_sync();  // rank 0's shared memory is there
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const uint32_t tS = tmem, tK = tmem + kBufs * 128;  // K tile w at columns tK + w * 64
@@ -128,17 +172,14 @@ fa_key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const KwArgs a)
         if (lane == 0) {
             prefetch_tmap(&tm_q);
             bool ok = true;
-            int issued = 0, qb = qb0, qh = qh0;
-            for (int i = 0; i < nq; ++i) {
+            int issued = 0;
+            for (int i = 0; i < nq; ++i, walk.next()) {
                 const int st = i % kStages;
                 if (i >= kStages && !(ok = mbar_wait(BAR(KW_Q_FREE + st), (i / kStages - 1) & 1, kWaitLimitNs))) break;
                 mbar_arrive_expect_tx(BAR(KW_Q_FULL + st), C::kStageBytes);
                 for (int c = 0; c < D / 64; ++c)
-                    tma_load_3d(sb + st * C::kStageBytes + c * 16384, &tm_q, BAR(KW_Q_FULL + st), c * 64, qb * kQBlock, qh);
-                if (++qb == a.n_qblocks) {
-                    qb = qb0;
-                    ++qh;
-                }
+                    tma_load_3d(sb + st * C::kStageBytes + c * 16384, &tm_q, BAR(KW_Q_FULL + st), c * 64, walk.qb * kQBlock,
+                                walk.qh);
                 ++issued;
             }
             if (!ok) kw_report(FA_ERR_TIMEOUT);
@@ -149,11 +190,11 @@ fa_key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const KwArgs a)
     } else if (warp == kKwLse) {
         // -LSE log2 e of each query; -inf (weight 0) for rows past N, before first, or without a key
         bool ok = true;
-        for (int i = 0; i < nq && ok; ++i) {
+        for (int i = 0; i < nq && ok; ++i, walk.next()) {
             const int st = i % kStages;
             if (i >= kStages && !(ok = mbar_wait_warp(BAR(KW_LSE_FREE + st), (i / kStages - 1) & 1, kWaitLimitNs))) break;
-            const int q0 = (qb0 + i % per_head) * kQBlock;
-            const float *src = a.lse + static_cast<int64_t>(qh0 + i / per_head) * a.N;
+            const int q0 = walk.qb * kQBlock;
+            const float *src = a.lse + static_cast<int64_t>(walk.qh) * a.N;
             float *dst = reinterpret_cast<float *>(smem + C::kLse) + st * kQBlock;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -231,11 +272,9 @@ fa_key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const KwArgs a)
         const float2 sc = make_float2(a.scale_log2, a.scale_log2);
         float total = 0.f;
         bool ok = true;
-        int qb = qb0;  // query block within the head
-        for (int i = 0; i < nq && ok; ++i) {
+        for (int i = 0; i < nq && ok; ++i, walk.next()) {
             const int st = i % kStages, n = 2 * i + w, buf = n % kBufs;
-            const int q0 = qb * kQBlock;
-            if (++qb == a.n_qblocks) qb = qb0;
+            const int q0 = walk.qb * kQBlock;
             if (!mbar_wait_warp(BAR(KW_LSE_FULL + st), (i / kStages) & 1, kWaitLimitNs) ||
                 !mbar_wait_warp(BAR(KW_S_FULL + kw_slot(n)), (n / 6) & 1, kWaitLimitNs)) {
                 ok = false;
@@ -294,14 +333,31 @@ fa_key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const KwArgs a)
         asm volatile("barrier.cta.sync 1, 512;\n" ::: "memory");
         if (half == 1) sum[w * kKeyTile + (warp & 3) * 32 + lane] = total;
         asm volatile("barrier.cta.sync 1, 512;\n" ::: "memory");
-        if (ok && half == 0 && key < a.N)
-            a.weights[static_cast<int64_t>(bhk) * a.N + key] = total + sum[w * kKeyTile + (warp & 3) * 32 + lane];
+        if (half == 0) {
+            const int i = w * kKeyTile + (warp & 3) * 32 + lane;
+            total += sum[i];
+            if (a.ranks == 1) {
+                if (ok && key < a.N) a.weights[static_cast<int64_t>(bhk) * a.N + key] = total;
+            } else {
+                st_cluster_f32(mapa(sb + C::kSum + (rank * kKeys + i) * 4, 0), ok ? total : NAN);
+            }
+        }
     }
     tc_fence_before();
     __syncthreads();
     if (warp == kKwMma) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
+    }
+    __syncwarp();
+    if (a.ranks > 1) {  // every thread of the cluster; the ranks' sums are added in their order
+        cluster_sync();
+        if (rank == 0 && run && tid < kKeys && k0 + tid < a.N) {
+            const float *sum = reinterpret_cast<const float *>(smem + C::kSum);
+            float total = 0.f;
+            for (int r = 0; r < a.ranks; ++r) total += sum[r * kKeys + tid];
+            a.weights[static_cast<int64_t>(bhk) * a.N + k0 + tid] = total;
+        }
     }
 }
 
@@ -324,11 +380,25 @@ cudaError_t launch_kw(const FaKeyWeightsProblem &p, cudaStream_t s)
     a.n_qblocks = static_cast<int>((p.N + kQBlock - 1) / kQBlock);
     a.first = static_cast<int>(p.first_query);
     a.scale_log2 = static_cast<float>(static_cast<double>(p.scale) * 1.4426950408889634);
-    const int64_t grid = p.B * p.Hkv * a.n_kblocks;
+    // ranks a key block: as many (1, 2, 4 or 8) as leave every rank two query blocks and the SMs not more than full
+    const int64_t units = p.B * p.Hkv * a.n_kblocks, blocks = (p.H / p.Hkv) * (a.n_qblocks - a.first / kQBlock);
+    a.ranks = 1;
+    while (a.ranks < kMaxRanks && units * a.ranks * 2 <= p.sm_count && blocks >= a.ranks * 4) a.ranks *= 2;
+    const int64_t grid = units * a.ranks;
     if (grid > 0x7fffffffLL || p.B * p.H > 0x7fffffffLL || (p.H / p.Hkv) * a.n_qblocks > 0x3fffffffLL)
         return cudaErrorInvalidConfiguration;
-    fa_key_weights_kernel<D, CAUSAL><<<static_cast<unsigned>(grid), kKwThreads, C::kSmemBytes, s>>>(mq, a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(kKwThreads);
+    cfg.dynamicSmemBytes = C::kSmemBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(a.ranks);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = a.ranks > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, fa_key_weights_kernel<D, CAUSAL>, mq, a);
 }
 
 }  // namespace

@@ -520,7 +520,9 @@ def _lse(q, k, scale, causal):
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("B,H,Hkv,N,first", [(1, 1, 1, 1, 0), (1, 1, 1, 2, 1), (2, 2, 1, 127, 0), (1, 4, 2, 128, 5), (1, 3, 3, 129, 128),
                                              (2, 8, 1, 255, 0), (1, 2, 2, 256, 200), (1, 7, 1, 257, 0), (1, 2, 1, 511, 300),
-                                             (1, 4, 2, 1000, 0), (1, 1, 1, 2049, 2048)])
+                                             (1, 4, 2, 1000, 0), (1, 1, 1, 2049, 2048),
+                                             # a few key blocks, shared by the CTAs of a cluster (2 to 8 of them)
+                                             (1, 8, 1, 300, 0), (2, 16, 2, 513, 0), (1, 32, 1, 900, 250), (1, 8, 2, 2500, 0)])
 def test_key_weights(B, H, Hkv, N, first, d, causal):
     rng = np.random.default_rng(N + H)
     q, k = bf16(rng.standard_normal((B, H, N, d))), bf16(rng.standard_normal((B, Hkv, N, d)))
