@@ -28,11 +28,10 @@
 // takes its share as segments of items.  A segment that is a whole item is finished in
 // place; the others leave (m, l, O) in the workspace, which a second kernel merges
 // (O = sum 2^(m_s - m) O_s / sum 2^(m_s - m) l_s).
-// Roles (192 threads, three CTAs an SM up to 8 rows, two up to 16): warps 0-3 the softmax, one thread a
-// TMEM lane; warp 4 loads, a lane a page (or the part of a page in the tile); warp 5
-// issues the products.  A softmax takes about 2000 cycles a tile, waits between its steps
-// for the most part, so an SM needs three of them at work to keep up with the 720
-// cycles that a tile's bytes take.  K and V have stages of their own, K's free as soon as S is there.
+// Roles: a softmax warpgroup per 8 rows (1, 2 or 4), one thread a TMEM lane; a warp that loads, a lane a page (or the
+// part of a page in the tile); a warp that issues the products.  A softmax takes about 2000 cycles a tile, waits between
+// its steps for the most part, so an SM needs several at work to keep up with the 720 cycles that a tile's bytes
+// take: three CTAs of 8 rows, two of 16, one of 32.  K and V have stages of their own, K's free as soon as S is there.
 // Copies of 8 bytes a lane by the load warps (cp.async) in the TMA's place took 3500 cycles
 // to issue a tile, two and a half times what all of the tile may take.
 #include <cuda.h>
@@ -48,8 +47,6 @@ using namespace sm100;
 
 namespace {
 
-constexpr int kDecThreads = 192, kDecWarps = 6;
-constexpr int kLoadWarp = 4, kMmaWarp = 5;
 constexpr int kMinShare = 4;   // units: a shorter share costs more in merging than it saves
 constexpr int kItemUnits = 3;  // what starting and ending an item costs, in tiles (4 to 6 us beside 1.4 us a tile)
 constexpr int kWholeTiles = 4;  // tables of so few tiles: items go to CTAs whole, and nothing is merged
@@ -89,6 +86,7 @@ struct DecodeArgs {
 template <int D, int RT>
 struct DecCfg {
     static constexpr int RP = 8 * RT;          // rows a CTA takes
+    static constexpr int kLoadWarp = 4 * RT, kMmaWarp = kLoadWarp + 1, kWarps = kLoadWarp + 2, kThreads = 32 * kWarps;
     static constexpr int N = 16 * RT;          // columns: per 8 rows, 8 high parts and 8 rests
     static constexpr int KPT = 128 / D;        // keys a thread (and a 128-byte row) holds
     static constexpr int TK = 128 * KPT;       // keys a tile
@@ -103,9 +101,10 @@ struct DecCfg {
     static constexpr int kPBytes = 128 * N * KPT;
     static constexpr int kScale = kP + kPBufs * kPBytes;         // with V's stage: K scales 512, V scales 256, page flags 64
     static constexpr int kScaleBytes = 512 + 256 + 64;
-    static constexpr int kFloat = kScale + kStages * kScaleBytes;  // mult, m, alpha [32]; red [4][32]; misc [32]
-    static constexpr int kWalk = kFloat + (3 * 32 + 4 * 32 + 32) * 4;  // the scan's sums, the share's start
-    static constexpr int kBar = kWalk + 128;
+    static constexpr int kFloat = kScale + kStages * kScaleBytes;
+    static constexpr int kGroupFloats = 3 * 8 + 4 * 8 + 8;  // mult, m, alpha [8]; red [4][8]; misc [8]
+    static constexpr int kWalk = kFloat + RT * kGroupFloats * 4;  // the share's start, the scan's sums
+    static constexpr int kBar = kWalk + 64 + 8 * kWarps;
     static constexpr int kNumBars = 4 * kStages + 7;
     static constexpr int kSmemBytes = kBar + kNumBars * 8 + 16;
     static constexpr int kSCols = 4 * N, kOCols = N * KPT;
@@ -174,15 +173,15 @@ __device__ __forceinline__ float2 e4m3x2_f32(uint32_t b)
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
-// Barrier of the softmax warps; with an OR over their threads.
-__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, 128;\n" ::: "memory"); }
-__device__ __forceinline__ bool softmax_or(bool x)
+// Barrier of a softmax warpgroup; with an OR over its threads.
+__device__ __forceinline__ void group_sync(int id) { asm volatile("barrier.cta.sync %0, 128;\n" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool group_or(int id, bool x)
 {
     uint32_t r;
     asm volatile(
-        "{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbarrier.cta.red.or.pred q, 1, 128, p;\nselp.u32 %0, 1, 0, q;\n}\n"
+        "{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbarrier.cta.red.or.pred q, %2, 128, p;\nselp.u32 %0, 1, 0, q;\n}\n"
         : "=r"(r)
-        : "r"(static_cast<uint32_t>(x))
+        : "r"(static_cast<uint32_t>(x)), "r"(id)
         : "memory");
     return r != 0;
 }
@@ -201,11 +200,12 @@ __device__ __forceinline__ uint32_t lo32(uint64_t x) { return static_cast<uint32
 __device__ __forceinline__ uint32_t hi32(uint64_t x) { return static_cast<uint32_t>(x >> 32); }
 
 template <int D, int RT, bool SCORES>
-__global__ void __launch_bounds__(kDecThreads, DecCfg<D, RT>::kPerSm)
+__global__ void __launch_bounds__(DecCfg<D, RT>::kThreads, DecCfg<D, RT>::kPerSm)
 fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const DecodeArgs a)
 {
     using C = DecCfg<D, RT>;
     constexpr int RP = C::RP, N = C::N, KPT = C::KPT, TK = C::TK, ST = C::kStages;
+    constexpr int kLoadWarp = C::kLoadWarp, kMmaWarp = C::kMmaWarp, kDecThreads = C::kThreads, kDecWarps = C::kWarps;
     constexpr int K_FULL = D_STAGES, K_FREE = K_FULL + ST, V_FULL = K_FREE + ST, V_FREE = V_FULL + ST;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sb = smem_u32(smem);
@@ -217,18 +217,16 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     const uint32_t bar0 = sb + C::kBar;
     auto BAR = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kBar + C::kNumBars * 8);
-    float *sm_mult = reinterpret_cast<float *>(smem + C::kFloat), *sm_m = sm_mult + 32, *sm_alpha = sm_m + 32;
-    float *sm_red = sm_alpha + 32, *sm_misc = sm_red + 4 * 32;
     const int64_t cap = a.max_pages << a.c.log2_page;
 
     if (tid == 0) {
         for (int s = 0; s < 4 * ST; ++s) mbar_init(BAR(D_STAGES + s), 1);
         mbar_init(BAR(D_S_FULL), 1);
-        mbar_init(BAR(D_S_FREE), 4);
-        mbar_init(BAR(D_P_READY), 4);
+        mbar_init(BAR(D_S_FREE), 4 * RT);
+        mbar_init(BAR(D_P_READY), 4 * RT);
         mbar_init(BAR(D_PV_DONE), 1);
         mbar_init(BAR(D_PV_DONE1), 1);
-        mbar_init(BAR(D_Q_READY), 4);
+        mbar_init(BAR(D_Q_READY), 4 * RT);
         mbar_init(BAR(D_DONE), 1);
         fence_mbar_init();
     }
@@ -240,10 +238,10 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     // the kernel behind this one may be set up meanwhile (it waits for this one's end before it reads)
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 
-    // the share of this CTA: units before each sequence by a scan over the lengths, 192 at a time
-    int64_t *scan = reinterpret_cast<int64_t *>(smem + C::kWalk);
-    Walk &start = *reinterpret_cast<Walk *>(smem + C::kWalk + 64);
-    static_assert(sizeof(Walk) <= 64, "fits behind the scan");
+    // the share of this CTA: units before each sequence by a scan over the lengths, a thread each at a time
+    Walk &start = *reinterpret_cast<Walk *>(smem + C::kWalk);
+    int64_t *scan = reinterpret_cast<int64_t *>(smem + C::kWalk + 64);
+    static_assert(sizeof(Walk) <= 64, "fits before the scan");
     const int items = a.c.heads * a.n_rc;
     auto units_of = [&](int b) -> int64_t {
         return b < a.B ? static_cast<int64_t>(item_units(a, tiles_of(kv4_length(a.lens, b, cap), TK))) * items : 0;
@@ -410,99 +408,101 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         __syncwarp();
         mbar_wait_warp(BAR(D_DONE), 0, ok ? kWaitLimitNs : kCleanupLimitNs);
     } else {
-        // ------------------------------------------------------------------- softmax
-        const uint32_t loff = static_cast<uint32_t>(warp * 32) << 16;
+        // ------------------------------------------------- softmax: warpgroup g has rows 8 g .. 8 g + 7
+        const int g = warp >> 2, wl = warp & 3, tl = tid & 127;  // tl: TMEM lane
+        const uint32_t loff = static_cast<uint32_t>(wl * 32) << 16;
+        float *sm_mult = reinterpret_cast<float *>(smem + C::kFloat) + g * C::kGroupFloats;
+        float *sm_m = sm_mult + 8, *sm_alpha = sm_m + 8, *sm_red = sm_alpha + 8, *sm_misc = sm_red + 4 * 8;
+        volatile float *sm_fail = sm_misc + 1;  // a warp's wait gave up: all of the group leave at the next barrier
+        auto sync = [&]() { group_sync(1 + g); };
         int n = 0;
         bool ok = true;
+        if (tl == 0) *sm_fail = 0.f;
         for (; w.left > 0 && ok; walk_next<TK>(w, a)) {
             if (w.t0 == w.t1) continue;
             const int h = w.it / a.n_rc, rc = w.it - h * a.n_rc;
             const int64_t bh = static_cast<int64_t>(w.b) * a.c.heads + h;
-            const int row0 = rc * RP, n_rows = min(RP, a.R - row0);
+            const int row0 = rc * RP + g * 8, n_rows = min(8, a.R - row0);  // (0 or less: this group has padding only)
             // Q: 8 channels a thread, D / 8 threads a row
-            {
-                constexpr int TPR = D / 8;
-                for (int r = tid / TPR; r < RP; r += 128 / TPR) {
-                    uint4 u = make_uint4(0, 0, 0, 0);
-                    const int ch = tid % TPR;
-                    if (r < n_rows) u = *reinterpret_cast<const uint4 *>(a.q + (bh * a.R + row0 + r) * D + ch * 8);
-                    const uint32_t x[4] = {u.x, u.y, u.z, u.w};
-                    float2 f[4];
-                    float amax = 0.f;
+            constexpr int TPR = D / 8;
+            if (tl < 8 * TPR) {
+                const int r = tl / TPR, ch = tl % TPR;
+                uint4 u = make_uint4(0, 0, 0, 0);
+                if (r < n_rows) u = *reinterpret_cast<const uint4 *>(a.q + (bh * a.R + row0 + r) * D + ch * 8);
+                const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+                float2 f[4];
+                float amax = 0.f;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        f[i] = make_float2(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xFFFF0000u));
-                        amax = fmaxf(amax, fmaxf(fabsf(f[i].x), fabsf(f[i].y)));
-                    }
-#pragma unroll
-                    for (int o = 1; o < TPR; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                    // exponent of the row's maximum, held where 2^(7 - e) and 2^(e - 7) are normal numbers
-                    int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
-                    e = amax == 0.f ? 7 : min(max(e, -100), 127);
-                    const float up = __uint_as_float(static_cast<uint32_t>(7 - e + 127) << 23);
-                    uint32_t hb[4], lb[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        f[i].x *= up;
-                        f[i].y *= up;
-                        hb[i] = e4m3x2(f[i]);
-                        const float2 g = e4m3x2_f32(hb[i]);
-                        lb[i] = e4m3x2(make_float2((f[i].x - g.x) * 16.f, (f[i].y - g.y) * 16.f));
-                    }
-                    // row r's high part in column (r / 8) * 16 + r % 8, its rest 8 columns on
-#pragma unroll
-                    for (int part = 0; part < 2; ++part) {
-                        const int col = (r >> 3) * 16 + (r & 7) + part * 8;
-                        const uint32_t *y = part ? lb : hb;
-                        *reinterpret_cast<uint2 *>(smem + C::kQ + col * 128 + (((ch >> 1) ^ (col & 7)) << 4) + (ch & 1) * 8) =
-                            make_uint2(y[0] | (y[1] << 16), y[2] | (y[3] << 16));
-                    }
-                    if (ch == 0) {
-                        sm_mult[r] = !(amax < INFINITY) ? NAN : a.scale_log2 * __uint_as_float(static_cast<uint32_t>(e - 7 + 127) << 23);
-                        sm_m[r] = -FLT_MAX;
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    f[i] = make_float2(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xFFFF0000u));
+                    amax = fmaxf(amax, fmaxf(fabsf(f[i].x), fabsf(f[i].y)));
                 }
-                // V's scale reference: P carries scale / reference * 256; two octaves above every scale so far
-                if (tid == 0) sm_misc[0] = 0x1p-16f;
-                fence_proxy_async_smem();
-                softmax_sync();
-                if (lane == 0) mbar_arrive(BAR(D_Q_READY));
-            }
-            float2 l[RP / 2];
 #pragma unroll
-            for (int i = 0; i < RP / 2; ++i) l[i] = make_float2(0.f, 0.f);
+                for (int o = 1; o < TPR; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                // exponent of the row's maximum, held where 2^(7 - e) and 2^(e - 7) are normal numbers
+                int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
+                e = amax == 0.f ? 7 : min(max(e, -100), 127);
+                const float up = __uint_as_float(static_cast<uint32_t>(7 - e + 127) << 23);
+                uint32_t hb[4], lb[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    f[i].x *= up;
+                    f[i].y *= up;
+                    hb[i] = e4m3x2(f[i]);
+                    const float2 v = e4m3x2_f32(hb[i]);
+                    lb[i] = e4m3x2(make_float2((f[i].x - v.x) * 16.f, (f[i].y - v.y) * 16.f));
+                }
+                // row r's high part in column g * 16 + r, its rest 8 columns on
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                    const int col = g * 16 + r + part * 8;
+                    const uint32_t *y = part ? lb : hb;
+                    *reinterpret_cast<uint2 *>(smem + C::kQ + col * 128 + (((ch >> 1) ^ (col & 7)) << 4) + (ch & 1) * 8) =
+                        make_uint2(y[0] | (y[1] << 16), y[2] | (y[3] << 16));
+                }
+                if (ch == 0) {
+                    sm_mult[r] = !(amax < INFINITY) ? NAN : a.scale_log2 * __uint_as_float(static_cast<uint32_t>(e - 7 + 127) << 23);
+                    sm_m[r] = -FLT_MAX;
+                }
+            }
+            // V's scale reference: P carries scale / reference * 256; two octaves above every scale so far
+            if (tl == 0) sm_misc[0] = 0x1p-16f;
+            fence_proxy_async_smem();
+            sync();
+            if (lane == 0) mbar_arrive(BAR(D_Q_READY));
+            float2 l[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) l[i] = make_float2(0.f, 0.f);
 
             for (int t = w.t0; t < w.t1; ++t, ++n) {
                 const int st = n % ST;
                 const uint8_t *scale = smem + C::kScale + st * C::kScaleBytes;
+                const int *flag = reinterpret_cast<const int *>(scale + 768);
                 const int key0 = t * TK;
-                if (!mbar_wait_warp(BAR(V_FULL + st), (n / ST) & 1, kWaitLimitNs) ||
-                    !mbar_wait_warp(BAR(D_S_FULL), n & 1, kWaitLimitNs)) {
-                    ok = false;
-                    break;
-                }
+                // (P's buffer has been read, too)
+                ok = mbar_wait_warp(BAR(V_FULL + st), (n / ST) & 1, kWaitLimitNs) &&
+                     mbar_wait_warp(BAR(D_S_FULL), n & 1, kWaitLimitNs) &&
+                     (n < C::kPBufs || mbar_wait_warp(pv_bar(n), pv_phase(n - C::kPBufs), kWaitLimitNs));
+                if (!ok) *sm_fail = 1.f;
                 tc_fence_after();
                 // log2 scores of this thread's keys
-                float2 x[KPT][RP / 2];
+                float2 x[KPT][4];
                 float ks[4], vs[KPT];
                 {
-                    const uint32_t b = *reinterpret_cast<const uint32_t *>(scale + tid * 4);
+                    const uint32_t b = *reinterpret_cast<const uint32_t *>(scale + tl * 4);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) ks[i] = kv4_scale((b >> (8 * i)) & 255u);
 #pragma unroll
-                    for (int k = 0; k < KPT; ++k) vs[k] = kv4_scale(scale[512 + tid * KPT + k]);
+                    for (int k = 0; k < KPT; ++k) vs[k] = kv4_scale(scale[512 + tl * KPT + k]);
                 }
-#pragma unroll
-                for (int rg = 0; rg < RT; ++rg) {
+                {
                     uint32_t s[4][16];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) tmem_ld16(tS + loff + i * N + rg * 16, s[i]);
+                    for (int i = 0; i < 4; ++i) tmem_ld16(tS + loff + i * N + g * 16, s[i]);
                     tmem_wait_ld();
-                    if (rg == RT - 1) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(BAR(D_S_FREE));
-                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(BAR(D_S_FREE));
 #pragma unroll
                     for (int k = 0; k < KPT; ++k)
 #pragma unroll
@@ -517,21 +517,20 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                                 hi = i == 0 ? mul2(f, sh) : fma2(f, sh, hi);
                                 lo = i == 0 ? mul2(f, sl) : fma2(f, sl, lo);
                             }
-                            const float2 m = *reinterpret_cast<const float2 *>(sm_mult + rg * 8 + 2 * j);
-                            x[k][rg * 4 + j] = mul2(fma2(lo, make_float2(0.0625f, 0.0625f), hi), m);
+                            const float2 m = *reinterpret_cast<const float2 *>(sm_mult + 2 * j);
+                            x[k][j] = mul2(fma2(lo, make_float2(0.0625f, 0.0625f), hi), m);
                         }
                 }
                 // keys that a row does not admit, or that no page holds, leave it; what lies there may be anything
-                const bool edge = key0 + TK > w.len - a.n_q + 1 ||
-                                  __any_sync(0xffffffffu, lane < C::NG && reinterpret_cast<const int *>(scale + 768)[lane < C::NG ? lane : 0] == 0);
+                const bool edge = key0 + TK > w.len - a.n_q + 1 || __any_sync(0xffffffffu, flag[lane % C::NG] == 0);
                 if (edge) {
 #pragma unroll
                     for (int k = 0; k < KPT; ++k) {
-                        const int j = tid * KPT + k, key = key0 + j;
-                        const bool gone = key >= w.len || reinterpret_cast<const int *>(scale + 768)[j >> 4] == 0;
+                        const int j = tl * KPT + k, key = key0 + j;
+                        const bool gone = key >= w.len || flag[j >> 4] == 0;
                         if (gone) vs[k] = 0.f;
 #pragma unroll
-                        for (int r = 0; r < RP; ++r) {
+                        for (int r = 0; r < 8; ++r) {
                             const int limit = w.len - a.n_q + 1 + (row0 + r) % a.n_q;
                             if (gone || key >= limit) (r & 1 ? x[k][r / 2].y : x[k][r / 2].x) = -INFINITY;
                         }
@@ -540,16 +539,16 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 if constexpr (SCORES) {
 #pragma unroll
                     for (int k = 0; k < KPT; ++k) {
-                        const int key = key0 + tid * KPT + k;
+                        const int key = key0 + tl * KPT + k;
                         if (key < w.len) {
                             float *s = a.scores + (bh * cap + key) * a.Rs + row0;
                             if (a.R <= 2) {
-                                s[0] = x[k][0].x;
-                                if (a.R == 2) s[1] = x[k][0].y;
+                                if (n_rows > 0) s[0] = x[k][0].x;
+                                if (n_rows > 1) s[1] = x[k][0].y;
                             } else {
 #pragma unroll
-                                for (int r = 0; r < RP / 4; ++r)
-                                    if (row0 + 4 * r < a.R)
+                                for (int r = 0; r < 2; ++r)
+                                    if (4 * r < n_rows)
                                         *reinterpret_cast<float4 *>(s + 4 * r) =
                                             make_float4(x[k][2 * r].x, x[k][2 * r].y, x[k][2 * r + 1].x, x[k][2 * r + 1].y);
                             }
@@ -562,63 +561,64 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
 #pragma unroll
                 for (int k = 0; k < KPT; ++k) grows |= vs[k] > vref;
 #pragma unroll
-                for (int r = 0; r < RP / 2; ++r) {
+                for (int r = 0; r < 4; ++r) {
                     const float2 m = *reinterpret_cast<const float2 *>(sm_m + 2 * r);
 #pragma unroll
                     for (int k = 0; k < KPT; ++k) grows |= x[k][r].x > m.x || x[k][r].y > m.y;
                 }
-                grows = softmax_or(grows);
-                // O is complete so far, where it will be rescaled; P's buffer has been read
-                if (grows && t > w.t0 && !mbar_wait_warp(pv_bar(n - 1), pv_phase(n - 1), kWaitLimitNs)) {
-                    ok = false;
-                    break;
-                }
-                if (n >= C::kPBufs && !mbar_wait_warp(pv_bar(n), pv_phase(n - C::kPBufs), kWaitLimitNs)) {
+                grows = group_or(1 + g, grows);
+                if (*sm_fail != 0.f) {
                     ok = false;
                     break;
                 }
                 if (grows) {
+                    // O is complete so far, where it will be rescaled
+                    if (t > w.t0 && !mbar_wait_warp(pv_bar(n - 1), pv_phase(n - 1), kWaitLimitNs)) *sm_fail = 1.f;
 #pragma unroll
-                    for (int r = 0; r < RP; ++r) {
+                    for (int r = 0; r < 8; ++r) {
                         float v = -FLT_MAX;
 #pragma unroll
                         for (int k = 0; k < KPT; ++k) v = fmaxf(v, r & 1 ? x[k][r / 2].y : x[k][r / 2].x);
                         v = warp_max(v);
-                        if (lane == 0) sm_red[warp * 32 + r] = v;
+                        if (lane == 0) sm_red[wl * 8 + r] = v;
                     }
                     {
                         float v = 0.f;
 #pragma unroll
                         for (int k = 0; k < KPT; ++k) v = fmaxf(v, vs[k]);
                         v = warp_max(v);
-                        if (lane == 0) sm_misc[4 + warp] = v;
+                        if (lane == 0) sm_misc[4 + wl] = v;
                     }
-                    softmax_sync();
+                    sync();
+                    if (*sm_fail != 0.f) {
+                        ok = false;
+                        break;
+                    }
                     const float vmax = fmaxf(fmaxf(sm_misc[4], sm_misc[5]), fmaxf(sm_misc[6], sm_misc[7]));
                     const float vnew = vmax > vref ? __uint_as_float((__float_as_uint(vmax) & 0x7F800000u) + (2u << 23)) : vref;
-                    if (tid < RP) {
-                        const float old = sm_m[tid];
-                        float v = fmaxf(fmaxf(sm_red[tid], sm_red[32 + tid]), fmaxf(sm_red[64 + tid], sm_red[96 + tid]));
+                    if (tl < 8) {
+                        const float old = sm_m[tl];
+                        float v = fmaxf(fmaxf(sm_red[tl], sm_red[8 + tl]), fmaxf(sm_red[16 + tl], sm_red[24 + tl]));
                         v = v > old ? v + kHeadroom : old;
-                        sm_m[tid] = v;
-                        sm_alpha[tid] = ex2(old - v);
+                        sm_m[tl] = v;
+                        sm_alpha[tl] = ex2(old - v);
                     }
-                    if (tid == 0) sm_misc[0] = vnew;
-                    softmax_sync();
+                    if (tl == 0) sm_misc[0] = vnew;
+                    sync();
 #pragma unroll
-                    for (int r = 0; r < RP / 2; ++r) l[r] = mul2(l[r], *reinterpret_cast<const float2 *>(sm_alpha + 2 * r));
+                    for (int r = 0; r < 4; ++r) l[r] = mul2(l[r], *reinterpret_cast<const float2 *>(sm_alpha + 2 * r));
                     if (t > w.t0) {
                         tc_fence_after();
                         const float vf = vref / vnew;
 #pragma unroll
-                        for (int c = 0; c < C::kOCols / 16; ++c) {
+                        for (int k = 0; k < KPT; ++k) {
                             uint32_t o[16];
-                            tmem_ld16(tO + loff + c * 16, o);
+                            tmem_ld16(tO + loff + k * N + g * 16, o);
                             tmem_wait_ld();
 #pragma unroll
                             for (int j = 0; j < 16; ++j)
-                                o[j] = __float_as_uint(__uint_as_float(o[j]) * (sm_alpha[(c % RT) * 8 + (j & 7)] * vf));
-                            tmem_st16(tO + loff + c * 16, o);
+                                o[j] = __float_as_uint(__uint_as_float(o[j]) * (sm_alpha[j & 7] * vf));
+                            tmem_st16(tO + loff + k * N + g * 16, o);
                         }
                         tmem_wait_st();
                     }
@@ -628,26 +628,23 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
 #pragma unroll
                 for (int k = 0; k < KPT; ++k) {
                     const float c1 = vs[k] * vc, c16 = c1 * 16.f;
+                    uint32_t hb[4], lb[4];
 #pragma unroll
-                    for (int rg = 0; rg < RT; ++rg) {
-                        uint32_t hb[4], lb[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float2 m = *reinterpret_cast<const float2 *>(sm_m + rg * 8 + 2 * j);
-                            const float2 xx = x[k][rg * 4 + j];
-                            const float2 p = make_float2(ex2(xx.x - m.x), ex2(xx.y - m.y));
-                            l[rg * 4 + j] = add2(l[rg * 4 + j], p);
-                            float2 y = mul2(p, make_float2(c1, c1)), y16 = mul2(p, make_float2(c16, c16));
-                            if (edge) {  // a value that a row does not admit stays out of it, a NaN too
-                                if (xx.x == -INFINITY) y.x = y16.x = 0.f;
-                                if (xx.y == -INFINITY) y.y = y16.y = 0.f;
-                            }
-                            hb[j] = e4m3x2(y);
-                            lb[j] = e4m3x2(fma2(e4m3x2_f32(hb[j]), make_float2(-16.f, -16.f), y16));
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 m = *reinterpret_cast<const float2 *>(sm_m + 2 * j);
+                        const float2 xx = x[k][j];
+                        const float2 p = make_float2(ex2(xx.x - m.x), ex2(xx.y - m.y));
+                        l[j] = add2(l[j], p);
+                        float2 y = mul2(p, make_float2(c1, c1)), y16 = mul2(p, make_float2(c16, c16));
+                        if (edge) {  // a value that a row does not admit stays out of it, a NaN too
+                            if (xx.x == -INFINITY) y.x = y16.x = 0.f;
+                            if (xx.y == -INFINITY) y.y = y16.y = 0.f;
                         }
-                        *reinterpret_cast<uint4 *>(smem + C::kP + pbuf(n) * C::kPBytes + (k * RT + rg) * 2048 + tid * 16) =
-                            make_uint4(hb[0] | (hb[1] << 16), hb[2] | (hb[3] << 16), lb[0] | (lb[1] << 16), lb[2] | (lb[3] << 16));
+                        hb[j] = e4m3x2(y);
+                        lb[j] = e4m3x2(fma2(e4m3x2_f32(hb[j]), make_float2(-16.f, -16.f), y16));
                     }
+                    *reinterpret_cast<uint4 *>(smem + C::kP + pbuf(n) * C::kPBytes + (k * RT + g) * 2048 + tl * 16) =
+                        make_uint4(hb[0] | (hb[1] << 16), hb[2] | (hb[3] << 16), lb[0] | (lb[1] << 16), lb[2] | (lb[3] << 16));
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
@@ -657,71 +654,70 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             if (!ok) break;
 
             // ---------------------------------------------------- end of the segment
-            if (!mbar_wait_warp(pv_bar(n - 1), pv_phase(n - 1), kWaitLimitNs)) {
-                ok = false;
-                break;
-            }
+            if (!mbar_wait_warp(pv_bar(n - 1), pv_phase(n - 1), kWaitLimitNs)) *sm_fail = 1.f;
             tc_fence_after();
 #pragma unroll
-            for (int r = 0; r < RP; ++r) {
+            for (int r = 0; r < 8; ++r) {
                 float v = r & 1 ? l[r / 2].y : l[r / 2].x;
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                if (lane == 0) sm_red[warp * 32 + r] = v;
+                if (lane == 0) sm_red[wl * 8 + r] = v;
             }
             // this lane's channel of every row: high part and a sixteenth of the rest, P's factor taken out
-            float y[RP];
+            float y[8];
             const float back = sm_misc[0] * 0.00390625f;
-            const int half = D == 64 ? warp >> 1 : 0;  // d = 64: lanes 64-127 hold the odd keys' part of channel lane - 64
-#pragma unroll
-            for (int rg = 0; rg < RT; ++rg) {
+            const int half = D == 64 ? wl >> 1 : 0;  // d = 64: lanes 64-127 hold the odd keys' part of channel lane - 64
+            {
                 uint32_t o[16];
-                tmem_ld16(tO + loff + half * N + rg * 16, o);
+                tmem_ld16(tO + loff + half * N + g * 16, o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    y[rg * 8 + j] = fmaf(__uint_as_float(o[8 + j]), 0.0625f, __uint_as_float(o[j])) * back;
+                for (int j = 0; j < 8; ++j) y[j] = fmaf(__uint_as_float(o[8 + j]), 0.0625f, __uint_as_float(o[j])) * back;
             }
             tc_fence_before();
-            float *sx = reinterpret_cast<float *>(smem + C::kP);  // (the products have read P)
+            float *sx = reinterpret_cast<float *>(smem + C::kP) + g * 8 * 64;  // (the products have read P)
             if (D == 64 && half == 1) {
 #pragma unroll
-                for (int r = 0; r < RP; ++r) sx[r * 64 + tid - 64] = y[r];
+                for (int r = 0; r < 8; ++r) sx[r * 64 + tl - 64] = y[r];
             }
-            softmax_sync();
+            sync();
+            if (*sm_fail != 0.f) {
+                ok = false;
+                break;
+            }
             if (D == 128 || half == 0) {
                 const bool whole = w.t0 == 0 && w.t1 == w.n_t;
                 const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (n == w.t1 - w.t0 ? 0 : 1);
                 if (tid == 0 && w.t0 == 0 && !whole) {
                     Split sp;
                     sp.row = bh * a.R + row0;
-                    sp.n_rows = n_rows;
+                    sp.n_rows = min(RP, a.R - row0);
                     sp.parts = 1 + static_cast<int>((w.n_t - w.t1 + share - 1) / share);
                     sp.slot = static_cast<int>(slot);
                     sp.pad = 0;
                     a.split[blockIdx.x] = sp;
                 }
 #pragma unroll
-                for (int r = 0; r < RP; ++r) {
+                for (int r = 0; r < 8; ++r) {
                     if (r >= n_rows) break;
                     float v = y[r];
-                    if (D == 64) v += sx[r * 64 + tid];
-                    const float ll = (sm_red[r] + sm_red[32 + r]) + (sm_red[64 + r] + sm_red[96 + r]);
+                    if (D == 64) v += sx[r * 64 + tl];
+                    const float ll = (sm_red[r] + sm_red[8 + r]) + (sm_red[16 + r] + sm_red[24 + r]);
                     const int64_t row = bh * a.R + row0 + r;
                     if (whole) {
                         const float inv = ll == 0.f ? 0.f : 1.f / ll;
-                        a.o[row * D + tid] = __float2bfloat16_rn(v * inv);
-                        if (tid == 0) {
+                        a.o[row * D + tl] = __float2bfloat16_rn(v * inv);
+                        if (tl == 0) {
                             a.lse[row] = ll == 0.f ? -INFINITY : (sm_m[r] + log2f(ll)) * kLn2;
                             if (SCORES) a.row_ml[row] = make_float2(ll == 0.f ? 0.f : sm_m[r], inv);
                         }
                     } else {
-                        a.part_o[(slot * RP + r) * D + tid] = v;
-                        if (tid == 0) a.part_ml[slot * RP + r] = make_float2(sm_m[r], ll);
+                        a.part_o[(slot * RP + g * 8 + r) * D + tl] = v;
+                        if (tl == 0) a.part_ml[slot * RP + g * 8 + r] = make_float2(sm_m[r], ll);
                     }
                 }
             }
-            softmax_sync();  // before the next segment's Q and state take the place of these
+            sync();  // before the next segment's Q and state take the place of these
         }
         if (!ok && lane == 0) kv4_timeout();
     }
@@ -742,7 +738,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
 fa_kv4_merge_kernel(const DecodeArgs a, int RP)
 {
     constexpr int PER = D / 32;
-    __shared__ float sm_l[kMergeWarps];
+    __shared__ float sm_l[kMergeWarps], sm_m[kMergeWarps];
     __shared__ float sm_x[kMergeWarps][D];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
@@ -757,36 +753,60 @@ fa_kv4_merge_kernel(const DecodeArgs a, int RP)
         float m = -FLT_MAX, l = 0.f, x[PER];
 #pragma unroll
         for (int i = 0; i < PER; ++i) x[i] = 0.f;
-        if (live) {
-            for (int i = lane; i < sp.parts; i += 32) m = fmaxf(m, a.part_ml[slot(i) * RP + rr].x);
-            m = warp_max(m);
-#pragma unroll 8
-            for (int i = w; i < sp.parts; i += per_row) {
-                const int64_t s = slot(i) * RP + rr;
-                const float2 v = a.part_ml[s];
-                const float *po = a.part_o + s * D + lane * PER;
-                float y[PER];
-                if constexpr (PER == 4)
-                    *reinterpret_cast<float4 *>(y) = *reinterpret_cast<const float4 *>(po);
-                else
-                    *reinterpret_cast<float2 *>(y) = *reinterpret_cast<const float2 *>(po);
-                const float f = ex2(v.x - m);
-                l = fmaf(f, v.y, l);
+        constexpr int kBatch = 8;  // parts whose loads go out together, against a maximum of their own
+        for (int i0 = live ? w : sp.parts; i0 < sp.parts; i0 += kBatch * per_row) {
+            float2 v[kBatch];
+            float y[kBatch][PER], mb = m;
 #pragma unroll
-                for (int j = 0; j < PER; ++j) x[j] = fmaf(f, y[j], x[j]);
+            for (int u = 0; u < kBatch; ++u) {
+                const int i = i0 + u * per_row;
+                const int64_t s = slot(min(i, sp.parts - 1)) * RP + rr;
+                const float *po = a.part_o + s * D + lane * PER;
+                v[u] = a.part_ml[s];
+                if constexpr (PER == 4)
+                    *reinterpret_cast<float4 *>(y[u]) = *reinterpret_cast<const float4 *>(po);
+                else
+                    *reinterpret_cast<float2 *>(y[u]) = *reinterpret_cast<const float2 *>(po);
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) mb = fmaxf(mb, v[u].x);
+            const float back = ex2(m - mb);
+            m = mb;
+            l *= back;
+#pragma unroll
+            for (int j = 0; j < PER; ++j) x[j] *= back;
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                if (i0 + u * per_row >= sp.parts) break;
+                const float f = ex2(v[u].x - m);
+                l = fmaf(f, v[u].y, l);
+#pragma unroll
+                for (int j = 0; j < PER; ++j) x[j] = fmaf(f, y[u][j], x[j]);
             }
         }
         if (per_row > 1) {
-            if (lane == 0) sm_l[warp] = l;
+            if (lane == 0) {
+                sm_l[warp] = l;
+                sm_m[warp] = m;
+            }
 #pragma unroll
             for (int j = 0; j < PER; ++j) sm_x[warp][lane * PER + j] = x[j];
             __syncthreads();  // (with several warps a row all rows go in one turn)
-            if (live && w == 0)
-                for (int i = 1; i < per_row; ++i) {
-                    l += sm_l[warp + i];
+            if (live && w == 0) {
+                float mt = m;
+                for (int i = 1; i < per_row; ++i) mt = fmaxf(mt, sm_m[warp + i]);
+                const float back = ex2(m - mt);
+                l *= back;
 #pragma unroll
-                    for (int j = 0; j < PER; ++j) x[j] += sm_x[warp + i][lane * PER + j];
+                for (int j = 0; j < PER; ++j) x[j] *= back;
+                m = mt;
+                for (int i = 1; i < per_row; ++i) {
+                    const float f = ex2(sm_m[warp + i] - m);
+                    l = fmaf(f, sm_l[warp + i], l);
+#pragma unroll
+                    for (int j = 0; j < PER; ++j) x[j] = fmaf(f, sm_x[warp + i][lane * PER + j], x[j]);
                 }
+            }
         }
         if (!live || w != 0) continue;
         const int64_t row = sp.row + rr;
@@ -801,7 +821,7 @@ fa_kv4_merge_kernel(const DecodeArgs a, int RP)
     }
 }
 
-// weights[key] += sum over the rows of exp2(score - m) / l: one thread a key.
+// weights[key] += sum over the rows of exp2(score - m) / l: a thread has two keys under way.
 __global__ void __launch_bounds__(256)
 fa_kv4_weights_kernel(const DecodeArgs a, int blocks)
 {
@@ -811,23 +831,42 @@ fa_kv4_weights_kernel(const DecodeArgs a, int blocks)
     const int len = kv4_length(a.lens, b, cap);
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     const float2 *ml = a.row_ml + bh * a.R;
-    for (int key = blockIdx.x % blocks * 256 + threadIdx.x; key < len; key += blocks * 256) {
-        const int page = kv4_page(a.c, a.table, b, a.max_pages, key);
-        if (page < 0) continue;
-        const float *s = a.scores + (bh * cap + key) * a.Rs;
-        float w = 0.f;
+    for (int key0 = blockIdx.x % blocks * 512 + threadIdx.x; key0 < len; key0 += blocks * 512) {
+        const int n = key0 + 256 < len ? 2 : 1;
+        float w[2] = {0.f, 0.f}, old[2];
+        int64_t row[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int key = u < n ? key0 + 256 * u : key0;
+            bool valid;
+            const int page = kv4_page_quiet(a.c, a.table, b, a.max_pages, key, &valid);
+            row[u] = kv4_row(a.c, page, h, key);
+            old[u] = a.c.weights[row[u]];
+            if (!valid || u >= n) row[u] = -1;  // (a bad page is reported by the kernel before)
+        }
+        const float *s0 = a.scores + (bh * cap + key0) * a.Rs, *s1 = n == 2 ? s0 + 256 * a.Rs : s0;
         if (a.R <= 2) {
-            for (int r = 0; r < a.R; ++r) w = fmaf(ex2(s[r] - ml[r].x), ml[r].y, w);
+            for (int r = 0; r < a.R; ++r) {
+                w[0] = fmaf(ex2(s0[r] - ml[r].x), ml[r].y, w[0]);
+                w[1] = fmaf(ex2(s1[r] - ml[r].x), ml[r].y, w[1]);
+            }
         } else {
+#pragma unroll 3
             for (int r = 0; r < a.R; r += 4) {
-                const float4 v = *reinterpret_cast<const float4 *>(s + r);
-                w = fmaf(ex2(v.x - ml[r].x), ml[r].y, w);
-                if (r + 1 < a.R) w = fmaf(ex2(v.y - ml[r + 1].x), ml[r + 1].y, w);
-                if (r + 2 < a.R) w = fmaf(ex2(v.z - ml[r + 2].x), ml[r + 2].y, w);
-                if (r + 3 < a.R) w = fmaf(ex2(v.w - ml[r + 3].x), ml[r + 3].y, w);
+                const float4 v0 = *reinterpret_cast<const float4 *>(s0 + r), v1 = *reinterpret_cast<const float4 *>(s1 + r);
+                const float y0[4] = {v0.x, v0.y, v0.z, v0.w}, y1[4] = {v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (r + i >= a.R) break;
+                    const float2 p = ml[r + i];
+                    w[0] = fmaf(ex2(y0[i] - p.x), p.y, w[0]);
+                    w[1] = fmaf(ex2(y1[i] - p.x), p.y, w[1]);
+                }
             }
         }
-        a.c.weights[kv4_row(a.c, page, h, key)] += w;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            if (row[u] >= 0) a.c.weights[row[u]] = old[u] + w[u];
     }
 }
 
@@ -912,7 +951,7 @@ cudaError_t launch(const DecodeArgs &a, int ctas, cudaStream_t s)
     if (!make_code_map(&mk, a.c, a.c.k) || !make_code_map(&mv, a.c, a.c.v)) return cudaErrorInvalidValue;
     cudaError_t e = set_max_dynamic_smem<fa_kv4_decode_kernel<D, RT, SCORES>>(C::kSmemBytes);
     if (e != cudaSuccess) return e;
-    fa_kv4_decode_kernel<D, RT, SCORES><<<static_cast<unsigned>(ctas), kDecThreads, C::kSmemBytes, s>>>(mk, mv, a);
+    fa_kv4_decode_kernel<D, RT, SCORES><<<static_cast<unsigned>(ctas), C::kThreads, C::kSmemBytes, s>>>(mk, mv, a);
     return cudaGetLastError();
 }
 
@@ -990,7 +1029,7 @@ cudaError_t fa_launch_kv4_decode(const Kv4DecodeProblem &p, void *workspace, cud
         if (e != cudaSuccess) return e;
     }
     if (p.accumulate) {
-        int64_t blocks = (cap + 255) / 256;
+        int64_t blocks = (cap + 511) / 512;
         if (blocks > 512) blocks = 512;
         if (blocks * p.B * heads > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
         e = launch_behind(fa_kv4_weights_kernel, blocks * p.B * heads, 256, stream, a, static_cast<int>(blocks));
