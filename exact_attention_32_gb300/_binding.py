@@ -1,4 +1,5 @@
-"""ctypes binding of libfa.so: argument marshalling only.
+"""ctypes binding of libfa.so: argument marshalling only (the tensor-level calls
+of the 4-bit cache go through the extension _marshal.c, which does the same faster).
 
 Every function of include/fa.h is exposed under the same name; ``forward`` is
 the tensor-level convenience call.  Torch supplies device memory and the
@@ -8,7 +9,6 @@ no fallback: if libfa.so is missing or fails to load, every call raises.
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 import os
 import threading
@@ -598,49 +598,33 @@ def kv4_cache(n_pages: int, n_kv_heads: int, page_size: int, d: int, device="cud
                     zeros(*shape, dtype=torch.float32) if weights else None)
 
 
-def _kv4_struct(c: KV4Cache) -> KV4CacheStruct:
-    """The library's view of a cache, its arrays checked.  (A decode step is short: these checks and the calls below
-    avoid what costs a microsecond in torch, as making a device object or entering a device context.)"""
-    k, v, ks, vs, w = c
-    shape = k.shape
-    if len(shape) != 4:
-        raise ValueError("cache.k must be [n_pages, Hkv, page_size, d/2]")
-    n, heads, page, half = shape
-    if v.shape != shape or ks.shape != (n, heads, page, half // 16) or vs.shape != (n, heads, page):
-        raise ValueError("cache arrays must be k, v [n_pages, Hkv, page_size, d/2], k_scale [..., d/32], "
-                         "v_scale [n_pages, Hkv, page_size]")
-    dev = k.get_device()
-    if dev < 0:
-        raise ValueError("a 4-bit cache lives on a CUDA device")
-    for t in (k, v, ks, vs):
-        if t.dtype is not torch.uint8 or t.get_device() != dev or not t.is_contiguous():
-            raise ValueError("k, v, k_scale, v_scale of a cache must be contiguous uint8 tensors on one CUDA device")
-    if w is None:
-        pw = None
-    else:
-        if (w.shape != (n, heads, page) or w.dtype is not torch.float32 or w.get_device() != dev
-                or not w.is_contiguous()):
-            raise ValueError("cache.weights must be a contiguous fp32 tensor [n_pages, Hkv, page_size]")
-        pw = w.data_ptr()
-    return KV4CacheStruct(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), pw, n, heads, page, 2 * half)
+_marshal = None
 
 
-def _kv4_index(name: str, t: torch.Tensor, dims: int, B: int, dev: int) -> int:
-    """Pointer of an int32 index tensor ([B], or [B, columns])."""
-    if (t.dtype is not torch.int32 or t.dim() != dims or t.get_device() != dev or not t.is_contiguous()
-            or t.size(0) != B):
-        raise ValueError(f"{name} must be a contiguous int32 tensor {'[B]' if dims == 1 else '[B, pages]'} on the "
-                         "cache's device")
-    return t.data_ptr()
+def _calls():
+    """The extension behind the calls below (once: it gets the library's addresses).  Raises if it has not been built."""
+    global _marshal
+    if _marshal is None:
+        L = lib()
+        try:
+            from . import _marshal as m
+        except ImportError as e:
+            raise RuntimeError("_marshal is missing: build it with exact_attention_32_gb300.build.build()") from e
+        at = [ctypes.cast(f, ctypes.c_void_p).value for f in (
+            L.fa_kv4_append, L.fa_kv4_read, L.fa_fwd_kv4, L.fa_fwd_kv4_workspace_bytes, L.fa_kv4_evict, L.fa_key_weights)]
+        m.setup(torch.uint8, torch.bfloat16, torch.float32, torch.int32, torch.empty, torch._C._cuda_getCurrentRawStream,
+                torch._C._cuda_getDevice, FAError, tuple(at))
+        _marshal = m
+    return _marshal
 
 
-def _on_device(dev: int, stream, call, *args) -> int:
-    """call(*args, stream handle) with device ``dev`` current."""
-    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    if torch._C._cuda_getDevice() == dev:
-        return call(*args, s)
-    with torch.cuda.device(dev):
-        return call(*args, s)
+def _elsewhere(call, device, stream, *args):
+    """call(*args) on ``stream`` (outputs and workspace allocated for it), or with ``device`` current."""
+    with torch.cuda.device(device) if stream is None else torch.cuda.stream(stream):
+        r = call(*args)
+    if r is NotImplemented:
+        raise ValueError("stream must belong to the tensors' device")
+    return r
 
 
 def kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, lens: torch.Tensor, page_table: torch.Tensor,
@@ -652,31 +636,12 @@ def kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, lens: torch.Te
     the append; of its S rows sequence b gains the first n_new[b] (all where
     n_new is None), as its last positions.  page_table: int32 [B, pages].
     weights: fp32 [B, Hkv, S], what the new tokens' weights start from (0
-    where None)."""
-    c = _kv4_struct(cache)
-    dev = cache.k.get_device()
-    shape = k.shape
-    if len(shape) != 4 or v.shape != shape or shape[1] != c.Hkv or shape[3] != c.d:
-        raise ValueError("k and v must be [B, Hkv, S, d] with the cache's Hkv and d")
-    for t in (k, v):
-        if t.dtype is not torch.bfloat16 or t.get_device() != dev or not t.is_contiguous():
-            raise ValueError("k and v must be contiguous bf16 tensors on the cache's device")
-    B, heads, S, _ = shape
-    if weights is None:
-        pw = None
-    else:
-        if (weights.shape != (B, heads, S) or weights.dtype is not torch.float32 or weights.get_device() != dev
-                or not weights.is_contiguous()):
-            raise ValueError("weights must be a contiguous fp32 tensor [B, Hkv, S]")
-        if cache.weights is None:
-            raise ValueError("the cache holds no weights")
-        pw = weights.data_ptr()
-    st = _on_device(dev, stream, fa_kv4_append, c, k.data_ptr(), v.data_ptr(), pw,
-                    None if n_new is None else _kv4_index("n_new", n_new, 1, B, dev),
-                    _kv4_index("lens", lens, 1, B, dev), _kv4_index("page_table", page_table, 2, B, dev), B, S,
-                    page_table.size(1))
-    if st != FA_OK:
-        raise FAError(st, "fa_kv4_append")
+    where None).  Enqueued on ``stream`` (default: torch's current stream), as
+    the calls below."""
+    args = (cache, k, v, lens, page_table, n_new, weights)
+    call = (_marshal or _calls()).kv4_append
+    if stream is not None or call(*args) is NotImplemented:
+        _elsewhere(call, k.device, stream, *args)
 
 
 def kv4_read(cache: KV4Cache, lens: torch.Tensor, page_table: torch.Tensor, count: int,
@@ -684,22 +649,12 @@ def kv4_read(cache: KV4Cache, lens: torch.Tensor, page_table: torch.Tensor, coun
     """(K, V) bf16 [B, Hkv, count, d]: positions first[b] .. first[b] + count - 1
     (from 0 where first is None) of each sequence by ``fa_kv4_read``; rows at or
     past lens[b] are zero."""
-    c = _kv4_struct(cache)
-    dev = cache.k.get_device()
-    B = lens.shape[0] if lens.dim() == 1 else -1
-    pl, pt = _kv4_index("lens", lens, 1, B, dev), _kv4_index("page_table", page_table, 2, B, dev)
-    pf = None if first is None else _kv4_index("first", first, 1, B, dev)
-    if count < 1:
-        raise ValueError("count must be at least 1")
-    k = torch.empty((B, c.Hkv, count, c.d), dtype=torch.bfloat16, device=cache.k.device)
-    v = torch.empty_like(k)
-    st = _on_device(dev, stream, fa_kv4_read, c, pf, pl, pt, B, page_table.size(1), count, k.data_ptr(), v.data_ptr())
-    if st != FA_OK:
-        raise FAError(st, "fa_kv4_read")
-    return k, v
-
-
-_kv4_workspace = functools.lru_cache(maxsize=1024)(fa_fwd_kv4_workspace_bytes)  # a function of the sizes alone
+    call = (_marshal or _calls()).kv4_read
+    if stream is None:
+        r = call(cache, lens, page_table, count, first)
+        if r is not NotImplemented:
+            return r
+    return _elsewhere(call, lens.device, stream, cache, lens, page_table, count, first)
 
 
 def forward_kv4(q: torch.Tensor, cache: KV4Cache, lens: torch.Tensor, page_table: torch.Tensor,
@@ -711,35 +666,13 @@ def forward_kv4(q: torch.Tensor, cache: KV4Cache, lens: torch.Tensor, page_table
     q: contiguous bf16 [B, H, n_q, d], H a multiple of the cache's key heads;
     lens: int32 [B]; page_table: int32 [B, pages].  ``accumulate`` adds each
     key's attention weight over these rows to cache.weights.  The workspace
-    (uint8 CUDA tensor) is allocated with torch when not given."""
-    c = _kv4_struct(cache)
-    dev = cache.k.get_device()
-    shape = q.shape
-    if len(shape) != 4 or shape[3] != c.d or shape[1] % c.Hkv != 0:
-        raise ValueError("q must be [B, H, n_q, d] with the cache's d and H a multiple of its key heads")
-    if q.dtype is not torch.bfloat16 or q.get_device() != dev or not q.is_contiguous():
-        raise ValueError("q must be a contiguous bf16 tensor on the cache's device")
-    if accumulate and cache.weights is None:
-        raise ValueError("the cache holds no weights")
-    B, H, n_q, d = shape
-    pl, pt = _kv4_index("lens", lens, 1, B, dev), _kv4_index("page_table", page_table, 2, B, dev)
-    cols = page_table.size(1)
-    need = _kv4_workspace(B, H, c.Hkv, n_q, d, cols * c.page_size, bool(accumulate))
-    if need < 0:
-        raise FAError(1 if d in (64, 128) else 2, "fa_fwd_kv4_workspace_bytes")
-    o = torch.empty_like(q)
-    lse = torch.empty((B, H, n_q), dtype=torch.float32, device=q.device)
-    if workspace is None:
-        workspace, size = torch.empty(need, dtype=torch.uint8, device=q.device), need
-    else:
-        if workspace.get_device() != dev or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor on the cache's device")
-        size = workspace.numel() * workspace.element_size()
-    st = _on_device(dev, stream, fa_fwd_kv4, q.data_ptr(), c, pl, pt, o.data_ptr(), lse.data_ptr(), B, H, n_q, cols,
-                    default_scale(d) if scale is None else scale, bool(accumulate), workspace.data_ptr(), size)
-    if st != FA_OK:
-        raise FAError(st, "fa_fwd_kv4")
-    return o, lse
+    (uint8 CUDA tensor of ``fa_fwd_kv4_workspace_bytes`` bytes) is allocated with torch when not given."""
+    call = (_marshal or _calls()).forward_kv4
+    if stream is None:
+        r = call(q, cache, lens, page_table, scale, accumulate, workspace)
+        if r is not NotImplemented:
+            return r
+    return _elsewhere(call, q.device, stream, q, cache, lens, page_table, scale, accumulate, workspace)
 
 
 def kv4_evict(cache: KV4Cache, lens: torch.Tensor, page_table: torch.Tensor, to: KV4Cache, to_table: torch.Tensor,
@@ -750,26 +683,12 @@ def kv4_evict(cache: KV4Cache, lens: torch.Tensor, page_table: torch.Tensor, to:
     ``to_table`` (int32 [B, pages]) in ``to`` (another cache of the same layout, or the
     same one: the pages must then be free).  kept holds their positions, -1
     past the end."""
-    c = _kv4_struct(cache)
-    t = c if to is cache else _kv4_struct(to)
-    dev = cache.k.get_device()
-    if to.k.get_device() != dev or (t.Hkv, t.page_size, t.d) != (c.Hkv, c.page_size, c.d):
-        raise ValueError("both caches must have the same key heads, page size, d and device")
-    if cache.weights is None or to.weights is None:
-        raise ValueError("eviction needs the weights of both caches")
-    B = lens.shape[0] if lens.dim() == 1 else -1
-    pl, pt = _kv4_index("lens", lens, 1, B, dev), _kv4_index("page_table", page_table, 2, B, dev)
-    ptt = _kv4_index("to_table", to_table, 2, B, dev)
-    to_cols = to_table.size(1)
-    if keep < 1 or not 0 <= recent <= keep or keep > to_cols * c.page_size:
-        raise ValueError("need 1 <= keep <= the tokens of to_table's pages, and 0 <= recent <= keep")
-    kept = torch.empty((B, c.Hkv, keep), dtype=torch.int32, device=lens.device)
-    new_lens = torch.empty_like(lens)
-    st = _on_device(dev, stream, fa_kv4_evict, c, pl, pt, page_table.size(1), t, ptt, to_cols, B, keep, recent,
-                    kept.data_ptr(), new_lens.data_ptr())
-    if st != FA_OK:
-        raise FAError(st, "fa_kv4_evict")
-    return kept, new_lens
+    call = (_marshal or _calls()).kv4_evict
+    if stream is None:
+        r = call(cache, lens, page_table, to, to_table, keep, recent)
+        if r is not NotImplemented:
+            return r
+    return _elsewhere(call, lens.device, stream, cache, lens, page_table, to, to_table, keep, recent)
 
 
 def key_weights(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor, scale: float | None = None, causal: bool = False,
@@ -778,23 +697,9 @@ def key_weights(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor, scale: floa
     its group's heads and the queries from ``first_query`` on, by
     ``fa_key_weights``.  q: contiguous bf16 [B, H, N, d]; k: [B, Hkv, N, d], H a
     multiple of Hkv; lse: fp32 [B, H, N], ``forward``'s."""
-    if q.dim() != 4 or k.dim() != 4:
-        raise ValueError("q must be [B, H, N, d] and k [B, Hkv, N, d]")
-    B, H, N, d = q.shape
-    heads = k.size(1)
-    if k.shape != (B, heads, N, d) or heads < 1 or H % heads != 0:
-        raise ValueError("k must be [B, Hkv, N, d] with H a multiple of Hkv")
-    dev = q.get_device()
-    for t in (q, k):
-        if t.dtype is not torch.bfloat16 or dev < 0 or t.get_device() != dev or not t.is_contiguous():
-            raise ValueError("q and k must be contiguous bf16 CUDA tensors on one device")
-    if lse.shape != (B, H, N) or lse.dtype is not torch.float32 or lse.get_device() != dev or not lse.is_contiguous():
-        raise ValueError("lse must be a contiguous fp32 tensor [B, H, N]")
-    if not 0 <= first_query < N:
-        raise ValueError("first_query must lie in [0, N)")
-    w = torch.empty((B, heads, N), dtype=torch.float32, device=q.device)
-    st = _on_device(dev, stream, fa_key_weights, q.data_ptr(), k.data_ptr(), lse.data_ptr(), w.data_ptr(), B, H, heads,
-                    N, d, default_scale(d) if scale is None else scale, bool(causal), first_query)
-    if st != FA_OK:
-        raise FAError(st, "fa_key_weights")
-    return w
+    call = (_marshal or _calls()).key_weights
+    if stream is None:
+        r = call(q, k, lse, scale, causal, first_query)
+        if r is not NotImplemented:
+            return r
+    return _elsewhere(call, q.device, stream, q, k, lse, scale, causal, first_query)

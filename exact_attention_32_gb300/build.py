@@ -1,7 +1,8 @@
 """Build libfa.so (the CUDA library behind include/fa.h) in-tree for sm_103a.
 
 Each .cu under csrc/ is compiled by nvcc in parallel, then linked into
-``exact_attention_32_gb300/libfa.so`` (static CUDA runtime).  ptxas resource
+``exact_attention_32_gb300/libfa.so`` (static CUDA runtime); the binding's
+extension ``_marshal.so`` is compiled by gcc.  ptxas resource
 reports (registers, spills, shared memory) are kept next to the objects in
 ``_build/<name>.ptxas.txt``.
 """
@@ -12,6 +13,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfa.so")
+MARSHAL_SRC = os.path.join(PKG, "_marshal.c")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
@@ -53,8 +57,24 @@ def _compile(src: str) -> str:
     return obj
 
 
+def build_marshal(force: bool = False) -> str:
+    """Compile the binding's extension unless it is newer than its sources."""
+    deps = [MARSHAL_SRC, os.path.join(INCLUDE, "fa.h"), __file__]
+    if (not force and os.path.exists(MARSHAL)
+            and os.path.getmtime(MARSHAL) >= max(os.path.getmtime(p) for p in deps)):
+        return MARSHAL
+    tmp = MARSHAL + ".tmp"
+    r = subprocess.run([shutil.which("gcc") or "cc", "-O2", "-shared", "-fPIC", "-I", INCLUDE,
+                        "-I", sysconfig.get_paths()["include"], MARSHAL_SRC, "-o", tmp], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed on {MARSHAL_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
+
+
 def build(force: bool = False) -> str:
-    """Compile and link libfa.so unless it is newer than every source."""
+    """Compile the extension, and compile and link libfa.so, unless newer than every source."""
+    build_marshal(force)
     if (not force and os.path.exists(LIB)
             and os.path.getmtime(LIB) >= max(os.path.getmtime(p) for p in _deps())):
         return LIB

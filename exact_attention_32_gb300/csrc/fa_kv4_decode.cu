@@ -235,8 +235,6 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         tmem_relinquish();
     }
 
-    // the kernel behind this one may be set up meanwhile (it waits for this one's end before it reads)
-    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 
     // the share of this CTA: units before each sequence by a scan over the lengths, a thread each at a time
     Walk &start = *reinterpret_cast<Walk *>(smem + C::kWalk);
@@ -742,7 +740,6 @@ fa_kv4_merge_kernel(const DecodeArgs a, int RP)
     __shared__ float sm_x[kMergeWarps][D];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     const Split sp = a.split[blockIdx.x];
     if (sp.parts == 0) return;
     auto slot = [&](int i) -> int64_t { return i == 0 ? sp.slot : (static_cast<int64_t>(blockIdx.x) + i) * 2; };

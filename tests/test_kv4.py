@@ -415,7 +415,8 @@ def test_workspace_is_all_that_is_used_and_small_ones_are_refused():
 def test_overlapping_and_misplaced_pointers_are_refused():
     lens, pool = np.array([20], np.int32), Pool(1, 1, 64, 16, [20], seed=41)
     c, p = pool.cache(), dev(pool.table)
-    s, n = fa._binding._kv4_struct(c), dev(lens)
+    n = dev(lens)
+    s = fa.KV4CacheStruct(*(t.data_ptr() for t in c), pool.n_pages, 1, 16, 64)
     q = torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16, device="cuda")
     ws, lse = torch.empty(1 << 20, dtype=torch.uint8, device="cuda"), torch.zeros(1, device="cuda")
     call = lambda o, l, w: fa.fa_fwd_kv4(q.data_ptr(), s, n.data_ptr(), p.data_ptr(), o, l, 1, 1, 1, p.shape[1], 0.1,  # noqa: E731
