@@ -105,12 +105,14 @@ struct DecCfg {
     static constexpr int kGroupFloats = 3 * 8 + 4 * 8 + 8;  // mult, m, alpha [8]; red [4][8]; misc [8]
     static constexpr int kWalk = kFloat + RT * kGroupFloats * 4;  // the share's start, the scan's sums
     static constexpr int kBar = kWalk + 64 + 8 * kWarps;
-    static constexpr int kNumBars = 4 * kStages + 7;
+    static constexpr int kNumBars = 4 * kStages + 8;
     static constexpr int kSmemBytes = kBar + kNumBars * 8 + 16;
     static constexpr int kSCols = 4 * N, kOCols = N * KPT;
     static constexpr int kTmemCols = kSCols + kOCols <= 128 ? 128 : kSCols + kOCols <= 256 ? 256 : 512;
 };
-enum { D_S_FULL = 0, D_S_FREE, D_P_READY, D_PV_DONE, D_PV_DONE1, D_Q_READY, D_DONE, D_STAGES };  // then K_FULL, K_FREE, V_FULL, V_FREE
+// P_READY is a barrier a buffer: a group may have tile n + 1's P written while another still works on tile n's, and its
+// arrival must not count for tile n.  (It reaches tile n + 2 only behind the product of tile n.)
+enum { D_S_FULL = 0, D_S_FREE, D_P_READY, D_P_READY1, D_PV_DONE, D_PV_DONE1, D_Q_READY, D_DONE, D_STAGES };  // then K_FULL, K_FREE, V_FULL, V_FREE
 
 __host__ __device__ inline int tile_keys(int d) { return 128 * (128 / d); }
 
@@ -224,6 +226,7 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         mbar_init(BAR(D_S_FULL), 1);
         mbar_init(BAR(D_S_FREE), 4 * RT);
         mbar_init(BAR(D_P_READY), 4 * RT);
+        mbar_init(BAR(D_P_READY1), 4 * RT);
         mbar_init(BAR(D_PV_DONE), 1);
         mbar_init(BAR(D_PV_DONE1), 1);
         mbar_init(BAR(D_Q_READY), 4 * RT);
@@ -297,7 +300,7 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const uint32_t tS = tmem, tO = tmem + C::kSCols;
-    // P's buffer of tile n, and the barrier and phase of its product
+    // P's buffer of tile n, and the barriers and phase of its writing and its product
     auto pbuf = [&](int n) { return C::kPBufs == 2 ? n & 1 : 0; };
     auto pv_bar = [&](int n) { return BAR(D_PV_DONE + pbuf(n)); };
     auto pv_phase = [&](int n) -> uint32_t { return (C::kPBufs == 2 ? n >> 1 : n) & 1; };
@@ -365,7 +368,7 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         int n = 0, seg = 0;
         auto pv = [&](int m, bool first) -> bool {  // O^T (+)= V^T P^T of tile m
             if (!mbar_wait_warp(BAR(V_FULL + m % ST), (m / ST) & 1, kWaitLimitNs) ||
-                !mbar_wait_warp(BAR(D_P_READY), m & 1, kWaitLimitNs))
+                !mbar_wait_warp(BAR(D_P_READY + pbuf(m)), pv_phase(m), kWaitLimitNs))
                 return false;
             tc_fence_after();
             const uint32_t v = lo32(dA) + ((C::kV + m % ST * C::kHalf) >> 4);
@@ -647,7 +650,7 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(BAR(D_P_READY));
+                if (lane == 0) mbar_arrive(BAR(D_P_READY + pbuf(n)));
             }
             if (!ok) break;
 

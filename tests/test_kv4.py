@@ -662,6 +662,22 @@ def test_given_stream_and_repeated_calls_give_the_same_bits():
 
 
 @gpu
+@pytest.mark.parametrize("d,G,n_q", [(128, 4, 3), (128, 16, 1), (128, 8, 4), (64, 4, 3), (64, 8, 4), (128, 4, 9)])
+def test_groups_of_rows_run_apart_and_agree(d, G, n_q):
+    # 9 to 36 rows a key head: two or four groups of threads share the products, each at its own pace, over many tiles;
+    # calls back to back, so that the tiles come from L2 as fast as they ever do
+    lens = np.array([5000, 900, 2300, 1, 3700, 130, 4096, 640], np.int32)
+    pool = Pool(8, 4, d, 32, lens, seed=d + G)
+    q = bf16(2 * np.random.default_rng(G).standard_normal((8, 4 * G, n_q, d))).cuda()
+    c, table, n = pool.cache(), dev(pool.table), dev(lens)
+    runs = [fa.forward_kv4(q, c, n, table) for _ in range(12)]
+    o, lse = fa.forward_kv4(q, c, n, table, accumulate=True)
+    ok()
+    check_attention(pool, q, lens, fa.default_scale(d), o, lse, pool.w, f64(c.weights))
+    assert all(torch.equal(o, x) and torch.equal(lse, y) for x, y in runs)
+
+
+@gpu
 def test_sequences_may_share_pages_that_are_read():
     lens = np.array([90, 50], np.int32)
     pool = Pool(2, 1, 64, 16, lens, seed=71)
