@@ -1,5 +1,5 @@
 """ctypes binding of libfa.so: argument marshalling only (the tensor-level calls
-of the 4-bit cache go through the extension _marshal.c, which does the same faster).
+of the 4-bit cache go through the extension _marshal.cpp, which does the same faster).
 
 Every function of include/fa.h is exposed under the same name; ``forward`` is
 the tensor-level convenience call.  Torch supplies device memory and the
@@ -612,8 +612,7 @@ def _calls():
             raise RuntimeError("_marshal is missing: build it with exact_attention_32_gb300.build.build()") from e
         at = [ctypes.cast(f, ctypes.c_void_p).value for f in (
             L.fa_kv4_append, L.fa_kv4_read, L.fa_fwd_kv4, L.fa_fwd_kv4_workspace_bytes, L.fa_kv4_evict, L.fa_key_weights)]
-        m.setup(torch.uint8, torch.bfloat16, torch.float32, torch.int32, torch.empty, torch._C._cuda_getCurrentRawStream,
-                torch._C._cuda_getDevice, FAError, tuple(at))
+        m.setup(FAError, tuple(at))
         _marshal = m
     return _marshal
 

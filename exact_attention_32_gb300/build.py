@@ -2,7 +2,7 @@
 
 Each .cu under csrc/ is compiled by nvcc in parallel, then linked into
 ``exact_attention_32_gb300/libfa.so`` (static CUDA runtime); the binding's
-extension ``_marshal.so`` is compiled by gcc.  ptxas resource
+extension ``_marshal.so`` by g++ against the installed torch.  ptxas resource
 reports (registers, spills, shared memory) are kept next to the objects in
 ``_build/<name>.ptxas.txt``.
 """
@@ -21,7 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfa.so")
-MARSHAL_SRC = os.path.join(PKG, "_marshal.c")
+MARSHAL_SRC = os.path.join(PKG, "_marshal.cpp")
 MARSHAL = os.path.join(PKG, "_marshal.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -58,30 +58,47 @@ def _compile(src: str) -> str:
 
 
 def build_marshal(force: bool = False) -> str:
-    """Compile the binding's extension unless it is newer than its sources."""
+    """Compile the binding's extension unless it is newer than its sources and was built with this torch."""
+    import torch
+
     deps = [MARSHAL_SRC, os.path.join(INCLUDE, "fa.h"), __file__]
-    if (not force and os.path.exists(MARSHAL)
+    stamp, made_with = os.path.join(BUILD, "_marshal.torch.txt"), None
+    if os.path.exists(stamp):
+        with open(stamp) as f:
+            made_with = f.read()
+    if (not force and made_with == torch.__version__ and os.path.exists(MARSHAL)
             and os.path.getmtime(MARSHAL) >= max(os.path.getmtime(p) for p in deps)):
         return MARSHAL
-    tmp = MARSHAL + ".tmp"
-    r = subprocess.run([shutil.which("gcc") or "cc", "-O2", "-shared", "-fPIC", "-I", INCLUDE,
-                        "-I", sysconfig.get_paths()["include"], MARSHAL_SRC, "-o", tmp], capture_output=True, text=True)
+    os.makedirs(BUILD, exist_ok=True)
+    tmp, at = MARSHAL + ".tmp", os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    inc = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(at, "include"),
+           os.path.join(at, "include", "torch", "csrc", "api", "include"), cuda]
+    r = subprocess.run([shutil.which("g++") or "c++", "-O2", "-std=c++17", "-shared", "-fPIC"] +
+                       [x for i in inc for x in ("-isystem" if i != INCLUDE else "-I", i)] +
+                       [f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", MARSHAL_SRC, "-o", tmp,
+                        "-L", os.path.join(at, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"],
+                       capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"gcc failed on {MARSHAL_SRC}:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"g++ failed on {MARSHAL_SRC}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, MARSHAL)
+    with open(stamp, "w") as f:
+        f.write(torch.__version__)
     return MARSHAL
 
 
 def build(force: bool = False) -> str:
     """Compile the extension, and compile and link libfa.so, unless newer than every source."""
-    build_marshal(force)
     if (not force and os.path.exists(LIB)
             and os.path.getmtime(LIB) >= max(os.path.getmtime(p) for p in _deps())):
+        build_marshal()
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        marshal = ex.submit(build_marshal, force)
         objs = list(ex.map(_compile, srcs))
+        marshal.result()
     tmp = LIB + ".tmp"
     r = subprocess.run([nvcc()] + ARCH + ["-shared", "-o", tmp] + objs,
                        capture_output=True, text=True)

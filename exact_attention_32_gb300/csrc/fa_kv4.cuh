@@ -105,4 +105,23 @@ __device__ __forceinline__ uint32_t kv4_encode8(const uint32_t (&y)[4])
     return r;
 }
 
+// A kernel behind another whose results it needs: launched before that one has ended, so that its launch overlaps it, it
+// waits for the end itself.
+__device__ __forceinline__ void kv4_wait_for_the_one_before() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t kv4_launch_behind(void (*kern)(P...), int64_t grid, int threads, cudaStream_t s, A... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.stream = s;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
 }  // namespace

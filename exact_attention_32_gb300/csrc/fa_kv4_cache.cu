@@ -356,6 +356,7 @@ fa_kv4_move_kernel(Kv4Cache from, Kv4Cache to, const int32_t *__restrict__ table
     const int t = threadIdx.x % TPR, i = t % HALF;
     constexpr int kStep = 256 / TPR;  // rows of a block at a time
     bool bad = false;
+    kv4_wait_for_the_one_before();  // (the selection)
     for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * (U * kStep) + threadIdx.x / TPR; r0 < rows;
          r0 += static_cast<int64_t>(gridDim.x) * (U * kStep)) {
         int src[U];
@@ -448,10 +449,8 @@ cudaError_t fa_launch_kv4_evict(const Kv4EvictProblem &p, cudaStream_t stream)
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     auto *kern = p.from.d == 128 ? fa_kv4_move_kernel<128> : fa_kv4_move_kernel<64>;
-    kern<<<row_grid(rows, p.from.d / 16, 2, p.sm_count, 64), 256, 0, stream>>>(p.from, p.to, p.table, p.max_pages, p.to_table,
-                                                                        p.to_max_pages, p.kept, rows,
-                                                                        static_cast<int>(p.keep));
-    return cudaGetLastError();
+    return kv4_launch_behind(kern, row_grid(rows, p.from.d / 16, 2, p.sm_count, 64), 256, stream, p.from, p.to, p.table, p.max_pages,
+                             p.to_table, p.to_max_pages, p.kept, rows, static_cast<int>(p.keep));
 }
 
 int fa_kv4_cache_take_status(cudaStream_t stream) { return kv4_take_status_here(stream); }

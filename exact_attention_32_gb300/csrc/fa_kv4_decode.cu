@@ -742,7 +742,7 @@ fa_kv4_merge_kernel(const DecodeArgs a, int RP)
     __shared__ float sm_l[kMergeWarps], sm_m[kMergeWarps];
     __shared__ float sm_x[kMergeWarps][D];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    kv4_wait_for_the_one_before();
     const Split sp = a.split[blockIdx.x];
     if (sp.parts == 0) return;
     auto slot = [&](int i) -> int64_t { return i == 0 ? sp.slot : (static_cast<int64_t>(blockIdx.x) + i) * 2; };
@@ -829,7 +829,7 @@ fa_kv4_weights_kernel(const DecodeArgs a, int blocks)
     const int h = static_cast<int>(bh - b * a.c.heads);
     const int64_t cap = a.max_pages << a.c.log2_page;
     const int len = kv4_length(a.lens, b, cap);
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    kv4_wait_for_the_one_before();
     const float2 *ml = a.row_ml + bh * a.R;
     for (int key0 = blockIdx.x % blocks * 512 + threadIdx.x; key0 < len; key0 += blocks * 512) {
         const int n = key0 + 256 < len ? 2 : 1;
@@ -964,26 +964,6 @@ cudaError_t launch_rt(const DecodeArgs &a, int rt, int ctas, cudaStream_t s)
 
 }  // namespace
 
-namespace {
-
-// Launch of a kernel that waits for the one before it itself (griddepcontrol.wait), so that its own launch overlaps that one.
-template <typename K>
-cudaError_t launch_behind(K kern, int64_t grid, int threads, cudaStream_t s, const DecodeArgs &a, int arg)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
-    cfg.stream = s;
-    cudaLaunchAttribute attr = {};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, a, arg);
-}
-
-}  // namespace
-
 int64_t fa_kv4_decode_workspace(int64_t B, int64_t H, int64_t heads, int64_t n_q, int64_t d, int64_t max_tokens,
                                 int accumulate)
 {
@@ -1024,15 +1004,15 @@ cudaError_t fa_launch_kv4_decode(const Kv4DecodeProblem &p, void *workspace, cud
         e = p.accumulate ? launch_rt<64, true>(a, g.rt, g.ctas, stream) : launch_rt<64, false>(a, g.rt, g.ctas, stream);
     if (e != cudaSuccess) return e;
     if (!g.whole && g.ctas > 1) {
-        e = p.cache.d == 128 ? launch_behind(fa_kv4_merge_kernel<128>, g.ctas, kMergeWarps * 32, stream, a, 8 * g.rt)
-                             : launch_behind(fa_kv4_merge_kernel<64>, g.ctas, kMergeWarps * 32, stream, a, 8 * g.rt);
+        e = p.cache.d == 128 ? kv4_launch_behind(fa_kv4_merge_kernel<128>, g.ctas, kMergeWarps * 32, stream, a, 8 * g.rt)
+                             : kv4_launch_behind(fa_kv4_merge_kernel<64>, g.ctas, kMergeWarps * 32, stream, a, 8 * g.rt);
         if (e != cudaSuccess) return e;
     }
     if (p.accumulate) {
         int64_t blocks = (cap + 511) / 512;
         if (blocks > 512) blocks = 512;
         if (blocks * p.B * heads > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-        e = launch_behind(fa_kv4_weights_kernel, blocks * p.B * heads, 256, stream, a, static_cast<int>(blocks));
+        e = kv4_launch_behind(fa_kv4_weights_kernel, blocks * p.B * heads, 256, stream, a, static_cast<int>(blocks));
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

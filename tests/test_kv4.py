@@ -187,6 +187,53 @@ def test_python_calls_refuse_wrong_tensors():
         fa.key_weights(torch.zeros(1, 3, 8, 64).bfloat16(), torch.zeros(1, 2, 8, 64).bfloat16(), torch.zeros(1, 3, 8))
 
 
+def test_python_calls_refuse_what_is_no_tensor_or_cache():
+    c = fa.kv4_cache(2, 1, 16, 64, device="cpu")
+    i = torch.zeros(1, dtype=torch.int32)
+    for cache in (None, tuple(c)[:4], (1, 2, 3, 4, 5), c._replace(k=[0]), c._replace(k=torch.zeros(2, 1, 16, 32, dtype=torch.uint8).to_sparse())):
+        with pytest.raises(ValueError):
+            fa.kv4_read(cache, i, i[None], 1)
+    with pytest.raises(ValueError):
+        fa.key_weights(None, None, None)
+    with pytest.raises(TypeError):
+        fa.kv4_read(c, i)
+
+
+@gpu
+def test_python_calls_refuse_wrong_gpu_tensors():
+    c = fa.kv4_cache(4, 2, 16, 64)
+    i, x = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros(1, 2, 1, 64, dtype=torch.bfloat16, device="cuda")
+    t = i[None]
+    for bad in (x.float(), x[:, :1], x[..., :32], x.cpu(), x.expand(2, 2, 1, 64), x.transpose(1, 2), None):
+        with pytest.raises(ValueError):
+            fa.kv4_append(c, x, bad, i, t)
+    for lens in (i.long(), i[None], i.cpu(), torch.zeros(2, dtype=torch.int32, device="cuda"), 0):
+        with pytest.raises(ValueError):
+            fa.kv4_append(c, x, x, lens, t)
+    with pytest.raises(ValueError):
+        fa.kv4_read(c._replace(v=c.v.cpu()), i, t, 1)
+    with pytest.raises(ValueError):
+        fa.kv4_read(c, i, t, 0)
+    with pytest.raises(TypeError):
+        fa.kv4_read(c, i, t, 1.5)
+    with pytest.raises(ValueError):
+        fa.forward_kv4(x[:, :1].contiguous(), c, i, t)  # 1 head over 2 key heads
+    with pytest.raises(TypeError):
+        fa.forward_kv4(x, c, i, t, scale="1")
+    for scale in (0.0, -1.0, float("nan"), float("inf")):
+        with pytest.raises(fa.FAError):
+            fa.forward_kv4(x, c, i, t, scale=scale)
+    with pytest.raises(ValueError):
+        fa.forward_kv4(x, c, i, t, workspace=torch.zeros(4, device="cuda"))
+    with pytest.raises(ValueError):
+        fa.forward_kv4(x, c._replace(weights=None), i, t, accumulate=True)
+    with pytest.raises(ValueError):
+        fa.kv4_evict(c, i, t, fa.kv4_cache(4, 2, 32, 64), t, 1)
+    with pytest.raises(ValueError):
+        fa.kv4_evict(c, i, t, c, t, 17)
+    ok()
+
+
 # ------------------------------------------------------------------------------- append, read
 
 SPECIAL = np.array([0.0, -0.0, 1e-30, 2.0 ** -18 * 6, 2.0 ** -17 * 5, 3e-4, 0.1, 1.0, 5.0, 6.0, 448.0, 61440.0, 65000.0, 3e38])
