@@ -51,7 +51,8 @@ struct KwCfg {
     static constexpr int kStageBytes = kQBlock * D * 2;
     static constexpr int kLse = kStages * kStageBytes;  // per stage: 128 floats
     static constexpr int kSum = kLse + kStages * kQBlock * 4;  // rank 0: [rank][key] sums of its cluster
-    static constexpr int kBar = kSum + kMaxRanks * kKeys * 4;
+    static constexpr int kOut = kSum + kMaxRanks * kKeys * 4;  // per stage: does it hold a query that adds nothing?
+    static constexpr int kBar = kOut + kStages * 4;
     static constexpr int kNumBars = 4 * kStages + 4 * kBufs + 2;
     static constexpr int kSmemBytes = kBar + kNumBars * 8 + 16;
 };
@@ -188,7 +189,8 @@ fa_key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const KwArgs a)
                 mbar_wait(BAR(KW_Q_FULL + i % kStages), (i / kStages) & 1, ok ? kWaitLimitNs : kCleanupLimitNs);
         }
     } else if (warp == kKwLse) {
-        // -LSE log2 e of each query; -inf (weight 0) for rows past N, before first, or without a key
+        // -LSE log2 e of each query; -inf (weight 0) for rows past N, whose scores the TMA's zeros make 0; +inf for those
+        // before first or without a key, whose scores may be anything: their blocks go through the guarded sum
         bool ok = true;
         for (int i = 0; i < nq && ok; ++i, walk.next()) {
             const int st = i % kStages;
@@ -196,16 +198,19 @@ fa_key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const KwArgs a)
             const int q0 = walk.qb * kQBlock;
             const float *src = a.lse + static_cast<int64_t>(walk.qh) * a.N;
             float *dst = reinterpret_cast<float *>(smem + C::kLse) + st * kQBlock;
+            bool out = false;
+            float x[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = src[min(q0 + j * 32 + lane, a.N - 1)];  // (without branches: the loads go out together)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int q = q0 + j * 32 + lane;
-                float x = -INFINITY;
-                if (q < a.N && q >= a.first) {
-                    x = src[q];
-                    x = x == -INFINITY ? x : -x * 1.4426950408889634f;
-                }
-                dst[j * 32 + lane] = x;
+                if (q < a.first) x[j] = -INFINITY;
+                out |= x[j] == -INFINITY;
+                dst[j * 32 + lane] = q < a.N ? x[j] * -1.4426950408889634f : -INFINITY;
             }
+            out = __any_sync(0xffffffffu, out);
+            if (lane == 0) reinterpret_cast<int *>(smem + C::kOut)[st] = out;
             __syncwarp();
             if (lane == 0) mbar_arrive(BAR(KW_LSE_FULL + st));
         }
@@ -286,7 +291,7 @@ fa_key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const KwArgs a)
             // 32 queries of this key: their scores in x, their sum added to s0, s1 (the tile's sums in registers of
             // their own first: 64 terms, then one addition to the total)
             float2 s0 = make_float2(0.f, 0.f), s1 = s0;
-            auto take = [&](const uint32_t (&x)[32], int c, auto diag) {
+            auto take = [&](const uint32_t (&x)[32], int c, auto guard) {
 #pragma unroll
                 for (int j = 0; j < 32; j += 4) {
                     const float4 l = *reinterpret_cast<const float4 *>(ls + c * 32 + j);
@@ -295,31 +300,32 @@ fa_key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const KwArgs a)
                     const float2 y1 = fma2(make_float2(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3])), sc,
                                            make_float2(l.z, l.w));
                     float2 p0 = make_float2(ex2(y0.x), ex2(y0.y)), p1 = make_float2(ex2(y1.x), ex2(y1.y));
-                    if constexpr (decltype(diag)::value) {
-                        const int q = q0 + half * 64 + c * 32 + j;
-                        if (key > q) p0.x = 0.f;
-                        if (key > q + 1) p0.y = 0.f;
-                        if (key > q + 2) p1.x = 0.f;
-                        if (key > q + 3) p1.y = 0.f;
+                    if constexpr (decltype(guard)::value) {
+                        const int q = CAUSAL ? q0 + half * 64 + c * 32 + j : key;
+                        if (key > q || l.x == INFINITY) p0.x = 0.f;
+                        if (key > q + 1 || l.y == INFINITY) p0.y = 0.f;
+                        if (key > q + 2 || l.z == INFINITY) p1.x = 0.f;
+                        if (key > q + 3 || l.w == INFINITY) p1.y = 0.f;
                     }
                     s0 = add2(s0, p0);
                     s1 = add2(s1, p1);
                 }
             };
             // the next 32 scores are on their way from tensor memory while the last are used
-            auto tile = [&](auto diag) {
+            auto tile = [&](auto guard) {
                 uint32_t x0[32], x1[32];
                 tmem_ld32(src, x0);
                 tmem_wait_ld();
                 tmem_ld32(src + 32, x1);
-                take(x0, 0, diag);
+                take(x0, 0, guard);
                 tmem_wait_ld();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(BAR(KW_S_FREE + kw_slot(n)));
-                take(x1, 1, diag);
+                take(x1, 1, guard);
             };
-            if (CAUSAL && q0 < k0 + w * kKeyTile + kKeyTile - 1)
+            const bool out = reinterpret_cast<volatile int *>(smem + C::kOut)[st] != 0;
+            if ((CAUSAL && q0 < k0 + w * kKeyTile + kKeyTile - 1) || out)
                 tile(std::true_type{});
             else
                 tile(std::false_type{});

@@ -384,6 +384,21 @@ def test_attention_over_long_ragged_lengths(d, P, Hkv, G, n_q):
 
 
 @gpu
+@pytest.mark.parametrize("d,P,B,n_q,stored", [(64, 16, 700, 1, 80), (128, 16, 1300, 2, 40), (128, 32, 450, 1, 900), (64, 64, 400, 3, 1500)])
+def test_attention_over_many_sequences(d, P, B, n_q, stored):
+    # more sequences than a CTA has threads, most of them shorter than a tile, among them empty ones
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, stored // 8, B).astype(np.int32)
+    lens[::37], lens[5], lens[B - 1] = 0, stored, stored - 1
+    pool = Pool(B, 1, d, P, lens, seed=B)
+    q = bf16(rng.standard_normal((B, 3, n_q, d))).cuda()
+    c = pool.cache()
+    o, lse = fa.forward_kv4(q, c, dev(lens), dev(pool.table), accumulate=True)
+    ok()
+    check_attention(pool, q, lens, fa.default_scale(d), o, lse, pool.w, f64(c.weights))
+
+
+@gpu
 @pytest.mark.parametrize("gain", [1e-4, 1e3])
 @pytest.mark.parametrize("q_gain", [1e-20, 1e-3, 40.0])
 def test_attention_over_small_and_large_values(gain, q_gain):
@@ -584,6 +599,34 @@ def test_key_weights(B, H, Hkv, N, first, d, causal):
     top = np.abs(np.where(np.isfinite(lse), lse, 0)).max()
     tol = want * (2 * (d + 8) * 2.0 ** -23 * reach + 2.0 ** -21 * (top + 2)) + 1e-37
     assert w.shape == want.shape and (np.abs(f64(w) - want) <= tol).all()
+
+
+@gpu
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("H,Hkv,N,first", [(2, 1, 200, 0), (2, 2, 700, 300), (16, 1, 515, 129)])
+def test_key_weights_of_queries_left_out_may_hold_anything(H, Hkv, N, first, causal):
+    # queries before first_query, and those without a key (LSE -inf): NaN, infinities and the largest numbers in them
+    g = torch.Generator().manual_seed(N)
+    q, k = torch.randn(1, H, N, 64, generator=g).bfloat16(), torch.randn(1, Hkv, N, 64, generator=g).bfloat16()
+    lse = dev(_lse(f64(q), f64(k), fa.default_scale(64), causal))
+    gone = torch.zeros(N, dtype=torch.bool)
+    gone[:first] = True
+    gone[first + 3::31] = True
+    lse[:, :, torch.arange(first + 3, N, 31)] = -np.inf
+    fill = torch.tensor([float("nan"), float("inf"), -float("inf"), 3e38]).bfloat16()
+    bad = q.clone()
+    bad[:, :, gone] = fill[torch.arange(int(gone.sum())) % 4, None]
+    w, w2 = (fa.key_weights(x.cuda(), k.cuda(), lse, causal=causal, first_query=first) for x in (q, bad))
+    ok()
+    assert torch.isfinite(w).all() and torch.equal(w, w2)
+    # and a NaN among the others reaches the keys that they admit, no others
+    i = int(torch.nonzero(~gone)[len(torch.nonzero(~gone)) // 2])
+    q[0, H - 1, i, 5] = float("nan")
+    w3 = fa.key_weights(q.cuda(), k.cuda(), lse, causal=causal, first_query=first)
+    ok()
+    last = i + 1 if causal else N
+    assert torch.isnan(w3[0, -1, :last]).all() and torch.equal(w3[0, -1, last:], w[0, -1, last:])
+    assert torch.equal(w3[0, :-1], w[0, :-1])
 
 
 @gpu
