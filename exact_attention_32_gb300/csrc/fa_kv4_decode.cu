@@ -99,20 +99,22 @@ struct DecCfg {
     static constexpr int kQ = 2 * kStages * kHalf;
     static constexpr int kP = kQ + N * 128;
     static constexpr int kPBytes = 128 * N * KPT;
-    static constexpr int kScale = kP + kPBufs * kPBytes;         // with V's stage: K scales 512, V scales 256, page flags 64
+    static constexpr int kScale = kP + kPBufs * kPBytes;         // a tile's K scales 512, V scales 256, page flags 64
     static constexpr int kScaleBytes = 512 + 256 + 64;
-    static constexpr int kFloat = kScale + kStages * kScaleBytes;
+    static constexpr int kScales = kStages + 1;                  // of these
+    static constexpr int kFloat = kScale + kScales * kScaleBytes;
     static constexpr int kGroupFloats = 3 * 8 + 4 * 8 + 8;  // mult, m, alpha [8]; red [4][8]; misc [8]
     static constexpr int kWalk = kFloat + RT * kGroupFloats * 4;  // the share's start, the scan's sums
     static constexpr int kBar = kWalk + 64 + 8 * kWarps;
-    static constexpr int kNumBars = 4 * kStages + 8;
+    static constexpr int kNumBars = 5 * kStages + 9;
     static constexpr int kSmemBytes = kBar + kNumBars * 8 + 16;
     static constexpr int kSCols = 4 * N, kOCols = N * KPT;
     static constexpr int kTmemCols = kSCols + kOCols <= 128 ? 128 : kSCols + kOCols <= 256 ? 256 : 512;
 };
 // P_READY is a barrier a buffer: a group may have tile n + 1's P written while another still works on tile n's, and its
 // arrival must not count for tile n.  (It reaches tile n + 2 only behind the product of tile n.)
-enum { D_S_FULL = 0, D_S_FREE, D_P_READY, D_P_READY1, D_PV_DONE, D_PV_DONE1, D_Q_READY, D_DONE, D_STAGES };  // then K_FULL, K_FREE, V_FULL, V_FREE
+enum { D_S_FULL = 0, D_S_FREE, D_P_READY, D_P_READY1, D_PV_DONE, D_PV_DONE1, D_Q_READY, D_DONE, D_STAGES };
+// then K_FULL, K_FREE, V_FULL, V_FREE of the stages and X_FULL of the scales
 
 __host__ __device__ inline int tile_keys(int d) { return 128 * (128 / d); }
 
@@ -208,7 +210,8 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     using C = DecCfg<D, RT>;
     constexpr int RP = C::RP, N = C::N, KPT = C::KPT, TK = C::TK, ST = C::kStages;
     constexpr int kLoadWarp = C::kLoadWarp, kMmaWarp = C::kMmaWarp, kDecThreads = C::kThreads, kDecWarps = C::kWarps;
-    constexpr int K_FULL = D_STAGES, K_FREE = K_FULL + ST, V_FULL = K_FREE + ST, V_FREE = V_FULL + ST;
+    constexpr int K_FULL = D_STAGES, K_FREE = K_FULL + ST, V_FULL = K_FREE + ST, V_FREE = V_FULL + ST,
+                  X_FULL = V_FREE + ST, XS = C::kScales;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sb = smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -222,7 +225,7 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     const int64_t cap = a.max_pages << a.c.log2_page;
 
     if (tid == 0) {
-        for (int s = 0; s < 4 * ST; ++s) mbar_init(BAR(D_STAGES + s), 1);
+        for (int s = 0; s < 4 * ST + XS; ++s) mbar_init(BAR(D_STAGES + s), 1);
         mbar_init(BAR(D_S_FULL), 1);
         mbar_init(BAR(D_S_FREE), 4 * RT);
         mbar_init(BAR(D_P_READY), 4 * RT);
@@ -314,49 +317,80 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             prefetch_tmap(&tm_k);
             prefetch_tmap(&tm_v);
         }
-        const int bt = min(1 << a.c.log2_page, TK);  // tokens a box: a page, or the tile's part of one
+        const int bt = min(1 << a.c.log2_page, TK), n_boxes = TK / bt;  // tokens a box: a page, or the tile's part of one
         const int in_page = (1 << a.c.log2_page) - 1;
-        int n = 0;
+        // the table's entry for this lane's box, asked for a tile ahead
+        auto entry = [&](int t) -> int {
+            const int key = t * TK + lane * bt;
+            return lane < n_boxes && key < w.len ? a.table[w.b * a.max_pages + (key >> a.c.log2_page)] : 0;
+        };
+        struct Tile {  // this lane's box of a tile (rows of a box that is left out keep stale codes, as good as any: their weight is 0)
+            int page, slot, h;
+            uint32_t tokens;
+            bool there;
+        } cur, before;
+        int nk = 0, nv = 0;  // tiles whose K, whose V are on their way
         bool ok = true;
-        for (; w.left > 0 && ok; walk_next<TK>(w, a)) {
-            const int h = w.it / a.n_rc;  // (a segment without a tile falls through every role)
-            for (int t = w.t0; t < w.t1; ++t, ++n) {
-                const int st = n % ST, key = t * TK + lane * bt;
-                int page = -1;
-                if (lane * bt < TK && key < w.len) page = kv4_page(a.c, a.table, w.b, a.max_pages, key);
-                const uint32_t boxes = __ballot_sync(0xffffffffu, page >= 0);
-                const uint32_t tokens = __popc(boxes) * bt;
-                if (n >= ST && !(ok = mbar_wait_warp(BAR(K_FREE + st), (n / ST - 1) & 1, kWaitLimitNs))) break;
-                if (lane == 0) mbar_arrive_expect_tx(BAR(K_FULL + st), tokens * (D / 2));
-                __syncwarp();
-                // (rows of a box that is left out keep stale codes, as good as any: their weight is 0)
-                if (page >= 0)
-                    tma_load_4d(sb + st * C::kHalf + lane * bt / KPT * 128, &tm_k, BAR(K_FULL + st), 0,
-                                (key & in_page) / KPT, h, page);
-                if (n >= ST && !(ok = mbar_wait_warp(BAR(V_FREE + st), (n / ST - 1) & 1, kWaitLimitNs))) break;
-                uint8_t *scale = smem + C::kScale + st * C::kScaleBytes;
+        while (w.left > 0 && w.t0 == w.t1) walk_next<TK>(w, a);  // (a segment without a tile falls through every role)
+        int t = w.t0, next = w.left > 0 ? entry(t) : 0;
+        // K of a tile, then V of the one before it: the order in which their stages come free
+        while (w.left > 0 || nv < nk) {
+            const bool more = w.left > 0;
+            if (more) {
+                cur.page = next;
+                cur.there = lane < n_boxes && t * TK + lane * bt < w.len;
+                if (cur.there && static_cast<unsigned>(cur.page) >= static_cast<unsigned>(a.c.n_pages)) {
+                    kv4_report();
+                    cur.there = false;
+                }
+                cur.slot = (t * TK & in_page) / KPT;  // (a tile begins a page, or lies in one)
+                cur.h = w.it / a.n_rc;
+                const uint32_t boxes = __ballot_sync(0xffffffffu, cur.there);
+                cur.tokens = __popc(boxes) * bt;
+                if (++t == w.t1) {
+                    do walk_next<TK>(w, a);
+                    while (w.left > 0 && w.t0 == w.t1);
+                    t = w.t0;
+                }
+                if (w.left > 0) next = entry(t);
+                const int st = nk % ST, xs = nk % XS;
+                if (nk >= ST && !(ok = mbar_wait_warp(BAR(K_FREE + st), (nk / ST - 1) & 1, kWaitLimitNs))) break;
+                // (K's stage was freed by the product of tile nk - ST, which waited for the scores of the tile before that
+                // to be read, and so for its scales)
+                uint8_t *scale = smem + C::kScale + xs * C::kScaleBytes;
                 if (lane < C::NG) reinterpret_cast<int *>(scale + 768)[lane] = (boxes >> (lane * 16 / bt)) & 1u;
                 __syncwarp();
-                if (lane == 0) mbar_arrive_expect_tx(BAR(V_FULL + st), tokens * (D / 2 + D / 32 + 1));
-                __syncwarp();
-                if (page >= 0) {
-                    tma_load_4d(sb + C::kV + st * C::kHalf + lane * bt / KPT * 128, &tm_v, BAR(V_FULL + st), 0,
-                                (key & in_page) / KPT, h, page);
-                    const int64_t row = kv4_row(a.c, page, h, key);
-                    bulk_load(smem_u32(scale) + lane * bt * (D / 32), a.c.k_scale + row * (D / 32), bt * (D / 32),
-                              BAR(V_FULL + st));
-                    bulk_load(smem_u32(scale) + 512 + lane * bt, a.c.v_scale + row, bt, BAR(V_FULL + st));
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(BAR(K_FULL + st), cur.tokens * (D / 2));
+                    mbar_arrive_expect_tx(BAR(X_FULL + xs), cur.tokens * (D / 32 + 1));
                 }
+                __syncwarp();
+                if (cur.there) {
+                    tma_load_4d(sb + st * C::kHalf + lane * bt / KPT * 128, &tm_k, BAR(K_FULL + st), 0, cur.slot, cur.h, cur.page);
+                    const int64_t row = kv4_row(a.c, cur.page, cur.h, cur.slot * KPT);
+                    bulk_load(smem_u32(scale) + lane * bt * (D / 32), a.c.k_scale + row * (D / 32), bt * (D / 32), BAR(X_FULL + xs));
+                    bulk_load(smem_u32(scale) + 512 + lane * bt, a.c.v_scale + row, bt, BAR(X_FULL + xs));
+                }
+                ++nk;
             }
+            if (nv < nk - (more ? 1 : 0)) {
+                const int st = nv % ST;
+                if (nv >= ST && !(ok = mbar_wait_warp(BAR(V_FREE + st), (nv / ST - 1) & 1, kWaitLimitNs))) break;
+                if (lane == 0) mbar_arrive_expect_tx(BAR(V_FULL + st), before.tokens * (D / 2));
+                __syncwarp();
+                if (before.there)
+                    tma_load_4d(sb + C::kV + st * C::kHalf + lane * bt / KPT * 128, &tm_v, BAR(V_FULL + st), 0, before.slot, before.h,
+                                before.page);
+                ++nv;
+            }
+            before = cur;
         }
         if (!ok && lane == 0) kv4_timeout();
-        // no copy in flight when the CTA ends (after a break, K of one tile more than V is)
+        // no copy in flight when the CTA ends
         const uint64_t lim = ok ? kWaitLimitNs : kCleanupLimitNs;
-        for (int i = n > ST ? n - ST : 0; i < n; ++i) {
-            mbar_wait(BAR(K_FULL + i % ST), (i / ST) & 1, lim);
-            mbar_wait(BAR(V_FULL + i % ST), (i / ST) & 1, lim);
-        }
-        if (!ok) mbar_wait(BAR(K_FULL + n % ST), (n / ST) & 1, lim);
+        for (int i = nk > ST ? nk - ST : 0; i < nk; ++i) mbar_wait(BAR(K_FULL + i % ST), (i / ST) & 1, lim);
+        for (int i = nk > XS ? nk - XS : 0; i < nk; ++i) mbar_wait(BAR(X_FULL + i % XS), (i / XS) & 1, lim);
+        for (int i = nv > ST ? nv - ST : 0; i < nv; ++i) mbar_wait(BAR(V_FULL + i % ST), (i / ST) & 1, lim);
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------------- products
         constexpr uint32_t idS = idesc_e2m1_e4m3_f32(128, N, false, false);
@@ -476,12 +510,11 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             for (int i = 0; i < 4; ++i) l[i] = make_float2(0.f, 0.f);
 
             for (int t = w.t0; t < w.t1; ++t, ++n) {
-                const int st = n % ST;
-                const uint8_t *scale = smem + C::kScale + st * C::kScaleBytes;
-                const int *flag = reinterpret_cast<const int *>(scale + 768);
+                const int xs = n % XS;
+                const uint8_t *scale = smem + C::kScale + xs * C::kScaleBytes;
                 const int key0 = t * TK;
                 // (P's buffer has been read, too)
-                ok = mbar_wait_warp(BAR(V_FULL + st), (n / ST) & 1, kWaitLimitNs) &&
+                ok = mbar_wait_warp(BAR(X_FULL + xs), (n / XS) & 1, kWaitLimitNs) &&
                      mbar_wait_warp(BAR(D_S_FULL), n & 1, kWaitLimitNs) &&
                      (n < C::kPBufs || mbar_wait_warp(pv_bar(n), pv_phase(n - C::kPBufs), kWaitLimitNs));
                 if (!ok) *sm_fail = 1.f;
@@ -496,6 +529,7 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
 #pragma unroll
                     for (int k = 0; k < KPT; ++k) vs[k] = kv4_scale(scale[512 + tl * KPT + k]);
                 }
+                const bool here = reinterpret_cast<const int *>(scale + 768)[tl * KPT >> 4] != 0;
                 {
                     uint32_t s[4][16];
 #pragma unroll
@@ -523,12 +557,12 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                         }
                 }
                 // keys that a row does not admit, or that no page holds, leave it; what lies there may be anything
-                const bool edge = key0 + TK > w.len - a.n_q + 1 || __any_sync(0xffffffffu, flag[lane % C::NG] == 0);
+                const bool edge = key0 + TK > w.len - a.n_q + 1 || __any_sync(0xffffffffu, !here);
                 if (edge) {
 #pragma unroll
                     for (int k = 0; k < KPT; ++k) {
-                        const int j = tl * KPT + k, key = key0 + j;
-                        const bool gone = key >= w.len || flag[j >> 4] == 0;
+                        const int key = key0 + tl * KPT + k;
+                        const bool gone = key >= w.len || !here;
                         if (gone) vs[k] = 0.f;
 #pragma unroll
                         for (int r = 0; r < 8; ++r) {
