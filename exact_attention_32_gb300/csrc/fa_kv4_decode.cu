@@ -86,7 +86,7 @@ struct DecodeArgs {
 template <int D, int RT>
 struct DecCfg {
     static constexpr int RP = 8 * RT;          // rows a CTA takes
-    static constexpr int kLoadWarp = 4 * RT, kMmaWarp = kLoadWarp + 1, kWarps = kLoadWarp + 2, kThreads = 32 * kWarps;
+    static constexpr int kLoadWarp = 4 * RT, kMmaWarp = kLoadWarp + 2, kWarps = kLoadWarp + 3, kThreads = 32 * kWarps;
     static constexpr int N = 16 * RT;          // columns: per 8 rows, 8 high parts and 8 rests
     static constexpr int KPT = 128 / D;        // keys a thread (and a 128-byte row) holds
     static constexpr int TK = 128 * KPT;       // keys a tile
@@ -311,86 +311,66 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     Walk w = start;
     if (!run) w.left = 0;
 
-    if (warp == kLoadWarp) {
-        // -------------------------------------------------------------------- loads
-        if (lane == 0) {
-            prefetch_tmap(&tm_k);
-            prefetch_tmap(&tm_v);
-        }
+    if (warp == kLoadWarp || warp == kLoadWarp + 1) {
+        // -------------------------------------------------------------------- loads: K with the scales, and V
+        const bool is_k = warp == kLoadWarp;
+        if (lane == 0) prefetch_tmap(is_k ? &tm_k : &tm_v);
         const int bt = min(1 << a.c.log2_page, TK), n_boxes = TK / bt;  // tokens a box: a page, or the tile's part of one
         const int in_page = (1 << a.c.log2_page) - 1;
+        const uint32_t dst = sb + (is_k ? 0 : C::kV) + lane * bt / KPT * 128;
+        const int full = is_k ? K_FULL : V_FULL, free = is_k ? K_FREE : V_FREE;
         // the table's entry for this lane's box, asked for a tile ahead
         auto entry = [&](int t) -> int {
             const int key = t * TK + lane * bt;
             return lane < n_boxes && key < w.len ? a.table[w.b * a.max_pages + (key >> a.c.log2_page)] : 0;
         };
-        struct Tile {  // this lane's box of a tile (rows of a box that is left out keep stale codes, as good as any: their weight is 0)
-            int page, slot, h;
-            uint32_t tokens;
-            bool there;
-        } cur, before;
-        int nk = 0, nv = 0;  // tiles whose K, whose V are on their way
+        int n = 0;
         bool ok = true;
         while (w.left > 0 && w.t0 == w.t1) walk_next<TK>(w, a);  // (a segment without a tile falls through every role)
         int t = w.t0, next = w.left > 0 ? entry(t) : 0;
-        // K of a tile, then V of the one before it: the order in which their stages come free
-        while (w.left > 0 || nv < nk) {
-            const bool more = w.left > 0;
-            if (more) {
-                cur.page = next;
-                cur.there = lane < n_boxes && t * TK + lane * bt < w.len;
-                if (cur.there && static_cast<unsigned>(cur.page) >= static_cast<unsigned>(a.c.n_pages)) {
-                    kv4_report();
-                    cur.there = false;
-                }
-                cur.slot = (t * TK & in_page) / KPT;  // (a tile begins a page, or lies in one)
-                cur.h = w.it / a.n_rc;
-                const uint32_t boxes = __ballot_sync(0xffffffffu, cur.there);
-                cur.tokens = __popc(boxes) * bt;
-                if (++t == w.t1) {
-                    do walk_next<TK>(w, a);
-                    while (w.left > 0 && w.t0 == w.t1);
-                    t = w.t0;
-                }
-                if (w.left > 0) next = entry(t);
-                const int st = nk % ST, xs = nk % XS;
-                if (nk >= ST && !(ok = mbar_wait_warp(BAR(K_FREE + st), (nk / ST - 1) & 1, kWaitLimitNs))) break;
-                // (K's stage was freed by the product of tile nk - ST, which waited for the scores of the tile before that
-                // to be read, and so for its scales)
-                uint8_t *scale = smem + C::kScale + xs * C::kScaleBytes;
-                if (lane < C::NG) reinterpret_cast<int *>(scale + 768)[lane] = (boxes >> (lane * 16 / bt)) & 1u;
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(BAR(K_FULL + st), cur.tokens * (D / 2));
-                    mbar_arrive_expect_tx(BAR(X_FULL + xs), cur.tokens * (D / 32 + 1));
-                }
-                __syncwarp();
-                if (cur.there) {
-                    tma_load_4d(sb + st * C::kHalf + lane * bt / KPT * 128, &tm_k, BAR(K_FULL + st), 0, cur.slot, cur.h, cur.page);
-                    const int64_t row = kv4_row(a.c, cur.page, cur.h, cur.slot * KPT);
+        for (; w.left > 0; ++n) {
+            const int page = next, h = w.it / a.n_rc, slot = (t * TK & in_page) / KPT;  // (a tile begins a page, or lies in one)
+            bool there = lane < n_boxes && t * TK + lane * bt < w.len;
+            if (there && static_cast<unsigned>(page) >= static_cast<unsigned>(a.c.n_pages)) {
+                kv4_report();
+                there = false;
+            }
+            const uint32_t boxes = __ballot_sync(0xffffffffu, there);
+            const uint32_t tokens = __popc(boxes) * bt;
+            if (++t == w.t1) {
+                do walk_next<TK>(w, a);
+                while (w.left > 0 && w.t0 == w.t1);
+                t = w.t0;
+            }
+            if (w.left > 0) next = entry(t);
+            const int st = n % ST, xs = n % XS;
+            if (n >= ST && !(ok = mbar_wait_warp(BAR(free + st), (n / ST - 1) & 1, kWaitLimitNs))) break;
+            // (K's stage was freed by the product of tile n - ST, which waited for the scores of the tile before that
+            // to be read, and so for its scales)
+            uint8_t *scale = smem + C::kScale + xs * C::kScaleBytes;
+            if (is_k && lane < C::NG) reinterpret_cast<int *>(scale + 768)[lane] = (boxes >> (lane * 16 / bt)) & 1u;
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive_expect_tx(BAR(full + st), tokens * (D / 2));
+                if (is_k) mbar_arrive_expect_tx(BAR(X_FULL + xs), tokens * (D / 32 + 1));
+            }
+            __syncwarp();
+            // (rows of a box that is left out keep stale codes, as good as any: their weight is 0)
+            if (there) {
+                tma_load_4d(dst + st * C::kHalf, is_k ? &tm_k : &tm_v, BAR(full + st), 0, slot, h, page);
+                if (is_k) {
+                    const int64_t row = kv4_row(a.c, page, h, slot * KPT);
                     bulk_load(smem_u32(scale) + lane * bt * (D / 32), a.c.k_scale + row * (D / 32), bt * (D / 32), BAR(X_FULL + xs));
                     bulk_load(smem_u32(scale) + 512 + lane * bt, a.c.v_scale + row, bt, BAR(X_FULL + xs));
                 }
-                ++nk;
             }
-            if (nv < nk - (more ? 1 : 0)) {
-                const int st = nv % ST;
-                if (nv >= ST && !(ok = mbar_wait_warp(BAR(V_FREE + st), (nv / ST - 1) & 1, kWaitLimitNs))) break;
-                if (lane == 0) mbar_arrive_expect_tx(BAR(V_FULL + st), before.tokens * (D / 2));
-                __syncwarp();
-                if (before.there)
-                    tma_load_4d(sb + C::kV + st * C::kHalf + lane * bt / KPT * 128, &tm_v, BAR(V_FULL + st), 0, before.slot, before.h,
-                                before.page);
-                ++nv;
-            }
-            before = cur;
         }
         if (!ok && lane == 0) kv4_timeout();
         // no copy in flight when the CTA ends
         const uint64_t lim = ok ? kWaitLimitNs : kCleanupLimitNs;
-        for (int i = nk > ST ? nk - ST : 0; i < nk; ++i) mbar_wait(BAR(K_FULL + i % ST), (i / ST) & 1, lim);
-        for (int i = nk > XS ? nk - XS : 0; i < nk; ++i) mbar_wait(BAR(X_FULL + i % XS), (i / XS) & 1, lim);
-        for (int i = nv > ST ? nv - ST : 0; i < nv; ++i) mbar_wait(BAR(V_FULL + i % ST), (i / ST) & 1, lim);
+        for (int i = n > ST ? n - ST : 0; i < n; ++i) mbar_wait(BAR(full + i % ST), (i / ST) & 1, lim);
+        if (is_k)
+            for (int i = n > XS ? n - XS : 0; i < n; ++i) mbar_wait(BAR(X_FULL + i % XS), (i / XS) & 1, lim);
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------------- products
         constexpr uint32_t idS = idesc_e2m1_e4m3_f32(128, N, false, false);
