@@ -86,7 +86,7 @@ struct DecodeArgs {
 template <int D, int RT>
 struct DecCfg {
     static constexpr int RP = 8 * RT;          // rows a CTA takes
-    static constexpr int kLoadWarp = 4 * RT, kMmaWarp = kLoadWarp + 2, kWarps = kLoadWarp + 3, kThreads = 32 * kWarps;
+    static constexpr int kLoadWarp = 4 * RT, kMmaWarp = kLoadWarp + 3, kWarps = kLoadWarp + 4, kThreads = 32 * kWarps;
     static constexpr int N = 16 * RT;          // columns: per 8 rows, 8 high parts and 8 rests
     static constexpr int KPT = 128 / D;        // keys a thread (and a 128-byte row) holds
     static constexpr int TK = 128 * KPT;       // keys a tile
@@ -106,7 +106,7 @@ struct DecCfg {
     static constexpr int kGroupFloats = 3 * 8 + 4 * 8 + 8;  // mult, m, alpha [8]; red [4][8]; misc [8]
     static constexpr int kWalk = kFloat + RT * kGroupFloats * 4;  // the share's start, the scan's sums
     static constexpr int kBar = kWalk + 64 + 8 * kWarps;
-    static constexpr int kNumBars = 5 * kStages + 9;
+    static constexpr int kNumBars = 6 * kStages + 10;
     static constexpr int kSmemBytes = kBar + kNumBars * 8 + 16;
     static constexpr int kSCols = 4 * N, kOCols = N * KPT;
     static constexpr int kTmemCols = kSCols + kOCols <= 128 ? 128 : kSCols + kOCols <= 256 ? 256 : 512;
@@ -114,7 +114,7 @@ struct DecCfg {
 // P_READY is a barrier a buffer: a group may have tile n + 1's P written while another still works on tile n's, and its
 // arrival must not count for tile n.  (It reaches tile n + 2 only behind the product of tile n.)
 enum { D_S_FULL = 0, D_S_FREE, D_P_READY, D_P_READY1, D_PV_DONE, D_PV_DONE1, D_Q_READY, D_DONE, D_STAGES };
-// then K_FULL, K_FREE, V_FULL, V_FREE of the stages and X_FULL of the scales
+// then K_FULL, K_FREE, V_FULL, V_FREE of the stages and X_FULL, X_FREE of the scales
 
 __host__ __device__ inline int tile_keys(int d) { return 128 * (128 / d); }
 
@@ -228,7 +228,7 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     constexpr int RP = C::RP, N = C::N, KPT = C::KPT, TK = C::TK, ST = C::kStages;
     constexpr int kLoadWarp = C::kLoadWarp, kMmaWarp = C::kMmaWarp, kDecThreads = C::kThreads, kDecWarps = C::kWarps;
     constexpr int K_FULL = D_STAGES, K_FREE = K_FULL + ST, V_FULL = K_FREE + ST, V_FREE = V_FULL + ST,
-                  X_FULL = V_FREE + ST, XS = C::kScales;
+                  XS = C::kScales, X_FULL = V_FREE + ST, X_FREE = X_FULL + XS;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sb = smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -242,7 +242,7 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     const int64_t cap = a.max_pages << a.c.log2_page;
 
     if (tid == 0) {
-        for (int s = 0; s < 4 * ST + XS; ++s) mbar_init(BAR(D_STAGES + s), 1);
+        for (int s = 0; s < 4 * ST + 2 * XS; ++s) mbar_init(BAR(D_STAGES + s), 1);
         mbar_init(BAR(D_S_FULL), 1);
         mbar_init(BAR(D_S_FREE), 4 * RT);
         mbar_init(BAR(D_P_READY), 4 * RT);
@@ -328,14 +328,15 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     Walk w = start;
     if (!run) w.left = 0;
 
-    if (warp == kLoadWarp || warp == kLoadWarp + 1) {
-        // -------------------------------------------------------------------- loads: K with the scales, and V
-        const bool is_k = warp == kLoadWarp;
-        if (lane == 0) prefetch_tmap(is_k ? &tm_k : &tm_v);
+    if (warp >= kLoadWarp && warp < kMmaWarp) {
+        // -------------------------------------------------------------------- loads: K, V, scales
+        const int role = warp - kLoadWarp, depth = role == 2 ? XS : ST;
+        const CUtensorMap *map = role == 0 ? &tm_k : &tm_v;
+        if (lane == 0 && role < 2) prefetch_tmap(map);
         const int bt = min(1 << a.c.log2_page, TK), n_boxes = TK / bt;  // tokens a box: a page, or the tile's part of one
         const int in_page = (1 << a.c.log2_page) - 1;
-        const uint32_t dst = sb + (is_k ? 0 : C::kV) + lane * bt / KPT * 128;
-        const int full = is_k ? K_FULL : V_FULL, free = is_k ? K_FREE : V_FREE;
+        const uint32_t dst = sb + (role == 0 ? 0 : C::kV) + lane * bt / KPT * 128;
+        const int full = role == 0 ? K_FULL : role == 1 ? V_FULL : X_FULL, free = role == 0 ? K_FREE : role == 1 ? V_FREE : X_FREE;
         // the table's entry for this lane's box, asked for a tile ahead
         auto entry = [&](int t) -> int {
             const int key = t * TK + lane * bt;
@@ -360,34 +361,25 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 t = w.t0;
             }
             if (w.left > 0) next = entry(t);
-            const int st = n % ST, xs = n % XS;
-            if (n >= ST && !(ok = mbar_wait_warp(BAR(free + st), (n / ST - 1) & 1, kWaitLimitNs))) break;
-            // (K's stage was freed by the product of tile n - ST, which waited for the scores of the tile before that
-            // to be read, and so for its scales)
-            uint8_t *scale = smem + C::kScale + xs * C::kScaleBytes;
-            if (is_k && lane < C::NG) reinterpret_cast<int *>(scale + 768)[lane] = (boxes >> (lane * 16 / bt)) & 1u;
+            const int st = n % depth;
+            if (n >= depth && !(ok = mbar_wait_warp(BAR(free + st), (n / depth - 1) & 1, kWaitLimitNs))) break;
+            uint8_t *scale = smem + C::kScale + st * C::kScaleBytes;
+            if (role == 2 && lane < C::NG) reinterpret_cast<int *>(scale + 768)[lane] = (boxes >> (lane * 16 / bt)) & 1u;
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive_expect_tx(BAR(full + st), tokens * (D / 2));
-                if (is_k) mbar_arrive_expect_tx(BAR(X_FULL + xs), tokens * (D / 32 + 1));
-            }
+            if (lane == 0) mbar_arrive_expect_tx(BAR(full + st), tokens * (role == 2 ? D / 32 + 1 : D / 2));
             __syncwarp();
             // (rows of a box that is left out keep stale codes, as good as any: their weight is 0)
-            if (there) {
-                tma_load_4d(dst + st * C::kHalf, is_k ? &tm_k : &tm_v, BAR(full + st), 0, slot, h, page);
-                if (is_k) {
-                    const int64_t row = kv4_row(a.c, page, h, slot * KPT);
-                    bulk_load(smem_u32(scale) + lane * bt * (D / 32), a.c.k_scale + row * (D / 32), bt * (D / 32), BAR(X_FULL + xs));
-                    bulk_load(smem_u32(scale) + 512 + lane * bt, a.c.v_scale + row, bt, BAR(X_FULL + xs));
-                }
+            if (there && role < 2) tma_load_4d(dst + st * C::kHalf, map, BAR(full + st), 0, slot, h, page);
+            if (there && role == 2) {
+                const int64_t row = kv4_row(a.c, page, h, slot * KPT);
+                bulk_load(smem_u32(scale) + lane * bt * (D / 32), a.c.k_scale + row * (D / 32), bt * (D / 32), BAR(full + st));
+                bulk_load(smem_u32(scale) + 512 + lane * bt, a.c.v_scale + row, bt, BAR(full + st));
             }
         }
         if (!ok && lane == 0) kv4_timeout();
         // no copy in flight when the CTA ends
         const uint64_t lim = ok ? kWaitLimitNs : kCleanupLimitNs;
-        for (int i = n > ST ? n - ST : 0; i < n; ++i) mbar_wait(BAR(full + i % ST), (i / ST) & 1, lim);
-        if (is_k)
-            for (int i = n > XS ? n - XS : 0; i < n; ++i) mbar_wait(BAR(X_FULL + i % XS), (i / XS) & 1, lim);
+        for (int i = n > depth ? n - depth : 0; i < n; ++i) mbar_wait(BAR(full + i % depth), (i / depth) & 1, lim);
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------------- products
         constexpr uint32_t idS = idesc_e2m1_e4m3_f32(128, N, false, false);
@@ -428,6 +420,7 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                         mma_ss_f8_lohi(tS + i * N, k + i * 2, hi32(dA), lo32(dQ) + (D == 128 ? i : i & 1) * 2, hi32(dQ), idS, 0u);
                     mma_commit(BAR(D_S_FULL));
                     mma_commit(BAR(K_FREE + st));
+                    if (n > 0) mbar_arrive(BAR(X_FREE + (n - 1) % XS));  // (the scales were read before the scores)
                 }
                 __syncwarp();
                 if (t > w.t0 && !(ok = pv(n - 1, t - 1 == w.t0))) break;
