@@ -110,10 +110,10 @@ __device__ __forceinline__ uint32_t kv4_encode8(const uint32_t (&y)[4])
 __device__ __forceinline__ void kv4_wait_for_the_one_before() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 
 template <typename... P, typename... A>
-cudaError_t kv4_launch_behind(void (*kern)(P...), int64_t grid, int threads, cudaStream_t s, A... args)
+cudaError_t kv4_launch_behind(void (*kern)(P...), dim3 grid, int threads, cudaStream_t s, A... args)
 {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(static_cast<unsigned>(threads));
     cfg.stream = s;
     cudaLaunchAttribute attr = {};

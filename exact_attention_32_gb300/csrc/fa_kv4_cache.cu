@@ -449,7 +449,7 @@ cudaError_t fa_launch_kv4_evict(const Kv4EvictProblem &p, cudaStream_t stream)
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     auto *kern = p.from.d == 128 ? fa_kv4_move_kernel<128> : fa_kv4_move_kernel<64>;
-    return kv4_launch_behind(kern, row_grid(rows, p.from.d / 16, 2, p.sm_count, 64), 256, stream, p.from, p.to, p.table, p.max_pages,
+    return kv4_launch_behind(kern, dim3(row_grid(rows, p.from.d / 16, 2, p.sm_count, 64)), 256, stream, p.from, p.to, p.table, p.max_pages,
                              p.to_table, p.to_max_pages, p.kept, rows, static_cast<int>(p.keep));
 }
 

@@ -753,7 +753,8 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
 }
 
 // Merge of the items that lie in several shares: a block per CTA of the kernel before, for the item whose first part that
-// CTA holds; its warps over the item's rows and each row's parts.
+// CTA holds; its warps over the item's rows and each row's parts.  Where there are few items, and so many parts of each, a
+// block for every row of an item (gridDim.y).
 constexpr int kMergeWarps = 16;
 
 template <int D>
@@ -768,10 +769,12 @@ fa_kv4_merge_kernel(const DecodeArgs a, int RP)
     const Split sp = a.split[blockIdx.x];
     if (sp.parts == 0) return;
     auto slot = [&](int i) -> int64_t { return i == 0 ? sp.slot : (static_cast<int64_t>(blockIdx.x) + i) * 2; };
-    const int per_row = max(1, kMergeWarps / sp.n_rows);  // warps a row
-    for (int r0 = 0; r0 < sp.n_rows; r0 += kMergeWarps / per_row) {
+    const int rows = (sp.n_rows + gridDim.y - 1) / gridDim.y;  // of this block
+    const int row_end = min(sp.n_rows, static_cast<int>(blockIdx.y + 1) * rows);
+    const int per_row = max(1, kMergeWarps / rows);  // warps a row
+    for (int r0 = blockIdx.y * rows; r0 < row_end; r0 += kMergeWarps / per_row) {
         const int rr = r0 + warp / per_row, w = warp % per_row;
-        const bool live = rr < sp.n_rows;
+        const bool live = rr < row_end;
         float m = -FLT_MAX, l = 0.f, x[PER];
 #pragma unroll
         for (int i = 0; i < PER; ++i) x[i] = 0.f;
@@ -1026,15 +1029,19 @@ cudaError_t fa_launch_kv4_decode(const Kv4DecodeProblem &p, void *workspace, cud
         e = p.accumulate ? launch_rt<64, true>(a, g.rt, g.ctas, stream) : launch_rt<64, false>(a, g.rt, g.ctas, stream);
     if (e != cudaSuccess) return e;
     if (!g.whole && g.ctas > 1) {
-        e = p.cache.d == 128 ? kv4_launch_behind(fa_kv4_merge_kernel<128>, g.ctas, kMergeWarps * 32, stream, a, 8 * g.rt)
-                             : kv4_launch_behind(fa_kv4_merge_kernel<64>, g.ctas, kMergeWarps * 32, stream, a, 8 * g.rt);
+        // few items of many parts: 8 of 57 parts and 4 rows took 12.3 us with a block an item, 9.2 with one a row
+        const int64_t items = p.B * heads * g.n_rc;
+        const int rows = a.R < 8 * g.rt ? a.R : 8 * g.rt;
+        const dim3 grid(static_cast<unsigned>(g.ctas), items * 8 <= g.ctas ? rows : 1);
+        e = p.cache.d == 128 ? kv4_launch_behind(fa_kv4_merge_kernel<128>, grid, kMergeWarps * 32, stream, a, 8 * g.rt)
+                             : kv4_launch_behind(fa_kv4_merge_kernel<64>, grid, kMergeWarps * 32, stream, a, 8 * g.rt);
         if (e != cudaSuccess) return e;
     }
     if (p.accumulate) {
-        int64_t blocks = (cap + 511) / 512;
+        int64_t blocks = (cap + 511) / 512, most = 0x7fffffffLL / (p.B * heads);
         if (blocks > 512) blocks = 512;
-        if (blocks * p.B * heads > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-        e = kv4_launch_behind(fa_kv4_weights_kernel, blocks * p.B * heads, 256, stream, a, static_cast<int>(blocks));
+        if (blocks > most) blocks = most;  // (at least 1: the rows fit 31 bits)
+        e = kv4_launch_behind(fa_kv4_weights_kernel, dim3(static_cast<unsigned>(blocks * p.B * heads)), 256, stream, a, static_cast<int>(blocks));
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
