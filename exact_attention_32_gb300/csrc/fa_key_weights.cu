@@ -189,25 +189,24 @@ fa_key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const KwArgs a)
                 mbar_wait(BAR(KW_Q_FULL + i % kStages), (i / kStages) & 1, ok ? kWaitLimitNs : kCleanupLimitNs);
         }
     } else if (warp == kKwLse) {
-        // -LSE log2 e of each query; -inf (weight 0) for rows past N, whose scores the TMA's zeros make 0; +inf for those
-        // before first or without a key, whose scores may be anything: their blocks go through the guarded sum
+        // -LSE log2 e of each query; +inf for those past N, before first or without a key, which add nothing whatever their
+        // scores are (a NaN in them, or in the key): a block that has some goes through the guarded sum
         bool ok = true;
         for (int i = 0; i < nq && ok; ++i, walk.next()) {
-            const int st = i % kStages;
+            const int st = i % kStages, q0 = walk.qb * kQBlock;
             if (i >= kStages && !(ok = mbar_wait_warp(BAR(KW_LSE_FREE + st), (i / kStages - 1) & 1, kWaitLimitNs))) break;
-            const int q0 = walk.qb * kQBlock;
             const float *src = a.lse + static_cast<int64_t>(walk.qh) * a.N;
-            float *dst = reinterpret_cast<float *>(smem + C::kLse) + st * kQBlock;
-            bool out = false;
             float x[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) x[j] = src[min(q0 + j * 32 + lane, a.N - 1)];  // (without branches: the loads go out together)
+            float *dst = reinterpret_cast<float *>(smem + C::kLse) + st * kQBlock;
+            bool out = false;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int q = q0 + j * 32 + lane;
-                if (q < a.first) x[j] = -INFINITY;
+                if (q < a.first || q >= a.N) x[j] = -INFINITY;
                 out |= x[j] == -INFINITY;
-                dst[j * 32 + lane] = q < a.N ? x[j] * -1.4426950408889634f : -INFINITY;
+                dst[j * 32 + lane] = x[j] * -1.4426950408889634f;
             }
             out = __any_sync(0xffffffffu, out);
             if (lane == 0) reinterpret_cast<int *>(smem + C::kOut)[st] = out;
@@ -280,11 +279,9 @@ fa_key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const KwArgs a)
         for (int i = 0; i < nq && ok; ++i, walk.next()) {
             const int st = i % kStages, n = 2 * i + w, buf = n % kBufs;
             const int q0 = walk.qb * kQBlock;
-            if (!mbar_wait_warp(BAR(KW_LSE_FULL + st), (i / kStages) & 1, kWaitLimitNs) ||
-                !mbar_wait_warp(BAR(KW_S_FULL + kw_slot(n)), (n / 6) & 1, kWaitLimitNs)) {
-                ok = false;
-                break;
-            }
+            if (!(ok = mbar_wait_warp(BAR(KW_LSE_FULL + st), (i / kStages) & 1, kWaitLimitNs))) break;
+            const bool out = reinterpret_cast<volatile int *>(smem + C::kOut)[st] != 0;
+            if (!(ok = mbar_wait_warp(BAR(KW_S_FULL + kw_slot(n)), (n / 6) & 1, kWaitLimitNs))) break;
             tc_fence_after();
             const float *ls = reinterpret_cast<const float *>(smem + C::kLse) + st * kQBlock + half * 64;
             const uint32_t src = tS + buf * 128 + loff + half * 64;
@@ -324,7 +321,6 @@ fa_key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const KwArgs a)
                 if (lane == 0) mbar_arrive(BAR(KW_S_FREE + kw_slot(n)));
                 take(x1, 1, guard);
             };
-            const bool out = reinterpret_cast<volatile int *>(smem + C::kOut)[st] != 0;
             if ((CAUSAL && q0 < k0 + w * kKeyTile + kKeyTile - 1) || out)
                 tile(std::true_type{});
             else

@@ -630,6 +630,24 @@ def test_key_weights_of_queries_left_out_may_hold_anything(H, Hkv, N, first, cau
 
 
 @gpu
+@pytest.mark.parametrize("N,real", [(300, 171), (384, 256), (129, 1)])
+def test_key_weights_of_a_padded_prompt(N, real):
+    # keys and queries past the prompt's end hold NaN, and those queries no LSE: their keys weigh nothing, the others as before
+    g = torch.Generator().manual_seed(N)
+    q, k = torch.randn(1, 4, N, 128, generator=g).bfloat16(), torch.randn(1, 2, N, 128, generator=g).bfloat16()
+    short = dev(_lse(f64(q[:, :, :real]), f64(k[:, :, :real]), fa.default_scale(128), True))
+    w = fa.key_weights(q[:, :, :real].contiguous().cuda(), k[:, :, :real].contiguous().cuda(), short, causal=True)
+    lse = torch.full((1, 4, N), -np.inf, device="cuda")
+    lse[:, :, :real] = short
+    q[:, :, real:], k[:, :, real:] = float("nan"), float("nan")
+    w2 = fa.key_weights(q.cuda(), k.cuda(), lse, causal=True)
+    ok()
+    assert (w2[:, :, real:] == 0).all()
+    # the same terms, added in blocks that may differ: N roundings of at most 2^-24 of the sum on either side
+    assert ((w2[:, :, :real] - w).abs() <= w * 2 * N * 2 * 2.0 ** -24).all()
+
+
+@gpu
 def test_key_weights_sum_to_the_number_of_queries():
     # from the forward's own LSE: the columns of a softmax matrix add up to its rows
     q, k, v = (t.cuda() for t in fa.make_inputs(1, 4, 3000, 128, seed=3))
@@ -765,6 +783,32 @@ def test_groups_of_rows_run_apart_and_agree(d, G, n_q):
     ok()
     check_attention(pool, q, lens, fa.default_scale(d), o, lse, pool.w, f64(c.weights))
     assert all(torch.equal(o, x) and torch.equal(lse, y) for x, y in runs)
+
+
+@gpu
+def test_calls_on_several_streams_at_once():
+    # attention with different groupings, key weights, an append and an eviction side by side: each as it is alone
+    lens = np.array([2500, 60, 700], np.int32)
+    pools = [Pool(3, 2, d, 32, lens, seed=91 + i) for i, d in enumerate((128, 128, 64))]
+    g = torch.Generator().manual_seed(7)
+    rnd = lambda *s: torch.randn(s, generator=g).bfloat16().cuda()  # noqa: E731
+    qs = [rnd(3, 2 * G, 1, p.d) for p, G in zip(pools, (4, 12, 24))]
+    qw, kw, lse = rnd(1, 8, 1000, 128), rnd(1, 2, 1000, 128), torch.full((1, 8, 1000), 7.0, device="cuda")
+    n, caches, tables = dev(lens), [p.cache() for p in pools], [dev(p.table) for p in pools]
+    other = fa.kv4_cache(40, 2, 32, 128)
+    to = torch.arange(30, dtype=torch.int32, device="cuda").view(3, 10)
+    jobs = [lambda s, i=i: fa.forward_kv4(qs[i], caches[i], n, tables[i], stream=s) for i in range(3)]
+    jobs += [lambda s: (fa.key_weights(qw, kw, lse, causal=True, stream=s),),
+             lambda s: fa.kv4_evict(caches[0], n, tables[0], other, to, 300, recent=20, stream=s)]
+    alone = [job(None) for job in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _ in range(5):
+        outs = [job(s) for job, s in zip(jobs, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(alone, outs):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+    ok()
 
 
 @gpu
