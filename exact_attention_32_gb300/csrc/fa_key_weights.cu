@@ -10,17 +10,20 @@
 // TMEM lane, so a thread owns a key: it takes exp2(S scale log2e - LSE log2e) of 128
 // queries and adds them up in fp32, with nothing to exchange between threads.
 //
-// What bounds it is the tensor pipe (2 d operations per pair; the exponentials
-// take half the time).  A product whose operands both come from shared memory
+// What bounds it: at d = 128 a tile's product and its 16384 exponentials (32 a clock and SM) take 512 cycles each, side by
+// side, at d = 64 the product half of that.  32 heads of 16384 queries, causal, take 800 us (1.38 PFLOP/s, 71 % of the
+// measured bf16 rate), and with an eighth of the exponentials still 630 to 690.
+// A product whose operands both come from shared memory
 // at N = 128 would need all of its 128 bytes a clock, so K lies in tensor memory
 // as the A operand (2 x d/2 columns, for the CTA's life) and only Q streams
 // through shared memory (TMA, 128-byte swizzle, four stages); a Q block is used for
 // both key tiles.  The other columns hold three 128 x 128 accumulators in turn,
 // so the pipe runs on while the warpgroups read theirs.
 // Roles (608 threads): warps 0-15 four warpgroups, two per key tile, each with half of a
-// block's queries (with one per tile a warpgroup's waits between its steps left the
-// tensor pipe idle: 829 us in place of XXX for 32 heads of 16384 queries, causal); warp 16
-// loads Q, warp 17 issues the products and owns the tensor memory, warp 18 loads LSE log2 e.
+// block's queries (one per tile took 831 us, two 842, both with the products issued by lane 0); warp 16 loads Q, warp 17
+// issues the products, from an elected lane (829 -> 774 us), and owns the tensor memory, warp 18 loads LSE log2 e.
+// Measured and not kept, against 774: exp2 by a polynomial for a share of the scores; the two warpgroups of a tile in
+// turns (900); two issuing warps (774); an accumulator given back before its scores are used (823).
 //
 // Every mbarrier wait is bounded; one that gives up sets FA_ERR_TIMEOUT in this
 // file's status word and the CTA winds down.

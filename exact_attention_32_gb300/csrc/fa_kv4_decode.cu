@@ -28,12 +28,18 @@
 // takes its share as segments of items.  A segment that is a whole item is finished in
 // place; the others leave (m, l, O) in the workspace, which a second kernel merges
 // (O = sum 2^(m_s - m) O_s / sum 2^(m_s - m) l_s).
-// Roles: a softmax warpgroup per 8 rows (1, 2 or 4), one thread a TMEM lane; a warp that loads, a lane a page (or the
-// part of a page in the tile); a warp that issues the products.  A softmax takes about 2000 cycles a tile, waits between
+// Roles: a softmax warpgroup per 8 rows (1, 2 or 4), one thread a TMEM lane; three warps that load (K, V, the scales), a lane
+// a page (or the part of a page in the tile); a warp that issues the products.  A copy takes its warp 77 cycles to issue,
+// so one warp for all copies was too slow where pages are small (32 sequences of 8192 in pages of 16: 86 us, two warps 70,
+// three 65; in pages of 1024 58).  A softmax takes about 2000 cycles a tile, waits between
 // its steps for the most part, so an SM needs several at work to keep up with the 720 cycles that a tile's bytes
 // take: three CTAs of 8 rows, two of 16, one of 32.  K and V have stages of their own, K's free as soon as S is there.
+// What a softmax needs to begin, K and the scales, comes ahead of V, which it needs at its end: with the scales behind V's
+// barrier 64 sequences of 16384 (8 key heads, 8 rows each, 1.12 GB) took 208 us, so 188, 5.9 TB/s (the copies alone 6.9).
 // Copies of 8 bytes a lane by the load warps (cp.async) in the TMA's place took 3500 cycles
-// to issue a tile, two and a half times what all of the tile may take.
+// to issue a tile, two and a half times what all of the tile may take; TMA copies from an elected lane, box by box, more
+// than those of several lanes in one instruction (pages of 16: 102 us against 87).  Softmax code for 4 rows instead of 8, where
+// no more are live, gained 1 to 2 % only: its time is latency.
 #include <cuda.h>
 #include <float.h>
 #include <math.h>

@@ -460,8 +460,9 @@ int fa_kv4_read(const fa_kv4_cache *cache, const int32_t *first, const int32_t *
  *         fa_fwd_kv4_workspace_bytes(...) bytes; contents on entry do not
  *         matter.  Calls that share one must be ordered on one stream (or by
  *         events): two that overlap race on it.
- * Keys are read once per 32 rows of a key head; the split of a sequence's keys
- * depends on the sizes alone, and so do the results, bit for bit.
+ * Keys are read once per 32 rows of a key head.  The batch's keys are shared out among
+ * the SMs evenly, so where a sequence is split, and with it the last bits of its rows,
+ * depends on the lengths of the whole batch; the same call gives the same bits.
  */
 int fa_fwd_kv4(const void *q, const fa_kv4_cache *cache, const int32_t *lens, const int32_t *page_table,
                void *o, float *lse, int64_t B, int64_t H, int64_t n_q, int64_t max_pages, float scale,
