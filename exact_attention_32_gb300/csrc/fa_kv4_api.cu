@@ -9,7 +9,8 @@
 
 namespace {
 
-constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 256;
+// Tokens of a sequence: positions, and what loops over them step beyond (up to 2^18), fit 31 bits.
+constexpr int64_t kMaxTokens = (int64_t(1) << 31) - (1 << 20);
 
 int check_cache_sizes(const fa_kv4_cache *c)
 {

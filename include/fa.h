@@ -406,6 +406,7 @@ int64_t fa_bwd_workspace_bytes(int64_t B, int64_t H, int64_t N, int64_t d);
  * outside [0, max_pages * page_size], cannot be refused by the host: the kernels
  * leave such a page's tokens out, hold the length to the range, and report
  * FA_ERR_BAD_PAGE through fa_get_device_status (later calls run as usual).
+ * max_pages * page_size is at most 2^31 - 2^20.
  * Several sequences may share pages that are only read.  A page that a call writes
  * (append, evict's destination, weights under accumulate) must appear once.
  */

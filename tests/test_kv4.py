@@ -165,6 +165,14 @@ def test_bad_arguments_are_refused_before_any_device_call():
     assert fa.fa_key_weights(p, p, p, p, 1, 2, 2, 8, 96, 0.1, 0, 0, 0) == 2
 
 
+def test_capacities_that_pass_31_bits_are_refused():
+    c, x = _struct(d=64, Hkv=1, page_size=1024), 1 << 20
+    for pages in (1 << 21, (1 << 21) - 1023):
+        assert fa.fa_kv4_read(c, 0, x, x, 1, pages, 1, x, x, 0) == 1
+    assert fa.fa_fwd_kv4_workspace_bytes(1, 1, 1, 1, 64, (1 << 31) - (1 << 20), 0) > 0
+    assert fa.fa_fwd_kv4_workspace_bytes(1, 1, 1, 1, 64, (1 << 31) - (1 << 20) + 1, 0) == -1
+
+
 def test_workspace_bytes():
     f = fa.fa_fwd_kv4_workspace_bytes
     assert f(1, 8, 2, 1, 96, 64, 0) == -1 and f(1, 7, 2, 1, 64, 64, 0) == -1 and f(1, 8, 2, 0, 64, 64, 0) == -1
@@ -392,6 +400,22 @@ def test_attention_over_many_sequences(d, P, B, n_q, stored):
     lens[::37], lens[5], lens[B - 1] = 0, stored, stored - 1
     pool = Pool(B, 1, d, P, lens, seed=B)
     q = bf16(rng.standard_normal((B, 3, n_q, d))).cuda()
+    c = pool.cache()
+    o, lse = fa.forward_kv4(q, c, dev(lens), dev(pool.table), accumulate=True)
+    ok()
+    check_attention(pool, q, lens, fa.default_scale(d), o, lse, pool.w, f64(c.weights))
+
+
+@gpu
+@pytest.mark.parametrize("d,P,Hkv,G,n_q,lens", [(128, 1024, 1, 2, 1, [1024, 0, 1023]), (64, 16, 2, 4, 2, [640, 640, 1]),
+                                                (64, 1024, 1, 1, 3, [4096, 4095, 2]), (128, 16, 1, 16, 64, [640, 63, 64]),
+                                                (64, 16, 1, 1024, 1, [700, 32, 5]), (128, 128, 1, 33, 1, [1280, 129, 1])])
+def test_attention_over_full_tables_and_many_rows(d, P, Hkv, G, n_q, lens):
+    # sequences as long as the table allows, and up to 1024 rows a key head
+    lens = np.array(lens, np.int32)
+    pool = Pool(len(lens), Hkv, d, P, lens, seed=P + G)
+    pool.table = np.ascontiguousarray(pool.table[:, :-(-int(lens.max()) // P)])
+    q = bf16(np.random.default_rng(G).standard_normal((len(lens), Hkv * G, n_q, d))).cuda()
     c = pool.cache()
     o, lse = fa.forward_kv4(q, c, dev(lens), dev(pool.table), accumulate=True)
     ok()
@@ -748,6 +772,38 @@ def test_captured_step_replays_with_new_lengths():
         torch.cuda.synchronize()
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
         assert all(torch.equal(a, b) for a, b in zip(c, plain))
+    ok()
+
+
+@gpu
+def test_captured_prompt_and_eviction_replay_with_new_values():
+    # key weights, append, eviction and reading back in one graph, replayed with other inputs in the same places
+    g = torch.Generator().manual_seed(55)
+    rnd = lambda *s: torch.randn(s, generator=g).bfloat16().cuda()  # noqa: E731
+    B, H, Hkv, N, d, P, keep = 2, 4, 2, 300, 64, 32, 100
+    q, k, v = rnd(B, H, N, d), rnd(B, Hkv, N, d), rnd(B, Hkv, N, d)
+    lse, lens = torch.full((B, H, N), 6.0, device="cuda"), torch.tensor([300, 170], dtype=torch.int32, device="cuda")
+    order = torch.randperm(40, generator=g).to(torch.int32).cuda()
+    table, to = order[:20].view(2, 10).contiguous(), order[20:28].view(2, 4).contiguous()
+
+    def work(cache):
+        w = fa.key_weights(q, k, lse, causal=True)
+        fa.kv4_append(cache, k, v, lens, table, n_new=lens, weights=w)
+        kept, now = fa.kv4_evict(cache, lens, table, cache, to, keep, recent=9)
+        return (kept, now, *fa.kv4_read(cache, now, to, keep))
+
+    work(fa.kv4_cache(40, Hkv, P, d))
+    torch.cuda.synchronize()
+    cache, graph = fa.kv4_cache(40, Hkv, P, d), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = work(cache)
+    for turn in range(3):
+        for t in (q, k, v):
+            t.copy_(rnd(*t.shape))
+        lens.copy_(torch.tensor([300 - 90 * turn, 101 + turn], dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, work(fa.kv4_cache(40, Hkv, P, d))))
     ok()
 
 
