@@ -852,52 +852,77 @@ fa_kv4_merge_kernel(const DecodeArgs a, int RP)
     }
 }
 
-// weights[key] += sum over the rows of exp2(score - m) / l: a thread has two keys under way.
+// weights[key] += sum over the rows of exp2(score - m) / l.  Memory-bound by the scores, 4 Rs bytes a key.  L lanes read a key's
+// rows, 4 C each (C = 0: one or two rows, a thread a key), and add them up; a warp has 32 U keys under way, 32 / L a turn, and
+// each lane ends with the sums of U of them.  A thread a key is as fast up to 12 rows (24 sequences of 8 key heads with 12 rows: the
+// whole call 68 us, with four lanes 70), but reads 16 bytes of a line at a time: with 32 rows 52 us for 67 MB of scores where
+// eight lanes take 20; with 16 the whole call 63 us, with four lanes 59.
+template <int L, int C, int U>
 __global__ void __launch_bounds__(256)
 fa_kv4_weights_kernel(const DecodeArgs a, int blocks)
 {
+    constexpr int KEYS = 32 / L, CC = C == 0 ? 1 : C;  // keys of a turn
     const int64_t bh = blockIdx.x / blocks, b = bh / a.c.heads;
-    const int h = static_cast<int>(bh - b * a.c.heads);
+    const int h = static_cast<int>(bh - b * a.c.heads), lane = threadIdx.x & 31, sub = lane % L;
     const int64_t cap = a.max_pages << a.c.log2_page;
     const int len = kv4_length(a.lens, b, cap);
     kv4_wait_for_the_one_before();
     const float2 *ml = a.row_ml + bh * a.R;
-    for (int key0 = blockIdx.x % blocks * 512 + threadIdx.x; key0 < len; key0 += blocks * 512) {
-        const int n = key0 + 256 < len ? 2 : 1;
-        float w[2] = {0.f, 0.f}, old[2];
-        int64_t row[2];
+    for (int key0 = blockIdx.x % blocks * 256 * U + (threadIdx.x & ~31); key0 < len; key0 += blocks * 256 * U) {
+        int64_t row[U];
+        float old[U], v[U][L][CC][4];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int key = u < n ? key0 + 256 * u : key0;
+        for (int u = 0; u < U; ++u) {
+            const int own = key0 + u * 256 + sub * KEYS + lane / L;  // the key whose sum this lane takes
             bool valid;
-            const int page = kv4_page_quiet(a.c, a.table, b, a.max_pages, key, &valid);
-            row[u] = kv4_row(a.c, page, h, key);
+            const int page = kv4_page_quiet(a.c, a.table, b, a.max_pages, min(own, len - 1), &valid);
+            row[u] = kv4_row(a.c, page, h, min(own, len - 1));
             old[u] = a.c.weights[row[u]];
-            if (!valid || u >= n) row[u] = -1;  // (a bad page is reported by the kernel before)
+            if (!valid || own >= len) row[u] = -1;  // (a bad page is reported by the kernel before)
         }
-        const float *s0 = a.scores + (bh * cap + key0) * a.Rs, *s1 = n == 2 ? s0 + 256 * a.Rs : s0;
-        if (a.R <= 2) {
-            for (int r = 0; r < a.R; ++r) {
-                w[0] = fmaf(ex2(s0[r] - ml[r].x), ml[r].y, w[0]);
-                w[1] = fmaf(ex2(s1[r] - ml[r].x), ml[r].y, w[1]);
-            }
-        } else {
-#pragma unroll 3
-            for (int r = 0; r < a.R; r += 4) {
-                const float4 v0 = *reinterpret_cast<const float4 *>(s0 + r), v1 = *reinterpret_cast<const float4 *>(s1 + r);
-                const float y0[4] = {v0.x, v0.y, v0.z, v0.w}, y1[4] = {v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (r + i >= a.R) break;
-                    const float2 p = ml[r + i];
-                    w[0] = fmaf(ex2(y0[i] - p.x), p.y, w[0]);
-                    w[1] = fmaf(ex2(y1[i] - p.x), p.y, w[1]);
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < L; ++i) {
+                const int key = min(key0 + u * 256 + i * KEYS + lane / L, len - 1);
+                const float *s = a.scores + (bh * cap + key) * a.Rs;
+                if constexpr (C == 0) {
+                    v[u][i][0][0] = s[0];
+                    v[u][i][0][1] = a.R == 2 ? s[1] : 0.f;
+                    v[u][i][0][2] = v[u][i][0][3] = 0.f;
+                } else {
+#pragma unroll
+                    for (int c = 0; c < CC; ++c)
+                        *reinterpret_cast<float4 *>(v[u][i][c]) = *reinterpret_cast<const float4 *>(s + min(4 * (sub + c * L), a.Rs - 4));
                 }
             }
-        }
+        float mine[U];
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-            if (row[u] >= 0) a.c.weights[row[u]] = old[u] + w[u];
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < L; ++i) {
+                float w = 0.f;
+#pragma unroll
+                for (int c = 0; c < CC; ++c)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int r = 4 * (sub + c * L) + j;
+                        if (r >= a.R) continue;  // (what lies behind the last row may be anything)
+                        const float2 p = ml[r];
+                        w = fmaf(ex2(v[u][i][c][j] - p.x), p.y, w);
+                    }
+                if constexpr (L == 8) {  // more than 32 rows
+                    const float *s = a.scores + (bh * cap + min(key0 + u * 256 + i * KEYS + lane / L, len - 1)) * a.Rs;
+                    for (int r0 = 4 * (CC * L + sub); r0 < a.R; r0 += 4 * L)
+                        for (int r = r0; r < r0 + 4 && r < a.R; ++r) w = fmaf(ex2(s[r] - ml[r].x), ml[r].y, w);
+                }
+#pragma unroll
+                for (int o = 1; o < L; o <<= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+                if (sub == i) mine[u] = w;
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (row[u] >= 0) a.c.weights[row[u]] = old[u] + mine[u];
     }
 }
 
@@ -912,7 +937,7 @@ Geometry geometry(int64_t B, int64_t H, int64_t heads, int64_t n_q, int64_t d, i
 {
     Geometry g;
     const int64_t R = H / heads * n_q, rows = B * H * n_q;
-    g.rt = R <= 8 ? 1 : R <= 16 ? 2 : 4;
+    g.rt = R <= 8 ? 1 : R <= 16 ? 2 : 4;  // (32 rows of 32 sequences of 8192: 78 us in one CTA, in two of 16 rows 85)
     g.n_rc = static_cast<int>((R + 8 * g.rt - 1) / (8 * g.rt));
     const int64_t tk = tile_keys(static_cast<int>(d));
     const int64_t items = B * heads * g.n_rc, tiles = (max_tokens + tk - 1) / tk;
@@ -1047,7 +1072,10 @@ cudaError_t fa_launch_kv4_decode(const Kv4DecodeProblem &p, void *workspace, cud
         int64_t blocks = (cap + 511) / 512, most = 0x7fffffffLL / (p.B * heads);
         if (blocks > 512) blocks = 512;
         if (blocks > most) blocks = most;  // (at least 1: the rows fit 31 bits)
-        e = kv4_launch_behind(fa_kv4_weights_kernel, dim3(static_cast<unsigned>(blocks * p.B * heads)), 256, stream, a, static_cast<int>(blocks));
+        auto *kern = a.R <= 2 ? fa_kv4_weights_kernel<1, 0, 2> : a.Rs <= 4 ? fa_kv4_weights_kernel<1, 1, 2>
+                     : a.Rs <= 8 ? fa_kv4_weights_kernel<1, 2, 2> : a.Rs <= 12 ? fa_kv4_weights_kernel<1, 3, 2>
+                     : a.Rs <= 16 ? fa_kv4_weights_kernel<4, 1, 1> : fa_kv4_weights_kernel<8, 1, 1>;
+        e = kv4_launch_behind(kern, dim3(static_cast<unsigned>(blocks * p.B * heads)), 256, stream, a, static_cast<int>(blocks));
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

@@ -409,7 +409,7 @@ def test_attention_over_many_sequences(d, P, B, n_q, stored):
 @gpu
 @pytest.mark.parametrize("d,P,Hkv,G,n_q,lens", [(128, 1024, 1, 2, 1, [1024, 0, 1023]), (64, 16, 2, 4, 2, [640, 640, 1]),
                                                 (64, 1024, 1, 1, 3, [4096, 4095, 2]), (128, 16, 1, 16, 64, [640, 63, 64]),
-                                                (64, 16, 1, 1024, 1, [700, 32, 5]), (128, 128, 1, 33, 1, [1280, 129, 1])])
+                                                (64, 16, 1, 1024, 1, [700, 32, 5]), (128, 16, 2, 2, 1, [640, 333, 1]), (64, 32, 1, 20, 1, [640, 333, 1]), (128, 128, 1, 33, 1, [1280, 129, 1])])
 def test_attention_over_full_tables_and_many_rows(d, P, Hkv, G, n_q, lens):
     # sequences as long as the table allows, and up to 1024 rows a key head
     lens = np.array(lens, np.int32)
