@@ -366,6 +366,34 @@ fa_key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const KwArgs a)
     }
 }
 
+// CTAs a key block (1, 2, 4 or 8): those with the shortest time by the longest CTA, the SMs' share of all query blocks, and
+// what a CTA costs besides (8 blocks' time: 7.5 us, from launch to the last sum).  Only where the key blocks do not fill the SMs:
+// 5 key heads of 5414 keys, 20 of queries, causal: 110 CTAs 154 us, 220 84, 440 85, 880 126; 2 key heads of 6281, 16 of queries from 3140
+// on: 50 CTAs 188 us, 100 101, 200 70, 400 85; 32 of 700, d = 64, 96 CTAs 27, 192 33.
+int fewest_rounds(const KwArgs &a, int64_t units, int64_t G, bool causal, int sm_count)
+{
+    if (units >= sm_count) return 1;
+    const int64_t b0 = a.first / kQBlock;
+    int64_t all = 0;  // query blocks of a (b, key head)
+    for (int64_t kb = 0; kb < a.n_kblocks; ++kb) {
+        const int64_t from = kb * (kKeys / kQBlock);
+        all += (a.n_qblocks - (causal && from > b0 ? from : b0)) * G;
+    }
+    const int64_t longest = (a.n_qblocks - b0) * G, total = all * (units / a.n_kblocks);
+    int best = 1;
+    int64_t best_time = 0;
+    for (int r = 1; r <= kMaxRanks && (r == 1 || longest >= 2 * r); r *= 2) {
+        const int64_t rounds = (units * r + sm_count - 1) / sm_count, own = (longest + r - 1) / r;
+        const int64_t shared = causal ? total / sm_count : rounds * own;
+        const int64_t time = 8 * rounds + (own > shared ? own : shared);
+        if (r == 1 || time < best_time) {
+            best = r;
+            best_time = time;
+        }
+    }
+    return best;
+}
+
 template <int D, bool CAUSAL>
 cudaError_t launch_kw(const FaKeyWeightsProblem &p, cudaStream_t s)
 {
@@ -385,10 +413,8 @@ cudaError_t launch_kw(const FaKeyWeightsProblem &p, cudaStream_t s)
     a.n_qblocks = static_cast<int>((p.N + kQBlock - 1) / kQBlock);
     a.first = static_cast<int>(p.first_query);
     a.scale_log2 = static_cast<float>(static_cast<double>(p.scale) * 1.4426950408889634);
-    // ranks a key block: as many (1, 2, 4 or 8) as leave every rank two query blocks and the SMs not more than full
-    const int64_t units = p.B * p.Hkv * a.n_kblocks, blocks = (p.H / p.Hkv) * (a.n_qblocks - a.first / kQBlock);
-    a.ranks = 1;
-    while (a.ranks < kMaxRanks && units * a.ranks * 2 <= p.sm_count && blocks >= a.ranks * 4) a.ranks *= 2;
+    const int64_t units = p.B * p.Hkv * a.n_kblocks;
+    a.ranks = fewest_rounds(a, units, p.H / p.Hkv, CAUSAL, p.sm_count);
     const int64_t grid = units * a.ranks;
     if (grid > 0x7fffffffLL || p.B * p.H > 0x7fffffffLL || (p.H / p.Hkv) * a.n_qblocks > 0x3fffffffLL)
         return cudaErrorInvalidConfiguration;
