@@ -911,10 +911,18 @@ fa_kv4_weights_kernel(const DecodeArgs a, int blocks)
                         const float2 p = ml[r];
                         w = fmaf(ex2(v[u][i][c][j] - p.x), p.y, w);
                     }
-                if constexpr (L == 8) {  // more than 32 rows
+                if constexpr (L * C == 16) {  // more than 64 rows
                     const float *s = a.scores + (bh * cap + min(key0 + u * 256 + i * KEYS + lane / L, len - 1)) * a.Rs;
-                    for (int r0 = 4 * (CC * L + sub); r0 < a.R; r0 += 4 * L)
-                        for (int r = r0; r < r0 + 4 && r < a.R; ++r) w = fmaf(ex2(s[r] - ml[r].x), ml[r].y, w);
+                    for (int r0 = 4 * (C * L + sub); r0 < a.R; r0 += 4 * L) {
+                        const float4 f = *reinterpret_cast<const float4 *>(s + r0);
+                        const float y[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            if (r0 + j >= a.R) break;
+                            const float2 p = ml[r0 + j];
+                            w = fmaf(ex2(y[j] - p.x), p.y, w);
+                        }
+                    }
                 }
 #pragma unroll
                 for (int o = 1; o < L; o <<= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
@@ -937,7 +945,9 @@ Geometry geometry(int64_t B, int64_t H, int64_t heads, int64_t n_q, int64_t d, i
 {
     Geometry g;
     const int64_t R = H / heads * n_q, rows = B * H * n_q;
-    g.rt = R <= 8 ? 1 : R <= 16 ? 2 : 4;  // (32 rows of 32 sequences of 8192: 78 us in one CTA, in two of 16 rows 85)
+    // 16 rows of 32 sequences of 8192 (4 key heads) take 37 to 42 us, 32 rows 69 to 78: 32 rows in one CTA 78, in two of 16 85;
+    // 40 rows in two of 32 136, in three of 16 116; 80 rows 197 and 183
+    g.rt = R <= 8 ? 1 : R <= 16 || (R + 15) / 16 * 7 < (R + 31) / 32 * 13 ? 2 : 4;
     g.n_rc = static_cast<int>((R + 8 * g.rt - 1) / (8 * g.rt));
     const int64_t tk = tile_keys(static_cast<int>(d));
     const int64_t items = B * heads * g.n_rc, tiles = (max_tokens + tk - 1) / tk;
@@ -1074,7 +1084,8 @@ cudaError_t fa_launch_kv4_decode(const Kv4DecodeProblem &p, void *workspace, cud
         if (blocks > most) blocks = most;  // (at least 1: the rows fit 31 bits)
         auto *kern = a.R <= 2 ? fa_kv4_weights_kernel<1, 0, 2> : a.Rs <= 4 ? fa_kv4_weights_kernel<1, 1, 2>
                      : a.Rs <= 8 ? fa_kv4_weights_kernel<1, 2, 2> : a.Rs <= 12 ? fa_kv4_weights_kernel<1, 3, 2>
-                     : a.Rs <= 16 ? fa_kv4_weights_kernel<4, 1, 1> : fa_kv4_weights_kernel<8, 1, 1>;
+                     : a.Rs <= 16 ? fa_kv4_weights_kernel<4, 1, 1> : a.Rs <= 32 ? fa_kv4_weights_kernel<8, 1, 1>
+                     : a.Rs <= 48 ? fa_kv4_weights_kernel<4, 3, 1> : fa_kv4_weights_kernel<8, 2, 1>;
         e = kv4_launch_behind(kern, dim3(static_cast<unsigned>(blocks * p.B * heads)), 256, stream, a, static_cast<int>(blocks));
         if (e != cudaSuccess) return e;
     }
