@@ -282,26 +282,31 @@ fa_key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const KwArgs a)
         for (int i = 0; i < nq && ok; ++i, walk.next()) {
             const int st = i % kStages, n = 2 * i + w, buf = n % kBufs;
             const int q0 = walk.qb * kQBlock;
-            if (!(ok = mbar_wait_warp(BAR(KW_LSE_FULL + st), (i / kStages) & 1, kWaitLimitNs))) break;
+            {
+                const uint32_t b0 = BAR(KW_LSE_FULL + st), b1 = BAR(KW_S_FULL + kw_slot(n)), f0 = (i / kStages) & 1, f1 = (n / 6) & 1;
+                const bool there0 = mbar_try_wait(b0, f0), there1 = mbar_try_wait(b1, f1);  // (one vote where both are)
+                if (!__all_sync(0xffffffffu, there0 && there1) &&
+                    !(ok = mbar_wait_warp(b0, f0, kWaitLimitNs) && mbar_wait_warp(b1, f1, kWaitLimitNs)))
+                    break;
+            }
             const bool out = reinterpret_cast<volatile int *>(smem + C::kOut)[st] != 0;
-            if (!(ok = mbar_wait_warp(BAR(KW_S_FULL + kw_slot(n)), (n / 6) & 1, kWaitLimitNs))) break;
             tc_fence_after();
             const float *ls = reinterpret_cast<const float *>(smem + C::kLse) + st * kQBlock + half * 64;
             const uint32_t src = tS + buf * 128 + loff + half * 64;
-            // 32 queries of this key: their scores in x, their sum added to s0, s1 (the tile's sums in registers of
+            // 16 queries of this key: their scores in x, their sum added to s0, s1 (the tile's sums in registers of
             // their own first: 64 terms, then one addition to the total)
             float2 s0 = make_float2(0.f, 0.f), s1 = s0;
-            auto take = [&](const uint32_t (&x)[32], int c, auto guard) {
+            auto take = [&](const uint32_t (&x)[16], int c, auto guard) {
 #pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                    const float4 l = *reinterpret_cast<const float4 *>(ls + c * 32 + j);
+                for (int j = 0; j < 16; j += 4) {
+                    const float4 l = *reinterpret_cast<const float4 *>(ls + c * 16 + j);
                     const float2 y0 = fma2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), sc,
                                            make_float2(l.x, l.y));
                     const float2 y1 = fma2(make_float2(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3])), sc,
                                            make_float2(l.z, l.w));
                     float2 p0 = make_float2(ex2(y0.x), ex2(y0.y)), p1 = make_float2(ex2(y1.x), ex2(y1.y));
                     if constexpr (decltype(guard)::value) {
-                        const int q = CAUSAL ? q0 + half * 64 + c * 32 + j : key;
+                        const int q = CAUSAL ? q0 + half * 64 + c * 16 + j : key;
                         if (key > q || l.x == INFINITY) p0.x = 0.f;
                         if (key > q + 1 || l.y == INFINITY) p0.y = 0.f;
                         if (key > q + 2 || l.z == INFINITY) p1.x = 0.f;
@@ -311,18 +316,25 @@ fa_key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const KwArgs a)
                     s1 = add2(s1, p1);
                 }
             };
-            // the next 32 scores are on their way from tensor memory while the last are used
+            // the next 16 scores are on their way from tensor memory while the last are used (in pieces of 32: 119 in place of 114 us
+            // for 2 x 32 heads on 8 of 4096; all 64 before the first is used, and the accumulator given back then: 127)
             auto tile = [&](auto guard) {
-                uint32_t x0[32], x1[32];
-                tmem_ld32(src, x0);
+                uint32_t x0[16], x1[16];
+                tmem_ld16(src, x0);
                 tmem_wait_ld();
-                tmem_ld32(src + 32, x1);
+                tmem_ld16(src + 16, x1);
                 take(x0, 0, guard);
+                tmem_wait_ld();
+                tmem_ld16(src + 32, x0);
+                take(x1, 1, guard);
+                tmem_wait_ld();
+                tmem_ld16(src + 48, x1);
+                take(x0, 2, guard);
                 tmem_wait_ld();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(BAR(KW_S_FREE + kw_slot(n)));
-                take(x1, 1, guard);
+                take(x1, 3, guard);
             };
             if ((CAUSAL && q0 < k0 + w * kKeyTile + kKeyTile - 1) || out)
                 tile(std::true_type{});
