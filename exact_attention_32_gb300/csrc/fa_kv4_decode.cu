@@ -1083,7 +1083,7 @@ cudaError_t fa_launch_kv4_decode(const Kv4DecodeProblem &p, void *workspace, cud
         if (blocks > 512) blocks = 512;
         if (blocks > most) blocks = most;  // (at least 1: the rows fit 31 bits)
         auto *kern = a.R <= 2 ? fa_kv4_weights_kernel<1, 0, 2> : a.Rs <= 4 ? fa_kv4_weights_kernel<1, 1, 2>
-                     : a.Rs <= 8 ? fa_kv4_weights_kernel<1, 2, 2> : a.Rs <= 12 ? fa_kv4_weights_kernel<1, 3, 2>
+                     : a.Rs <= 8 ? fa_kv4_weights_kernel<1, 2, 2> : a.Rs <= 12 ? fa_kv4_weights_kernel<1, 3, 1>
                      : a.Rs <= 16 ? fa_kv4_weights_kernel<4, 1, 1> : a.Rs <= 32 ? fa_kv4_weights_kernel<8, 1, 1>
                      : a.Rs <= 48 ? fa_kv4_weights_kernel<4, 3, 1> : fa_kv4_weights_kernel<8, 2, 1>;
         e = kv4_launch_behind(kern, dim3(static_cast<unsigned>(blocks * p.B * heads)), 256, stream, a, static_cast<int>(blocks));
