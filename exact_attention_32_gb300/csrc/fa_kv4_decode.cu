@@ -14,12 +14,15 @@
 //   S^T = K Q^T      A = K as stored (128 rows, K-major), B = Q in E4M3.  One product per 32
 //                    channels, into columns of its own: K's scale differs per 32 channels
 //                    and is applied to the sums, one thread per key.
-//   O^T += V^T P^T   A = V as stored, MN-major; B = P times V's scale, in E4M3.
-// E4M3 has four significant bits, so what is not 4-bit goes in twice, as a high part
-// and 16 times the rest, in columns next to one another (N = 16 for 8 rows; a product's time
-// is A's, so they cost nothing).  For q (bf16, eight bits, scaled by a power of
-// two to a maximum in [128, 256)) that is exact down to 2^-13 of the row's maximum, and
-// to 2^-21 of it below.  P is off by at most 2^-8 of itself, as if rounded to bf16,
+//   O^T += V^T P^T   A = V as stored, MN-major; B = P times V's scale, in E5M2.
+// What is not 4-bit goes in as several parts, each 8 to 32 times what the ones before leave, in columns next to one
+// another (a product's time is A's, so they cost nothing).  q (bf16, eight bits, scaled by a power of
+// two to a maximum in [128, 256)) is two parts of E4M3, four bits each: exact down to 2^-13 of the row's maximum, and
+// to 2^-21 of it below.  P s (s: V's scale) spans far more, since a key of a thousandth of another's weight counts where there
+// are thousands of them, or where the other's V is small: it is rounded to a half, under a power of two of its row
+// that keeps the largest p s so far between 2^11 and 2^15, and goes in as three parts of E5M2 (a half's exponents, three bits
+// each).  So it is off by at most 2^-11 of itself down to 2^-24 of that largest term, and by 2^-34 of the term below (two
+// parts of E4M3 under one factor for all rows lost the keys behind a heavy one: O of 16384 keys was off by half).
 // l is summed in fp32.  The products are exact and added in fp32.
 //
 // Work: a tile is 128 rows of 128 values: 128 keys at d = 128, 256 at d = 64 (keys 2i and
@@ -93,28 +96,33 @@ template <int D, int RT>
 struct DecCfg {
     static constexpr int RP = 8 * RT;          // rows a CTA takes
     static constexpr int kLoadWarp = 4 * RT, kMmaWarp = kLoadWarp + 3, kWarps = kLoadWarp + 4, kThreads = 32 * kWarps;
-    static constexpr int N = 16 * RT;          // columns: per 8 rows, 8 high parts and 8 rests
+    static constexpr int N = 16 * RT;          // columns of S: per 8 rows, 8 high parts and 8 rests of q
     static constexpr int KPT = 128 / D;        // keys a thread (and a 128-byte row) holds
+    static constexpr int U = KPT * RT;         // 8 rows of every KPT-th key: P and O have 24 columns of each, parts 1 and 2 of
+    static constexpr int kPart3 = 16 * U;      // all of them first, then the parts 3
+    static constexpr int NP = (24 * U + 15) / 16 * 16;  // (a product's N is a multiple of 16: of a last odd 8, 8 more that hold anything)
     static constexpr int TK = 128 * KPT;       // keys a tile
     static constexpr int NG = TK / 16;         // runs of 16 tokens, each in one page
     static constexpr int kHalf = 16384;        // K or V of a tile
     static constexpr int kPerSm = RT == 1 ? 3 : RT == 2 ? 2 : 1;   // CTAs an SM
-    static constexpr int kStages = RT == 1 ? 2 : RT == 2 ? 3 : 5;  // of K, and of V
-    static constexpr int kPBufs = RT == 2 && D == 64 ? 1 : 2;      // (what fits two CTAs an SM)
+    static constexpr int kStages = RT == 1 ? 2 : RT == 2 ? 3 : 5;  // of K
+    static constexpr int kStagesV = RT == 2 && D == 64 ? 2 : kStages;  // of V
+    // (what fits kPerSm CTAs an SM; two stages of V and two buffers of P at d = 128 and 16 rows: 56 us in place of 55 for 32 x 8192)
+    static constexpr int kPBufs = D == 128 && RT < 4 ? 1 : 2;
     static constexpr int kV = kStages * kHalf;
-    static constexpr int kQ = 2 * kStages * kHalf;
+    static constexpr int kQ = kV + kStagesV * kHalf;
     static constexpr int kP = kQ + N * 128;
-    static constexpr int kPBytes = 128 * N * KPT;
+    static constexpr int kPBytes = 128 * NP;
     static constexpr int kScale = kP + kPBufs * kPBytes;         // a tile's K scales 512, V scales 256, page flags 64
     static constexpr int kScaleBytes = 512 + 256 + 64;
     static constexpr int kScales = kStages + 1;                  // of these
     static constexpr int kFloat = kScale + kScales * kScaleBytes;
-    static constexpr int kGroupFloats = 3 * 8 + 4 * 8 + 8;  // mult, m, alpha [8]; red [4][8]; misc [8]
+    static constexpr int kGroupFloats = 6 * 8 + 8;  // mult, m, alpha, top, f, o_alpha [8]; fail
     static constexpr int kWalk = kFloat + RT * kGroupFloats * 4;  // the share's start, the scan's sums
     static constexpr int kBar = kWalk + 64 + 8 * kWarps;
-    static constexpr int kNumBars = 6 * kStages + 10;
+    static constexpr int kNumBars = 2 * (kStages + kStagesV + kScales) + 8;
     static constexpr int kSmemBytes = kBar + kNumBars * 8 + 16;
-    static constexpr int kSCols = 4 * N, kOCols = N * KPT;
+    static constexpr int kSCols = 4 * N, kOCols = NP;
     static constexpr int kTmemCols = kSCols + kOCols <= 128 ? 128 : kSCols + kOCols <= 256 ? 256 : 512;
 };
 // P_READY is a barrier a buffer: a group may have tile n + 1's P written while another still works on tile n's, and its
@@ -183,6 +191,25 @@ __device__ __forceinline__ float2 e4m3x2_f32(uint32_t b)
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
+// Two halves of at most 2^15 as E5M2 three times: y = a + b / 8 + c / 256.  An E5M2 value is the top byte of a half, with three of
+// its eleven bits; what rounding leaves fits three bits twice more, so this is exact from 2^-13 on (below, off by at most 2^-24: the
+// smallest halves).  a and b are rounded to nearest on the bits, in the upper byte of each half (conversions back and forth took 2 % of
+// the kernel at 32 rows); a NaN, 0x7FFF here, comes out of c.
+__device__ __forceinline__ uint32_t round3(__half2 y) { return (*reinterpret_cast<const uint32_t *>(&y) + 0x00800080u) & 0xFF00FF00u; }
+__device__ __forceinline__ __half2 half2_of(uint32_t x) { return *reinterpret_cast<const __half2 *>(&x); }
+__device__ __forceinline__ void e5m2_parts(__half2 y, uint32_t &a, uint32_t &b, uint32_t &c)
+{
+    a = round3(y);
+    const __half2 y1 = __hmul2(__hsub2(y, half2_of(a)), __float2half2_rn(8.f));
+    b = round3(y1);
+    const __half2 y2 = __hmul2(__hsub2(y1, half2_of(b)), __float2half2_rn(32.f));
+    uint16_t r;
+    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;\n" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t *>(&y2)));
+    c = r;
+}
+// 1 / x of a power of two
+__device__ __forceinline__ float inverse_pow2(float x) { return __uint_as_float(0x7F000000u - __float_as_uint(x)); }
+
 // Barrier of a softmax warpgroup; with an OR over its threads.
 __device__ __forceinline__ void group_sync(int id) { asm volatile("barrier.cta.sync %0, 128;\n" ::"r"(id) : "memory"); }
 __device__ __forceinline__ bool group_or(int id, bool x)
@@ -214,15 +241,6 @@ __device__ __forceinline__ bool wait_both(uint32_t bar0, uint32_t phase0, uint32
     if (__all_sync(0xffffffffu, a && b)) return true;
     return mbar_wait_warp(bar0, phase0, kWaitLimitNs) && mbar_wait_warp(bar1, phase1, kWaitLimitNs);
 }
-__device__ __forceinline__ bool wait_three(uint32_t bar0, uint32_t phase0, uint32_t bar1, uint32_t phase1, uint32_t bar2,
-                                           uint32_t phase2)
-{
-    const bool a = mbar_try_wait(bar0, phase0), b = mbar_try_wait(bar1, phase1), c = mbar_try_wait(bar2, phase2);
-    if (__all_sync(0xffffffffu, a && b && c)) return true;
-    return mbar_wait_warp(bar0, phase0, kWaitLimitNs) && mbar_wait_warp(bar1, phase1, kWaitLimitNs) &&
-           mbar_wait_warp(bar2, phase2, kWaitLimitNs);
-}
-
 __device__ __forceinline__ uint32_t lo32(uint64_t x) { return static_cast<uint32_t>(x); }
 __device__ __forceinline__ uint32_t hi32(uint64_t x) { return static_cast<uint32_t>(x >> 32); }
 
@@ -231,10 +249,10 @@ __global__ void __launch_bounds__(DecCfg<D, RT>::kThreads, DecCfg<D, RT>::kPerSm
 fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const DecodeArgs a)
 {
     using C = DecCfg<D, RT>;
-    constexpr int RP = C::RP, N = C::N, KPT = C::KPT, TK = C::TK, ST = C::kStages;
+    constexpr int RP = C::RP, N = C::N, KPT = C::KPT, TK = C::TK, ST = C::kStages, SV = C::kStagesV;
     constexpr int kLoadWarp = C::kLoadWarp, kMmaWarp = C::kMmaWarp, kDecThreads = C::kThreads, kDecWarps = C::kWarps;
-    constexpr int K_FULL = D_STAGES, K_FREE = K_FULL + ST, V_FULL = K_FREE + ST, V_FREE = V_FULL + ST,
-                  XS = C::kScales, X_FULL = V_FREE + ST, X_FREE = X_FULL + XS;
+    constexpr int K_FULL = D_STAGES, K_FREE = K_FULL + ST, V_FULL = K_FREE + ST, V_FREE = V_FULL + SV,
+                  XS = C::kScales, X_FULL = V_FREE + SV, X_FREE = X_FULL + XS;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sb = smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -248,7 +266,7 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     const int64_t cap = a.max_pages << a.c.log2_page;
 
     if (tid == 0) {
-        for (int s = 0; s < 4 * ST + 2 * XS; ++s) mbar_init(BAR(D_STAGES + s), 1);
+        for (int s = 0; s < 2 * (ST + SV + XS); ++s) mbar_init(BAR(D_STAGES + s), 1);
         mbar_init(BAR(D_S_FULL), 1);
         mbar_init(BAR(D_S_FREE), 4 * RT);
         mbar_init(BAR(D_P_READY), 4 * RT);
@@ -336,7 +354,7 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
 
     if (warp >= kLoadWarp && warp < kMmaWarp) {
         // -------------------------------------------------------------------- loads: K, V, scales
-        const int role = warp - kLoadWarp, depth = role == 2 ? XS : ST;
+        const int role = warp - kLoadWarp, depth = role == 0 ? ST : role == 1 ? SV : XS;
         const CUtensorMap *map = role == 0 ? &tm_k : &tm_v;
         if (lane == 0 && role < 2) prefetch_tmap(map);
         const int bt = min(1 << a.c.log2_page, TK), n_boxes = TK / bt;  // tokens a box: a page, or the tile's part of one
@@ -388,24 +406,24 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         for (int i = n > depth ? n - depth : 0; i < n; ++i) mbar_wait(BAR(full + i % depth), (i / depth) & 1, lim);
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------------- products
-        constexpr uint32_t idS = idesc_e2m1_e4m3_f32(128, N, false, false);
-        constexpr uint32_t idO = idesc_e2m1_e4m3_f32(128, N * KPT, true, true);
+        constexpr uint32_t idS = idesc_e2m1_f8_f32(128, N, false, false, kE4M3);
+        constexpr uint32_t idO = idesc_e2m1_f8_f32(128, C::NP, true, true, kE5M2);
         const uint64_t dA = smem_desc_sw128(sb, 16, 1024);  // K tiles, and V tiles read the other way
         const uint64_t dQ = smem_desc_sw128(sb + C::kQ, 16, 1024);
         const uint64_t dP = smem_desc_plain(sb + C::kP, 128, 2048);
         bool ok = true;
         int n = 0, seg = 0;
         auto pv = [&](int m, bool first) -> bool {  // O^T (+)= V^T P^T of tile m
-            if (!wait_both(BAR(V_FULL + m % ST), (m / ST) & 1, BAR(D_P_READY + pbuf(m)), pv_phase(m))) return false;
+            if (!wait_both(BAR(V_FULL + m % SV), (m / SV) & 1, BAR(D_P_READY + pbuf(m)), pv_phase(m))) return false;
             tc_fence_after();
-            const uint32_t v = lo32(dA) + ((C::kV + m % ST * C::kHalf) >> 4);
+            const uint32_t v = lo32(dA) + ((C::kV + m % SV * C::kHalf) >> 4);
             if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
                     mma_ss_f8_lohi(tO, v + kk * 256, hi32(dA), lo32(dP) + pbuf(m) * (C::kPBytes >> 4) + kk * 32, hi32(dP), idO,
                                    first && kk == 0 ? 0u : 1u);
                 mma_commit(pv_bar(m));
-                mma_commit(BAR(V_FREE + m % ST));
+                mma_commit(BAR(V_FREE + m % SV));
             }
             __syncwarp();
             return true;
@@ -442,8 +460,11 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         const int g = warp >> 2, wl = warp & 3, tl = tid & 127;  // tl: TMEM lane
         const uint32_t loff = static_cast<uint32_t>(wl * 32) << 16;
         float *sm_mult = reinterpret_cast<float *>(smem + C::kFloat) + g * C::kGroupFloats;
-        float *sm_m = sm_mult + 8, *sm_alpha = sm_m + 8, *sm_red = sm_alpha + 8, *sm_misc = sm_red + 4 * 8;
-        volatile float *sm_fail = sm_misc + 1;  // a warp's wait gave up: all of the group leave at the next barrier
+        float *sm_m = sm_mult + 8, *sm_alpha = sm_m + 8, *sm_top = sm_alpha + 8, *sm_f = sm_top + 8, *sm_oalpha = sm_f + 8;
+        volatile float *sm_fail = sm_oalpha + 8;  // a warp's wait gave up: all of the group leave at the next barrier
+        // reductions over the group's warps, in its own part of P's first buffer where the products have read all of P
+        float *sm_red = reinterpret_cast<float *>(smem + C::kP + ((KPT - 1) * RT + g) * 2048);
+        auto unit = [&](int k) { return k * RT + g; };  // its columns of P and O
         auto sync = [&]() { group_sync(1 + g); };
         int n = 0;
         bool ok = true;
@@ -493,10 +514,10 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 if (ch == 0) {
                     sm_mult[r] = !(amax < INFINITY) ? NAN : a.scale_log2 * __uint_as_float(static_cast<uint32_t>(e - 7 + 127) << 23);
                     sm_m[r] = -FLT_MAX;
+                    sm_top[r] = -FLT_MAX;
+                    sm_f[r] = 1.f;
                 }
             }
-            // V's scale reference: P carries scale / reference * 256; two octaves above every scale so far
-            if (tl == 0) sm_misc[0] = 0x1p-16f;
             fence_proxy_async_smem();
             sync();
             if (lane == 0) mbar_arrive(BAR(D_Q_READY));
@@ -508,9 +529,7 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 const int xs = n % XS;
                 const uint8_t *scale = smem + C::kScale + xs * C::kScaleBytes;
                 const int key0 = t * TK;
-                // (P's buffer has been read, too)
-                ok = n < C::kPBufs ? wait_both(BAR(X_FULL + xs), (n / XS) & 1, BAR(D_S_FULL), n & 1)
-                                   : wait_three(BAR(X_FULL + xs), (n / XS) & 1, BAR(D_S_FULL), n & 1, pv_bar(n), pv_phase(n - C::kPBufs));
+                ok = wait_both(BAR(X_FULL + xs), (n / XS) & 1, BAR(D_S_FULL), n & 1);
                 if (!ok) *sm_fail = 1.f;
                 tc_fence_after();
                 // log2 scores of this thread's keys
@@ -584,16 +603,19 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                         }
                     }
                 }
-                // does a key pass its row's maximum, or a V scale the reference?  Soon that is rare.
+                // does a key pass its row's maximum, or its term the row's largest?  Soon that is rare.
                 bool grows = false;
-                const float vref = sm_misc[0];
+                float lv[KPT];  // log2 of V's scale
 #pragma unroll
-                for (int k = 0; k < KPT; ++k) grows |= vs[k] > vref;
+                for (int k = 0; k < KPT; ++k) lv[k] = lg2(vs[k]);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const float2 m = *reinterpret_cast<const float2 *>(sm_m + 2 * r);
+                    const float2 m = *reinterpret_cast<const float2 *>(sm_m + 2 * r), top = *reinterpret_cast<const float2 *>(sm_top + 2 * r);
 #pragma unroll
-                    for (int k = 0; k < KPT; ++k) grows |= x[k][r].x > m.x || x[k][r].y > m.y;
+                    for (int k = 0; k < KPT; ++k) {
+                        const float2 z = add2(x[k][r], make_float2(lv[k], lv[k]));
+                        grows |= x[k][r].x > m.x || x[k][r].y > m.y || z.x > top.x || z.y > top.y;
+                    }
                 }
                 grows = group_or(1 + g, grows);
                 if (*sm_fail != 0.f) {
@@ -601,79 +623,99 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                     break;
                 }
                 if (grows) {
-                    // O is complete so far, where it will be rescaled
+                    // O is complete so far, where it will be rescaled, and P's buffers are free
                     if (t > w.t0 && !mbar_wait_warp(pv_bar(n - 1), pv_phase(n - 1), kWaitLimitNs)) *sm_fail = 1.f;
 #pragma unroll
                     for (int r = 0; r < 8; ++r) {
-                        float v = -FLT_MAX;
+                        float v = -FLT_MAX, z = -FLT_MAX;
 #pragma unroll
-                        for (int k = 0; k < KPT; ++k) v = fmaxf(v, r & 1 ? x[k][r / 2].y : x[k][r / 2].x);
+                        for (int k = 0; k < KPT; ++k) {
+                            const float xr = r & 1 ? x[k][r / 2].y : x[k][r / 2].x;
+                            v = fmaxf(v, xr);
+                            z = fmaxf(z, xr + lv[k]);
+                        }
                         v = warp_max(v);
-                        if (lane == 0) sm_red[wl * 8 + r] = v;
-                    }
-                    {
-                        float v = 0.f;
-#pragma unroll
-                        for (int k = 0; k < KPT; ++k) v = fmaxf(v, vs[k]);
-                        v = warp_max(v);
-                        if (lane == 0) sm_misc[4 + wl] = v;
+                        z = warp_max(z);
+                        if (lane == 0) *reinterpret_cast<float2 *>(sm_red + (wl * 8 + r) * 2) = make_float2(v, z);
                     }
                     sync();
                     if (*sm_fail != 0.f) {
                         ok = false;
                         break;
                     }
-                    const float vmax = fmaxf(fmaxf(sm_misc[4], sm_misc[5]), fmaxf(sm_misc[6], sm_misc[7]));
-                    const float vnew = vmax > vref ? __uint_as_float((__float_as_uint(vmax) & 0x7F800000u) + (2u << 23)) : vref;
                     if (tl < 8) {
-                        const float old = sm_m[tl];
-                        float v = fmaxf(fmaxf(sm_red[tl], sm_red[8 + tl]), fmaxf(sm_red[16 + tl], sm_red[24 + tl]));
+                        float v = -FLT_MAX, z = -FLT_MAX;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 y = *reinterpret_cast<const float2 *>(sm_red + (i * 8 + tl) * 2);
+                            v = fmaxf(v, y.x);
+                            z = fmaxf(z, y.y);
+                        }
+                        const float old = sm_m[tl], top = sm_top[tl], f = sm_f[tl];
                         v = v > old ? v + kHeadroom : old;
+                        z = z > top ? z + kHeadroom : top;
+                        const float alpha = ex2(old - v);
+                        // the power of two that keeps the terms up to 2^15; held at 2^100 where p itself is next to nothing
+                        const int e = min(max(__float2int_rd((v - z) + 15.f), -100), 100);
+                        const float now = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
                         sm_m[tl] = v;
-                        sm_alpha[tl] = ex2(old - v);
+                        sm_top[tl] = z;
+                        sm_alpha[tl] = alpha;
+                        sm_f[tl] = now;
+                        sm_oalpha[tl] = alpha * (now * inverse_pow2(f));
                     }
-                    if (tl == 0) sm_misc[0] = vnew;
                     sync();
 #pragma unroll
                     for (int r = 0; r < 4; ++r) l[r] = mul2(l[r], *reinterpret_cast<const float2 *>(sm_alpha + 2 * r));
                     if (t > w.t0) {
                         tc_fence_after();
-                        const float vf = vref / vnew;
 #pragma unroll
                         for (int k = 0; k < KPT; ++k) {
-                            uint32_t o[16];
-                            tmem_ld16(tO + loff + k * N + g * 16, o);
-                            tmem_wait_ld();
 #pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                o[j] = __float_as_uint(__uint_as_float(o[j]) * (sm_alpha[j & 7] * vf));
-                            tmem_st16(tO + loff + k * N + g * 16, o);
+                            for (int part = 0; part < 3; ++part) {
+                                const uint32_t at = tO + loff + (part < 2 ? unit(k) * 16 + part * 8 : C::kPart3 + unit(k) * 8);
+                                uint32_t o[8];
+                                tmem_ld8(at, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * sm_oalpha[j]);
+                                tmem_st8(at, o);
+                            }
                         }
                         tmem_wait_st();
                     }
                 }
-                // P: the sum in fp32; the product's operand times V's scale, as a high part and 16 times the rest
-                const float vc = 256.f / sm_misc[0];
+                // has P's buffer been read?  (asked ahead; a wait where nothing is left to wait for takes 170 cycles)
+                const bool free = n < C::kPBufs || mbar_test_wait(pv_bar(n), pv_phase(n - C::kPBufs));
+                // P: the sum in fp32; the product's operand times V's scale and the row's factor, in three parts
+                __half2 y[KPT][4];
 #pragma unroll
-                for (int k = 0; k < KPT; ++k) {
-                    const float c1 = vs[k] * vc, c16 = c1 * 16.f;
-                    uint32_t hb[4], lb[4];
+                for (int k = 0; k < KPT; ++k)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float2 m = *reinterpret_cast<const float2 *>(sm_m + 2 * j);
+                        const float2 m = *reinterpret_cast<const float2 *>(sm_m + 2 * j), f = *reinterpret_cast<const float2 *>(sm_f + 2 * j);
                         const float2 xx = x[k][j];
                         const float2 p = make_float2(ex2(xx.x - m.x), ex2(xx.y - m.y));
                         l[j] = add2(l[j], p);
-                        float2 y = mul2(p, make_float2(c1, c1)), y16 = mul2(p, make_float2(c16, c16));
+                        float2 pv = mul2(p, mul2(f, make_float2(vs[k], vs[k])));
                         if (edge) {  // a value that a row does not admit stays out of it, a NaN too
-                            if (xx.x == -INFINITY) y.x = y16.x = 0.f;
-                            if (xx.y == -INFINITY) y.y = y16.y = 0.f;
+                            if (xx.x == -INFINITY) pv.x = 0.f;
+                            if (xx.y == -INFINITY) pv.y = 0.f;
                         }
-                        hb[j] = e4m3x2(y);
-                        lb[j] = e4m3x2(fma2(e4m3x2_f32(hb[j]), make_float2(-16.f, -16.f), y16));
+                        y[k][j] = __floats2half2_rn(pv.x, pv.y);
                     }
-                    *reinterpret_cast<uint4 *>(smem + C::kP + pbuf(n) * C::kPBytes + (k * RT + g) * 2048 + tl * 16) =
-                        make_uint4(hb[0] | (hb[1] << 16), hb[2] | (hb[3] << 16), lb[0] | (lb[1] << 16), lb[2] | (lb[3] << 16));
+                if (!__all_sync(0xffffffffu, free) && !mbar_wait_warp(pv_bar(n), pv_phase(n - C::kPBufs), kWaitLimitNs)) *sm_fail = 1.f;
+#pragma unroll
+                for (int k = 0; k < KPT; ++k) {
+                    uint32_t pa[4], pb[4], pc[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) e5m2_parts(y[k][j], pa[j], pb[j], pc[j]);
+                    uint8_t *to = smem + C::kP + pbuf(n) * C::kPBytes + tl * 16;
+                    *reinterpret_cast<uint4 *>(to + unit(k) * 2048) =
+                        make_uint4(__byte_perm(pa[0], pa[1], 0x7531), __byte_perm(pa[2], pa[3], 0x7531),
+                                   __byte_perm(pb[0], pb[1], 0x7531), __byte_perm(pb[2], pb[3], 0x7531));
+                    *reinterpret_cast<uint2 *>(to + (C::U + unit(k) / 2) * 2048 + unit(k) % 2 * 8) =
+                        make_uint2(pc[0] | (pc[1] << 16), pc[2] | (pc[3] << 16));
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
@@ -692,16 +734,18 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
                 if (lane == 0) sm_red[wl * 8 + r] = v;
             }
-            // this lane's channel of every row: high part and a sixteenth of the rest, P's factor taken out
+            // this lane's channel of every row: the three parts' sums, the row's factor taken out
             float y[8];
-            const float back = sm_misc[0] * 0.00390625f;
             const int half = D == 64 ? wl >> 1 : 0;  // d = 64: lanes 64-127 hold the odd keys' part of channel lane - 64
             {
-                uint32_t o[16];
-                tmem_ld16(tO + loff + half * N + g * 16, o);
+                uint32_t o[16], o3[8];
+                tmem_ld16(tO + loff + unit(half) * 16, o);
+                tmem_ld8(tO + loff + C::kPart3 + unit(half) * 8, o3);
                 tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 8; ++j) y[j] = fmaf(__uint_as_float(o[8 + j]), 0.0625f, __uint_as_float(o[j])) * back;
+                for (int j = 0; j < 8; ++j)
+                    y[j] = fmaf(__uint_as_float(o3[j]), 0x1p-8f, fmaf(__uint_as_float(o[8 + j]), 0.125f, __uint_as_float(o[j]))) *
+                           inverse_pow2(sm_f[j]);
             }
             tc_fence_before();
             float *sx = reinterpret_cast<float *>(smem + C::kP) + g * 8 * 64;  // (the products have read P)

@@ -282,12 +282,13 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, bool b_mn_ma
 }
 
 // Instruction descriptor, kind::f8f6f4 with A in E2M1 (16 values in the first 8 of every
-// 16 bytes of shared memory) and B in E4M3, fp32 accumulator.
-__host__ __device__ constexpr uint32_t idesc_e2m1_e4m3_f32(int M, int N, bool a_mn_major, bool b_mn_major)
+// 16 bytes of shared memory) and B in E4M3 or E5M2, fp32 accumulator.
+constexpr uint32_t kE4M3 = 0, kE5M2 = 1;
+__host__ __device__ constexpr uint32_t idesc_e2m1_f8_f32(int M, int N, bool a_mn_major, bool b_mn_major, uint32_t b_format)
 {
     return (1u << 4)                                 // D format: f32
            | (5u << 7)                               // A format: E2M1
-           | (0u << 10)                              // B format: E4M3
+           | (b_format << 10)                        // B format
            | ((a_mn_major ? 1u : 0u) << 15)          // A major-ness
            | ((b_mn_major ? 1u : 0u) << 16)          // B major-ness
            | (static_cast<uint32_t>(N >> 3) << 17)   // N / 8
@@ -373,6 +374,20 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
         : "r"(taddr));
 }
 
+// 32 lanes x 8 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
 // tmem_ld32 of fp32 values that also returns each thread's largest of its 32
 // values (tcgen05.ld with a max reduction: sm_103a; the row max of a softmax
 // without a separate pass over the registers).
@@ -437,6 +452,14 @@ __device__ __forceinline__ float ex2(float x)
 {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// log2 of x (approximate; -inf for 0)
+__device__ __forceinline__ float lg2(float x)
+{
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
     return y;
 }
 

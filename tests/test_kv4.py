@@ -14,7 +14,7 @@ S    a score is a sum of d products, exact in what the MMA multiplies, added in 
 LSE  its scores' error, and fp32's: eS + 2^-22 (|LSE| + 1).
 w    a probability is off by the factor exp(eS + error of LSE) and the exponential's 2^-22:
      w (2 eS + 2^-21 (|LSE| + 2)), a sum of n rows in fp32 adds n 2^-24.
-O    the weights' relative error on sum p |v|; P in two E4M3 parts: the first is off by half a step, at most 2^-4,
+O    the weights' relative error on sum p |v|; what a P in two E4M3 parts may be off by (the kernel's is closer, check_tail holds it to that): the first is off by half a step, at most 2^-4,
      the second by 2^-4 of that, 2^-8 together; the smallest steps, as above, 2^-14 of a scale of 256 that
      stands for at most 2^3 times the row's largest term and four times the largest V scale: 2^-17 times 6
      (a code) times that scale a key, over the sum l; and bf16's rounding of the result (eight significant bits: half a step is 2^-8 of the value).
@@ -432,6 +432,98 @@ def test_attention_over_small_and_large_values(gain, q_gain):
     o, lse = fa.forward_kv4(q, pool.cache(), dev(lens), dev(pool.table))
     ok()
     check_attention(pool, q, lens, fa.default_scale(128), o, lse)
+
+
+def _put(pool, b, j, k=None, v=None):
+    """Token j of sequence b becomes the rows k, v (each [Hkv, d], or None to leave what is there)."""
+    at = pool.table[b, j // pool.P], slice(None), j % pool.P
+    if k is not None:
+        pool.k[at], pool.ks[at] = ref.quantise(f64(bf16(k)), 32)
+    if v is not None:
+        code, s = ref.quantise(f64(bf16(v)), pool.d)
+        pool.v[at], pool.vs[at] = code, s[..., 0]
+
+
+def check_tail(pool, q, lens, scale, copies):
+    """Attention over the pool's sequences, each `copies` times in the batch (many copies make long shares, cut in other places in
+    each).  O within 2^-10 of sum p |v| and bf16's rounding (2^-8 of the value), beside the scores' error (as above): whatever a
+    row's largest terms are, the small ones count, and nothing grows with the number of keys.  p s (s: V's scale) is rounded to a
+    half: 2^-11 of itself down to 2^-24 of the row's largest one, which none of the keys here that matter lies below; each of the sums
+    over n / 32 products is off by at most 2^-23 of it: 2^-14 at 16384 keys."""
+    B = len(lens)
+    o, lse = fa.forward_kv4(q.repeat(copies, 1, 1, 1), pool.cache(), dev(np.tile(lens, copies)), dev(np.tile(pool.table, (copies, 1))))
+    ok()
+    o, lse = f64(o).reshape(copies, *q.shape), f64(lse).reshape(copies, *q.shape[:-1])
+    for b in range(B):
+        n = int(lens[b])
+        r = ref.attention(f64(q[b]), *pool.kv(b, n), scale, n)
+        eS = (pool.d + 8) * 2.0 ** -23 * r["reach"] + 2.0 ** -21 * r["top_q"]
+        assert (np.abs(lse[:, b] - r["lse"]) <= eS + 2.0 ** -22 * (np.abs(r["lse"]) + 1)).all()
+        rel = 2 * eS + 2.0 ** -21 * (np.abs(r["lse"]) + 2)
+        err, tol = np.abs(o[:, b] - r["o"]), (rel + 2.0 ** -10)[..., None] * r["spread"] + 2.0 ** -8 * np.abs(r["o"])
+        assert (err <= tol).all(), (b, (err / tol).max(), np.sqrt((err[0] ** 2).sum() / (r["o"] ** 2).sum()))
+
+
+@gpu
+@pytest.mark.parametrize("Hkv,G,n_q,d", [(2, 1, 1, 64), (1, 4, 1, 128), (1, 12, 1, 64), (1, 8, 2, 128), (1, 32, 1, 64), (1, 8, 5, 128)])
+@pytest.mark.parametrize("n,at,copies", [(300, 0, 1), (2048, 0, 200), (2048, 1000, 1), (16384, 0, 1), (16384, 5000, 150)])
+def test_attention_behind_a_heavy_key_keeps_the_others(n, at, copies, Hkv, G, n_q, d):
+    # a key 8, 11 or 14 nats above the others' mean whose V is small (an attention sink), first or in the middle
+    lens = np.array([n, n - 7, n // 2 + at], np.int32)
+    pool = Pool(3, Hkv, d, 64, lens, seed=n + at + G)
+    rng = np.random.default_rng(G + d)
+    scale = fa.default_scale(d)
+    q = rng.standard_normal((3, Hkv * G, n_q, d))
+    q[..., 0] = 16.0  # channel 0 is the heavy key's alone
+    pool.k[..., 0] &= 0xF0
+    for b, nats in enumerate((8.0, 11.0, 14.0)):
+        k, v = np.zeros((Hkv, d)), rng.standard_normal((Hkv, d)) / 64
+        k[:, 0] = nats / (scale * 16.0)
+        _put(pool, b, at, k, v)
+    check_tail(pool, bf16(q).cuda(), lens, scale, copies)
+
+
+@gpu
+@pytest.mark.parametrize("Hkv,G,n_q,d", [(2, 4, 1, 64), (1, 4, 2, 128), (1, 12, 1, 128), (1, 16, 2, 64)])
+@pytest.mark.parametrize("gain", [64.0, 300.0, 4096.0])
+def test_a_large_value_of_next_to_no_weight_leaves_the_others_alone(gain, Hkv, G, n_q, d):
+    # a V row `gain` times the others' at a key far below them; and one that only the last query admits
+    lens = np.array([8192, 8192], np.int32)
+    pool = Pool(2, Hkv, d, 64, lens, seed=int(gain) + G)
+    rng = np.random.default_rng(G + d)
+    scale = fa.default_scale(d)
+    q = rng.standard_normal((2, Hkv * G, n_q, d))
+    q[..., 0] = 16.0
+    pool.k[..., 0] &= 0xF0
+    for b, j in ((0, 0), (1, 8191)):
+        k = np.zeros((Hkv, d))
+        k[:, 0] = -20.0 / (scale * 16.0)
+        _put(pool, b, j, k, gain * rng.standard_normal((Hkv, d)))
+    check_tail(pool, bf16(q).cuda(), lens, scale, 250)
+
+
+@gpu
+@pytest.mark.parametrize("d,G", [(64, 8), (128, 8), (128, 16), (64, 32)])
+def test_heavy_keys_without_values_and_rising_scores(d, G):
+    # V scale 0 at the heaviest keys (their terms vanish, the others' remain), scores that rise and fall over the sequence by 25 nats, V
+    # that falls and rises against them
+    n = 6000
+    lens = np.array([n, n], np.int32)
+    pool = Pool(2, 1, d, 128, lens, seed=d + G)
+    rng = np.random.default_rng(G)
+    scale = fa.default_scale(d)
+    q = rng.standard_normal((2, G, 1, d))
+    q[..., 0] = 16.0
+    for b in range(2):
+        for j in range(n):
+            nats = (j * 25 / n) if b else 25 - j * 25 / n
+            k, v = 0.5 * rng.standard_normal((1, d)), rng.standard_normal((1, d)) * np.exp(0.8 * (12 - nats))
+            k[:, 0] = nats / (scale * 16.0)
+            _put(pool, b, j, k, 0 * v if j % 97 == 5 else v)
+        k[:, 0] = 30.0 / (scale * 16.0)
+        _put(pool, b, 3000, k, np.zeros((1, d)))
+    for copies in (1, 250):
+        check_tail(pool, bf16(q).cuda(), lens, scale, copies)
 
 
 @gpu
