@@ -107,8 +107,9 @@ struct DecCfg {
     static constexpr int kPerSm = RT == 1 ? 3 : RT == 2 ? 2 : 1;   // CTAs an SM
     static constexpr int kStages = RT == 1 ? 2 : RT == 2 ? 3 : 5;  // of K
     static constexpr int kStagesV = RT == 2 && D == 64 ? 2 : kStages;  // of V
-    // (what fits kPerSm CTAs an SM; two stages of V and two buffers of P at d = 128 and 16 rows: 56 us in place of 55 for 32 x 8192)
-    static constexpr int kPBufs = D == 128 && RT < 4 ? 1 : 2;
+    // What fits kPerSm CTAs an SM.  d = 64, 8 rows, with two buffers: two CTAs an SM, 64 sequences of 16384 194 us in place of 133;
+    // d = 128, 16 rows, with two stages of V and two buffers: 32 of 8192 56 us in place of 55.
+    static constexpr int kPBufs = RT == 1 || (RT == 2 && D == 128) ? 1 : 2;
     static constexpr int kV = kStages * kHalf;
     static constexpr int kQ = kV + kStagesV * kHalf;
     static constexpr int kP = kQ + N * 128;
@@ -124,6 +125,9 @@ struct DecCfg {
     static constexpr int kSmemBytes = kBar + kNumBars * 8 + 16;
     static constexpr int kSCols = 4 * N, kOCols = NP;
     static constexpr int kTmemCols = kSCols + kOCols <= 128 ? 128 : kSCols + kOCols <= 256 ? 256 : 512;
+    // The grid's equal shares are for kPerSm CTAs on every SM at once; a second round for those that do not fit would double its
+    // time.  (228 KB of shared memory an SM, 1 KB of it for each CTA, and 512 columns of tensor memory.)
+    static_assert(kPerSm * (kSmemBytes + 1024) <= 228 * 1024 && kPerSm * kTmemCols <= 512, "kPerSm CTAs fit an SM");
 };
 // P_READY is a barrier a buffer: a group may have tile n + 1's P written while another still works on tile n's, and its
 // arrival must not count for tile n.  (It reaches tile n + 2 only behind the product of tile n.)
