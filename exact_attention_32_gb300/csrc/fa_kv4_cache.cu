@@ -114,11 +114,13 @@ fa_kv4_append_kernel(Kv4Cache c, const uint4 *__restrict__ k_new, const uint4 *_
             }
         }
         const float w = mine && t == 0 && w_new != nullptr ? w_new[rr] : 0.f;
-        // (a thread without a row looks up position 0's page, and drops it)
-        const int pos = static_cast<int>(at) - n + kv4_length(lens, b, max_pages << c.log2_page);
+        // the place is made of the length as it is given: held to the table, a length past it would put the tokens over others
+        const int64_t place = at - n + lens[b];
+        const bool in = mine && place >= 0 && place < (max_pages << c.log2_page);
+        const int pos = in ? static_cast<int>(place) : 0;  // (a thread without a place looks up position 0's page, and drops it)
         bool valid;
-        const int page = kv4_page_quiet(c, table, b, max_pages, max(0, mine ? pos : 0), &valid);
-        valid = valid && pos >= 0;
+        const int page = kv4_page_quiet(c, table, b, max_pages, pos, &valid);
+        valid = valid && in;
         bad |= mine && !valid;
         float xk[2][8], xv[2][8];
         uint32_t mk = max_u16x2(unpack8(uk[0], xk[0]), unpack8(uk[1], xk[1]));

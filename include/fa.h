@@ -425,8 +425,9 @@ typedef struct fa_kv4_cache {
  *   n_new  : const int32 [B], how many of the S tokens sequence b gains (held to
  *            [0, S]), or NULL for S
  *   lens   : lengths AFTER the append: token i goes to position
- *            lens[b] - n_new[b] + i (tokens whose position is negative are
- *            dropped and reported as FA_ERR_BAD_PAGE)
+ *            lens[b] - n_new[b] + i, with the length as it is given (tokens whose
+ *            position lies outside [0, max_pages * page_size) are dropped and
+ *            reported as FA_ERR_BAD_PAGE)
  * Everything else in the pages is left as it was.
  */
 int fa_kv4_append(const fa_kv4_cache *cache, const void *k_new, const void *v_new, const float *w_new,

@@ -309,6 +309,31 @@ def test_append_without_counts_or_weights():
 
 
 @gpu
+@pytest.mark.parametrize("S,over", [(1, 1), (8, 3), (8, 8), (8, 100), (300, 290), (4, 2 ** 31 - 1 - 48), (4, -48 - 3), (4, -(2 ** 31) - 48)])
+def test_append_past_the_table_drops_what_has_no_place(S, over):
+    # the length after the append is `over` tokens past the table's 48 (or before 0): tokens with a place go there, the others
+    # nowhere, and no row that is stored changes
+    d, P, cap = 64, 16, 48
+    pool = Pool(2, 2, d, P, [cap, 20], seed=S + 1000)
+    pool.table = np.ascontiguousarray(pool.table[:, :cap // P])
+    x = bf16(np.random.default_rng(S).standard_normal((2, 2, S, d)))
+    n = np.array([S, 0], np.int32)
+    c = pool.cache()
+    fa.kv4_append(c, x.cuda(), x.cuda(), dev(np.array([cap + over, 20], np.int32)), dev(pool.table), n_new=dev(n))
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_status(0) == 8 and fa.fa_get_device_status(0) == 0
+    want = [pool.k.copy(), pool.v.copy(), pool.ks.copy(), pool.vs.copy(), pool.w.copy()]
+    at = cap + over - S + np.arange(S, dtype=np.int64)
+    i = np.flatnonzero((at >= 0) & (at < cap))
+    pg, sl = pool.table[0, at[i] // P], at[i] % P
+    (kc, ks), (vc, vs) = ref.quantise(f64(x[0]), 32), ref.quantise(f64(x[0]), d)
+    for t, y in zip(want, (kc, vc, ks, vs[..., 0], np.zeros((2, S)))):
+        t[pg, :, sl] = np.moveaxis(y[:, i], 0, 1)
+    for got, t in zip(c, want):
+        assert torch.equal(got.cpu(), torch.as_tensor(t))
+
+
+@gpu
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("P", [16, 128])
 def test_read_gives_the_stored_values_and_zeros_behind_them(P, d):
