@@ -370,20 +370,20 @@ fa_kv4_move_kernel(Kv4Cache from, Kv4Cache to, const int32_t *__restrict__ table
         int64_t rs[U], rd[U];
         uint4 x[U];
         uint32_t y[U];
-        bool go[U];
+        bool go[U], there[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) src[u] = r0 + u * kStep < rows ? kept[r0 + u * kStep] : -1;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             int64_t dst, h;
             const int64_t bh = row_div(min(r0 + u * kStep, rows - 1), keep, rows, &dst), b = row_div(bh, from.heads, rows, &h);
-            bool vs, vd;
-            const int ps = kv4_page_quiet(from, table, b, max_pages, max(src[u], 0), &vs);
+            bool vd;
+            const int ps = kv4_page_quiet(from, table, b, max_pages, max(src[u], 0), &there[u]);
             const int pd = kv4_page_quiet(to, to_table, b, to_max_pages, static_cast<int>(dst), &vd);
             rs[u] = kv4_row(from, ps, static_cast<int>(h), max(src[u], 0));
             rd[u] = kv4_row(to, pd, static_cast<int>(h), static_cast<int>(dst));
-            go[u] = src[u] >= 0 && vs && vd;
-            bad |= src[u] >= 0 && !go[u];
+            go[u] = src[u] >= 0 && vd;
+            bad |= src[u] >= 0 && !(there[u] && vd);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -399,6 +399,10 @@ fa_kv4_move_kernel(Kv4Cache from, Kv4Cache to, const int32_t *__restrict__ table
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (!go[u]) continue;
+            if (!there[u]) {  // a token that no page holds: zeros without weight, not what lies in the new page
+                x[u] = make_uint4(0, 0, 0, 0);
+                y[u] = 0;
+            }
             reinterpret_cast<uint4 *>(t < HALF ? to.k : to.v)[rd[u] * HALF + i] = x[u];
             if (t == 0) {
                 if (D == 128)

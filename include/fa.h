@@ -488,6 +488,8 @@ int64_t fa_fwd_kv4_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t n_
  *   to_table : const int32 [B][to_max_pages], to_max_pages * page_size >= keep
  *   keep : >= 1;  recent : 0 .. keep
  *   kept : int32 out [B][Hkv][keep], the positions kept, ascending, -1 past the end
+ *         (a kept token whose page lies outside the pool is lighter than every
+ *         other; where it stays its row becomes zeros with weight 0)
  *   new_lens : int32 out [B], min(lens[b], keep)
  */
 int fa_kv4_evict(const fa_kv4_cache *from, const int32_t *lens, const int32_t *page_table,

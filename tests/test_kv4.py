@@ -708,6 +708,41 @@ def test_eviction_from_long_sequences(n):
     check_eviction(pool, w, lens, n // 3, 512, False)
 
 
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens,keep,recent", [([70, 100], 128, 5), ([70, 100], 60, 40), ([100, 100], 1, 1)])
+def test_eviction_from_a_bad_page_leaves_rows_of_zeros(lens, keep, recent, d):
+    # sequence 0's page 3 and sequence 1's last page are no pages of the pool: what is kept of them is zeros without weight, not what
+    # lay in the new pages, and everything else is as without the fault
+    lens, P = np.array(lens, np.int32), 16
+    pool = Pool(2, 2, d, P, lens, seed=keep, spare=8)
+    table = pool.table.copy()
+    table[0, 3], table[1, (lens[1] - 1) // P] = pool.n_pages, -1
+    to = fa.KV4Cache(*(torch.randint(1, 200, t.shape, device="cuda").to(t.dtype) for t in pool.cache()))
+    cols = -(-keep // P)
+    to_table = np.arange(2 * cols, dtype=np.int32).reshape(2, cols)
+    want = [t.cpu().numpy().copy() for t in to]
+    kept, now = fa.kv4_evict(pool.cache(), dev(lens), dev(table), to, dev(to_table), keep, recent=recent)
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_status(0) == 8 and fa.fa_get_device_status(0) == 0
+    kept = kept.cpu().numpy()
+    met = 0
+    for b in range(2):
+        m = min(int(lens[b]), keep)
+        assert int(now[b]) == m
+        for h in range(2):
+            assert (np.diff(kept[b, h, :m]) > 0).all()
+            for i, j in enumerate(kept[b, h, :m]):
+                src, at = table[b, j // P], (to_table[b, i // P], h, i % P)
+                bad = not 0 <= src < pool.n_pages
+                met += bad
+                for t, x in zip(want, (pool.k, pool.v, pool.ks, pool.vs, pool.w)):
+                    t[at] = 0 if bad else x[src, h, j % P]
+    assert met
+    for got, t in zip(to, want):
+        assert np.array_equal(got.cpu().numpy(), t)
+
+
 # --------------------------------------------------------------------------------- key weights
 
 def _lse(q, k, scale, causal):
