@@ -915,6 +915,10 @@ fa_kv4_weights_kernel(const DecodeArgs a, int blocks)
     const int64_t cap = a.max_pages << a.c.log2_page;
     const int len = kv4_length(a.lens, b, cap);
     kv4_wait_for_the_one_before();
+    // A wait gave up, in this call or in one before, and nobody has read so yet: the scores are not all there, and weights, which
+    // a caller cannot compute again from what it has, stay as they are.  (An ordinary load, held against the store only: volatile
+    // ones of every warp meet in one place of L2 and took 4 us of 61.)
+    const bool off = g_kv4_status == FA_ERR_TIMEOUT;
     const float2 *ml = a.row_ml + bh * a.R;
     for (int key0 = blockIdx.x % blocks * 256 * U + (threadIdx.x & ~31); key0 < len; key0 += blocks * 256 * U) {
         int64_t row[U];
@@ -978,7 +982,7 @@ fa_kv4_weights_kernel(const DecodeArgs a, int blocks)
             }
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (row[u] >= 0) a.c.weights[row[u]] = old[u] + mine[u];
+            if (row[u] >= 0 && !off) a.c.weights[row[u]] = old[u] + mine[u];
     }
 }
 

@@ -518,8 +518,10 @@ int fa_key_weights(const void *q, const void *k, const float *lse, float *weight
  * fa_get_device_status - synchronise `stream`, then return and clear the
  * current device's sticky in-kernel status (FA_OK, or FA_ERR_TIMEOUT when a
  * bounded wait inside a kernel gave up and the kernel returned early, leaving
- * its outputs incomplete; or FA_ERR_BAD_PAGE, see the 4-bit cache).  While FA_ERR_TIMEOUT is set, fa_fwd launches do
- * no work (their outputs are left unwritten) until this call clears it.
+ * its outputs incomplete; or FA_ERR_BAD_PAGE, see the 4-bit cache).  While
+ * FA_ERR_TIMEOUT is set, fa_fwd and fa_fwd_kv4 launches do no work (their
+ * outputs are left unwritten) until this call clears it; a fa_fwd_kv4 call
+ * in which a wait gave up adds nothing to the cache's weights.
  * Returns FA_ERR_LAUNCH if the synchronisation itself reports a CUDA error.
  */
 int fa_get_device_status(void *stream);
