@@ -565,6 +565,29 @@ def test_a_stored_nan_reaches_the_rows_that_admit_it_and_no_other():
 
 
 @gpu
+@pytest.mark.parametrize("d,G,n", [(64, 1, 40), (128, 2, 70), (64, 4, 300), (128, 8, 3000), (64, 16, 2000)])
+def test_a_row_of_nan_weighs_no_key_that_it_does_not_admit(d, G, n):
+    # three new tokens: the first of them has a NaN in q (every head's).  The two newest keys are not among those that it admits: their
+    # weights are the other queries'
+    lens = np.array([n, 2], np.int32)  # (of the second sequence's rows the first admits nothing at all)
+    pool = Pool(2, 1, d, 16, lens, seed=n)
+    q = np.random.default_rng(n).standard_normal((2, G, 3, d))
+    q[:, :, 0, 7] = np.nan
+    c = pool.cache()
+    o, lse = fa.forward_kv4(bf16(q).cuda(), c, dev(lens), dev(pool.table), accumulate=True)
+    ok()
+    got = f64(c.weights)
+    q[:, :, 0] = 0
+    for b in range(2):
+        j = np.arange(int(lens[b]))
+        added = got[pool.table[b, j // 16], 0, j % 16] - pool.w[pool.table[b, j // 16], 0, j % 16]
+        r = ref.attention(f64(bf16(q[b])), *pool.kv(b, len(j)), fa.default_scale(d), len(j))
+        first = max(0, len(j) - 2)
+        assert np.isnan(added[:first]).all() and np.isnan(f64(o[b, :, 0])).all() == (first > 0)
+        assert np.abs(added[first:] - r["weights"][0, first:]).max() <= 1e-4 * G and np.isfinite(f64(o[b, :, 1:])).all()
+
+
+@gpu
 def test_bad_pages_and_lengths_are_left_out_and_reported():
     # the kernels check the table and the lengths themselves: nothing outside the pool is read or written
     lens = np.array([100, 60], np.int32)
