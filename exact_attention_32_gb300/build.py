@@ -13,6 +13,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -87,24 +88,41 @@ def build_marshal(force: bool = False) -> str:
     return MARSHAL
 
 
-def build(force: bool = False) -> str:
-    """Compile the extension, and compile and link libfa.so, unless newer than every source."""
+def _extension(force: bool) -> None:
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        print("torch is not there: the Python calls of the 4-bit cache (_marshal.so) are not built", file=sys.stderr)
+    else:
+        build_marshal(force)
+
+
+def _library(force: bool) -> None:
     if (not force and os.path.exists(LIB)
             and os.path.getmtime(LIB) >= max(os.path.getmtime(p) for p in _deps())):
-        build_marshal()
-        return LIB
+        return
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
-        marshal = ex.submit(build_marshal, force)
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
         objs = list(ex.map(_compile, srcs))
-        marshal.result()
     tmp = LIB + ".tmp"
     r = subprocess.run([nvcc()] + ARCH + ["-shared", "-o", tmp] + objs,
                        capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+
+
+def build(force: bool = False) -> str:
+    """Compile and link libfa.so, and compile the extension beside it, unless newer than every source.
+
+    The library needs nvcc alone: it is there whatever becomes of the
+    extension, which is left out, with a note, where torch cannot be imported
+    (C callers); what else goes wrong with it raises once the library is linked."""
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        extension = ex.submit(_extension, force)
+        _library(force)
+        extension.result()
     return LIB
 
 
