@@ -529,6 +529,8 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             float2 l[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) l[i] = make_float2(0.f, 0.f);
+            // this thread's scores: an address carried along (made anew each tile it spilled 44 bytes: 12 rows with weights 76 us for 71)
+            float *sc = SCORES ? a.scores + (bh * cap + w.t0 * TK + tl * KPT) * a.Rs + row0 : nullptr;
 
             for (int t = w.t0; t < w.t1; ++t, ++n) {
                 const int xs = n % XS;
@@ -594,7 +596,7 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                     for (int k = 0; k < KPT; ++k) {
                         const int key = key0 + tl * KPT + k;
                         if (key < w.len) {
-                            float *s = a.scores + (bh * cap + key) * a.Rs + row0;
+                            float *s = sc + k * a.Rs;
                             if (a.R <= 2) {
                                 if (n_rows > 0) s[0] = x[k][0].x;
                                 if (n_rows > 1) s[1] = x[k][0].y;
@@ -608,6 +610,7 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                         }
                     }
                 }
+                if (SCORES) sc += TK * a.Rs;
                 // does a key pass its row's maximum, or its term the row's largest?  Soon that is rare.
                 bool grows = false;
                 float lv[KPT];  // log2 of V's scale
