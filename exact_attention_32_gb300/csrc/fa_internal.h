@@ -130,7 +130,6 @@ struct Kv4DecodeProblem {
     int64_t B, H, n_q, max_pages;
     float scale;
     int accumulate;
-    int sm_count;
 };
 // Bytes of workspace for sequences of at most max_pages pages.
 int64_t fa_kv4_decode_workspace(int64_t B, int64_t H, int64_t heads, int64_t n_q, int64_t d, int64_t max_tokens,

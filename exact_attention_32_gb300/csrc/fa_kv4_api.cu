@@ -211,7 +211,6 @@ extern "C" int fa_fwd_kv4(const void *q, const fa_kv4_cache *cache, const int32_
     p.max_pages = max_pages;
     p.scale = scale;
     p.accumulate = accumulate;
-    p.sm_count = sm_count;
     return fa_launch_kv4_decode(p, workspace, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
