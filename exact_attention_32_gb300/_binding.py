@@ -633,7 +633,8 @@ def kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, lens: torch.Te
 
     k, v: contiguous bf16 [B, Hkv, S, d].  lens: int32 [B], the lengths AFTER
     the append; of its S rows sequence b gains the first n_new[b] (all where
-    n_new is None), as its last positions.  page_table: int32 [B, pages].
+    n_new is None), as its last positions; what lies past the table's pages is
+    dropped (FA_ERR_BAD_PAGE).  page_table: int32 [B, pages], a page that gains tokens once in it.
     weights: fp32 [B, Hkv, S], what the new tokens' weights start from (0
     where None).  Enqueued on ``stream`` (default: torch's current stream), as
     the calls below."""
@@ -664,8 +665,11 @@ def forward_kv4(q: torch.Tensor, cache: KV4Cache, lens: torch.Tensor, page_table
 
     q: contiguous bf16 [B, H, n_q, d], H a multiple of the cache's key heads;
     lens: int32 [B]; page_table: int32 [B, pages].  ``accumulate`` adds each
-    key's attention weight over these rows to cache.weights.  The workspace
-    (uint8 CUDA tensor of ``fa_fwd_kv4_workspace_bytes`` bytes) is allocated with torch when not given."""
+    key's attention weight over these rows to cache.weights; a page must then
+    appear once in the table (sequences that share one lose each other's
+    additions).  The workspace (uint8 CUDA tensor of
+    ``fa_fwd_kv4_workspace_bytes`` bytes) is allocated with torch when not
+    given; with ``accumulate`` it grows with the table's columns, used or not."""
     call = (_marshal or _calls()).forward_kv4
     if stream is None:
         r = call(q, cache, lens, page_table, scale, accumulate, workspace)

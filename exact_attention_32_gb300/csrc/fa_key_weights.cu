@@ -11,8 +11,8 @@
 // queries and adds them up in fp32, with nothing to exchange between threads.
 //
 // What bounds it: at d = 128 a tile's product and its 16384 exponentials (32 a clock and SM) take 512 cycles each, side by
-// side, at d = 64 the product half of that.  32 heads of 16384 queries, causal, take 800 us (1.38 PFLOP/s, 71 % of the
-// measured bf16 rate), and with an eighth of the exponentials still 630 to 690.
+// side, at d = 64 the product half of that.  32 heads of 16384 queries, causal, take 850 us (1.29 PFLOP/s, 67 % of the
+// measured bf16 rate; 790 to 870, as the card's power allows), and with an eighth of the exponentials still 630 to 690.
 // A product whose operands both come from shared memory
 // at N = 128 would need all of its 128 bytes a clock, so K lies in tensor memory
 // as the A operand (2 x d/2 columns, for the CTA's life) and only Q streams

@@ -34,11 +34,11 @@
 // Roles: a softmax warpgroup per 8 rows (1, 2 or 4), one thread a TMEM lane; three warps that load (K, V, the scales), a lane
 // a page (or the part of a page in the tile); a warp that issues the products.  A copy takes its warp 77 cycles to issue,
 // so one warp for all copies was too slow where pages are small (32 sequences of 8192 in pages of 16: 86 us, two warps 70,
-// three 65; in pages of 1024 58).  A softmax takes about 2000 cycles a tile, waits between
+// three 66; in pages of 1024 60).  A softmax takes about 2000 cycles a tile, waits between
 // its steps for the most part, so an SM needs several at work to keep up with the 720 cycles that a tile's bytes
 // take: three CTAs of 8 rows, two of 16, one of 32.  K and V have stages of their own, K's free as soon as S is there.
 // What a softmax needs to begin, K and the scales, comes ahead of V, which it needs at its end: with the scales behind V's
-// barrier 64 sequences of 16384 (8 key heads, 8 rows each, 1.12 GB) took 208 us, so 188, 5.9 TB/s (the copies alone 6.9).
+// barrier 64 sequences of 16384 (8 key heads, 8 rows each, 1.12 GB) took 208 us, so 190, 5.9 TB/s (the copies alone 6.9).
 // Copies of 8 bytes a lane by the load warps (cp.async) in the TMA's place took 3500 cycles
 // to issue a tile, two and a half times what all of the tile may take; TMA copies from an elected lane, box by box, more
 // than those of several lanes in one instruction (pages of 16: 102 us against 87).  Softmax code for 4 rows instead of 8, where
@@ -907,7 +907,7 @@ fa_kv4_merge_kernel(const DecodeArgs a, int RP)
 // weights[key] += sum over the rows of exp2(score - m) / l.  Memory-bound by the scores, 4 Rs bytes a key.  L lanes read a key's
 // rows, 4 C each (C = 0: one or two rows, a thread a key), and add them up; a warp has 32 U keys under way, 32 / L a turn, and
 // each lane ends with the sums of U of them.  A thread a key is as fast up to 12 rows (24 sequences of 8 key heads with 12 rows: the
-// whole call 68 us, with four lanes 70), but reads 16 bytes of a line at a time: with 32 rows 52 us for 67 MB of scores where
+// whole call 71 us, with four lanes 2 more), but reads 16 bytes of a line at a time: with 32 rows 52 us for 67 MB of scores where
 // eight lanes take 20; with 16 the whole call 63 us, with four lanes 59.
 template <int L, int C, int U>
 __global__ void __launch_bounds__(256)
@@ -1006,8 +1006,8 @@ Geometry geometry(int64_t B, int64_t H, int64_t heads, int64_t n_q, int64_t d, i
 {
     Geometry g;
     const int64_t R = H / heads * n_q, rows = B * H * n_q;
-    // 16 rows of 32 sequences of 8192 (4 key heads) take 37 to 42 us, 32 rows 69 to 78: 32 rows in one CTA 78, in two of 16 85;
-    // 40 rows in two of 32 136, in three of 16 116; 80 rows 197 and 183
+    // 32 sequences of 8192, 4 key heads: a chunk of 16 rows takes 39 to 41 us among others, one of 32 74 (32 rows in one CTA 85, in
+    // two of 16 89; 40 rows in two of 32 144, in three of 16 123; 1 key head: 80 rows 67 and 62, 96 rows 67 and 71, 176 even)
     g.rt = R <= 8 ? 1 : R <= 16 || (R + 15) / 16 * 7 < (R + 31) / 32 * 13 ? 2 : 4;
     g.n_rc = static_cast<int>((R + 8 * g.rt - 1) / (8 * g.rt));
     const int64_t tk = tile_keys(static_cast<int>(d));

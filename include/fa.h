@@ -461,8 +461,15 @@ int fa_kv4_read(const fa_kv4_cache *cache, const int32_t *first, const int32_t *
  *   workspace : device scratch, 16-byte aligned, at least
  *         fa_fwd_kv4_workspace_bytes(...) bytes; contents on entry do not
  *         matter.  Calls that share one must be ordered on one stream (or by
- *         events): two that overlap race on it.
- * Keys are read once per 32 rows of a key head.  The batch's keys are shared out among
+ *         events): two that overlap race on it.  With accumulate it holds a score a
+ *         row and token that the table has room for, whatever the lengths are
+ *         (4 B H n_q max_pages page_size bytes and more): give a table of the
+ *         columns that are in use.
+ * The rows of a key head go in chunks of at most 8, 16 or 32 (16, too, where that
+ * makes 3, 5, 7, 9 or 11 of them); its keys are read once per chunk.
+ * A row's terms p s (s: the scale of the key's V) go to the product rounded to a half
+ * under a power of two of the row: 2^-11 of themselves down to 2^-24 of the largest one,
+ * 2^-34 of that one below.  The batch's keys are shared out among
  * the SMs evenly, so where a sequence is split, and with it the last bits of its rows,
  * depends on the lengths of the whole batch; the same call gives the same bits.
  */
