@@ -1,5 +1,5 @@
 """ctypes binding of libfa.so: argument marshalling only (the tensor-level calls
-of the 4-bit cache go through the extension _marshal.cpp, which does the same faster).
+of packed sequences and of the 4-bit cache go through the extension _marshal.cpp, which does the same faster).
 
 Every function of include/fa.h is exposed under the same name; ``forward`` is
 the tensor-level convenience call.  Torch supplies device memory and the
@@ -25,11 +25,12 @@ _lock = threading.Lock()
 FA_OK = 0
 STATUS_NAMES = {0: "FA_OK", 1: "FA_ERR_INVALID_ARG", 2: "FA_ERR_UNSUPPORTED", 3: "FA_ERR_NO_DEVICE",
                 4: "FA_ERR_ARCH", 5: "FA_ERR_LAUNCH", 6: "FA_ERR_TIMEOUT", 7: "FA_ERR_WORKSPACE_LIMIT",
-                8: "FA_ERR_BAD_PAGE"}
+                8: "FA_ERR_BAD_PAGE", 9: "FA_ERR_BAD_SEQUENCE"}
 EXPORTED = ("fa_fwd", "fa_fwd_kernel", "fa_bh_partition", "fa_kv_shard", "fa_fwd_kv_shard", "fa_fwd_slab", "fa_fwd_host", "fa_fwd_mma", "fa_fwd_splitkv", "fa_fwd_splitkv_workspace_bytes", "fa_combine",
             "fa_fwd_splitkv_noalloc", "fa_fwd_fp8", "fa_fwd_blocksparse", "fa_bwd", "fa_bwd_workspace_bytes", "fa_get_device_status",
             "fa_status_string", "fa_version", "fa_kv4_append", "fa_kv4_read", "fa_fwd_kv4", "fa_fwd_kv4_workspace_bytes",
-            "fa_kv4_evict", "fa_key_weights")
+            "fa_kv4_evict", "fa_key_weights", "fa_fwd_kv4_tree", "fa_kv4_keep", "fa_kv4_copy_pages", "fa_packed_plan",
+            "fa_packed_plan_bytes", "fa_fwd_packed", "fa_bwd_packed", "fa_bwd_packed_workspace_bytes")
 
 
 class KV4CacheStruct(ctypes.Structure):
@@ -37,6 +38,11 @@ class KV4CacheStruct(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p), ("weights", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
                 ("Hkv", ctypes.c_int64), ("page_size", ctypes.c_int64), ("d", ctypes.c_int64)]
+
+
+class RowsStruct(ctypes.Structure):
+    """``fa_rows`` of include/fa.h."""
+    _fields_ = [("p", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
 class FAError(RuntimeError):
@@ -109,6 +115,24 @@ def lib():
             L.fa_kv4_evict.argtypes = [cp, vp, vp, i64, cp, vp, i64, i64, i64, i64, vp, vp, vp]
             L.fa_key_weights.restype = ctypes.c_int
             L.fa_key_weights.argtypes = [vp, vp, vp, vp, i64, i64, i64, i64, i64, ctypes.c_float, ctypes.c_int, i64, vp]
+            L.fa_fwd_kv4_tree.restype = ctypes.c_int
+            L.fa_fwd_kv4_tree.argtypes = [vp, cp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, ctypes.c_float, vp, i64, vp]
+            L.fa_kv4_keep.restype = ctypes.c_int
+            L.fa_kv4_keep.argtypes = [cp, vp, vp, i64, vp, vp, vp, i64, i64, vp, vp]
+            L.fa_kv4_copy_pages.restype = ctypes.c_int
+            L.fa_kv4_copy_pages.argtypes = [cp, vp, cp, vp, i64, vp]
+            rp = ctypes.POINTER(RowsStruct)
+            L.fa_packed_plan.restype = ctypes.c_int
+            L.fa_packed_plan.argtypes = [vp, i64, i64, ctypes.c_int, vp, i64, vp]
+            L.fa_packed_plan_bytes.restype = i64
+            L.fa_packed_plan_bytes.argtypes = [i64, i64]
+            L.fa_fwd_packed.restype = ctypes.c_int
+            L.fa_fwd_packed.argtypes = [rp] * 4 + [vp, vp] + [i64] * 5 + [ctypes.c_float, ctypes.c_int, ctypes.c_int, vp]
+            L.fa_bwd_packed.restype = ctypes.c_int
+            L.fa_bwd_packed.argtypes = [rp] * 4 + [vp] + [rp] * 4 + [vp] + [i64] * 5 + [ctypes.c_float, ctypes.c_int,
+                                                                                       ctypes.c_int, vp, i64, vp]
+            L.fa_bwd_packed_workspace_bytes.restype = i64
+            L.fa_bwd_packed_workspace_bytes.argtypes = [i64] * 5
             L.fa_get_device_status.restype = ctypes.c_int
             L.fa_get_device_status.argtypes = [vp]
             L.fa_status_string.restype = ctypes.c_char_p
@@ -259,6 +283,51 @@ def fa_kv4_evict(cache, lens, page_table, max_pages, to, to_table, to_max_pages,
 def fa_key_weights(q, k, lse, weights, B, H, Hkv, N, d, scale, causal, first_query, stream) -> int:
     """Raw call of the accumulated attention weight of a prompt's keys."""
     return lib().fa_key_weights(q, k, lse, weights, B, H, Hkv, N, d, scale, int(causal), first_query, stream)
+
+
+def fa_fwd_kv4_tree(q, cache, lens, page_table, tree, n_new, o, lse, B, H, n_q, max_pages, scale, workspace,
+                    workspace_bytes, stream) -> int:
+    """Raw call of attention of a tree of drafts over a 4-bit cache (caller-owned workspace)."""
+    return lib().fa_fwd_kv4_tree(q, ctypes.byref(cache), lens, page_table, tree, n_new, o, lse, B, H, n_q, max_pages,
+                                 scale, workspace, workspace_bytes, stream)
+
+
+def fa_kv4_keep(cache, lens, page_table, max_pages, path, n_path, n_new, B, n_draft, new_lens, stream) -> int:
+    """Raw call of keeping an accepted path of the drafts in a 4-bit cache."""
+    return lib().fa_kv4_keep(ctypes.byref(cache), lens, page_table, max_pages, path, n_path, n_new, B, n_draft, new_lens,
+                             stream)
+
+
+def fa_kv4_copy_pages(cache, pages, to, to_pages, n, stream) -> int:
+    """Raw call of copying pages of a 4-bit cache."""
+    return lib().fa_kv4_copy_pages(ctypes.byref(cache), pages, ctypes.byref(to), to_pages, n, stream)
+
+
+def fa_packed_plan(cu_seqlens, B, T, causal, plan, plan_bytes, stream) -> int:
+    """Raw call of making a packed batch's plan."""
+    return lib().fa_packed_plan(cu_seqlens, B, T, int(causal), plan, plan_bytes, stream)
+
+
+def fa_packed_plan_bytes(B, T) -> int:
+    return lib().fa_packed_plan_bytes(B, T)
+
+
+def fa_fwd_packed(q, k, v, o, lse, plan, B, T, H, Hkv, d, scale, causal, fill, stream) -> int:
+    """Raw call of the forward of packed sequences; q, k, v and o are ``RowsStruct``."""
+    return lib().fa_fwd_packed(*(ctypes.byref(t) for t in (q, k, v, o)), lse, plan, B, T, H, Hkv, d, scale, int(causal),
+                               int(fill), stream)
+
+
+def fa_bwd_packed(q, k, v, o, lse, dout, dq, dk, dv, plan, B, T, H, Hkv, d, scale, causal, fill, workspace,
+                  workspace_bytes, stream) -> int:
+    """Raw call of the backward of packed sequences; tensors are ``RowsStruct``, the workspace the caller's."""
+    return lib().fa_bwd_packed(*(ctypes.byref(t) for t in (q, k, v, o)), lse,
+                               *(ctypes.byref(t) for t in (dout, dq, dk, dv)), plan, B, T, H, Hkv, d, scale, int(causal),
+                               int(fill), workspace, workspace_bytes, stream)
+
+
+def fa_bwd_packed_workspace_bytes(B, T, H, Hkv, d) -> int:
+    return lib().fa_bwd_packed_workspace_bytes(B, T, H, Hkv, d)
 
 
 def fa_get_device_status(stream=0) -> int:
@@ -611,7 +680,9 @@ def _calls():
         except ImportError as e:
             raise RuntimeError("_marshal is missing: build it with exact_attention_32_gb300.build.build()") from e
         at = [ctypes.cast(f, ctypes.c_void_p).value for f in (
-            L.fa_kv4_append, L.fa_kv4_read, L.fa_fwd_kv4, L.fa_fwd_kv4_workspace_bytes, L.fa_kv4_evict, L.fa_key_weights)]
+            L.fa_kv4_append, L.fa_kv4_read, L.fa_fwd_kv4, L.fa_fwd_kv4_workspace_bytes, L.fa_kv4_evict, L.fa_key_weights,
+            L.fa_fwd_kv4_tree, L.fa_kv4_keep, L.fa_kv4_copy_pages, L.fa_packed_plan, L.fa_packed_plan_bytes, L.fa_fwd_packed,
+            L.fa_bwd_packed, L.fa_bwd_packed_workspace_bytes)]
         m.setup(FAError, tuple(at))
         _marshal = m
     return _marshal
@@ -706,3 +777,132 @@ def key_weights(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor, scale: floa
         if r is not NotImplemented:
             return r
     return _elsewhere(call, q.device, stream, q, k, lse, scale, causal, first_query)
+
+
+def forward_kv4_tree(q: torch.Tensor, cache: KV4Cache, lens: torch.Tensor, page_table: torch.Tensor, tree: torch.Tensor,
+                     n_new: torch.Tensor | None = None, scale: float | None = None,
+                     workspace: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None):
+    """(O bf16 [B, H, n_q, d], LSE fp32 [B, H, n_q]) by ``fa_fwd_kv4_tree``: the newest tokens of each sequence
+    are a tree of drafts (their keys already appended), and each attends to the tokens before the drafts and to
+    the drafts that its mask names.
+
+    q, cache, lens, page_table, scale, workspace: ``forward_kv4``'s (without ``accumulate``).  tree: int64
+    [B, n_q], bit i of tree[b, t] set where draft t admits draft i: its ancestors and itself.  n_new: int32
+    [B], how many of the n_q drafts a sequence has (all where None); rows behind them get O = 0, LSE = -inf."""
+    call = (_marshal or _calls()).forward_kv4_tree
+    if stream is None:
+        r = call(q, cache, lens, page_table, tree, n_new, scale, workspace)
+        if r is not NotImplemented:
+            return r
+    return _elsewhere(call, q.device, stream, q, cache, lens, page_table, tree, n_new, scale, workspace)
+
+
+def kv4_keep(cache: KV4Cache, lens: torch.Tensor, page_table: torch.Tensor, path: torch.Tensor, n_path: torch.Tensor,
+             n_new: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """int32 [B], the new lengths, by ``fa_kv4_keep``: of each sequence's drafts (its newest n_new[b] tokens; as
+    many as ``path`` has columns where n_new is None) those that path[b, :n_path[b]] names stay, in order, at the
+    front of them.
+
+    path: int32 [B, drafts], up to 64 columns, ascending numbers of drafts; n_path: int32 [B]."""
+    call = (_marshal or _calls()).kv4_keep
+    if stream is None:
+        r = call(cache, lens, page_table, path, n_path, n_new)
+        if r is not NotImplemented:
+            return r
+    return _elsewhere(call, lens.device, stream, cache, lens, page_table, path, n_path, n_new)
+
+
+def kv4_copy_pages(cache: KV4Cache, pages: torch.Tensor, to: KV4Cache, to_pages: torch.Tensor,
+                   stream: torch.cuda.Stream | None = None) -> None:
+    """Copy page pages[i] of ``cache`` to page to_pages[i] of ``to`` (the same cache, or another of the same layout) by
+    ``fa_kv4_copy_pages``, with the weights where both have them.
+
+    pages, to_pages: int32 [n]; a negative page leaves its pair out.  No page is copied to twice, nor to and from."""
+    args = (cache, pages, to, to_pages)
+    call = (_marshal or _calls()).kv4_copy_pages
+    if stream is not None or call(*args) is NotImplemented:
+        _elsewhere(call, pages.device, stream, *args)
+
+
+class PackedPlan(NamedTuple):
+    """The work of a packed batch (``packed_plan``): device memory, and what it was made for."""
+    table: torch.Tensor
+    tokens: int
+    sequences: int
+    causal: bool
+
+
+def packed_plan(cu_seqlens: torch.Tensor, tokens: int, causal: bool = False,
+                stream: torch.cuda.Stream | None = None) -> PackedPlan:
+    """The plan of a packed batch by ``fa_packed_plan``: made once, for every layer and both directions.
+
+    cu_seqlens: int32 [sequences + 1] on a CUDA device, ascending in [0, tokens]; sequence b has the rows
+    cu_seqlens[b] .. cu_seqlens[b + 1] - 1.  The offsets are read on the device, at the call."""
+    call = (_marshal or _calls()).packed_plan
+    table = call(cu_seqlens, tokens, causal) if stream is None else NotImplemented
+    if table is NotImplemented:
+        table = _elsewhere(call, cu_seqlens.device, stream, cu_seqlens, tokens, causal)
+    return PackedPlan(table, int(tokens), cu_seqlens.shape[0] - 1, bool(causal))
+
+
+def forward_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                   scale: float | None = None, causal: bool = False, plan: PackedPlan | None = None,
+                   out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                   stream: torch.cuda.Stream | None = None):
+    """(O bf16 [T, H, d], LSE fp32 [H, T]) by ``fa_fwd_packed``: attention of each of the packed sequences over itself.
+
+    q: bf16 [T, H, d]; k, v: [T, Hkv, d], H a multiple of Hkv, any strides with the last axis contiguous (slices of
+    one projection's output).  cu_seqlens: int32 [sequences + 1], the sequences' offsets; ``plan``: packed_plan's
+    for them, made here where None.  Rows of no sequence get O = 0 and LSE = -inf in tensors that the call
+    allocates, and are left alone in ``out`` and ``lse`` where those are given."""
+    call = (_marshal or _calls()).forward_packed
+    if stream is None:
+        r = call(q, k, v, cu_seqlens, scale, causal, plan, out, lse)
+        if r is not NotImplemented:
+            return r
+    return _elsewhere(call, q.device, stream, q, k, v, cu_seqlens, scale, causal, plan, out, lse)
+
+
+def backward_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor, lse: torch.Tensor,
+                    dout: torch.Tensor, cu_seqlens: torch.Tensor, scale: float | None = None, causal: bool = False,
+                    plan: PackedPlan | None = None, workspace: torch.Tensor | None = None, out=None,
+                    stream: torch.cuda.Stream | None = None):
+    """(dQ, dK, dV) like q, k, v by ``fa_bwd_packed``; o and lse are ``forward_packed``'s outputs for the same batch.
+
+    The workspace (uint8 CUDA tensor of ``fa_bwd_packed_workspace_bytes`` bytes) is allocated where not given; ``out``: (dq, dk,
+    dv) to write into (slices of one gradient, if wanted), whose rows of no sequence are left alone; in
+    tensors that the call allocates those are zeros."""
+    call = (_marshal or _calls()).backward_packed
+    out = None if out is None else tuple(out)
+    if stream is None:
+        r = call(q, k, v, o, lse, dout, cu_seqlens, scale, causal, plan, workspace, out)
+        if r is not NotImplemented:
+            return r
+    return _elsewhere(call, q.device, stream, q, k, v, o, lse, dout, cu_seqlens, scale, causal, plan, workspace, out)
+
+
+class _AttentionPacked(torch.autograd.Function):
+    """fa_fwd_packed in the forward, fa_bwd_packed in the backward (O, LSE and the plan saved)."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, cu_seqlens, scale, causal, plan):
+        if plan is None:
+            plan = packed_plan(cu_seqlens, q.shape[0], causal=causal)
+        o, lse = forward_packed(q, k, v, cu_seqlens, scale=scale, causal=causal, plan=plan)
+        ctx.save_for_backward(q, k, v, o, lse, cu_seqlens, plan.table)
+        ctx.scale, ctx.causal, ctx.plan = scale, causal, plan[1:]
+        return o
+
+    @staticmethod
+    def backward(ctx, dout):
+        q, k, v, o, lse, cu_seqlens, table = ctx.saved_tensors
+        grads = backward_packed(q, k, v, o, lse, dout.contiguous(), cu_seqlens, scale=ctx.scale, causal=ctx.causal,
+                                plan=PackedPlan(table, *ctx.plan))
+        return (*grads, None, None, None, None)
+
+
+def attention_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                     scale: float | None = None, causal: bool = False, plan: PackedPlan | None = None) -> torch.Tensor:
+    """O = ``forward_packed``'s with autograd: ``fa_fwd_packed`` forward, ``fa_bwd_packed`` backward.  A plan that
+    several layers share is made once with ``packed_plan`` and given."""
+    return _AttentionPacked.apply(q, k, v, cu_seqlens, scale, bool(causal), plan)

@@ -1,5 +1,6 @@
 // C ABI of libfa.so: argument validation, device checks and kernel dispatch.
 // The operation and every argument are documented in include/fa.h.
+#include <cuda.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -20,6 +21,24 @@ struct DeviceInfo {
 DeviceInfo g_devices[kMaxDevices];
 std::mutex g_devices_mu;
 
+// A host thread that has made no CUDA call yet (one of autograd's, a server's worker) has a current device but no
+// context, which the encoding of a tensor map asks for: it gets the device's.  A context of the caller's own stays.
+void bind_context(int dev)
+{
+    typedef CUresult (*GetCurrent)(CUcontext *);
+    static const GetCurrent get = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuCtxGetCurrent", &p, 4000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            return reinterpret_cast<GetCurrent>(p);
+        cudaGetLastError();
+        return GetCurrent(nullptr);
+    }();
+    CUcontext c = nullptr;
+    if (get != nullptr && get(&c) == CUDA_SUCCESS && c == nullptr && cudaSetDevice(dev) != cudaSuccess) cudaGetLastError();
+}
+
 int current_device(int *dev, int *sm_count)
 {
     if (cudaGetDevice(dev) != cudaSuccess) {
@@ -27,6 +46,7 @@ int current_device(int *dev, int *sm_count)
         return FA_ERR_NO_DEVICE;
     }
     if (*dev < 0 || *dev >= kMaxDevices) return FA_ERR_NO_DEVICE;
+    bind_context(*dev);
     std::lock_guard<std::mutex> lock(g_devices_mu);
     DeviceInfo &info = g_devices[*dev];
     if (!info.checked) {
@@ -553,9 +573,14 @@ extern "C" int fa_get_device_status(void *stream)
     const int weights = fa_key_weights_take_status(static_cast<cudaStream_t>(stream));
     const int decode = fa_kv4_decode_take_status(static_cast<cudaStream_t>(stream));
     const int cache = fa_kv4_cache_take_status(static_cast<cudaStream_t>(stream));
-    for (const int st : {fwd, dp, bwd, weights, decode})
+    const int move = fa_kv4_move_take_status(static_cast<cudaStream_t>(stream));
+    const int plan = fa_packed_plan_take_status(static_cast<cudaStream_t>(stream));
+    const int packed_fwd = fa_packed_fwd_take_status(static_cast<cudaStream_t>(stream));
+    const int packed_bwd = fa_packed_bwd_take_status(static_cast<cudaStream_t>(stream));
+    // (the packed kernels' own before the plan's: a wait that gave up counts for more than offsets)
+    for (const int st : {fwd, dp, bwd, weights, decode, cache, move, packed_fwd, packed_bwd})
         if (st != FA_OK) return st;
-    return cache;
+    return plan;
 }
 
 extern "C" const char *fa_status_string(int status)
@@ -571,6 +596,8 @@ extern "C" const char *fa_status_string(int status)
     case FA_ERR_WORKSPACE_LIMIT:
         return "FA_ERR_WORKSPACE_LIMIT: the problem needs more scratch than the static array holds";
     case FA_ERR_BAD_PAGE: return "FA_ERR_BAD_PAGE: a page index or a length lay outside the cache";
+    case FA_ERR_BAD_SEQUENCE:
+        return "FA_ERR_BAD_SEQUENCE: offsets of packed sequences do not ascend inside the tensors, or the plan is another batch's";
     default: return "unknown fa_status";
     }
 }

@@ -120,6 +120,19 @@ struct Kv4EvictProblem {
 cudaError_t fa_launch_kv4_evict(const Kv4EvictProblem &p, cudaStream_t stream);
 int fa_kv4_cache_take_status(cudaStream_t stream);
 
+// fa_kv4_keep / fa_kv4_copy_pages on validated arguments (fa_kv4_move.cu).
+struct Kv4KeepProblem {
+    Kv4Cache cache;
+    const int32_t *lens, *table, *path, *n_path, *n_new;
+    int32_t *new_lens;
+    int64_t B, max_pages;
+    int n_draft;
+};
+cudaError_t fa_launch_kv4_keep(const Kv4KeepProblem &p, cudaStream_t stream);
+cudaError_t fa_launch_kv4_copy(const Kv4Cache &from, const int32_t *pages, const Kv4Cache &to, const int32_t *to_pages, int64_t n,
+                               int sm_count, cudaStream_t stream);
+int fa_kv4_move_take_status(cudaStream_t stream);
+
 // Attention over the 4-bit cache (fa_kv4_decode.cu).
 struct Kv4DecodeProblem {
     Kv4Cache cache;
@@ -130,6 +143,8 @@ struct Kv4DecodeProblem {
     int64_t B, H, n_q, max_pages;
     float scale;
     int accumulate;
+    const uint64_t *tree = nullptr;   // fa_fwd_kv4_tree: [B][n_q] masks over the drafts (accumulate is then 0),
+    const int32_t *n_new = nullptr;   // and their numbers, or null
 };
 // Bytes of workspace for sequences of at most max_pages pages.
 int64_t fa_kv4_decode_workspace(int64_t B, int64_t H, int64_t heads, int64_t n_q, int64_t d, int64_t max_tokens,
@@ -150,6 +165,31 @@ struct FaKeyWeightsProblem {
 };
 cudaError_t fa_launch_key_weights(const FaKeyWeightsProblem &p, cudaStream_t stream);
 int fa_key_weights_take_status(cudaStream_t stream);
+
+// Packed sequences.  A tensor [T][heads][d], d contiguous, strides in elements; the caller's (fa_packed_api.cu checked it).
+struct FaRows {
+    void *p;
+    int64_t token_stride, head_stride;
+};
+int64_t fa_packed_plan_size(int64_t B, int64_t T);
+cudaError_t fa_launch_packed_plan(const int32_t *cu_seqlens, int64_t B, int64_t T, int causal, void *plan, cudaStream_t stream);
+int fa_packed_plan_take_status(cudaStream_t stream);
+struct FaPackedProblem {
+    FaRows q, k, v, o;
+    float *lse;  // [H][T]
+    void *plan;
+    int64_t B, T, H, Hkv;
+    int d;
+    float scale;
+    int causal, fill;  // fill: zeros (LSE: -inf) in rows of no sequence
+    int sm_count;
+    FaRows dout, dq, dk, dv;  // backward only (o and lse are then inputs)
+};
+cudaError_t fa_launch_packed_fwd(const FaPackedProblem &p, cudaStream_t stream);
+int fa_packed_fwd_take_status(cudaStream_t stream);
+int64_t fa_packed_bwd_workspace_size(int64_t B, int64_t T, int64_t H, int64_t Hkv, int64_t d);
+cudaError_t fa_launch_packed_bwd(const FaPackedProblem &p, void *workspace, cudaStream_t stream);
+int fa_packed_bwd_take_status(cudaStream_t stream);
 
 // Forward on host buffers (fa_fwd_host): q, k, v, o, lse are host pointers,
 // *_dev the caller's device staging buffers of the same shapes; the (b, h)

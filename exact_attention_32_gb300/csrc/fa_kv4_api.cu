@@ -171,9 +171,12 @@ extern "C" int64_t fa_fwd_kv4_workspace_bytes(int64_t B, int64_t H, int64_t Hkv,
     return fa_kv4_decode_workspace(B, H, Hkv, n_q, d, max_tokens, accumulate);
 }
 
-extern "C" int fa_fwd_kv4(const void *q, const fa_kv4_cache *cache, const int32_t *lens, const int32_t *page_table,
-                          void *o, float *lse, int64_t B, int64_t H, int64_t n_q, int64_t max_pages, float scale,
-                          int accumulate, void *workspace, int64_t workspace_bytes, void *stream)
+namespace {
+
+// fa_fwd_kv4, and with masks fa_fwd_kv4_tree.
+int attend(const void *q, const fa_kv4_cache *cache, const int32_t *lens, const int32_t *page_table, const uint64_t *tree,
+           const int32_t *n_new, void *o, float *lse, int64_t B, int64_t H, int64_t n_q, int64_t max_pages, float scale,
+           int accumulate, void *workspace, int64_t workspace_bytes, void *stream)
 {
     int st = check_cache_sizes(cache);
     if (st != FA_OK || (st = check_table_sizes(cache, B, max_pages)) != FA_OK) return st;
@@ -190,13 +193,16 @@ extern "C" int fa_fwd_kv4(const void *q, const fa_kv4_cache *cache, const int32_
     for (const void *p : {static_cast<const void *>(lse), static_cast<const void *>(lens),
                           static_cast<const void *>(page_table)})
         if ((st = fa_check_device_pointer(p, dev, 4)) != FA_OK) return st;
+    if (tree != nullptr && (st = fa_check_device_pointer(tree, dev, 8)) != FA_OK) return st;
+    if (n_new != nullptr && (st = fa_check_device_pointer(n_new, dev, 4)) != FA_OK) return st;
     Range c[5];
     cache_ranges(cache, c);
     const int64_t rows = B * H * n_q;
     const Range out[4] = {{o, bytes(rows * cache->d * 2)}, {lse, bytes(rows * 4)}, {workspace, bytes(need)},
                           {c[4].p, accumulate ? c[4].bytes : 0}};
-    const Range in[7] = {{q, bytes(rows * cache->d * 2)}, c[0], c[1], c[2], c[3], {lens, bytes(B * 4)},
-                         {page_table, bytes(B * max_pages * 4)}};
+    const Range in[9] = {{q, bytes(rows * cache->d * 2)}, c[0], c[1], c[2], c[3], {lens, bytes(B * 4)},
+                         {page_table, bytes(B * max_pages * 4)}, {tree, tree ? bytes(B * n_q * 8) : 0},
+                         {n_new, n_new ? bytes(B * 4) : 0}};
     if (!outputs_clear(out, in)) return FA_ERR_INVALID_ARG;
     Kv4DecodeProblem p;
     p.cache = view(cache);
@@ -211,7 +217,98 @@ extern "C" int fa_fwd_kv4(const void *q, const fa_kv4_cache *cache, const int32_
     p.max_pages = max_pages;
     p.scale = scale;
     p.accumulate = accumulate;
+    p.tree = tree;
+    p.n_new = n_new;
     return fa_launch_kv4_decode(p, workspace, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+// Two caches of one layout: the same pool, or arrays apart.
+int check_same_layout(const fa_kv4_cache *a, const fa_kv4_cache *b)
+{
+    return a->Hkv == b->Hkv && a->page_size == b->page_size && a->d == b->d ? FA_OK : FA_ERR_INVALID_ARG;
+}
+bool one_pool_or_two(const Range (&a)[5], const Range (&b)[5])
+{
+    for (int i = 0; i < 5; ++i)
+        for (int j = 0; j < 5; ++j)
+            if (meet(a[i], b[j]) && !(i == j && a[i].p == b[j].p)) return false;
+    return true;
+}
+
+}  // namespace
+
+extern "C" int fa_fwd_kv4(const void *q, const fa_kv4_cache *cache, const int32_t *lens, const int32_t *page_table,
+                          void *o, float *lse, int64_t B, int64_t H, int64_t n_q, int64_t max_pages, float scale,
+                          int accumulate, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    return attend(q, cache, lens, page_table, nullptr, nullptr, o, lse, B, H, n_q, max_pages, scale, accumulate, workspace,
+                  workspace_bytes, stream);
+}
+
+extern "C" int fa_fwd_kv4_tree(const void *q, const fa_kv4_cache *cache, const int32_t *lens, const int32_t *page_table,
+                               const uint64_t *tree, const int32_t *n_new, void *o, float *lse, int64_t B, int64_t H,
+                               int64_t n_q, int64_t max_pages, float scale, void *workspace, int64_t workspace_bytes,
+                               void *stream)
+{
+    if (tree == nullptr) return FA_ERR_INVALID_ARG;
+    return attend(q, cache, lens, page_table, tree, n_new, o, lse, B, H, n_q, max_pages, scale, 0, workspace, workspace_bytes, stream);
+}
+
+extern "C" int fa_kv4_keep(const fa_kv4_cache *cache, const int32_t *lens, const int32_t *page_table, int64_t max_pages,
+                           const int32_t *path, const int32_t *n_path, const int32_t *n_new, int64_t B, int64_t n_draft,
+                           int32_t *new_lens, void *stream)
+{
+    int st = check_cache_sizes(cache);
+    if (st != FA_OK || (st = check_table_sizes(cache, B, max_pages)) != FA_OK) return st;
+    if (n_draft < 1 || n_draft > 64) return FA_ERR_INVALID_ARG;
+    int dev = 0, sm_count = 0;
+    if ((st = fa_current_device(&dev, &sm_count)) != FA_OK || (st = check_cache_pointers(cache, dev)) != FA_OK) return st;
+    for (const void *p : {static_cast<const void *>(lens), static_cast<const void *>(page_table), static_cast<const void *>(path),
+                          static_cast<const void *>(n_path), static_cast<const void *>(new_lens)})
+        if ((st = fa_check_device_pointer(p, dev, 4)) != FA_OK) return st;
+    if (n_new != nullptr && (st = fa_check_device_pointer(n_new, dev, 4)) != FA_OK) return st;
+    Range c[5];
+    cache_ranges(cache, c);
+    const Range out[6] = {c[0], c[1], c[2], c[3], c[4], {new_lens, bytes(B * 4)}};
+    const Range in[5] = {{lens, bytes(B * 4)}, {page_table, bytes(B * max_pages * 4)}, {path, bytes(B * n_draft * 4)},
+                         {n_path, bytes(B * 4)}, {n_new, n_new ? bytes(B * 4) : 0}};
+    if (!outputs_clear(out, in)) return FA_ERR_INVALID_ARG;
+    Kv4KeepProblem p;
+    p.cache = view(cache);
+    p.lens = lens;
+    p.table = page_table;
+    p.path = path;
+    p.n_path = n_path;
+    p.n_new = n_new;
+    p.new_lens = new_lens;
+    p.B = B;
+    p.max_pages = max_pages;
+    p.n_draft = static_cast<int>(n_draft);
+    return fa_launch_kv4_keep(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+extern "C" int fa_kv4_copy_pages(const fa_kv4_cache *from, const int32_t *pages, const fa_kv4_cache *to, const int32_t *to_pages,
+                                 int64_t n, void *stream)
+{
+    int st = check_cache_sizes(from);
+    if (st != FA_OK || (st = check_cache_sizes(to)) != FA_OK || (st = check_same_layout(from, to)) != FA_OK) return st;
+    if (n < 1 || n > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
+    // a page's pieces are counted in 31 bits
+    if (from->Hkv * from->page_size > (int64_t(1) << 28) / from->d) return FA_ERR_INVALID_ARG;
+    int dev = 0, sm_count = 0;
+    if ((st = fa_current_device(&dev, &sm_count)) != FA_OK || (st = check_cache_pointers(from, dev)) != FA_OK ||
+        (st = check_cache_pointers(to, dev)) != FA_OK)
+        return st;
+    for (const void *p : {static_cast<const void *>(pages), static_cast<const void *>(to_pages)})
+        if ((st = fa_check_device_pointer(p, dev, 4)) != FA_OK) return st;
+    Range cf[5], out[5];
+    cache_ranges(from, cf);
+    cache_ranges(to, out);
+    const Range in[2] = {{pages, bytes(n * 4)}, {to_pages, bytes(n * 4)}};
+    if (!outputs_clear(out, in) || !one_pool_or_two(cf, out)) return FA_ERR_INVALID_ARG;
+    return fa_launch_kv4_copy(view(from), pages, view(to), to_pages, n, sm_count, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? FA_OK
+               : FA_ERR_LAUNCH;
 }
 
 extern "C" int fa_kv4_evict(const fa_kv4_cache *from, const int32_t *lens, const int32_t *page_table,
@@ -222,7 +319,7 @@ extern "C" int fa_kv4_evict(const fa_kv4_cache *from, const int32_t *lens, const
     if (st != FA_OK || (st = check_cache_sizes(to)) != FA_OK) return st;
     if ((st = check_table_sizes(from, B, max_pages)) != FA_OK || (st = check_table_sizes(to, B, to_max_pages)) != FA_OK)
         return st;
-    if (from->Hkv != to->Hkv || from->page_size != to->page_size || from->d != to->d) return FA_ERR_INVALID_ARG;
+    if ((st = check_same_layout(from, to)) != FA_OK) return st;
     if (from->weights == nullptr || to->weights == nullptr) return FA_ERR_INVALID_ARG;
     if (keep < 1 || recent < 0 || recent > keep || keep > to_max_pages * to->page_size) return FA_ERR_INVALID_ARG;
     int dev = 0, sm_count = 0;
@@ -245,9 +342,7 @@ extern "C" int fa_kv4_evict(const fa_kv4_cache *from, const int32_t *lens, const
     for (int i = 5; i < 7; ++i)
         for (const Range &r : cf)
             if (meet(out[i], r)) return FA_ERR_INVALID_ARG;
-    for (int i = 0; i < 5; ++i)
-        for (int j = 0; j < 5; ++j)  // the same array of one pool, or arrays apart
-            if (meet(cf[i], ct[j]) && !(i == j && cf[i].p == ct[j].p)) return FA_ERR_INVALID_ARG;
+    if (!one_pool_or_two(cf, ct)) return FA_ERR_INVALID_ARG;
     Kv4EvictProblem p;
     p.from = view(from);
     p.to = view(to);

@@ -81,6 +81,8 @@ struct DecodeArgs {
     Kv4Cache c;
     const __nv_bfloat16 *q;
     const int32_t *lens, *table;
+    const uint64_t *tree;  // [B][n_q] which drafts a row admits, and how many a sequence has (or null); TREE only
+    const int32_t *n_new;
     __nv_bfloat16 *o;
     float *lse;
     float *part_o;     // [CTA][2][RP][D], unnormalised; slot 0: the segment that starts its share, 1: that ends it
@@ -249,7 +251,8 @@ __device__ __forceinline__ bool wait_both(uint32_t bar0, uint32_t phase0, uint32
 __device__ __forceinline__ uint32_t lo32(uint64_t x) { return static_cast<uint32_t>(x); }
 __device__ __forceinline__ uint32_t hi32(uint64_t x) { return static_cast<uint32_t>(x >> 32); }
 
-template <int D, int RT, bool SCORES>
+// TREE: the newest tokens are drafts, and which of them a row admits is a bit mask; the tokens before them everyone admits.
+template <int D, int RT, bool SCORES, bool TREE>
 __global__ void __launch_bounds__(DecCfg<D, RT>::kThreads, DecCfg<D, RT>::kPerSm)
 fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const DecodeArgs a)
 {
@@ -479,6 +482,12 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             const int h = w.it / a.n_rc, rc = w.it - h * a.n_rc;
             const int64_t bh = static_cast<int64_t>(w.b) * a.c.heads + h;
             const int row0 = rc * RP + g * 8, n_rows = min(8, a.R - row0);  // (0 or less: this group has padding only)
+            // newest tokens that not every row admits: all n_q, whatever the length is, or the sequence's drafts
+            int newest = a.n_q;
+            if constexpr (TREE) {
+                newest = min(newest, w.len);
+                if (a.n_new != nullptr) newest = min(max(a.n_new[w.b], 0), newest);
+            }
             // Q: 8 channels a thread, D / 8 threads a row
             constexpr int TPR = D / 8;
             if (tl < 8 * TPR) {
@@ -577,7 +586,7 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                         }
                 }
                 // keys that a row does not admit, or that no page holds, leave it; what lies there may be anything
-                const bool edge = key0 + TK > w.len - a.n_q + 1 || __any_sync(0xffffffffu, !here);
+                const bool edge = key0 + TK > w.len - newest + (TREE ? 0 : 1) || __any_sync(0xffffffffu, !here);
                 if (edge) {
 #pragma unroll
                     for (int k = 0; k < KPT; ++k) {
@@ -586,8 +595,15 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                         if (gone) vs[k] = 0.f;
 #pragma unroll
                         for (int r = 0; r < 8; ++r) {
-                            const int limit = w.len - a.n_q + 1 + (row0 + r) % a.n_q;
-                            if (gone || key >= limit) (r & 1 ? x[k][r / 2].y : x[k][r / 2].x) = -INFINITY;
+                            bool out = gone;
+                            if constexpr (TREE) {
+                                const int draft = key - (w.len - newest);
+                                const uint64_t seen = a.tree[static_cast<int64_t>(w.b) * a.n_q + (row0 + r) % a.n_q];
+                                out |= draft >= 0 && ((seen >> (draft & 63)) & 1u) == 0;
+                            } else {
+                                out |= key >= w.len - a.n_q + 1 + (row0 + r) % a.n_q;
+                            }
+                            if (out) (r & 1 ? x[k][r / 2].y : x[k][r / 2].x) = -INFINITY;
                         }
                     }
                 }
@@ -783,8 +799,9 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                     if (r >= n_rows) break;
                     float v = y[r];
                     if (D == 64) v += sx[r * 64 + tl];
-                    const float ll = (sm_red[r] + sm_red[8 + r]) + (sm_red[16 + r] + sm_red[24 + r]);
+                    float ll = (sm_red[r] + sm_red[8 + r]) + (sm_red[16 + r] + sm_red[24 + r]);
                     const int64_t row = bh * a.R + row0 + r;
+                    if (TREE && (row0 + r) % a.n_q >= newest) v = ll = 0.f;  // no draft of this sequence
                     if (whole) {
                         const float inv = ll == 0.f ? 0.f : 1.f / ll;
                         a.o[row * D + tl] = __float2bfloat16_rn(v * inv);
@@ -1070,23 +1087,30 @@ bool make_code_map(CUtensorMap *m, const Kv4Cache &c, void *base)
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int RT, bool SCORES>
+template <int D, int RT, bool SCORES, bool TREE>
 cudaError_t launch(const DecodeArgs &a, int ctas, cudaStream_t s)
 {
     using C = DecCfg<D, RT>;
     CUtensorMap mk, mv;
     if (!make_code_map(&mk, a.c, a.c.k) || !make_code_map(&mv, a.c, a.c.v)) return cudaErrorInvalidValue;
-    cudaError_t e = set_max_dynamic_smem<fa_kv4_decode_kernel<D, RT, SCORES>>(C::kSmemBytes);
+    cudaError_t e = set_max_dynamic_smem<fa_kv4_decode_kernel<D, RT, SCORES, TREE>>(C::kSmemBytes);
     if (e != cudaSuccess) return e;
-    fa_kv4_decode_kernel<D, RT, SCORES><<<static_cast<unsigned>(ctas), C::kThreads, C::kSmemBytes, s>>>(mk, mv, a);
+    fa_kv4_decode_kernel<D, RT, SCORES, TREE><<<static_cast<unsigned>(ctas), C::kThreads, C::kSmemBytes, s>>>(mk, mv, a);
     return cudaGetLastError();
 }
 
-template <int D, bool SCORES>
+template <int D, bool SCORES, bool TREE>
 cudaError_t launch_rt(const DecodeArgs &a, int rt, int ctas, cudaStream_t s)
 {
-    return rt == 1 ? launch<D, 1, SCORES>(a, ctas, s)
-                   : rt == 2 ? launch<D, 2, SCORES>(a, ctas, s) : launch<D, 4, SCORES>(a, ctas, s);
+    return rt == 1 ? launch<D, 1, SCORES, TREE>(a, ctas, s)
+                   : rt == 2 ? launch<D, 2, SCORES, TREE>(a, ctas, s) : launch<D, 4, SCORES, TREE>(a, ctas, s);
+}
+
+template <int D>
+cudaError_t launch_kind(const DecodeArgs &a, int rt, int ctas, cudaStream_t s)
+{
+    if (a.tree != nullptr) return launch_rt<D, false, true>(a, rt, ctas, s);
+    return a.scores != nullptr ? launch_rt<D, true, false>(a, rt, ctas, s) : launch_rt<D, false, false>(a, rt, ctas, s);
 }
 
 }  // namespace
@@ -1109,6 +1133,8 @@ cudaError_t fa_launch_kv4_decode(const Kv4DecodeProblem &p, void *workspace, cud
     a.q = static_cast<const __nv_bfloat16 *>(p.q);
     a.lens = p.lens;
     a.table = p.table;
+    a.tree = p.tree;
+    a.n_new = p.n_new;
     a.o = static_cast<__nv_bfloat16 *>(p.o);
     a.lse = p.lse;
     a.part_o = reinterpret_cast<float *>(ws + g.part_o);
@@ -1124,11 +1150,7 @@ cudaError_t fa_launch_kv4_decode(const Kv4DecodeProblem &p, void *workspace, cud
     a.Rs = g.Rs;
     a.whole = g.whole;
     a.scale_log2 = static_cast<float>(static_cast<double>(p.scale) * 1.4426950408889634);
-    cudaError_t e;
-    if (p.cache.d == 128)
-        e = p.accumulate ? launch_rt<128, true>(a, g.rt, g.ctas, stream) : launch_rt<128, false>(a, g.rt, g.ctas, stream);
-    else
-        e = p.accumulate ? launch_rt<64, true>(a, g.rt, g.ctas, stream) : launch_rt<64, false>(a, g.rt, g.ctas, stream);
+    cudaError_t e = p.cache.d == 128 ? launch_kind<128>(a, g.rt, g.ctas, stream) : launch_kind<64>(a, g.rt, g.ctas, stream);
     if (e != cudaSuccess) return e;
     if (!g.whole && g.ctas > 1) {
         // few items of many parts: 8 of 57 parts and 4 rows took 12.3 us with a block an item, 9.2 with one a row

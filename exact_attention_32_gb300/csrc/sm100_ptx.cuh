@@ -446,6 +446,13 @@ __device__ __forceinline__ void tmem_st1(uint32_t taddr, uint32_t r)
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 
+// Registers a thread of this warpgroup (all four warps execute it): what one gives up another may take, up to what
+// the block was launched with.
+template <int N>
+__device__ __forceinline__ void registers_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void registers_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
+
 // ------------------------------------------------------------------- misc
 
 __device__ __forceinline__ float ex2(float x)

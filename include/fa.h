@@ -47,8 +47,10 @@ enum fa_status {
     FA_ERR_TIMEOUT = 6,     /* a bounded in-kernel wait gave up (see fa_get_device_status) */
     FA_ERR_WORKSPACE_LIMIT = 7, /* fa_fwd_splitkv_noalloc: the problem needs more scratch
                                    than FA_SPLITKV_NOALLOC_MAX_BYTES */
-    FA_ERR_BAD_PAGE = 8 /* reported by fa_get_device_status: a kernel met a page index or a
+    FA_ERR_BAD_PAGE = 8, /* reported by fa_get_device_status: a kernel met a page index or a
                            length outside its 4-bit cache and left that part out */
+    FA_ERR_BAD_SEQUENCE = 9 /* reported by fa_get_device_status: offsets of packed sequences that do
+                           not ascend inside the tensors, or a plan made for another batch */
 };
 
 /* Size of the library-owned scratch array behind fa_fwd_splitkv_noalloc. */
@@ -376,6 +378,82 @@ int fa_bwd(const void *q, const void *k, const void *v, const void *o, const flo
 int64_t fa_bwd_workspace_bytes(int64_t B, int64_t H, int64_t N, int64_t d);
 
 /*
+ * Packed sequences: attention of sequences of different lengths that lie one behind the
+ * other in tensors of T rows, without padding, for the prompts of a serving step and for
+ * training, with H query heads on Hkv key heads (query head h reads key head
+ * h / (H / Hkv)).  The pages describe one length and equal heads; this form is this
+ * library's own.
+ *
+ * A tensor is [T][heads][d] with d contiguous and any strides (in elements, multiples of
+ * 8, the pointer 16-byte aligned): slices of one projection's output, or head-major ones.
+ * An output's rows must not meet one another, an input or another output.  (Two tensors
+ * may interleave: slices of rows of one stride.)
+ */
+typedef struct fa_rows {
+    void *p;
+    int64_t token_stride, head_stride;
+} fa_rows;
+
+/*
+ * fa_packed_plan - the work of a packed batch, made on the device from its offsets: once a
+ * batch, for every layer and both directions.  The lengths are not read by the host.
+ *
+ *   cu_seqlens : const int32 [B + 1]; sequence b has rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1
+ *                (a length of 0 is a sequence without rows).  Rows before cu_seqlens[0] or from
+ *                cu_seqlens[B] on belong to no sequence.  The offsets must ascend inside [0, T];
+ *                others are held to that (each to at least the ones before) and reported as
+ *                FA_ERR_BAD_SEQUENCE by fa_get_device_status.
+ *   B, T       : sequences and rows, 1 .. 2^31 - 512
+ *   plan       : device memory, 16-byte aligned, fa_packed_plan_bytes(B, T) bytes at least
+ * Calls that take the plan must be ordered behind this one, with the same B, T and causal (a
+ * plan of another batch is noticed by the kernels, which then do nothing and report
+ * FA_ERR_BAD_SEQUENCE).
+ */
+int fa_packed_plan(const int32_t *cu_seqlens, int64_t B, int64_t T, int causal, void *plan, int64_t plan_bytes,
+                   void *stream);
+
+/* Bytes of a plan, or -1 for invalid sizes.  Pure host computation. */
+int64_t fa_packed_plan_bytes(int64_t B, int64_t T);
+
+/*
+ * fa_fwd_packed - fa_fwd of every sequence of a packed batch: row i of a sequence admits its
+ * keys (causal: its keys j <= i) and no other sequence's, whatever those hold.
+ *
+ *   q, k, v : const bf16 [T][H][d], [T][Hkv][d], [T][Hkv][d]
+ *   o       : bf16 out [T][H][d];  lse : fp32 out, contiguous [H][T], 4-byte aligned
+ *   plan    : fa_packed_plan's, for the same B, T and causal
+ *   H, Hkv  : query heads, a multiple of the key heads;  d : 64 or 128 (else FA_ERR_UNSUPPORTED)
+ *   fill    : 1 gives rows of no sequence O = 0, LSE = -inf; 0 leaves them as they were
+ * A value of V that is not finite reaches, as in fa_fwd, the rows of its own sequence that lie in
+ * or behind its block of 128 rows (counted from the sequence's first), causal or not.  Errors as fa_fwd.
+ */
+int fa_fwd_packed(const fa_rows *q, const fa_rows *k, const fa_rows *v, const fa_rows *o, float *lse,
+                  const void *plan, int64_t B, int64_t T, int64_t H, int64_t Hkv, int64_t d, float scale,
+                  int causal, int fill, void *stream);
+
+/*
+ * fa_bwd_packed - fa_bwd of every sequence of a packed batch.  dK and dV sum over the query heads
+ * of their key head.
+ *
+ *   q, k, v, o, lse, plan, B, T, H, Hkv, d, scale, causal : fa_fwd_packed's (o and lse its outputs)
+ *   dout       : const bf16 [T][H][d]
+ *   dq, dk, dv : bf16 out [T][H][d], [T][Hkv][d], [T][Hkv][d]
+ *   fill       : 1 gives rows of no sequence zeros; 0 leaves them as they were
+ *   workspace  : device scratch, 16-byte aligned, fa_bwd_packed_workspace_bytes(...) bytes at
+ *                least (an fp32 dQ accumulator, and two vectors of the rows); contents on entry do not
+ *                matter.  Calls that share one must be ordered.
+ * dK and dV are summed in a fixed order; dQ by reductions in L2, in none: its last bit may differ
+ * from call to call.  Three launches; errors as fa_fwd.
+ */
+int fa_bwd_packed(const fa_rows *q, const fa_rows *k, const fa_rows *v, const fa_rows *o, const float *lse,
+                  const fa_rows *dout, const fa_rows *dq, const fa_rows *dk, const fa_rows *dv, const void *plan,
+                  int64_t B, int64_t T, int64_t H, int64_t Hkv, int64_t d, float scale, int causal, int fill,
+                  void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Workspace bytes fa_bwd_packed needs, or -1 for invalid sizes.  Pure host computation. */
+int64_t fa_bwd_packed_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Hkv, int64_t d);
+
+/*
  * The 4-bit KV cache: keys and values of many sequences in pages of a shared
  * pool, for single-token serving (fa_fwd_kv4), which reads all of it for every
  * token and is bound by those bytes.  Nothing on the pages describes it; the
@@ -483,6 +561,59 @@ int64_t fa_fwd_kv4_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t n_
                                    int64_t max_tokens, int accumulate);
 
 /*
+ * fa_fwd_kv4_tree - fa_fwd_kv4 for a tree of drafted tokens: the newest n_new[b] tokens of
+ * sequence b are drafts that continue its other tokens (the context, c = lens[b] - n_new[b] of them)
+ * along several branches, their keys and values already appended in any order in which a
+ * draft comes behind the ones it continues.  Query t admits the context, and draft i
+ * (position c + i, i < n_new[b]) iff bit i of tree[b][t] is set: a tree sets a draft's own bit and those of
+ * its ancestors, and other masks are taken as they are.
+ *
+ *   tree  : const uint64 [B][n_q], 8-byte aligned
+ *   n_new : const int32 [B], how many of the n_q drafts sequence b has (held to [0, min(n_q, lens[b])]), or NULL
+ *           for n_q (for min(n_q, lens[b]) where the sequence is shorter).  Rows t >= n_new[b] get O = 0, LSE = -inf, as does a row
+ *           that admits nothing.
+ * The other arguments, the workspace (fa_fwd_kv4_workspace_bytes(..., 0)) and the errors are fa_fwd_kv4's
+ * without accumulate.  With a chain's masks, (2 << t) - 1, of sequences of n_q tokens and more the result is
+ * fa_fwd_kv4's, bit for bit.
+ */
+int fa_fwd_kv4_tree(const void *q, const fa_kv4_cache *cache, const int32_t *lens, const int32_t *page_table,
+                    const uint64_t *tree, const int32_t *n_new, void *o, float *lse, int64_t B, int64_t H,
+                    int64_t n_q, int64_t max_pages, float scale, void *workspace, int64_t workspace_bytes,
+                    void *stream);
+
+/*
+ * fa_kv4_keep - keep an accepted path of the drafts: in each sequence, draft path[b][i] (0 <= i < n_path[b]; at
+ * position c + path[b][i], c = lens[b] - n_new[b]) is moved to position c + i, for every key head, with its weight
+ * if the cache has them.
+ *
+ *   n_draft : drafts a sequence may have, 1 .. 64 (the columns of path)
+ *   path    : const int32 [B][n_draft], ascending (each larger than the one before), each in [0, n_new[b]).  A path
+ *             that is not is kept up to the first entry that breaks this, and reported as FA_ERR_BAD_PAGE.
+ *   n_path  : const int32 [B], held to [0, n_new[b]]
+ *   n_new   : const int32 [B], held to [0, min(n_draft, lens[b])], or NULL for that upper end
+ *   new_lens : int32 out [B], c + the number kept
+ * What lies behind the new lengths is left as it is.  Pages that hold drafts appear once in the table.  A draft
+ * in a page outside the pool, or one that would go to such a page, is reported as FA_ERR_BAD_PAGE; the first leaves zeros.
+ */
+int fa_kv4_keep(const fa_kv4_cache *cache, const int32_t *lens, const int32_t *page_table, int64_t max_pages,
+                const int32_t *path, const int32_t *n_path, const int32_t *n_new, int64_t B, int64_t n_draft,
+                int32_t *new_lens, void *stream);
+
+/*
+ * fa_kv4_copy_pages - copy pages whole, every key head, with the weights where both caches have them (where only
+ * `to` has, they become 0): a fork's copy of the last page of its parent (the pages before it are shared by the
+ * tables), a sequence's move to another pool, the closing of gaps in one.
+ *
+ *   from, to : caches of the same Hkv, page_size, d; the same pool or two
+ *   pages, to_pages : const int32 [n]; page pages[i] of `from` goes to page to_pages[i] of `to`.  A pair with a
+ *         negative page is left out silently (lists of a fixed length), one with a page past the pool is left out and
+ *         reported as FA_ERR_BAD_PAGE.
+ * A page may be copied to many; no page may be copied to twice, nor to and from in one call.
+ */
+int fa_kv4_copy_pages(const fa_kv4_cache *from, const int32_t *pages, const fa_kv4_cache *to, const int32_t *to_pages,
+                      int64_t n, void *stream);
+
+/*
  * fa_kv4_evict - keep `keep` tokens of every (sequence, key head): the last
  * `recent` ones, and of the others those with the largest weights (ties: the lowest
  * position; a NaN counts as larger than every number), in their order, as rows
@@ -525,7 +656,8 @@ int fa_key_weights(const void *q, const void *k, const float *lse, float *weight
  * fa_get_device_status - synchronise `stream`, then return and clear the
  * current device's sticky in-kernel status (FA_OK, or FA_ERR_TIMEOUT when a
  * bounded wait inside a kernel gave up and the kernel returned early, leaving
- * its outputs incomplete; or FA_ERR_BAD_PAGE, see the 4-bit cache).  While
+ * its outputs incomplete; or FA_ERR_BAD_PAGE, see the 4-bit cache; or
+ * FA_ERR_BAD_SEQUENCE, see packed sequences).  While
  * FA_ERR_TIMEOUT is set, fa_fwd and fa_fwd_kv4 launches do no work (their
  * outputs are left unwritten) until this call clears it; a fa_fwd_kv4 call
  * in which a wait gave up adds nothing to the cache's weights.

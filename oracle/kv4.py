@@ -78,6 +78,27 @@ def attention(q, k, v, scale, length):
     return dict(o=o, lse=lse, weights=w, reach=reach, spread=spread, top_q=top_q, total=total)
 
 
+def tree_attention(q, k, v, scale, length, masks, n_new):
+    """One sequence whose newest n_new tokens are drafts: q [H, n_q, d], k, v [Hkv, length, d], masks n_q whole numbers, bit
+    i for draft i -> what attention gives (without the keys' weights); rows from n_new on admit nothing."""
+    H, n_q, d = q.shape
+    G = H // k.shape[0]
+    drafts = min(n_q if n_new is None else max(0, n_new), n_q, length)
+    r = dict(o=np.zeros((H, n_q, d)), lse=np.full((H, n_q), -np.inf), reach=np.zeros((H, n_q)), spread=np.zeros((H, n_q, d)),
+             top_q=np.zeros((H, n_q)), total=np.ones((H, n_q)))
+    for t in range(drafts):
+        seen = [j for j in range(length) if j < length - drafts or (masks[t] >> (j - length + drafts)) & 1]
+        for h in range(H if seen else 0):
+            kk, vv = k[h // G, seen], v[h // G, seen]
+            s = scale * (kk @ q[h, t])
+            e = np.exp(s - s.max())
+            p = e / e.sum()
+            r["o"][h, t], r["lse"][h, t] = p @ vv, s.max() + np.log(e.sum())
+            r["reach"][h, t], r["spread"][h, t] = scale * (np.abs(kk) @ np.abs(q[h, t])).max(), p @ np.abs(vv)
+            r["top_q"][h, t], r["total"][h, t] = scale * np.abs(q[h, t]).max() * np.abs(kk).sum(-1).max(), e.sum()
+    return r
+
+
 def evict(weights, length, keep, recent):
     """Positions of one (sequence, key head) that stay, ascending."""
     first = max(0, length - recent)
