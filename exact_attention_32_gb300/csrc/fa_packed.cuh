@@ -106,19 +106,39 @@ inline bool make_rows_map(CUtensorMap *m, const FaRows &r, int64_t T, int64_t he
 }
 
 // Rows [n, n rounded up to 16) of a 128-row tile of D columns (128-byte swizzle: the swizzle stays inside a row) to
-// zeros, by a whole warp, visible to the products that follow.  The tile is loaded 128 rows at a time, so behind a
+// zeros, by `lanes` threads of a warp; a fence makes it visible to the products that follow.  The tile is loaded 128 rows at a time, so behind a
 // sequence's last row it holds the next sequence's, or whatever lies behind the last one; a product over these rows
 // has weight 0 for them, which keeps them out only as long as they are finite.  Products step 16 rows at a time and end
 // behind the last step that has a row of the sequence, so no more rows than these matter.
 template <int D>
-__device__ __forceinline__ void zero_tail_rows(uint8_t *tile, int n, int lane)
+__device__ __forceinline__ void zero_tail_rows(uint8_t *tile, int n, int lane, int lanes = 32)
 {
     constexpr int kPieces = D / 8;  // of 16 bytes, in a row
     const int rows = ((n + 15) & ~15) - n;
-    for (int i = lane; i < rows * kPieces; i += 32) {
+    for (int i = lane; i < rows * kPieces; i += lanes) {
         const int r = n + i / kPieces, c = i % kPieces;
         *reinterpret_cast<uint4 *>(tile + (c >> 3) * 16384 + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
     }
+}
+
+// A kernel behind another whose results it needs: launched before that one has ended, so that its launch and what it does
+// first overlap it, it waits for the end itself.  (The plan is not among those results: it is older.)
+__device__ __forceinline__ void wait_for_the_one_before() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kern)(P...), unsigned grid, int threads, int smem, cudaStream_t s, const A &...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = s;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 // Rows of no sequence: [0, first) and [last, T).  n of them; the i-th.

@@ -4,32 +4,39 @@
 //   dV_j = sum over the key head's query heads and rows i of P_ij dO_i
 //   dS_ij = P_ij (dO_i . v_j - D_i),   dQ_i = scale sum_j dS_ij k_j,   dK_j = scale sum dS_ij q_i
 //
-// Three launches, as in fa_bwd_tc.cu, whose pipeline the main one is:
+// Three launches:
 //   pre   D and LSE log2 e of every row, in vectors padded to whole blocks of 128 rows (+inf and 0 behind a sequence's
 //         end, so that P is 0 there); the fp32 dQ accumulator zeroed
 //   main  a CTA per 128 keys of one key head of one sequence, the longest loops first (the plan's list), over the 128-row
 //         query blocks (causal: from the diagonal) of each of the key head's query heads in turn: dK and dV, which
 //         sum over those heads, stay in tensor memory through all of it; each block's part of dQ is added to
-//         the accumulator by one bulk reduction
+//         the accumulator in L2
 //   post  dQ = bf16(scale accumulator); zeros in rows of no sequence where they are asked for
-// Per query block (S^T etc. are key-major: TMEM lane = key):
+// Per query block i (S^T etc. are key-major: TMEM lane = key):
 //   S^T  = K Q^T      SS product -> TMEM A
-//   dP^T = V dO^T     SS product -> TMEM B
 //   P^T  = exp2(S^T scale log2 e - LSE log2 e)   softmax warps, bf16 back into A
-//   dV  += P^T dO     A from TMEM, B = dO MN-major -> TMEM C
+//   dP^T = V dO^T     SS product -> TMEM B
 //   dS^T = P^T (dP^T - D)                        softmax warps, bf16 into B and into shared memory
+//   dV  += P^T dO     A from TMEM, B = dO MN-major -> TMEM C
 //   dK  += dS^T Q     A from TMEM -> TMEM D
-//   dQ   = dS K       A = dS MN-major, B = K MN-major -> TMEM A, read into registers, staged in the Q / dO stage that the
-//                     block no longer needs, and added to the accumulator by the load warp
-// The accumulator is blocked: a 128 x d fp32 block per (query head, block), as the 8 warps' slices (warpgroup, 32
-// rows) one behind the other, each 32 rows x d/2 columns with the 16-byte piece c of row l at piece c ^ (l mod d/8).
+//   dQ   = dS K       A = dS MN-major, B = K MN-major -> TMEM B, read into registers, added to the accumulator
+// The products are issued so that one block's last overlap the next one's softmax:
+//   dP_i  dV_i  S_i+1  dK_i  dQ_i  (dQ_i read out)  dP_i+1 ...
+// S_i+1 takes A's place behind dV_i, which read P_i there, and while dK_i and dQ_i run the softmax warps take P_i+1;
+// dQ_i takes B's place behind dK_i, which read dS_i there.  (In the order S_i dP_i dV_i dK_i dQ_i, with dQ in A, the tensor
+// pipe waited for both halves of the softmax of every block.)
+// The accumulator is blocked: a 128 x d fp32 block per (query head, block), as pieces of 32 rows x 32 columns, 4 KB each: its
+// 8 groups of 4 columns one behind the other, in each the 32 rows next to one another.  A warpgroup of its own reads dQ
+// out, stages it piece by piece and adds each by a bulk reduction: done by the softmax warps between a block's P
+// and its dS, that cost a quarter of all the time (32 heads of 16384: 4600 us, without it 3720).
 //
 // A 128-row tile that reaches behind its sequence holds rows of others.  Sums over rows (dV, dK over queries, dQ over
 // keys) step 16 rows at a time and end behind the sequence's last one; of that step the rows behind are made zeros in
-// Q, dO, K and V (zero_tail_rows), so that their P, dP and dS are zeros too, whatever the tile held.  Rows past that
-// step are lanes and columns of results that nothing reads.
-// Roles (320 threads): warps 0-3 and 4-7 are two warpgroups that take query columns 0-63 and 64-127 of a block (and halves
-// of dQ's, dK's and dV's columns); warp 8 loads; warp 9 issues the products and owns the tensor memory.
+// Q, dO, K and V (zero_tail_rows, by a warp of its own), so that their P, dP and dS are zeros too, whatever the tile
+// held.  Rows past that step are lanes and columns of results that nothing reads.
+// Roles: warps 0-3 and 4-7 are two warpgroups that take query columns 0-63 and 64-127 of a block (and halves of dK's
+// and dV's columns at the end); warps 8-11 add dQ; warp 12 loads; warp 13 issues the products and owns the tensor memory;
+// warp 14 zeroes tails.
 // Every mbarrier wait is bounded; a wait that gives up sets FA_ERR_TIMEOUT and the CTA winds down.
 #include <math.h>
 
@@ -40,9 +47,15 @@ using namespace sm100;
 namespace {
 
 constexpr int kBlock = 128;  // keys per CTA, rows of a query block
-constexpr int kThreads = 320;
-constexpr int kLoadWarp = 8;
-constexpr int kMmaWarp = 9;
+// Launched with 128 registers a thread (what 512 threads may have): the softmax, which holds a block's P until its dP is
+// there, takes 32 more each of what the others give up.
+constexpr int kThreads = 512;
+constexpr int kLaunchRegs = 128, kSoftmaxRegs = 160, kAddRegs = 88, kOtherRegs = 104;
+static_assert(2 * kSoftmaxRegs + kAddRegs + kOtherRegs <= 4 * kLaunchRegs, "the warpgroups' shares are what the block has");
+constexpr int kAddWarp = 8;
+constexpr int kLoadWarp = 12;
+constexpr int kMmaWarp = 13;
+constexpr int kTailWarp = 14;
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 constexpr uint64_t kCleanupLimitNs = 20000000ull;
 
@@ -52,18 +65,20 @@ struct BCfg {
     static constexpr int kAtoms = D / 64;
     static constexpr int kK = 0;
     static constexpr int kV = kTile;
-    static constexpr int kStage0 = 2 * kTile;  // stage s: Q at kStage0 + s * kStageBytes, dO behind it
-    static constexpr int kStageBytes = 2 * kTile;
-    static constexpr int kDS = kStage0 + 2 * kStageBytes;   // dS, 128 keys x 128 queries bf16, MN-major
-    static constexpr int kVec = kDS + kBlock * kBlock * 2;  // per stage: LSE log2 e (512 B), D (512 B)
+    // Q in two buffers, dO in one: dO_i+1 has S_i+1, dK_i and dQ_i to arrive in
+    static constexpr int kQ = 2 * kTile;
+    static constexpr int kDO = kQ + 2 * kTile;
+    static constexpr int kDS = kDO + kTile;                 // dS, 128 keys x 128 queries bf16, MN-major
+    static constexpr int kDQ = kDS + kBlock * kBlock * 2;   // dQ on its way out: two pieces a warp
+    static constexpr int kVec = kDQ + 4 * 8192;             // per Q buffer: LSE log2 e (512 B), D (512 B)
     static constexpr int kBar = kVec + 2 * 1024;
-    static constexpr int kNumBars = 13;
+    static constexpr int kNumBars = 18;
     static constexpr int kSmemBytes = kBar + kNumBars * 8 + 16;
     static_assert(kSmemBytes <= 232448, "shared memory plan exceeds 227 KB");
 };
 
-enum { KV_FULL = 0, Q_FULL = 1, DQ_STAGED = 3, S_FULL = 5, DP_FULL = 6, P_READY = 7, DS_READY = 8, DQ_FULL = 9,
-       DQ_CONSUMED = 10, DONE = 11, MMA_DONE = 12 };
+enum { KV_FULL = 0, Q_FULL = 1, Q_FREE = 3, DO_FULL = 5, DO_FREE, S_FULL, DP_FULL, P_READY, DS_READY, DQ_FULL, DQ_CONSUMED, KV_TAIL,
+       Q_TAIL, DO_TAIL = Q_TAIL + 2, DONE, MMA_DONE };
 
 struct BwdArgs {
     PlanView plan;
@@ -123,14 +138,19 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         mbar_init(BAR(KV_FULL), 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(BAR(Q_FULL + s), 1);
-            mbar_init(BAR(DQ_STAGED + s), 8);  // the softmax warps, once their dQ slices are staged
+            mbar_init(BAR(Q_FREE + s), 1);
+            mbar_init(BAR(Q_TAIL + s), 1);
         }
+        mbar_init(BAR(DO_FULL), 1);
+        mbar_init(BAR(DO_FREE), 1);
+        mbar_init(BAR(DO_TAIL), 1);
         mbar_init(BAR(S_FULL), 1);
         mbar_init(BAR(DP_FULL), 1);
         mbar_init(BAR(P_READY), 8);
         mbar_init(BAR(DS_READY), 8);
         mbar_init(BAR(DQ_FULL), 1);
-        mbar_init(BAR(DQ_CONSUMED), 8);
+        mbar_init(BAR(DQ_CONSUMED), 4);
+        mbar_init(BAR(KV_TAIL), 1);
         mbar_init(BAR(DONE), 1);
         mbar_init(BAR(MMA_DONE), 1);
         fence_mbar_init();
@@ -146,13 +166,15 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const bool run = tmem_slot[1] != 0;  // no wait has given up that nobody has read so yet
+    wait_for_the_one_before();  // (D, LSE and the accumulator's zeros)
     const uint32_t tA = tmem, tB = tmem + 128, tC = tmem + 256, tD = tmem + 384;
 
     if (!run) {
         // nothing to do
-    } else if (warp == kLoadWarp) {
-        // ------------------------------------------------------------ loads
-        if (lane == 0) {
+    } else if (warp >= kLoadWarp) {
+        registers_down<kOtherRegs>();
+        if (warp == kLoadWarp && lane == 0) {
+            // ------------------------------------------------------------ loads
             prefetch_tmap(&tm_q);
             prefetch_tmap(&tm_k);
             prefetch_tmap(&tm_v);
@@ -162,141 +184,179 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 tma_load_3d(sb + C::kK + c * 16384, &tm_k, BAR(KV_FULL), c * 64, start + k0, kvh);
                 tma_load_3d(sb + C::kV + c * 16384, &tm_v, BAR(KV_FULL), c * 64, start + k0, kvh);
             }
-            // (query head, block) of iteration i
-            auto place = [&](int i, int &h, int &qb) {
-                h = kvh * a.group + i / nq;
-                qb = qb0 + i % nq;
-            };
-            // add the dQ block that iteration j staged in stage j & 1 to the accumulator
-            auto flush = [&](int j) -> bool {
-                if (!mbar_wait(BAR(DQ_STAGED + (j & 1)), (j >> 1) & 1, kWaitLimitNs)) return false;
-                int h, qb;
-                place(j, h, qb);
-                bulk_reduce_add_f32(a.dq_acc + (static_cast<int64_t>(h) * a.nb + blk0 + qb) * (kBlock * D),
-                                    sb + C::kStage0 + (j & 1) * C::kStageBytes, kBlock * D * 4);
-                bulk_commit();
-                return true;
-            };
             bool ok = true;
-            int issued = 0;
-            for (int i = 0; i < n_it; ++i) {
-                const int st = i & 1;
-                if (i >= 2) {  // the stage is free once the block staged in it two iterations ago is read out
-                    if (!(ok = flush(i - 2))) break;
-                    bulk_wait_read0();
+            int i = 0, n_do = 0;
+            for (int h = kvh * a.group; h < (kvh + 1) * a.group && ok; ++h)
+                for (int qb = qb0; qb < n_seq; ++qb, ++i) {
+                    const int st = i & 1;
+                    if (i >= 2 && !(ok = mbar_wait(BAR(Q_FREE + st), ((i >> 1) - 1) & 1, kWaitLimitNs))) break;
+                    const int row = start + qb * kBlock;
+                    mbar_arrive_expect_tx(BAR(Q_FULL + st), C::kTile + 1024);
+                    for (int c = 0; c < C::kAtoms; ++c)
+                        tma_load_3d(sb + C::kQ + st * C::kTile + c * 16384, &tm_q, BAR(Q_FULL + st), c * 64, row, h);
+                    const int64_t vo = (static_cast<int64_t>(h) * a.nb + blk0 + qb) * kBlock;
+                    bulk_load(sb + C::kVec + st * 1024, a.lse2 + vo, 512, BAR(Q_FULL + st));
+                    bulk_load(sb + C::kVec + st * 1024 + 512, a.dvec + vo, 512, BAR(Q_FULL + st));
+                    if (i >= 1 && !(ok = mbar_wait(BAR(DO_FREE), (i - 1) & 1, kWaitLimitNs))) {
+                        ++i;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(BAR(DO_FULL), C::kTile);
+                    for (int c = 0; c < C::kAtoms; ++c) tma_load_3d(sb + C::kDO + c * 16384, &tm_do, BAR(DO_FULL), c * 64, row, h);
+                    ++n_do;
                 }
-                int h, qb;
-                place(i, h, qb);
-                const int row = start + qb * kBlock;
-                const uint32_t sq = sb + C::kStage0 + st * C::kStageBytes, sdo = sq + C::kTile;
-                mbar_arrive_expect_tx(BAR(Q_FULL + st), 2 * C::kTile + 1024);
-                for (int c = 0; c < C::kAtoms; ++c) {
-                    tma_load_3d(sq + c * 16384, &tm_q, BAR(Q_FULL + st), c * 64, row, h);
-                    tma_load_3d(sdo + c * 16384, &tm_do, BAR(Q_FULL + st), c * 64, row, h);
-                }
-                const int64_t vo = (static_cast<int64_t>(h) * a.nb + blk0 + qb) * kBlock;
-                bulk_load(sb + C::kVec + st * 1024, a.lse2 + vo, 512, BAR(Q_FULL + st));
-                bulk_load(sb + C::kVec + st * 1024 + 512, a.dvec + vo, 512, BAR(Q_FULL + st));
-                ++issued;
-            }
-            for (int j = n_it >= 2 ? n_it - 2 : 0; j < n_it && ok; ++j) ok = flush(j);
-            bulk_wait0();  // the accumulator additions complete before the CTA ends
             if (!ok) packed_timeout();
+            // every copy this thread issued has landed before the CTA may exit
             const uint64_t lim = ok ? kWaitLimitNs : kCleanupLimitNs;
             mbar_wait(BAR(KV_FULL), 0, lim);
-            for (int i = issued > 2 ? issued - 2 : 0; i < issued; ++i) mbar_wait(BAR(Q_FULL + (i & 1)), (i >> 1) & 1, lim);
-        }
-    } else if (warp == kMmaWarp) {
-        // ------------------------------------------------------------- products
-        constexpr uint32_t idS = idesc_bf16_f32(kBlock, kBlock, false);   // S^T, dP^T: K-major operands
-        constexpr uint32_t idAcc = idesc_bf16_f32(kBlock, D, true);       // dV, dK: A in TMEM, B MN-major
-        constexpr uint32_t idQ = idesc_bf16_f32(kBlock, D, true, true);   // dQ: A and B MN-major
-        constexpr uint32_t kStage16 = C::kStageBytes >> 4, kTile16 = C::kTile >> 4;
-        const uint64_t d_k_kmaj = smem_desc_sw128(sb + C::kK, 16, 1024);
-        const uint64_t d_v_kmaj = smem_desc_sw128(sb + C::kV, 16, 1024);
-        const uint64_t d_k_mn = smem_desc_sw128(sb + C::kK, 16384, 1024);
-        const uint64_t d_ds_mn = smem_desc_sw128(sb + C::kDS, 16384, 1024);
-        const uint64_t d_q_kmaj = smem_desc_sw128(sb + C::kStage0, 16, 1024);
-        const uint64_t d_q_mn = smem_desc_sw128(sb + C::kStage0, 16384, 1024);
-        const int k_steps = (k_rows + 15) / 16, tail_steps = (q_left + 15) / 16;
-        bool ok = mbar_wait_warp(BAR(KV_FULL), 0, kWaitLimitNs);
-        if (ok && (k_rows & 15)) {
-            zero_tail_rows<D>(smem + C::kK, k_rows, lane);
-            zero_tail_rows<D>(smem + C::kV, k_rows, lane);
-            fence_proxy_async_smem();
-            __syncwarp();
-        }
-        int block = 0;  // of the query head's nq
-        for (int i = 0; i < n_it && ok; ++i) {
-            const int st = i & 1;
-            if (!(ok = mbar_wait_warp(BAR(Q_FULL + st), (i >> 1) & 1, kWaitLimitNs))) break;
-            const bool tail = ++block == nq;
-            if (tail) {
-                block = 0;
-                if (q_left & 15) {
-                    zero_tail_rows<D>(smem + C::kStage0 + st * C::kStageBytes, q_left, lane);
-                    zero_tail_rows<D>(smem + C::kStage0 + st * C::kStageBytes + C::kTile, q_left, lane);
-                    fence_proxy_async_smem();
-                    __syncwarp();
+            for (int j = i > 2 ? i - 2 : 0; j < i; ++j) mbar_wait(BAR(Q_FULL + (j & 1)), (j >> 1) & 1, lim);
+            if (n_do > 0) mbar_wait(BAR(DO_FULL), (n_do - 1) & 1, lim);
+        } else if (warp == kTailWarp) {
+            // -------------------------------------------------- rows behind the sequence's end
+            bool ok = true;
+            if (k_rows & 15) {
+                ok = mbar_wait_warp(BAR(KV_FULL), 0, kWaitLimitNs);
+                zero_tail_rows<D>(smem + C::kK, k_rows, lane);
+                zero_tail_rows<D>(smem + C::kV, k_rows, lane);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(BAR(KV_TAIL));
+            }
+            if (q_left & 15) {  // every block's tiles go by this warp then (a wait for some of a barrier's phases can mistake one for another)
+                int block = 0;
+                for (int i = 0; i < n_it && ok; ++i) {
+                    const int st = i & 1;
+                    const bool tail = ++block == nq;
+                    if (tail) block = 0;
+                    auto pass = [&](int from, uint32_t phase, int to, uint8_t *tile) -> bool {
+                        if (!mbar_wait_warp(BAR(from), phase, kWaitLimitNs)) return false;
+                        if (tail) {
+                            zero_tail_rows<D>(tile, q_left, lane);
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                        }
+                        if (lane == 0) mbar_arrive(BAR(to));
+                        return true;
+                    };
+                    ok = pass(Q_FULL + st, (i >> 1) & 1, Q_TAIL + st, smem + C::kQ + st * C::kTile) &&
+                         pass(DO_FULL, i & 1, DO_TAIL, smem + C::kDO);
                 }
             }
-            const int q_steps = tail ? tail_steps : kBlock / 16;
-            if (i > 0 && !(ok = mbar_wait_warp(BAR(DQ_CONSUMED), (i - 1) & 1, kWaitLimitNs))) break;
-            tc_fence_after();
-            const uint32_t q_lo = lo32(d_q_kmaj) + st * kStage16, do_lo = q_lo + kTile16;
-            const uint32_t qmn_lo = lo32(d_q_mn) + st * kStage16, domn_lo = qmn_lo + kTile16;
-            // S^T = K Q^T and dP^T = V dO^T
-            if (elect_one()) {
+            if (!ok && lane == 0) packed_timeout();
+        } else if (warp == kMmaWarp && lane == 0) {
+            // ------------------------------------------------------------- products
+            constexpr uint32_t idS = idesc_bf16_f32(kBlock, kBlock, false);   // S^T, dP^T: K-major operands
+            constexpr uint32_t idAcc = idesc_bf16_f32(kBlock, D, true);       // dV, dK: A in TMEM, B MN-major
+            constexpr uint32_t idQ = idesc_bf16_f32(kBlock, D, true, true);   // dQ: A and B MN-major
+            constexpr uint32_t kTile16 = C::kTile >> 4;
+            const uint64_t d_kmaj = smem_desc_sw128(sb, 16, 1024), d_mn = smem_desc_sw128(sb, 16384, 1024);
+            const uint32_t kmaj_hi = hi32(d_kmaj), mn_hi = hi32(d_mn);
+            const uint32_t kmaj = lo32(d_kmaj), mn = lo32(d_mn);
+            const uint32_t k_kmaj = kmaj + (C::kK >> 4), v_kmaj = kmaj + (C::kV >> 4), k_mn = mn + (C::kK >> 4), ds_mn = mn + (C::kDS >> 4),
+                           q_kmaj = kmaj + (C::kQ >> 4), q_mn = mn + (C::kQ >> 4), do_kmaj = kmaj + (C::kDO >> 4), do_mn = mn + (C::kDO >> 4);
+            const int k_steps = (k_rows + 15) / 16, tail_steps = (q_left + 15) / 16;
+            int block = 0;  // of the query head's nq
+            const int q_there = (q_left & 15) ? Q_TAIL : Q_FULL, do_there = (q_left & 15) ? DO_TAIL : DO_FULL;
+            // block i's tile is there, and its rows behind the end are zeros; S_i = K Q_i^T
+            auto scores = [&](int i) -> bool {
+                const int st = i & 1;
+                if (!mbar_wait(BAR(q_there + st), (i >> 1) & 1, kWaitLimitNs)) return false;
+                tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t koff = ((kk / 4) * 16384 + (kk % 4) * 32) >> 4;
-                    mma_ss_lohi(tA, lo32(d_k_kmaj) + koff, hi32(d_k_kmaj), q_lo + koff, hi32(d_q_kmaj), idS, kk > 0 ? 1u : 0u);
+                    mma_ss_lohi(tA, k_kmaj + koff, kmaj_hi, q_kmaj + st * kTile16 + koff, kmaj_hi, idS, kk > 0 ? 1u : 0u);
                 }
                 mma_commit(BAR(S_FULL));
+                return true;
+            };
+            bool ok = mbar_wait(BAR(KV_FULL), 0, kWaitLimitNs) && (!(k_rows & 15) || mbar_wait(BAR(KV_TAIL), 0, kWaitLimitNs)) && scores(0);
+            for (int i = 0; i < n_it && ok; ++i) {
+                const int st = i & 1;
+                const bool tail = ++block == nq;
+                if (tail) block = 0;
+                const int q_steps = tail ? tail_steps : kBlock / 16;
+                // dP^T = V dO^T, once B's dQ of the block before has been read
+                if (!(ok = mbar_wait(BAR(do_there), i & 1, kWaitLimitNs))) break;
+                if (i > 0 && !(ok = mbar_wait(BAR(DQ_CONSUMED), (i - 1) & 1, kWaitLimitNs))) break;
+                tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t koff = ((kk / 4) * 16384 + (kk % 4) * 32) >> 4;
-                    mma_ss_lohi(tB, lo32(d_v_kmaj) + koff, hi32(d_v_kmaj), do_lo + koff, hi32(d_q_kmaj), idS, kk > 0 ? 1u : 0u);
+                    mma_ss_lohi(tB, v_kmaj + koff, kmaj_hi, do_kmaj + koff, kmaj_hi, idS, kk > 0 ? 1u : 0u);
                 }
                 mma_commit(BAR(DP_FULL));
-            }
-            __syncwarp();
-            // dV += P^T dO
-            if (!(ok = mbar_wait_warp(BAR(P_READY), i & 1, kWaitLimitNs))) break;
-            tc_fence_after();
-            if (elect_one()) {
+                // dV += P^T dO
+                if (!(ok = mbar_wait(BAR(P_READY), i & 1, kWaitLimitNs))) break;
+                tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < kBlock / 16; ++kk)
-                    if (kk < q_steps)
-                        mma_ts_lohi(tC, tA + packed_col(kk), domn_lo + kk * 128, hi32(d_q_mn), idAcc, (i > 0 || kk > 0) ? 1u : 0u);
-            }
-            __syncwarp();
-            // dK += dS^T Q, then dQ = dS K
-            if (!(ok = mbar_wait_warp(BAR(DS_READY), i & 1, kWaitLimitNs))) break;
-            tc_fence_after();
-            if (elect_one()) {
+                    if (kk < q_steps) mma_ts_lohi(tC, tA + packed_col(kk), do_mn + kk * 128, mn_hi, idAcc, (i > 0 || kk > 0) ? 1u : 0u);
+                mma_commit(BAR(DO_FREE));
+                if (i + 1 < n_it && !(ok = scores(i + 1))) break;
+                // dK += dS^T Q, then dQ = dS K
+                if (!(ok = mbar_wait(BAR(DS_READY), i & 1, kWaitLimitNs))) break;
+                tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < kBlock / 16; ++kk)
-                    if (kk < q_steps)
-                        mma_ts_lohi(tD, tB + packed_col(kk), qmn_lo + kk * 128, hi32(d_q_mn), idAcc, (i > 0 || kk > 0) ? 1u : 0u);
+                    if (kk < q_steps) mma_ts_lohi(tD, tB + packed_col(kk), q_mn + st * kTile16 + kk * 128, mn_hi, idAcc, (i > 0 || kk > 0) ? 1u : 0u);
+                mma_commit(BAR(Q_FREE + st));
 #pragma unroll
                 for (int kk = 0; kk < kBlock / 16; ++kk)
-                    if (kk < k_steps)
-                        mma_ss_lohi(tA, lo32(d_ds_mn) + kk * 128, hi32(d_ds_mn), lo32(d_k_mn) + kk * 128, hi32(d_k_mn), idQ,
-                                    kk > 0 ? 1u : 0u);
+                    if (kk < k_steps) mma_ss_lohi(tB, ds_mn + kk * 128, mn_hi, k_mn + kk * 128, mn_hi, idQ, kk > 0 ? 1u : 0u);
                 mma_commit(BAR(DQ_FULL));
             }
-            __syncwarp();
-        }
-        if (!ok && lane == 0) packed_timeout();
-        if (elect_one()) {
+            if (!ok) packed_timeout();
             if (ok) mma_commit(BAR(DONE));
             mma_commit(BAR(MMA_DONE));
+            mbar_wait(BAR(MMA_DONE), 0, ok ? kWaitLimitNs : kCleanupLimitNs);
         }
         __syncwarp();
-        mbar_wait_warp(BAR(MMA_DONE), 0, ok ? kWaitLimitNs : kCleanupLimitNs);
+    } else if (warp >= kAddWarp) {
+        // ---------------------------------------------------------------- dQ (TMEM lane = query row)
+        registers_down<kAddRegs>();
+        const int q = warp - kAddWarp;  // this warp's 32 rows
+        const uint32_t tQ = tB + (static_cast<uint32_t>(q * 32) << 16);
+        uint8_t *stage = smem + C::kDQ + q * 8192;
+        bool ok = true;
+        int i = 0;
+        for (int h = kvh * a.group; h < (kvh + 1) * a.group && ok; ++h)
+            for (int qb = qb0; qb < n_seq; ++qb, ++i) {
+                float *acc = a.dq_acc + (static_cast<int64_t>(h) * a.nb + blk0 + qb) * (kBlock * D) + q * (32 * D);
+                if (!(ok = mbar_wait_warp(BAR(DQ_FULL), i & 1, kWaitLimitNs))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int half = 0; half < D / 64; ++half) {
+                    uint32_t x[2][32];
+                    tmem_ld32(tQ + half * 64, x[0]);
+                    tmem_ld32(tQ + half * 64 + 32, x[1]);
+                    tmem_wait_ld();
+                    if (half == D / 64 - 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(BAR(DQ_CONSUMED));
+                    }
+                    if (lane == 0) bulk_wait_read0();  // (what was added before has left the buffers)
+                    __syncwarp();
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            *reinterpret_cast<uint4 *>(stage + u * 4096 + (c * 32 + lane) * 16) =
+                                make_uint4(x[u][4 * c], x[u][4 * c + 1], x[u][4 * c + 2], x[u][4 * c + 3]);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        bulk_reduce_add_f32(acc + half * 2048, smem_u32(stage), 8192);
+                        bulk_commit();
+                    }
+                }
+            }
+        if (!ok && lane == 0) packed_timeout();
+        if (lane == 0) bulk_wait0();  // the additions have completed before the CTA ends
     } else {
         // ------------------------------------------------ softmax-side warpgroups
+        registers_up<kSoftmaxRegs>();
         const int wg = warp >> 2;              // query columns [64 wg, 64 wg + 64); d columns [wg D/2, (wg + 1) D/2)
         const int r = (warp & 3) * 32 + lane;  // TMEM lane
         const uint32_t loff = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -305,7 +365,7 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         int block = 0;
         for (int i = 0; i < n_it && ok; ++i) {
             const int st = i & 1;
-            const int q0 = (qb0 + block) * kBlock;
+            const int qb = qb0 + block;
             const bool diagonal = CAUSAL && block == 0;
             if (++block == nq) block = 0;
             if (!mbar_wait_warp(BAR(Q_FULL + st), (i >> 1) & 1, kWaitLimitNs) || !mbar_wait_warp(BAR(S_FULL), i & 1, kWaitLimitNs)) {
@@ -317,41 +377,31 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             const float *d_s = lse2_s + kBlock;
             // P^T = exp2(S^T scale log2 e - LSE log2 e); 0 for keys behind the sequence and, causal, keys after the query
             float p[64];
-            {
-                uint32_t a0[32], a1[32];
-                tmem_ld32(tA + loff + wg * 64, a0);
-                tmem_ld32(tA + loff + wg * 64 + 32, a1);
+            const float2 sl = make_float2(a.scale_log2, a.scale_log2);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t x[32], pk[16];
+                tmem_ld32(tA + loff + wg * 64 + h * 32, x);
                 tmem_wait_ld();
-                const float2 sl = make_float2(a.scale_log2, a.scale_log2);
 #pragma unroll
-                for (int j = 0; j < 32; j += 2) {
-                    const float2 l0 = *reinterpret_cast<const float2 *>(lse2_s + j);
-                    const float2 l1 = *reinterpret_cast<const float2 *>(lse2_s + 32 + j);
-                    const float2 x0 = fma2(make_float2(__uint_as_float(a0[j]), __uint_as_float(a0[j + 1])), sl, make_float2(-l0.x, -l0.y));
-                    const float2 x1 = fma2(make_float2(__uint_as_float(a1[j]), __uint_as_float(a1[j + 1])), sl, make_float2(-l1.x, -l1.y));
-                    p[j] = ex2(x0.x);
-                    p[j + 1] = ex2(x0.y);
-                    p[32 + j] = ex2(x1.x);
-                    p[32 + j + 1] = ex2(x1.y);
+                for (int j = 0; j < 32; j += 4) {
+                    const float4 l = *reinterpret_cast<const float4 *>(lse2_s + h * 32 + j);
+                    const float2 y = fma2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), sl, make_float2(-l.x, -l.y));
+                    const float2 z = fma2(make_float2(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3])), sl, make_float2(-l.z, -l.w));
+                    p[h * 32 + j] = ex2(y.x);
+                    p[h * 32 + j + 1] = ex2(y.y);
+                    p[h * 32 + j + 2] = ex2(z.x);
+                    p[h * 32 + j + 3] = ex2(z.y);
                 }
-            }
-            if (key >= len) {
+                if (key >= len || diagonal) {  // query q0 + j admits key iff key <= q0 + j
+                    const int q0 = key >= len ? -64 : qb * kBlock + wg * 64 + h * 32;
 #pragma unroll
-                for (int j = 0; j < 64; ++j) p[j] = 0.f;
-            } else if (diagonal) {
-                const int qb = q0 + wg * 64;  // query qb + j admits key iff key <= qb + j
-#pragma unroll
-                for (int j = 0; j < 64; ++j)
-                    if (key > qb + j) p[j] = 0.f;
-            }
-            {
-                uint32_t pk[16];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) pk[j] = pack_bf16x2(p[h * 32 + 2 * j], p[h * 32 + 2 * j + 1]);
-                    tmem_st16(tA + loff + wg * 64 + h * 16, pk);
+                    for (int j = 0; j < 32; ++j)
+                        if (key > q0 + j) p[h * 32 + j] = 0.f;
                 }
+#pragma unroll
+                for (int j = 0; j < 16; ++j) pk[j] = pack_bf16x2(p[h * 32 + 2 * j], p[h * 32 + 2 * j + 1]);
+                tmem_st16(tA + loff + wg * 64 + h * 16, pk);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -364,72 +414,36 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 break;
             }
             tc_fence_after();
-            uint32_t dsk[32];
-            {
-                uint32_t b0[32], b1[32];
-                tmem_ld32(tB + loff + wg * 64, b0);
-                tmem_ld32(tB + loff + wg * 64 + 32, b1);
-                tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 32; j += 2) {
-                    const float2 dd0 = *reinterpret_cast<const float2 *>(d_s + j);
-                    const float2 dd1 = *reinterpret_cast<const float2 *>(d_s + 32 + j);
-                    dsk[j / 2] = pack_bf16x2(p[j] * (__uint_as_float(b0[j]) - dd0.x), p[j + 1] * (__uint_as_float(b0[j + 1]) - dd0.y));
-                    dsk[16 + j / 2] = pack_bf16x2(p[32 + j] * (__uint_as_float(b1[j]) - dd1.x),
-                                                  p[32 + j + 1] * (__uint_as_float(b1[j + 1]) - dd1.y));
-                }
-            }
-            {
-                uint32_t h0[16], h1[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    h0[j] = dsk[j];
-                    h1[j] = dsk[16 + j];
-                }
-                tmem_st16(tB + loff + wg * 64, h0);
-                tmem_st16(tB + loff + wg * 64 + 16, h1);
-            }
-            // dS^T's row (this key) into the MN-major dS tile: column block wg, 16-byte piece c (queries 8c .. 8c+7) at
-            // piece c ^ (key row mod 8)
             uint8_t *row_base = smem + C::kDS + wg * 16384 + r * 128;
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-                *reinterpret_cast<uint4 *>(row_base + ((c ^ (r & 7)) * 16)) =
-                    make_uint4(dsk[4 * c], dsk[4 * c + 1], dsk[4 * c + 2], dsk[4 * c + 3]);
+            for (int h = 0; h < 2; ++h) {
+                uint32_t b[32], dsk[16];
+                tmem_ld32(tB + loff + wg * 64 + h * 32, b);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    const float4 dd = *reinterpret_cast<const float4 *>(d_s + h * 32 + j);
+                    const float2 y = mul2(make_float2(p[h * 32 + j], p[h * 32 + j + 1]),
+                                          add2(make_float2(__uint_as_float(b[j]), __uint_as_float(b[j + 1])), make_float2(-dd.x, -dd.y)));
+                    const float2 z = mul2(make_float2(p[h * 32 + j + 2], p[h * 32 + j + 3]),
+                                          add2(make_float2(__uint_as_float(b[j + 2]), __uint_as_float(b[j + 3])), make_float2(-dd.z, -dd.w)));
+                    dsk[j / 2] = pack_bf16x2(y.x, y.y);
+                    dsk[j / 2 + 1] = pack_bf16x2(z.x, z.y);
+                }
+                // (columns [32 h, 32 h + 16) of this warpgroup's 64: the first half's lie in columns that have been read)
+                tmem_st16(tB + loff + wg * 64 + h * 16, dsk);
+                // dS^T's row (this key) into the MN-major dS tile: column block wg, 16-byte piece c (queries 8c .. 8c+7) at
+                // piece c ^ (key row mod 8)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    *reinterpret_cast<uint4 *>(row_base + (((h * 4 + c) ^ (r & 7)) * 16)) =
+                        make_uint4(dsk[4 * c], dsk[4 * c + 1], dsk[4 * c + 2], dsk[4 * c + 3]);
+            }
             fence_proxy_async_smem();
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(BAR(DS_READY));
-
-            // this block's part of dQ (TMEM lane = query row): into registers, TMEM A released, then staged in this
-            // block's Q / dO stage (every product that read it has completed by DQ_FULL) for the load warp's reduction
-            if (!mbar_wait_warp(BAR(DQ_FULL), i & 1, kWaitLimitNs)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            uint32_t x0[32], x1[32];
-            tmem_ld32(tA + loff + wg * (D / 2), x0);
-            if constexpr (D == 128) tmem_ld32(tA + loff + wg * (D / 2) + 32, x1);
-            tmem_wait_ld();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(DQ_CONSUMED));
-            constexpr int kPieces = D / 8;  // of 16 bytes, in a row of the warp's slice
-            constexpr int kSliceBytes = 32 * (D / 2) * 4;
-            const int slot = wg * 4 + (warp & 3);
-            uint8_t *srow = smem + C::kStage0 + st * C::kStageBytes + slot * kSliceBytes + lane * (D * 2);
-#pragma unroll
-            for (int c = 0; c < kPieces; ++c) {
-                const uint32_t *x = c < 8 ? x0 : x1;
-                const int cl = c & 7;
-                *reinterpret_cast<uint4 *>(srow + ((c ^ (lane & (kPieces - 1))) * 16)) =
-                    make_uint4(x[4 * cl], x[4 * cl + 1], x[4 * cl + 2], x[4 * cl + 3]);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(DQ_STAGED + st));
         }
         if (ok) ok = mbar_wait_warp(BAR(DONE), 0, kWaitLimitNs);
         if (!ok) packed_timeout();
@@ -512,27 +526,29 @@ fa_packed_pre_kernel(const BwdArgs a, int causal)
     }
 }
 
-// dQ = bf16(scale accumulator), a block of threads per 128 rows of a head, four elements a thread at a time; zeros in rows of
-// no sequence.  Memory-bound.
+// dQ = bf16(scale accumulator), a block of threads per 128 rows of a head, 8 columns a thread at a time: a warp reads 4 whole lines
+// and writes 64 bytes of 8 rows.  (Half a row a thread, whose stores lie a row apart, took 145 us for 15600 rows of 32 heads, d =
+// 128; this ... .)  Zeros in rows of no sequence.  Memory-bound.
 template <int D>
 __global__ void __launch_bounds__(256)
 fa_packed_post_kernel(const BwdArgs a, int causal)
 {
-    constexpr int kPieces = D / 8;  // of 4 floats, in half a row
     if (!plan_fits(a.plan.head, a.T, a.B, causal)) return;
     const int64_t n = static_cast<int64_t>(a.plan.head->n_blocks) * a.heads;
+    wait_for_the_one_before();
     for (int64_t it = blockIdx.x; it < n; it += gridDim.x) {
         const int4 e = a.plan.blocks[it / a.heads];
         const int h = static_cast<int>(it % a.heads);
         const float4 *acc = reinterpret_cast<const float4 *>(a.dq_acc + (static_cast<int64_t>(h) * a.nb + e.w + e.z) * (kBlock * D));
-#pragma unroll 4
-        for (int i = threadIdx.x; i < kBlock * D / 4; i += 256) {
-            const int rr = i / (D / 4), c4 = i % (D / 4), row = e.z * kBlock + rr;
-            if (row >= e.y) break;
-            const int slot = (c4 / kPieces) * 4 + rr / 32, l = rr % 32, c = c4 % kPieces;
-            const float4 x = acc[slot * (32 * kPieces) + l * kPieces + (c ^ (l & (kPieces - 1)))];
-            reinterpret_cast<uint2 *>(packed_row(a.dq, e.x + row, h))[c4] =
-                make_uint2(pack_bf16x2(x.x * a.scale, x.y * a.scale), pack_bf16x2(x.z * a.scale, x.w * a.scale));
+#pragma unroll
+        for (int u = 0; u < kBlock * D / 8 / 256; ++u) {
+            const int i = u * 256 + threadIdx.x, pair = i & 3, r = (i >> 2) & 31, piece = i >> 7;  // (a piece: 32 rows x 32 columns)
+            const int row = e.z * kBlock + piece / (D / 32) * 32 + r;
+            if (row >= e.y) continue;
+            const float4 x = acc[piece * 256 + pair * 64 + r], y = acc[piece * 256 + pair * 64 + 32 + r];
+            reinterpret_cast<uint4 *>(packed_row(a.dq, e.x + row, h))[piece % (D / 32) * 4 + pair] =
+                make_uint4(pack_bf16x2(x.x * a.scale, x.y * a.scale), pack_bf16x2(x.z * a.scale, x.w * a.scale),
+                           pack_bf16x2(y.x * a.scale, y.y * a.scale), pack_bf16x2(y.z * a.scale, y.w * a.scale));
         }
     }
     if (!a.fill) return;
@@ -565,10 +581,9 @@ cudaError_t launch(const FaPackedProblem &p, const BwdArgs &a, cudaStream_t s)
     const unsigned around = static_cast<unsigned>(rows < cap ? rows : cap);
     fa_packed_pre_kernel<D><<<around, 256, 0, s>>>(a, CAUSAL);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    fa_packed_bwd_kernel<D, CAUSAL><<<static_cast<unsigned>(a.nb * p.Hkv), kThreads, C::kSmemBytes, s>>>(mq, mk, mv, mdo, a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    fa_packed_post_kernel<D><<<around, 256, 0, s>>>(a, CAUSAL);
-    return cudaGetLastError();
+    e = launch_behind(fa_packed_bwd_kernel<D, CAUSAL>, static_cast<unsigned>(a.nb * p.Hkv), kThreads, C::kSmemBytes, s, mq, mk, mv, mdo, a);
+    if (e != cudaSuccess) return e;
+    return launch_behind(fa_packed_post_kernel<D>, around, 256, 0, s, a, static_cast<int>(CAUSAL));
 }
 
 }  // namespace
@@ -600,9 +615,10 @@ cudaError_t fa_launch_packed_bwd(const FaPackedProblem &p, void *workspace, cuda
     a.kv_heads = static_cast<int>(p.Hkv);
     a.group = static_cast<int>(p.H / p.Hkv);
     a.fill = p.fill;
-    // about 256 CTAs per group of key heads (at least one head)
-    const int64_t hpg = a.nb >= 256 ? 1 : 256 / a.nb;
-    a.heads_per_group = static_cast<int>(hpg < p.Hkv ? hpg : p.Hkv);
+    // Key heads in groups of about 512 CTAs, of equal size: fewer in one leave SMs without work at its end (8 sequences of 700
+    // to 4096 rows, 8 key heads, 130 blocks: groups of 1 head 1160 us, of 2 1094, of 4 1011), more share less of L2 (of 8 1060).
+    const int64_t most = a.nb < 512 ? 512 / a.nb : 1, groups = p.Hkv > most ? (p.Hkv + most - 1) / most : 1;
+    a.heads_per_group = static_cast<int>((p.Hkv + groups - 1) / groups);
     a.scale = p.scale;
     a.scale_log2 = static_cast<float>(static_cast<double>(p.scale) * 1.4426950408889634);
     if (p.d == 64) return p.causal ? launch<64, true>(p, a, s) : launch<64, false>(p, a, s);
