@@ -19,6 +19,8 @@
 // Every mbarrier wait is bounded; a wait that gives up sets FA_ERR_TIMEOUT and the CTA winds down.
 #include <math.h>
 
+#include <type_traits>
+
 #include "fa_packed.cuh"
 
 using namespace sm100;
@@ -120,27 +122,20 @@ struct Items {
     }
 };
 
-// Keys past `hi` of the tile starting at key k0 to -inf.
-__device__ __forceinline__ void mask_keys(float (&s)[kTile], int k0, int hi)
+// Piece c of the tile of S at tS whose first key is k0, keys past `hi` at -inf; the largest of the others.
+__device__ __forceinline__ float masked_piece(uint32_t tS, int c, int k0, int hi, float (&s)[32])
 {
+    uint32_t r[32];
+    tmem_ld32(tS + c * 32, r);
+    tmem_wait_ld();
+    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-    for (int i = 0; i < kTile; ++i)
-        if (k0 + i > hi) s[i] = -INFINITY;
-}
-
-// Row max of a tile: eight independent chains of 3-input maxes.
-__device__ __forceinline__ float row_max(const float (&s)[kTile])
-{
-    float mx[8];
-#pragma unroll
-    for (int g = 0; g < 8; ++g) {
-        const int b = 16 * g;
-        float a = fmax3(s[b], s[b + 1], s[b + 2]);
-#pragma unroll
-        for (int i = 3; i < 15; i += 2) a = fmax3(a, s[b + i], s[b + i + 1]);
-        mx[g] = fmaxf(a, s[b + 15]);
+    for (int i = 0; i < 32; i += 2) {
+        s[i] = k0 + c * 32 + i > hi ? -INFINITY : __uint_as_float(r[i]);
+        s[i + 1] = k0 + c * 32 + i + 1 > hi ? -INFINITY : __uint_as_float(r[i + 1]);
+        m[i / 2 & 3] = fmax3(m[i / 2 & 3], s[i], s[i + 1]);
     }
-    return fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+    return fmax3(fmaxf(m[0], m[1]), m[2], m[3]);
 }
 
 template <int D, bool CAUSAL, bool PAIR>
@@ -362,23 +357,27 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             float m_ref = -INFINITY;  // reference max, unscaled units
             float l = 0.f;            // exp-sum relative to m_ref (fp32 terms; gives LSE)
             float lr = 0.f;           // the divisor of O (d = 128)
-            for (int j = 0; j < n_mine; ++j) {
-                if (!(ok = mbar_wait_warp(BAR(S_FULL + t), jg & 1, kWaitLimitNs))) break;
+            // One key tile; `masked`: some row does not admit some of its keys (an item's last tile: the diagonal's, or one that
+            // reaches behind the sequence's end).
+            auto tile = [&](auto masked, int j) -> bool {
+                if (!mbar_wait_warp(BAR(S_FULL + t), jg & 1, kWaitLimitNs)) return false;
                 tc_fence_after();
-                // S_t and its row max over the admitted keys: each 32-column piece's max comes with the load; a tile with
-                // masked keys takes the max again over the admitted ones
-                float s[kTile], mt;
-                const int k0 = j * kTile;
-                {
+                // S_t and its row max over the admitted keys: each 32-column piece's max comes with the load.  A masked tile goes
+                // piece by piece, read twice, and leaves out pieces whose keys no row of this warp admits.
+                float s[decltype(masked)::value ? 32 : kTile], mt;
+                const int k0 = j * kTile, hi = CAUSAL ? min(w.len - 1, row0 + row) : w.len - 1;
+                const int hi_warp = CAUSAL ? min(w.len - 1, row0 + (warp & 3) * 32 + 31) : w.len - 1;
+                const int pieces = min((hi_warp - k0) / 32 + 1, 4);
+                if constexpr (decltype(masked)::value) {
+                    mt = -INFINITY;
+#pragma unroll 1
+                    for (int c = 0; c < pieces; ++c) mt = fmaxf(mt, masked_piece(tS, c, k0, hi, s));
+                } else {
                     float pm[4];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) tmem_ld32_max(tS + c * 32, *reinterpret_cast<float(*)[32]>(&s[c * 32]), pm[c]);
                     tmem_wait_ld();
                     mt = fmax3(fmaxf(pm[0], pm[1]), pm[2], pm[3]);
-                }
-                if (k0 + kTile > w.len || (CAUSAL && j == n_mine - 1)) {
-                    mask_keys(s, k0, CAUSAL ? min(w.len - 1, row0 + row) : w.len - 1);
-                    mt = row_max(s);
                 }
                 const float m_new = fmaxf(m_ref, mt);
                 const bool need = (m_new - m_ref) * c_u > kRescaleLog2;  // true while m_ref = -inf
@@ -392,21 +391,43 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 // rounded sum is taken in "heavy" tiles, where the tile's largest P exceeds kHeavyShare of the row's running sum;
                 // over many comparable keys the roundings average out and the fp32 sum serves.  (d = 64: column 64 of O.)  Lanes
                 // behind the sequence's end have no say: what lies there is another's.
-                bool heavy = false;
+                [[maybe_unused]] bool heavy = false;
                 if constexpr (!C::kOnesCol) heavy = __any_sync(0xffffffffu, mine && ex2(fmaf(mt, c_u, -mc)) > kHeavyShare * (l * alpha));
                 const float2 c2 = make_float2(c_u, c_u), nmc2 = make_float2(-mc, -mc);
                 float2 lf[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                if constexpr (decltype(masked)::value) {
+                    // (P's piece c takes the place of half of S's piece c / 2, which has been read; the product reads P up to the
+                    // sequence's end, causal that is behind this warp's rows)
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t p[16];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t p[16];
+                        for (int i = 0; i < 16; ++i) p[i] = 0;
+                        if (c < pieces) {
+                            masked_piece(tS, c, k0, hi, s);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float2 x = fma2(make_float2(s[c * 32 + 2 * i], s[c * 32 + 2 * i + 1]), c2, nmc2);
-                        const float p0 = ex2(x.x), p1 = ex2(x.y);
-                        p[i] = pack_bf16x2(p0, p1);
-                        lf[c] = add2(lf[c], make_float2(p0, p1));
+                            for (int i = 0; i < 16; ++i) {
+                                const float2 x = fma2(make_float2(s[2 * i], s[2 * i + 1]), c2, nmc2);
+                                const float p0 = ex2(x.x), p1 = ex2(x.y);
+                                p[i] = pack_bf16x2(p0, p1);
+                                lf[i & 3] = add2(lf[i & 3], make_float2(p0, p1));
+                            }
+                        }
+                        tmem_st16(tS + c * 16, p);
                     }
-                    tmem_st16(tS + c * 16, p);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t p[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 x = fma2(make_float2(s[c * 32 + 2 * i], s[c * 32 + 2 * i + 1]), c2, nmc2);
+                            const float p0 = ex2(x.x), p1 = ex2(x.y);
+                            p[i] = pack_bf16x2(p0, p1);
+                            lf[c] = add2(lf[c], make_float2(p0, p1));
+                        }
+                        tmem_st16(tS + c * 16, p);
+                    }
                 }
                 const float2 lfs = add2(add2(lf[0], lf[1]), add2(lf[2], lf[3]));
                 if constexpr (!C::kOnesCol) {
@@ -453,7 +474,11 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 __syncwarp();
                 if (lane == 0) mbar_arrive(BAR(P_FULL + t));
                 ++jg;
-            }
+                return true;
+            };
+            const int plain = n_mine - (CAUSAL || n_mine * kTile > w.len ? 1 : 0);
+            for (int j = 0; j < plain && ok; ++j) ok = tile(std::false_type{}, j);
+            if (ok && plain < n_mine) ok = tile(std::true_type{}, plain);
             if (!ok || !(ok = mbar_wait_warp(BAR(O_FULL + t), uc & 1, kWaitLimitNs))) break;
             tc_fence_after();
             // O = u / lr in bf16, LSE from the fp32 sum.  The next item's first product over O_t is issued only after this
