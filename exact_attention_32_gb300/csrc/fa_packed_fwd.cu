@@ -15,7 +15,7 @@
 //   - A 128-row tile that reaches behind its sequence holds rows of others.  Their keys' scores become -inf, their rows of V
 //     zeros (zero_tail_rows, up to a step of the product), their rows of O stay in tensor memory: a whole warp's 32 rows
 //     leave by TMA, the rows of a cut one by stores of their own.
-//   - A thread finds its item in the list, so the next one is asked for an item ahead.
+//   - A thread finds its item in the list; the next one is asked for an item ahead.
 // Every mbarrier wait is bounded; a wait that gives up sets FA_ERR_TIMEOUT and the CTA winds down.
 #include <math.h>
 
@@ -29,10 +29,10 @@ namespace {
 
 constexpr int kTile = 128;    // query rows of a tile, keys of a K/V tile
 // Three warpgroups: two of softmax, and the load and product warps' (two of its warps idle).  Launched with 168 registers a
-// thread (what 384 threads may have); the third gives 80 of its own up, and the softmax, a row's 128 scores a thread, takes 40 more each
+// thread (what 384 threads may have); the third gives 64 of its own up, and the softmax, a row's 128 scores a thread, takes 32 more each
 // (with 168 it spilled up to 250 bytes).
 constexpr int kThreads = 384;
-constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
+constexpr int kLaunchRegs = 168, kSoftmaxRegs = 200, kOtherRegs = 104;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kLaunchRegs, "the warpgroups' shares are what the block has");
 constexpr int kLoadWarp = 8;
 constexpr int kMmaWarp = 9;
@@ -71,20 +71,9 @@ struct FwdArgs {
 
 // An item: up to two tiles of query rows against one key head's keys of a sequence.
 struct Item {
-    int start, len, row, head, kv;
+    int start, len, row, head;
 };
 
-template <bool PAIR>
-__device__ __forceinline__ Item item_of(int4 e, int unit, const FwdArgs &a)
-{
-    Item w;
-    w.start = e.x;
-    w.len = e.y;
-    w.row = e.z * (PAIR ? kTile : 2 * kTile);
-    w.head = PAIR ? 2 * unit : unit;
-    w.kv = w.head / a.group;
-    return w;
-}
 // First row (in the sequence) and head of tile t, and the key tiles it takes: none if it lies behind the sequence's end.
 template <bool PAIR>
 __device__ __forceinline__ int tile_row(const Item &w, int t) { return w.row + (PAIR ? 0 : t * kTile); }
@@ -98,44 +87,65 @@ __device__ __forceinline__ int tile_keys(const Item &w, int t)
     return CAUSAL ? row / kTile + 1 : (w.len + kTile - 1) / kTile;
 }
 
-// The items of this CTA: its r-th of the grid's G CTAs, the order turned around every other round.
+// The items of this CTA: in round r item r G + c of the grid's G CTAs, and in odd rounds r G + G - 1 - c.  The distance
+// from one to the next alternates between two values, so the entry and the unit of an item (entry * units + unit) are
+// carried along without a division (three of them took 600 cycles an item of every role's warp).
 struct Items {
     const int4 *list;
-    int n, units, r, u;
+    int left, units;  // items from this CTA's next on (at most 0: none), units of an entry
+    int entry, unit;
+    int step[2], step_entry[2], step_unit[2];
+    int odd;
     int4 next;
-    __device__ __forceinline__ Items(const int4 *l, int n_items, int n_units) : list(l), n(n_items), units(n_units), r(-1) { ask(); }
-    __device__ __forceinline__ void ask()
+    __device__ __forceinline__ Items(const int4 *l, int n_items, int n_units) : list(l), units(n_units), odd(0)
     {
-        ++r;
         const int G = gridDim.x, c = blockIdx.x;
-        u = r * G + ((r & 1) ? (G - 1 - c) : c);
-        if (u < n) next = __ldg(list + u / units);
+        left = n_items - c;
+        step[0] = 2 * (G - c) - 1;
+        step[1] = 2 * c + 1;
+        for (int i = 0; i < 2; ++i) {
+            step_entry[i] = step[i] / units;
+            step_unit[i] = step[i] - step_entry[i] * units;
+        }
+        entry = c / units;
+        unit = c - entry * units;
+        if (left > 0) next = __ldg(list + entry);
     }
     // The next item, if there is one; the one after it is asked for.
     template <bool PAIR>
-    __device__ __forceinline__ bool take(Item &w, const FwdArgs &a)
+    __device__ __forceinline__ bool take(Item &w)
     {
-        if (u >= n) return false;
-        w = item_of<PAIR>(next, u % units, a);
-        ask();
+        if (left <= 0) return false;
+        w.start = next.x;
+        w.len = next.y;
+        w.row = next.z * (PAIR ? kTile : 2 * kTile);
+        w.head = PAIR ? 2 * unit : unit;
+        left -= odd ? step[1] : step[0];
+        entry += odd ? step_entry[1] : step_entry[0];
+        unit += odd ? step_unit[1] : step_unit[0];
+        odd ^= 1;
+        if (unit >= units) {
+            unit -= units;
+            ++entry;
+        }
+        if (left > 0) next = __ldg(list + entry);
         return true;
     }
 };
 
-// Piece c of the tile of S at tS whose first key is k0, keys past `hi` at -inf; the largest of the others.
-__device__ __forceinline__ float masked_piece(uint32_t tS, int c, int k0, int hi, float (&s)[32])
+// Row max of a tile: eight independent chains of 3-input maxes.
+__device__ __forceinline__ float row_max(const float (&s)[kTile])
 {
-    uint32_t r[32];
-    tmem_ld32(tS + c * 32, r);
-    tmem_wait_ld();
-    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    float mx[8];
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-        s[i] = k0 + c * 32 + i > hi ? -INFINITY : __uint_as_float(r[i]);
-        s[i + 1] = k0 + c * 32 + i + 1 > hi ? -INFINITY : __uint_as_float(r[i + 1]);
-        m[i / 2 & 3] = fmax3(m[i / 2 & 3], s[i], s[i + 1]);
+    for (int g = 0; g < 8; ++g) {
+        const int b = 16 * g;
+        float a = fmax3(s[b], s[b + 1], s[b + 2]);
+#pragma unroll
+        for (int i = 3; i < 15; i += 2) a = fmax3(a, s[b + i], s[b + i + 1]);
+        mx[g] = fmaxf(a, s[b + 15]);
     }
-    return fmax3(fmaxf(m[0], m[1]), m[2], m[3]);
+    return fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
 }
 
 template <int D, bool CAUSAL, bool PAIR>
@@ -207,7 +217,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 prefetch_tmap(&tm_v);
                 bool ok = true;
                 int it = 0, uc = 0;
-                while (ok && items.take<PAIR>(w, a)) {
+                while (ok && items.take<PAIR>(w)) {
                     const int n0 = tile_keys<CAUSAL, PAIR>(w, 0), n1 = tile_keys<CAUSAL, PAIR>(w, 1), n_kv = max(n0, n1);
                     // the Q buffers are free once the item before has issued its last S
                     if (!(ok = mbar_wait(BAR(Q_EMPTY), (uc & 1) ^ 1, kWaitLimitNs))) break;
@@ -217,6 +227,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                             tma_load_3d(sb + t * C::kTileBytes + c * 16384, &tm_q, BAR(Q_FULL), c * 64, w.start + tile_row<PAIR>(w, t),
                                         tile_head<PAIR>(w, t));
                     ++uc;
+                    const int kv = w.head / a.group;
                     for (int j = 0; j < n_kv && ok; ++j)
                         for (int kind = 0; kind < 2; ++kind, ++it) {
                             const int slot = it % C::kStages, use = it / C::kStages;
@@ -224,7 +235,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                             mbar_arrive_expect_tx(FULL(slot), C::kTileBytes);
                             for (int c = 0; c < C::kAtoms; ++c)
                                 tma_load_3d(sb + C::kRing + slot * C::kTileBytes + c * 16384, kind == 0 ? &tm_k : &tm_v, FULL(slot),
-                                            c * 64, w.start + j * kTile, w.kv);
+                                            c * 64, w.start + j * kTile, kv);
                         }
                 }
                 if (!ok) packed_timeout();
@@ -249,7 +260,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             bool ok = true;
             int it = 0, uc = 0;
             int sent[2] = {0, 0};  // S tiles sent to tile 0 / 1 (all items)
-            while (ok && items.take<PAIR>(w, a)) {
+            while (ok && items.take<PAIR>(w)) {
                 const int n[2] = {tile_keys<CAUSAL, PAIR>(w, 0), tile_keys<CAUSAL, PAIR>(w, 1)}, n_kv = max(n[0], n[1]);
                 const int last = (w.len - 1) / kTile, left = w.len - last * kTile;  // the sequence's last key tile, its keys
                 if (!(ok = mbar_wait_warp(BAR(Q_FULL), uc & 1, kWaitLimitNs))) break;
@@ -349,7 +360,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         }
         bool ok = true;
         int jg = 0, uc = 0;
-        while (ok && items.take<PAIR>(w, a)) {
+        while (ok && items.take<PAIR>(w)) {
             const int n_mine = tile_keys<CAUSAL, PAIR>(w, t), row0 = tile_row<PAIR>(w, t);
             if (n_mine == 0) continue;
             const bool mine = row0 + row < w.len;
@@ -362,22 +373,24 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             auto tile = [&](auto masked, int j) -> bool {
                 if (!mbar_wait_warp(BAR(S_FULL + t), jg & 1, kWaitLimitNs)) return false;
                 tc_fence_after();
-                // S_t and its row max over the admitted keys: each 32-column piece's max comes with the load.  A masked tile goes
-                // piece by piece, read twice, and leaves out pieces whose keys no row of this warp admits.
-                float s[decltype(masked)::value ? 32 : kTile], mt;
-                const int k0 = j * kTile, hi = CAUSAL ? min(w.len - 1, row0 + row) : w.len - 1;
-                const int hi_warp = CAUSAL ? min(w.len - 1, row0 + (warp & 3) * 32 + 31) : w.len - 1;
-                const int pieces = min((hi_warp - k0) / 32 + 1, 4);
-                if constexpr (decltype(masked)::value) {
-                    mt = -INFINITY;
-#pragma unroll 1
-                    for (int c = 0; c < pieces; ++c) mt = fmaxf(mt, masked_piece(tS, c, k0, hi, s));
-                } else {
+                // S_t and its row max over the admitted keys: each 32-column piece's max comes with the load; a masked tile takes
+                // the max again over the admitted ones
+                float s[kTile], mt;
+                int pieces = 4;  // with keys that some row of this warp admits
+                {
                     float pm[4];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) tmem_ld32_max(tS + c * 32, *reinterpret_cast<float(*)[32]>(&s[c * 32]), pm[c]);
                     tmem_wait_ld();
                     mt = fmax3(fmaxf(pm[0], pm[1]), pm[2], pm[3]);
+                }
+                if constexpr (decltype(masked)::value) {
+                    const int k0 = j * kTile, hi = (CAUSAL ? min(w.len - 1, row0 + row) : w.len - 1) - k0;
+                    pieces = min(((CAUSAL ? min(w.len - 1, row0 + (warp & 3) * 32 + 31) : w.len - 1) - k0) / 32 + 1, 4);
+#pragma unroll
+                    for (int i = 0; i < kTile; ++i)
+                        if (i > hi) s[i] = -INFINITY;
+                    mt = row_max(s);
                 }
                 const float m_new = fmaxf(m_ref, mt);
                 const bool need = (m_new - m_ref) * c_u > kRescaleLog2;  // true while m_ref = -inf
@@ -395,30 +408,10 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 if constexpr (!C::kOnesCol) heavy = __any_sync(0xffffffffu, mine && ex2(fmaf(mt, c_u, -mc)) > kHeavyShare * (l * alpha));
                 const float2 c2 = make_float2(c_u, c_u), nmc2 = make_float2(-mc, -mc);
                 float2 lf[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                if constexpr (decltype(masked)::value) {
-                    // (P's piece c takes the place of half of S's piece c / 2, which has been read; the product reads P up to the
-                    // sequence's end, causal that is behind this warp's rows)
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t p[16];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) p[i] = 0;
-                        if (c < pieces) {
-                            masked_piece(tS, c, k0, hi, s);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const float2 x = fma2(make_float2(s[2 * i], s[2 * i + 1]), c2, nmc2);
-                                const float p0 = ex2(x.x), p1 = ex2(x.y);
-                                p[i] = pack_bf16x2(p0, p1);
-                                lf[i & 3] = add2(lf[i & 3], make_float2(p0, p1));
-                            }
-                        }
-                        tmem_st16(tS + c * 16, p);
-                    }
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t p[16];
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t p[16];
+                    if (!decltype(masked)::value || c < pieces) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             const float2 x = fma2(make_float2(s[c * 32 + 2 * i], s[c * 32 + 2 * i + 1]), c2, nmc2);
@@ -426,8 +419,11 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                             p[i] = pack_bf16x2(p0, p1);
                             lf[c] = add2(lf[c], make_float2(p0, p1));
                         }
-                        tmem_st16(tS + c * 16, p);
+                    } else {  // (the product reads P up to the sequence's end; causal that is behind this warp's rows)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) p[i] = 0;
                     }
+                    tmem_st16(tS + c * 16, p);
                 }
                 const float2 lfs = add2(add2(lf[0], lf[1]), add2(lf[2], lf[3]));
                 if constexpr (!C::kOnesCol) {
@@ -491,39 +487,43 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             const int head = tile_head<PAIR>(w, t), wrow = row0 + (warp & 3) * 32;  // this warp's first row
             const bool whole = wrow + 32 <= w.len;
             const uint32_t stage = sb + C::kStage + warp * 4096;
-            if (lane == 0) bulk_wait_read0();  // (the item before's O has left the staging buffers)
-            __syncwarp();
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t r[32];
-                tmem_ld32(tO + c * 32, r);
+            for (int c = 0; c < D / 64; ++c) {  // 64 columns at a time: two pieces of 32 rows of 64 bytes
+                uint32_t r[2][32];
+                tmem_ld32(tO + c * 64, r[0]);
+                tmem_ld32(tO + c * 64 + 32, r[1]);
+                if (lane == 0) bulk_wait_read0();  // (what was stored before has left the staging buffers)
                 tmem_wait_ld();
-                uint4 y[4];
+                __syncwarp();
 #pragma unroll
-                for (int q4 = 0; q4 < 4; ++q4) {
-                    y[q4].x = pack_bf16x2(__uint_as_float(r[q4 * 8 + 0]) * inv_l, __uint_as_float(r[q4 * 8 + 1]) * inv_l);
-                    y[q4].y = pack_bf16x2(__uint_as_float(r[q4 * 8 + 2]) * inv_l, __uint_as_float(r[q4 * 8 + 3]) * inv_l);
-                    y[q4].z = pack_bf16x2(__uint_as_float(r[q4 * 8 + 4]) * inv_l, __uint_as_float(r[q4 * 8 + 5]) * inv_l);
-                    y[q4].w = pack_bf16x2(__uint_as_float(r[q4 * 8 + 6]) * inv_l, __uint_as_float(r[q4 * 8 + 7]) * inv_l);
-                }
-                if (whole) {  // 32 rows of 64 bytes in the 64-byte swizzle, one TMA store; two buffers take turns
-                    if (c >= 2) {
-                        if (lane == 0) bulk_wait_read1();
-                        __syncwarp();
+                for (int u = 0; u < 2; ++u) {
+                    uint4 y[4];
+#pragma unroll
+                    for (int q4 = 0; q4 < 4; ++q4) {
+                        const uint32_t *x = r[u] + q4 * 8;
+                        y[q4].x = pack_bf16x2(__uint_as_float(x[0]) * inv_l, __uint_as_float(x[1]) * inv_l);
+                        y[q4].y = pack_bf16x2(__uint_as_float(x[2]) * inv_l, __uint_as_float(x[3]) * inv_l);
+                        y[q4].z = pack_bf16x2(__uint_as_float(x[4]) * inv_l, __uint_as_float(x[5]) * inv_l);
+                        y[q4].w = pack_bf16x2(__uint_as_float(x[6]) * inv_l, __uint_as_float(x[7]) * inv_l);
                     }
-                    const uint32_t buf = stage + (c & 1) * 2048 + lane * 64;
+                    if (whole) {  // in the 64-byte swizzle
+                        const uint32_t buf = stage + u * 2048 + lane * 64;
 #pragma unroll
-                    for (int q4 = 0; q4 < 4; ++q4) st_shared_v4(buf + ((q4 ^ ((lane >> 1) & 3)) << 4), y[q4]);
+                        for (int q4 = 0; q4 < 4; ++q4) st_shared_v4(buf + ((q4 ^ ((lane >> 1) & 3)) << 4), y[q4]);
+                    } else if (mine) {
+                        uint4 *to = reinterpret_cast<uint4 *>(packed_row(a.o, w.start + row0 + row, head) + c * 64 + u * 32);
+#pragma unroll
+                        for (int q4 = 0; q4 < 4; ++q4) to[q4] = y[q4];
+                    }
+                }
+                if (whole) {
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        tma_store_3d(&tm_o, stage + (c & 1) * 2048, c * 32, w.start + wrow, head);
+                        tma_store_3d(&tm_o, stage, c * 64, w.start + wrow, head);
+                        tma_store_3d(&tm_o, stage + 2048, c * 64 + 32, w.start + wrow, head);
                         bulk_commit();
                     }
-                } else if (mine) {
-                    uint4 *to = reinterpret_cast<uint4 *>(packed_row(a.o, w.start + row0 + row, head) + c * 32);
-#pragma unroll
-                    for (int q4 = 0; q4 < 4; ++q4) to[q4] = y[q4];
                 }
             }
             if (mine) a.lse[static_cast<int64_t>(head) * a.T + w.start + row0 + row] = l > 0.f ? m_ref * a.scale + logf(l) : -INFINITY;
