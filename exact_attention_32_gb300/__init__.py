@@ -14,6 +14,7 @@ from ._binding import (FAError, attention, backward, combine, default_scale, fa_
                        KV4Cache, kv4_cache, kv4_append, kv4_read, forward_kv4, kv4_evict, key_weights,
                        KV4CacheStruct, fa_kv4_append, fa_kv4_read, fa_fwd_kv4, fa_fwd_kv4_workspace_bytes,
                        fa_kv4_evict, fa_key_weights, forward_kv4_tree, kv4_keep, kv4_copy_pages, fa_fwd_kv4_tree,
+                       fa_fwd_kv4_tree_workspace_bytes,
                        fa_kv4_keep, fa_kv4_copy_pages, PackedPlan, packed_plan, forward_packed, backward_packed,
                        attention_packed, RowsStruct, fa_packed_plan, fa_packed_plan_bytes, fa_fwd_packed, fa_bwd_packed,
                        fa_bwd_packed_workspace_bytes, fa_get_device_status,

@@ -29,7 +29,7 @@ STATUS_NAMES = {0: "FA_OK", 1: "FA_ERR_INVALID_ARG", 2: "FA_ERR_UNSUPPORTED", 3:
 EXPORTED = ("fa_fwd", "fa_fwd_kernel", "fa_bh_partition", "fa_kv_shard", "fa_fwd_kv_shard", "fa_fwd_slab", "fa_fwd_host", "fa_fwd_mma", "fa_fwd_splitkv", "fa_fwd_splitkv_workspace_bytes", "fa_combine",
             "fa_fwd_splitkv_noalloc", "fa_fwd_fp8", "fa_fwd_blocksparse", "fa_bwd", "fa_bwd_workspace_bytes", "fa_get_device_status",
             "fa_status_string", "fa_version", "fa_kv4_append", "fa_kv4_read", "fa_fwd_kv4", "fa_fwd_kv4_workspace_bytes",
-            "fa_kv4_evict", "fa_key_weights", "fa_fwd_kv4_tree", "fa_kv4_keep", "fa_kv4_copy_pages", "fa_packed_plan",
+            "fa_kv4_evict", "fa_key_weights", "fa_fwd_kv4_tree", "fa_fwd_kv4_tree_workspace_bytes", "fa_kv4_keep", "fa_kv4_copy_pages", "fa_packed_plan",
             "fa_packed_plan_bytes", "fa_fwd_packed", "fa_bwd_packed", "fa_bwd_packed_workspace_bytes")
 
 
@@ -117,6 +117,8 @@ def lib():
             L.fa_key_weights.argtypes = [vp, vp, vp, vp, i64, i64, i64, i64, i64, ctypes.c_float, ctypes.c_int, i64, vp]
             L.fa_fwd_kv4_tree.restype = ctypes.c_int
             L.fa_fwd_kv4_tree.argtypes = [vp, cp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, ctypes.c_float, vp, i64, vp]
+            L.fa_fwd_kv4_tree_workspace_bytes.restype = i64
+            L.fa_fwd_kv4_tree_workspace_bytes.argtypes = [i64] * 6
             L.fa_kv4_keep.restype = ctypes.c_int
             L.fa_kv4_keep.argtypes = [cp, vp, vp, i64, vp, vp, vp, i64, i64, vp, vp]
             L.fa_kv4_copy_pages.restype = ctypes.c_int
@@ -290,6 +292,10 @@ def fa_fwd_kv4_tree(q, cache, lens, page_table, tree, n_new, o, lse, B, H, n_q, 
     """Raw call of attention of a tree of drafts over a 4-bit cache (caller-owned workspace)."""
     return lib().fa_fwd_kv4_tree(q, ctypes.byref(cache), lens, page_table, tree, n_new, o, lse, B, H, n_q, max_pages,
                                  scale, workspace, workspace_bytes, stream)
+
+
+def fa_fwd_kv4_tree_workspace_bytes(B, H, Hkv, n_q, d, max_tokens) -> int:
+    return lib().fa_fwd_kv4_tree_workspace_bytes(B, H, Hkv, n_q, d, max_tokens)
 
 
 def fa_kv4_keep(cache, lens, page_table, max_pages, path, n_path, n_new, B, n_draft, new_lens, stream) -> int:
@@ -682,7 +688,7 @@ def _calls():
         at = [ctypes.cast(f, ctypes.c_void_p).value for f in (
             L.fa_kv4_append, L.fa_kv4_read, L.fa_fwd_kv4, L.fa_fwd_kv4_workspace_bytes, L.fa_kv4_evict, L.fa_key_weights,
             L.fa_fwd_kv4_tree, L.fa_kv4_keep, L.fa_kv4_copy_pages, L.fa_packed_plan, L.fa_packed_plan_bytes, L.fa_fwd_packed,
-            L.fa_bwd_packed, L.fa_bwd_packed_workspace_bytes)]
+            L.fa_bwd_packed, L.fa_bwd_packed_workspace_bytes, L.fa_fwd_kv4_tree_workspace_bytes)]
         m.setup(FAError, tuple(at))
         _marshal = m
     return _marshal
@@ -786,7 +792,7 @@ def forward_kv4_tree(q: torch.Tensor, cache: KV4Cache, lens: torch.Tensor, page_
     are a tree of drafts (their keys already appended), and each attends to the tokens before the drafts and to
     the drafts that its mask names.
 
-    q, cache, lens, page_table, scale, workspace: ``forward_kv4``'s (without ``accumulate``).  tree: int64
+    q, cache, lens, page_table, scale: ``forward_kv4``'s; workspace: ``fa_fwd_kv4_tree_workspace_bytes`` bytes.  tree: int64
     [B, n_q], bit i of tree[b, t] set where draft t admits draft i: its ancestors and itself.  n_new: int32
     [B], how many of the n_q drafts a sequence has (all where None); rows behind them get O = 0, LSE = -inf."""
     call = (_marshal or _calls()).forward_kv4_tree

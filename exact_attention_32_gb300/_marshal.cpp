@@ -38,6 +38,7 @@ decltype(&fa_packed_plan_bytes) p_plan_bytes;
 decltype(&fa_fwd_packed) p_fwd_packed;
 decltype(&fa_bwd_packed) p_bwd_packed;
 decltype(&fa_bwd_packed_workspace_bytes) p_bwd_packed_bytes;
+decltype(&fa_fwd_kv4_tree_workspace_bytes) p_tree_bytes;
 
 constexpr at::ScalarType t_u8 = at::kByte, t_bf16 = at::kBFloat16, t_f32 = at::kFloat, t_i32 = at::kInt, t_i64 = at::kLong;
 
@@ -252,8 +253,12 @@ PyObject *attend(PyObject *const *a, PyObject *tree_arg, PyObject *n_new_arg)
         if (tree.dim[1] != q.dim[2]) return refuse(masks), nullptr;
         if (n_new_arg != Py_None && get_index(n_new_arg, 1, &B, dev, &n_new, N_NEW)) return nullptr;
     }
-    const int64_t need = p_fwd_bytes(B, q.dim[1], c.Hkv, q.dim[2], c.d, table.dim[1] * c.page_size, acc);
-    if (need < 0) return fail(c.d == 64 || c.d == 128 ? FA_ERR_INVALID_ARG : FA_ERR_UNSUPPORTED, "fa_fwd_kv4_workspace_bytes");
+    const int64_t room = table.dim[1] * c.page_size;
+    const int64_t need = tree_arg == nullptr ? p_fwd_bytes(B, q.dim[1], c.Hkv, q.dim[2], c.d, room, acc)
+                                             : p_tree_bytes(B, q.dim[1], c.Hkv, q.dim[2], c.d, room);
+    if (need < 0)
+        return fail(c.d == 64 || c.d == 128 ? FA_ERR_INVALID_ARG : FA_ERR_UNSUPPORTED,
+                    tree_arg == nullptr ? "fa_fwd_kv4_workspace_bytes" : "fa_fwd_kv4_tree_workspace_bytes");
     if (!here(dev)) Py_RETURN_NOTIMPLEMENTED;
     if (a[6] != Py_None &&
         get_tensor(a[6], t_u8, 1, dev, &ws, "workspace must be a contiguous uint8 tensor [bytes] on the cache's device"))
@@ -600,13 +605,13 @@ PyObject *backward_packed(PyObject *const *a, Py_ssize_t n)
 
 // setup(FAError, addresses: a tuple of fa_kv4_append, fa_kv4_read, fa_fwd_kv4, fa_fwd_kv4_workspace_bytes, fa_kv4_evict,
 // fa_key_weights, fa_fwd_kv4_tree, fa_kv4_keep, fa_kv4_copy_pages, fa_packed_plan, fa_packed_plan_bytes, fa_fwd_packed,
-// fa_bwd_packed, fa_bwd_packed_workspace_bytes)
+// fa_bwd_packed, fa_bwd_packed_workspace_bytes, fa_fwd_kv4_tree_workspace_bytes)
 PyObject *setup(PyObject *, PyObject *args)
 {
     PyObject *e;
-    unsigned long long f[14];
-    if (!PyArg_ParseTuple(args, "O(KKKKKKKKKKKKKK)", &e, &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6], &f[7], &f[8], &f[9], &f[10],
-                          &f[11], &f[12], &f[13]))
+    unsigned long long f[15];
+    if (!PyArg_ParseTuple(args, "O(KKKKKKKKKKKKKKK)", &e, &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6], &f[7], &f[8], &f[9], &f[10],
+                          &f[11], &f[12], &f[13], &f[14]))
         return nullptr;
     Py_INCREF(e);  // (lives as long as the module)
     Py_XSETREF(c_error, e);
@@ -624,6 +629,7 @@ PyObject *setup(PyObject *, PyObject *args)
     p_fwd_packed = reinterpret_cast<decltype(p_fwd_packed)>(f[11]);
     p_bwd_packed = reinterpret_cast<decltype(p_bwd_packed)>(f[12]);
     p_bwd_packed_bytes = reinterpret_cast<decltype(p_bwd_packed_bytes)>(f[13]);
+    p_tree_bytes = reinterpret_cast<decltype(p_tree_bytes)>(f[14]);
     Py_RETURN_NONE;
 }
 

@@ -148,7 +148,7 @@ struct Kv4DecodeProblem {
 };
 // Bytes of workspace for sequences of at most max_pages pages.
 int64_t fa_kv4_decode_workspace(int64_t B, int64_t H, int64_t heads, int64_t n_q, int64_t d, int64_t max_tokens,
-                                int accumulate);
+                                int accumulate, bool tree);
 cudaError_t fa_launch_kv4_decode(const Kv4DecodeProblem &p, void *workspace, cudaStream_t stream);
 int fa_kv4_decode_take_status(cudaStream_t stream);
 

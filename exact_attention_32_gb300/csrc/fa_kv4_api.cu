@@ -168,7 +168,13 @@ extern "C" int64_t fa_fwd_kv4_workspace_bytes(int64_t B, int64_t H, int64_t Hkv,
                                               int64_t max_tokens, int accumulate)
 {
     if (check_decode_sizes(B, H, Hkv, n_q, d, max_tokens, accumulate) != FA_OK) return -1;
-    return fa_kv4_decode_workspace(B, H, Hkv, n_q, d, max_tokens, accumulate);
+    return fa_kv4_decode_workspace(B, H, Hkv, n_q, d, max_tokens, accumulate, false);
+}
+
+extern "C" int64_t fa_fwd_kv4_tree_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t n_q, int64_t d, int64_t max_tokens)
+{
+    if (check_decode_sizes(B, H, Hkv, n_q, d, max_tokens, 0) != FA_OK) return -1;
+    return fa_kv4_decode_workspace(B, H, Hkv, n_q, d, max_tokens, 0, true);
 }
 
 namespace {
@@ -184,7 +190,7 @@ int attend(const void *q, const fa_kv4_cache *cache, const int32_t *lens, const 
     if ((st = check_decode_sizes(B, H, cache->Hkv, n_q, cache->d, max_tokens, accumulate)) != FA_OK) return st;
     if (!(scale > 0.f) || !isfinite(scale)) return FA_ERR_INVALID_ARG;
     if (accumulate && cache->weights == nullptr) return FA_ERR_INVALID_ARG;
-    const int64_t need = fa_kv4_decode_workspace(B, H, cache->Hkv, n_q, cache->d, max_tokens, accumulate);
+    const int64_t need = fa_kv4_decode_workspace(B, H, cache->Hkv, n_q, cache->d, max_tokens, accumulate, tree != nullptr);
     if (workspace_bytes < need) return FA_ERR_INVALID_ARG;
     int dev = 0, sm_count = 0;
     if ((st = fa_current_device(&dev, &sm_count)) != FA_OK || (st = check_cache_pointers(cache, dev)) != FA_OK) return st;

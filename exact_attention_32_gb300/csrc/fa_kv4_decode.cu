@@ -61,6 +61,7 @@ constexpr int kMinShare = 4;   // units: a shorter share costs more in merging t
 constexpr int kItemUnits = 3;  // what starting and ending an item costs, in tiles (4 to 6 us beside 1.4 us a tile)
 constexpr int kWholeTiles = 4;  // tables of so few tiles: items go to CTAs whole, and nothing is merged
 constexpr int kSms = 152;
+constexpr int kWideRows = 16;  // trees of more rows a key head: see fa_kv4_rows.cuh
 // A row's reference is set this far (log2) above the largest score when one passes it: with the maximum itself some of a
 // tile's 8 or 16 rows grow in nearly every one of the first dozens of tiles, at 1300 cycles each time.
 constexpr float kHeadroom = 3.f;
@@ -92,6 +93,7 @@ struct DecodeArgs {
     float2 *row_ml;    // [rows]: maximum (log2), 1 / sum; with scores
     int64_t max_pages;
     int B, R, Rs, n_q, n_rc, whole;
+    int item_cost;  // what starting and ending an item costs, in tiles
     float scale_log2;
 };
 
@@ -141,8 +143,8 @@ __host__ __device__ inline int tile_keys(int d) { return 128 * (128 / d); }
 
 // Tiles of one (sequence, head, row chunk): at least one, so that an empty sequence's rows are written too.
 __device__ __forceinline__ int tiles_of(int len, int tk) { return len <= tk ? 1 : (len + tk - 1) / tk; }
-// Units of it: its tiles behind kItemUnits for its start and end; one where items go whole.
-__device__ __forceinline__ int item_units(const DecodeArgs &a, int n_t) { return a.whole ? 1 : n_t + kItemUnits; }
+// Units of it: its tiles behind item_cost for its start and end; one where items go whole.
+__device__ __forceinline__ int item_units(const DecodeArgs &a, int n_t) { return a.whole ? 1 : n_t + a.item_cost; }
 
 // A CTA's way through its share: segments [t0, t1) of the n_t tiles of item `it` (head * n_rc + chunk) of sequence b.
 // The segment that a share begins or ends with may lie in an item's first units and hold no tile.
@@ -165,9 +167,9 @@ __device__ __forceinline__ void walk_clip(Walk &w, const DecodeArgs &a)
         w.t1 = w.n_t;
         return;
     }
-    const int end = static_cast<int>(min(static_cast<int64_t>(w.n_t + kItemUnits), w.at + w.left));
-    w.t0 = max(0, w.at - kItemUnits);
-    w.t1 = max(0, end - kItemUnits);
+    const int end = static_cast<int>(min(static_cast<int64_t>(w.n_t + a.item_cost), w.at + w.left));
+    w.t0 = max(0, w.at - a.item_cost);
+    w.t1 = max(0, end - a.item_cost);
 }
 
 template <int TK>
@@ -182,6 +184,69 @@ __device__ __forceinline__ void walk_next(Walk &w, const DecodeArgs &a)
         walk_open<TK>(w, a);
     }
     walk_clip(w, a);
+}
+
+// The share of this CTA (returned: its units), by all of its THREADS threads: units before each sequence by a scan over the
+// lengths, a thread each at a time; `start`, where it begins, is there behind the next barrier.  `scan` holds a value a warp.
+template <int TK, int THREADS>
+__device__ __forceinline__ int64_t walk_begin(const DecodeArgs &a, Walk &start, int64_t *scan)
+{
+    constexpr int kWarps = THREADS / 32;
+    static_assert(sizeof(Walk) <= 64, "fits before the scan");
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int64_t cap = a.max_pages << a.c.log2_page;
+    const int items = a.c.heads * a.n_rc;
+    auto units_of = [&](int b) -> int64_t {
+        return b < a.B ? static_cast<int64_t>(item_units(a, tiles_of(kv4_length(a.lens, b, cap), TK))) * items : 0;
+    };
+    int64_t total = 0;
+    const int64_t units0 = units_of(tid);  // (most batches have no more sequences than this)
+    {
+        int64_t n = units0;
+        for (int b = tid + THREADS; b < a.B; b += THREADS) n += units_of(b);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+        if (lane == 0) scan[warp] = n;
+        __syncthreads();
+        for (int i = 0; i < kWarps; ++i) total += scan[i];
+    }
+    int64_t share = (total + gridDim.x - 1) / gridDim.x;
+    if (!a.whole && share < kMinShare) share = kMinShare;
+    const int64_t u0 = blockIdx.x * share;
+    if (tid == 0) start.left = 0;
+    int64_t base = 0;
+    for (int b0 = 0; b0 < a.B && base <= u0; b0 += THREADS) {
+        const int b = b0 + tid;
+        const int64_t mine = b0 == 0 ? units0 : units_of(b);
+        int64_t x = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        __syncthreads();
+        if (lane == 31) scan[warp] = x;
+        __syncthreads();
+        int64_t all = 0;
+        for (int i = 0; i < kWarps; ++i) {
+            if (i < warp) x += scan[i];
+            all += scan[i];
+        }
+        const int64_t before = base + x - mine;
+        if (b < a.B && u0 >= before && u0 < before + mine) {
+            Walk w;
+            w.b = b;
+            w.left = min(share, total - u0);
+            walk_open<TK>(w, a);
+            const int units = item_units(a, w.n_t);
+            w.it = static_cast<int>((u0 - before) / units);
+            w.at = static_cast<int>((u0 - before) % units);
+            walk_clip(w, a);
+            start = w;
+        }
+        base += all;
+    }
+    return share;
 }
 
 // Two fp32 -> two E4M3 bytes (`lo` in the low one), and back, exactly.
@@ -258,7 +323,7 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
 {
     using C = DecCfg<D, RT>;
     constexpr int RP = C::RP, N = C::N, KPT = C::KPT, TK = C::TK, ST = C::kStages, SV = C::kStagesV;
-    constexpr int kLoadWarp = C::kLoadWarp, kMmaWarp = C::kMmaWarp, kDecThreads = C::kThreads, kDecWarps = C::kWarps;
+    constexpr int kLoadWarp = C::kLoadWarp, kMmaWarp = C::kMmaWarp, kDecThreads = C::kThreads;
     constexpr int K_FULL = D_STAGES, K_FREE = K_FULL + ST, V_FULL = K_FREE + ST, V_FREE = V_FULL + SV,
                   XS = C::kScales, X_FULL = V_FREE + SV, X_FREE = X_FULL + XS;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -291,61 +356,8 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     }
 
 
-    // the share of this CTA: units before each sequence by a scan over the lengths, a thread each at a time
     Walk &start = *reinterpret_cast<Walk *>(smem + C::kWalk);
-    int64_t *scan = reinterpret_cast<int64_t *>(smem + C::kWalk + 64);
-    static_assert(sizeof(Walk) <= 64, "fits before the scan");
-    const int items = a.c.heads * a.n_rc;
-    auto units_of = [&](int b) -> int64_t {
-        return b < a.B ? static_cast<int64_t>(item_units(a, tiles_of(kv4_length(a.lens, b, cap), TK))) * items : 0;
-    };
-    int64_t total = 0;
-    const int64_t units0 = units_of(tid);  // (most batches have no more sequences than this)
-    {
-        int64_t n = units0;
-        for (int b = tid + kDecThreads; b < a.B; b += kDecThreads) n += units_of(b);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-        if (lane == 0) scan[warp] = n;
-        __syncthreads();
-        for (int i = 0; i < kDecWarps; ++i) total += scan[i];
-    }
-    int64_t share = (total + gridDim.x - 1) / gridDim.x;
-    if (!a.whole && share < kMinShare) share = kMinShare;
-    const int64_t u0 = blockIdx.x * share;
-    if (tid == 0) start.left = 0;
-    int64_t base = 0;
-    for (int b0 = 0; b0 < a.B && base <= u0; b0 += kDecThreads) {
-        const int b = b0 + tid;
-        const int64_t mine = b0 == 0 ? units0 : units_of(b);
-        int64_t x = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-        }
-        __syncthreads();
-        if (lane == 31) scan[warp] = x;
-        __syncthreads();
-        int64_t all = 0;
-        for (int i = 0; i < kDecWarps; ++i) {
-            if (i < warp) x += scan[i];
-            all += scan[i];
-        }
-        const int64_t before = base + x - mine;
-        if (b < a.B && u0 >= before && u0 < before + mine) {
-            Walk w;
-            w.b = b;
-            w.left = min(share, total - u0);
-            walk_open<TK>(w, a);
-            const int units = item_units(a, w.n_t);
-            w.it = static_cast<int>((u0 - before) / units);
-            w.at = static_cast<int>((u0 - before) % units);
-            walk_clip(w, a);
-            start = w;
-        }
-        base += all;
-    }
+    const int64_t share = walk_begin<TK, kDecThreads>(a, start, reinterpret_cast<int64_t *>(smem + C::kWalk + 64));
     if (tid == 0) a.split[blockIdx.x].parts = 0;
     tc_fence_before();
     __syncthreads();
@@ -827,6 +839,8 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     }
 }
 
+#include "fa_kv4_rows.cuh"
+
 // Merge of the items that lie in several shares: a block per CTA of the kernel before, for the item whose first part that
 // CTA holds; its warps over the item's rows and each row's parts.  Where there are few items, and so many parts of each, a
 // block for every row of an item (gridDim.y).
@@ -1015,31 +1029,38 @@ fa_kv4_weights_kernel(const DecodeArgs a, int blocks)
 // ------------------------------------------------------------------ host side
 
 struct Geometry {
-    int rt, n_rc, ctas, whole, Rs;
+    int rt, ng, rows, n_rc, ctas, whole, Rs;  // rows: of a chunk
     int64_t part_o, part_ml, split, scores, row_ml, total;  // byte offsets in the workspace
 };
 
-Geometry geometry(int64_t B, int64_t H, int64_t heads, int64_t n_q, int64_t d, int64_t max_tokens, int accumulate)
+// tree: for fa_fwd_kv4_tree, whose items of more than kWideRows rows a key head go to fa_kv4_rows_kernel (g.ng > 0).
+Geometry geometry(int64_t B, int64_t H, int64_t heads, int64_t n_q, int64_t d, int64_t max_tokens, int accumulate, bool tree)
 {
     Geometry g;
     const int64_t R = H / heads * n_q, rows = B * H * n_q;
+    g.ng = 0;
+    if (tree && R > kWideRows) {
+        g.n_rc = static_cast<int>((R + 47) / 48);
+        g.ng = static_cast<int>(((R + g.n_rc - 1) / g.n_rc + 15) / 16);
+    }
     // 32 sequences of 8192, 4 key heads: a chunk of 16 rows takes 39 to 41 us among others, one of 32 74 (32 rows in one CTA 85, in
     // two of 16 89; 40 rows in two of 32 144, in three of 16 123; 1 key head: 80 rows 67 and 62, 96 rows 67 and 71, 176 even)
     g.rt = R <= 8 ? 1 : R <= 16 || (R + 15) / 16 * 7 < (R + 31) / 32 * 13 ? 2 : 4;
-    g.n_rc = static_cast<int>((R + 8 * g.rt - 1) / (8 * g.rt));
-    const int64_t tk = tile_keys(static_cast<int>(d));
+    if (g.ng == 0) g.n_rc = static_cast<int>((R + 8 * g.rt - 1) / (8 * g.rt));
+    g.rows = g.ng > 0 ? 16 * g.ng : 8 * g.rt;
+    const int64_t tk = g.ng > 0 ? 128 : tile_keys(static_cast<int>(d));
     const int64_t items = B * heads * g.n_rc, tiles = (max_tokens + tk - 1) / tk;
     g.whole = tiles <= kWholeTiles;
     g.Rs = static_cast<int>(R <= 2 ? R : (R + 3) / 4 * 4);
-    const int64_t ctas = kSms * (g.rt == 1 ? 3 : g.rt == 2 ? 2 : 1);
-    const int64_t need = g.whole ? items : (items * (tiles + kItemUnits) + kMinShare - 1) / kMinShare;
+    const int64_t ctas = kSms * (g.ng > 0 ? 1 : g.rt == 1 ? 3 : g.rt == 2 ? 2 : 1);
+    const int64_t need = g.whole ? items : (items * (tiles + (g.ng > 0 ? kRowsItemUnits : kItemUnits)) + kMinShare - 1) / kMinShare;
     g.ctas = static_cast<int>(need < ctas ? need : ctas);
     auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
     int64_t at = 0;
     g.part_o = at;
-    at = up(at + g.ctas * 2 * 8 * g.rt * d * 4);
+    at = up(at + g.ctas * 2 * g.rows * d * 4);
     g.part_ml = at;
-    at = up(at + g.ctas * 2 * 8 * g.rt * 8);
+    at = up(at + g.ctas * 2 * g.rows * 8);
     g.split = at;
     at = up(at + g.ctas * static_cast<int64_t>(sizeof(Split)));
     g.scores = at;
@@ -1106,9 +1127,22 @@ cudaError_t launch_rt(const DecodeArgs &a, int rt, int ctas, cudaStream_t s)
                    : rt == 2 ? launch<D, 2, SCORES, TREE>(a, ctas, s) : launch<D, 4, SCORES, TREE>(a, ctas, s);
 }
 
-template <int D>
-cudaError_t launch_kind(const DecodeArgs &a, int rt, int ctas, cudaStream_t s)
+template <int D, int NG>
+cudaError_t launch_rows(const DecodeArgs &a, int ctas, cudaStream_t s)
 {
+    using C = RowCfg<D, NG>;
+    const cudaError_t e = set_max_dynamic_smem<fa_kv4_rows_kernel<D, NG>>(C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    fa_kv4_rows_kernel<D, NG><<<static_cast<unsigned>(ctas), C::kThreads, C::kSmemBytes, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_kind(const DecodeArgs &a, int rt, int ng, int ctas, cudaStream_t s)
+{
+    if (ng > 0)
+        return ng == 1 ? launch_rows<D, 1>(a, ctas, s) : ng == 2 ? launch_rows<D, 2>(a, ctas, s)
+                       : launch_rows<D, 3>(a, ctas, s);
     if (a.tree != nullptr) return launch_rt<D, false, true>(a, rt, ctas, s);
     return a.scores != nullptr ? launch_rt<D, true, false>(a, rt, ctas, s) : launch_rt<D, false, false>(a, rt, ctas, s);
 }
@@ -1116,15 +1150,15 @@ cudaError_t launch_kind(const DecodeArgs &a, int rt, int ctas, cudaStream_t s)
 }  // namespace
 
 int64_t fa_kv4_decode_workspace(int64_t B, int64_t H, int64_t heads, int64_t n_q, int64_t d, int64_t max_tokens,
-                                int accumulate)
+                                int accumulate, bool tree)
 {
-    return geometry(B, H, heads, n_q, d, max_tokens, accumulate).total;
+    return geometry(B, H, heads, n_q, d, max_tokens, accumulate, tree).total;
 }
 
 cudaError_t fa_launch_kv4_decode(const Kv4DecodeProblem &p, void *workspace, cudaStream_t stream)
 {
     const int64_t cap = p.max_pages << p.cache.log2_page, heads = p.cache.heads;
-    const Geometry g = geometry(p.B, p.H, heads, p.n_q, p.cache.d, cap, p.accumulate);
+    const Geometry g = geometry(p.B, p.H, heads, p.n_q, p.cache.d, cap, p.accumulate, p.tree != nullptr);
     const int64_t rows = p.B * p.H * p.n_q;
     if (rows > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     char *ws = static_cast<char *>(workspace);
@@ -1149,16 +1183,18 @@ cudaError_t fa_launch_kv4_decode(const Kv4DecodeProblem &p, void *workspace, cud
     a.n_rc = g.n_rc;
     a.Rs = g.Rs;
     a.whole = g.whole;
+    a.item_cost = g.ng > 0 ? kRowsItemUnits : kItemUnits;
     a.scale_log2 = static_cast<float>(static_cast<double>(p.scale) * 1.4426950408889634);
-    cudaError_t e = p.cache.d == 128 ? launch_kind<128>(a, g.rt, g.ctas, stream) : launch_kind<64>(a, g.rt, g.ctas, stream);
+    cudaError_t e = p.cache.d == 128 ? launch_kind<128>(a, g.rt, g.ng, g.ctas, stream)
+                                        : launch_kind<64>(a, g.rt, g.ng, g.ctas, stream);
     if (e != cudaSuccess) return e;
     if (!g.whole && g.ctas > 1) {
         // few items of many parts: 8 of 57 parts and 4 rows took 12.3 us with a block an item, 9.2 with one a row
         const int64_t items = p.B * heads * g.n_rc;
-        const int rows = a.R < 8 * g.rt ? a.R : 8 * g.rt;
+        const int rows = a.R < g.rows ? a.R : g.rows;
         const dim3 grid(static_cast<unsigned>(g.ctas), items * 8 <= g.ctas ? rows : 1);
-        e = p.cache.d == 128 ? kv4_launch_behind(fa_kv4_merge_kernel<128>, grid, kMergeWarps * 32, stream, a, 8 * g.rt)
-                             : kv4_launch_behind(fa_kv4_merge_kernel<64>, grid, kMergeWarps * 32, stream, a, 8 * g.rt);
+        e = p.cache.d == 128 ? kv4_launch_behind(fa_kv4_merge_kernel<128>, grid, kMergeWarps * 32, stream, a, g.rows)
+                             : kv4_launch_behind(fa_kv4_merge_kernel<64>, grid, kMergeWarps * 32, stream, a, g.rows);
         if (e != cudaSuccess) return e;
     }
     if (p.accumulate) {

@@ -1,0 +1,697 @@
+// Attention over a 4-bit cache for many rows a key head (part of fa_kv4_decode.cu; its shares, merge and notation).
+//
+// fa_kv4_decode_kernel leaves the codes as they are, since with few rows there is no time to decode them; it pays for that
+// with every score: four products of 32 channels (K's scale differs between them) in two parts of q, and P in three parts.
+// With many rows a key the score's work is what counts.  Here a warpgroup decodes each tile once for up to 48 rows:
+//   S^T = K Q^T      K as halves, code times scale (exact: at most 6 significant bits), Q as halves under one power of two for
+//                    all rows of the item (bf16's 8 bits: exact down to 2^-24 of the largest value of all, off by at most
+//                    2^-32 of that below); one value a score, summed in fp32
+//   O^T += V^T P^T   V's codes as halves, P times V's scale as one half, under a power of two of its row that keeps the
+//                    largest so far between 2^8 and 2^15 (as the decode kernel's, before it is cut in parts)
+// d = 64: V's rows of keys 0-63 and 64-127 of a tile lie side by side, so that the product has 128 rows; P's columns of
+// the second half of the keys lie behind those of the first, and O is the sum of the two diagonal blocks.
+//
+// A tile is 128 keys; a CTA an SM.  A softmax warpgroup takes half of the rows, one thread a key.  Its steps hang on one
+// another (scores, whether a row's maximum grows, P), so two teams of two warpgroups take turns by tile, each with a
+// maximum, a sum and an O of its own, joined at the end of a segment: with one team a tile of 48 rows took 3430 cycles, of which
+// the warps issued in 40 %.
+// Roles (896 threads): warps 0-7 and 8-15 the teams; 16-19 decode K and 20-23 V; 24 loads K's codes and scales, 25 V's; 26 issues S's
+// products and 27 O's (from one warp, in one order, each would wait for what the other waits for: 4000 cycles a tile).
+// Launched with 72 registers a thread, of which the last twelve warps give some to the softmax.
+
+constexpr int kRowsLaunchRegs = 72, kRowsSoftmaxRegs = 88, kRowsOtherRegs = 48;
+// A row's reference is set this far (log2) above the largest score: with the decode kernel's 3 one of 24 rows grew in every
+// sixth tile, at 5000 cycles each time.  Terms of 2^-21 of the largest are then still normal halves.
+constexpr float kRowsHeadroom = 6.f;
+constexpr int kRowsItemUnits = 5;  // what starting and ending an item costs, in tiles
+static_assert(4 * kRowsSoftmaxRegs + 3 * kRowsOtherRegs <= 7 * kRowsLaunchRegs, "the warpgroups' shares are what the block has");
+
+template <int D, int NG>
+struct RowCfg {
+    static constexpr int N = 16 * NG, NH = 8 * NG;  // rows of a CTA, of a softmax warpgroup
+    static constexpr int kThreads = 896, kDecodeWarp = 16, kLoadWarp = 24, kMmaWarp = 26, kPvWarp = 27;
+    static constexpr int TK = 128;
+    static constexpr int kTile = TK * D * 2;
+    static constexpr int kK = 0, kV = 2 * kTile;  // two each
+    static constexpr int kQ = kV + 2 * kTile;
+    static constexpr int kP = kQ + D / 64 * 8192;  // one a team
+    static constexpr int kPBytes = 16384;
+    // tiles as they lie in the pages: K's codes and scales; V's codes; V's scales and whether each run of 16 tokens is there
+    // (which the softmax reads, later than the decoding warps read theirs)
+    static constexpr int kStages = 2, kSmallStages = 4;
+    static constexpr int kCodes = TK * D / 2, kRawKBytes = kCodes + TK * (D / 32), kSmallBytes = TK + 32;
+    static constexpr int kRawK = kP + 2 * kPBytes, kRawV = kRawK + kStages * kRawKBytes, kSmall = kRawV + kStages * kCodes;
+    // a softmax warpgroup's, per pair of rows: {m, m', t, t'} (t: the largest term so far over the maximum, log2), {f, f'},
+    // {alpha, alpha'}, {o_alpha, o_alpha'}; a failed wait
+    static constexpr int kState = kSmall + kSmallStages * kSmallBytes;
+    static constexpr int kStateBytes = 16 * (16 + 8 + 8 + 8) + 16;
+    static constexpr int kRed = kState + 4 * kStateBytes;  // its reductions over warps: float2 [4][32]
+    static constexpr int kMax = kRed + 4 * 1024;           // [warp]: Q's largest value
+    static constexpr int kWalk = kMax + 64;
+    static constexpr int kBar = kWalk + 64 + 8 * (kThreads / 32);
+    static constexpr int kNumBars = 19 + 4 * kStages + 2 * kSmallStages;
+    static constexpr int kSmemBytes = kBar + kNumBars * 8 + 16;
+    static_assert(kSmemBytes <= 232448 && kRawKBytes % 16 == 0 && kStateBytes % 16 == 0 && kWalk % 16 == 0, "shared memory plan");
+    static constexpr int kTmemCols = 512, kO = 128;  // S in columns [0, 64) and [64, 128), O behind them, 128 columns a team
+};
+// of the two buffers of a kind: + 0, + 1; then full and free of the stages of K, of V, and of V's scales
+enum { R_K_READY = 0, R_K_FREE = 2, R_V_READY = 4, R_V_FREE = 6, R_S_FULL = 8, R_S_FREE = 10, R_P_READY = 12, R_PV_DONE = 14, R_Q_READY = 16,
+       R_DONE, R_RAW = R_DONE + 2 };
+
+// Joins V values of every lane over the warp: lane i (i < V) gets the i-th values', by halving: V + 32 / V exchanges, where
+// one value after the other takes 5 V.
+template <int V, typename F>
+__device__ __forceinline__ float over_lanes(float (&v)[V], F join)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = V / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+            const bool upper = lane & o;
+            const float mine = upper ? v[i + o] : v[i], theirs = upper ? v[i] : v[i + o];
+            v[i] = join(mine, __shfl_xor_sync(0xffffffffu, theirs, o));
+        }
+    float x = v[0];
+#pragma unroll
+    for (int o = V; o < 32; o <<= 1) x = join(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+}
+
+template <int D, int NG>
+__global__ void __launch_bounds__(RowCfg<D, NG>::kThreads, 1)
+fa_kv4_rows_kernel(const DecodeArgs a)
+{
+    using C = RowCfg<D, NG>;
+    constexpr int N = C::N, NH = C::NH, TK = C::TK, RS = C::kStages, XS = C::kSmallStages;
+    constexpr int KRAW_FULL = R_RAW, KRAW_FREE = KRAW_FULL + RS, VRAW_FULL = KRAW_FREE + RS, VRAW_FREE = VRAW_FULL + RS, X_FULL = VRAW_FREE + RS,
+                  X_FREE = X_FULL + XS;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sb = smem_u32(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if ((sb & 1023u) != 0) {  // the swizzled tiles need a 1024-byte-aligned base
+        if (tid == 0) kv4_timeout();
+        return;
+    }
+    const uint32_t bar0 = sb + C::kBar;
+    auto BAR = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kBar + C::kNumBars * 8);
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(BAR(R_K_READY + i), 4);
+            mbar_init(BAR(R_K_FREE + i), 1);
+            mbar_init(BAR(R_V_READY + i), 4);
+            mbar_init(BAR(R_V_FREE + i), 1);
+            mbar_init(BAR(R_S_FULL + i), 1);
+            mbar_init(BAR(R_S_FREE + i), 8);
+            mbar_init(BAR(R_P_READY + i), 8);
+            mbar_init(BAR(R_PV_DONE + i), 1);
+        }
+        mbar_init(BAR(R_Q_READY), 16);
+        mbar_init(BAR(R_DONE), 1);
+        mbar_init(BAR(R_DONE + 1), 1);
+        for (int s = 0; s < RS; ++s) {
+            mbar_init(BAR(KRAW_FULL + s), 1);
+            mbar_init(BAR(KRAW_FREE + s), 4);
+            mbar_init(BAR(VRAW_FULL + s), 1);
+            mbar_init(BAR(VRAW_FREE + s), 4);
+        }
+        for (int s = 0; s < XS; ++s) {
+            mbar_init(BAR(X_FULL + s), 1);
+            mbar_init(BAR(X_FREE + s), 8);
+        }
+        fence_mbar_init();
+        // (one thread asks: the status may change while a block starts, and its roles have to agree)
+        tmem_slot[1] = *reinterpret_cast<volatile int *>(&g_kv4_status) != FA_ERR_TIMEOUT;
+    }
+    if (warp == C::kMmaWarp) {
+        tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
+        tmem_relinquish();
+    }
+    Walk &start = *reinterpret_cast<Walk *>(smem + C::kWalk);
+    const int64_t share = walk_begin<TK, C::kThreads>(a, start, reinterpret_cast<int64_t *>(smem + C::kWalk + 64));
+    if (tid == 0) a.split[blockIdx.x].parts = 0;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    Walk w = start;
+    if (tmem_slot[1] == 0) w.left = 0;
+
+    if (warp >= C::kDecodeWarp) {
+        registers_down<kRowsOtherRegs>();
+        if (warp == C::kLoadWarp || warp == C::kLoadWarp + 1) {
+            // ----------------------------------------------------------------- loads: K, or V and its scales
+            const bool values = warp != C::kLoadWarp;
+            const int bt = min(1 << a.c.log2_page, TK), n_boxes = TK / bt;  // tokens a lane loads: a page, or the tile's part of one
+            // the table's entry for this lane's tokens, asked for a tile ahead
+            auto entry = [&](int t) -> int {
+                const int key = t * TK + lane * bt;
+                return lane < n_boxes && key < w.len ? a.table[w.b * a.max_pages + (key >> a.c.log2_page)] : 0;
+            };
+            int n = 0;
+            bool ok = true;
+            while (w.left > 0 && w.t0 == w.t1) walk_next<TK>(w, a);
+            int t = w.t0, next = w.left > 0 ? entry(t) : 0;
+            for (; w.left > 0; ++n) {
+                const int page = next, h = w.it / a.n_rc, key = t * TK + lane * bt;
+                bool there = lane < n_boxes && key < w.len;
+                if (there && static_cast<unsigned>(page) >= static_cast<unsigned>(a.c.n_pages)) {
+                    kv4_report();
+                    there = false;
+                }
+                const uint32_t boxes = __ballot_sync(0xffffffffu, there);
+                if (++t == w.t1) {
+                    do walk_next<TK>(w, a);
+                    while (w.left > 0 && w.t0 == w.t1);
+                    t = w.t0;
+                }
+                if (w.left > 0) next = entry(t);
+                const int st = n % RS, xs = n % XS, tokens = __popc(boxes) * bt;
+                const int64_t row = there ? kv4_row(a.c, page, h, key) : 0;
+                // (rows that are left out keep stale bytes, as good as any: their weight is 0)
+                if (!values) {
+                    if (n >= RS && !(ok = mbar_wait_warp(BAR(KRAW_FREE + st), (n / RS - 1) & 1, kWaitLimitNs))) break;
+                    const uint32_t to = sb + C::kRawK + st * C::kRawKBytes;
+                    if (lane == 0) mbar_arrive_expect_tx(BAR(KRAW_FULL + st), tokens * (D / 2 + D / 32));
+                    __syncwarp();
+                    if (there) {
+                        bulk_load(to + lane * bt * (D / 2), a.c.k + row * (D / 2), bt * (D / 2), BAR(KRAW_FULL + st));
+                        bulk_load(to + C::kCodes + lane * bt * (D / 32), a.c.k_scale + row * (D / 32), bt * (D / 32), BAR(KRAW_FULL + st));
+                    }
+                } else {
+                    if (n >= XS && !(ok = mbar_wait_warp(BAR(X_FREE + xs), (n / XS - 1) & 1, kWaitLimitNs))) break;
+                    uint8_t *small = smem + C::kSmall + xs * C::kSmallBytes;
+                    if (lane < TK / 16) reinterpret_cast<int *>(small + TK)[lane] = (boxes >> (lane * 16 / bt)) & 1u;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_expect_tx(BAR(X_FULL + xs), tokens);
+                    __syncwarp();
+                    if (there) bulk_load(smem_u32(small) + lane * bt, a.c.v_scale + row, bt, BAR(X_FULL + xs));
+                    if (n >= RS && !(ok = mbar_wait_warp(BAR(VRAW_FREE + st), (n / RS - 1) & 1, kWaitLimitNs))) {
+                        ++n;
+                        break;
+                    }
+                    if (lane == 0) mbar_arrive_expect_tx(BAR(VRAW_FULL + st), tokens * (D / 2));
+                    __syncwarp();
+                    if (there)
+                        bulk_load(sb + C::kRawV + st * C::kCodes + lane * bt * (D / 2), a.c.v + row * (D / 2), bt * (D / 2), BAR(VRAW_FULL + st));
+                }
+            }
+            if (!ok && lane == 0) kv4_timeout();
+            // no copy in flight when the CTA ends
+            const uint64_t lim = ok ? kWaitLimitNs : kCleanupLimitNs;
+            for (int i = n > RS ? n - RS : 0; i < n; ++i) mbar_wait(BAR((values ? VRAW_FULL : KRAW_FULL) + i % RS), (i / RS) & 1, lim);
+            for (int i = n > XS ? n - XS : 0; values && i < n; ++i) mbar_wait(BAR(X_FULL + i % XS), (i / XS) & 1, lim);
+        } else if (warp == C::kMmaWarp) {
+            // ------------------------------------------------------------- products of the scores
+            constexpr uint32_t idS = idesc_f16_f32(128, N, false);
+            const uint64_t d_kmaj = smem_desc_sw128(sb, 16, 1024);
+            const uint32_t kmaj = lo32(d_kmaj), kmaj_hi = hi32(d_kmaj);
+            bool ok = true;
+            int n = 0, seg = 0;
+            for (; w.left > 0 && ok; walk_next<TK>(w, a)) {
+                if (w.t0 == w.t1) continue;
+                if (!(ok = mbar_wait_warp(BAR(R_Q_READY), seg++ & 1, kWaitLimitNs))) break;
+                for (int t = w.t0; t < w.t1; ++t, ++n) {
+                    const int buf = n & 1;
+                    if (!(ok = n < 2 ? mbar_wait_warp(BAR(R_K_READY + buf), 0, kWaitLimitNs)
+                                     : wait_both(BAR(R_K_READY + buf), (n >> 1) & 1, BAR(R_S_FREE + buf), ((n >> 1) - 1) & 1)))
+                        break;
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            mma_ss_lohi(tmem + buf * 64, kmaj + ((C::kK + buf * C::kTile + kk / 4 * 16384 + kk % 4 * 32) >> 4), kmaj_hi,
+                                        kmaj + ((C::kQ + kk / 4 * 8192 + kk % 4 * 32) >> 4), kmaj_hi, idS, kk > 0 ? 1u : 0u);
+                        mma_commit(BAR(R_S_FULL + buf));
+                        mma_commit(BAR(R_K_FREE + buf));
+                    }
+                    __syncwarp();
+                }
+            }
+            if (!ok && lane == 0) kv4_timeout();
+            if (elect_one()) mma_commit(BAR(R_DONE));
+            __syncwarp();
+            mbar_wait_warp(BAR(R_DONE), 0, ok ? kWaitLimitNs : kCleanupLimitNs);
+        } else if (warp == C::kPvWarp) {
+            // -------------------------------------------- products of the outputs: O^T (+)= V^T P^T
+            constexpr uint32_t idO = idesc_f16_f32(128, D == 128 ? N : 2 * N, true, true);
+            constexpr int kHalf = D == 128 ? 16384 : 8192;  // between V's (and P's) blocks of 64 columns
+            const uint64_t d_mn = smem_desc_sw128(sb, kHalf, 1024);
+            const uint32_t mn = lo32(d_mn), mn_hi = hi32(d_mn);
+            bool ok = true;
+            int n = 0;
+            for (; w.left > 0 && ok; walk_next<TK>(w, a))
+                for (int t = w.t0; t < w.t1; ++t, ++n) {
+                    const int buf = n & 1;
+                    if (!(ok = wait_both(BAR(R_V_READY + buf), (n >> 1) & 1, BAR(R_P_READY + buf), (n >> 1) & 1))) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < (D == 128 ? 8 : 4); ++kk)
+                            mma_ss_lohi(tmem + C::kO + buf * 128, mn + ((C::kV + buf * C::kTile) >> 4) + kk * 128, mn_hi,
+                                        mn + ((C::kP + buf * C::kPBytes) >> 4) + kk * 128, mn_hi, idO, t < w.t0 + 2 && kk == 0 ? 0u : 1u);
+                        mma_commit(BAR(R_PV_DONE + buf));
+                        mma_commit(BAR(R_V_FREE + buf));
+                    }
+                    __syncwarp();
+                }
+            if (!ok && lane == 0) kv4_timeout();
+            if (elect_one()) mma_commit(BAR(R_DONE + 1));
+            __syncwarp();
+            mbar_wait_warp(BAR(R_DONE + 1), 0, ok ? kWaitLimitNs : kCleanupLimitNs);
+        } else if (warp < C::kLoadWarp) {
+            // ------------------------------------------------ decoding: 32 channels of a key a thread at a time
+            constexpr int PPR = D / 32, TURNS = TK * PPR / 128;
+            bool ok = true;
+            int n = 0;
+            const bool values = warp >= C::kDecodeWarp + 4;  // V (else K)
+            const int free = values ? R_V_FREE : R_K_FREE, ready = values ? R_V_READY : R_K_READY, full = values ? VRAW_FULL : KRAW_FULL,
+                      raw_free = values ? VRAW_FREE : KRAW_FREE;
+            for (; w.left > 0 && ok; walk_next<TK>(w, a))
+                for (int t = w.t0; t < w.t1; ++t, ++n) {
+                    const int st = n % RS, buf = n & 1;
+                    const uint8_t *raw = smem + (values ? C::kRawV + st * C::kCodes : C::kRawK + st * C::kRawKBytes);
+                    if (!(ok = n < 2 ? mbar_wait_warp(BAR(full + st), (n / RS) & 1, kWaitLimitNs)
+                                     : wait_both(BAR(full + st), (n / RS) & 1, BAR(free + buf), ((n >> 1) - 1) & 1)))
+                        break;
+                    // all of a thread's pieces ahead of its stores, which would hold the loads back
+                    uint4 x[TURNS];
+                    __half2 scale[TURNS];
+#pragma unroll
+                    for (int i = 0; i < TURNS; ++i) {
+                        const int piece = i * 128 + (tid & 127);
+                        x[i] = reinterpret_cast<const uint4 *>(raw)[piece];
+                        if (!values) scale[i] = __half2half2(kv4_scale_half(raw[C::kCodes + piece]));
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(BAR(raw_free + st));
+                    // piece i to its row, times a scale or as it is; pieces of the second 64 channels (d = 128) write the other
+                    // half of theirs first, so that the eight lanes of a store meet in no bank
+                    auto put = [&](int i, uint8_t *to, auto scaled) {
+                        const int piece = i * 128 + (tid & 127), key = piece / PPR, p = piece % PPR;
+                        const bool turn = p & 2;
+                        const uint32_t word[4] = {turn ? x[i].z : x[i].x, turn ? x[i].w : x[i].y, turn ? x[i].x : x[i].z, turn ? x[i].y : x[i].w};
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            uint32_t y[4];
+                            kv4_decode8(word[u], y);
+                            if constexpr (decltype(scaled)::value) {
+#pragma unroll
+                                for (int c = 0; c < 4; ++c) {
+                                    const __half2 v = __hmul2(half2_of(y[c]), scale[i]);
+                                    y[c] = *reinterpret_cast<const uint32_t *>(&v);
+                                }
+                            }
+                            *reinterpret_cast<uint4 *>(to + ((((p & 1) * 4 + (u ^ (p & 2))) ^ (key & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+                        }
+                    };
+#pragma unroll
+                    for (int i = 0; i < TURNS; ++i) {
+                        const int piece = i * 128 + (tid & 127), key = piece / PPR, p = piece % PPR;
+                        if (values)
+                            put(i, smem + C::kV + buf * C::kTile + (D == 128 ? (p >> 1) * 16384 + key * 128 : (key >> 6) * 8192 + (key & 63) * 128),
+                                std::false_type{});
+                        else
+                            put(i, smem + C::kK + buf * C::kTile + (p >> 1) * 16384 + key * 128, std::true_type{});
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(BAR(ready + buf));
+                }
+            if (!ok && lane == 0) kv4_timeout();
+        }
+    } else {
+        // --------------------- softmax: warpgroup (team, g) has rows g NH .. g NH + NH - 1 of the team's tiles
+        registers_up<kRowsSoftmaxRegs>();
+        const int wg = warp >> 2, team = wg >> 1, g = wg & 1, wl = warp & 3, tl = tid & 127;  // tl: TMEM lane, the tile's key
+        const uint32_t loff = static_cast<uint32_t>(wl * 32) << 16;
+        uint8_t *const state = smem + C::kState + wg * C::kStateBytes;
+        float4 *sm_mt = reinterpret_cast<float4 *>(state);                         // [row pair] {m, m', t, t'}
+        float2 *sm_f = reinterpret_cast<float2 *>(state + 16 * 16), *sm_alpha = sm_f + 16, *sm_oalpha = sm_alpha + 16;
+        volatile float *sm_fail = reinterpret_cast<volatile float *>(state + 16 * 40);  // a wait gave up: the group leaves together
+        float2 *sm_red = reinterpret_cast<float2 *>(smem + C::kRed + wg * 1024);  // [warp][row]
+        float *sm_max = reinterpret_cast<float *>(smem + C::kMax);                // [warp of team 0]
+        auto sync = [&]() { group_sync(1 + wg); };
+        auto both_sync = [&]() { asm volatile("barrier.cta.sync %0, 256;\n" ::"r"(5 + g) : "memory"); };  // both teams' warpgroups of these rows
+        auto all_sync = [&]() { asm volatile("barrier.cta.sync 7, 512;\n" ::: "memory"); };
+        constexpr int V = NH <= 8 ? 8 : NH <= 16 ? 16 : 32;  // values that over_lanes joins
+        // O's columns of this group's rows, for the tile's keys 0-63 and 64-127 (d = 64)
+        auto o_col = [&](int half, int r) -> uint32_t { return tmem + loff + C::kO + team * 128 + half * N + g * NH + r; };
+        int n = 0;  // tiles of all segments before this one
+        bool ok = true;
+        if (tl == 0) *sm_fail = 0.f;
+        for (; w.left > 0 && ok; walk_next<TK>(w, a)) {
+            if (w.t0 == w.t1) continue;
+            const int h = w.it / a.n_rc, rc = w.it - h * a.n_rc;
+            const int64_t bh = static_cast<int64_t>(w.b) * a.c.heads + h;
+            const int row0 = rc * N + g * NH, n_rows = min(NH, a.R - row0);  // (0 or less: this group has padding only)
+            int newest = min(a.n_q, w.len);  // the sequence's drafts
+            if (a.n_new != nullptr) newest = min(max(a.n_new[w.b], 0), newest);
+            // Q: 8 channels a thread, D / 8 threads a row; the teams share the rows out.  Its largest finite value first.
+            constexpr int TPR = D / 8, TURNS = (N * TPR + 511) / 512;
+            const int64_t q_row0 = bh * a.R + rc * N;
+            uint4 u[TURNS];
+            float amax = 0.f;
+#pragma unroll
+            for (int i = 0; i < TURNS; ++i) {
+                const int r = (i * 512 + tid) / TPR, ch = tid % TPR;
+                u[i] = make_uint4(0, 0, 0, 0);
+                if (r < N && rc * N + r < a.R) u[i] = *reinterpret_cast<const uint4 *>(a.q + (q_row0 + r) * D + ch * 8);
+                const uint32_t x[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float lo = fabsf(__uint_as_float(x[c] << 16)), hi = fabsf(__uint_as_float(x[c] & 0xFFFF0000u));
+                    amax = fmaxf(amax, fmaxf(lo < INFINITY ? lo : 0.f, hi < INFINITY ? hi : 0.f));
+                }
+            }
+            amax = warp_max(amax);
+            if (lane == 0) sm_max[warp] = amax;
+            all_sync();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) amax = fmaxf(amax, sm_max[i]);
+            // its exponent, held where 2^(7 - e) and 2^(e - 7) are normal numbers
+            int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
+            e = amax == 0.f ? 7 : min(max(e, -100), 127);
+            const float up = __uint_as_float(static_cast<uint32_t>(7 - e + 127) << 23);
+            const float mult = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(e - 7 + 127) << 23);
+#pragma unroll
+            for (int i = 0; i < TURNS; ++i) {
+                const int r = (i * 512 + tid) / TPR, ch = tid % TPR;
+                const uint32_t x[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+                uint32_t y[4], bad = 0;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    bad |= (x[c] & 0x7F800000u) == 0x7F800000u || (x[c] & 0x7F80u) == 0x7F80u;
+                    const __half2 z = __floats2half2_rn(__uint_as_float(x[c] << 16) * up, __uint_as_float(x[c] & 0xFFFF0000u) * up);
+                    y[c] = *reinterpret_cast<const uint32_t *>(&z);
+                }
+#pragma unroll
+                for (int o = 1; o < TPR; o <<= 1) bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) y[c] = bad ? 0x7FFF7FFFu : y[c];  // a row with a NaN or an infinity is NaN
+                if (r < N)
+                    *reinterpret_cast<uint4 *>(smem + C::kQ + (ch >> 3) * 8192 + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) =
+                        make_uint4(y[0], y[1], y[2], y[3]);
+            }
+            if (tl < NH / 2) {
+                sm_mt[tl] = make_float4(-FLT_MAX, -FLT_MAX, 0.f, 0.f);
+                sm_f[tl] = make_float2(1.f, 1.f);
+            }
+            fence_proxy_async_smem();
+            sync();
+            if (lane == 0) mbar_arrive(BAR(R_Q_READY));
+            float2 l[NG][4];
+#pragma unroll
+            for (int q = 0; q < NG; ++q)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) l[q][i] = make_float2(0.f, 0.f);
+
+            const int tiles = w.t1 - w.t0, mine0 = (n & 1) == team ? 0 : 1;  // this team's tiles: mine0, mine0 + 2, ...
+            for (int i = mine0; i < tiles; i += 2) {
+                const int nn = n + i, xs = nn % XS, key = (w.t0 + i) * TK + tl;
+                const uint32_t phase = (nn >> 1) & 1;
+                const uint8_t *small = smem + C::kSmall + xs * C::kSmallBytes;
+                ok = wait_both(BAR(X_FULL + xs), (nn / XS) & 1, BAR(R_S_FULL + team), phase);
+                if (!ok) *sm_fail = 1.f;
+                tc_fence_after();
+                // log2 scores of this thread's key
+                float2 x[NG][4];
+                float vs;
+                bool here;
+                {
+                    uint32_t s[NG][8];
+#pragma unroll
+                    for (int q = 0; q < NG; ++q) tmem_ld8(tmem + loff + team * 64 + g * NH + q * 8, s[q]);
+                    vs = kv4_scale(small[tl]);
+                    here = reinterpret_cast<const int *>(small + TK)[tl >> 4] != 0;
+                    tmem_wait_ld();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(BAR(R_S_FREE + team));
+                        mbar_arrive(BAR(X_FREE + xs));
+                    }
+#pragma unroll
+                    for (int q = 0; q < NG; ++q)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            x[q][j] = mul2(make_float2(__uint_as_float(s[q][2 * j]), __uint_as_float(s[q][2 * j + 1])), make_float2(mult, mult));
+                }
+                // keys that a row does not admit, or that no page holds, leave it; what lies there may be anything
+                const bool edge = (w.t0 + i) * TK + TK > w.len - newest || __any_sync(0xffffffffu, !here);
+                if (edge) {
+                    const bool gone = key >= w.len || !here;
+                    const int draft = key - (w.len - newest);
+                    if (gone) vs = 0.f;
+#pragma unroll
+                    for (int q = 0; q < NG; ++q)
+#pragma unroll
+                        for (int r = 0; r < 8; ++r) {
+                            const uint64_t seen = a.tree[static_cast<int64_t>(w.b) * a.n_q + (row0 + q * 8 + r) % a.n_q];
+                            if (gone || (draft >= 0 && ((seen >> (draft & 63)) & 1u) == 0)) (r & 1 ? x[q][r / 2].y : x[q][r / 2].x) = -INFINITY;
+                        }
+                }
+                // does a key pass its row's maximum, or its term the row's largest?  Soon that is rare.  (d: over the maximum)
+                const float lv = lg2(vs);
+                float over = -INFINITY;
+#pragma unroll
+                for (int q = 0; q < NG; ++q)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 mt = sm_mt[q * 4 + j];
+                        const float2 d = add2(x[q][j], make_float2(-mt.x, -mt.y)), z = add2(d, make_float2(lv - mt.z, lv - mt.w));
+                        over = fmaxf(fmax3(over, d.x, d.y), fmaxf(z.x, z.y));
+                    }
+                const bool grows = group_or(1 + wg, over > 0.f);
+                if (*sm_fail != 0.f) {
+                    ok = false;
+                    break;
+                }
+                // the product of the team's tile before has read P (and its O is complete so far)
+                if (nn > 1 && !mbar_wait_warp(BAR(R_PV_DONE + team), phase ^ 1, kWaitLimitNs)) *sm_fail = 1.f;
+                if (grows) {
+                    auto largest = [&](float add) {  // of the warp's keys, row `lane`
+                        float v[V];
+#pragma unroll
+                        for (int r = 0; r < V; ++r) {
+                            const float xr = r < NH ? (r & 1 ? x[r / 8][r / 2 % 4].y : x[r / 8][r / 2 % 4].x) : 0.f;
+                            v[r] = fmaxf(xr + add, -FLT_MAX);
+                        }
+                        return over_lanes<V>(v, [](float p, float q) { return fmaxf(p, q); });
+                    };
+                    const float vm = largest(0.f), zm = largest(lv);
+                    if (lane < NH) sm_red[wl * 32 + lane] = make_float2(vm, zm);
+                    sync();
+                    if (*sm_fail != 0.f) {
+                        ok = false;
+                        break;
+                    }
+                    if (tl < NH) {
+                        float v = -FLT_MAX, z = -FLT_MAX;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const float2 y = sm_red[c * 32 + tl];
+                            v = fmaxf(v, y.x);
+                            z = fmaxf(z, y.y);
+                        }
+                        float *mt = reinterpret_cast<float *>(sm_mt + (tl >> 1)) + (tl & 1);
+                        float *f = reinterpret_cast<float *>(sm_f) + tl;
+                        const float old = mt[0], top = old == -FLT_MAX ? -FLT_MAX : old + mt[2];
+                        v = v > old ? v + kRowsHeadroom : old;
+                        z = z > top ? z + kRowsHeadroom : top;
+                        const float alpha = ex2(old - v);
+                        // the power of two that keeps the terms up to 2^15; held at 2^100 where p itself is next to nothing
+                        const int ef = min(max(__float2int_rd((v - z) + 15.f), -100), 100);
+                        const float now = __uint_as_float(static_cast<uint32_t>(ef + 127) << 23);
+                        reinterpret_cast<float *>(sm_alpha)[tl] = alpha;
+                        reinterpret_cast<float *>(sm_oalpha)[tl] = alpha * (now * inverse_pow2(*f));
+                        mt[0] = v;
+                        mt[2] = fmaxf(z - v, -FLT_MAX);
+                        *f = now;
+                    }
+                    sync();
+#pragma unroll
+                    for (int q = 0; q < NG; ++q)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) l[q][j] = mul2(l[q][j], sm_alpha[q * 4 + j]);
+                    if (i > mine0) {
+                        tc_fence_after();
+#pragma unroll
+                        for (int half = 0; half < 128 / D; ++half)
+#pragma unroll
+                            for (int q = 0; q < NG; ++q) {
+                                uint32_t o[8];
+                                tmem_ld8(o_col(half, q * 8), o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int j = 0; j < 8; j += 2) {
+                                    const float2 y = mul2(make_float2(__uint_as_float(o[j]), __uint_as_float(o[j + 1])), sm_oalpha[q * 4 + j / 2]);
+                                    o[j] = __float_as_uint(y.x);
+                                    o[j + 1] = __float_as_uint(y.y);
+                                }
+                                tmem_st8(o_col(half, q * 8), o);
+                            }
+                        tmem_wait_st();
+                    }
+                }
+                // P: the sum in fp32; the product's operand times V's scale and the row's factor
+                uint32_t y[NG][4];
+#pragma unroll
+                for (int q = 0; q < NG; ++q)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 mt = sm_mt[q * 4 + j];
+                        const float2 d = add2(x[q][j], make_float2(-mt.x, -mt.y));
+                        const float2 p = make_float2(ex2(d.x), ex2(d.y));
+                        l[q][j] = add2(l[q][j], p);
+                        float2 pv = mul2(p, mul2(sm_f[q * 4 + j], make_float2(vs, vs)));
+                        if (edge) {  // a value that a row does not admit stays out of it, a NaN too
+                            if (x[q][j].x == -INFINITY) pv.x = 0.f;
+                            if (x[q][j].y == -INFINITY) pv.y = 0.f;
+                        }
+                        const __half2 z = __floats2half2_rn(pv.x, pv.y);
+                        y[q][j] = *reinterpret_cast<const uint32_t *>(&z);
+                    }
+#pragma unroll
+                for (int q = 0; q < NG; ++q) {  // (behind the loads above: a store in between would hold them back)
+                    const int col = (D == 128 ? 0 : (tl >> 6) * N) + g * NH + q * 8, k = D == 128 ? tl : tl & 63;
+                    *reinterpret_cast<uint4 *>(smem + C::kP + team * C::kPBytes + (col >> 6) * 8192 + k * 128 + ((((col & 63) >> 3) ^ (k & 7)) << 4)) =
+                        make_uint4(y[q][0], y[q][1], y[q][2], y[q][3]);
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(BAR(R_P_READY + team));
+            }
+            // (a group whose wait gave up still meets the others at the barriers below; all leave behind them)
+
+            // ---------------------------------------------------- end of the segment
+            const bool any = mine0 < tiles;  // this team had a tile
+            const int last = n + mine0 + (tiles - 1 - mine0) / 2 * 2;
+            if (any && ok && !mbar_wait_warp(BAR(R_PV_DONE + team), (last >> 1) & 1, kWaitLimitNs)) *sm_fail = 1.f;
+            tc_fence_after();
+            {
+                float v[V];
+#pragma unroll
+                for (int r = 0; r < V; ++r) v[r] = r < NH ? (r & 1 ? l[r / 8][r / 2 % 4].y : l[r / 8][r / 2 % 4].x) : 0.f;
+                const float sum = over_lanes<V>(v, [](float p, float q) { return p + q; });
+                if (lane < NH) sm_red[wl * 32 + lane].x = sum;
+            }
+            all_sync();
+            bool failed = false;  // (all leave where one has to: they meet again at the barriers below)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) failed |= *reinterpret_cast<const volatile float *>(smem + C::kState + i * C::kStateBytes + 16 * 40) != 0.f;
+            if (failed) {
+                ok = false;
+                break;
+            }
+            // A thread a row: what this team's O is multiplied with (the row's factor taken out, under the larger of the teams'
+            // maxima, and over the sum if the segment is the whole item), 0 where nothing is to come of it
+            const bool whole = w.t0 == 0 && w.t1 == w.n_t;
+            const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (n == 0 ? 0 : 1);
+            float *sm_factor = reinterpret_cast<float *>(sm_alpha);
+            if (tl < NH) {
+                const float *state_other = reinterpret_cast<const float *>(smem + C::kState + (wg ^ 2) * C::kStateBytes);
+                const float2 *red_other = reinterpret_cast<const float2 *>(smem + C::kRed + (wg ^ 2) * 1024);
+                const int at = (tl >> 1) * 4 + (tl & 1);
+                const float own = reinterpret_cast<const float *>(sm_mt)[at], other = state_other[at], m = fmaxf(own, other);
+                const float own_f = ex2(own - m);
+                float ll = ((sm_red[tl].x + sm_red[32 + tl].x) + (sm_red[64 + tl].x + sm_red[96 + tl].x)) * own_f +
+                           ((red_other[tl].x + red_other[32 + tl].x) + (red_other[64 + tl].x + red_other[96 + tl].x)) * ex2(other - m);
+                float factor = any ? own_f * inverse_pow2(reinterpret_cast<const float *>(sm_f)[tl]) : 0.f;
+                if ((row0 + tl) % a.n_q >= newest) factor = ll = 0.f;  // no draft of this sequence
+                if (whole) factor *= ll == 0.f ? 0.f : 1.f / ll;
+                sm_factor[tl] = factor;
+                if (team == 0 && tl < n_rows) {
+                    if (whole)
+                        a.lse[bh * a.R + row0 + tl] = ll == 0.f ? -INFINITY : (m + log2f(ll)) * kLn2;
+                    else
+                        a.part_ml[slot * N + g * NH + tl] = make_float2(m, ll);
+                }
+            }
+            if (tid == 0 && w.t0 == 0 && !whole) {
+                Split sp;
+                sp.row = bh * a.R + row0;
+                sp.n_rows = min(N, a.R - row0);
+                sp.parts = 1 + static_cast<int>((w.n_t - w.t1 + share - 1) / share);
+                sp.slot = static_cast<int>(slot);
+                sp.pad = 0;
+                a.split[blockIdx.x] = sp;
+            }
+            sync();
+            const int half = D == 64 ? wl >> 1 : 0;  // d = 64: lanes 64-127 hold keys 64-127's part of channel lane - 64
+            float y[NG][8];
+            {
+                uint32_t o[NG][8];
+#pragma unroll
+                for (int q = 0; q < NG; ++q) tmem_ld8(o_col(half, q * 8), o[q]);
+                tmem_wait_ld();
+#pragma unroll
+                for (int q = 0; q < NG; ++q)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float f = sm_factor[q * 8 + j];
+                        y[q][j] = f == 0.f ? 0.f : __uint_as_float(o[q][j]) * f;
+                    }
+            }
+            tc_fence_before();
+            // scratch: a P buffer of these rows', which the products have read; team 1's values, and (d = 64) lanes 64-127's of each
+            // team
+            float *sx = reinterpret_cast<float *>(smem + C::kP + g * C::kPBytes);
+            if constexpr (D == 128) {
+                if (team == 1)
+#pragma unroll
+                    for (int q = 0; q < NG; ++q)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) sx[(q * 8 + j) * 128 + tl] = y[q][j];
+            } else {
+                if (half == 1)
+#pragma unroll
+                    for (int q = 0; q < NG; ++q)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) sx[(team * NH + q * 8 + j) * 64 + tl - 64] = y[q][j];
+                sync();
+                if (half == 0) {
+#pragma unroll
+                    for (int q = 0; q < NG; ++q)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) y[q][j] += sx[(team * NH + q * 8 + j) * 64 + tl];
+                    if (team == 1)
+#pragma unroll
+                        for (int q = 0; q < NG; ++q)
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) sx[(NH + q * 8 + j) * 64 + tl] = y[q][j];
+                }
+            }
+            both_sync();
+            if (team == 0 && (D == 128 || half == 0)) {
+#pragma unroll
+                for (int q = 0; q < NG; ++q)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) y[q][j] += sx[D == 128 ? (q * 8 + j) * 128 + tl : (NH + q * 8 + j) * 64 + tl];
+#pragma unroll
+                for (int q = 0; q < NG; ++q)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int r = q * 8 + j;
+                        if (r >= n_rows) continue;
+                        if (whole)
+                            a.o[(bh * a.R + row0 + r) * D + tl] = __float2bfloat16_rn(y[q][j]);
+                        else
+                            a.part_o[(slot * N + g * NH + r) * D + tl] = y[q][j];
+                    }
+            }
+            n += tiles;
+            all_sync();  // before the next segment's Q and state take the place of these
+        }
+        if (!ok && lane == 0) kv4_timeout();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == C::kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kTmemCols);
+    }
+}

@@ -235,6 +235,12 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool b_mn_ma
            | (static_cast<uint32_t>(M >> 4) << 24);  // M / 16
 }
 
+// The same with halves as A and B.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major, bool a_mn_major = false)
+{
+    return idesc_bf16_f32(M, N, b_mn_major, a_mn_major) & ~((1u << 7) | (1u << 10));
+}
+
 // D[tmem] (+)= A[smem] * B[smem], descriptors given as (low, high) 32-bit
 // halves: the low half holds the start address, so a K step inside a tile is a
 // 32-bit add on it.

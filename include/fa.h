@@ -572,14 +572,20 @@ int64_t fa_fwd_kv4_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t n_
  *   n_new : const int32 [B], how many of the n_q drafts sequence b has (held to [0, min(n_q, lens[b])]), or NULL
  *           for n_q (for min(n_q, lens[b]) where the sequence is shorter).  Rows t >= n_new[b] get O = 0, LSE = -inf, as does a row
  *           that admits nothing.
- * The other arguments, the workspace (fa_fwd_kv4_workspace_bytes(..., 0)) and the errors are fa_fwd_kv4's
- * without accumulate.  With a chain's masks, (2 << t) - 1, of sequences of n_q tokens and more the result is
- * fa_fwd_kv4's, bit for bit.
+ * The other arguments and the errors are fa_fwd_kv4's without accumulate; the workspace is of
+ * fa_fwd_kv4_tree_workspace_bytes(...).  With a chain's masks, (2 << t) - 1, of sequences of n_q tokens and
+ * more the result is fa_fwd_kv4's up to rounding, and bit for bit where H / Hkv * n_q is at most 16.
+ * The rows of a key head go in chunks of up to 64; its keys are read once per chunk.
  */
 int fa_fwd_kv4_tree(const void *q, const fa_kv4_cache *cache, const int32_t *lens, const int32_t *page_table,
                     const uint64_t *tree, const int32_t *n_new, void *o, float *lse, int64_t B, int64_t H,
                     int64_t n_q, int64_t max_pages, float scale, void *workspace, int64_t workspace_bytes,
                     void *stream);
+
+/* Workspace bytes fa_fwd_kv4_tree needs for sequences of at most max_tokens =
+ * max_pages * page_size tokens, or -1 for invalid sizes.  Pure host computation. */
+int64_t fa_fwd_kv4_tree_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t n_q, int64_t d,
+                                        int64_t max_tokens);
 
 /*
  * fa_kv4_keep - keep an accepted path of the drafts: in each sequence, draft path[b][i] (0 <= i < n_path[b]; at

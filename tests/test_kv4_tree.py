@@ -67,7 +67,7 @@ def test_bad_caches_are_refused_before_any_device_call(kw, code):
 
 def test_bad_arguments_are_refused_before_any_device_call():
     c, p = _struct(), 1 << 20
-    ws = fa.fa_fwd_kv4_workspace_bytes(1, 4, 2, 3, 64, 16, 0)
+    ws = fa.fa_fwd_kv4_tree_workspace_bytes(1, 4, 2, 3, 64, 16)
 
     def tree(tree=p, B=1, H=4, n_q=3, cols=1, scale=0.1, bytes=ws):
         return fa.fa_fwd_kv4_tree(p, c, p, p, tree, None, p, p, B, H, n_q, cols, scale, p, bytes, 0)
@@ -130,7 +130,8 @@ def test_tree_over_long_ragged_lengths(d, P, Hkv, G, n_q):
 
 @gpu
 @pytest.mark.parametrize("d,G,n_q", [(64, 4, 3), (128, 8, 1), (128, 2, 16), (64, 3, 7)])
-def test_a_chain_gives_the_causal_call_bit_for_bit(d, G, n_q):
+def test_a_chain_gives_the_causal_call(d, G, n_q):
+    # bit for bit up to 16 rows a key head; above that another kernel's sums, within the same bounds
     lens = np.array([n_q, 500, 2000, 129, n_q + 1], np.int32)
     rng = np.random.default_rng(n_q)
     pool = Pool(5, 2, d, 32, lens, seed=n_q)
@@ -140,7 +141,10 @@ def test_a_chain_gives_the_causal_call_bit_for_bit(d, G, n_q):
     a = fa.forward_kv4(q, c, dev(lens), dev(pool.table))
     b = fa.forward_kv4_tree(q, c, dev(lens), dev(pool.table), chain)
     ok()
-    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    if G * n_q <= 16:
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    for o, lse in (a, b):
+        check_tree(pool, q, lens, fa.default_scale(d), chain.cpu().numpy(), None, o, lse)
 
 
 @gpu
