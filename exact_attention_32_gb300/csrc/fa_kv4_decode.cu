@@ -61,7 +61,10 @@ constexpr int kMinShare = 4;   // units: a shorter share costs more in merging t
 constexpr int kItemUnits = 3;  // what starting and ending an item costs, in tiles (4 to 6 us beside 1.4 us a tile)
 constexpr int kWholeTiles = 4;  // tables of so few tiles: items go to CTAs whole, and nothing is merged
 constexpr int kSms = 152;
-constexpr int kWideRows = 16;  // trees of more rows a key head: see fa_kv4_rows.cuh
+// Trees of more rows a key head than this: fa_kv4_rows_kernel.  32 sequences of up to 8192, 8 key heads, that kernel and the
+// other: d = 128 24 rows 93 and 101 us, 32 rows 98 and 108, 48 rows 111 and 160, 64 rows 165 and 186, 128 rows 261 and 350;
+// d = 64 24 rows 89 and 81, 32 rows 82 and 77, 48 rows 108 and 124, 64 rows 141 and 140, 128 rows 249 and 268.
+constexpr int wide_rows(int64_t d) { return d == 128 ? 16 : 32; }
 // A row's reference is set this far (log2) above the largest score when one passes it: with the maximum itself some of a
 // tile's 8 or 16 rows grow in nearly every one of the first dozens of tiles, at 1300 cycles each time.
 constexpr float kHeadroom = 3.f;
@@ -496,9 +499,12 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             const int row0 = rc * RP + g * 8, n_rows = min(8, a.R - row0);  // (0 or less: this group has padding only)
             // newest tokens that not every row admits: all n_q, whatever the length is, or the sequence's drafts
             int newest = a.n_q;
+            uint2 seen = make_uint2(0, 0);  // the drafts that row row0 + lane % 8 admits
             if constexpr (TREE) {
                 newest = min(newest, w.len);
                 if (a.n_new != nullptr) newest = min(max(a.n_new[w.b], 0), newest);
+                const uint64_t s = a.tree[static_cast<int64_t>(w.b) * a.n_q + (row0 + (lane & 7)) % a.n_q];
+                seen = make_uint2(static_cast<uint32_t>(s), static_cast<uint32_t>(s >> 32));
             }
             // Q: 8 channels a thread, D / 8 threads a row
             constexpr int TPR = D / 8;
@@ -610,8 +616,8 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                             bool out = gone;
                             if constexpr (TREE) {
                                 const int draft = key - (w.len - newest);
-                                const uint64_t seen = a.tree[static_cast<int64_t>(w.b) * a.n_q + (row0 + r) % a.n_q];
-                                out |= draft >= 0 && ((seen >> (draft & 63)) & 1u) == 0;
+                                const uint32_t lo = __shfl_sync(0xffffffffu, seen.x, r), hi = __shfl_sync(0xffffffffu, seen.y, r);
+                                out |= draft >= 0 && (((draft & 32 ? hi : lo) >> (draft & 31)) & 1u) == 0;
                             } else {
                                 out |= key >= w.len - a.n_q + 1 + (row0 + r) % a.n_q;
                             }
@@ -1033,13 +1039,13 @@ struct Geometry {
     int64_t part_o, part_ml, split, scores, row_ml, total;  // byte offsets in the workspace
 };
 
-// tree: for fa_fwd_kv4_tree, whose items of more than kWideRows rows a key head go to fa_kv4_rows_kernel (g.ng > 0).
+// tree: for fa_fwd_kv4_tree, whose items of more than wide_rows(d) rows a key head go to fa_kv4_rows_kernel (g.ng > 0).
 Geometry geometry(int64_t B, int64_t H, int64_t heads, int64_t n_q, int64_t d, int64_t max_tokens, int accumulate, bool tree)
 {
     Geometry g;
     const int64_t R = H / heads * n_q, rows = B * H * n_q;
     g.ng = 0;
-    if (tree && R > kWideRows) {
+    if (tree && R > wide_rows(d)) {
         g.n_rc = static_cast<int>((R + 47) / 48);
         g.ng = static_cast<int>(((R + g.n_rc - 1) / g.n_rc + 15) / 16);
     }
@@ -1123,8 +1129,10 @@ cudaError_t launch(const DecodeArgs &a, int ctas, cudaStream_t s)
 template <int D, bool SCORES, bool TREE>
 cudaError_t launch_rt(const DecodeArgs &a, int rt, int ctas, cudaStream_t s)
 {
-    return rt == 1 ? launch<D, 1, SCORES, TREE>(a, ctas, s)
-                   : rt == 2 ? launch<D, 2, SCORES, TREE>(a, ctas, s) : launch<D, 4, SCORES, TREE>(a, ctas, s);
+    if (rt == 1) return launch<D, 1, SCORES, TREE>(a, ctas, s);
+    if constexpr (!TREE || wide_rows(D) > 16)
+        if (rt == 4) return launch<D, 4, SCORES, TREE>(a, ctas, s);
+    return launch<D, 2, SCORES, TREE>(a, ctas, s);
 }
 
 template <int D, int NG>

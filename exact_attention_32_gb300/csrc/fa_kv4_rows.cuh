@@ -3,9 +3,9 @@
 // fa_kv4_decode_kernel leaves the codes as they are, since with few rows there is no time to decode them; it pays for that
 // with every score: four products of 32 channels (K's scale differs between them) in two parts of q, and P in three parts.
 // With many rows a key the score's work is what counts.  Here a warpgroup decodes each tile once for up to 48 rows:
-//   S^T = K Q^T      K as halves, code times scale (exact: at most 6 significant bits), Q as halves under one power of two for
-//                    all rows of the item (bf16's 8 bits: exact down to 2^-24 of the largest value of all, off by at most
-//                    2^-32 of that below); one value a score, summed in fp32
+//   S^T = K Q^T      K as halves, code times scale (exact: at most 6 significant bits), Q as halves under a power of two of its
+//                    row (bf16's 8 bits: exact down to 2^-24 of the row's largest value, off by at most 2^-32 of that
+//                    below); one value a score, summed in fp32
 //   O^T += V^T P^T   V's codes as halves, P times V's scale as one half, under a power of two of its row that keeps the
 //                    largest so far between 2^8 and 2^15 (as the decode kernel's, before it is cut in parts)
 // d = 64: V's rows of keys 0-63 and 64-127 of a tile lie side by side, so that the product has 128 rows; P's columns of
@@ -23,7 +23,9 @@ constexpr int kRowsLaunchRegs = 72, kRowsSoftmaxRegs = 88, kRowsOtherRegs = 48;
 // A row's reference is set this far (log2) above the largest score: with the decode kernel's 3 one of 24 rows grew in every
 // sixth tile, at 5000 cycles each time.  Terms of 2^-21 of the largest are then still normal halves.
 constexpr float kRowsHeadroom = 6.f;
-constexpr int kRowsItemUnits = 5;  // what starting and ending an item costs, in tiles
+// What starting and ending an item costs, in tiles.  48 rows, 32 sequences of up to 8192: 6 126 us, 9 112, 12 111, 16 117; 32 rows
+// 96, 98, 103, 103; 128 rows 300, 261, 266, 270.
+constexpr int kRowsItemUnits = 9;
 static_assert(4 * kRowsSoftmaxRegs + 3 * kRowsOtherRegs <= 7 * kRowsLaunchRegs, "the warpgroups' shares are what the block has");
 
 template <int D, int NG>
@@ -42,12 +44,12 @@ struct RowCfg {
     static constexpr int kCodes = TK * D / 2, kRawKBytes = kCodes + TK * (D / 32), kSmallBytes = TK + 32;
     static constexpr int kRawK = kP + 2 * kPBytes, kRawV = kRawK + kStages * kRawKBytes, kSmall = kRawV + kStages * kCodes;
     // a softmax warpgroup's, per pair of rows: {m, m', t, t'} (t: the largest term so far over the maximum, log2), {f, f'},
-    // {alpha, alpha'}, {o_alpha, o_alpha'}; a failed wait
+    // {alpha, alpha'}, {o_alpha, o_alpha'}; the rows' masks; a failed wait
     static constexpr int kState = kSmall + kSmallStages * kSmallBytes;
-    static constexpr int kStateBytes = 16 * (16 + 8 + 8 + 8) + 16;
+    static constexpr int kSeen = 16 * (16 + 8 + 8 + 8), kFail = kSeen + 8 * 32, kStateBytes = kFail + 16;
     static constexpr int kRed = kState + 4 * kStateBytes;  // its reductions over warps: float2 [4][32]
-    static constexpr int kMax = kRed + 4 * 1024;           // [warp]: Q's largest value
-    static constexpr int kWalk = kMax + 64;
+    static constexpr int kMult = kRed + 4 * 1024;          // of all rows
+    static constexpr int kWalk = kMult + 4 * 48;
     static constexpr int kBar = kWalk + 64 + 8 * (kThreads / 32);
     static constexpr int kNumBars = 19 + 4 * kStages + 2 * kSmallStages;
     static constexpr int kSmemBytes = kBar + kNumBars * 8 + 16;
@@ -330,9 +332,10 @@ fa_kv4_rows_kernel(const DecodeArgs a)
         uint8_t *const state = smem + C::kState + wg * C::kStateBytes;
         float4 *sm_mt = reinterpret_cast<float4 *>(state);                         // [row pair] {m, m', t, t'}
         float2 *sm_f = reinterpret_cast<float2 *>(state + 16 * 16), *sm_alpha = sm_f + 16, *sm_oalpha = sm_alpha + 16;
-        volatile float *sm_fail = reinterpret_cast<volatile float *>(state + 16 * 40);  // a wait gave up: the group leaves together
+        volatile float *sm_fail = reinterpret_cast<volatile float *>(state + C::kFail);  // a wait gave up: the group leaves together
+        uint64_t *sm_seen = reinterpret_cast<uint64_t *>(state + C::kSeen);
         float2 *sm_red = reinterpret_cast<float2 *>(smem + C::kRed + wg * 1024);  // [warp][row]
-        float *sm_max = reinterpret_cast<float *>(smem + C::kMax);                // [warp of team 0]
+        float *sm_mult = reinterpret_cast<float *>(smem + C::kMult);              // [row]: a product of its halves times this is the score
         auto sync = [&]() { group_sync(1 + wg); };
         auto both_sync = [&]() { asm volatile("barrier.cta.sync %0, 256;\n" ::"r"(5 + g) : "memory"); };  // both teams' warpgroups of these rows
         auto all_sync = [&]() { asm volatile("barrier.cta.sync 7, 512;\n" ::: "memory"); };
@@ -349,58 +352,49 @@ fa_kv4_rows_kernel(const DecodeArgs a)
             const int row0 = rc * N + g * NH, n_rows = min(NH, a.R - row0);  // (0 or less: this group has padding only)
             int newest = min(a.n_q, w.len);  // the sequence's drafts
             if (a.n_new != nullptr) newest = min(max(a.n_new[w.b], 0), newest);
-            // Q: 8 channels a thread, D / 8 threads a row; the teams share the rows out.  Its largest finite value first.
+            // Q: 8 channels a thread, D / 8 threads a row; the teams share the rows out.
             constexpr int TPR = D / 8, TURNS = (N * TPR + 511) / 512;
             const int64_t q_row0 = bh * a.R + rc * N;
             uint4 u[TURNS];
-            float amax = 0.f;
 #pragma unroll
             for (int i = 0; i < TURNS; ++i) {
                 const int r = (i * 512 + tid) / TPR, ch = tid % TPR;
                 u[i] = make_uint4(0, 0, 0, 0);
                 if (r < N && rc * N + r < a.R) u[i] = *reinterpret_cast<const uint4 *>(a.q + (q_row0 + r) * D + ch * 8);
-                const uint32_t x[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const float lo = fabsf(__uint_as_float(x[c] << 16)), hi = fabsf(__uint_as_float(x[c] & 0xFFFF0000u));
-                    amax = fmaxf(amax, fmaxf(lo < INFINITY ? lo : 0.f, hi < INFINITY ? hi : 0.f));
-                }
             }
-            amax = warp_max(amax);
-            if (lane == 0) sm_max[warp] = amax;
-            all_sync();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) amax = fmaxf(amax, sm_max[i]);
-            // its exponent, held where 2^(7 - e) and 2^(e - 7) are normal numbers
-            int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
-            e = amax == 0.f ? 7 : min(max(e, -100), 127);
-            const float up = __uint_as_float(static_cast<uint32_t>(7 - e + 127) << 23);
-            const float mult = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(e - 7 + 127) << 23);
 #pragma unroll
             for (int i = 0; i < TURNS; ++i) {
                 const int r = (i * 512 + tid) / TPR, ch = tid % TPR;
                 const uint32_t x[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-                uint32_t y[4], bad = 0;
+                uint32_t top = 0;  // the largest magnitude's bits
+#pragma unroll
+                for (int c = 0; c < 4; ++c) top = max(top, max((x[c] << 16) & 0x7FFFFFFFu, x[c] & 0x7FFF0000u));
+#pragma unroll
+                for (int o = 1; o < TPR; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const bool bad = top >= 0x7F800000u;
+                // its exponent, held where 2^(7 - e) and 2^(e - 7) are normal numbers
+                const int e = top == 0 ? 7 : min(max(static_cast<int>(top >> 23) - 127, -100), 127);
+                const float up = __uint_as_float(static_cast<uint32_t>(7 - e + 127) << 23);
+                if (r < N && ch == 0) sm_mult[r] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(e - 7 + 127) << 23);
+                uint32_t y[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    bad |= (x[c] & 0x7F800000u) == 0x7F800000u || (x[c] & 0x7F80u) == 0x7F80u;
                     const __half2 z = __floats2half2_rn(__uint_as_float(x[c] << 16) * up, __uint_as_float(x[c] & 0xFFFF0000u) * up);
                     y[c] = *reinterpret_cast<const uint32_t *>(&z);
                 }
-#pragma unroll
-                for (int o = 1; o < TPR; o <<= 1) bad |= __shfl_xor_sync(0xffffffffu, bad, o);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) y[c] = bad ? 0x7FFF7FFFu : y[c];  // a row with a NaN or an infinity is NaN
                 if (r < N)
                     *reinterpret_cast<uint4 *>(smem + C::kQ + (ch >> 3) * 8192 + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) =
                         make_uint4(y[0], y[1], y[2], y[3]);
             }
+            if (tl < NH) sm_seen[tl] = a.tree[static_cast<int64_t>(w.b) * a.n_q + (row0 + tl) % a.n_q];
             if (tl < NH / 2) {
                 sm_mt[tl] = make_float4(-FLT_MAX, -FLT_MAX, 0.f, 0.f);
                 sm_f[tl] = make_float2(1.f, 1.f);
             }
             fence_proxy_async_smem();
-            sync();
+            all_sync();
             if (lane == 0) mbar_arrive(BAR(R_Q_READY));
             float2 l[NG][4];
 #pragma unroll
@@ -437,21 +431,22 @@ fa_kv4_rows_kernel(const DecodeArgs a)
                     for (int q = 0; q < NG; ++q)
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            x[q][j] = mul2(make_float2(__uint_as_float(s[q][2 * j]), __uint_as_float(s[q][2 * j + 1])), make_float2(mult, mult));
+                            x[q][j] = mul2(make_float2(__uint_as_float(s[q][2 * j]), __uint_as_float(s[q][2 * j + 1])),
+                                           *reinterpret_cast<const float2 *>(sm_mult + g * NH + q * 8 + 2 * j));
                 }
                 // keys that a row does not admit, or that no page holds, leave it; what lies there may be anything
                 const bool edge = (w.t0 + i) * TK + TK > w.len - newest || __any_sync(0xffffffffu, !here);
                 if (edge) {
                     const bool gone = key >= w.len || !here;
-                    const int draft = key - (w.len - newest);
+                    const int draft = key - (w.len - newest), bit = draft & 63;
                     if (gone) vs = 0.f;
+                    const uint32_t *seen = reinterpret_cast<const uint32_t *>(sm_seen) + (bit >> 5);
 #pragma unroll
                     for (int q = 0; q < NG; ++q)
 #pragma unroll
-                        for (int r = 0; r < 8; ++r) {
-                            const uint64_t seen = a.tree[static_cast<int64_t>(w.b) * a.n_q + (row0 + q * 8 + r) % a.n_q];
-                            if (gone || (draft >= 0 && ((seen >> (draft & 63)) & 1u) == 0)) (r & 1 ? x[q][r / 2].y : x[q][r / 2].x) = -INFINITY;
-                        }
+                        for (int r = 0; r < 8; ++r)
+                            if (gone || (draft >= 0 && ((seen[2 * (q * 8 + r)] >> (bit & 31)) & 1u) == 0))
+                                (r & 1 ? x[q][r / 2].y : x[q][r / 2].x) = -INFINITY;
                 }
                 // does a key pass its row's maximum, or its term the row's largest?  Soon that is rare.  (d: over the maximum)
                 const float lv = lg2(vs);
@@ -582,7 +577,7 @@ fa_kv4_rows_kernel(const DecodeArgs a)
             all_sync();
             bool failed = false;  // (all leave where one has to: they meet again at the barriers below)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) failed |= *reinterpret_cast<const volatile float *>(smem + C::kState + i * C::kStateBytes + 16 * 40) != 0.f;
+            for (int i = 0; i < 4; ++i) failed |= *reinterpret_cast<const volatile float *>(smem + C::kState + i * C::kStateBytes + C::kFail) != 0.f;
             if (failed) {
                 ok = false;
                 break;

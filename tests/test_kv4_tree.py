@@ -129,6 +129,22 @@ def test_tree_over_long_ragged_lengths(d, P, Hkv, G, n_q):
 
 
 @gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,n_q", [(2, 5), (5, 8), (4, 16)])
+def test_rows_of_very_different_size(d, G, n_q):
+    # the bounds are each row's own: what is rounded under the largest value of other rows would pass them
+    lens = np.array([200, 700], np.int32)
+    rng = np.random.default_rng(d + n_q)
+    pool = Pool(2, 2, d, 32, lens, seed=d + n_q)
+    q = bf16(rng.standard_normal((2, 2 * G, n_q, d)) * 2.0 ** rng.integers(-30, 4, (2, 2 * G, n_q, 1))).cuda()
+    _, masks = random_tree(rng, 2, n_q)
+    for gain in (1.0, 2.0 ** 24):
+        o, lse = fa.forward_kv4_tree(q * gain, pool.cache(), dev(lens), dev(pool.table), dev(masks), scale=float(0.125 / gain))
+        ok()
+        check_tree(pool, q * gain, lens, 0.125 / gain, masks, None, o, lse)
+
+
+@gpu
 @pytest.mark.parametrize("d,G,n_q", [(64, 4, 3), (128, 8, 1), (128, 2, 16), (64, 3, 7)])
 def test_a_chain_gives_the_causal_call(d, G, n_q):
     # bit for bit up to 16 rows a key head; above that another kernel's sums, within the same bounds
