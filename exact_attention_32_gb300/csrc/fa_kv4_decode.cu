@@ -61,10 +61,6 @@ constexpr int kMinShare = 4;   // units: a shorter share costs more in merging t
 constexpr int kItemUnits = 3;  // what starting and ending an item costs, in tiles (4 to 6 us beside 1.4 us a tile)
 constexpr int kWholeTiles = 4;  // tables of so few tiles: items go to CTAs whole, and nothing is merged
 constexpr int kSms = 152;
-// Trees of more rows a key head than this: fa_kv4_rows_kernel.  32 sequences of up to 8192, 8 key heads, that kernel and the
-// other: d = 128 24 rows 93 and 101 us, 32 rows 98 and 108, 48 rows 111 and 160, 64 rows 165 and 186, 128 rows 261 and 350;
-// d = 64 24 rows 89 and 81, 32 rows 82 and 77, 48 rows 108 and 124, 64 rows 141 and 140, 128 rows 249 and 268.
-constexpr int wide_rows(int64_t d) { return d == 128 ? 16 : 32; }
 // A row's reference is set this far (log2) above the largest score when one passes it: with the maximum itself some of a
 // tile's 8 or 16 rows grow in nearly every one of the first dozens of tiles, at 1300 cycles each time.
 constexpr float kHeadroom = 3.f;
@@ -1039,19 +1035,35 @@ struct Geometry {
     int64_t part_o, part_ml, split, scores, row_ml, total;  // byte offsets in the workspace
 };
 
-// tree: for fa_fwd_kv4_tree, whose items of more than wide_rows(d) rows a key head go to fa_kv4_rows_kernel (g.ng > 0).
+// tree: for fa_fwd_kv4_tree, whose items of many rows a key head go to fa_kv4_rows_kernel (g.ng > 0) or, where there is little work,
+// in smaller chunks.  Up to 16 rows it has the chain's chunks and shares, and so its bits.
 Geometry geometry(int64_t B, int64_t H, int64_t heads, int64_t n_q, int64_t d, int64_t max_tokens, int accumulate, bool tree)
 {
     Geometry g;
     const int64_t R = H / heads * n_q, rows = B * H * n_q;
     g.ng = 0;
-    if (tree && R > wide_rows(d)) {
-        g.n_rc = static_cast<int>((R + 47) / 48);
-        g.ng = static_cast<int>(((R + g.n_rc - 1) / g.n_rc + 15) / 16);
-    }
     // 32 sequences of 8192, 4 key heads: a chunk of 16 rows takes 39 to 41 us among others, one of 32 74 (32 rows in one CTA 85, in
     // two of 16 89; 40 rows in two of 32 144, in three of 16 123; 1 key head: 80 rows 67 and 62, 96 rows 67 and 71, 176 even)
     g.rt = R <= 8 ? 1 : R <= 16 || (R + 15) / 16 * 7 < (R + 31) / 32 * 13 ? 2 : 4;
+    if (tree && R > 16) {
+        // Units (tiles, and kItemUnits an item) for each CTA that the SMs hold, in chunks of 8 and of 16 rows.
+        // Few: chunks of 8.  1 sequence of 700, 4 key heads, 64 rows, d = 64 (0.3 units): chunks of 8 11.1 us, of 16 12.2, the other
+        // kernel 19.3; 1 of 4000, 8 key heads, 48 rows, d = 128 (3.7) 23.0, 22.9, 27.6; 2 of 2000, 64 rows (5.3) 20.8, 18.6, 21.7.
+        // Many: the other kernel, whose first tile takes 15 us more and the others less.  8 key heads, 48 rows, d = 128, chunks
+        // of 16 and the other kernel: 4 sequences of up to 4000 (11 units) 21.7 and 30.3; 1 of 30000 (18.8) 46.7 and 42.8; 32 of up
+        // to 8192 (169) 160 and 111, 24 rows 101 and 93, 64 rows 186 and 165, 128 rows 350 and 261; d = 64, 48 rows 124
+        // and 108, 64 rows 140 and 141, 128 rows 268 and 249, but 24 rows (in one chunk of 32) 81 and 89, 32 rows 77 and 82.
+        const int64_t tiles = (max_tokens + tile_keys(static_cast<int>(d)) - 1) / tile_keys(static_cast<int>(d));
+        auto work = [&](int64_t rows, int64_t per_sm) { return B * heads * ((R + rows - 1) / rows) * (tiles + kItemUnits) / (kSms * per_sm); };
+        if (work(8, 3) < 2) {
+            g.rt = 1;
+        } else if (work(16, 2) < 14) {
+            g.rt = 2;
+        } else if (d == 128 || R > 32) {
+            g.n_rc = static_cast<int>((R + 47) / 48);
+            g.ng = static_cast<int>(((R + g.n_rc - 1) / g.n_rc + 15) / 16);
+        }
+    }
     if (g.ng == 0) g.n_rc = static_cast<int>((R + 8 * g.rt - 1) / (8 * g.rt));
     g.rows = g.ng > 0 ? 16 * g.ng : 8 * g.rt;
     const int64_t tk = g.ng > 0 ? 128 : tile_keys(static_cast<int>(d));
@@ -1130,7 +1142,7 @@ template <int D, bool SCORES, bool TREE>
 cudaError_t launch_rt(const DecodeArgs &a, int rt, int ctas, cudaStream_t s)
 {
     if (rt == 1) return launch<D, 1, SCORES, TREE>(a, ctas, s);
-    if constexpr (!TREE || wide_rows(D) > 16)
+    if constexpr (!TREE || D == 64)  // (d = 128: more than 16 rows of a tree go elsewhere)
         if (rt == 4) return launch<D, 4, SCORES, TREE>(a, ctas, s);
     return launch<D, 2, SCORES, TREE>(a, ctas, s);
 }
@@ -1149,8 +1161,7 @@ template <int D>
 cudaError_t launch_kind(const DecodeArgs &a, int rt, int ng, int ctas, cudaStream_t s)
 {
     if (ng > 0)
-        return ng == 1 ? launch_rows<D, 1>(a, ctas, s) : ng == 2 ? launch_rows<D, 2>(a, ctas, s)
-                       : launch_rows<D, 3>(a, ctas, s);
+        return ng == 2 ? launch_rows<D, 2>(a, ctas, s) : launch_rows<D, 3>(a, ctas, s);
     if (a.tree != nullptr) return launch_rt<D, false, true>(a, rt, ctas, s);
     return a.scores != nullptr ? launch_rt<D, true, false>(a, rt, ctas, s) : launch_rt<D, false, false>(a, rt, ctas, s);
 }

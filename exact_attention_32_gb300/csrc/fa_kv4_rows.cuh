@@ -339,7 +339,7 @@ fa_kv4_rows_kernel(const DecodeArgs a)
         auto sync = [&]() { group_sync(1 + wg); };
         auto both_sync = [&]() { asm volatile("barrier.cta.sync %0, 256;\n" ::"r"(5 + g) : "memory"); };  // both teams' warpgroups of these rows
         auto all_sync = [&]() { asm volatile("barrier.cta.sync 7, 512;\n" ::: "memory"); };
-        constexpr int V = NH <= 8 ? 8 : NH <= 16 ? 16 : 32;  // values that over_lanes joins
+        constexpr int V = NH <= 16 ? 16 : 32;  // values that over_lanes joins
         // O's columns of this group's rows, for the tile's keys 0-63 and 64-127 (d = 64)
         auto o_col = [&](int half, int r) -> uint32_t { return tmem + loff + C::kO + team * 128 + half * N + g * NH + r; };
         int n = 0;  // tiles of all segments before this one

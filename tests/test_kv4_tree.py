@@ -96,10 +96,21 @@ def test_python_calls_refuse_wrong_tensors():
 
 # ----------------------------------------------------------------------------------- tree (GPU)
 
+# The kernel for many rows a key head is taken where the table has room for many tokens, used or not.
+rooms = pytest.mark.parametrize("room", [0, 1 << 18])
+
+
+def table_of(pool, room):
+    table = np.full((pool.B, max(pool.table.shape[1], room // pool.P)), -7, np.int32)
+    table[:, :pool.table.shape[1]] = pool.table
+    return dev(table)
+
+
 @gpu
+@rooms
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("Hkv,G,n_q", [(1, 1, 1), (2, 4, 2), (3, 7, 3), (1, 1, 9), (2, 3, 16), (1, 12, 5), (2, 2, 64), (1, 16, 8)])
-def test_tree_over_short_and_odd_lengths(Hkv, G, n_q, d):
+def test_tree_over_short_and_odd_lengths(Hkv, G, n_q, d, room):
     # fewer tokens than drafts, drafts across tile and page borders, sequences that are all drafts, and counts of them
     lens = np.array([0, 1, 2, 15, 16, 17, 33, 63, 64, 65, 127, 129, 140, 255, 256, 257, 300, 321], np.int32)
     rng = np.random.default_rng(Hkv * 100 + G * 10 + n_q)
@@ -109,29 +120,31 @@ def test_tree_over_short_and_odd_lengths(Hkv, G, n_q, d):
     c = pool.cache()
     counts = rng.integers(-1, n_q + 2, len(lens)).astype(np.int32)
     for n_new in (None, counts):
-        o, lse = fa.forward_kv4_tree(q, c, dev(lens), dev(pool.table), dev(masks), n_new=None if n_new is None else dev(n_new))
+        o, lse = fa.forward_kv4_tree(q, c, dev(lens), table_of(pool, room), dev(masks), n_new=None if n_new is None else dev(n_new))
         ok()
         check_tree(pool, q, lens, fa.default_scale(d), masks, n_new, o, lse)
 
 
 @gpu
+@rooms
 @pytest.mark.parametrize("d,P,Hkv,G,n_q", [(128, 64, 2, 4, 12), (64, 32, 1, 8, 4), (128, 1024, 1, 1, 3), (128, 16, 1, 2, 64), (64, 128, 2, 5, 13)])
-def test_tree_over_long_ragged_lengths(d, P, Hkv, G, n_q):
+def test_tree_over_long_ragged_lengths(d, P, Hkv, G, n_q, room):
     lens = np.array([9000, 4097, 70, 700, 8192], np.int32)
     rng = np.random.default_rng(d + P)
     pool = Pool(5, Hkv, d, P, lens, seed=d + P)
     q = bf16(3 * rng.standard_normal((5, Hkv * G, n_q, d))).cuda()
     _, masks = random_tree(rng, 5, n_q)
     n_new = np.array([n_q, 1, n_q, 0, max(1, n_q - 2)], np.int32)
-    o, lse = fa.forward_kv4_tree(q, pool.cache(), dev(lens), dev(pool.table), dev(masks), n_new=dev(n_new), scale=0.11)
+    o, lse = fa.forward_kv4_tree(q, pool.cache(), dev(lens), table_of(pool, room), dev(masks), n_new=dev(n_new), scale=0.11)
     ok()
     check_tree(pool, q, lens, float(np.float32(0.11)), masks, n_new, o, lse)
 
 
 @gpu
+@rooms
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("G,n_q", [(2, 5), (5, 8), (4, 16)])
-def test_rows_of_very_different_size(d, G, n_q):
+def test_rows_of_very_different_size(d, G, n_q, room):
     # the bounds are each row's own: what is rounded under the largest value of other rows would pass them
     lens = np.array([200, 700], np.int32)
     rng = np.random.default_rng(d + n_q)
@@ -139,23 +152,24 @@ def test_rows_of_very_different_size(d, G, n_q):
     q = bf16(rng.standard_normal((2, 2 * G, n_q, d)) * 2.0 ** rng.integers(-30, 4, (2, 2 * G, n_q, 1))).cuda()
     _, masks = random_tree(rng, 2, n_q)
     for gain in (1.0, 2.0 ** 24):
-        o, lse = fa.forward_kv4_tree(q * gain, pool.cache(), dev(lens), dev(pool.table), dev(masks), scale=float(0.125 / gain))
+        o, lse = fa.forward_kv4_tree(q * gain, pool.cache(), dev(lens), table_of(pool, room), dev(masks), scale=float(0.125 / gain))
         ok()
         check_tree(pool, q * gain, lens, 0.125 / gain, masks, None, o, lse)
 
 
 @gpu
+@rooms
 @pytest.mark.parametrize("d,G,n_q", [(64, 4, 3), (128, 8, 1), (128, 2, 16), (64, 3, 7)])
-def test_a_chain_gives_the_causal_call(d, G, n_q):
-    # bit for bit up to 16 rows a key head; above that another kernel's sums, within the same bounds
+def test_a_chain_gives_the_causal_call(d, G, n_q, room):
+    # bit for bit up to 16 rows a key head; above that in other chunks or another kernel's sums, within the same bounds
     lens = np.array([n_q, 500, 2000, 129, n_q + 1], np.int32)
     rng = np.random.default_rng(n_q)
     pool = Pool(5, 2, d, 32, lens, seed=n_q)
     q = bf16(rng.standard_normal((5, 2 * G, n_q, d))).cuda()
     chain = dev(np.tile(np.array([(2 << t) - 1 for t in range(n_q)], np.int64), (5, 1)))
     c = pool.cache()
-    a = fa.forward_kv4(q, c, dev(lens), dev(pool.table))
-    b = fa.forward_kv4_tree(q, c, dev(lens), dev(pool.table), chain)
+    a = fa.forward_kv4(q, c, dev(lens), table_of(pool, room))
+    b = fa.forward_kv4_tree(q, c, dev(lens), table_of(pool, room), chain)
     ok()
     if G * n_q <= 16:
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
@@ -164,8 +178,10 @@ def test_a_chain_gives_the_causal_call(d, G, n_q):
 
 
 @gpu
+@rooms
 @pytest.mark.parametrize("d", [64, 128])
-def test_masks_are_taken_as_they_are(d):
+@pytest.mark.parametrize("G", [2, 8])
+def test_masks_are_taken_as_they_are(d, G, room):
     # none, all, only others, bits behind the drafts; a stored NaN among the drafts reaches the rows that admit it
     n_q, lens = 6, np.array([6, 40, 300], np.int32)
     pool = Pool(3, 1, d, 16, lens, seed=3)
@@ -173,8 +189,8 @@ def test_masks_are_taken_as_they_are(d):
         j = lens[b] - 2  # draft 4
         pool.ks[pool.table[b, j // 16], :, j % 16] = 255
     masks = np.tile(np.array([0, 0x2F, 0x2, -1 ^ 0x10, 0x3F, (1 << 63) - 1 - 0x10], np.int64), (3, 1))
-    q = bf16(np.random.default_rng(4).standard_normal((3, 2, n_q, d))).cuda()
-    o, lse = fa.forward_kv4_tree(q, pool.cache(), dev(lens), dev(pool.table), dev(masks))
+    q = bf16(np.random.default_rng(4).standard_normal((3, G, n_q, d))).cuda()
+    o, lse = fa.forward_kv4_tree(q, pool.cache(), dev(lens), table_of(pool, room), dev(masks))
     ok()
     assert torch.isnan(lse[:, :, 4]).all() and (lse[0, :, 0] == -np.inf).all() and (o[0, :, 0] == 0).all()
     rest = [0, 1, 2, 3, 5]
@@ -208,18 +224,20 @@ def test_tree_refuses_wrong_gpu_tensors():
 
 
 @gpu
-def test_tree_leaves_bad_pages_out_and_reports_them():
+@rooms
+@pytest.mark.parametrize("G", [2, 8])
+def test_tree_leaves_bad_pages_out_and_reports_them(G, room):
     lens = np.array([100, 60], np.int32)
     pool = Pool(2, 1, 64, 16, lens, seed=6)
-    q = bf16(np.random.default_rng(7).standard_normal((2, 2, 4, 64))).cuda()
+    q = bf16(np.random.default_rng(7).standard_normal((2, G, 4, 64))).cuda()
     _, masks = random_tree(np.random.default_rng(8), 2, 4)
-    table = pool.table.copy()
+    table = table_of(pool, room)
     table[0, 6] = pool.n_pages  # holds tokens 96 .. 99: all four drafts
-    o, lse = fa.forward_kv4_tree(q, pool.cache(), dev(lens), dev(table), dev(masks))
+    o, lse = fa.forward_kv4_tree(q, pool.cache(), dev(lens), table, dev(masks))
     torch.cuda.synchronize()
     assert fa.fa_get_device_status(0) == 8
     k, v = pool.kv(0, 96)
-    r = ref.tree_attention(np.concatenate([f64(q)[0], np.zeros((2, 0, 64))], 1), np.concatenate([k, k[:, :4]], 1),
+    r = ref.tree_attention(f64(q)[0], np.concatenate([k, k[:, :4]], 1),
                            np.concatenate([v, v[:, :4]], 1), fa.default_scale(64), 100, [0] * 4, None)
     assert np.abs(f64(lse)[0] - r["lse"]).max() <= 1e-4
     ok()
