@@ -124,6 +124,8 @@ __device__ __forceinline__ void zero_tail_rows(uint8_t *tile, int n, int lane, i
 // A kernel behind another whose results it needs: launched before that one has ended, so that its launch and what it does
 // first overlap it, it waits for the end itself.  (The plan is not among those results: it is older.)
 __device__ __forceinline__ void wait_for_the_one_before() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+// In the kernel before: once all its CTAs have come here (or ended), the next one's may take what room there is.
+__device__ __forceinline__ void let_the_next_one_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 
 template <typename... P, typename... A>
 cudaError_t launch_behind(void (*kern)(P...), unsigned grid, int threads, int smem, cudaStream_t s, const A &...args)

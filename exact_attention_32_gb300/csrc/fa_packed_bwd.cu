@@ -107,13 +107,17 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     const uint32_t sb = smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // The grid has a CTA for every block that the lengths could make; those past the list end here, and all do for a plan
-    // of another batch (which the pre kernel reports).
-    if (!plan_fits(a.plan.head, a.T, a.B, CAUSAL)) return;
-    const int n_blocks = a.plan.head->n_blocks;
+    // of another batch (which the pre kernel reports); not before the pre kernel, which the post kernel does not wait for.
+    // (The post kernel is not let in early from here: its blocks, waiting beside the last CTAs, took 1017 us in place of 988.)
+    const bool fits = plan_fits(a.plan.head, a.T, a.B, CAUSAL);
+    const int n_blocks = fits ? a.plan.head->n_blocks : 0;
     // The key heads go in groups, so that the CTAs resident at one time share a few heads' Q, dO and dQ blocks in L2; inside
     // a group the list's order, the longest loops first.
     const int64_t per_group = static_cast<int64_t>(a.heads_per_group) * n_blocks;
-    if (blockIdx.x >= static_cast<int64_t>(a.kv_heads) * n_blocks) return;
+    if (blockIdx.x >= static_cast<int64_t>(a.kv_heads) * n_blocks) {
+        wait_for_the_one_before();
+        return;
+    }
     if ((sb & 1023u) != 0) {  // the swizzled tiles need a 1024-byte-aligned base
         if (tid == 0) packed_timeout();
         return;
@@ -489,6 +493,7 @@ __global__ void __launch_bounds__(256)
 fa_packed_pre_kernel(const BwdArgs a, int causal)
 {
     constexpr int TPR = D / 8;  // threads a row, 8 channels each
+    let_the_next_one_start();
     if (!plan_fits(a.plan.head, a.T, a.B, causal)) {
         if (blockIdx.x == 0 && threadIdx.x == 0) packed_bad_sequence();
         return;
@@ -533,9 +538,10 @@ template <int D>
 __global__ void __launch_bounds__(256)
 fa_packed_post_kernel(const BwdArgs a, int causal)
 {
-    if (!plan_fits(a.plan.head, a.T, a.B, causal)) return;
-    const int64_t n = static_cast<int64_t>(a.plan.head->n_blocks) * a.heads;
+    const bool fits = plan_fits(a.plan.head, a.T, a.B, causal);
     wait_for_the_one_before();
+    if (!fits) return;
+    const int64_t n = static_cast<int64_t>(a.plan.head->n_blocks) * a.heads;
     for (int64_t it = blockIdx.x; it < n; it += gridDim.x) {
         const int4 e = a.plan.blocks[it / a.heads];
         const int h = static_cast<int>(it % a.heads);
