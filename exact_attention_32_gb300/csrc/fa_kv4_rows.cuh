@@ -6,26 +6,32 @@
 //   S^T = K Q^T      K as halves, code times scale (exact: at most 6 significant bits), Q as halves under a power of two of its
 //                    row (bf16's 8 bits: exact down to 2^-24 of the row's largest value, off by at most 2^-32 of that
 //                    below); one value a score, summed in fp32
-//   O^T += V^T P^T   V's codes as halves, P times V's scale as one half, under a power of two of its row that keeps the
-//                    largest so far between 2^8 and 2^15 (as the decode kernel's, before it is cut in parts)
+//   O^T += V^T P^T   V's codes as halves, P times V's scale as one half.  A row has one reference r, a whole number that
+//                    stands in for its maximum (log2): p = 2^(x - r) in fp32 goes into the sum, p times the key's V scale into the
+//                    product.  r keeps the largest such product so far between 2^8 and 2^15 (of a half's 2^-24 to
+//                    2^16), and every p below 2^60 (of V rows that are all zeros).
 // d = 64: V's rows of keys 0-63 and 64-127 of a tile lie side by side, so that the product has 128 rows; P's columns of
 // the second half of the keys lie behind those of the first, and O is the sum of the two diagonal blocks.
 //
 // A tile is 128 keys; a CTA an SM.  A softmax warpgroup takes half of the rows, one thread a key.  Its steps hang on one
-// another (scores, whether a row's maximum grows, P), so two teams of two warpgroups take turns by tile, each with a
-// maximum, a sum and an O of its own, joined at the end of a segment: with one team a tile of 48 rows took 3430 cycles, of which
-// the warps issued in 40 %.
+// another (scores, whether a row's reference grows, P), so two teams of two warpgroups take turns by tile, each with a
+// reference, a sum and an O of its own, joined at the end of a segment: with one team a tile of 48 rows took 3430 cycles, of which
+// the warps issued in 40 %, with two 2000 (60 %).  32 sequences of up to 8192, 8 key heads, 48 rows: 98 us, 1.5 TB/s of cache
+// (22 us would be the bytes): the chain load, decode, S, P, O through pairs of buffers bounds it, no unit alone (without
+// the conversions, the decoded tiles' stores or the exponentials a tile would take 3 % less).
 // Roles (896 threads): warps 0-7 and 8-15 the teams; 16-19 decode K and 20-23 V; 24 loads K's codes and scales, 25 V's; 26 issues S's
 // products and 27 O's (from one warp, in one order, each would wait for what the other waits for: 4000 cycles a tile).
-// Launched with 72 registers a thread, of which the last twelve warps give some to the softmax.
+// Launched with 72 registers a thread, of which the last twelve warps give some to the softmax (80 and 56 in place of 88 and 48: 1
+// to 2 % slower; 72 and 72: 12 %).
 
 constexpr int kRowsLaunchRegs = 72, kRowsSoftmaxRegs = 88, kRowsOtherRegs = 48;
-// A row's reference is set this far (log2) above the largest score: with the decode kernel's 3 one of 24 rows grew in every
-// sixth tile, at 5000 cycles each time.  Terms of 2^-21 of the largest are then still normal halves.
-constexpr float kRowsHeadroom = 6.f;
-// What starting and ending an item costs, in tiles.  48 rows, 32 sequences of up to 8192: 6 126 us, 9 112, 12 111, 16 117; 32 rows
-// 96, 98, 103, 103; 128 rows 300, 261, 266, 270.
-constexpr int kRowsItemUnits = 9;
+// A row's reference is set this far (log2) above what the largest term needs: with the decode kernel's 3 one of 24 rows grew in
+// every sixth tile, at 5000 cycles each time.
+constexpr float kRowsHeadroom = 6.f, kRowsTopLog2 = 15.f, kRowsSumLog2 = 60.f;
+constexpr float kRowsNone = 1e30f;  // minus the reference of a row that has met no key
+// What starting and ending an item costs, in tiles.  48 rows, 32 sequences of up to 8192: 6 134 us, 9 113, 13 104; 32 rows 100, 96,
+// 100; 128 rows 296, 266, 246.
+constexpr int kRowsItemUnits = 12;
 static_assert(4 * kRowsSoftmaxRegs + 3 * kRowsOtherRegs <= 7 * kRowsLaunchRegs, "the warpgroups' shares are what the block has");
 
 template <int D, int NG>
@@ -43,12 +49,12 @@ struct RowCfg {
     static constexpr int kStages = 2, kSmallStages = 4;
     static constexpr int kCodes = TK * D / 2, kRawKBytes = kCodes + TK * (D / 32), kSmallBytes = TK + 32;
     static constexpr int kRawK = kP + 2 * kPBytes, kRawV = kRawK + kStages * kRawKBytes, kSmall = kRawV + kStages * kCodes;
-    // a softmax warpgroup's, per pair of rows: {m, m', t, t'} (t: the largest term so far over the maximum, log2), {f, f'},
-    // {alpha, alpha'}, {o_alpha, o_alpha'}; the rows' masks; a failed wait
+    // a softmax warpgroup's, per pair of rows: {mult, mult', -r, -r'}, {mult, mult', 0, 0}, {alpha, alpha'}; the rows' masks; a
+    // failed wait
     static constexpr int kState = kSmall + kSmallStages * kSmallBytes;
-    static constexpr int kSeen = 16 * (16 + 8 + 8 + 8), kFail = kSeen + 8 * 32, kStateBytes = kFail + 16;
-    static constexpr int kRed = kState + 4 * kStateBytes;  // its reductions over warps: float2 [4][32]
-    static constexpr int kMult = kRed + 4 * 1024;          // of all rows
+    static constexpr int kSeen = 16 * (16 + 16 + 8), kFail = kSeen + 8 * 32, kStateBytes = kFail + 16;
+    static constexpr int kRed = kState + 4 * kStateBytes;  // its reductions over warps: float [4][32]
+    static constexpr int kMult = kRed + 4 * 512;           // of all rows
     static constexpr int kWalk = kMult + 4 * 48;
     static constexpr int kBar = kWalk + 64 + 8 * (kThreads / 32);
     static constexpr int kNumBars = 19 + 4 * kStages + 2 * kSmallStages;
@@ -330,11 +336,11 @@ fa_kv4_rows_kernel(const DecodeArgs a)
         const int wg = warp >> 2, team = wg >> 1, g = wg & 1, wl = warp & 3, tl = tid & 127;  // tl: TMEM lane, the tile's key
         const uint32_t loff = static_cast<uint32_t>(wl * 32) << 16;
         uint8_t *const state = smem + C::kState + wg * C::kStateBytes;
-        float4 *sm_mt = reinterpret_cast<float4 *>(state);                         // [row pair] {m, m', t, t'}
-        float2 *sm_f = reinterpret_cast<float2 *>(state + 16 * 16), *sm_alpha = sm_f + 16, *sm_oalpha = sm_alpha + 16;
+        float4 *sm_ref = reinterpret_cast<float4 *>(state), *sm_raw = sm_ref + 16;  // [row pair]
+        float2 *sm_alpha = reinterpret_cast<float2 *>(state + 32 * 16);
         volatile float *sm_fail = reinterpret_cast<volatile float *>(state + C::kFail);  // a wait gave up: the group leaves together
         uint64_t *sm_seen = reinterpret_cast<uint64_t *>(state + C::kSeen);
-        float2 *sm_red = reinterpret_cast<float2 *>(smem + C::kRed + wg * 1024);  // [warp][row]
+        float *sm_red = reinterpret_cast<float *>(smem + C::kRed + wg * 512);  // [warp][row]
         float *sm_mult = reinterpret_cast<float *>(smem + C::kMult);              // [row]: a product of its halves times this is the score
         auto sync = [&]() { group_sync(1 + wg); };
         auto both_sync = [&]() { asm volatile("barrier.cta.sync %0, 256;\n" ::"r"(5 + g) : "memory"); };  // both teams' warpgroups of these rows
@@ -389,13 +395,15 @@ fa_kv4_rows_kernel(const DecodeArgs a)
                         make_uint4(y[0], y[1], y[2], y[3]);
             }
             if (tl < NH) sm_seen[tl] = a.tree[static_cast<int64_t>(w.b) * a.n_q + (row0 + tl) % a.n_q];
-            if (tl < NH / 2) {
-                sm_mt[tl] = make_float4(-FLT_MAX, -FLT_MAX, 0.f, 0.f);
-                sm_f[tl] = make_float2(1.f, 1.f);
-            }
             fence_proxy_async_smem();
             all_sync();
             if (lane == 0) mbar_arrive(BAR(R_Q_READY));
+            if (tl < NH / 2) {
+                const float2 mult = *reinterpret_cast<const float2 *>(sm_mult + g * NH + 2 * tl);
+                sm_ref[tl] = make_float4(mult.x, mult.y, kRowsNone, kRowsNone);
+                sm_raw[tl] = make_float4(mult.x, mult.y, 0.f, 0.f);
+            }
+            sync();
             float2 l[NG][4];
 #pragma unroll
             for (int q = 0; q < NG; ++q)
@@ -410,103 +418,77 @@ fa_kv4_rows_kernel(const DecodeArgs a)
                 ok = wait_both(BAR(X_FULL + xs), (nn / XS) & 1, BAR(R_S_FULL + team), phase);
                 if (!ok) *sm_fail = 1.f;
                 tc_fence_after();
-                // log2 scores of this thread's key
+                float vs = kv4_scale(small[tl]);
+                const bool here = reinterpret_cast<const int *>(small + TK)[tl >> 4] != 0;
+                // keys that a row does not admit, or that no page holds, leave it; what lies there may be anything
+                const bool edge = (w.t0 + i) * TK + TK > w.len - newest || __any_sync(0xffffffffu, !here);
+                const bool gone = key >= w.len || !here;
+                if (gone) vs = 0.f;
+                const float limit = fminf(kRowsTopLog2 - lg2(vs), kRowsSumLog2);  // x - r of this key stays below
+                // this key's log2 scores less the rows' references; anew where a row's grows (always in its first tile, soon
+                // seldom): first the scores themselves, then against what the references have become
                 float2 x[NG][4];
-                float vs;
-                bool here;
-                {
+                const float4 *from = i == mine0 ? sm_raw : sm_ref;
+                for (bool grown = false;;) {
                     uint32_t s[NG][8];
 #pragma unroll
                     for (int q = 0; q < NG; ++q) tmem_ld8(tmem + loff + team * 64 + g * NH + q * 8, s[q]);
-                    vs = kv4_scale(small[tl]);
-                    here = reinterpret_cast<const int *>(small + TK)[tl >> 4] != 0;
                     tmem_wait_ld();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(BAR(R_S_FREE + team));
-                        mbar_arrive(BAR(X_FREE + xs));
-                    }
 #pragma unroll
                     for (int q = 0; q < NG; ++q)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            x[q][j] = mul2(make_float2(__uint_as_float(s[q][2 * j]), __uint_as_float(s[q][2 * j + 1])),
-                                           *reinterpret_cast<const float2 *>(sm_mult + g * NH + q * 8 + 2 * j));
-                }
-                // keys that a row does not admit, or that no page holds, leave it; what lies there may be anything
-                const bool edge = (w.t0 + i) * TK + TK > w.len - newest || __any_sync(0xffffffffu, !here);
-                if (edge) {
-                    const bool gone = key >= w.len || !here;
-                    const int draft = key - (w.len - newest), bit = draft & 63;
-                    if (gone) vs = 0.f;
-                    const uint32_t *seen = reinterpret_cast<const uint32_t *>(sm_seen) + (bit >> 5);
-#pragma unroll
-                    for (int q = 0; q < NG; ++q)
-#pragma unroll
-                        for (int r = 0; r < 8; ++r)
-                            if (gone || (draft >= 0 && ((seen[2 * (q * 8 + r)] >> (bit & 31)) & 1u) == 0))
-                                (r & 1 ? x[q][r / 2].y : x[q][r / 2].x) = -INFINITY;
-                }
-                // does a key pass its row's maximum, or its term the row's largest?  Soon that is rare.  (d: over the maximum)
-                const float lv = lg2(vs);
-                float over = -INFINITY;
-#pragma unroll
-                for (int q = 0; q < NG; ++q)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float4 mt = sm_mt[q * 4 + j];
-                        const float2 d = add2(x[q][j], make_float2(-mt.x, -mt.y)), z = add2(d, make_float2(lv - mt.z, lv - mt.w));
-                        over = fmaxf(fmax3(over, d.x, d.y), fmaxf(z.x, z.y));
-                    }
-                const bool grows = group_or(1 + wg, over > 0.f);
-                if (*sm_fail != 0.f) {
-                    ok = false;
-                    break;
-                }
-                // the product of the team's tile before has read P (and its O is complete so far)
-                if (nn > 1 && !mbar_wait_warp(BAR(R_PV_DONE + team), phase ^ 1, kWaitLimitNs)) *sm_fail = 1.f;
-                if (grows) {
-                    auto largest = [&](float add) {  // of the warp's keys, row `lane`
-                        float v[V];
-#pragma unroll
-                        for (int r = 0; r < V; ++r) {
-                            const float xr = r < NH ? (r & 1 ? x[r / 8][r / 2 % 4].y : x[r / 8][r / 2 % 4].x) : 0.f;
-                            v[r] = fmaxf(xr + add, -FLT_MAX);
+                        for (int j = 0; j < 4; ++j) {
+                            const float4 c = from[q * 4 + j];
+                            x[q][j] = fma2(make_float2(__uint_as_float(s[q][2 * j]), __uint_as_float(s[q][2 * j + 1])), make_float2(c.x, c.y),
+                                           make_float2(c.z, c.w));
                         }
-                        return over_lanes<V>(v, [](float p, float q) { return fmaxf(p, q); });
-                    };
-                    const float vm = largest(0.f), zm = largest(lv);
-                    if (lane < NH) sm_red[wl * 32 + lane] = make_float2(vm, zm);
+                    if (edge) {
+                        const int draft = key - (w.len - newest), bit = draft & 63;
+                        const uint32_t *seen = reinterpret_cast<const uint32_t *>(sm_seen) + (bit >> 5);
+#pragma unroll
+                        for (int q = 0; q < NG; ++q)
+#pragma unroll
+                            for (int r = 0; r < 8; ++r)
+                                if (gone || (draft >= 0 && ((seen[2 * (q * 8 + r)] >> (bit & 31)) & 1u) == 0))
+                                    (r & 1 ? x[q][r / 2].y : x[q][r / 2].x) = -INFINITY;
+                    }
+                    if (grown) break;
+                    if (from == sm_ref) {
+                        float top = -INFINITY;
+#pragma unroll
+                        for (int q = 0; q < NG; ++q)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) top = fmax3(top, x[q][j].x, x[q][j].y);
+                        const bool grows = group_or(1 + wg, top > limit);
+                        if (*sm_fail != 0.f) ok = false;
+                        if (!grows || !ok) break;
+                        from = sm_raw;
+                        continue;
+                    }
+                    // of the warp's keys, what row `lane`'s reference has to be at least
+                    float v[V];
+#pragma unroll
+                    for (int r = 0; r < V; ++r) {
+                        const float xr = r < NH ? (r & 1 ? x[r / 8][r / 2 % 4].y : x[r / 8][r / 2 % 4].x) : 0.f;
+                        v[r] = fmaxf(xr - limit, -FLT_MAX);
+                    }
+                    const float need = over_lanes<V>(v, [](float p, float q) { return fmaxf(p, q); });
+                    if (lane < NH) sm_red[wl * 32 + lane] = need;
+                    sync();
+                    if (tl < NH) {
+                        const float most = fmaxf(fmaxf(sm_red[tl], sm_red[32 + tl]), fmaxf(sm_red[64 + tl], sm_red[96 + tl]));
+                        float *minus_r = reinterpret_cast<float *>(sm_ref + (tl >> 1)) + 2 + (tl & 1);
+                        const float old = -*minus_r, r = most > old ? ceilf(most + kRowsHeadroom) : old;
+                        reinterpret_cast<float *>(sm_alpha)[tl] = ex2(old - r);
+                        *minus_r = -r;
+                    }
+                    // O is complete so far
+                    if (i > mine0 && !mbar_wait_warp(BAR(R_PV_DONE + team), phase ^ 1, kWaitLimitNs)) *sm_fail = 1.f;
                     sync();
                     if (*sm_fail != 0.f) {
                         ok = false;
                         break;
                     }
-                    if (tl < NH) {
-                        float v = -FLT_MAX, z = -FLT_MAX;
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const float2 y = sm_red[c * 32 + tl];
-                            v = fmaxf(v, y.x);
-                            z = fmaxf(z, y.y);
-                        }
-                        float *mt = reinterpret_cast<float *>(sm_mt + (tl >> 1)) + (tl & 1);
-                        float *f = reinterpret_cast<float *>(sm_f) + tl;
-                        const float old = mt[0], top = old == -FLT_MAX ? -FLT_MAX : old + mt[2];
-                        v = v > old ? v + kRowsHeadroom : old;
-                        z = z > top ? z + kRowsHeadroom : top;
-                        const float alpha = ex2(old - v);
-                        // the power of two that keeps the terms up to 2^15; held at 2^100 where p itself is next to nothing
-                        const int ef = min(max(__float2int_rd((v - z) + 15.f), -100), 100);
-                        const float now = __uint_as_float(static_cast<uint32_t>(ef + 127) << 23);
-                        reinterpret_cast<float *>(sm_alpha)[tl] = alpha;
-                        reinterpret_cast<float *>(sm_oalpha)[tl] = alpha * (now * inverse_pow2(*f));
-                        mt[0] = v;
-                        mt[2] = fmaxf(z - v, -FLT_MAX);
-                        *f = now;
-                    }
-                    sync();
 #pragma unroll
                     for (int q = 0; q < NG; ++q)
 #pragma unroll
@@ -522,7 +504,7 @@ fa_kv4_rows_kernel(const DecodeArgs a)
                                 tmem_wait_ld();
 #pragma unroll
                                 for (int j = 0; j < 8; j += 2) {
-                                    const float2 y = mul2(make_float2(__uint_as_float(o[j]), __uint_as_float(o[j + 1])), sm_oalpha[q * 4 + j / 2]);
+                                    const float2 y = mul2(make_float2(__uint_as_float(o[j]), __uint_as_float(o[j + 1])), sm_alpha[q * 4 + j / 2]);
                                     o[j] = __float_as_uint(y.x);
                                     o[j + 1] = __float_as_uint(y.y);
                                 }
@@ -530,27 +512,38 @@ fa_kv4_rows_kernel(const DecodeArgs a)
                             }
                         tmem_wait_st();
                     }
+                    grown = true;
+                    from = sm_ref;
                 }
-                // P: the sum in fp32; the product's operand times V's scale and the row's factor
+                if (!ok) break;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(BAR(R_S_FREE + team));
+                    mbar_arrive(BAR(X_FREE + xs));
+                }
+                // P: the sum in fp32, the product's operand times V's scale
                 uint32_t y[NG][4];
 #pragma unroll
                 for (int q = 0; q < NG; ++q)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float4 mt = sm_mt[q * 4 + j];
-                        const float2 d = add2(x[q][j], make_float2(-mt.x, -mt.y));
-                        const float2 p = make_float2(ex2(d.x), ex2(d.y));
+                        const float2 p = make_float2(ex2(x[q][j].x), ex2(x[q][j].y)), pv = mul2(p, make_float2(vs, vs));
                         l[q][j] = add2(l[q][j], p);
-                        float2 pv = mul2(p, mul2(sm_f[q * 4 + j], make_float2(vs, vs)));
-                        if (edge) {  // a value that a row does not admit stays out of it, a NaN too
-                            if (x[q][j].x == -INFINITY) pv.x = 0.f;
-                            if (x[q][j].y == -INFINITY) pv.y = 0.f;
-                        }
                         const __half2 z = __floats2half2_rn(pv.x, pv.y);
                         y[q][j] = *reinterpret_cast<const uint32_t *>(&z);
                     }
+                if (edge) {  // a value that a row does not admit stays out of it, a NaN too
 #pragma unroll
-                for (int q = 0; q < NG; ++q) {  // (behind the loads above: a store in between would hold them back)
+                    for (int q = 0; q < NG; ++q)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            y[q][j] &= (x[q][j].x == -INFINITY ? 0u : 0xFFFFu) | (x[q][j].y == -INFINITY ? 0u : 0xFFFF0000u);
+                }
+                // the product of the team's tile before has read P
+                if (nn > 1 && !mbar_wait_warp(BAR(R_PV_DONE + team), phase ^ 1, kWaitLimitNs)) *sm_fail = 1.f;
+#pragma unroll
+                for (int q = 0; q < NG; ++q) {
                     const int col = (D == 128 ? 0 : (tl >> 6) * N) + g * NH + q * 8, k = D == 128 ? tl : tl & 63;
                     *reinterpret_cast<uint4 *>(smem + C::kP + team * C::kPBytes + (col >> 6) * 8192 + k * 128 + ((((col & 63) >> 3) ^ (k & 7)) << 4)) =
                         make_uint4(y[q][0], y[q][1], y[q][2], y[q][3]);
@@ -572,7 +565,7 @@ fa_kv4_rows_kernel(const DecodeArgs a)
 #pragma unroll
                 for (int r = 0; r < V; ++r) v[r] = r < NH ? (r & 1 ? l[r / 8][r / 2 % 4].y : l[r / 8][r / 2 % 4].x) : 0.f;
                 const float sum = over_lanes<V>(v, [](float p, float q) { return p + q; });
-                if (lane < NH) sm_red[wl * 32 + lane].x = sum;
+                if (lane < NH) sm_red[wl * 32 + lane] = sum;
             }
             all_sync();
             bool failed = false;  // (all leave where one has to: they meet again at the barriers below)
@@ -582,20 +575,20 @@ fa_kv4_rows_kernel(const DecodeArgs a)
                 ok = false;
                 break;
             }
-            // A thread a row: what this team's O is multiplied with (the row's factor taken out, under the larger of the teams'
-            // maxima, and over the sum if the segment is the whole item), 0 where nothing is to come of it
+            // A thread a row: what this team's O is multiplied with (to be under the larger of the teams' references, and over
+            // the sum if the segment is the whole item), 0 where nothing is to come of it
             const bool whole = w.t0 == 0 && w.t1 == w.n_t;
             const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (n == 0 ? 0 : 1);
             float *sm_factor = reinterpret_cast<float *>(sm_alpha);
             if (tl < NH) {
                 const float *state_other = reinterpret_cast<const float *>(smem + C::kState + (wg ^ 2) * C::kStateBytes);
-                const float2 *red_other = reinterpret_cast<const float2 *>(smem + C::kRed + (wg ^ 2) * 1024);
-                const int at = (tl >> 1) * 4 + (tl & 1);
-                const float own = reinterpret_cast<const float *>(sm_mt)[at], other = state_other[at], m = fmaxf(own, other);
+                const float *red_other = reinterpret_cast<const float *>(smem + C::kRed + (wg ^ 2) * 512);
+                const int at = (tl >> 1) * 4 + 2 + (tl & 1);
+                const float own = -reinterpret_cast<const float *>(sm_ref)[at], other = -state_other[at], m = fmaxf(own, other);
                 const float own_f = ex2(own - m);
-                float ll = ((sm_red[tl].x + sm_red[32 + tl].x) + (sm_red[64 + tl].x + sm_red[96 + tl].x)) * own_f +
-                           ((red_other[tl].x + red_other[32 + tl].x) + (red_other[64 + tl].x + red_other[96 + tl].x)) * ex2(other - m);
-                float factor = any ? own_f * inverse_pow2(reinterpret_cast<const float *>(sm_f)[tl]) : 0.f;
+                float ll = ((sm_red[tl] + sm_red[32 + tl]) + (sm_red[64 + tl] + sm_red[96 + tl])) * own_f +
+                           ((red_other[tl] + red_other[32 + tl]) + (red_other[64 + tl] + red_other[96 + tl])) * ex2(other - m);
+                float factor = any ? own_f : 0.f;
                 if ((row0 + tl) % a.n_q >= newest) factor = ll = 0.f;  // no draft of this sequence
                 if (whole) factor *= ll == 0.f ? 0.f : 1.f / ll;
                 sm_factor[tl] = factor;
