@@ -128,18 +128,21 @@ __device__ __forceinline__ void wait_for_the_one_before() { asm volatile("gridde
 __device__ __forceinline__ void let_the_next_one_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 
 template <typename... P, typename... A>
-cudaError_t launch_behind(void (*kern)(P...), unsigned grid, int threads, int smem, cudaStream_t s, const A &...args)
+cudaError_t launch_behind(void (*kern)(P...), unsigned grid, int threads, int smem, cudaStream_t s, unsigned cluster, const A &...args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(static_cast<unsigned>(threads));
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = s;
-    cudaLaunchAttribute attr = {};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute attrs[2] = {};
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = cluster;
+    attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
+    cfg.attrs = attrs;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 

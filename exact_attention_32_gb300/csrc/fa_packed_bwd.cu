@@ -10,7 +10,8 @@
 //   main  a CTA per 128 keys of one key head of one sequence, the longest loops first (the plan's list), over the 128-row
 //         query blocks (causal: from the diagonal) of each of the key head's query heads in turn: dK and dV, which
 //         sum over those heads, stay in tensor memory through all of it; each block's part of dQ is added to
-//         the accumulator in L2
+//         the accumulator in L2.  Where that leaves SMs idle, a cluster of CTAs shares the loop (ranks_of) and adds its dK and dV
+//         through distributed shared memory in the ranks' order.
 //   post  dQ = bf16(scale accumulator); zeros in rows of no sequence where they are asked for
 // Per query block i (S^T etc. are key-major: TMEM lane = key):
 //   S^T  = K Q^T      SS product -> TMEM A
@@ -39,6 +40,8 @@
 // warp 14 zeroes tails.
 // Every mbarrier wait is bounded; a wait that gives up sets FA_ERR_TIMEOUT and the CTA winds down.
 #include <math.h>
+
+#include <type_traits>
 
 #include "fa_packed.cuh"
 
@@ -88,8 +91,24 @@ struct BwdArgs {
     int T, B, heads, kv_heads, group, fill;
     int nb;                         // blocks that the padded arrays have room for
     int heads_per_group;            // see the order of the CTAs
+    int ranks;                      // CTAs (a cluster) that share a key block
     float scale, scale_log2;
 };
+
+// Four floats at an address of this CTA's shared memory in the cluster's CTA `rank`; the cluster's barrier.
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr, uint32_t rank)
+{
+    float4 x;
+    asm volatile("{\n.reg .b32 a;\nmapa.shared::cluster.u32 a, %4, %5;\nld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n}\n"
+                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                 : "r"(addr), "r"(rank)
+                 : "memory");
+    return x;
+}
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
 
 __device__ __forceinline__ uint32_t lo32(uint64_t x) { return static_cast<uint32_t>(x); }
 __device__ __forceinline__ uint32_t hi32(uint64_t x) { return static_cast<uint32_t>(x >> 32); }
@@ -97,7 +116,8 @@ __device__ __forceinline__ uint32_t hi32(uint64_t x) { return static_cast<uint32
 // TMEM column of the packed (bf16 pairs) 16-query step kk: warpgroup w packs its 64 queries into columns [64 w, 64 w + 32).
 __device__ __forceinline__ uint32_t packed_col(int kk) { return kk < 4 ? kk * 8 : 64 + (kk - 4) * 8; }
 
-template <int D, bool CAUSAL>
+// SHARED: a.ranks CTAs share a key block (compiled apart: with the code for it the plain kernel took 1014 us in place of 988).
+template <int D, bool CAUSAL, bool SHARED>
 __global__ void __launch_bounds__(kThreads, 1)
 fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do, const BwdArgs a)
@@ -114,7 +134,8 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     // The key heads go in groups, so that the CTAs resident at one time share a few heads' Q, dO and dQ blocks in L2; inside
     // a group the list's order, the longest loops first.
     const int64_t per_group = static_cast<int64_t>(a.heads_per_group) * n_blocks;
-    if (blockIdx.x >= static_cast<int64_t>(a.kv_heads) * n_blocks) {
+    const unsigned ranks = SHARED ? a.ranks : 1, work = blockIdx.x / ranks, rank = blockIdx.x % ranks;  // (a cluster's CTAs have one `work`)
+    if (work >= static_cast<int64_t>(a.kv_heads) * n_blocks) {
         wait_for_the_one_before();
         return;
     }
@@ -122,7 +143,7 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         if (tid == 0) packed_timeout();
         return;
     }
-    const int grp = static_cast<int>(blockIdx.x / per_group), rem = static_cast<int>(blockIdx.x - grp * per_group);
+    const int grp = static_cast<int>(work / per_group), rem = static_cast<int>(work - grp * per_group);
     const int gsize = min(a.heads_per_group, a.kv_heads - grp * a.heads_per_group);
     const int kvh = grp * a.heads_per_group + rem % gsize;
     const int4 entry = a.plan.blocks[rem / gsize];
@@ -131,7 +152,10 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     // entries hold the number of a query block whose loop over keys is as long as this key block's over queries
     const int kb = CAUSAL ? n_seq - 1 - entry.z : entry.z;
     const int k0 = kb * kBlock, qb0 = CAUSAL ? kb : 0, nq = n_seq - qb0;
-    const int n_it = nq * a.group;  // query blocks of all of the key head's query heads
+    // query blocks of all of the key head's query heads, from which this CTA takes n_it behind the first it0
+    const int all_it = nq * a.group, it0 = SHARED ? static_cast<int>(static_cast<int64_t>(all_it) * rank / ranks) : 0,
+              n_it = SHARED ? static_cast<int>(static_cast<int64_t>(all_it) * (rank + 1) / ranks) - it0 : all_it;
+    const int h0 = kvh * a.group + (SHARED ? it0 / nq : 0), block0 = SHARED ? it0 % nq : 0;  // the first one's head, and its number among the head's
     const int q_left = len - (n_seq - 1) * kBlock;           // rows of the sequence's last block
     const int k_rows = min(kBlock, len - k0);                // keys of this block
     const uint32_t bar0 = sb + C::kBar;
@@ -183,42 +207,47 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             prefetch_tmap(&tm_k);
             prefetch_tmap(&tm_v);
             prefetch_tmap(&tm_do);
-            mbar_arrive_expect_tx(BAR(KV_FULL), 2 * C::kTile);
-            for (int c = 0; c < C::kAtoms; ++c) {
-                tma_load_3d(sb + C::kK + c * 16384, &tm_k, BAR(KV_FULL), c * 64, start + k0, kvh);
-                tma_load_3d(sb + C::kV + c * 16384, &tm_v, BAR(KV_FULL), c * 64, start + k0, kvh);
+            if (n_it > 0) {
+                mbar_arrive_expect_tx(BAR(KV_FULL), 2 * C::kTile);
+                for (int c = 0; c < C::kAtoms; ++c) {
+                    tma_load_3d(sb + C::kK + c * 16384, &tm_k, BAR(KV_FULL), c * 64, start + k0, kvh);
+                    tma_load_3d(sb + C::kV + c * 16384, &tm_v, BAR(KV_FULL), c * 64, start + k0, kvh);
+                }
             }
             bool ok = true;
             int i = 0, n_do = 0;
-            for (int h = kvh * a.group; h < (kvh + 1) * a.group && ok; ++h)
-                for (int qb = qb0; qb < n_seq; ++qb, ++i) {
-                    const int st = i & 1;
-                    if (i >= 2 && !(ok = mbar_wait(BAR(Q_FREE + st), ((i >> 1) - 1) & 1, kWaitLimitNs))) break;
-                    const int row = start + qb * kBlock;
-                    mbar_arrive_expect_tx(BAR(Q_FULL + st), C::kTile + 1024);
-                    for (int c = 0; c < C::kAtoms; ++c)
-                        tma_load_3d(sb + C::kQ + st * C::kTile + c * 16384, &tm_q, BAR(Q_FULL + st), c * 64, row, h);
-                    const int64_t vo = (static_cast<int64_t>(h) * a.nb + blk0 + qb) * kBlock;
-                    bulk_load(sb + C::kVec + st * 1024, a.lse2 + vo, 512, BAR(Q_FULL + st));
-                    bulk_load(sb + C::kVec + st * 1024 + 512, a.dvec + vo, 512, BAR(Q_FULL + st));
-                    if (i >= 1 && !(ok = mbar_wait(BAR(DO_FREE), (i - 1) & 1, kWaitLimitNs))) {
-                        ++i;
-                        break;
-                    }
-                    mbar_arrive_expect_tx(BAR(DO_FULL), C::kTile);
-                    for (int c = 0; c < C::kAtoms; ++c) tma_load_3d(sb + C::kDO + c * 16384, &tm_do, BAR(DO_FULL), c * 64, row, h);
-                    ++n_do;
+            for (int h = h0, qb = qb0 + block0; i < n_it; ++i) {
+                const int st = i & 1;
+                if (i >= 2 && !(ok = mbar_wait(BAR(Q_FREE + st), ((i >> 1) - 1) & 1, kWaitLimitNs))) break;
+                const int row = start + qb * kBlock;
+                mbar_arrive_expect_tx(BAR(Q_FULL + st), C::kTile + 1024);
+                for (int c = 0; c < C::kAtoms; ++c)
+                    tma_load_3d(sb + C::kQ + st * C::kTile + c * 16384, &tm_q, BAR(Q_FULL + st), c * 64, row, h);
+                const int64_t vo = (static_cast<int64_t>(h) * a.nb + blk0 + qb) * kBlock;
+                bulk_load(sb + C::kVec + st * 1024, a.lse2 + vo, 512, BAR(Q_FULL + st));
+                bulk_load(sb + C::kVec + st * 1024 + 512, a.dvec + vo, 512, BAR(Q_FULL + st));
+                if (i >= 1 && !(ok = mbar_wait(BAR(DO_FREE), (i - 1) & 1, kWaitLimitNs))) {
+                    ++i;
+                    break;
                 }
+                mbar_arrive_expect_tx(BAR(DO_FULL), C::kTile);
+                for (int c = 0; c < C::kAtoms; ++c) tma_load_3d(sb + C::kDO + c * 16384, &tm_do, BAR(DO_FULL), c * 64, row, h);
+                ++n_do;
+                if (++qb == n_seq) {
+                    qb = qb0;
+                    ++h;
+                }
+            }
             if (!ok) packed_timeout();
             // every copy this thread issued has landed before the CTA may exit
             const uint64_t lim = ok ? kWaitLimitNs : kCleanupLimitNs;
-            mbar_wait(BAR(KV_FULL), 0, lim);
+            if (n_it > 0) mbar_wait(BAR(KV_FULL), 0, lim);
             for (int j = i > 2 ? i - 2 : 0; j < i; ++j) mbar_wait(BAR(Q_FULL + (j & 1)), (j >> 1) & 1, lim);
             if (n_do > 0) mbar_wait(BAR(DO_FULL), (n_do - 1) & 1, lim);
         } else if (warp == kTailWarp) {
             // -------------------------------------------------- rows behind the sequence's end
             bool ok = true;
-            if (k_rows & 15) {
+            if ((k_rows & 15) && n_it > 0) {
                 ok = mbar_wait_warp(BAR(KV_FULL), 0, kWaitLimitNs);
                 zero_tail_rows<D>(smem + C::kK, k_rows, lane);
                 zero_tail_rows<D>(smem + C::kV, k_rows, lane);
@@ -227,7 +256,7 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 if (lane == 0) mbar_arrive(BAR(KV_TAIL));
             }
             if (q_left & 15) {  // every block's tiles go by this warp then (a wait for some of a barrier's phases can mistake one for another)
-                int block = 0;
+                int block = block0;
                 for (int i = 0; i < n_it && ok; ++i) {
                     const int st = i & 1;
                     const bool tail = ++block == nq;
@@ -259,7 +288,7 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             const uint32_t k_kmaj = kmaj + (C::kK >> 4), v_kmaj = kmaj + (C::kV >> 4), k_mn = mn + (C::kK >> 4), ds_mn = mn + (C::kDS >> 4),
                            q_kmaj = kmaj + (C::kQ >> 4), q_mn = mn + (C::kQ >> 4), do_kmaj = kmaj + (C::kDO >> 4), do_mn = mn + (C::kDO >> 4);
             const int k_steps = (k_rows + 15) / 16, tail_steps = (q_left + 15) / 16;
-            int block = 0;  // of the query head's nq
+            int block = block0;  // of the query head's nq
             const int q_there = (q_left & 15) ? Q_TAIL : Q_FULL, do_there = (q_left & 15) ? DO_TAIL : DO_FULL;
             // block i's tile is there, and its rows behind the end are zeros; S_i = K Q_i^T
             auto scores = [&](int i) -> bool {
@@ -274,7 +303,8 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 mma_commit(BAR(S_FULL));
                 return true;
             };
-            bool ok = mbar_wait(BAR(KV_FULL), 0, kWaitLimitNs) && (!(k_rows & 15) || mbar_wait(BAR(KV_TAIL), 0, kWaitLimitNs)) && scores(0);
+            bool ok = n_it == 0 || (mbar_wait(BAR(KV_FULL), 0, kWaitLimitNs) &&
+                                    (!(k_rows & 15) || mbar_wait(BAR(KV_TAIL), 0, kWaitLimitNs)) && scores(0));
             for (int i = 0; i < n_it && ok; ++i) {
                 const int st = i & 1;
                 const bool tail = ++block == nq;
@@ -323,39 +353,42 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         const uint32_t tQ = tB + (static_cast<uint32_t>(q * 32) << 16);
         uint8_t *stage = smem + C::kDQ + q * 8192;
         bool ok = true;
-        int i = 0;
-        for (int h = kvh * a.group; h < (kvh + 1) * a.group && ok; ++h)
-            for (int qb = qb0; qb < n_seq; ++qb, ++i) {
-                float *acc = a.dq_acc + (static_cast<int64_t>(h) * a.nb + blk0 + qb) * (kBlock * D) + q * (32 * D);
-                if (!(ok = mbar_wait_warp(BAR(DQ_FULL), i & 1, kWaitLimitNs))) break;
-                tc_fence_after();
+        int h = h0, qb = qb0 + block0;
+        for (int i = 0; i < n_it; ++i) {
+            float *acc = a.dq_acc + (static_cast<int64_t>(h) * a.nb + blk0 + qb) * (kBlock * D) + q * (32 * D);
+            if (!(ok = mbar_wait_warp(BAR(DQ_FULL), i & 1, kWaitLimitNs))) break;
+            tc_fence_after();
 #pragma unroll
-                for (int half = 0; half < D / 64; ++half) {
-                    uint32_t x[2][32];
-                    tmem_ld32(tQ + half * 64, x[0]);
-                    tmem_ld32(tQ + half * 64 + 32, x[1]);
-                    tmem_wait_ld();
-                    if (half == D / 64 - 1) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(BAR(DQ_CONSUMED));
-                    }
-                    if (lane == 0) bulk_wait_read0();  // (what was added before has left the buffers)
+            for (int half = 0; half < D / 64; ++half) {
+                uint32_t x[2][32];
+                tmem_ld32(tQ + half * 64, x[0]);
+                tmem_ld32(tQ + half * 64 + 32, x[1]);
+                tmem_wait_ld();
+                if (half == D / 64 - 1) {
+                    tc_fence_before();
                     __syncwarp();
+                    if (lane == 0) mbar_arrive(BAR(DQ_CONSUMED));
+                }
+                if (lane == 0) bulk_wait_read0();  // (what was added before has left the buffers)
+                __syncwarp();
 #pragma unroll
-                    for (int u = 0; u < 2; ++u)
+                for (int u = 0; u < 2; ++u)
 #pragma unroll
-                        for (int c = 0; c < 8; ++c)
-                            *reinterpret_cast<uint4 *>(stage + u * 4096 + (c * 32 + lane) * 16) =
-                                make_uint4(x[u][4 * c], x[u][4 * c + 1], x[u][4 * c + 2], x[u][4 * c + 3]);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        bulk_reduce_add_f32(acc + half * 2048, smem_u32(stage), 8192);
-                        bulk_commit();
-                    }
+                    for (int c = 0; c < 8; ++c)
+                        *reinterpret_cast<uint4 *>(stage + u * 4096 + (c * 32 + lane) * 16) =
+                            make_uint4(x[u][4 * c], x[u][4 * c + 1], x[u][4 * c + 2], x[u][4 * c + 3]);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    bulk_reduce_add_f32(acc + half * 2048, smem_u32(stage), 8192);
+                    bulk_commit();
                 }
             }
+            if (++qb == n_seq) {
+                qb = qb0;
+                ++h;
+            }
+        }
         if (!ok && lane == 0) packed_timeout();
         if (lane == 0) bulk_wait0();  // the additions have completed before the CTA ends
     } else {
@@ -366,7 +399,7 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         const uint32_t loff = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const int key = k0 + r;
         bool ok = true;
-        int block = 0;
+        int block = block0;
         for (int i = 0; i < n_it && ok; ++i) {
             const int st = i & 1;
             const int qb = qb0 + block;
@@ -452,7 +485,9 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         if (ok) ok = mbar_wait_warp(BAR(DONE), 0, kWaitLimitNs);
         if (!ok) packed_timeout();
         tc_fence_after();
-        // dV (TMEM C) and scale dK (TMEM D), this warpgroup's half of the columns; every lane takes part in the loads
+        // dV (TMEM C) and scale dK (TMEM D), this warpgroup's half of the columns; every lane takes part in the loads.  Shared with other
+        // CTAs, in fp32 into the place of K, V and Q, which the products have read: [dV, dK][key][d], 16-byte pieces at
+        // piece ^ (key mod 8)
         if (ok) {
 #pragma unroll
             for (int which = 0; which < 2; ++which) {
@@ -464,6 +499,15 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     uint32_t x[32];
                     tmem_ld32(tsrc + cc * 32, x);
                     tmem_wait_ld();
+                    if constexpr (SHARED) {
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            *reinterpret_cast<float4 *>(smem + (which * kBlock + r) * (D * 4) + (((wg * (D / 8) + cc * 8 + c) ^ (r & 7)) << 4)) =
+                                n_it == 0 ? make_float4(0.f, 0.f, 0.f, 0.f)  // (there is nothing in tensor memory)
+                                          : make_float4(__uint_as_float(x[4 * c]) * mul, __uint_as_float(x[4 * c + 1]) * mul,
+                                                        __uint_as_float(x[4 * c + 2]) * mul, __uint_as_float(x[4 * c + 3]) * mul);
+                        continue;
+                    }
                     if (key >= len) continue;
 #pragma unroll
                     for (int q4 = 0; q4 < 4; ++q4) {
@@ -477,6 +521,29 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 }
             }
         }
+    }
+    if constexpr (SHARED) {
+        __syncwarp();
+        cluster_sync();
+        if (warp < kAddWarp) {  // rank by rank, in their order; each CTA takes its part of the result's 8-column pieces
+            constexpr int kPieces = 2 * kBlock * D / 8;
+            const int end = kPieces * static_cast<int>(rank + 1) / static_cast<int>(ranks);
+            for (int i = kPieces * static_cast<int>(rank) / static_cast<int>(ranks) + tid; i < end; i += kAddWarp * 32) {
+                const int c = i % (D / 8), r = i / (D / 8) % kBlock, which = i / (D / 8) / kBlock;
+                if (k0 + r >= len) continue;
+                const uint32_t from = sb + (which * kBlock + r) * (D * 4), p0 = ((2 * c) ^ (r & 7)) << 4, p1 = ((2 * c + 1) ^ (r & 7)) << 4;
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+                for (unsigned other = 0; other < ranks; ++other) {
+                    const float4 u = ld_cluster_v4(from + p0, other), v = ld_cluster_v4(from + p1, other);
+                    x = make_float4(x.x + u.x, x.y + u.y, x.z + u.z, x.w + u.w);
+                    y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
+                }
+                reinterpret_cast<uint4 *>(packed_row(which == 0 ? a.dv : a.dk, start + k0 + r, kvh))[c] =
+                    make_uint4(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w), pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+            }
+        }
+        __syncwarp();
+        cluster_sync();  // no CTA ends while others read its shared memory
     }
     tc_fence_before();
     __syncthreads();
@@ -573,7 +640,7 @@ fa_packed_post_kernel(const BwdArgs a, int causal)
 
 // ------------------------------------------------------------------ host side
 
-template <int D, bool CAUSAL>
+template <int D, bool CAUSAL, bool SHARED>
 cudaError_t launch(const FaPackedProblem &p, const BwdArgs &a, cudaStream_t s)
 {
     using C = BCfg<D>;
@@ -581,15 +648,49 @@ cudaError_t launch(const FaPackedProblem &p, const BwdArgs &a, cudaStream_t s)
     if (!make_rows_map(&mq, p.q, p.T, p.H, D) || !make_rows_map(&mk, p.k, p.T, p.Hkv, D) ||
         !make_rows_map(&mv, p.v, p.T, p.Hkv, D) || !make_rows_map(&mdo, p.dout, p.T, p.H, D))
         return cudaErrorInvalidValue;
-    cudaError_t e = set_max_dynamic_smem<fa_packed_bwd_kernel<D, CAUSAL>>(C::kSmemBytes);
+    cudaError_t e = set_max_dynamic_smem<fa_packed_bwd_kernel<D, CAUSAL, SHARED>>(C::kSmemBytes);
     if (e != cudaSuccess) return e;
     const int64_t rows = static_cast<int64_t>(a.nb) * p.H, cap = static_cast<int64_t>(p.sm_count) * 8;
     const unsigned around = static_cast<unsigned>(rows < cap ? rows : cap);
     fa_packed_pre_kernel<D><<<around, 256, 0, s>>>(a, CAUSAL);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    e = launch_behind(fa_packed_bwd_kernel<D, CAUSAL>, static_cast<unsigned>(a.nb * p.Hkv), kThreads, C::kSmemBytes, s, mq, mk, mv, mdo, a);
+    e = launch_behind(fa_packed_bwd_kernel<D, CAUSAL, SHARED>, static_cast<unsigned>(a.nb * p.Hkv * a.ranks), kThreads, C::kSmemBytes, s,
+                      static_cast<unsigned>(a.ranks), mq, mk, mv, mdo, a);
     if (e != cudaSuccess) return e;
-    return launch_behind(fa_packed_post_kernel<D>, around, 256, 0, s, a, static_cast<int>(CAUSAL));
+    return launch_behind(fa_packed_post_kernel<D>, around, 256, 0, s, 1, a, static_cast<int>(CAUSAL));
+}
+
+// How many CTAs share a key block's loop over query blocks: with one, few key heads and long groups leave most SMs idle.  The least by
+// an estimate of the time in query blocks, for sequences of equal lengths: a CTA costs 4 besides its share.  Where not
+// all are resident at one time: causal, with the longest loops first, the work over the SMs and the last ones' end (an eighth more, as
+// measured), else whole turns.  Measured (us, a sequence where not said otherwise; the one chosen here first):
+//   500 rows, 8 heads on 1    8 35   4 42   1 92     2048, 8 on 1   8 64    6 77   4 99    1 313
+//   2048, 16 on 2             6 80   4 101  1 316    4096, 16 on 2  4 187   3 236  8 274   1 621
+//   8192, 8 on 1              4 336  6 385  1 1216   4096, 4 on 4   2 67    1 93   3 91
+//   3000, 24 on 3             4 169  3 185  1 475    10 of 300, 8 on 2   2 37  1 47  4 48
+//   3 of 1024, 8 on 8         1 39   2 60            2000 and 1500, 6 on 2, d = 64, not causal   2 54  4 60  1 88
+// (5 and 7 are never the best.)
+int ranks_of(const FaPackedProblem &p)
+{
+    const int64_t mean = (p.T / p.B + kBlock - 1) / kBlock, blocks = mean > 0 ? mean : 1;
+    const double n = static_cast<double>(p.B * blocks * p.Hkv), group = static_cast<double>(p.H / p.Hkv), loop = group * static_cast<double>(blocks);
+    // CTAs, in clusters of that many, that the GPU's groups of SMs hold at one time
+    constexpr struct {
+        int ranks, resident;
+    } kClusters[] = {{1, 152}, {2, 152}, {3, 138}, {4, 144}, {6, 138}, {8, 120}};
+    int best = 1;
+    double least = 0;
+    for (const auto &c : kClusters) {
+        if (c.ranks > 1 && c.ranks > loop) break;
+        const double share = 4 + ceil(loop / c.ranks), turns = ceil(n * c.ranks / c.resident);
+        double t = share * turns;
+        if (turns > 1 && p.causal) t = 1.125 * fmax(share, n * (loop / 2 + 4 * c.ranks) / c.resident + 4 + group / c.ranks);
+        if (c.ranks == 1 || t < least) {
+            least = t;
+            best = c.ranks;
+        }
+    }
+    return best;
 }
 
 }  // namespace
@@ -625,10 +726,15 @@ cudaError_t fa_launch_packed_bwd(const FaPackedProblem &p, void *workspace, cuda
     // to 4096 rows, 8 key heads, 130 blocks: groups of 1 head 1160 us, of 2 1094, of 4 1011), more share less of L2 (of 8 1060).
     const int64_t most = a.nb < 512 ? 512 / a.nb : 1, groups = p.Hkv > most ? (p.Hkv + most - 1) / most : 1;
     a.heads_per_group = static_cast<int>((p.Hkv + groups - 1) / groups);
+    a.ranks = ranks_of(p);
     a.scale = p.scale;
     a.scale_log2 = static_cast<float>(static_cast<double>(p.scale) * 1.4426950408889634);
-    if (p.d == 64) return p.causal ? launch<64, true>(p, a, s) : launch<64, false>(p, a, s);
-    return p.causal ? launch<128, true>(p, a, s) : launch<128, false>(p, a, s);
+    auto run = [&](auto shared) {
+        constexpr bool SHARED = decltype(shared)::value;
+        if (p.d == 64) return p.causal ? launch<64, true, SHARED>(p, a, s) : launch<64, false, SHARED>(p, a, s);
+        return p.causal ? launch<128, true, SHARED>(p, a, s) : launch<128, false, SHARED>(p, a, s);
+    };
+    return a.ranks > 1 ? run(std::true_type{}) : run(std::false_type{});
 }
 
 int fa_packed_bwd_take_status(cudaStream_t stream) { return packed_take_status_here(stream); }

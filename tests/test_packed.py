@@ -398,7 +398,9 @@ def test_backward_over_short_and_odd_lengths(lens, H, Hkv, d, causal):
 @gpu
 @pytest.mark.parametrize("causal", [False, True])
 @pytest.mark.parametrize("lens,H,Hkv,d,gain", [([1500, 1, 900, 77], 4, 2, 128, 1.0), ([1100, 130], 3, 1, 64, 4.0),
-                                              ([600] * 4, 2, 2, 128, 4.0), ([40] * 90, 8, 2, 64, 1.0), ([700], 16, 1, 128, 1.0)])
+                                              ([600] * 4, 2, 2, 128, 4.0), ([40] * 90, 8, 2, 64, 1.0), ([700], 16, 1, 128, 1.0),
+                                              (list(range(1, 300, 9)), 16, 8, 128, 1.0), (list(range(1, 300, 9)), 8, 8, 64, 1.0),
+                                              ([1500, 1, 1, 2], 2, 1, 64, 1.0), ([1030], 4, 1, 128, 1.0), ([900, 17], 3, 1, 128, 1.0)])
 def test_backward_over_many_tiles_and_large_scores(lens, H, Hkv, d, gain, causal):
     q, k, v, cu = batch(lens, H, Hkv, d, seed=15, gain=gain)
     dout, scale = randn(*q.shape, seed=8), fa.default_scale(d)
