@@ -14,6 +14,7 @@
 
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "fa.h"
@@ -127,8 +128,9 @@ __device__ __forceinline__ void wait_for_the_one_before() { asm volatile("gridde
 // In the kernel before: once all its CTAs have come here (or ended), the next one's may take what room there is.
 __device__ __forceinline__ void let_the_next_one_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 
+// In clusters of `cluster` CTAs; behind: with the launch above.
 template <typename... P, typename... A>
-cudaError_t launch_behind(void (*kern)(P...), unsigned grid, int threads, int smem, cudaStream_t s, unsigned cluster, const A &...args)
+cudaError_t launch_with(void (*kern)(P...), unsigned grid, int threads, int smem, cudaStream_t s, unsigned cluster, bool behind, const A &...args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
@@ -136,14 +138,62 @@ cudaError_t launch_behind(void (*kern)(P...), unsigned grid, int threads, int sm
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = s;
     cudaLaunchAttribute attrs[2] = {};
-    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attrs[0].val.programmaticStreamSerializationAllowed = 1;
-    attrs[1].id = cudaLaunchAttributeClusterDimension;
-    attrs[1].val.clusterDim.x = cluster;
-    attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
     cfg.attrs = attrs;
-    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    if (behind) {
+        attrs[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attrs[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1) {
+        attrs[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attrs[cfg.numAttrs].val.clusterDim.x = cluster;
+        attrs[cfg.numAttrs].val.clusterDim.y = attrs[cfg.numAttrs].val.clusterDim.z = 1;
+        ++cfg.numAttrs;
+    }
     return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+// Four floats at an address of this CTA's shared memory in the cluster's CTA `rank`; the cluster's barrier.
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr, uint32_t rank)
+{
+    float4 x;
+    asm volatile("{\n.reg .b32 a;\nmapa.shared::cluster.u32 a, %4, %5;\nld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n}\n"
+                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                 : "r"(addr), "r"(rank)
+                 : "memory");
+    return x;
+}
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+
+// How many CTAs (a cluster) share a loop: the least by an estimate of the time, in steps of the loop, for sequences of equal lengths.
+// n loops, the longest of `loop` steps, which go `step` at a time; a CTA costs `alone` besides its steps, in a cluster `fixed`.
+// Where not all are resident at one time: causal, with the longest loops first, the work over the SMs and the last ones' end (an
+// eighth more for clusters, as measured), else whole turns.
+inline int cluster_ranks(double n, double loop, double step, double alone, double fixed, bool causal)
+{
+    // CTAs, in clusters of that many, that the GPU's groups of SMs hold at one time, with one CTA an SM
+    constexpr struct {
+        int ranks, resident;
+    } kClusters[] = {{1, 152}, {2, 152}, {3, 138}, {4, 144}, {6, 138}, {8, 120}};
+    int best = 1;
+    double least = 0;
+    for (const auto &c : kClusters) {
+        if (c.ranks > 1 && c.ranks > loop) break;
+        const double cost = c.ranks == 1 ? alone : fixed;
+        const double share = cost + ceil(loop / c.ranks), turns = ceil(n * c.ranks / c.resident);
+        double t = share * turns;
+        if (turns > 1 && causal) {
+            t = fmax(share, n * (loop / 2 + cost * c.ranks) / c.resident + cost + step / c.ranks);
+            if (c.ranks > 1) t *= 1.125;
+        }
+        if (c.ranks == 1 || t < least) {
+            least = t;
+            best = c.ranks;
+        }
+    }
+    return best;
 }
 
 // Rows of no sequence: [0, first) and [last, T).  n of them; the i-th.

@@ -95,21 +95,6 @@ struct BwdArgs {
     float scale, scale_log2;
 };
 
-// Four floats at an address of this CTA's shared memory in the cluster's CTA `rank`; the cluster's barrier.
-__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr, uint32_t rank)
-{
-    float4 x;
-    asm volatile("{\n.reg .b32 a;\nmapa.shared::cluster.u32 a, %4, %5;\nld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n}\n"
-                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
-                 : "r"(addr), "r"(rank)
-                 : "memory");
-    return x;
-}
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
-}
-
 __device__ __forceinline__ uint32_t lo32(uint64_t x) { return static_cast<uint32_t>(x); }
 __device__ __forceinline__ uint32_t hi32(uint64_t x) { return static_cast<uint32_t>(x >> 32); }
 
@@ -654,43 +639,24 @@ cudaError_t launch(const FaPackedProblem &p, const BwdArgs &a, cudaStream_t s)
     const unsigned around = static_cast<unsigned>(rows < cap ? rows : cap);
     fa_packed_pre_kernel<D><<<around, 256, 0, s>>>(a, CAUSAL);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    e = launch_behind(fa_packed_bwd_kernel<D, CAUSAL, SHARED>, static_cast<unsigned>(a.nb * p.Hkv * a.ranks), kThreads, C::kSmemBytes, s,
-                      static_cast<unsigned>(a.ranks), mq, mk, mv, mdo, a);
+    e = launch_with(fa_packed_bwd_kernel<D, CAUSAL, SHARED>, static_cast<unsigned>(a.nb * p.Hkv * a.ranks), kThreads, C::kSmemBytes, s,
+                    static_cast<unsigned>(a.ranks), true, mq, mk, mv, mdo, a);
     if (e != cudaSuccess) return e;
-    return launch_behind(fa_packed_post_kernel<D>, around, 256, 0, s, 1, a, static_cast<int>(CAUSAL));
+    return launch_with(fa_packed_post_kernel<D>, around, 256, 0, s, 1, true, a, static_cast<int>(CAUSAL));
 }
 
-// How many CTAs share a key block's loop over query blocks: with one, few key heads and long groups leave most SMs idle.  The least by
-// an estimate of the time in query blocks, for sequences of equal lengths: a CTA costs 4 besides its share.  Where not
-// all are resident at one time: causal, with the longest loops first, the work over the SMs and the last ones' end (an eighth more, as
-// measured), else whole turns.  Measured (us, a sequence where not said otherwise; the one chosen here first):
+// How many CTAs share a key block's loop over query blocks: with one, few key heads and long groups leave most SMs idle.  Measured
+// (us, a sequence where not said otherwise, causal; the one chosen here first; 5 and 7 are never the best):
 //   500 rows, 8 heads on 1    8 35   4 42   1 92     2048, 8 on 1   8 64    6 77   4 99    1 313
 //   2048, 16 on 2             6 80   4 101  1 316    4096, 16 on 2  4 187   3 236  8 274   1 621
 //   8192, 8 on 1              4 336  6 385  1 1216   4096, 4 on 4   2 67    1 93   3 91
 //   3000, 24 on 3             4 169  3 185  1 475    10 of 300, 8 on 2   2 37  1 47  4 48
 //   3 of 1024, 8 on 8         1 39   2 60            2000 and 1500, 6 on 2, d = 64, not causal   2 54  4 60  1 88
-// (5 and 7 are never the best.)
 int ranks_of(const FaPackedProblem &p)
 {
     const int64_t mean = (p.T / p.B + kBlock - 1) / kBlock, blocks = mean > 0 ? mean : 1;
-    const double n = static_cast<double>(p.B * blocks * p.Hkv), group = static_cast<double>(p.H / p.Hkv), loop = group * static_cast<double>(blocks);
-    // CTAs, in clusters of that many, that the GPU's groups of SMs hold at one time
-    constexpr struct {
-        int ranks, resident;
-    } kClusters[] = {{1, 152}, {2, 152}, {3, 138}, {4, 144}, {6, 138}, {8, 120}};
-    int best = 1;
-    double least = 0;
-    for (const auto &c : kClusters) {
-        if (c.ranks > 1 && c.ranks > loop) break;
-        const double share = 4 + ceil(loop / c.ranks), turns = ceil(n * c.ranks / c.resident);
-        double t = share * turns;
-        if (turns > 1 && p.causal) t = 1.125 * fmax(share, n * (loop / 2 + 4 * c.ranks) / c.resident + 4 + group / c.ranks);
-        if (c.ranks == 1 || t < least) {
-            least = t;
-            best = c.ranks;
-        }
-    }
-    return best;
+    const double group = static_cast<double>(p.H / p.Hkv);
+    return cluster_ranks(static_cast<double>(p.B * blocks * p.Hkv), group * static_cast<double>(blocks), group, 4, 4, p.causal);
 }
 
 }  // namespace

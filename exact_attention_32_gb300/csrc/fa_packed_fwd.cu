@@ -16,6 +16,7 @@
 //     zeros (zero_tail_rows, up to a step of the product), their rows of O stay in tensor memory: a whole warp's 32 rows
 //     leave by TMA, the rows of a cut one by stores of their own.
 //   - A thread finds its item in the list; the next one is asked for an item ahead.
+//   - Where few long items leave SMs idle, a cluster of CTAs shares each (ranks_of).
 // Every mbarrier wait is bounded; a wait that gives up sets FA_ERR_TIMEOUT and the CTA winds down.
 #include <math.h>
 
@@ -66,6 +67,7 @@ struct FwdArgs {
     FaRows o;
     float *lse;
     int T, B, heads, units, group, fill;  // heads: H; units: items of a list entry; group: H / Hkv
+    int ranks;                            // CTAs (a cluster) that share an item
     float scale, scale_log2;
 };
 
@@ -97,9 +99,8 @@ struct Items {
     int step[2], step_entry[2], step_unit[2];
     int odd;
     int4 next;
-    __device__ __forceinline__ Items(const int4 *l, int n_items, int n_units) : list(l), units(n_units), odd(0)
+    __device__ __forceinline__ Items(const int4 *l, int n_items, int n_units, int G, int c) : list(l), units(n_units), odd(0)
     {
-        const int G = gridDim.x, c = blockIdx.x;
         left = n_items - c;
         step[0] = 2 * (G - c) - 1;
         step[1] = 2 * c + 1;
@@ -148,7 +149,9 @@ __device__ __forceinline__ float row_max(const float (&s)[kTile])
     return fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
 }
 
-template <int D, bool CAUSAL, bool PAIR>
+// SHARED: there is a cluster of a.ranks CTAs for every item, each for its part of the key tiles; what they have of a row is joined
+// through distributed shared memory, in the ranks' order.
+template <int D, bool CAUSAL, bool PAIR, bool SHARED>
 __global__ void __launch_bounds__(kThreads, 1)
 fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o, const FwdArgs a)
@@ -204,8 +207,12 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     const uint32_t tmem = *tmem_slot;
     const bool run = tmem_slot[1] != 0;
     const int n_items = run ? (PAIR ? a.plan.head->n_blocks : a.plan.head->n_pairs) * a.units : 0;
-    Items items(PAIR ? a.plan.blocks : a.plan.pairs, n_items, a.units);
+    const int ranks = SHARED ? a.ranks : 1, rank = SHARED ? blockIdx.x % ranks : 0;
+    Items items(PAIR ? a.plan.blocks : a.plan.pairs, n_items, a.units, gridDim.x / ranks, blockIdx.x / ranks);
     Item w;
+    // this CTA's key tiles [begin, end) of an item's n
+    auto begin = [&](int n) { return SHARED ? n * rank / ranks : 0; };
+    auto end = [&](int n) { return SHARED ? n * (rank + 1) / ranks : n; };
 
     if (warp >= kLoadWarp) {
         registers_down<kOtherRegs>();
@@ -218,7 +225,8 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 bool ok = true;
                 int it = 0, uc = 0;
                 while (ok && items.take<PAIR>(w)) {
-                    const int n0 = tile_keys<CAUSAL, PAIR>(w, 0), n1 = tile_keys<CAUSAL, PAIR>(w, 1), n_kv = max(n0, n1);
+                    const int n0 = tile_keys<CAUSAL, PAIR>(w, 0), n1 = tile_keys<CAUSAL, PAIR>(w, 1), n_kv = max(n0, n1), j1 = end(n_kv);
+                    if (SHARED && begin(n_kv) == j1) continue;
                     // the Q buffers are free once the item before has issued its last S
                     if (!(ok = mbar_wait(BAR(Q_EMPTY), (uc & 1) ^ 1, kWaitLimitNs))) break;
                     mbar_arrive_expect_tx(BAR(Q_FULL), (n1 > 0 ? 2 : 1) * C::kTileBytes);
@@ -228,7 +236,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                                         tile_head<PAIR>(w, t));
                     ++uc;
                     const int kv = w.head / a.group;
-                    for (int j = 0; j < n_kv && ok; ++j)
+                    for (int j = begin(n_kv); j < j1 && ok; ++j)
                         for (int kind = 0; kind < 2; ++kind, ++it) {
                             const int slot = it % C::kStages, use = it / C::kStages;
                             if (!(ok = mbar_wait(EMPTY(slot), (use & 1) ^ 1, kWaitLimitNs))) break;
@@ -261,7 +269,9 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             int it = 0, uc = 0;
             int sent[2] = {0, 0};  // S tiles sent to tile 0 / 1 (all items)
             while (ok && items.take<PAIR>(w)) {
-                const int n[2] = {tile_keys<CAUSAL, PAIR>(w, 0), tile_keys<CAUSAL, PAIR>(w, 1)}, n_kv = max(n[0], n[1]);
+                const int all = max(tile_keys<CAUSAL, PAIR>(w, 0), tile_keys<CAUSAL, PAIR>(w, 1)), j0 = begin(all), n_kv = end(all);
+                const int n[2] = {min(tile_keys<CAUSAL, PAIR>(w, 0), n_kv), min(tile_keys<CAUSAL, PAIR>(w, 1), n_kv)};
+                if (SHARED && j0 == n_kv) continue;
                 const int last = (w.len - 1) / kTile, left = w.len - last * kTile;  // the sequence's last key tile, its keys
                 if (!(ok = mbar_wait_warp(BAR(Q_FULL), uc & 1, kWaitLimitNs))) break;
                 tc_fence_after();
@@ -276,13 +286,13 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                         for (int kk = 0; kk < kTile / 16; ++kk)
                             if (kk < v_steps)
                                 mma_ts_lohi(tmem + 256 + t * 128, tmem + t * 128 + kk * 8, v_lo + kk * 128, dv_hi, idO,
-                                            (j > 0 || kk > 0) ? 1u : 0u);
+                                            (j > j0 || kk > 0) ? 1u : 0u);
                         if (j == n[t] - 1) mma_commit(BAR(O_FULL + t));
                     }
                     __syncwarp();
                     return true;
                 };
-                for (int j = 0; j < n_kv && ok; ++j) {
+                for (int j = j0; j < n_kv && ok; ++j) {
                     const int kslot = it % C::kStages, kuse = it / C::kStages;
                     ++it;
                     const int vslot = it % C::kStages, vuse = it / C::kStages;
@@ -292,7 +302,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     const uint32_t dk_lo = static_cast<uint32_t>(dk) + kslot * kTile16;
     #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        if (j > 0 && j <= n[t] && !(ok = pv(t, j - 1))) break;
+                        if (j > j0 && j <= n[t] && !(ok = pv(t, j - 1))) break;
                         if (j >= n[t]) continue;
                         if (elect_one()) {
     #pragma unroll
@@ -308,7 +318,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     if (!ok) break;
                     if (elect_one()) {
                         mma_commit(EMPTY(kslot));
-                        if (j > 0) mma_commit(EMPTY(v_slot));
+                        if (j > j0) mma_commit(EMPTY(v_slot));
                         if (j == n_kv - 1) mma_commit(BAR(Q_EMPTY));  // the item's last reads of Q are issued
                     }
                     __syncwarp();
@@ -360,14 +370,19 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         }
         bool ok = true;
         int jg = 0, uc = 0;
+        const float c_u = a.scale_log2;
+        float m_ref = -INFINITY;  // reference max, unscaled units
+        float l = 0.f;            // exp-sum relative to m_ref (fp32 terms; gives LSE)
+        float lr = 0.f;           // the divisor of O (d = 128)
+        bool any = false;         // SHARED: this CTA has an item, and key tiles of it
         while (ok && items.take<PAIR>(w)) {
+            const int all = SHARED ? max(tile_keys<CAUSAL, PAIR>(w, 0), tile_keys<CAUSAL, PAIR>(w, 1)) : 0;
             const int n_mine = tile_keys<CAUSAL, PAIR>(w, t), row0 = tile_row<PAIR>(w, t);
-            if (n_mine == 0) continue;
+            const int j0 = begin(all), j1 = SHARED ? min(n_mine, end(all)) : n_mine;
+            if (j1 <= j0) continue;
             const bool mine = row0 + row < w.len;
-            const float c_u = a.scale_log2;
-            float m_ref = -INFINITY;  // reference max, unscaled units
-            float l = 0.f;            // exp-sum relative to m_ref (fp32 terms; gives LSE)
-            float lr = 0.f;           // the divisor of O (d = 128)
+            m_ref = -INFINITY;
+            l = lr = 0.f;
             // One key tile; `masked`: some row does not admit some of its keys (an item's last tile: the diagonal's, or one that
             // reaches behind the sequence's end).
             auto tile = [&](auto masked, int j) -> bool {
@@ -445,7 +460,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 }
                 l = l * alpha + (lfs.x + lfs.y);
                 // the numerator rescaled (it holds P V up to the tile before: that product was issued ahead of this S)
-                if (j > 0 && __any_sync(0xffffffffu, need)) {
+                if (j > j0 && __any_sync(0xffffffffu, need)) {
 #pragma unroll
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t r[32];
@@ -473,8 +488,8 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 return true;
             };
             const int plain = n_mine - (CAUSAL || n_mine * kTile > w.len ? 1 : 0);
-            for (int j = 0; j < plain && ok; ++j) ok = tile(std::false_type{}, j);
-            if (ok && plain < n_mine) ok = tile(std::true_type{}, plain);
+            for (int j = j0; j < min(plain, j1) && ok; ++j) ok = tile(std::false_type{}, j);
+            if (ok && plain < j1) ok = tile(std::true_type{}, plain);
             if (!ok || !(ok = mbar_wait_warp(BAR(O_FULL + t), uc & 1, kWaitLimitNs))) break;
             tc_fence_after();
             // O = u / lr in bf16, LSE from the fp32 sum.  The next item's first product over O_t is issued only after this
@@ -482,6 +497,10 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             if constexpr (C::kOnesCol) {
                 lr = __uint_as_float(tmem_ld1(tO + 64));
                 tmem_wait_ld();
+            }
+            if constexpr (SHARED) {
+                any = true;
+                continue;
             }
             const float inv_l = lr > 0.f ? 1.f / lr : 0.f;
             const int head = tile_head<PAIR>(w, t), wrow = row0 + (warp & 3) * 32;  // this warp's first row
@@ -531,6 +550,60 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         }
         if (!ok) packed_timeout();
         if (lane == 0) bulk_wait0();  // every O store of this warp has completed
+        if constexpr (SHARED) {
+            // the sums and the unnormalised O where K and V were, once both tiles' products have read them: [tile][row][d] fp32, 16-byte
+            // pieces at piece ^ (row mod 8)
+            __syncwarp();
+            asm volatile("barrier.cta.sync 1, 256;\n" ::: "memory");
+            reinterpret_cast<float4 *>(smem + C::kStage)[tid] = any ? make_float4(m_ref, l, lr, 0.f) : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+            if (any) {
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t r[32];
+                    tmem_ld32(tO + c * 32, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<uint4 *>(smem + C::kRing + tid * (D * 4) + (((c * 8 + i) ^ (row & 7)) << 4)) =
+                            make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+                }
+            }
+        }
+    }
+    if constexpr (SHARED) {
+        __syncwarp();
+        cluster_sync();
+        Items again(PAIR ? a.plan.blocks : a.plan.pairs, n_items, a.units, gridDim.x / ranks, blockIdx.x / ranks);
+        if (warp < kLoadWarp && again.take<PAIR>(w)) {
+            // each CTA takes its part of the item's 8-column pieces
+            constexpr int kPieces = 2 * kTile * D / 8;
+            for (int i = kPieces * rank / ranks + tid; i < kPieces * (rank + 1) / ranks; i += 256) {
+                const int c = i % (D / 8), at = i / (D / 8), t = at / kTile, row = tile_row<PAIR>(w, t) + at % kTile, head = tile_head<PAIR>(w, t);
+                if (row >= w.len) continue;
+                float m = -INFINITY;
+                for (int other = 0; other < ranks; ++other) m = fmaxf(m, ld_cluster_v4(sb + C::kStage + at * 16, other).x);
+                float l = 0.f, lr = 0.f;
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+                const uint32_t from = sb + C::kRing + at * (D * 4), p0 = ((2 * c) ^ (at & 7)) << 4, p1 = ((2 * c + 1) ^ (at & 7)) << 4;
+                for (int other = 0; other < ranks; ++other) {
+                    const float4 part = ld_cluster_v4(sb + C::kStage + at * 16, other);
+                    if (part.y == 0.f) continue;  // no keys of this row
+                    const float4 u = ld_cluster_v4(from + p0, other), v = ld_cluster_v4(from + p1, other);
+                    const float f = ex2((part.x - m) * a.scale_log2);
+                    l = fmaf(f, part.y, l);
+                    lr = fmaf(f, part.z, lr);
+                    x = make_float4(fmaf(f, u.x, x.x), fmaf(f, u.y, x.y), fmaf(f, u.z, x.z), fmaf(f, u.w, x.w));
+                    y = make_float4(fmaf(f, v.x, y.x), fmaf(f, v.y, y.y), fmaf(f, v.z, y.z), fmaf(f, v.w, y.w));
+                }
+                const float inv = lr > 0.f ? 1.f / lr : 0.f;
+                reinterpret_cast<uint4 *>(packed_row(a.o, w.start + row, head))[c] =
+                    make_uint4(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv), pack_bf16x2(y.x * inv, y.y * inv),
+                               pack_bf16x2(y.z * inv, y.w * inv));
+                if (c == 0) a.lse[static_cast<int64_t>(head) * a.T + w.start + row] = l > 0.f ? m * a.scale + logf(l) : -INFINITY;
+            }
+        }
+        __syncwarp();
+        cluster_sync();  // no CTA ends while others read its shared memory
     }
     tc_fence_before();
     __syncthreads();
@@ -540,15 +613,15 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     }
 }
 
-template <int D, bool CAUSAL, bool PAIR>
-cudaError_t launch(const FaPackedProblem &p, cudaStream_t stream)
+template <int D, bool CAUSAL, bool PAIR, bool SHARED>
+cudaError_t launch(const FaPackedProblem &p, int ranks, cudaStream_t stream)
 {
     using C = PCfg<D>;
     CUtensorMap mq, mk, mv, mo;
     if (!make_rows_map(&mq, p.q, p.T, p.H, D) || !make_rows_map(&mk, p.k, p.T, p.Hkv, D) ||
         !make_rows_map(&mv, p.v, p.T, p.Hkv, D) || !make_rows_map(&mo, p.o, p.T, p.H, D, true))
         return cudaErrorInvalidValue;
-    const cudaError_t e = set_max_dynamic_smem<fa_packed_fwd_kernel<D, CAUSAL, PAIR>>(C::kSmemBytes);
+    const cudaError_t e = set_max_dynamic_smem<fa_packed_fwd_kernel<D, CAUSAL, PAIR, SHARED>>(C::kSmemBytes);
     if (e != cudaSuccess) return e;
     FwdArgs a;
     a.plan = plan_view(p.plan, p.B, p.T);
@@ -560,26 +633,42 @@ cudaError_t launch(const FaPackedProblem &p, cudaStream_t stream)
     a.units = static_cast<int>(PAIR ? p.H / 2 : p.H);
     a.group = static_cast<int>(p.H / p.Hkv);
     a.fill = p.fill;
+    a.ranks = ranks;
     a.scale = p.scale;
     a.scale_log2 = static_cast<float>(static_cast<double>(p.scale) * 1.4426950408889634);
     const int64_t most = (p.T / (PAIR ? 128 : 256) + p.B) * a.units;  // items, whatever the lengths are
-    const int64_t grid = most < p.sm_count ? most : p.sm_count;
-    fa_packed_fwd_kernel<D, CAUSAL, PAIR><<<static_cast<unsigned>(grid), kThreads, C::kSmemBytes, stream>>>(mq, mk, mv, mo, a);
+    const int64_t grid = SHARED ? most * ranks : most < p.sm_count ? most : p.sm_count;
+    auto kern = fa_packed_fwd_kernel<D, CAUSAL, PAIR, SHARED>;
+    if constexpr (SHARED) return launch_with(kern, static_cast<unsigned>(grid), kThreads, C::kSmemBytes, stream, static_cast<unsigned>(ranks), false, mq, mk, mv, mo, a);
+    kern<<<static_cast<unsigned>(grid), kThreads, C::kSmemBytes, stream>>>(mq, mk, mv, mo, a);
     return cudaGetLastError();
 }
 
-template <int D>
-cudaError_t launch_d(const FaPackedProblem &p, cudaStream_t s)
+template <int D, bool SHARED>
+cudaError_t launch_d(const FaPackedProblem &p, int ranks, cudaStream_t s)
 {
-    if (p.H / p.Hkv % 2 == 0) return p.causal ? launch<D, true, true>(p, s) : launch<D, false, true>(p, s);
-    return p.causal ? launch<D, true, false>(p, s) : launch<D, false, false>(p, s);
+    if (p.H / p.Hkv % 2 == 0) return p.causal ? launch<D, true, true, SHARED>(p, ranks, s) : launch<D, false, true, SHARED>(p, ranks, s);
+    return p.causal ? launch<D, true, false, SHARED>(p, ranks, s) : launch<D, false, false, SHARED>(p, ranks, s);
+}
+
+// How many CTAs share an item's key tiles: long loops of few items leave SMs idle, but joining them costs as much as 8 tiles.
+// Measured (us, d = 128, one sequence, causal; 1, 2, 3 and 4 CTAs): 4096 rows, 4 heads on 4 (64 items) 54, 39, 45, 43; 12000, 3 on 1
+// (141) 146, 99, 135, 135; 2048, 8 on 1 (64) 30, 27, 39, 37; 4096, 16 on 2 (256) 56, 102, 147, 164.
+int ranks_of(const FaPackedProblem &p)
+{
+    const bool pair = p.H / p.Hkv % 2 == 0;
+    const int64_t mean = (p.T / p.B + kTile - 1) / kTile, tiles = mean > 0 ? mean : 1;
+    const int64_t n = p.B * (pair ? tiles * (p.H / 2) : (tiles + 1) / 2 * p.H);
+    return cluster_ranks(static_cast<double>(n), static_cast<double>(tiles), 1, 1, 8, p.causal);
 }
 
 }  // namespace
 
 cudaError_t fa_launch_packed_fwd(const FaPackedProblem &p, cudaStream_t stream)
 {
-    return p.d == 64 ? launch_d<64>(p, stream) : launch_d<128>(p, stream);
+    const int ranks = ranks_of(p);
+    if (ranks > 1) return p.d == 64 ? launch_d<64, true>(p, ranks, stream) : launch_d<128, true>(p, ranks, stream);
+    return p.d == 64 ? launch_d<64, false>(p, 1, stream) : launch_d<128, false>(p, 1, stream);
 }
 
 int fa_packed_fwd_take_status(cudaStream_t stream) { return packed_take_status_here(stream); }

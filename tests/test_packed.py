@@ -209,7 +209,10 @@ def test_forward_over_short_and_odd_lengths(lens, H, Hkv, d, causal):
 @gpu
 @pytest.mark.parametrize("causal", [False, True])
 @pytest.mark.parametrize("lens,H,Hkv,d,gain", [([1500, 1, 900, 77], 4, 2, 128, 1.0), ([2048, 130], 3, 1, 64, 8.0),
-                                              ([1000] * 5, 2, 2, 128, 8.0), ([40] * 90, 8, 2, 64, 1.0)])
+                                              ([1000] * 5, 2, 2, 128, 8.0), ([40] * 90, 8, 2, 64, 1.0),
+                                              # few long items, which clusters of 2 to 4 share; short sequences beside them
+                                              ([3000], 4, 2, 128, 1.0), ([2900, 1, 3300], 2, 1, 64, 4.0), ([3, 4100], 1, 1, 128, 8.0),
+                                              ([4500, 129], 2, 2, 64, 1.0), ([2700], 3, 1, 128, 1.0)])
 def test_forward_over_many_tiles_and_large_scores(lens, H, Hkv, d, gain, causal):
     q, k, v, cu = batch(lens, H, Hkv, d, seed=5, gain=gain)
     o, lse = fa.forward_packed(q.cuda(), k.cuda(), v.cuda(), dev_cu(cu), causal=causal)
@@ -265,10 +268,10 @@ def test_slices_of_one_projection_and_given_outputs(H, Hkv, d):
 @gpu
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])
 @pytest.mark.parametrize("causal", [False, True])
-@pytest.mark.parametrize("H,Hkv,d", [(4, 2, 64), (2, 2, 128), (4, 1, 128), (3, 1, 64)])
-def test_what_other_sequences_hold_stays_out(H, Hkv, d, causal, value):
+@pytest.mark.parametrize("H,Hkv,d,last", [(4, 2, 64, 150), (2, 2, 128, 150), (4, 1, 128, 150), (3, 1, 64, 150), (2, 1, 128, 9000), (1, 1, 64, 9000)])
+def test_what_other_sequences_hold_stays_out(H, Hkv, d, last, causal, value):
     # the second of three sequences, and the rows behind the last, hold rubbish; the others are as without it
-    lens = [77, 100, 150]
+    lens = [77, 100, last]
     q, k, v, cu = batch(lens, H, Hkv, d, seed=21, tail=60)
     dout = randn(*q.shape, seed=24)
     bad = [t.clone() for t in (q, k, v, dout)]
