@@ -10,7 +10,8 @@ constexpr int kMostDrafts = 64;
 
 // A block per (sequence, key head), D / 16 threads a draft (half for K, half for V), 16 bytes each.  Every
 // row is read before any is written: a path is moved over drafts that it passes.  A call is a few rows of 137 bytes a head,
-// so its time is latency: lengths and path, the page, the row, the store, one behind the other, and nothing else.
+// so its time is latency: lengths and path, the page, the row, the store, one behind the other, and nothing else (with an append
+// before and a read behind it, in a graph: 16 drafts of 1 sequence 6.0 us, 32 drafts of 64 sequences 9.8).
 template <int D>
 __global__ void __launch_bounds__(kMostDrafts * D / 16)
 fa_kv4_keep_kernel(const Kv4KeepProblem p)
@@ -76,7 +77,7 @@ fa_kv4_keep_kernel(const Kv4KeepProblem p)
 constexpr int kCopyThreads = 256, kCopyTurns = 4;  // 16-byte pieces a thread has under way
 
 // A page is five runs of bytes, one in each array, each a multiple of 16 bytes; a block takes kCopyThreads
-// kCopyTurns pieces of one page.  Memory-bound.
+// kCopyTurns pieces of one page.  Memory-bound: 262 MB each way, 8 key heads, d = 128, pages of 64, 88 us (6.0 TB/s).
 __global__ void __launch_bounds__(kCopyThreads)
 fa_kv4_copy_kernel(Kv4Cache from, Kv4Cache to, const int32_t *__restrict__ pages, const int32_t *__restrict__ to_pages, int64_t items,
                    int slices)

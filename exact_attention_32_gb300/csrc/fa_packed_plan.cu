@@ -1,7 +1,8 @@
 // The plan of a packed batch (format: fa_packed.cuh), made on the device from the sequences' offsets, so that no
 // length is read back by the host and a captured step can run with new ones.
 //
-// One block: a plan is small (an entry per 128 rows) and made once a batch for all layers and both directions.  The
+// One block: a plan is small (an entry per 128 rows) and made once a batch for all layers and both directions; 7 to 8 us, most of it
+// barriers, for 3 to 48 sequences.  The
 // offsets are held to an ascending run inside [0, T] (a prefix maximum), the lists are sorted by the
 // length of their loops by counting (1024 bins; past 1023 tiles a bin holds several lengths, which only loosens the order).
 #include "fa_packed.cuh"
