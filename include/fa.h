@@ -665,9 +665,9 @@ int fa_key_weights(const void *q, const void *k, const float *lse, float *weight
  * bounded wait inside a kernel gave up and the kernel returned early, leaving
  * its outputs incomplete; or FA_ERR_BAD_PAGE, see the 4-bit cache; or
  * FA_ERR_BAD_SEQUENCE, see packed sequences).  While
- * FA_ERR_TIMEOUT is set, fa_fwd and fa_fwd_kv4 launches do no work (their
- * outputs are left unwritten) until this call clears it; a fa_fwd_kv4 call
- * in which a wait gave up adds nothing to the cache's weights.
+ * FA_ERR_TIMEOUT is set, fa_fwd, fa_fwd_packed, fa_fwd_kv4 and fa_fwd_kv4_tree launches do no work (their
+ * outputs are left unwritten), and fa_bwd_packed leaves out its products (what it writes means nothing),
+ * until this call clears it; a fa_fwd_kv4 call in which a wait gave up adds nothing to the cache's weights.
  * Returns FA_ERR_LAUNCH if the synchronisation itself reports a CUDA error.
  */
 int fa_get_device_status(void *stream);
