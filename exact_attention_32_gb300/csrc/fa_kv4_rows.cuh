@@ -28,7 +28,7 @@ constexpr int kRowsLaunchRegs = 72, kRowsSoftmaxRegs = 88, kRowsOtherRegs = 48;
 // A row's reference is set this far (log2) above what the largest term needs: with the decode kernel's 3 one of 24 rows grew in
 // every sixth tile, at 5000 cycles each time.
 constexpr float kRowsHeadroom = 6.f, kRowsTopLog2 = 15.f, kRowsSumLog2 = 60.f;
-constexpr float kRowsNone = 1e30f;  // minus the reference of a row that has met no key
+constexpr float kRowsNone = FLT_MAX;  // minus the reference of a row that has met no key
 // What starting and ending an item costs, in tiles.  48 rows, 32 sequences of up to 8192: 6 134 us, 9 113, 13 104; 32 rows 100, 96,
 // 100; 128 rows 296, 266, 246.
 constexpr int kRowsItemUnits = 12;
@@ -429,6 +429,9 @@ fa_kv4_rows_kernel(const DecodeArgs a)
                 // seldom): first the scores themselves, then against what the references have become
                 float2 x[NG][4];
                 const float4 *from = i == mine0 ? sm_raw : sm_ref;
+                // (the same rounded product both times, so its addend is one that is not known to be 0: mul and add are made one fma,
+                // which is off by more than a reference allows where scores pass 2^28)
+                const float zero = *reinterpret_cast<const volatile float *>(&sm_raw[0].z);
                 for (bool grown = false;;) {
                     uint32_t s[NG][8];
 #pragma unroll
@@ -439,8 +442,9 @@ fa_kv4_rows_kernel(const DecodeArgs a)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const float4 c = from[q * 4 + j];
-                            x[q][j] = fma2(make_float2(__uint_as_float(s[q][2 * j]), __uint_as_float(s[q][2 * j + 1])), make_float2(c.x, c.y),
-                                           make_float2(c.z, c.w));
+                            const float2 p = fma2(make_float2(__uint_as_float(s[q][2 * j]), __uint_as_float(s[q][2 * j + 1])), make_float2(c.x, c.y),
+                                                  make_float2(zero, zero));
+                            x[q][j] = add2(p, make_float2(c.z, c.w));
                         }
                     if (edge) {
                         const int draft = key - (w.len - newest), bit = draft & 63;

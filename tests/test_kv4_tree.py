@@ -25,6 +25,10 @@ def random_tree(rng, B, n_q):
     return parent, masks.view(np.int64)
 
 
+def randn_bf16(shape, seed):
+    return torch.randn(shape, generator=torch.Generator().manual_seed(seed)).bfloat16()
+
+
 def check_tree(pool, q, lens, scale, masks, n_new, o, lse):
     d = q.shape[3]
     o, lse, qd = f64(o), f64(lse), f64(q)
@@ -155,6 +159,36 @@ def test_rows_of_very_different_size(d, G, n_q, room):
         o, lse = fa.forward_kv4_tree(q * gain, pool.cache(), dev(lens), table_of(pool, room), dev(masks), scale=float(0.125 / gain))
         ok()
         check_tree(pool, q * gain, lens, 0.125 / gain, masks, None, o, lse)
+
+
+@gpu
+@rooms
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("size", [-1e33, 1e33, -1e-30])
+def test_scores_of_any_size(size, d, room):
+    # 24 rows over three tokens of a context and a draft, whose keys are 1, 2, 3 and 4 in every channel: all scores
+    # far below or above zero, or next to it; the largest takes all, or all are alike
+    B, G, n_q, P = 3, 8, 3, 16
+    cache = fa.kv4_cache(4, 1, P, d)
+    k = (torch.arange(1, 5).view(4, 1) * torch.ones(d)).bfloat16().cuda().expand(B, 1, 4, d).contiguous()
+    v = randn_bf16((B, 1, 4, d), 3).cuda()
+    table = np.full((B, max(1, room // P)), -7, np.int32)
+    table[:, 0] = [2, 0, 3]
+    table, lens = dev(table), dev(np.full(B, 4, np.int32))
+    fa.kv4_append(cache, k, v, lens, table)
+    ks, vs = (f64(t) for t in fa.kv4_read(cache, lens, table, 4))
+    q = torch.full((B, G, n_q, d), size).bfloat16().cuda()
+    masks = np.tile(np.array([1, 1, 1], np.int64), (B, 1))
+    o, lse = fa.forward_kv4_tree(q, cache, lens, table, dev(masks), n_new=dev(np.ones(B, np.int32)))
+    ok()
+    s = float(q[0, 0, 0, 0]) * fa.default_scale(d) * ks[:, 0].sum(-1)  # [B, 4]
+    e = np.exp(s - s.max(-1, keepdims=True))
+    want_lse, want = s.max(-1) + np.log(e.sum(-1)), np.einsum("bn,bnd->bd", e / e.sum(-1, keepdims=True), vs[:, 0])
+    for b in range(B):
+        # |lse| to (d + 8) roundings of the sum and the two of its last product; O to bf16's and P's (a half) roundings
+        assert (np.abs(f64(lse)[b, :, 0] - want_lse[b]) <= (d + 16) * 2.0 ** -23 * np.abs(want_lse[b]) + 1e-6).all()
+        assert (np.abs(f64(o)[b, :, 0] - want[b]) <= (2.0 ** -8 + 2.0 ** -10) * np.abs(vs[b, 0]).max(0)).all()
+        assert (f64(lse)[b, :, 1:] == -np.inf).all() and (f64(o)[b, :, 1:] == 0).all()
 
 
 @gpu
