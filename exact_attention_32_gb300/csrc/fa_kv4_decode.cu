@@ -1037,7 +1037,7 @@ struct Geometry {
 };
 
 // tree: for fa_fwd_kv4_tree, whose items of many rows a key head go to fa_kv4_rows_kernel (g.ng > 0) or, where there is little work,
-// in smaller chunks.  Up to 16 rows it has the chain's chunks and shares, and so its bits.
+// in smaller chunks.  Up to 8 rows it has the chain's chunks and shares, and so its bits.
 Geometry geometry(int64_t B, int64_t H, int64_t heads, int64_t n_q, int64_t d, int64_t max_tokens, int accumulate, bool tree)
 {
     Geometry g;
@@ -1046,10 +1046,11 @@ Geometry geometry(int64_t B, int64_t H, int64_t heads, int64_t n_q, int64_t d, i
     // 32 sequences of 8192, 4 key heads: a chunk of 16 rows takes 39 to 41 us among others, one of 32 74 (32 rows in one CTA 85, in
     // two of 16 89; 40 rows in two of 32 144, in three of 16 123; 1 key head: 80 rows 67 and 62, 96 rows 67 and 71, 176 even)
     g.rt = R <= 8 ? 1 : R <= 16 || (R + 15) / 16 * 7 < (R + 31) / 32 * 13 ? 2 : 4;
-    if (tree && R > 16) {
+    if (tree && R > 8) {
         // Units (tiles, and kItemUnits an item) for each CTA that the SMs hold, in chunks of 8 and of 16 rows.
         // Few: chunks of 8.  1 sequence of 700, 4 key heads, 64 rows, d = 64 (0.3 units): chunks of 8 11.1 us, of 16 12.2, the other
-        // kernel 19.3; 1 of 4000, 8 key heads, 48 rows, d = 128 (3.7) 23.0, 22.9, 27.6; 2 of 2000, 64 rows (5.3) 20.8, 18.6, 21.7.
+        // kernel 19.3; 1 of 4000, 8 key heads, 48 rows, d = 128 (3.7) 23.0, 22.9, 27.6; 2 of 2000, 64 rows (5.3) 20.8, 18.6, 21.7; 1 of
+        // 4000, 4 key heads, 16 rows (0.6) 13.9 and 15.1.
         // Many: the other kernel, whose first tile takes 15 us more and the others less.  8 key heads, 48 rows, d = 128, chunks
         // of 16 and the other kernel: 4 sequences of up to 4000 (11 units) 21.7 and 30.3; 1 of 30000 (18.8) 46.7 and 42.7; 32 of up
         // to 8192 (169) 160 and 101, 24 rows 101 and 93, 32 rows 108 and 100, 64 rows 186 and 165, 128 rows 350 and 243; d = 64,
@@ -1059,7 +1060,7 @@ Geometry geometry(int64_t B, int64_t H, int64_t heads, int64_t n_q, int64_t d, i
         auto work = [&](int64_t rows, int64_t per_sm) { return B * heads * ((R + rows - 1) / rows) * (tiles + kItemUnits) / (kSms * per_sm); };
         if (work(8, 3) < 2) {
             g.rt = 1;
-        } else if (work(16, 2) < 14) {
+        } else if (R <= 16 || work(16, 2) < 14) {
             g.rt = 2;
         } else if (d == 128 || R > 32) {
             g.n_rc = static_cast<int>((R + 47) / 48);
@@ -1214,9 +1215,10 @@ cudaError_t fa_launch_kv4_decode(const Kv4DecodeProblem &p, void *workspace, cud
         const int64_t items = p.B * heads * g.n_rc;
         const int rows = a.R < g.rows ? a.R : g.rows;
         int parts_of_rows = items * 8 <= g.ctas ? rows : 1;
-        // (trees of more than 16 rows, whose sums are in an order of their own: no more blocks than are resident at one time; 1
-        // sequence of 4000, 8 key heads, 48 rows, 23.0 -> 18.5 us for the call, of 30000 42.8 -> 37.0)
-        if (a.tree != nullptr && a.R > 16) parts_of_rows = std::min(parts_of_rows, std::max(1, 4 * kSms / g.ctas));
+        // (trees of more than 8 rows, whose sums are in an order of their own: no more blocks than are resident at one time; 1
+        // sequence of 4000, 8 key heads, 48 rows, 23.0 -> 18.5 us for the call, of 30000 42.8 -> 37.0; 8 of up to 4000, 4 key heads,
+        // 16 rows, 22.6 -> 16.8)
+        if (a.tree != nullptr && a.R > 8) parts_of_rows = std::min(parts_of_rows, std::max(1, 4 * kSms / g.ctas));
         const dim3 grid(static_cast<unsigned>(g.ctas), parts_of_rows);
         e = p.cache.d == 128 ? kv4_launch_behind(fa_kv4_merge_kernel<128>, grid, kMergeWarps * 32, stream, a, g.rows)
                              : kv4_launch_behind(fa_kv4_merge_kernel<64>, grid, kMergeWarps * 32, stream, a, g.rows);

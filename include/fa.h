@@ -574,7 +574,7 @@ int64_t fa_fwd_kv4_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t n_
  *           that admits nothing.
  * The other arguments and the errors are fa_fwd_kv4's without accumulate; the workspace is of
  * fa_fwd_kv4_tree_workspace_bytes(...).  With a chain's masks, (2 << t) - 1, of sequences of n_q tokens and
- * more the result is fa_fwd_kv4's up to rounding, and bit for bit where H / Hkv * n_q is at most 16.
+ * more the result is fa_fwd_kv4's up to rounding, and bit for bit where H / Hkv * n_q is at most 8.
  * The rows of a key head go in chunks of at most 8, 16 or 32, of even ones of at most 48 where there are many and
  * the table has room for many tokens (used or not); its keys are read once per chunk.
  */

@@ -193,9 +193,9 @@ def test_scores_of_any_size(size, d, room):
 
 @gpu
 @rooms
-@pytest.mark.parametrize("d,G,n_q", [(64, 4, 3), (128, 8, 1), (128, 2, 16), (64, 3, 7)])
+@pytest.mark.parametrize("d,G,n_q", [(64, 4, 3), (128, 8, 1), (64, 2, 4), (128, 2, 16), (64, 3, 7)])
 def test_a_chain_gives_the_causal_call(d, G, n_q, room):
-    # bit for bit up to 16 rows a key head; above that in other chunks or another kernel's sums, within the same bounds
+    # bit for bit up to 8 rows a key head; above that in other chunks or another kernel's sums, within the same bounds
     lens = np.array([n_q, 500, 2000, 129, n_q + 1], np.int32)
     rng = np.random.default_rng(n_q)
     pool = Pool(5, 2, d, 32, lens, seed=n_q)
@@ -205,7 +205,7 @@ def test_a_chain_gives_the_causal_call(d, G, n_q, room):
     a = fa.forward_kv4(q, c, dev(lens), table_of(pool, room))
     b = fa.forward_kv4_tree(q, c, dev(lens), table_of(pool, room), chain)
     ok()
-    if G * n_q <= 16:
+    if G * n_q <= 8:
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     for o, lse in (a, b):
         check_tree(pool, q, lens, fa.default_scale(d), chain.cpu().numpy(), None, o, lse)
