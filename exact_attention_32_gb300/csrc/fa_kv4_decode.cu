@@ -1145,7 +1145,7 @@ template <int D, bool SCORES, bool TREE>
 cudaError_t launch_rt(const DecodeArgs &a, int rt, int ctas, cudaStream_t s)
 {
     if (rt == 1) return launch<D, 1, SCORES, TREE>(a, ctas, s);
-    if constexpr (!TREE || D == 64)  // (d = 128: more than 16 rows of a tree go elsewhere)
+    if constexpr (!TREE || D == 64)  // (d = 128: trees go in chunks of 8 or 16, or to the other kernel)
         if (rt == 4) return launch<D, 4, SCORES, TREE>(a, ctas, s);
     return launch<D, 2, SCORES, TREE>(a, ctas, s);
 }

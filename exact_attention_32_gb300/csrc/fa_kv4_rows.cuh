@@ -21,10 +21,9 @@
 // the conversions, the decoded tiles' stores or the exponentials a tile would take 3 % less).
 // Roles (896 threads): warps 0-7 and 8-15 the teams; 16-19 decode K and 20-23 V; 24 loads K's codes and scales, 25 V's; 26 issues S's
 // products and 27 O's (from one warp, in one order, each would wait for what the other waits for: 4000 cycles a tile).
-// Launched with 72 registers a thread, of which the last twelve warps give some to the softmax (80 and 56 in place of 88 and 48: 1
-// to 2 % slower; 72 and 72: 12 %).
+// Launched with 72 registers a thread, of which the last twelve warps give some to the softmax of 48 rows.
 
-constexpr int kRowsLaunchRegs = 72, kRowsSoftmaxRegs = 88, kRowsOtherRegs = 48;
+constexpr int kRowsLaunchRegs = 72;
 // A row's reference is set this far (log2) above what the largest term needs: with the decode kernel's 3 one of 24 rows grew in
 // every sixth tile, at 5000 cycles each time.
 constexpr float kRowsHeadroom = 6.f, kRowsTopLog2 = 15.f, kRowsSumLog2 = 60.f;
@@ -32,11 +31,14 @@ constexpr float kRowsNone = FLT_MAX;  // minus the reference of a row that has m
 // What starting and ending an item costs, in tiles.  48 rows, 32 sequences of up to 8192: 6 134 us, 9 113, 13 104; 32 rows 100, 96,
 // 100; 128 rows 296, 266, 246.
 constexpr int kRowsItemUnits = 12;
-static_assert(4 * kRowsSoftmaxRegs + 3 * kRowsOtherRegs <= 7 * kRowsLaunchRegs, "the warpgroups' shares are what the block has");
 
 template <int D, int NG>
 struct RowCfg {
     static constexpr int N = 16 * NG, NH = 8 * NG;  // rows of a CTA, of a softmax warpgroup
+    // 32 rows: with more for the softmax 100 us in place of 95 (32 sequences of up to 8192).  48 rows: as launched 111 us, this
+    // split 101, others within 1 to 20 % above.
+    static constexpr int kSoftmaxRegs = NG == 3 ? 88 : 72, kDecodeRegs = NG == 3 ? 48 : 72, kOtherRegs = NG == 3 ? 56 : 72;
+    static_assert(4 * kSoftmaxRegs + 2 * kDecodeRegs + kOtherRegs <= 7 * kRowsLaunchRegs, "the warpgroups' shares are what the block has");
     static constexpr int kThreads = 896, kDecodeWarp = 16, kLoadWarp = 24, kMmaWarp = 26, kPvWarp = 27;
     static constexpr int TK = 128;
     static constexpr int kTile = TK * D * 2;
@@ -147,8 +149,8 @@ fa_kv4_rows_kernel(const DecodeArgs a)
     Walk w = start;
     if (tmem_slot[1] == 0) w.left = 0;
 
-    if (warp >= C::kDecodeWarp) {
-        registers_down<kRowsOtherRegs>();
+    if (warp >= C::kLoadWarp) {
+        registers_to<kRowsLaunchRegs, C::kOtherRegs>();
         if (warp == C::kLoadWarp || warp == C::kLoadWarp + 1) {
             // ----------------------------------------------------------------- loads: K, or V and its scales
             const bool values = warp != C::kLoadWarp;
@@ -269,7 +271,10 @@ fa_kv4_rows_kernel(const DecodeArgs a)
             if (elect_one()) mma_commit(BAR(R_DONE + 1));
             __syncwarp();
             mbar_wait_warp(BAR(R_DONE + 1), 0, ok ? kWaitLimitNs : kCleanupLimitNs);
-        } else if (warp < C::kLoadWarp) {
+        }
+    } else if (warp >= C::kDecodeWarp) {
+        registers_to<kRowsLaunchRegs, C::kDecodeRegs>();
+        {
             // ------------------------------------------------ decoding: 32 channels of a key a thread at a time
             constexpr int PPR = D / 32, TURNS = TK * PPR / 128;
             bool ok = true;
@@ -332,7 +337,7 @@ fa_kv4_rows_kernel(const DecodeArgs a)
         }
     } else {
         // --------------------- softmax: warpgroup (team, g) has rows g NH .. g NH + NH - 1 of the team's tiles
-        registers_up<kRowsSoftmaxRegs>();
+        registers_to<kRowsLaunchRegs, C::kSoftmaxRegs>();
         const int wg = warp >> 2, team = wg >> 1, g = wg & 1, wl = warp & 3, tl = tid & 127;  // tl: TMEM lane, the tile's key
         const uint32_t loff = static_cast<uint32_t>(wl * 32) << 16;
         uint8_t *const state = smem + C::kState + wg * C::kStateBytes;

@@ -458,6 +458,13 @@ template <int N>
 __device__ __forceinline__ void registers_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N)); }
 template <int N>
 __device__ __forceinline__ void registers_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
+// From what the block was launched with to N.
+template <int LAUNCHED, int N>
+__device__ __forceinline__ void registers_to()
+{
+    if constexpr (N > LAUNCHED) registers_up<N>();
+    if constexpr (N < LAUNCHED) registers_down<N>();
+}
 
 // ------------------------------------------------------------------- misc
 
