@@ -1053,8 +1053,8 @@ Geometry geometry(int64_t B, int64_t H, int64_t heads, int64_t n_q, int64_t d, i
         // 4000, 4 key heads, 16 rows (0.6) 13.9 and 15.1.
         // Many: the other kernel, whose first tile takes 15 us more and the others less.  8 key heads, 48 rows, d = 128, chunks
         // of 16 and the other kernel: 4 sequences of up to 4000 (11 units) 21.7 and 30.3; 1 of 30000 (18.8) 46.7 and 42.7; 32 of up
-        // to 8192 (169) 160 and 101, 24 rows 101 and 93, 32 rows 108 and 100, 64 rows 186 and 165, 128 rows 350 and 243; d = 64,
-        // 48 rows 124 and 106, 64 rows 140 and 144, 128 rows 268 and 236, but 24 rows (in one chunk of 32) 81 and 89, 32 rows 77
+        // to 8192 (169) 160 and 101, 24 rows 101 and 89, 32 rows 108 and 95, 64 rows 186 and 156, 128 rows 350 and 245; d = 64,
+        // 48 rows 124 and 106, 64 rows 140 and 145, 128 rows 268 and 237, but 24 rows (in one chunk of 32) 81 and 89, 32 rows 77
         // and 82.
         const int64_t tiles = (max_tokens + tile_keys(static_cast<int>(d)) - 1) / tile_keys(static_cast<int>(d));
         auto work = [&](int64_t rows, int64_t per_sm) { return B * heads * ((R + rows - 1) / rows) * (tiles + kItemUnits) / (kSms * per_sm); };
