@@ -642,7 +642,9 @@ cudaError_t launch(const FaPackedProblem &p, int ranks, cudaStream_t stream)
     const int64_t most = (p.T / (PAIR ? 128 : 256) + p.B) * a.units;  // items, whatever the lengths are
     const int64_t grid = SHARED ? most * ranks : most < p.sm_count ? most : p.sm_count;
     auto kern = fa_packed_fwd_kernel<D, CAUSAL, PAIR, SHARED>;
-    if constexpr (SHARED) return launch_with(kern, static_cast<unsigned>(grid), kThreads, C::kSmemBytes, stream, static_cast<unsigned>(ranks), false, mq, mk, mv, mo, a);
+    if constexpr (SHARED)
+        return launch_with(kern, static_cast<unsigned>(grid), kThreads, C::kSmemBytes, stream, static_cast<unsigned>(ranks), false, mq, mk,
+                           mv, mo, a);
     kern<<<static_cast<unsigned>(grid), kThreads, C::kSmemBytes, stream>>>(mq, mk, mv, mo, a);
     return cudaGetLastError();
 }
