@@ -479,7 +479,7 @@ fa_kv4_rows_kernel(const DecodeArgs a)
 #pragma unroll
                     for (int r = 0; r < V; ++r) {
                         const float xr = r < NH ? (r & 1 ? x[r / 8][r / 2 % 4].y : x[r / 8][r / 2 % 4].x) : 0.f;
-                        v[r] = fmaxf(xr - limit, -FLT_MAX);
+                        v[r] = fmaxf(__fsub_ru(xr, limit), -FLT_MAX);  // (up: a reference below x - limit lets P pass a half's range)
                     }
                     const float need = over_lanes<V>(v, [](float p, float q) { return fmaxf(p, q); });
                     if (lane < NH) sm_red[wl * 32 + lane] = need;

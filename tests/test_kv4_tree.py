@@ -191,6 +191,69 @@ def test_scores_of_any_size(size, d, room):
         assert (f64(lse)[b, :, 1:] == -np.inf).all() and (f64(o)[b, :, 1:] == 0).all()
 
 
+V_SCALES = [2.0 ** -17, 2.0 ** -15, 2.0 ** -10, 2.0 ** -9, 0.3125, 0.4375, 0.5, 1.0, 1.75, 12.0, 1024.0, 10240.0]
+# log2 of the largest score's magnitude (log2 units): a step of fp32 is as large as, or larger than, what separates a
+# row's reference from its largest term (3 to 60) from 2^25 on
+SIZES = [-31.2, -29.5, -28.4, -27.6, -26.5, 25.3, 26.5, 27.2, 27.8, 28.3, 28.8, 29.5, 30.5, 60.0]
+
+
+def check_scores_under_v_scales(call, size, d, H, n_q, room, N):
+    """Sequences of N tokens, keys 1, 1, 4 and 4 in every channel of a quarter of them each, V scales of one
+    size or of two in turn; all queries alike, so that log2 scores reach +-2^size: half of the tokens tie and the others
+    weigh nothing.  Their V are a code of at most 6 under the scale, 6 itself once at least."""
+    rng = np.random.default_rng(N)
+    pairs = [(s, s) for s in V_SCALES] + list(zip(V_SCALES, V_SCALES[::-1]))
+    B, P = len(pairs), 16
+    cols = -(-N // P)
+    cache = fa.kv4_cache(B * cols, 1, P, d)
+    key = np.repeat(np.array([1.0, 1.0, 4.0, 4.0]), N // 4)
+    k = bf16(np.tile(key[None, None, :, None], (B, 1, 1, d))).cuda()
+    v = ref.E2M1[rng.integers(0, 8, (B, 1, N, d))] * rng.choice([-1.0, 1.0], (B, 1, N, d))
+    v[..., 0] = 6.0
+    v *= np.array([[p[j % 2] for j in range(N)] for p in pairs])[:, None, :, None]
+    table = np.full((B, max(cols, room // P)), -7, np.int32)
+    table[:, :cols] = np.arange(B * cols).reshape(B, cols)
+    table, lens = dev(table), dev(np.full(B, N, np.int32))
+    fa.kv4_append(cache, k, bf16(v).cuda(), lens, table)
+    ks, vs = (f64(t) for t in fa.kv4_read(cache, lens, table, N))
+    assert (vs == v).all()
+    scale = fa.default_scale(d)
+    q = bf16(np.full((B, H, n_q, d), np.sign(size) * 2.0 ** abs(size) * np.log(2) / ((4 if size > 0 else 1) * d * scale))).cuda()
+    o, lse = call(q, cache, lens, table)
+    ok()
+    s = float(q[0, 0, 0, 0]) * scale * ks[:, 0].sum(-1)  # [B, N]
+    e = np.exp(s - s.max(-1, keepdims=True))
+    want_lse, want = s.max(-1) + np.log(e.sum(-1)), np.einsum("bn,bnd->bd", e / e.sum(-1, keepdims=True), vs[:, 0])
+    o, lse = f64(o), f64(lse)
+    # |lse| to (d + 8) roundings of the sum and the two of its last product.  O to bf16's rounding and P's, of itself (a half's,
+    # 2^-11) and of the smallest step.  P times V's scale is a half that is off by at most 2^-25 near its smallest step.  With many rows:
+    # the row's reference r is at least x - L (x a tie's score, L = 15 - log2 of its V scale), at most one step u of fp32 at x
+    # and 8 (headroom, rounded up to a whole number or a step) above that for the tie it is set by.  u <= 8: that tie's term is
+    # 2^(15 - u - 8) or more; u = 16, where the headroom is lost in x's rounding, 2^(15 - 16): at least 2^-1 both, and 2^-25 is
+    # 2^-24 of it.  u >= 32: r is at most x, so p is a power of two from 1 on, and p times a scale (a multiple of 2^-17) is
+    # exact.  With few rows the largest term is kept between 2^11 and 2^15 and the parts are off by 2^-34 of it.  So a term is off by at
+    # most 2^-24 of the largest, p max(V scale), which after the division by sum p >= p is 2^-24 max(V scale), times a code of
+    # at most 6.
+    assert np.isfinite(o).all() and np.isfinite(lse).all()
+    for b in range(B):
+        assert (np.abs(lse[b] - want_lse[b]) <= (d + 16) * 2.0 ** -23 * np.abs(want_lse[b]) + 1e-6).all(), pairs[b]
+        assert (np.abs(o[b] - want[b]) <= (2.0 ** -8 + 2.0 ** -10) * np.abs(vs[b, 0]).max(0) + 6 * 2.0 ** -24 * max(pairs[b])).all(), pairs[b]
+
+
+def tree_of_alike(q, cache, lens, table):
+    """The newest n_q tokens as drafts that every row admits."""
+    masks = torch.full(q.shape[::2], (1 << q.shape[2]) - 1, dtype=torch.int64, device="cuda")
+    return fa.forward_kv4_tree(q, cache, lens, table, masks)
+
+
+@gpu
+@pytest.mark.parametrize("N", [4, 600])
+@pytest.mark.parametrize("d,H,n_q", [(128, 8, 3), (128, 16, 3), (64, 16, 3)])
+@pytest.mark.parametrize("size", SIZES)
+def test_large_scores_under_any_v_scale_with_many_rows(size, d, H, n_q, N):
+    check_scores_under_v_scales(tree_of_alike, size, d, H, n_q, 1 << 18, N)
+
+
 @gpu
 @rooms
 @pytest.mark.parametrize("d,G,n_q", [(64, 4, 3), (128, 8, 1), (64, 2, 4), (128, 2, 16), (64, 3, 7)])
