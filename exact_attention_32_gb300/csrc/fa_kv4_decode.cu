@@ -642,7 +642,8 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                     }
                 }
                 if (SCORES) sc += TK * a.Rs;
-                // does a key pass its row's maximum, or its term the row's largest?  Soon that is rare.
+                // does a key pass its row's maximum, or its term the row's largest?  Soon that is rare.  (Terms are held against
+                // the largest relative to the maximum: a large score's step may pass a scale's log2.)
                 bool grows = false;
                 float lv[KPT];  // log2 of V's scale
 #pragma unroll
@@ -652,8 +653,8 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                     const float2 m = *reinterpret_cast<const float2 *>(sm_m + 2 * r), top = *reinterpret_cast<const float2 *>(sm_top + 2 * r);
 #pragma unroll
                     for (int k = 0; k < KPT; ++k) {
-                        const float2 z = add2(x[k][r], make_float2(lv[k], lv[k]));
-                        grows |= x[k][r].x > m.x || x[k][r].y > m.y || z.x > top.x || z.y > top.y;
+                        const float2 y = make_float2(x[k][r].x - m.x, x[k][r].y - m.y), z = add2(y, make_float2(lv[k], lv[k]));
+                        grows |= y.x > 0.f || y.y > 0.f || z.x > top.x || z.y > top.y;
                     }
                 }
                 grows = group_or(1 + g, grows);
@@ -664,16 +665,15 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 if (grows) {
                     // O is complete so far, where it will be rescaled, and P's buffers are free
                     if (t > w.t0 && !mbar_wait_warp(pv_bar(n - 1), pv_phase(n - 1), kWaitLimitNs)) *sm_fail = 1.f;
+                    // of the warp's keys, each row's maximum and its largest term over that
 #pragma unroll
                     for (int r = 0; r < 8; ++r) {
                         float v = -FLT_MAX, z = -FLT_MAX;
 #pragma unroll
-                        for (int k = 0; k < KPT; ++k) {
-                            const float xr = r & 1 ? x[k][r / 2].y : x[k][r / 2].x;
-                            v = fmaxf(v, xr);
-                            z = fmaxf(z, xr + lv[k]);
-                        }
+                        for (int k = 0; k < KPT; ++k) v = fmaxf(v, r & 1 ? x[k][r / 2].y : x[k][r / 2].x);
                         v = warp_max(v);
+#pragma unroll
+                        for (int k = 0; k < KPT; ++k) z = fmaxf(z, ((r & 1 ? x[k][r / 2].y : x[k][r / 2].x) - v) + lv[k]);
                         z = warp_max(z);
                         if (lane == 0) *reinterpret_cast<float2 *>(sm_red + (wl * 8 + r) * 2) = make_float2(v, z);
                     }
@@ -683,19 +683,22 @@ fa_kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                         break;
                     }
                     if (tl < 8) {
-                        float v = -FLT_MAX, z = -FLT_MAX;
+                        const float old = sm_m[tl], f = sm_f[tl];
+                        float2 y[4];
+                        float v = old, z = -FLT_MAX;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const float2 y = *reinterpret_cast<const float2 *>(sm_red + (i * 8 + tl) * 2);
-                            v = fmaxf(v, y.x);
-                            z = fmaxf(z, y.y);
+                            y[i] = *reinterpret_cast<const float2 *>(sm_red + (i * 8 + tl) * 2);
+                            v = fmaxf(v, y[i].x);
                         }
-                        const float old = sm_m[tl], top = sm_top[tl], f = sm_f[tl];
-                        v = v > old ? v + kHeadroom : old;
-                        z = z > top ? z + kHeadroom : top;
+                        if (v > old) v += kHeadroom;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) z = fmaxf(z, (y[i].x - v) + y[i].y);
+                        const float rel = (old - v) + sm_top[tl];  // the row's largest term so far
+                        z = z > rel ? z + kHeadroom : rel;
                         const float alpha = ex2(old - v);
                         // the power of two that keeps the terms up to 2^15; held at 2^100 where p itself is next to nothing
-                        const int e = min(max(__float2int_rd((v - z) + 15.f), -100), 100);
+                        const int e = min(max(__float2int_rd(15.f - z), -100), 100);
                         const float now = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
                         sm_m[tl] = v;
                         sm_top[tl] = z;

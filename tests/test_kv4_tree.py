@@ -255,6 +255,16 @@ def test_large_scores_under_any_v_scale_with_many_rows(size, d, H, n_q, N):
 
 
 @gpu
+@pytest.mark.parametrize("N", [4, 600])
+@pytest.mark.parametrize("d,H,n_q,room", [(128, 1, 1, 0), (64, 4, 2, 0), (128, 8, 3, 0), (64, 8, 3, 1 << 18)])
+@pytest.mark.parametrize("size", SIZES)
+def test_large_scores_under_any_v_scale_with_few_rows(size, d, H, n_q, room, N):
+    check_scores_under_v_scales(tree_of_alike, size, d, H, n_q, room, N)
+    if n_q == 1:
+        check_scores_under_v_scales(fa.forward_kv4, size, d, H, n_q, room, N)
+
+
+@gpu
 @rooms
 @pytest.mark.parametrize("d,G,n_q", [(64, 4, 3), (128, 8, 1), (64, 2, 4), (128, 2, 16), (64, 3, 7)])
 def test_a_chain_gives_the_causal_call(d, G, n_q, room):
