@@ -843,7 +843,8 @@ def packed_plan(cu_seqlens: torch.Tensor, tokens: int, causal: bool = False,
     """The plan of a packed batch by ``fa_packed_plan``: made once, for every layer and both directions.
 
     cu_seqlens: int32 [sequences + 1] on a CUDA device, ascending in [0, tokens]; sequence b has the rows
-    cu_seqlens[b] .. cu_seqlens[b + 1] - 1.  The offsets are read on the device, at the call."""
+    cu_seqlens[b] .. cu_seqlens[b + 1] - 1.  The offsets are read on the device, at the call, and are the plan's from then on:
+    new lengths need a new plan, also where their number and their sum are the same."""
     call = (_marshal or _calls()).packed_plan
     table = call(cu_seqlens, tokens, causal) if stream is None else NotImplemented
     if table is NotImplemented:
@@ -859,7 +860,8 @@ def forward_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens
 
     q: bf16 [T, H, d]; k, v: [T, Hkv, d], H a multiple of Hkv, any strides with the last axis contiguous (slices of
     one projection's output).  cu_seqlens: int32 [sequences + 1], the sequences' offsets; ``plan``: packed_plan's
-    for them, made here where None.  Rows of no sequence get O = 0 and LSE = -inf in tensors that the call
+    for them, made here where None.  Given, the plan's own offsets are what counts: of cu_seqlens only the size is
+    looked at, of the plan that it was made for this many sequences and tokens and this ``causal``.  Rows of no sequence get O = 0 and LSE = -inf in tensors that the call
     allocates, and are left alone in ``out`` and ``lse`` where those are given."""
     call = (_marshal or _calls()).forward_packed
     if stream is None:

@@ -597,7 +597,7 @@ extern "C" const char *fa_status_string(int status)
         return "FA_ERR_WORKSPACE_LIMIT: the problem needs more scratch than the static array holds";
     case FA_ERR_BAD_PAGE: return "FA_ERR_BAD_PAGE: a page index or a length lay outside the cache";
     case FA_ERR_BAD_SEQUENCE:
-        return "FA_ERR_BAD_SEQUENCE: offsets of packed sequences do not ascend inside the tensors, or the plan is another batch's";
+        return "FA_ERR_BAD_SEQUENCE: offsets of packed sequences do not ascend inside the tensors, or the plan was made for another B, T or causal";
     default: return "unknown fa_status";
     }
 }

@@ -24,7 +24,7 @@
 namespace {
 
 // Sticky status of this translation unit's kernels: FA_ERR_BAD_SEQUENCE (offsets that do not ascend inside the tensors, or a
-// plan of another batch), FA_ERR_TIMEOUT once a bounded wait gave up (which the other does not overwrite).
+// plan of another T, B or mask), FA_ERR_TIMEOUT once a bounded wait gave up (which the other does not overwrite).
 __device__ int g_packed_status;
 
 __device__ __forceinline__ void packed_bad_sequence() { atomicCAS(&g_packed_status, 0, FA_ERR_BAD_SEQUENCE); }
@@ -67,7 +67,8 @@ __host__ __device__ inline PlanView plan_view(void *plan, int64_t B, int64_t T)
     return v;
 }
 
-// Whether the plan in memory was made for this batch; every length in it then lies inside the tensors.
+// Whether the plan in memory was made for this T, B and mask; every length in it then lies inside the tensors.  (Whether they are this
+// batch's lengths is the caller's to know.)
 __device__ __forceinline__ bool plan_fits(const PlanHead *h, int T, int B, int causal)
 {
     return h->magic == kPlanMagic && h->T == T && h->B == B && h->causal == causal;

@@ -115,7 +115,7 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     const uint32_t sb = smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // The grid has a CTA for every block that the lengths could make; those past the list end here, and all do for a plan
-    // of another batch (which the pre kernel reports); not before the pre kernel, which the post kernel does not wait for.
+    // of another T, B or mask (which the pre kernel reports); not before the pre kernel, which the post kernel does not wait for.
     // (The post kernel is not let in early from here: its blocks, waiting beside the last CTAs, took 1017 us in place of 988.)
     const bool fits = plan_fits(a.plan.head, a.T, a.B, CAUSAL);
     const int n_blocks = fits ? a.plan.head->n_blocks : 0;

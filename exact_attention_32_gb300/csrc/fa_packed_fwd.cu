@@ -197,7 +197,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
-    // a plan of another batch, or a wait that gave up and nobody has read so yet: nothing is done (one thread asks: the
+    // a plan of another T, B or mask, or a wait that gave up and nobody has read so yet: nothing is done (one thread asks: the
     // status may change while a block starts, and its roles have to agree)
     if (tid == 0) {
         const bool fits = plan_fits(a.plan.head, a.T, a.B, CAUSAL);

@@ -50,7 +50,7 @@ enum fa_status {
     FA_ERR_BAD_PAGE = 8, /* reported by fa_get_device_status: a kernel met a page index or a
                            length outside its 4-bit cache and left that part out */
     FA_ERR_BAD_SEQUENCE = 9 /* reported by fa_get_device_status: offsets of packed sequences that do
-                           not ascend inside the tensors, or a plan made for another batch */
+                           not ascend inside the tensors, or a plan made for another B, T or causal */
 };
 
 /* Size of the library-owned scratch array behind fa_fwd_splitkv_noalloc. */
@@ -406,8 +406,10 @@ typedef struct fa_rows {
  *   B, T       : sequences and rows, 1 .. 2^31 - 512
  *   plan       : device memory, 16-byte aligned, fa_packed_plan_bytes(B, T) bytes at least
  * Calls that take the plan must be ordered behind this one, with the same B, T and causal (a
- * plan of another batch is noticed by the kernels, which then do nothing and report
- * FA_ERR_BAD_SEQUENCE).
+ * plan made for others is noticed by the kernels, which then do nothing and report
+ * FA_ERR_BAD_SEQUENCE).  The offsets are the plan's: those calls do not get them, so a batch of
+ * the same B and T with other lengths needs a plan of its own, and with an old one its rows
+ * attend as the old lengths say.
  */
 int fa_packed_plan(const int32_t *cu_seqlens, int64_t B, int64_t T, int causal, void *plan, int64_t plan_bytes,
                    void *stream);

@@ -343,6 +343,21 @@ def test_a_plan_of_another_batch_does_nothing_and_is_reported():
 
 
 @gpu
+def test_a_plan_holds_its_own_offsets():
+    # of the same number of sequences and rows: the plan's lengths are what counts, as its documentation says, in both directions
+    q, k, v, cu = batch([100, 28], 4, 2, 64, seed=53)
+    a, other = [t.cuda() for t in (q, k, v)], [0, 30, 128]
+    plan = fa.packed_plan(dev_cu(other), 128, causal=True)
+    o, lse = fa.forward_packed(*a, dev_cu(cu), causal=True, plan=plan)
+    want = fa.forward_packed(*a, dev_cu(other), causal=True)
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    check_forward(o.cpu(), lse.cpu(), q, k, v, np.array(other), fa.default_scale(64), True)
+    got = fa.backward_packed(*a, o, lse, a[0], dev_cu(cu), causal=True, plan=plan)
+    ok()
+    check_backward(got, q, k, v, o, lse, q, np.array(other), fa.default_scale(64), True)
+
+
+@gpu
 @pytest.mark.parametrize("cu,held", [([0, 50, 40, 100], [0, 50, 50, 100]), ([-5, 30, 60, 90], [0, 30, 60, 90]),
                                      ([0, 30, 60, 500], [0, 30, 60, 100]), ([0, 2 ** 31 - 1, 60, 100], [0, 100, 100, 100]),
                                      ([200, 300, -300, 5], [100, 100, 100, 100])])
