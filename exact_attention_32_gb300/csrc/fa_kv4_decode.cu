@@ -1039,12 +1039,38 @@ struct Geometry {
     int64_t part_o, part_ml, split, scores, row_ml, total;  // byte offsets in the workspace
 };
 
+// The CTAs and the workspace's layout of items of g.n_rc chunks of g.rows rows.
+void lay_out(Geometry &g, int64_t B, int64_t H, int64_t heads, int64_t n_q, int64_t d, int64_t max_tokens, int accumulate)
+{
+    const int64_t R = H / heads * n_q, rows = B * H * n_q;
+    const int64_t tk = g.ng > 0 ? 128 : tile_keys(static_cast<int>(d));
+    const int64_t items = B * heads * g.n_rc, tiles = (max_tokens + tk - 1) / tk;
+    g.whole = tiles <= kWholeTiles;
+    g.Rs = static_cast<int>(R <= 2 ? R : (R + 3) / 4 * 4);
+    const int64_t ctas = kSms * (g.ng > 0 ? 1 : g.rt == 1 ? 3 : g.rt == 2 ? 2 : 1);
+    const int64_t need = g.whole ? items : (items * (tiles + (g.ng > 0 ? kRowsItemUnits : kItemUnits)) + kMinShare - 1) / kMinShare;
+    g.ctas = static_cast<int>(need < ctas ? need : ctas);
+    auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
+    int64_t at = 0;
+    g.part_o = at;
+    at = up(at + g.ctas * 2 * g.rows * d * 4);
+    g.part_ml = at;
+    at = up(at + g.ctas * 2 * g.rows * 8);
+    g.split = at;
+    at = up(at + g.ctas * static_cast<int64_t>(sizeof(Split)));
+    g.scores = at;
+    if (accumulate) at = up(at + B * heads * g.Rs * max_tokens * 4);
+    g.row_ml = at;
+    if (accumulate) at = up(at + rows * 8);
+    g.total = at;
+}
+
 // tree: for fa_fwd_kv4_tree, whose items of many rows a key head go to fa_kv4_rows_kernel (g.ng > 0) or, where there is little work,
 // in smaller chunks.  Up to 8 rows it has the chain's chunks and shares, and so its bits.
 Geometry geometry(int64_t B, int64_t H, int64_t heads, int64_t n_q, int64_t d, int64_t max_tokens, int accumulate, bool tree)
 {
     Geometry g;
-    const int64_t R = H / heads * n_q, rows = B * H * n_q;
+    const int64_t R = H / heads * n_q;
     g.ng = 0;
     // 32 sequences of 8192, 4 key heads: a chunk of 16 rows takes 39 to 41 us among others, one of 32 74 (32 rows in one CTA 85, in
     // two of 16 89; 40 rows in two of 32 144, in three of 16 123; 1 key head: 80 rows 67 and 62, 96 rows 67 and 71, 176 even)
@@ -1072,27 +1098,31 @@ Geometry geometry(int64_t B, int64_t H, int64_t heads, int64_t n_q, int64_t d, i
     }
     if (g.ng == 0) g.n_rc = static_cast<int>((R + 8 * g.rt - 1) / (8 * g.rt));
     g.rows = g.ng > 0 ? 16 * g.ng : 8 * g.rt;
-    const int64_t tk = g.ng > 0 ? 128 : tile_keys(static_cast<int>(d));
-    const int64_t items = B * heads * g.n_rc, tiles = (max_tokens + tk - 1) / tk;
-    g.whole = tiles <= kWholeTiles;
-    g.Rs = static_cast<int>(R <= 2 ? R : (R + 3) / 4 * 4);
-    const int64_t ctas = kSms * (g.ng > 0 ? 1 : g.rt == 1 ? 3 : g.rt == 2 ? 2 : 1);
-    const int64_t need = g.whole ? items : (items * (tiles + (g.ng > 0 ? kRowsItemUnits : kItemUnits)) + kMinShare - 1) / kMinShare;
-    g.ctas = static_cast<int>(need < ctas ? need : ctas);
-    auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
-    int64_t at = 0;
-    g.part_o = at;
-    at = up(at + g.ctas * 2 * g.rows * d * 4);
-    g.part_ml = at;
-    at = up(at + g.ctas * 2 * g.rows * 8);
-    g.split = at;
-    at = up(at + g.ctas * static_cast<int64_t>(sizeof(Split)));
-    g.scores = at;
-    if (accumulate) at = up(at + B * heads * g.Rs * max_tokens * 4);
-    g.row_ml = at;
-    if (accumulate) at = up(at + rows * 8);
-    g.total = at;
+    lay_out(g, B, H, heads, n_q, d, max_tokens, accumulate);
     return g;
+}
+
+// Bytes for fa_fwd_kv4_tree with at most so many sequences, drafts and tokens of a table: the most over the forms that geometry
+// may choose for any such call.  (Of each the CTAs grow with the items and the tiles, up to what the SMs hold; it is the choice
+// that does not: 6 drafts of 32 heads on 8, d = 128, tables of 8192, go in chunks of 16 rows for 3 sequences, of 32 for 16, in less.)
+int64_t tree_workspace(int64_t B, int64_t H, int64_t heads, int64_t n_q, int64_t d, int64_t max_tokens)
+{
+    const int64_t R = H / heads * n_q;
+    int64_t most = 0;
+    auto form = [&](int rt, int ng, int rows) {
+        Geometry g;
+        g.rt = rt;
+        g.ng = ng;
+        g.rows = rows;
+        g.n_rc = static_cast<int>((R + rows - 1) / rows);
+        lay_out(g, B, H, heads, n_q, d, max_tokens, 0);
+        most = std::max(most, g.total);
+    };
+    form(1, 0, 8);
+    if (R > 8) form(2, 0, 16);
+    if (R > 16 && d == 64) form(4, 0, 32);
+    if (R > 16 && (d == 128 || R > 32)) form(4, 3, 48);  // (in even chunks of at most 48)
+    return most;
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -1177,7 +1207,7 @@ cudaError_t launch_kind(const DecodeArgs &a, int rt, int ng, int ctas, cudaStrea
 int64_t fa_kv4_decode_workspace(int64_t B, int64_t H, int64_t heads, int64_t n_q, int64_t d, int64_t max_tokens,
                                 int accumulate, bool tree)
 {
-    return geometry(B, H, heads, n_q, d, max_tokens, accumulate, tree).total;
+    return tree ? tree_workspace(B, H, heads, n_q, d, max_tokens) : geometry(B, H, heads, n_q, d, max_tokens, accumulate, false).total;
 }
 
 cudaError_t fa_launch_kv4_decode(const Kv4DecodeProblem &p, void *workspace, cudaStream_t stream)

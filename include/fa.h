@@ -585,7 +585,7 @@ int fa_fwd_kv4_tree(const void *q, const fa_kv4_cache *cache, const int32_t *len
                     int64_t n_q, int64_t max_pages, float scale, void *workspace, int64_t workspace_bytes,
                     void *stream);
 
-/* Workspace bytes fa_fwd_kv4_tree needs for sequences of at most max_tokens =
+/* Workspace bytes fa_fwd_kv4_tree needs for at most B sequences of at most n_q drafts and max_tokens =
  * max_pages * page_size tokens, or -1 for invalid sizes.  Pure host computation. */
 int64_t fa_fwd_kv4_tree_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t n_q, int64_t d,
                                         int64_t max_tokens);

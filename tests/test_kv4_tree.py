@@ -89,6 +89,25 @@ def test_bad_arguments_are_refused_before_any_device_call():
     assert fa.fa_kv4_copy_pages(big, p, big, p, 1, 0) == 1
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H,Hkv", [(32, 8), (8, 8), (8, 1), (6, 2), (64, 4)])
+def test_a_workspace_of_the_largest_call_serves_every_smaller_one(H, Hkv, d):
+    # a server allocates for its largest batch, table and number of drafts
+    def need(B, n_q, tokens):
+        return fa.fa_fwd_kv4_tree_workspace_bytes(B, H, Hkv, n_q, d, tokens)
+    Bs, drafts = [1, 2, 3, 5, 8, 16, 40, 200], [1, 2, 3, 4, 6, 8, 9, 12, 16, 31, 32, 48, 64]
+    drafts, rooms = [n for n in drafts if H // Hkv * n <= 1024], [16, 256, 512, 528, 640, 1040, 4000, 8192, 40000, 262144]
+    all_of = {(B, n, t): need(B, n, t) for B in Bs for n in drafts for t in rooms}
+    assert all(x > 0 for x in all_of.values())
+    for (B, n, t), x in all_of.items():
+        for up in ((Bs, 0, B), (drafts, 1, n), (rooms, 2, t)):
+            at = up[0].index(up[2])
+            if at + 1 < len(up[0]):
+                larger = [B, n, t]
+                larger[up[1]] = up[0][at + 1]
+                assert x <= all_of[tuple(larger)], ((B, n, t), larger)
+
+
 def test_python_calls_refuse_wrong_tensors():
     c = fa.kv4_cache(4, 2, 16, 64, device="cpu")
     i = torch.zeros(1, dtype=torch.int32)
@@ -313,6 +332,25 @@ def test_masks_are_taken_as_they_are(d, G, room):
         live = r["lse"][:, check] > -np.inf
         assert np.abs(f64(lse)[b][:, check][live] - r["lse"][:, check][live]).max() <= 1e-4
         assert np.abs(f64(o)[b][:, check] - r["o"][:, check]).max() <= 2.0 ** -6 * np.abs(v).max()
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_tree_in_the_workspace_of_a_larger_batch(d):
+    # and no byte behind it is touched, of a small batch's chunks and of a large one's
+    H, Hkv, n_q, room, P = 32, 8, 6, 8192, 64
+    need = fa.fa_fwd_kv4_tree_workspace_bytes(16, H, Hkv, n_q, d, room)
+    ws = torch.full((need + 4096,), 171, dtype=torch.uint8, device="cuda")
+    for B in (3, 16):
+        lens = np.array([200, 9, 700, 0, 64] * 4, np.int32)[:B]
+        rng = np.random.default_rng(B + d)
+        pool = Pool(B, Hkv, d, P, lens, seed=B + d)
+        q = bf16(rng.standard_normal((B, H, n_q, d))).cuda()
+        _, masks = random_tree(rng, B, n_q)
+        o, lse = fa.forward_kv4_tree(q, pool.cache(), dev(lens), table_of(pool, room), dev(masks), workspace=ws[:need])
+        ok()
+        check_tree(pool, q, lens, fa.default_scale(d), masks, None, o, lse)
+    assert (ws[need:] == 171).all()
 
 
 @gpu
