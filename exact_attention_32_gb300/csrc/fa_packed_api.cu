@@ -9,8 +9,12 @@
 namespace {
 
 constexpr int64_t kMost = (int64_t(1) << 31) - 512;  // rows: a tile past the last one still has a 31-bit number
+constexpr int64_t kMostSequences = (int64_t(1) << 31) - 2048;  // which the plan's block takes 1024 at a time, numbered likewise
 
-int check_batch(int64_t B, int64_t T) { return B >= 1 && T >= 1 && B <= kMost && T <= kMost ? FA_OK : FA_ERR_INVALID_ARG; }
+int check_batch(int64_t B, int64_t T)
+{
+    return B >= 1 && T >= 1 && B <= kMostSequences && T <= kMost ? FA_OK : FA_ERR_INVALID_ARG;
+}
 
 int check_sizes(int64_t B, int64_t T, int64_t H, int64_t Hkv, int64_t d)
 {

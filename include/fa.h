@@ -403,7 +403,7 @@ typedef struct fa_rows {
  *                cu_seqlens[B] on belong to no sequence.  The offsets must ascend inside [0, T];
  *                others are held to that (each to at least the ones before) and reported as
  *                FA_ERR_BAD_SEQUENCE by fa_get_device_status.
- *   B, T       : sequences and rows, 1 .. 2^31 - 512
+ *   B, T       : sequences, 1 .. 2^31 - 2048, and rows, 1 .. 2^31 - 512
  *   plan       : device memory, 16-byte aligned, fa_packed_plan_bytes(B, T) bytes at least
  * Calls that take the plan must be ordered behind this one, with the same B, T and causal (a
  * plan made for others is noticed by the kernels, which then do nothing and report

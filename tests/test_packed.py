@@ -182,6 +182,16 @@ def test_plan_sizes():
     assert fa.fa_packed_plan(16, 3, 1000, 0, 16, n - 1, 0) == 1 and fa.fa_packed_plan(16, 3, 1000, 2, 16, n, 0) == 1
 
 
+def test_the_largest_number_of_sequences():
+    # the plan goes 1024 of them at a time, and the number behind the last ones has to fit 31 bits
+    most = (1 << 31) - 2048
+    assert fa.fa_packed_plan_bytes(most, 1) == 128 + 16 * 3 * most
+    for B in (most + 1, (1 << 31) - 1024, (1 << 31) - 1023, (1 << 31) - 512):
+        assert fa.fa_packed_plan_bytes(B, 1) == -1 and fa.fa_packed_plan(16, B, 1, 0, 16, 1 << 50, 0) == 1
+        assert fa.fa_bwd_packed_workspace_bytes(B, 1, 1, 1, 64) == -1
+    assert fa.fa_packed_plan_bytes(1, (1 << 31) - 512) > 0 and fa.fa_packed_plan_bytes(1, (1 << 31) - 511) == -1
+
+
 def test_python_calls_refuse_wrong_tensors():
     q, k, cu = torch.zeros(4, 2, 64).bfloat16(), torch.zeros(4, 1, 64).bfloat16(), torch.zeros(2, dtype=torch.int32)
     for bad in (lambda: fa.forward_packed(q, k, k, cu), lambda: fa.forward_packed(1, k, k, cu), lambda: fa.packed_plan(cu, 4),
