@@ -572,6 +572,24 @@ def backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
     return dq, dk, dv
 
 
+class _Once(torch.autograd.Function):
+    """(dq, dk, dv) as they are, behind what they were made from: the kernels' results are constants to autograd, so a
+    second derivative through them raises in place of leaving that part out.  (torch's once_differentiable goes by the
+    incoming gradient alone, and that of a plain sum needs no gradient itself.)"""
+
+    @staticmethod
+    def forward(ctx, dq, dk, dv, *sources):
+        return dq.detach(), dk.detach(), dv.detach()
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("attention's gradients have no second derivative")
+
+
+def _once(grads, *sources):
+    return _Once.apply(*grads, *sources) if torch.is_grad_enabled() else grads
+
+
 class _Attention(torch.autograd.Function):
     """fa_fwd in the forward, fa_bwd in the backward (O and LSE saved)."""
 
@@ -585,14 +603,14 @@ class _Attention(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dout):
         q, k, v, o, lse = ctx.saved_tensors
-        dq, dk, dv = backward(q, k, v, o, lse, dout.contiguous(), scale=ctx.scale, causal=ctx.causal)
-        return dq, dk, dv, None, None
+        grads = backward(q, k, v, o, lse, dout.contiguous(), scale=ctx.scale, causal=ctx.causal)
+        return (*_once(grads, q, k, v, dout), None, None)
 
 
 def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: float | None = None,
               causal: bool = False) -> torch.Tensor:
     """O = attention(q, k, v) with autograd: ``fa_fwd`` forward, ``fa_bwd``
-    backward (dQ, dK, dV of the loss through O).  q, k, v: contiguous bf16
+    backward (dQ, dK, dV of the loss through O; once: a second derivative is refused).  q, k, v: contiguous bf16
     CUDA tensors [B, H, N, d] (d = 64 or 128)."""
     return _Attention.apply(q, k, v, default_scale(q.shape[-1]) if scale is None else scale, bool(causal))
 
@@ -906,11 +924,11 @@ class _AttentionPacked(torch.autograd.Function):
         q, k, v, o, lse, cu_seqlens, table = ctx.saved_tensors
         grads = backward_packed(q, k, v, o, lse, dout.contiguous(), cu_seqlens, scale=ctx.scale, causal=ctx.causal,
                                 plan=PackedPlan(table, *ctx.plan))
-        return (*grads, None, None, None, None)
+        return (*_once(grads, q, k, v, dout), None, None, None, None)
 
 
 def attention_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
                      scale: float | None = None, causal: bool = False, plan: PackedPlan | None = None) -> torch.Tensor:
-    """O = ``forward_packed``'s with autograd: ``fa_fwd_packed`` forward, ``fa_bwd_packed`` backward.  A plan that
-    several layers share is made once with ``packed_plan`` and given."""
+    """O = ``forward_packed``'s with autograd: ``fa_fwd_packed`` forward, ``fa_bwd_packed`` backward
+    (once: a second derivative is refused).  A plan that several layers share is made once with ``packed_plan`` and given."""
     return _AttentionPacked.apply(q, k, v, cu_seqlens, scale, bool(causal), plan)

@@ -1,0 +1,34 @@
+"""Autograd of attention() and attention_packed() on the CPU, their kernels' calls replaced by stand-ins of the same shapes."""
+import pytest
+import torch
+
+import exact_attention_32_gb300 as fa
+from exact_attention_32_gb300 import _binding
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_a_second_derivative_is_refused(packed, monkeypatch):
+    # the kernels' gradients are constants to autograd: a loss that holds them beside other terms would lose its derivative
+    # through them without a word
+    def forward(q, k, v, *a, **kw):
+        return q.clone(), q.new_zeros(1)
+
+    def backward(q, k, v, o, lse, dout, *a, **kw):
+        return dout.clone(), dout.clone(), dout.clone()
+
+    for name in ("forward", "forward_packed"):
+        monkeypatch.setattr(_binding, name, forward)
+    for name in ("backward", "backward_packed"):
+        monkeypatch.setattr(_binding, name, backward)
+    monkeypatch.setattr(_binding, "packed_plan", lambda cu, T, causal: _binding.PackedPlan(torch.zeros(1), T, 1, causal))
+    q = torch.randn(*((4, 1, 64) if packed else (1, 1, 4, 64)), requires_grad=True)
+
+    def out():
+        return fa.attention_packed(q, q, q, torch.tensor([0, 4])) if packed else fa.attention(q, q, q)
+
+    once, = torch.autograd.grad(out().sum(), q)
+    assert (once == 3).all()  # (q's, k's and v's)
+    g, = torch.autograd.grad(out().sum(), q, create_graph=True)
+    assert (g == 3).all()
+    with pytest.raises(RuntimeError, match="second derivative"):
+        (g.sum() + (q * q).sum()).backward()
