@@ -590,6 +590,12 @@ def _once(grads, *sources):
     return _Once.apply(*grads, *sources) if torch.is_grad_enabled() else grads
 
 
+def _laid_out(dout):
+    """An output's gradient as the kernels take it.  (Behind a concatenation it may be a contiguous view at any offset.)"""
+    dout = dout.contiguous()
+    return dout if dout.data_ptr() % 16 == 0 else dout.clone()
+
+
 class _Attention(torch.autograd.Function):
     """fa_fwd in the forward, fa_bwd in the backward (O and LSE saved)."""
 
@@ -603,7 +609,7 @@ class _Attention(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dout):
         q, k, v, o, lse = ctx.saved_tensors
-        grads = backward(q, k, v, o, lse, dout.contiguous(), scale=ctx.scale, causal=ctx.causal)
+        grads = backward(q, k, v, o, lse, _laid_out(dout), scale=ctx.scale, causal=ctx.causal)
         return (*_once(grads, q, k, v, dout), None, None)
 
 
@@ -922,7 +928,7 @@ class _AttentionPacked(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dout):
         q, k, v, o, lse, cu_seqlens, table = ctx.saved_tensors
-        grads = backward_packed(q, k, v, o, lse, dout.contiguous(), cu_seqlens, scale=ctx.scale, causal=ctx.causal,
+        grads = backward_packed(q, k, v, o, lse, _laid_out(dout), cu_seqlens, scale=ctx.scale, causal=ctx.causal,
                                 plan=PackedPlan(table, *ctx.plan))
         return (*_once(grads, q, k, v, dout), None, None, None, None)
 
