@@ -8,6 +8,7 @@
 
 #include "fa.h"
 #include "fa_internal.h"
+#include "fa_status.h"
 
 namespace {
 
@@ -567,20 +568,12 @@ extern "C" int fa_get_device_status(void *stream)
         cudaGetLastError();
         return FA_ERR_LAUNCH;
     }
-    const int fwd = fa_tc_take_status(static_cast<cudaStream_t>(stream));
-    const int dp = fa_dp_take_status(static_cast<cudaStream_t>(stream));
-    const int bwd = fa_bwd_take_status(static_cast<cudaStream_t>(stream));
-    const int weights = fa_key_weights_take_status(static_cast<cudaStream_t>(stream));
-    const int decode = fa_kv4_decode_take_status(static_cast<cudaStream_t>(stream));
-    const int cache = fa_kv4_cache_take_status(static_cast<cudaStream_t>(stream));
-    const int move = fa_kv4_move_take_status(static_cast<cudaStream_t>(stream));
-    const int plan = fa_packed_plan_take_status(static_cast<cudaStream_t>(stream));
-    const int packed_fwd = fa_packed_fwd_take_status(static_cast<cudaStream_t>(stream));
-    const int packed_bwd = fa_packed_bwd_take_status(static_cast<cudaStream_t>(stream));
-    // (the packed kernels' own before the plan's: a wait that gave up counts for more than offsets)
-    for (const int st : {fwd, dp, bwd, weights, decode, cache, move, packed_fwd, packed_bwd})
-        if (st != FA_OK) return st;
-    return plan;
+    int words[10], n = 0;
+    for (const auto take : {fa_tc_take_status, fa_dp_take_status, fa_bwd_take_status, fa_key_weights_take_status, fa_kv4_decode_take_status,
+                            fa_kv4_cache_take_status, fa_kv4_move_take_status, fa_packed_fwd_take_status, fa_packed_bwd_take_status,
+                            fa_packed_plan_take_status})
+        words[n++] = take(static_cast<cudaStream_t>(stream));
+    return fa_joined_status(words, n);
 }
 
 extern "C" const char *fa_status_string(int status)

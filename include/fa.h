@@ -666,7 +666,8 @@ int fa_key_weights(const void *q, const void *k, const float *lse, float *weight
  * current device's sticky in-kernel status (FA_OK, or FA_ERR_TIMEOUT when a
  * bounded wait inside a kernel gave up and the kernel returned early, leaving
  * its outputs incomplete; or FA_ERR_BAD_PAGE, see the 4-bit cache; or
- * FA_ERR_BAD_SEQUENCE, see packed sequences).  While
+ * FA_ERR_BAD_SEQUENCE, see packed sequences; FA_ERR_TIMEOUT where several kernels
+ * reported and one of them so).  While
  * FA_ERR_TIMEOUT is set, fa_fwd, fa_fwd_packed, fa_fwd_kv4 and fa_fwd_kv4_tree launches do no work (their
  * outputs are left unwritten), and fa_bwd_packed leaves out its products (what it writes means nothing),
  * until this call clears it; a fa_fwd_kv4 call in which a wait gave up adds nothing to the cache's weights.
