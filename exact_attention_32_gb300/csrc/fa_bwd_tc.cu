@@ -625,15 +625,4 @@ cudaError_t fa_launch_bwd(const FaBwdProblem &p, void *workspace, cudaStream_t s
     }
 }
 
-int fa_bwd_take_status(cudaStream_t stream)
-{
-    int h = 0;
-    const int zero = 0;
-    if (cudaMemcpyFromSymbolAsync(&h, g_bwd_status, sizeof(int), 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
-        cudaMemcpyToSymbolAsync(g_bwd_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, stream) != cudaSuccess ||
-        cudaStreamSynchronize(stream) != cudaSuccess) {
-        cudaGetLastError();
-        return FA_ERR_LAUNCH;
-    }
-    return h;
-}
+int fa_bwd_take_status(cudaStream_t stream) { return fa_take_status_word(g_bwd_status, stream); }

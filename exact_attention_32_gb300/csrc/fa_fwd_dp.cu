@@ -495,15 +495,4 @@ cudaError_t fa_launch_fp8(const FaProblem &p, const float *qs, const float *ks, 
     return p.causal ? launch_dp<true, true>(p, stream, qs, ks, vs) : launch_dp<false, true>(p, stream, qs, ks, vs);
 }
 
-int fa_dp_take_status(cudaStream_t stream)
-{
-    int h = 0;
-    const int zero = 0;
-    if (cudaMemcpyFromSymbolAsync(&h, g_dp_status, sizeof(int), 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
-        cudaMemcpyToSymbolAsync(g_dp_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, stream) != cudaSuccess ||
-        cudaStreamSynchronize(stream) != cudaSuccess) {
-        cudaGetLastError();
-        return FA_ERR_LAUNCH;
-    }
-    return h;
-}
+int fa_dp_take_status(cudaStream_t stream) { return fa_take_status_word(g_dp_status, stream); }

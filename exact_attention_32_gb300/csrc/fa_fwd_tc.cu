@@ -885,15 +885,4 @@ cudaError_t fa_launch_tc_sparse(const FaProblem &p, const uint8_t *block_mask, c
                     : launch<128, false, false, true>(p, p.o, p.lse, 1, N, stream, block_mask);
 }
 
-int fa_tc_take_status(cudaStream_t stream)
-{
-    int h = 0;
-    const int zero = 0;
-    if (cudaMemcpyFromSymbolAsync(&h, g_tc_status, sizeof(int), 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
-        cudaMemcpyToSymbolAsync(g_tc_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, stream) != cudaSuccess ||
-        cudaStreamSynchronize(stream) != cudaSuccess) {
-        cudaGetLastError();
-        return FA_ERR_LAUNCH;
-    }
-    return h;
-}
+int fa_tc_take_status(cudaStream_t stream) { return fa_take_status_word(g_tc_status, stream); }

@@ -6,6 +6,8 @@
 
 #include <atomic>
 
+#include "fa.h"
+
 // cudaFuncSetAttribute(Kernel, MaxDynamicSharedMemorySize, bytes), made once per
 // kernel and device (bit d of `done` records device d) instead of on every launch.
 template <auto Kernel>
@@ -19,6 +21,22 @@ cudaError_t set_max_dynamic_smem(int bytes)
     const cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == cudaSuccess && bit != 0) done.fetch_or(bit, std::memory_order_release);
     return e;
+}
+
+// Reads a translation unit's status word (a __device__ int) behind what `stream` holds, and clears it if it says something.
+template <typename Word>
+int fa_take_status_word(const Word &word, cudaStream_t stream)
+{
+    int h = 0;
+    const int zero = 0;
+    if (cudaMemcpyFromSymbolAsync(&h, word, sizeof(int), 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
+        cudaStreamSynchronize(stream) != cudaSuccess ||
+        (h != 0 && (cudaMemcpyToSymbolAsync(word, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, stream) != cudaSuccess ||
+                    cudaStreamSynchronize(stream) != cudaSuccess))) {
+        cudaGetLastError();
+        return FA_ERR_LAUNCH;
+    }
+    return h;
 }
 
 // Size rules shared by the entry points (pure host logic, no CUDA call):

@@ -452,17 +452,4 @@ cudaError_t fa_launch_key_weights(const FaKeyWeightsProblem &p, cudaStream_t s)
     return p.causal ? launch_kw<128, true>(p, s) : launch_kw<128, false>(p, s);
 }
 
-int fa_key_weights_take_status(cudaStream_t stream)
-{
-    int h = 0;
-    const int zero = 0;
-    if (cudaMemcpyFromSymbolAsync(&h, g_key_weights_status, sizeof(int), 0, cudaMemcpyDeviceToHost, stream) !=
-            cudaSuccess ||
-        cudaMemcpyToSymbolAsync(g_key_weights_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, stream) !=
-            cudaSuccess ||
-        cudaStreamSynchronize(stream) != cudaSuccess) {
-        cudaGetLastError();
-        return FA_ERR_LAUNCH;
-    }
-    return h;
-}
+int fa_key_weights_take_status(cudaStream_t stream) { return fa_take_status_word(g_key_weights_status, stream); }

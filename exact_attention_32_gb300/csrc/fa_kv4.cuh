@@ -27,19 +27,6 @@ __device__ int g_kv4_status;
 
 __device__ __forceinline__ void kv4_report() { atomicCAS(&g_kv4_status, 0, FA_ERR_BAD_PAGE); }
 
-int kv4_take_status_here(cudaStream_t stream)
-{
-    int h = 0;
-    const int zero = 0;
-    if (cudaMemcpyFromSymbolAsync(&h, g_kv4_status, sizeof(int), 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
-        cudaMemcpyToSymbolAsync(g_kv4_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, stream) != cudaSuccess ||
-        cudaStreamSynchronize(stream) != cudaSuccess) {
-        cudaGetLastError();
-        return FA_ERR_LAUNCH;
-    }
-    return h;
-}
-
 // Length of sequence b, held inside [0, capacity]; a length outside is reported.
 __device__ __forceinline__ int kv4_length(const int32_t *lens, int64_t b, int64_t capacity)
 {

@@ -464,4 +464,4 @@ cudaError_t fa_launch_kv4_evict(const Kv4EvictProblem &p, cudaStream_t stream)
                              p.to_table, p.to_max_pages, p.kept, rows, static_cast<int>(p.keep));
 }
 
-int fa_kv4_cache_take_status(cudaStream_t stream) { return kv4_take_status_here(stream); }
+int fa_kv4_cache_take_status(cudaStream_t stream) { return fa_take_status_word(g_kv4_status, stream); }

@@ -1271,4 +1271,4 @@ cudaError_t fa_launch_kv4_decode(const Kv4DecodeProblem &p, void *workspace, cud
     return cudaSuccess;
 }
 
-int fa_kv4_decode_take_status(cudaStream_t stream) { return kv4_take_status_here(stream); }
+int fa_kv4_decode_take_status(cudaStream_t stream) { return fa_take_status_word(g_kv4_status, stream); }

@@ -157,4 +157,4 @@ cudaError_t fa_launch_kv4_copy(const Kv4Cache &from, const int32_t *pages, const
     return cudaGetLastError();
 }
 
-int fa_kv4_move_take_status(cudaStream_t stream) { return kv4_take_status_here(stream); }
+int fa_kv4_move_take_status(cudaStream_t stream) { return fa_take_status_word(g_kv4_status, stream); }

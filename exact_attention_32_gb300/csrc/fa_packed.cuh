@@ -30,19 +30,6 @@ __device__ int g_packed_status;
 __device__ __forceinline__ void packed_bad_sequence() { atomicCAS(&g_packed_status, 0, FA_ERR_BAD_SEQUENCE); }
 __device__ __forceinline__ void packed_timeout() { atomicExch(&g_packed_status, FA_ERR_TIMEOUT); }
 
-inline int packed_take_status_here(cudaStream_t stream)
-{
-    int h = 0;
-    const int zero = 0;
-    if (cudaMemcpyFromSymbolAsync(&h, g_packed_status, sizeof(int), 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
-        cudaMemcpyToSymbolAsync(g_packed_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, stream) != cudaSuccess ||
-        cudaStreamSynchronize(stream) != cudaSuccess) {
-        cudaGetLastError();
-        return FA_ERR_LAUNCH;
-    }
-    return h;
-}
-
 struct PlanHead {
     int magic, T, B, causal;
     int n_blocks, n_pairs;  // entries of the two lists

@@ -709,4 +709,4 @@ cudaError_t fa_launch_packed_bwd(const FaPackedProblem &p, void *workspace, cuda
     return a.ranks > 1 ? run(std::true_type{}) : run(std::false_type{});
 }
 
-int fa_packed_bwd_take_status(cudaStream_t stream) { return packed_take_status_here(stream); }
+int fa_packed_bwd_take_status(cudaStream_t stream) { return fa_take_status_word(g_packed_status, stream); }

@@ -680,4 +680,4 @@ cudaError_t fa_launch_packed_fwd(const FaPackedProblem &p, cudaStream_t stream)
     return p.d == 64 ? launch_d<64, false>(p, 1, stream) : launch_d<128, false>(p, 1, stream);
 }
 
-int fa_packed_fwd_take_status(cudaStream_t stream) { return packed_take_status_here(stream); }
+int fa_packed_fwd_take_status(cudaStream_t stream) { return fa_take_status_word(g_packed_status, stream); }

@@ -117,4 +117,4 @@ cudaError_t fa_launch_packed_plan(const int32_t *cu_seqlens, int64_t B, int64_t 
     return cudaGetLastError();
 }
 
-int fa_packed_plan_take_status(cudaStream_t stream) { return packed_take_status_here(stream); }
+int fa_packed_plan_take_status(cudaStream_t stream) { return fa_take_status_word(g_packed_status, stream); }
