@@ -164,6 +164,26 @@ def test_tree_over_long_ragged_lengths(d, P, Hkv, G, n_q, room):
 
 
 @gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,n_q", [(5, 8), (4, 16), (3, 32)])
+def test_many_short_caches(G, n_q, d):
+    # tables of 512 tokens: items go to CTAs whole, several to each, of chunks of 48, 32 and 48 rows in the kernel for many rows
+    B, Hkv, P = 80, 4, 16
+    rng = np.random.default_rng(d + n_q)
+    lens = rng.integers(0, 513, B).astype(np.int32)
+    lens[:6] = [512, 0, 1, 511, 128, 129]
+    pool = Pool(B, Hkv, d, P, lens, seed=d + n_q)
+    q = bf16(rng.standard_normal((B, Hkv * G, n_q, d))).cuda()
+    _, masks = random_tree(rng, B, n_q)
+    n_new = rng.integers(0, n_q + 1, B).astype(np.int32)
+    c, table = pool.cache(), dev(pool.table[:, :512 // P])
+    for new in (None, n_new):
+        o, lse = fa.forward_kv4_tree(q, c, dev(lens), table, dev(masks), n_new=None if new is None else dev(new))
+        ok()
+        check_tree(pool, q, lens, fa.default_scale(d), masks, new, o, lse)
+
+
+@gpu
 @rooms
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("G,n_q", [(2, 5), (5, 8), (4, 16)])
@@ -580,6 +600,33 @@ def test_pages_past_four_gibibytes():
         ok()
         for t, x in zip(c[:4], (1, 2, 3, 4)):
             assert (t[to] == x).all() and (t[to - 1] == 0).all()
+
+
+@gpu
+@rooms
+def test_trees_and_kept_paths_past_four_gibibytes(room):
+    # the pages of two sequences at the end of a pool of 4.6 GB of K
+    lens, Hkv, G, n_q, d, P = np.array([400, 130], np.int32), 8, 6, 8, 128, 128
+    pool = Pool(2, Hkv, d, P, lens, seed=77)
+    first = 70000 - pool.n_pages
+    c = fa.kv4_cache(70000, Hkv, P, d)
+    for big, small in zip(c, (pool.k, pool.v, pool.ks, pool.vs, pool.w)):
+        big[first:] = dev(small)
+    rng = np.random.default_rng(78)
+    q = bf16(rng.standard_normal((2, Hkv * G, n_q, d))).cuda()
+    _, masks = random_tree(rng, 2, n_q)
+    table = table_of(pool, room)
+    table += torch.where(table >= 0, first, 0).int()
+    o, lse = fa.forward_kv4_tree(q, c, dev(lens), table, dev(masks))
+    ok()
+    check_tree(pool, q, lens, fa.default_scale(d), masks, None, o, lse)
+    path, n_path = np.tile(np.array([1, 2, 5, 7, 0, 0, 0, 0], np.int32), (2, 1)), np.array([4, 3], np.int32)
+    got = fa.kv4_keep(c, dev(lens), table, dev(path), dev(n_path))
+    ok()
+    want, now = kept(pool, lens, path, n_path, None, n_q)
+    assert got.tolist() == now
+    for big, small in zip(c, want):
+        assert np.array_equal(big[first:].cpu().numpy(), small) and not big[first - 4:first].any()
 
 
 # ------------------------------------------------------------------------- as they are used together (GPU)

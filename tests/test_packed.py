@@ -466,6 +466,38 @@ def test_gradients_into_slices_of_one_gradient(H, Hkv, d):
 
 
 @gpu
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("H,Hkv,d", [(4, 2, 64), (3, 3, 128), (8, 1, 128), (1, 1, 64)])
+def test_head_major_tensors_and_gradients(H, Hkv, d, causal):
+    # [heads, T, d] in memory, each head's rows in a longer run of them; gradients and O into such tensors too
+    lens = [130, 1, 64, 0, 301]
+    cu = offsets(lens, first=3)
+    T = int(cu[-1]) + 9
+
+    def head_major(t):  # [T, heads, d] -> the same, heads outermost with 5 rows of 7 between them
+        wide = torch.full((t.shape[1], T + 5, d), 7.0, device="cuda").bfloat16()
+        wide[:, :T] = t.cuda().transpose(0, 1)
+        return wide, wide[:, :T].transpose(0, 1)
+
+    cpu = [randn(T, h, d, seed=31 + i) for i, h in enumerate((H, Hkv, Hkv, H))]
+    q, k, v, dout = (head_major(t)[1] for t in cpu)
+    seven = [head_major(torch.full_like(t, 7.0)) for t in (cpu[0], *cpu[:3])]
+    o, *grads = (view for _, view in seven)
+    lse = torch.full((H, T), 7.0, device="cuda")
+    fa.forward_packed(q, k, v, dev_cu(cu), causal=causal, out=o, lse=lse)
+    fa.backward_packed(q, k, v, o, lse, dout, dev_cu(cu), causal=causal, out=grads)
+    ok()
+    outside = [0, 1, 2, *range(int(cu[-1]), T)]
+    for (wide, view) in seven:
+        assert (wide[:, T:] == 7).all() and (view[outside] == 7).all()
+        view[outside] = 0
+    assert (lse[:, outside] == 7).all()
+    lse[:, outside] = -np.inf
+    check_forward(o, lse, *cpu[:3], cu, fa.default_scale(d), causal)
+    check_backward(grads, *cpu[:3], o, lse, cpu[3], cu, fa.default_scale(d), causal)
+
+
+@gpu
 @pytest.mark.parametrize("d,causal", [(64, True), (128, False)])
 def test_autograd_of_packed_attention(d, causal):
     q, k, v, cu = batch([90, 0, 200, 7], 4, 2, d, seed=71, first=1, tail=2)
@@ -624,3 +656,25 @@ def test_rows_past_four_gibibytes():
     s = slice(T - 300, T)
     check_forward(out[s].cpu(), lse[:, s].cpu(), q[s].cpu(), k[s].cpu(), k[s].cpu(), np.array(cu) - (T - 300), fa.default_scale(d), True)
     assert (out[:T - 300] == 0).all()
+
+
+@gpu
+def test_gradients_past_four_gibibytes():
+    # 2^31 elements and more in q's gradient and in the fp32 accumulator behind it
+    H, Hkv, d = 32, 8, 128
+    cu = offsets([500] * 1079 + [300, 1, 129])
+    T = int(cu[-1])
+    q, dout = (torch.empty(T, H, d, device="cuda", dtype=torch.bfloat16).normal_() for _ in range(2))
+    k, v = (torch.empty(T, Hkv, d, device="cuda", dtype=torch.bfloat16).normal_() for _ in range(2))
+    plan = fa.packed_plan(dev_cu(cu), T, causal=True)
+    o, lse = fa.forward_packed(q, k, v, dev_cu(cu), causal=True, plan=plan)
+    got = fa.backward_packed(q, k, v, o, lse, dout, dev_cu(cu), causal=True, plan=plan)
+    ok()
+    middle = (1 << 31) // (H * d) // 500  # the sequence in which element 2^31 lies
+    assert cu[middle] * H * d < 1 << 31 < cu[middle + 1] * H * d
+    for i in (0, middle, 1079, 1080, 1081):
+        s = slice(int(cu[i]), int(cu[i + 1]))
+        a = [t[s].cpu() for t in (q, k, v, o, dout)]
+        own = np.array([0, s.stop - s.start])
+        check_forward(a[3], lse[:, s].cpu(), *a[:3], own, fa.default_scale(d), True)
+        check_backward([g[s].cpu() for g in got], *a[:4], lse[:, s].cpu(), a[4], own, fa.default_scale(d), True)
