@@ -1084,7 +1084,9 @@ Geometry geometry(int64_t B, int64_t H, int64_t heads, int64_t n_q, int64_t d, i
         // of 16 and the other kernel: 4 sequences of up to 4000 (11 units) 21.7 and 30.3; 1 of 30000 (18.8) 46.7 and 42.7; 32 of up
         // to 8192 (169) 160 and 101, 24 rows 101 and 89, 32 rows 108 and 95, 64 rows 186 and 156, 128 rows 350 and 245; d = 64,
         // 48 rows 124 and 106, 64 rows 140 and 145, 128 rows 268 and 237, but 24 rows (in one chunk of 32) 81 and 89, 32 rows 77
-        // and 82.
+        // and 82.  Short tables, 128 sequences, d = 128, 48 rows: of 640 tokens 129 and 117, 512 122 and 99, 384 109 and 104, 272 107 and 103; of
+        // 256, where the first tile is half of an item, 95 and 106, of 128 79 and 90 (128 rows 231 and 321, 188 and 259; d = 64, 48 rows 92
+        // and 100, 91 and 86): there the rule, which looks at the work alone, takes the slower one.
         const int64_t tiles = (max_tokens + tile_keys(static_cast<int>(d)) - 1) / tile_keys(static_cast<int>(d));
         auto work = [&](int64_t rows, int64_t per_sm) { return B * heads * ((R + rows - 1) / rows) * (tiles + kItemUnits) / (kSms * per_sm); };
         if (work(8, 3) < 2) {
