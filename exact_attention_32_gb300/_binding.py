@@ -921,14 +921,15 @@ class _AttentionPacked(torch.autograd.Function):
         if plan is None:
             plan = packed_plan(cu_seqlens, q.shape[0], causal=causal)
         o, lse = forward_packed(q, k, v, cu_seqlens, scale=scale, causal=causal, plan=plan)
-        ctx.save_for_backward(q, k, v, o, lse, cu_seqlens, plan.table)
-        ctx.scale, ctx.causal, ctx.plan = scale, causal, plan[1:]
+        ctx.save_for_backward(q, k, v, o, lse, plan.table)
+        # (the offsets are the plan's: the backward looks at the tensor's size alone, and it may hold the next batch's by then)
+        ctx.scale, ctx.causal, ctx.plan, ctx.cu_seqlens = scale, causal, plan[1:], cu_seqlens
         return o
 
     @staticmethod
     def backward(ctx, dout):
-        q, k, v, o, lse, cu_seqlens, table = ctx.saved_tensors
-        grads = backward_packed(q, k, v, o, lse, _laid_out(dout), cu_seqlens, scale=ctx.scale, causal=ctx.causal,
+        q, k, v, o, lse, table = ctx.saved_tensors
+        grads = backward_packed(q, k, v, o, lse, _laid_out(dout), ctx.cu_seqlens, scale=ctx.scale, causal=ctx.causal,
                                 plan=PackedPlan(table, *ctx.plan))
         return (*_once(grads, q, k, v, dout), None, None, None, None)
 

@@ -46,3 +46,21 @@ def test_an_output_gradient_that_lies_off_sixteen_bytes(packed, monkeypatch):
     weight = torch.arange(3 + q.numel(), dtype=torch.float32)
     (torch.cat([torch.zeros(3), out().flatten()]) * weight).sum().backward()
     assert seen == [(0, True)] and torch.equal(q.grad.flatten(), 3 * weight[3:])
+
+
+def test_offsets_that_change_before_the_backward(monkeypatch):
+    # a step's offsets in one buffer, overwritten with the next ones before this one's backward: the plan holds what it was made from
+    monkeypatch.setattr(_binding, "packed_plan", lambda cu, T, causal: _binding.PackedPlan(torch.zeros(1), T, cu.shape[0] - 1, causal))
+    monkeypatch.setattr(_binding, "forward_packed", lambda q, k, v, cu, **kw: (q.clone(), q.new_zeros(1)))
+    seen = []
+
+    def backward(q, k, v, o, lse, dout, cu, plan, **kw):
+        seen.append((cu.shape[0], plan[1:]))
+        return dout.clone(), dout.clone(), dout.clone()
+
+    monkeypatch.setattr(_binding, "backward_packed", backward)
+    q, cu = torch.randn(4, 1, 64, requires_grad=True), torch.tensor([0, 3, 4])
+    o = fa.attention_packed(q, q, q, cu, causal=True)
+    cu.copy_(torch.tensor([0, 1, 4]))
+    o.sum().backward()
+    assert (q.grad == 3).all() and seen == [(3, (4, 2, True))]
