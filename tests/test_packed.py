@@ -231,6 +231,32 @@ def test_forward_over_many_tiles_and_large_scores(lens, H, Hkv, d, gain, causal)
 
 
 @gpu
+@pytest.mark.parametrize("lens,H,Hkv", [([4, 600, 1], 4, 2), ([4, 600, 1], 3, 3), ([9000], 1, 1)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("size", [-2.0 ** 29, -3e6, 3e6, 2.0 ** 29])
+def test_scores_up_to_two_to_the_twenty_ninth(size, d, lens, H, Hkv):
+    # all queries alike, keys 1, 1, 4 and 4 (a quarter of the rows each) in every channel: those of the largest score tie, the others weigh
+    # nothing.  O is their mean: P's rounding (bf16, 2^-8, which the divisor may not share) and the result's
+    T, scale = sum(lens), fa.default_scale(d)
+    cu = offsets(lens)
+    key = np.concatenate([np.array([1.0, 1.0, 4.0, 4.0])[np.arange(n) * 4 // n] for n in lens])
+    top = 4 if size > 0 else 1
+    k = torch.tensor(key).bfloat16()[:, None, None].expand(T, Hkv, d).contiguous()
+    q, v = torch.full((T, H, d), size / (top * d * scale)).bfloat16(), randn(T, Hkv, d, seed=61)
+    o, lse = fa.forward_packed(q.cuda(), k.cuda(), v.cuda(), dev_cu(cu))
+    ok()
+    for a, e in zip(cu[:-1], cu[1:]):
+        s = float(q[0, 0, 0]) * scale * d * key[a:e]
+        tie = s == s.max()
+        want = f64(v[a:e])[tie].mean(0).repeat(H // Hkv, 0)
+        spread = np.abs(f64(v[a:e])[tie]).mean(0).repeat(H // Hkv, 0)
+        want_lse = s.max() + np.log(tie.sum())
+        assert (np.abs(f64(lse)[:, a:e] - want_lse) <= (d + 16) * 2.0 ** -23 * abs(want_lse)).all()
+        bound = (H8 + (e - a + 64) * 2.0 ** -22) * (spread + np.abs(want)) + H8 * np.abs(want)
+        assert (np.abs(f64(o)[a:e] - want) <= bound).all()
+
+
+@gpu
 @pytest.mark.parametrize("d", [64, 128])
 def test_one_sequence_of_equal_heads_is_the_dense_forward(d):
     q, k, v = (t.cuda() for t in fa.make_inputs(1, 3, 1111, d, seed=9))
