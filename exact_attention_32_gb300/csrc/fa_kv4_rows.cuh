@@ -16,12 +16,13 @@
 // A tile is 128 keys; a CTA an SM.  A softmax warpgroup takes half of the rows, one thread a key.  Its steps hang on one
 // another (scores, whether a row's reference grows, P), so two teams of two warpgroups take turns by tile, each with a
 // reference, a sum and an O of its own, joined at the end of a segment: with one team a tile of 48 rows took 3430 cycles, of which
-// the warps issued in 40 %, with two 2000 (60 %).  32 sequences of up to 8192, 8 key heads, 48 rows: 98 us, 1.5 TB/s of cache
-// (22 us would be the bytes): the chain load, decode, S, P, O through pairs of buffers bounds it, no unit alone (without
+// the warps issued in 40 %, with two 2000 (60 %).  32 sequences of up to 8192, 8 key heads, 48 rows: 95 to 109 us from box to box, 1.4 to
+// 1.6 TB/s of cache (22 us would be the bytes): the chain load, decode, S, P, O through pairs of buffers bounds it, no unit alone (without
 // the conversions, the decoded tiles' stores or the exponentials a tile would take 3 % less).
 // Roles (896 threads): warps 0-7 and 8-15 the teams; 16-19 decode K and 20-23 V; 24 loads K's codes and scales, 25 V's; 26 issues S's
 // products and 27 O's (from one warp, in one order, each would wait for what the other waits for: 4000 cycles a tile).
-// Launched with 72 registers a thread, of which the last twelve warps give some to the softmax of 48 rows.
+// Launched with 72 registers a thread, of which the last twelve warps give some to the softmax of 48 rows.  Spilled all the same: 140 to
+// 144 bytes stored and 132 to 136 loaded with 48 rows, 20 to 28 and 56 to 80 with 32.
 
 constexpr int kRowsLaunchRegs = 72;
 // A row's reference is set this far (log2) above what the largest term needs: with the decode kernel's 3 one of 24 rows grew in

@@ -18,8 +18,8 @@
 //   - A thread finds its item in the list; the next one is asked for an item ahead.
 //   - Where few long items leave SMs idle, a cluster of CTAs shares each (ranks_of).
 // What bounds it is the chain S, softmax, P V of a tile, as in fa_fwd_tc.cu, and an item's start and end, about two tiles: 3
-// sequences of up to 16384, 32 heads on 8, d = 128, causal, 1930 us (1.59 PFLOP/s), 16 of 200 to 4096 320 us (1.30; the tensor pipe 62 %
-// busy), 48 of 100 to 1000, 16 heads, d = 64, not causal 76 us (0.57, 35 %).
+// sequences of up to 16384, 32 heads on 8, d = 128, causal, 1930 to 2070 us (1.59 to 1.49 PFLOP/s, by the power), 16 of 200 to 4096 320 to 340 us (1.30; the tensor pipe
+// 62 % busy), 48 of 100 to 1000, 16 heads, d = 64, not causal 76 us (0.57, 35 %).
 // Every mbarrier wait is bounded; a wait that gives up sets FA_ERR_TIMEOUT and the CTA winds down.
 #include <math.h>
 
@@ -34,7 +34,8 @@ namespace {
 constexpr int kTile = 128;    // query rows of a tile, keys of a K/V tile
 // Three warpgroups: two of softmax, and the load and product warps' (two of its warps idle).  Launched with 168 registers a
 // thread (what 384 threads may have); the third gives 64 of its own up, and the softmax, a row's 128 scores a thread, takes 32 more each
-// (with 168 it spilled up to 250 bytes).
+// (with 168 it spilled up to 250 bytes).  What ptxas spills is left of that: 16 to 36 bytes stored and 28 to 64 loaded, 44 and 96 to 124
+// where a cluster shares an item.
 constexpr int kThreads = 384;
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 200, kOtherRegs = 104;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kLaunchRegs, "the warpgroups' shares are what the block has");

@@ -427,8 +427,9 @@ int64_t fa_packed_plan_bytes(int64_t B, int64_t T);
  *   H, Hkv  : query heads, a multiple of the key heads;  d : 64 or 128 (else FA_ERR_UNSUPPORTED)
  *   fill    : 1 gives rows of no sequence O = 0, LSE = -inf; 0 leaves them as they were
  * Scores, scale q . k, may reach 2^29 in magnitude: a row's reference rounds to fp32, and further out
- * what that leaves in the exponent passes fp32's range.  A value of V that is not finite reaches, as in fa_fwd, the rows of its own sequence that lie in
- * or behind its block of 128 rows (counted from the sequence's first), causal or not.  Errors as fa_fwd.
+ * what that leaves in the exponent passes fp32's range.  A value of V that is not finite reaches,
+ * as in fa_fwd, the rows of its own sequence that lie in or behind its block of 128 rows (counted
+ * from the sequence's first), causal or not.  Errors as fa_fwd.
  */
 int fa_fwd_packed(const fa_rows *q, const fa_rows *k, const fa_rows *v, const fa_rows *o, float *lse,
                   const void *plan, int64_t B, int64_t T, int64_t H, int64_t Hkv, int64_t d, float scale,
